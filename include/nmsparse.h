@@ -387,6 +387,95 @@ nm_status nm_spmm_bitmap(const void* X, int64_t Mtok, int64_t K, int64_t ldx, co
                          const uint8_t* mask, int64_t ldm, const int32_t* offs, int64_t ldo, int64_t R, void* Y,
                          nm_dtype ydt, int64_t ldy, void* ws, size_t ws_bytes, nm_stream_t stream);
 
+/* ---------------------------------------------------------------- gated feed-forward block
+ * The first half of a gated feed-forward block whose two projections are packed alike:
+ *   G = g_scale x_scale[m] (X Wg^T),  U = u_scale x_scale[m] (X Wu^T),  H = act(G) . U,
+ * one pass over X and both weights; sums, activation and product in f32 (exact int32 sums for
+ * int8), H rounded once.  x_scale NULL counts as 1.
+ *   act: NM_ACT_SILU g / (1 + e^-g); NM_ACT_GELU g Phi(g); NM_ACT_GELU_TANH its tanh form
+ *   g / 2 (1 + tanh(sqrt(2/pi) (g + 0.044715 g^3))); NM_ACT_RELU2 max(g, 0)^2.
+ *   X, the weights' dtype, Ns and the widths as in nm_spmm; vals_g/idx_g and vals_u/idx_u are
+ *   two weights of R rows each with the same ldv and ldi.  idx must be 4-byte aligned; 16-byte
+ *   aligned index rows (ldi % 4 == 0) let the fused kernels run.
+ *   H: [Mtok, R] (ldh), bf16 or f32.
+ *   G, U: both NULL, or bf16 [Mtok, R] (ldg): the pre-activations a training step keeps for
+ *   nm_spmm_glu_backward, rounded once.
+ * ws: nm_spmm_glu_workspace(...) bytes, 16-byte aligned, as for nm_spmm. */
+typedef enum { NM_ACT_SILU = 0, NM_ACT_GELU = 1, NM_ACT_GELU_TANH = 2, NM_ACT_RELU2 = 3 } nm_act;
+size_t nm_spmm_glu_workspace(int64_t Mtok, int64_t K, int64_t R, int Ns, nm_dtype xdt);
+nm_status nm_spmm_glu(const void* X, nm_dtype xdt, int64_t Mtok, int64_t K, int64_t ldx, const void* vals_g,
+                      const uint32_t* idx_g, const void* vals_u, const uint32_t* idx_u, nm_dtype vdt, int64_t R,
+                      int64_t ldv, int64_t ldi, int Ns, const float* x_scale, float g_scale, float u_scale,
+                      nm_act act, void* H, nm_dtype hdt, int64_t ldh, void* G, void* U, int64_t ldg, void* ws,
+                      size_t ws_bytes, nm_stream_t stream);
+
+/* ---------------------------------------------------------------- gradients
+ * Backward pass of the plain 2:4 layer Y = X W^T in bf16, for training the kept values of a
+ * fixed mask ("Sparse-BitNet", section 2 and "SparseForge", Methodology 3: training continues
+ * under the N:M mask):
+ *   dX = dY W                                          [Mtok, K] (lddx), bf16 or f32, or NULL
+ *   dV[r, j] = sum_m dY[m, r] X[m, column of value j]  [R, K/2] (lddv), bf16 or f32, or NULL
+ * dV has the layout of vals; a padding slot's entry is the derivative at its position.  All
+ * sums in f32 in a fixed order, one rounding.  dY: bf16 [Mtok, R] (lddy), any alignment of 2
+ * bytes (16-byte aligned rows are read faster).  X, vals: bf16 with 16-byte aligned rows; idx
+ * 4-byte aligned; dV 16-byte aligned rows.  Requires K % 16 == 0 and Mtok, K, R <= 2^21.
+ * Zero tokens give dV = 0.  vals may be NULL when dX is, X when dV is; idx is always needed.
+ * ws: nm_spmm_backward_workspace(...) bytes, 16-byte aligned. */
+size_t nm_spmm_backward_workspace(int64_t Mtok, int64_t K, int64_t R);
+nm_status nm_spmm_backward(const void* dY, int64_t lddy, const void* X, int64_t ldx, int64_t Mtok, int64_t K,
+                           const void* vals, const uint32_t* idx, int64_t R, int64_t ldv, int64_t ldi, void* dX,
+                           nm_dtype dxdt, int64_t lddx, void* dV, nm_dtype dvdt, int64_t lddv, void* ws,
+                           size_t ws_bytes, nm_stream_t stream);
+
+/* Backward pass of nm_spmm_glu (bf16, plain 2:4, scales 1) from its saved pre-activations:
+ *   dG = dH . U . act'(G),  dU = dH . act(G)   (f32, rounded once to bf16 as operands)
+ *   dX = dG Wg + dU Wu, dVg and dVu as dV of nm_spmm_backward from dG and dU.
+ * dH (lddh), G and U (ldg): bf16 [Mtok, R].  dX NULL, or dVg and dVu both NULL: not computed.
+ * Requirements of nm_spmm_backward for both weights.
+ * ws: nm_spmm_glu_backward_workspace(...) bytes, 16-byte aligned. */
+size_t nm_spmm_glu_backward_workspace(int64_t Mtok, int64_t K, int64_t R);
+nm_status nm_spmm_glu_backward(const void* dH, int64_t lddh, const void* G, const void* U, int64_t ldg, nm_act act,
+                               const void* X, int64_t ldx, int64_t Mtok, int64_t K, const void* vals_g,
+                               const uint32_t* idx_g, const void* vals_u, const uint32_t* idx_u, int64_t R,
+                               int64_t ldv, int64_t ldi, void* dX, nm_dtype dxdt, int64_t lddx, void* dVg, void* dVu,
+                               nm_dtype dvdt, int64_t lddv, void* ws, size_t ws_bytes, nm_stream_t stream);
+
+/* ---------------------------------------------------------------- optimiser
+ * One AdamW step (decoupled weight decay) over count tensors, for the packed values, adapters
+ * and whatever else is trained beside them:
+ *   g' = g * grad_scale,  m = beta1 m + (1 - beta1) g',  v = beta2 v + (1 - beta2) g'^2,
+ *   p  = p (1 - l weight_decay) - l / (1 - beta1^step) m / (sqrt(v / (1 - beta2^step)) + eps),
+ *   l  = lr lr_scale,
+ * in f32; m, v and sqrt(v) with one rounding per operation in the order written ((1 - beta2) g'
+ * first, then times g'), every stored value rounded once.  grad_scale: device f32 [1] (a clipping factor or the
+ * inverse of a loss scale), or NULL for 1.  step counts from 1.
+ *   p: pdt F32 or BF16; g: gdt F32 or BF16; copy: bf16 copy of the new p (the packed values a
+ *   product reads beside f32 masters), or NULL.
+ *   sdt F32: m, v f32 [n].  m_scale and v_scale are ignored.
+ *   sdt FP8: m and v hold e4m3 codes [n] of m and of r = sqrt(v), with f32 scales per 256
+ *   consecutive elements (m_scale, v_scale [ceil(n/256)]): value = code * scale, scale = max * (1/448)
+ *   with max the block's largest finite magnitude, code = the e4m3 value nearest (ties to even)
+ *   to x * (448 * (1 / max)), one rounding per operation; a nonzero r keeps at least the smallest code 2^-9, a block whose magnitudes are
+ *   all below 2^-118 is stored as zeros, NaN and infinities as the NaN code.  p is updated with
+ *   the m and v of before that rounding.  Zeroed codes and scales are the zero state.
+ * tensors is a HOST array, read before the call returns; the tensors must not overlap each
+ * other.  Element-aligned pointers are accepted; 16-byte aligned ones (8-byte for codes) are
+ * read and written in whole vectors.  Allocates nothing, one launch per 44 tensors. */
+typedef struct {
+    void* p;
+    const void* g;
+    void* m;
+    void* v;
+    float* m_scale;
+    float* v_scale;
+    void* copy;
+    int64_t n;
+    nm_dtype pdt, gdt;
+    float lr_scale, weight_decay;
+} nm_adamw_tensor;
+nm_status nm_adamw(const nm_adamw_tensor* tensors, int count, nm_dtype sdt, double lr, double beta1, double beta2,
+                   double eps, int64_t step, const float* grad_scale, nm_stream_t stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -26,6 +26,7 @@ STATUS_NAMES = ["NM_OK", "NM_ERR_NULL", "NM_ERR_SHAPE", "NM_ERR_PATTERN", "NM_ER
 NM_F32, NM_BF16, NM_I8, NM_I32, NM_FP8 = 0, 1, 2, 3, 4
 NM_SCORE_HESSIAN, NM_SCORE_MAGNITUDE = 0, 1
 NM_FLAG_VALIDATE = 1
+NM_ACT_SILU, NM_ACT_GELU, NM_ACT_GELU_TANH, NM_ACT_RELU2 = range(4)
 
 # NM_FP8 travels as torch.float8_e4m3fn (OCP e4m3 codes, one byte each)
 _DT = {torch.float32: NM_F32, torch.bfloat16: NM_BF16, torch.int8: NM_I8, torch.int32: NM_I32,
@@ -47,6 +48,7 @@ raw = ctypes.CDLL(str(LIB_PATH))
 
 _P, _I64, _I, _F, _U64, _SZ = ctypes.c_void_p, ctypes.c_int64, ctypes.c_int, ctypes.c_float, ctypes.c_uint64, ctypes.c_size_t
 _U = ctypes.c_uint
+_D = ctypes.c_double
 
 SIGNATURES = {
     "nm_abi_version": (_I, []),
@@ -82,6 +84,16 @@ SIGNATURES = {
     "nm_spmm_bitmap": (_I, [_P, _I64, _I64, _I64, _P, _I64, _P, _I64, _P, _I64, _I64, _P, _I, _I64, _P, _SZ, _P]),
     "nm_spmm_lowrank": (_I, [_P, _I64, _I64, _I64, _P, _P, _I64, _I64, _I64, _I, _P, _I64, _P, _I64, _I, _P, _I, _I64,
                              _P, _SZ, _P]),
+    "nm_spmm_glu_workspace": (_SZ, [_I64, _I64, _I64, _I, _I]),
+    "nm_spmm_glu": (_I, [_P, _I, _I64, _I64, _I64, _P, _P, _P, _P, _I, _I64, _I64, _I64, _I, _P, _F, _F, _I, _P, _I,
+                         _I64, _P, _P, _I64, _P, _SZ, _P]),
+    "nm_spmm_backward_workspace": (_SZ, [_I64, _I64, _I64]),
+    "nm_spmm_backward": (_I, [_P, _I64, _P, _I64, _I64, _I64, _P, _P, _I64, _I64, _I64, _P, _I, _I64, _P, _I, _I64,
+                              _P, _SZ, _P]),
+    "nm_spmm_glu_backward_workspace": (_SZ, [_I64, _I64, _I64]),
+    "nm_spmm_glu_backward": (_I, [_P, _I64, _P, _P, _I64, _I, _P, _I64, _I64, _I64, _P, _P, _P, _P, _I64, _I64, _I64,
+                                  _P, _I, _I64, _P, _P, _I, _I64, _P, _SZ, _P]),
+    "nm_adamw": (_I, [_P, _I, _I, _D, _D, _D, _D, _I64, _P, _P]),
 }
 for _name, (_res, _args) in SIGNATURES.items():
     _fn = getattr(raw, _name)
@@ -379,3 +391,189 @@ def nm_spmm_noalloc(X: torch.Tensor, vals: torch.Tensor, idx: torch.Tensor, R: i
     _check(raw.nm_spmm_noalloc(_ptr(X), xdt, Mtok, K, _ld(X), _ptr(vals), dtype_code(vals), _ptr(idx), R, _ld(vals),
                                _ld(idx), Ns, _ptr(x_scale), w_scale, _ptr(Y), ydt, _ld(Y), _stream(X)))
     return Y
+
+
+# ---------------------------------------------------------------- gated feed-forward block, training
+def _row_major(**tensors):
+    for name, t in tensors.items():
+        if t is not None and (t.dim() != 2 or (t.shape[1] > 1 and t.stride(1) != 1)):
+            raise ValueError(f"{name} must be a row-major 2-D tensor (unit stride along the last dimension)")
+
+
+def _ld2(t: torch.Tensor) -> int:
+    """Leading dimension of a 2-D row-major view; a one-row view's may be anything."""
+    return t.stride(0) if t.shape[0] > 1 else max(t.stride(0), t.shape[1])
+
+
+def _need(need: int, ws: torch.Tensor | None, device) -> torch.Tensor | None:
+    return ws if ws is not None and ws.numel() >= need else _ws(need, device)
+
+
+def _same(what: str, *pairs):
+    for a, b in pairs:
+        if a != b:
+            raise ValueError(f"{what}: got {a}, expected {b}")
+
+
+def nm_spmm_glu(X: torch.Tensor, vals_g: torch.Tensor, idx_g: torch.Tensor, vals_u: torch.Tensor, idx_u: torch.Tensor,
+                Ns: int = 0, act: int = NM_ACT_SILU, x_scale: torch.Tensor | None = None, g_scale: float = 1.0,
+                u_scale: float = 1.0, hdt: int | None = None, save: bool = False, out: torch.Tensor | None = None,
+                ws: torch.Tensor | None = None):
+    """H = act(G) . U with G = X Wg^T and U = X Wu^T on packed weights, in one pass: H, or with
+    save (H, G, U), the bf16 pre-activations that nm_spmm_glu_backward takes."""
+    _row_major(X=X, vals_g=vals_g, idx_g=idx_g, vals_u=vals_u, idx_u=idx_u, out=out)
+    Mtok, K = X.shape
+    R = vals_g.shape[0]
+    Kl = lifted_width(K, Ns) if Ns else K
+    _same("packed weights", (vals_u.shape[0], R), (idx_g.shape[0], R), (idx_u.shape[0], R))
+    for t in (vals_g, vals_u):
+        if t.shape[1] < Kl // 2 or t.dtype != X.dtype:
+            raise ValueError(f"vals must hold {Kl // 2} values of {X.dtype} per row, got {tuple(t.shape)} {t.dtype}")
+    for t in (idx_g, idx_u):
+        if t.shape[1] < (Kl + 31) // 32 or t.dtype != torch.int32:
+            raise ValueError("idx must be int32 with one word per 32 (lifted) columns")
+    if R > 1 and (vals_u.stride(0) != vals_g.stride(0) or idx_u.stride(0) != idx_g.stride(0)):
+        raise ValueError("the gate and up weights must have the same row strides")
+    if x_scale is not None and (x_scale.dtype != torch.float32 or x_scale.numel() != Mtok or not x_scale.is_contiguous()):
+        raise ValueError("x_scale must be a contiguous f32 tensor with one value per token")
+    hdt = (NM_BF16 if out is None else dtype_code(out)) if hdt is None else hdt
+    H = out if out is not None else torch.empty((Mtok, R), dtype=_TORCH[hdt], device=X.device)
+    _same("out", (tuple(H.shape), (Mtok, R)), (H.dtype, _TORCH[hdt]))
+    G = torch.empty((Mtok, R), dtype=torch.bfloat16, device=X.device) if save else None
+    U = torch.empty((Mtok, R), dtype=torch.bfloat16, device=X.device) if save else None
+    ws = _need(raw.nm_spmm_glu_workspace(Mtok, K, R, Ns, dtype_code(X)), ws, X.device)
+    _check(raw.nm_spmm_glu(_ptr(X), dtype_code(X), Mtok, K, _ld2(X), _ptr(vals_g), _ptr(idx_g), _ptr(vals_u),
+                           _ptr(idx_u), dtype_code(vals_g), R, _ld2(vals_g), _ld2(idx_g), Ns, _ptr(x_scale), g_scale,
+                           u_scale, act, _ptr(H), hdt, _ld2(H), _ptr(G), _ptr(U), R, _ptr(ws),
+                           0 if ws is None else ws.numel(), _stream(X)))
+    return (H, G, U) if save else H
+
+
+def _grad_out(t: torch.Tensor | None, want: bool, shape, dt: int, device):
+    if not want:
+        return None
+    if t is None:
+        return torch.empty(shape, dtype=_TORCH[dt], device=device)
+    _row_major(out=t)
+    _same("out", (tuple(t.shape), tuple(shape)), (t.dtype, _TORCH[dt]))
+    return t
+
+
+def _check_grad(X, dY, vals, idx):
+    Mtok, K = X.shape
+    R = vals[0].shape[0]
+    _row_major(X=X, dY=dY)
+    _same("dY", (tuple(dY.shape), (Mtok, R)))
+    for t in (X, dY, *vals):
+        if t.dtype != torch.bfloat16:
+            raise ValueError(f"the backward pass takes bf16 tensors, got {t.dtype}")
+    for v, i in zip(vals, idx):
+        _row_major(vals=v, idx=i)
+        if v.shape[0] != R or v.shape[1] < K // 2 or i.shape[0] != R or i.shape[1] < (K + 31) // 32 or \
+                i.dtype != torch.int32:
+            raise ValueError("vals / idx do not hold a 2:4 weight of this shape")
+        if R > 1 and (v.stride(0) != vals[0].stride(0) or i.stride(0) != idx[0].stride(0)):
+            raise ValueError("the gate and up weights must have the same row strides")
+    return Mtok, K, R
+
+
+def nm_spmm_backward(dY: torch.Tensor, X: torch.Tensor, vals: torch.Tensor, idx: torch.Tensor, want_dx: bool = True,
+                     want_dv: bool = True, dxdt: int = NM_BF16, dvdt: int = NM_BF16, out_dx: torch.Tensor | None = None,
+                     out_dv: torch.Tensor | None = None, ws: torch.Tensor | None = None):
+    """(dX, dvals) of Y = X W^T on a 2:4 packed bf16 weight; what is not wanted is None."""
+    Mtok, K, R = _check_grad(X, dY, [vals], [idx])
+    dX = _grad_out(out_dx, want_dx, (Mtok, K), dxdt, X.device)
+    dV = _grad_out(out_dv, want_dv, (R, K // 2), dvdt, X.device)
+    ws = _need(raw.nm_spmm_backward_workspace(Mtok, K, R), ws, X.device)
+    _check(raw.nm_spmm_backward(_ptr(dY), _ld2(dY), _ptr(X), _ld2(X), Mtok, K, _ptr(vals), _ptr(idx), R, _ld2(vals),
+                                _ld2(idx), _ptr(dX), dxdt, K if dX is None else _ld2(dX), _ptr(dV), dvdt,
+                                K // 2 if dV is None else _ld2(dV), _ptr(ws), 0 if ws is None else ws.numel(),
+                                _stream(X)))
+    return dX, dV
+
+
+def nm_spmm_glu_backward(dH: torch.Tensor, G: torch.Tensor, U: torch.Tensor, X: torch.Tensor, vals_g: torch.Tensor,
+                         idx_g: torch.Tensor, vals_u: torch.Tensor, idx_u: torch.Tensor, act: int = NM_ACT_SILU,
+                         want_dx: bool = True, want_dv: bool = True, dxdt: int = NM_BF16, dvdt: int = NM_BF16,
+                         out_dx: torch.Tensor | None = None,
+                         out_dv: tuple[torch.Tensor, torch.Tensor] | None = None, ws: torch.Tensor | None = None):
+    """(dX, dvals_g, dvals_u) of nm_spmm_glu from its saved pre-activations; what is not wanted
+    is None."""
+    Mtok, K, R = _check_grad(X, dH, [vals_g, vals_u], [idx_g, idx_u])
+    _row_major(G=G, U=U)
+    _same("G and U", (tuple(G.shape), (Mtok, R)), (tuple(U.shape), (Mtok, R)), (G.dtype, torch.bfloat16),
+          (U.dtype, torch.bfloat16), (_ld2(U), _ld2(G)))
+    dX = _grad_out(out_dx, want_dx, (Mtok, K), dxdt, X.device)
+    dVg = _grad_out(out_dv[0] if out_dv else None, want_dv, (R, K // 2), dvdt, X.device)
+    dVu = _grad_out(out_dv[1] if out_dv else None, want_dv, (R, K // 2), dvdt, X.device)
+    if want_dv:
+        _same("out_dv row strides", (_ld2(dVu), _ld2(dVg)))
+    ws = _need(raw.nm_spmm_glu_backward_workspace(Mtok, K, R), ws, X.device)
+    _check(raw.nm_spmm_glu_backward(_ptr(dH), _ld2(dH), _ptr(G), _ptr(U), _ld2(G), act, _ptr(X), _ld2(X), Mtok, K,
+                                    _ptr(vals_g), _ptr(idx_g), _ptr(vals_u), _ptr(idx_u), R, _ld2(vals_g),
+                                    _ld2(idx_g), _ptr(dX), dxdt, K if dX is None else _ld2(dX), _ptr(dVg), _ptr(dVu),
+                                    dvdt, K // 2 if dVg is None else _ld2(dVg), _ptr(ws),
+                                    0 if ws is None else ws.numel(), _stream(X)))
+    return dX, dVg, dVu
+
+
+class _AdamWTensor(ctypes.Structure):
+    _fields_ = [("p", _P), ("g", _P), ("m", _P), ("v", _P), ("m_scale", _P), ("v_scale", _P), ("copy", _P), ("n", _I64),
+                ("pdt", _I), ("gdt", _I), ("lr_scale", _F), ("weight_decay", _F)]
+
+
+class AdamWTensors:
+    """The tensors of an optimiser, as nm_adamw takes them: lists of contiguous parameters,
+    gradients and states (f32, or float8_e4m3fn codes with f32 scales per 256 elements), kept
+    for as long as the object lives.  copies: bf16 copies of the parameters, or None; lr_scale
+    and weight_decay: one number, or one per tensor.  Build it once and use it every step."""
+
+    def __init__(self, params, grads, m, v, m_scale=None, v_scale=None, copies=None, lr_scale=1.0, weight_decay=0.0):
+        n = len(params)
+        lists = {"grads": grads, "m": m, "v": v, "m_scale": m_scale, "v_scale": v_scale, "copies": copies}
+        for name, t in lists.items():
+            if t is not None and len(t) != n:
+                raise ValueError(f"{name}: {len(t)} tensors for {n} parameters")
+        per = lambda x: [float(x)] * n if isinstance(x, (int, float)) else [float(y) for y in x]  # noqa: E731
+        lr_scale, weight_decay = per(lr_scale), per(weight_decay)
+        _same("lr_scale and weight_decay", (len(lr_scale), n), (len(weight_decay), n))
+        self.keep = [list(params)] + [None if t is None else list(t) for t in lists.values()]
+        self.device = params[0].device if n else None
+        kinds = {t.dtype for t in [*m, *v]}
+        if kinds - {torch.float32} and kinds != {torch.float8_e4m3fn}:
+            raise ValueError(f"states must all be float32 or all float8_e4m3fn, got {kinds}")
+        self.sdt = NM_FP8 if kinds == {torch.float8_e4m3fn} else NM_F32
+        if self.sdt == NM_FP8 and (m_scale is None or v_scale is None):
+            raise ValueError("8-bit states need m_scale and v_scale")
+        self.count, self.array = n, (_AdamWTensor * max(n, 1))()
+        for i in range(n):
+            p, k = params[i], params[i].numel()
+            for name, t in lists.items():
+                if t is None or (self.sdt == NM_F32 and name.endswith("scale")):
+                    continue
+                want = (k + 255) // 256 if name.endswith("scale") else k
+                if t[i].numel() != want or not t[i].is_contiguous() or t[i].device != p.device:
+                    raise ValueError(f"{name}[{i}]: {want} contiguous elements on {p.device} expected")
+            if not p.is_contiguous() or p.device != self.device:
+                raise ValueError(f"params[{i}] must be contiguous and on {self.device}")
+            if copies is not None and copies[i].dtype != torch.bfloat16:
+                raise ValueError("copies are bf16")
+            if self.sdt == NM_FP8 and (m_scale[i].dtype != torch.float32 or v_scale[i].dtype != torch.float32):
+                raise ValueError("scales are float32")
+            f8 = self.sdt == NM_FP8
+            self.array[i] = _AdamWTensor(
+                _ptr(p), _ptr(grads[i]), _ptr(m[i]), _ptr(v[i]), _ptr(m_scale[i]) if f8 else None,
+                _ptr(v_scale[i]) if f8 else None, None if copies is None else _ptr(copies[i]), k, dtype_code(p),
+                dtype_code(grads[i]), lr_scale[i], weight_decay[i])
+
+
+def nm_adamw(tensors: AdamWTensors, lr: float, step: int, beta1: float = 0.9, beta2: float = 0.999, eps: float = 1e-8,
+             grad_scale: torch.Tensor | None = None) -> None:
+    """One AdamW step over every tensor of the list, in place; step counts from 1."""
+    if grad_scale is not None and (grad_scale.dtype != torch.float32 or grad_scale.numel() != 1):
+        raise ValueError("grad_scale must be one f32 value on the device")
+    if tensors.count == 0:
+        return
+    with torch.cuda.device(tensors.device):
+        _check(raw.nm_adamw(ctypes.addressof(tensors.array), tensors.count, tensors.sdt, lr, beta1, beta2, eps, step,
+                            _ptr(grad_scale), torch.cuda.current_stream(tensors.device).cuda_stream))

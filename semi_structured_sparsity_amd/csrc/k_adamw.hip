@@ -1,0 +1,307 @@
+// One AdamW step over many tensors (decoupled weight decay):
+//   g' = g * grad_scale,  m = b1 m + (1 - b1) g',  v = b2 v + (1 - b2) g'^2,
+//   p  = p (1 - lr wd) - lr / (1 - b1^t) * m / (sqrt(v / (1 - b2^t)) + eps),
+// all in f32.  m, v and r = sqrt(v) take one rounding per operation in the order written, with
+// no contraction, as does the quotient that picks a code below: codes are decided by them, so
+// every correct evaluation of this order gives the same codes.  The parameter's update uses
+// fused multiply-adds and the hardware's reciprocal (about 1e-7 relative).
+//
+// States in 8 bits: m and r = sqrt(v) are e4m3 codes with one f32 scale per 256 consecutive
+// elements, scale = max |x| * (1 / 448), code = the e4m3 value nearest x * (448 * (1 / max)).  e4m3
+// spans 18 binades below the scale's maximum, and r halves the binades v needs.  A nonzero r
+// keeps at least the smallest code: an r that became zero beside an m that did not would
+// divide m by eps.  The parameter update uses m and v before they are rounded to codes.
+// A block whose maximum is below 2^-118 (its reciprocal would overflow) stores zeros.  NaN and
+// infinite elements store the NaN code and do not enter the block's scale.
+//
+// The step is bound by HBM: per parameter 8 B (f32 p read and written) or 4 B (bf16), the
+// gradient's 2 or 4 B, 16 B of f32 states or 4 + 4/128 B of codes and scales, 2 B of the
+// bf16 copy.  Descriptors travel as kernel arguments (no table upload, graph capture
+// safe), kMaxTensors a launch; a block finds its tensor by a binary search over the
+// tensors' first block numbers, in scalar registers.
+#include <math.h>
+
+#include "nm_internal.h"
+
+namespace nm {
+
+constexpr int kMaxTensors = 44;     // descriptors per launch: kernel arguments stay below 4 KB
+constexpr int kPerThread = 8;       // consecutive elements of a thread: 32 lanes hold a 256-element block
+constexpr int kPass = 256 * kPerThread;
+constexpr int kPasses = 2;          // passes of a block over its tensor
+constexpr int kChunk = kPass * kPasses;
+
+enum : uint32_t { kPBf16 = 1, kGBf16 = 2, kVec = 4 };
+
+struct AdamWDesc {
+    void* p;
+    const void* g;
+    void* m;
+    void* v;
+    float* ms;
+    float* vs;
+    uint16_t* c;
+    int64_t n;
+    float alpha;    // lr / (1 - b1^t)
+    float decay;    // 1 - lr wd
+    uint32_t flags;
+    uint32_t pad;
+};
+struct AdamWArgs {
+    AdamWDesc t[kMaxTensors];
+    uint32_t first[kMaxTensors + 1];
+    int32_t count;
+    const float* grad_scale;
+    float b1, c1, b2, c2;   // betas and 1 - beta
+    float rbc2;             // 1 / sqrt(1 - b2^t)
+    float eps;
+};
+static_assert(sizeof(AdamWArgs) <= 4096, "kernel arguments");
+
+__device__ __forceinline__ float fin_abs(float x) {
+    const float a = __builtin_fabsf(x);
+    return a < __builtin_inff() ? a : 0.0f;   // NaN compares false
+}
+
+// max over the 32 lanes of a half-wave
+__device__ __forceinline__ float half_max(float x) {
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) x = __builtin_fmaxf(x, __shfl_xor(x, o));
+    return x;
+}
+
+// e4m3 codes of x[0..7] * inv, packed; LEAST: nonzero values keep at least 2^-9 (code 1)
+template <bool LEAST>
+__device__ __forceinline__ uint2 encode8(const float (&x)[8], float inv) {
+    uint32_t w[2];
+#pragma unroll
+    for (int q = 0; q < 2; ++q) {
+        float y[4];
+        uint32_t bad = 0;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            const float a = x[4 * q + e];
+            // finite values are within 448 (1 + 2^-23); the clamp keeps the conversion in range
+            y[e] = __builtin_fminf(__builtin_fmaxf(__fmul_rn(a, inv), -448.0f), 448.0f);
+            if (LEAST) y[e] = a > 0.0f && inv > 0.0f ? __builtin_fmaxf(y[e], 0x1p-9f) : y[e];
+            if (!(__builtin_fabsf(a) < __builtin_inff())) bad |= 0x7fu << (8 * e);
+        }
+        int v = __builtin_amdgcn_cvt_pk_fp8_f32(y[0], y[1], 0, false);
+        v = __builtin_amdgcn_cvt_pk_fp8_f32(y[2], y[3], v, true);
+        w[q] = (uint32_t)v | bad;
+    }
+    return make_uint2(w[0], w[1]);
+}
+
+__device__ __forceinline__ void decode8(uint2 c, float scale, float (&x)[8]) {
+    const uint32_t w[2] = {c.x, c.y};
+#pragma unroll
+    for (int q = 0; q < 2; ++q) {
+        x[4 * q + 0] = __builtin_amdgcn_cvt_f32_fp8((int)w[q], 0) * scale;
+        x[4 * q + 1] = __builtin_amdgcn_cvt_f32_fp8((int)w[q], 1) * scale;
+        x[4 * q + 2] = __builtin_amdgcn_cvt_f32_fp8((int)w[q], 2) * scale;
+        x[4 * q + 3] = __builtin_amdgcn_cvt_f32_fp8((int)w[q], 3) * scale;
+    }
+}
+
+// 8 elements from i (f32, or bf16 widened); elements at n and beyond read as zero
+template <bool VEC>
+__device__ __forceinline__ void load8(const void* base, bool bf16, int64_t i, int64_t n, float (&x)[8]) {
+    if (VEC && i + 8 <= n) {
+        if (bf16) {
+            const uint4 u = *(const uint4*)((const uint16_t*)base + i);
+            const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                x[2 * e] = __uint_as_float(w[e] << 16);
+                x[2 * e + 1] = __uint_as_float(w[e] & 0xffff0000u);
+            }
+        } else {
+            const float4 a = *(const float4*)((const float*)base + i), b = *(const float4*)((const float*)base + i + 4);
+            x[0] = a.x, x[1] = a.y, x[2] = a.z, x[3] = a.w, x[4] = b.x, x[5] = b.y, x[6] = b.z, x[7] = b.w;
+        }
+        return;
+    }
+#pragma unroll
+    for (int e = 0; e < 8; ++e)
+        x[e] = i + e < n ? (bf16 ? bf16_bits_to_f32(((const uint16_t*)base)[i + e]) : ((const float*)base)[i + e]) : 0.0f;
+}
+
+template <bool VEC>
+__device__ __forceinline__ void store8(void* base, bool bf16, int64_t i, int64_t n, const float (&x)[8]) {
+    if (VEC && i + 8 <= n) {
+        if (bf16) {
+            uint32_t w[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) w[e] = f32_to_bf16_bits(x[2 * e]) | (f32_to_bf16_bits(x[2 * e + 1]) << 16);
+            *(uint4*)((uint16_t*)base + i) = make_uint4(w[0], w[1], w[2], w[3]);
+        } else {
+            *(float4*)((float*)base + i) = make_float4(x[0], x[1], x[2], x[3]);
+            *(float4*)((float*)base + i + 4) = make_float4(x[4], x[5], x[6], x[7]);
+        }
+        return;
+    }
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+        if (i + e >= n) continue;
+        if (bf16) ((uint16_t*)base)[i + e] = (uint16_t)f32_to_bf16_bits(x[e]);
+        else ((float*)base)[i + e] = x[e];
+    }
+}
+
+template <bool VEC>
+__device__ __forceinline__ uint2 load_codes(const void* base, int64_t i, int64_t n) {
+    if (VEC && i + 8 <= n) return *(const uint2*)((const uint8_t*)base + i);
+    uint32_t w[2] = {0, 0};
+#pragma unroll
+    for (int e = 0; e < 8; ++e)
+        if (i + e < n) w[e >> 2] |= (uint32_t)((const uint8_t*)base)[i + e] << (8 * (e & 3));
+    return make_uint2(w[0], w[1]);
+}
+
+template <bool VEC>
+__device__ __forceinline__ void store_codes(void* base, int64_t i, int64_t n, uint2 c) {
+    if (VEC && i + 8 <= n) {
+        *(uint2*)((uint8_t*)base + i) = c;
+        return;
+    }
+    const uint32_t w[2] = {c.x, c.y};
+#pragma unroll
+    for (int e = 0; e < 8; ++e)
+        if (i + e < n) ((uint8_t*)base)[i + e] = (uint8_t)(w[e >> 2] >> (8 * (e & 3)));
+}
+
+template <bool S8, bool VEC>
+__device__ __forceinline__ void adamw_pass(const AdamWArgs& a, const AdamWDesc& t, int64_t i, float gs) {
+    const bool pb = (t.flags & kPBf16) != 0, gb = (t.flags & kGBf16) != 0;
+    const int64_t n = t.n;
+    float p[8], g[8], m[8], v[8], r[8];
+    load8<VEC>(t.p, pb, i, n, p);
+    load8<VEC>(t.g, gb, i, n, g);
+    const int64_t blk = i >> 8;
+    if constexpr (S8) {
+        // lanes past the end hold zeros; their block may not exist
+        const bool in = i < n;
+        const float sm = in ? t.ms[blk] : 0.0f, sv = in ? t.vs[blk] : 0.0f;
+        decode8(load_codes<VEC>(t.m, i, n), sm, m);
+        decode8(load_codes<VEC>(t.v, i, n), sv, v);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) v[e] = __fmul_rn(v[e], v[e]);
+    } else {
+        load8<VEC>(t.m, false, i, n, m);
+        load8<VEC>(t.v, false, i, n, v);
+    }
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+        const float x = g[e] * gs;
+        m[e] = __fadd_rn(__fmul_rn(a.b1, m[e]), __fmul_rn(a.c1, x));
+        v[e] = __fadd_rn(__fmul_rn(a.b2, v[e]), __fmul_rn(__fmul_rn(a.c2, x), x));
+        // 8-bit states: correctly rounded, it decides codes; otherwise the hardware's (1 ulp)
+        r[e] = S8 ? sqrtf(v[e]) : __builtin_amdgcn_sqrtf(v[e]);
+        const float d = __builtin_fmaf(r[e], a.rbc2, a.eps);
+        p[e] = __builtin_fmaf(-t.alpha, m[e] * __builtin_amdgcn_rcpf(d), p[e] * t.decay);
+    }
+    store8<VEC>(t.p, pb, i, n, p);
+    if (t.c) store8<VEC>(t.c, true, i, n, p);
+    if constexpr (S8) {
+        float mm = 0.0f, mv = 0.0f;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            mm = __builtin_fmaxf(mm, fin_abs(m[e]));
+            mv = __builtin_fmaxf(mv, fin_abs(r[e]));
+        }
+        mm = half_max(mm);
+        mv = half_max(mv);
+        const bool zm = mm < 0x1p-118f, zv = mv < 0x1p-118f;
+        store_codes<VEC>(t.m, i, n, encode8<false>(m, zm ? 0.0f : __fmul_rn(448.0f, 1.0f / mm)));
+        store_codes<VEC>(t.v, i, n, encode8<true>(r, zv ? 0.0f : __fmul_rn(448.0f, 1.0f / mv)));
+        if ((threadIdx.x & 31) == 0 && i < n) {
+            t.ms[blk] = zm ? 0.0f : mm * (1.0f / 448.0f);
+            t.vs[blk] = zv ? 0.0f : mv * (1.0f / 448.0f);
+        }
+    } else {
+        store8<VEC>(t.m, false, i, n, m);
+        store8<VEC>(t.v, false, i, n, v);
+    }
+}
+
+template <bool S8>
+__global__ __launch_bounds__(256) void adamw_kernel(AdamWArgs a) {
+    const uint32_t b = blockIdx.x;
+    int lo = 0, hi = a.count - 1;   // the last tensor whose first block is at or before b
+    while (lo < hi) {
+        const int mid = (lo + hi + 1) >> 1;
+        if (a.first[mid] <= b) lo = mid;
+        else hi = mid - 1;
+    }
+    const AdamWDesc& t = a.t[lo];
+    const float gs = a.grad_scale ? *a.grad_scale : 1.0f;
+    const int64_t i0 = (int64_t)(b - a.first[lo]) * kChunk + threadIdx.x * kPerThread;
+    // a block of 256 elements is 32 consecutive lanes, so a half-wave is in or past the end as
+    // a whole except where the tensor ends inside its block
+#pragma unroll
+    for (int k = 0; k < kPasses; ++k) {
+        const int64_t i = i0 + (int64_t)k * kPass;
+        if ((i & ~(int64_t)255) >= t.n) break;
+        if (t.flags & kVec) adamw_pass<S8, true>(a, t, i, gs);
+        else adamw_pass<S8, false>(a, t, i, gs);
+    }
+}
+
+nm_status launch_adamw(const nm_adamw_tensor* ts, int count, nm_dtype sdt, double lr, double beta1, double beta2,
+                       double eps, int64_t step, const float* grad_scale, hipStream_t s) {
+    AdamWArgs a;
+    const double bc1 = 1.0 - pow(beta1, (double)step), bc2 = 1.0 - pow(beta2, (double)step);
+    a.grad_scale = grad_scale;
+    a.b1 = (float)beta1;
+    a.c1 = (float)(1.0 - beta1);
+    a.b2 = (float)beta2;
+    a.c2 = (float)(1.0 - beta2);
+    a.rbc2 = (float)(1.0 / sqrt(bc2));
+    a.eps = (float)eps;
+    const bool s8 = sdt == NM_FP8;
+    const int64_t most = (int64_t)1 << 30;   // blocks of one launch
+    int k = 0;
+    int64_t blocks = 0;
+    auto flush = [&]() -> nm_status {
+        if (!k) return NM_OK;
+        a.count = k;
+        a.first[k] = (uint32_t)blocks;
+        if (s8) hipLaunchKernelGGL(adamw_kernel<true>, dim3((unsigned)blocks), dim3(256), 0, s, a);
+        else hipLaunchKernelGGL(adamw_kernel<false>, dim3((unsigned)blocks), dim3(256), 0, s, a);
+        k = 0;
+        blocks = 0;
+        return check_launch("nm_adamw");
+    };
+    for (int i = 0; i < count; ++i) {
+        const nm_adamw_tensor& t = ts[i];
+        if (t.n == 0) continue;
+        const int64_t nb = ceil_div(t.n, kChunk);
+        if (k == kMaxTensors || blocks + nb > most) {
+            const nm_status st = flush();
+            if (st != NM_OK) return st;
+        }
+        const double l = lr * (double)t.lr_scale;
+        AdamWDesc& d = a.t[k];
+        d.p = t.p;
+        d.g = t.g;
+        d.m = t.m;
+        d.v = t.v;
+        d.ms = t.m_scale;
+        d.vs = t.v_scale;
+        d.c = (uint16_t*)t.copy;
+        d.n = t.n;
+        d.alpha = (float)(l / bc1);
+        d.decay = (float)(1.0 - l * (double)t.weight_decay);
+        const uintptr_t al = (uintptr_t)t.p | (uintptr_t)t.g | (uintptr_t)t.copy |
+                             (s8 ? ((uintptr_t)t.m | (uintptr_t)t.v) << 1 : (uintptr_t)t.m | (uintptr_t)t.v);
+        d.flags = (t.pdt == NM_BF16 ? kPBf16 : 0u) | (t.gdt == NM_BF16 ? kGBf16 : 0u) | ((al & 15u) == 0 ? kVec : 0u);
+        d.pad = 0;
+        a.first[k] = (uint32_t)blocks;
+        blocks += nb;
+        ++k;
+    }
+    return flush();
+}
+
+}  // namespace nm

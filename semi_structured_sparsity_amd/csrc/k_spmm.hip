@@ -103,6 +103,11 @@ struct SpmmArgs {
     int64_t ldsw;
     float eps;
     double* mpart;
+    // gradients at the packed positions (dense split ring): the stacked B rows hold one or two
+    // weights of rowsp rows each, prows of them real; positions and outputs of the second
+    const uint32_t* idx2;
+    void* Y2;
+    int64_t rowsp;
 };
 
 // Per-dtype step geometry of the register-staged kernel: a step stages 128 bytes of
@@ -1123,6 +1128,68 @@ __device__ __forceinline__ Moments store_score_tile(const SpmmArgs& a, const f32
     return m;
 }
 
+// Gradient of packed 2:4 values: of the tile's columns k (rows rw .. of the accumulators) of
+// weight row r (the lane's token, from tw) only the kept positions are stored.  Elements
+// 4g .. 4g+3 of a lane's sub-tile are columns 32 i + 8 g + 4 h .. + 3, one group of 4, whose
+// two 2-bit positions are bits 4 (2 g + h) .. of the row's index word of those 32 columns.  A
+// lane's 8 kept values alternate in pairs with the other half-wave's; two swaps across the
+// halves leave each lane with the 8 consecutive values of 16 columns (K is a multiple of 16,
+// so all of them exist or none).
+template <int SR, int ST>
+__device__ __forceinline__ void store_grad_tile(const SpmmArgs& a, const f32x16_t (&acc)[SR][ST], int64_t rw,
+                                                int64_t tw, int lane) {
+    const int h = lane >> 5, l32 = lane & 31;
+#pragma unroll
+    for (int j = 0; j < ST; ++j) {
+        const int64_t q = tw + j * 32 + l32;   // stacked row
+        const int mat = q >= a.rowsp ? 1 : 0;
+        const int64_t r = q - mat * a.rowsp;
+        const bool row_ok = q < a.Mtok && r < a.prows;
+        const uint32_t* irow = (mat ? a.idx2 : a.idx) + (row_ok ? r : 0) * a.ldi;
+        uint8_t* orow = (uint8_t*)(mat ? a.Y2 : a.Y);
+#pragma unroll
+        for (int i = 0; i < SR; ++i) {
+            const int64_t k = rw + i * 32;
+            const uint32_t word = row_ok && k < a.R ? irow[k >> 5] : 0u;
+            float v0[4], v1[4];
+#pragma unroll
+            for (int g = 0; g < 4; ++g) {
+                const uint32_t b = (word >> (8 * g + 4 * h)) & 15u, p0 = b & 3u, p1 = b >> 2;
+                const float x0 = acc[i][j][4 * g], x1 = acc[i][j][4 * g + 1], x2 = acc[i][j][4 * g + 2],
+                            x3 = acc[i][j][4 * g + 3];
+                const float lo0 = p0 & 1u ? x1 : x0, hi0 = p0 & 1u ? x3 : x2;
+                const float lo1 = p1 & 1u ? x1 : x0, hi1 = p1 & 1u ? x3 : x2;
+                v0[g] = p0 & 2u ? hi0 : lo0;
+                v1[g] = p1 & 2u ? hi1 : lo1;
+            }
+            // lane half h: values of columns k + 16 h .. + 15
+            const int64_t kc = k + 16 * h;
+            const bool ok = row_ok && kc < a.R;
+            const int64_t o = r * a.ldy + kc / 2;
+            if (a.ydt == NM_BF16) {
+                uint32_t w[4];
+#pragma unroll
+                for (int g = 0; g < 4; ++g) w[g] = f32_to_bf16_bits(v0[g]) | (f32_to_bf16_bits(v1[g]) << 16);
+                const auto s0 = __builtin_amdgcn_permlane32_swap(w[0], w[2], false, false);
+                const auto s1 = __builtin_amdgcn_permlane32_swap(w[1], w[3], false, false);
+                if (ok) *(uint4*)((uint16_t*)orow + o) = make_uint4(s0[0], s0[1], s1[0], s1[1]);
+            } else {
+                uint32_t a0[4], a1[4];
+#pragma unroll
+                for (int g = 0; g < 4; ++g) a0[g] = __float_as_uint(v0[g]), a1[g] = __float_as_uint(v1[g]);
+                const auto s0 = __builtin_amdgcn_permlane32_swap(a0[0], a0[2], false, false);
+                const auto s1 = __builtin_amdgcn_permlane32_swap(a1[0], a1[2], false, false);
+                const auto s2 = __builtin_amdgcn_permlane32_swap(a0[1], a0[3], false, false);
+                const auto s3 = __builtin_amdgcn_permlane32_swap(a1[1], a1[3], false, false);
+                if (ok) {
+                    *(uint4*)((float*)orow + o) = make_uint4(s0[0], s1[0], s0[1], s1[1]);
+                    *(uint4*)((float*)orow + o + 4) = make_uint4(s2[0], s3[0], s2[1], s3[1]);
+                }
+            }
+        }
+    }
+}
+
 // ------------------------------------------------------------------ dense split ring (bf16)
 // Y = X W^T for a dense bf16 weight W [R, K] (ldv) with the split ring's tile, waves,
 // swizzles, DMA and epilogue, and dense MFMA (v_mfma_f32_32x32x16_bf16, whose operand and
@@ -1149,7 +1216,12 @@ __device__ __forceinline__ Moments store_score_tile(const SpmmArgs& a, const f32
 // for the A stages then measured the same as 2).
 // HUTCH_SCORE: HUTCH whose epilogue writes the score of D (store_score_tile) and the block's
 // moments of it instead of D.
-// MODE: 0 plain, 1 HUTCH, 2 GEN, 3 HUTCH_SCORE.
+// GRADX: the plain product with its stages split over gridDim.y blocks (f32 partials,
+// summed by spmm_reduce_kernel).
+// GRADV: the gradient of packed 2:4 values: rows of the tile are columns k of the weight (A:
+// X transposed), tokens are rows r of the weight (B: dY transposed), and the epilogue writes
+// only the two kept positions of each group of 4 (store_grad_tile).
+// MODE: 0 plain, 1 HUTCH, 2 GEN, 3 HUTCH_SCORE, 4 GRADX, 5 GRADV.
 template <int SR, int ST, int WRN, int WTN, int MODE = 0, int SK = 64, int NS = 2>
 __global__ __launch_bounds__(64 * WRN * WTN, 1) void dense_ring_kernel(SpmmArgs a) {
     constexpr bool HUTCH = MODE == 1 || MODE == 3, GEN = MODE == 2;
@@ -1171,14 +1243,16 @@ __global__ __launch_bounds__(64 * WRN * WTN, 1) void dense_ring_kernel(SpmmArgs 
     int tr, tt;
     tile_of(blockIdx.x, gridDim.x, a.tiles_r, a.tiles_t, tr, tt);
     const int64_t r0 = (int64_t)tr * BR, t0 = (int64_t)tt * BT;
-    const int nsteps = a.nsteps;   // K / SK >= 1 (HUTCH: probes * stages per probe)
+    // K / SK >= 1 (HUTCH: probes * stages per probe; GRADX: this split's, from s_begin)
+    const int s_begin = MODE == 4 ? (int)blockIdx.y * a.steps_per_split : 0;
+    const int nsteps = MODE == 4 && a.nsteps - s_begin > a.steps_per_split ? a.steps_per_split : a.nsteps - s_begin;
     const int PS = HUTCH ? a.pstages : nsteps;
     const uint32_t sbase = lds_addr(smem);
     // row / token r of CH chunks: logical chunk c at c ^ sw(r) (16 consecutive rows read by a
     // 16-byte LDS read then hit 64 distinct banks)
     auto sw = [](int r) { return CH == 8 ? ((r >> 1) & 7) : ((r >> 2) & 3); };
-    const void* baseW = uniform_ptr(a.vals + r0 * a.ldv * 2);
-    const void* baseX = uniform_ptr(a.X + t0 * a.ldx * 2);
+    const void* baseW = uniform_ptr(a.vals + r0 * a.ldv * 2 + (int64_t)s_begin * ROWB);
+    const void* baseX = uniform_ptr(a.X + t0 * a.ldx * 2 + (int64_t)s_begin * ROWB);
     const int64_t rmax = a.R - 1 - r0, tmax = a.Mtok - 1 - t0;
     uint32_t oW[NWL], oX[NXL];
     // GEN: half-wave h of a lane's B sub-tiles j = 0, 1 draws the Rademacher words of
@@ -1415,6 +1489,15 @@ __global__ __launch_bounds__(64 * WRN * WTN, 1) void dense_ring_kernel(SpmmArgs 
             __syncthreads();
         }
         if (tid < 3) a.mpart[(int64_t)tid * gridDim.x + blockIdx.x] = sh[tid * NT];
+    } else if constexpr (MODE == 5) {
+        store_grad_tile<SR, ST>(a, acc, r0 + wr * SR * 32, t0 + wt * ST * 32, lane);
+    } else if (MODE == 4 && a.part) {   // this split's partial tile into [split][Mtok][R]
+        SpmmArgs b = a;
+        b.Y = (float*)a.part + (int64_t)blockIdx.y * a.Mtok * a.R;
+        b.ydt = NM_F32;
+        b.ldy = a.R;
+        store_tile<uint16_t, SR, ST>(b, acc, r0 + wr * SR * 32, t0 + wt * ST * 32, false,
+                                     (uint32_t*)smem + wave * kStageWords<SR>, lane);
     } else {
         store_tile<uint16_t, SR, ST>(a, acc, r0 + wr * SR * 32, t0 + wt * ST * 32, r0 + BR <= a.R && t0 + BT <= a.Mtok,
                                      (uint32_t*)smem + wave * kStageWords<SR>, lane);
@@ -2658,6 +2741,135 @@ nm_status launch_hutch_u_ring(const uint16_t* X, int64_t ldx, int64_t n, int64_t
     hipLaunchKernelGGL((dense_ring_kernel<SR, ST, WRN, WTN, 2, kDenseSK, kDenseNS>), dim3((unsigned)tiles),
                        dim3(64 * WRN * WTN), 0, s, a);
     return check_launch("nm_hdiag_hutchinson");
+}
+
+// ------------------------------------------------------------------ gated feed-forward block
+// H = act(G) . U (and the rounded G and U) from the two products in f32, P [2][Mtok][R].
+template <int ACT>
+__global__ __launch_bounds__(256) void glu_combine_kernel(const float* __restrict__ P, GluIn g) {
+    const int64_t total = g.Mtok * g.R;
+    for (int64_t t = (int64_t)blockIdx.x * blockDim.x + threadIdx.x; t < total; t += (int64_t)gridDim.x * blockDim.x) {
+        const int64_t m = t / g.R, r = t - m * g.R;
+        const float x = P[t], u = P[total + t];
+        const float h = act_value<ACT>(x) * u;
+        if (g.hdt == NM_F32) ((float*)g.H)[m * g.ldh + r] = h;
+        else ((uint16_t*)g.H)[m * g.ldh + r] = (uint16_t)f32_to_bf16_bits(h);
+        if (g.G) {
+            ((uint16_t*)g.G)[m * g.ldg + r] = (uint16_t)f32_to_bf16_bits(x);
+            ((uint16_t*)g.U)[m * g.ldg + r] = (uint16_t)f32_to_bf16_bits(u);
+        }
+    }
+}
+
+#define NM_BY_ACT(act, CALL)                                       \
+    do {                                                           \
+        if ((act) == NM_ACT_SILU) CALL(NM_ACT_SILU);               \
+        else if ((act) == NM_ACT_GELU) CALL(NM_ACT_GELU);          \
+        else if ((act) == NM_ACT_GELU_TANH) CALL(NM_ACT_GELU_TANH); \
+        else CALL(NM_ACT_RELU2);                                   \
+    } while (0)
+
+size_t glu_ws(int64_t Mtok, int64_t K, int64_t R, int Ns, nm_dtype xdt) {
+    return 2 * round256((size_t)Mtok * (size_t)R * 4) + spmm_ws(Mtok, K, R, Ns, xdt);
+}
+
+nm_status launch_glu(const GluIn& g, void* ws, hipStream_t s) {
+    float* P = (float*)ws;
+    const size_t one = (size_t)g.Mtok * (size_t)g.R;
+    uint8_t* rest = (uint8_t*)ws + 2 * round256(one * 4);
+    const size_t need = spmm_ws(g.Mtok, g.K, g.R, g.Ns, g.xdt);
+    for (int i = 0; i < 2; ++i) {
+        const nm_status st = spmm_impl("nm_spmm_glu", g.X, g.xdt, g.Mtok, g.K, g.ldx, g.vals[i], g.idx[i], g.R, g.ldv,
+                                       g.ldi, g.Ns, g.x_scale, g.scale[i], nullptr, P + i * one, NM_F32, g.R, rest,
+                                       need, s);
+        if (st != NM_OK) return st;
+    }
+    const dim3 grid(grid_cap(ceil_div(g.Mtok * g.R, 256), 16384));
+#define NM_COMBINE(A) hipLaunchKernelGGL(glu_combine_kernel<A>, grid, dim3(256), 0, s, (const float*)P, g)
+    NM_BY_ACT(g.act, NM_COMBINE);
+#undef NM_COMBINE
+    return check_launch("nm_spmm_glu");
+}
+
+// ------------------------------------------------------------------ gradients
+// Splits of the summed dimension (Rn / 64 stages) of dX: the count whose rounds of blocks take
+// least, a stage of a 256 x 256 tile measured at about 0.9 us, and the partials written and
+// read back at about 4 TB/s with a launch of its own.
+static int grad_x_splits(int64_t M, int64_t K, int64_t Rn) {
+    const int64_t cus = device_cus(), tiles = ceil_div(K, 256) * ceil_div(M, 256), ns = Rn / kDenseSK;
+    int best = 1;
+    double best_us = 1e30;
+    for (int64_t ks = 1; ks <= 16 && ks * 4 <= ns + 3; ++ks) {
+        const double us = 0.9 * (double)(ceil_div(tiles * ks, cus) * (ceil_div(ns, ks) + 4)) +
+                          (ks > 1 ? 4.0 + 8e-6 / 4.0 * (double)(ks * M * K) : 0.0);
+        if (us < best_us) {
+            best_us = us;
+            best = (int)ks;
+        }
+    }
+    return best;
+}
+
+size_t grad_x_part_bytes(int64_t M, int64_t K, int64_t Rn) {
+    const int ks = grad_x_splits(M, K, Rn);
+    return ks > 1 ? (size_t)ks * (size_t)M * (size_t)K * 4 : 0;
+}
+
+nm_status launch_grad_x(const uint16_t* WT, int64_t Rn, const uint16_t* B, int64_t ldb, int64_t M, int64_t K, void* dX,
+                        nm_dtype dxdt, int64_t lddx, float* part, hipStream_t s) {
+    constexpr int SR = 4, ST = 2, WRN = 2, WTN = 4, BR = WRN * SR * 32, BT = WTN * ST * 32;
+    SpmmArgs a{};
+    a.vals = (const uint8_t*)WT;   // A: rows k of the transposed weight
+    a.ldv = Rn;
+    a.X = (const uint8_t*)B;       // B: token rows of dY
+    a.ldx = ldb;
+    a.Y = dX;
+    a.ydt = (int)dxdt;
+    a.ldy = lddx;
+    a.Mtok = M;
+    a.R = K;
+    a.K = Rn;
+    a.nsteps = (int)(Rn / kDenseSK);
+    a.steps_per_split = (int)ceil_div(a.nsteps, grad_x_splits(M, K, Rn));
+    a.KS = (int)ceil_div(a.nsteps, a.steps_per_split);
+    a.part = a.KS > 1 ? part : nullptr;
+    a.tiles_r = (int)ceil_div(K, BR);
+    a.tiles_t = (int)ceil_div(M, BT);
+    hipLaunchKernelGGL((dense_ring_kernel<SR, ST, WRN, WTN, 4, kDenseSK, kDenseNS>),
+                       dim3((unsigned)(a.tiles_r * a.tiles_t), (unsigned)a.KS), dim3(64 * WRN * WTN), 0, s, a);
+    if (a.KS > 1) {
+        const dim3 g(grid_cap(ceil_div(M * K, 256), 8192));
+        hipLaunchKernelGGL(spmm_reduce_kernel<float>, g, dim3(256), 0, s, a);
+    }
+    return check_launch("gradient of the activations");
+}
+
+nm_status launch_grad_v(const uint16_t* XT, const uint16_t* DT, int64_t Mp, const GradIn& in, const GradOut& out,
+                        int nmat, int64_t Rp, hipStream_t s) {
+    constexpr int SR = 4, ST = 2, WRN = 2, WTN = 4, BR = WRN * SR * 32, BT = WTN * ST * 32;
+    SpmmArgs a{};
+    a.vals = (const uint8_t*)XT;   // A: columns k of the weight
+    a.ldv = Mp;
+    a.X = (const uint8_t*)DT;      // B: stacked rows r of the weights
+    a.ldx = Mp;
+    a.Y = out.dV[0];
+    a.Y2 = out.dV[1];
+    a.ydt = (int)out.dvdt;
+    a.ldy = out.lddv;
+    a.idx = in.idx[0];
+    a.idx2 = in.idx[1];
+    a.ldi = in.ldi;
+    a.Mtok = nmat * Rp;
+    a.rowsp = Rp;
+    a.prows = in.R;
+    a.R = in.K;
+    a.K = Mp;
+    a.nsteps = (int)(Mp / kDenseSK);
+    a.tiles_r = (int)ceil_div(in.K, BR);
+    a.tiles_t = (int)ceil_div(a.Mtok, BT);
+    hipLaunchKernelGGL((dense_ring_kernel<SR, ST, WRN, WTN, 5, kDenseSK, kDenseNS>),
+                       dim3((unsigned)(a.tiles_r * a.tiles_t)), dim3(64 * WRN * WTN), 0, s, a);
+    return check_launch("gradient of the packed values");
 }
 
 }  // namespace nm

@@ -681,4 +681,215 @@ nm_status nm_spmm_lowrank(const void* X, int64_t Mtok, int64_t K, int64_t ldx, c
                                (hipStream_t)stream);
 }
 
+size_t nm_spmm_glu_workspace(int64_t Mtok, int64_t K, int64_t R, int Ns, nm_dtype xdt) {
+    if (Mtok <= 0 || K <= 0 || R <= 0) return 0;
+    return glu_ws(Mtok, K, R, Ns, xdt);
+}
+
+static bool act_ok(nm_act a) { return a == NM_ACT_SILU || a == NM_ACT_GELU || a == NM_ACT_GELU_TANH || a == NM_ACT_RELU2; }
+
+nm_status nm_spmm_glu(const void* X, nm_dtype xdt, int64_t Mtok, int64_t K, int64_t ldx, const void* vals_g,
+                      const uint32_t* idx_g, const void* vals_u, const uint32_t* idx_u, nm_dtype vdt, int64_t R,
+                      int64_t ldv, int64_t ldi, int Ns, const float* x_scale, float g_scale, float u_scale,
+                      nm_act act, void* H, nm_dtype hdt, int64_t ldh, void* G, void* U, int64_t ldg, void* ws,
+                      size_t ws_bytes, nm_stream_t stream) {
+    const char* fn = "nm_spmm_glu";
+    NM_REQ(act_ok(act), NM_ERR_SHAPE, "%s: unknown activation", fn);
+    NM_REQ(hdt == NM_BF16 || hdt == NM_F32, NM_ERR_DTYPE, "%s: H must be bf16 or f32", fn);
+    NM_REQ(!G == !U, NM_ERR_NULL, "%s: G and U are both given or both NULL", fn);
+    // each projection is held to the checks of the plain product (its output: H)
+    bool run = false;
+    nm_status st = spmm_check(fn, X, xdt, Mtok, K, ldx, vals_g, vdt, idx_g, R, ldv, ldi, Ns, x_scale, H, hdt, ldh, &run);
+    if (st != NM_OK) return st;
+    st = spmm_check(fn, X, xdt, Mtok, K, ldx, vals_u, vdt, idx_u, R, ldv, ldi, Ns, x_scale, H, hdt, ldh, &run);
+    if (st != NM_OK || !run) return st;
+    NM_REQ(((uintptr_t)H & (uintptr_t)(esize(hdt) - 1)) == 0 && ((uintptr_t)G & 1u) == 0 && ((uintptr_t)U & 1u) == 0,
+           NM_ERR_ALIGN, "%s: an output is not element-aligned", fn);
+    const size_t need = glu_ws(Mtok, K, R, Ns, xdt);
+    NM_REQ(need == 0 || (ws && ws_bytes >= need), NM_ERR_WORKSPACE, "%s: workspace of %zu bytes needed", fn, need);
+    NM_REQ(need == 0 || aligned16(ws), NM_ERR_ALIGN, "%s: ws must be 16-byte aligned", fn);
+    const int64_t Kl = Ns ? K / (2 * Ns) * 4 * (Ns - 1) : K, es = esize(xdt), iw = (Kl + 31) / 32;
+    const Range in[] = {span(X, Mtok, K, ldx, es),       span(vals_g, R, Kl / 2, ldv, es), span(idx_g, R, iw, ldi, 4),
+                        span(vals_u, R, Kl / 2, ldv, es), span(idx_u, R, iw, ldi, 4),       span(x_scale, 1, Mtok, Mtok, 4)};
+    Range out[4] = {span(H, Mtok, R, ldh, esize(hdt)), {0, 0}, {0, 0}, {0, 0}};
+    if (need) out[3] = Range{(uintptr_t)ws, (uintptr_t)ws + need};
+    if (G) {
+        NM_REQ(ldg >= R, NM_ERR_SHAPE, "%s: ldg < R", fn);
+        out[1] = span(G, Mtok, R, ldg, 2);
+        out[2] = span(U, Mtok, R, ldg, 2);
+    }
+    for (int i = 0; i < 4; ++i) {
+        for (const Range& r : in) NM_REQ(!overlap(out[i], r), NM_ERR_ALIAS, "%s: an output or ws overlaps an input", fn);
+        for (int j = 0; j < i; ++j) NM_REQ(!overlap(out[i], out[j]), NM_ERR_ALIAS, "%s: outputs or ws overlap", fn);
+    }
+    GluIn g{};
+    g.X = X;
+    g.xdt = xdt;
+    g.Mtok = Mtok;
+    g.K = K;
+    g.ldx = ldx;
+    g.vals[0] = vals_g;
+    g.vals[1] = vals_u;
+    g.idx[0] = idx_g;
+    g.idx[1] = idx_u;
+    g.R = R;
+    g.ldv = ldv;
+    g.ldi = ldi;
+    g.Ns = Ns;
+    g.x_scale = x_scale;
+    g.scale[0] = g_scale;
+    g.scale[1] = u_scale;
+    g.act = act;
+    g.H = H;
+    g.hdt = hdt;
+    g.ldh = ldh;
+    g.G = G;
+    g.U = U;
+    g.ldg = ldg;
+    return launch_glu(g, ws, (hipStream_t)stream);
+}
+
+// Checks and launch of both backward calls; nmat 2: the gated block (G and U given).
+static nm_status backward_impl(const char* fn, GradIn in, GradOut out, int nmat, void* ws, size_t ws_bytes,
+                               nm_stream_t stream) {
+    const int64_t M = in.M, K = in.K, R = in.R, most = 1 << 21;
+    NM_REQ(M >= 0 && K >= 0 && R >= 0, NM_ERR_SHAPE, "%s: negative size", fn);
+    NM_REQ(M <= most && K <= most && R <= most, NM_ERR_SHAPE, "%s: sizes up to 2^21", fn);
+    NM_REQ(K % 16 == 0, NM_ERR_SHAPE, "%s: K must be a multiple of 16", fn);
+    const bool dv = out.dV[0] != nullptr;
+    NM_REQ(nmat == 1 || !out.dV[0] == !out.dV[1], NM_ERR_NULL, "%s: dVg and dVu are both given or both NULL", fn);
+    NM_REQ(!out.dX || out.dxdt == NM_BF16 || out.dxdt == NM_F32, NM_ERR_DTYPE, "%s: dX must be bf16 or f32", fn);
+    NM_REQ(!dv || out.dvdt == NM_BF16 || out.dvdt == NM_F32, NM_ERR_DTYPE, "%s: dV must be bf16 or f32", fn);
+    if (K == 0 || (!out.dX && !dv)) return NM_OK;
+    // without tokens dV is zero, without rows dX is: nothing but the outputs is touched then
+    const int64_t iw = (K + 31) / 32;
+    if (M > 0 && R > 0) {
+        NM_REQ(in.dY && (nmat == 1 || (in.G && in.U)) && (in.X || !dv), NM_ERR_NULL, "%s: NULL input", fn);
+        for (int i = 0; i < nmat; ++i)
+            NM_REQ(in.idx[i] && (in.vals[i] || !out.dX), NM_ERR_NULL, "%s: NULL weight", fn);
+        NM_REQ(in.lddy >= R && (nmat == 1 || in.ldg >= R) && (!dv || in.ldx >= K) && (!out.dX || in.ldv >= K / 2) &&
+                   in.ldi >= iw,
+               NM_ERR_SHAPE, "%s: leading dimension too small", fn);
+        NM_REQ(((uintptr_t)in.dY & 1u) == 0 && ((uintptr_t)in.G & 1u) == 0 && ((uintptr_t)in.U & 1u) == 0, NM_ERR_ALIGN,
+               "%s: an input is not element-aligned", fn);
+        NM_REQ(!dv || (aligned16(in.X) && in.ldx % 8 == 0), NM_ERR_ALIGN, "%s: X needs 16-byte aligned rows", fn);
+        for (int i = 0; i < nmat; ++i)
+            NM_REQ(((uintptr_t)in.idx[i] & 3u) == 0 && (!out.dX || (aligned16(in.vals[i]) && in.ldv % 8 == 0)),
+                   NM_ERR_ALIGN, "%s: vals need 16-byte aligned rows, idx 4-byte alignment", fn);
+    }
+    const int64_t vs = dv ? esize(out.dvdt) : 2, xs = out.dX ? esize(out.dxdt) : 2;
+    NM_REQ(!out.dX || (out.lddx >= K && ((uintptr_t)out.dX & (uintptr_t)(xs - 1)) == 0), NM_ERR_SHAPE,
+           "%s: lddx < K, or dX not element-aligned", fn);
+    for (int i = 0; dv && i < nmat; ++i)
+        NM_REQ(out.lddv >= K / 2 && aligned16(out.dV[i]) && (out.lddv * vs) % 16 == 0, NM_ERR_ALIGN,
+               "%s: dV needs lddv >= K/2 and 16-byte aligned rows", fn);
+    const size_t need = grad_ws(M, K, R, nmat);
+    NM_REQ(need == 0 || (ws && ws_bytes >= need), NM_ERR_WORKSPACE, "%s: workspace of %zu bytes needed", fn, need);
+    NM_REQ(need == 0 || aligned16(ws), NM_ERR_ALIGN, "%s: ws must be 16-byte aligned", fn);
+    const Range rin[] = {span(in.dY, M, R, in.lddy, 2),         span(in.G, M, R, in.ldg, 2),
+                         span(in.U, M, R, in.ldg, 2),           span(in.X, M, K, in.ldx, 2),
+                         span(in.vals[0], R, K / 2, in.ldv, 2), span(in.vals[1], R, K / 2, in.ldv, 2),
+                         span(in.idx[0], R, iw, in.ldi, 4),     span(in.idx[1], R, iw, in.ldi, 4)};
+    Range rout[4] = {span(out.dX, M, K, out.lddx, xs), span(out.dV[0], R, K / 2, out.lddv, vs),
+                     span(out.dV[1], R, K / 2, out.lddv, vs), {0, 0}};
+    if (need) rout[3] = Range{(uintptr_t)ws, (uintptr_t)ws + need};
+    for (int i = 0; i < 4; ++i) {
+        for (const Range& r : rin) NM_REQ(!overlap(rout[i], r), NM_ERR_ALIAS, "%s: an output or ws overlaps an input", fn);
+        for (int j = 0; j < i; ++j) NM_REQ(!overlap(rout[i], rout[j]), NM_ERR_ALIAS, "%s: outputs or ws overlap", fn);
+    }
+    return launch_grad(in, out, nmat, ws, (hipStream_t)stream);
+}
+
+size_t nm_spmm_backward_workspace(int64_t Mtok, int64_t K, int64_t R) { return grad_ws(Mtok, K, R, 1); }
+
+nm_status nm_spmm_backward(const void* dY, int64_t lddy, const void* X, int64_t ldx, int64_t Mtok, int64_t K,
+                           const void* vals, const uint32_t* idx, int64_t R, int64_t ldv, int64_t ldi, void* dX,
+                           nm_dtype dxdt, int64_t lddx, void* dV, nm_dtype dvdt, int64_t lddv, void* ws,
+                           size_t ws_bytes, nm_stream_t stream) {
+    GradIn in{};
+    in.dY = (const uint16_t*)dY;
+    in.lddy = lddy;
+    in.X = (const uint16_t*)X;
+    in.ldx = ldx;
+    in.M = Mtok;
+    in.K = K;
+    in.R = R;
+    in.vals[0] = (const uint16_t*)vals;
+    in.idx[0] = idx;
+    in.ldv = ldv;
+    in.ldi = ldi;
+    GradOut out{dX, dxdt, lddx, {dV, nullptr}, dvdt, lddv};
+    return backward_impl("nm_spmm_backward", in, out, 1, ws, ws_bytes, stream);
+}
+
+size_t nm_spmm_glu_backward_workspace(int64_t Mtok, int64_t K, int64_t R) { return grad_ws(Mtok, K, R, 2); }
+
+nm_status nm_spmm_glu_backward(const void* dH, int64_t lddh, const void* G, const void* U, int64_t ldg, nm_act act,
+                               const void* X, int64_t ldx, int64_t Mtok, int64_t K, const void* vals_g,
+                               const uint32_t* idx_g, const void* vals_u, const uint32_t* idx_u, int64_t R,
+                               int64_t ldv, int64_t ldi, void* dX, nm_dtype dxdt, int64_t lddx, void* dVg, void* dVu,
+                               nm_dtype dvdt, int64_t lddv, void* ws, size_t ws_bytes, nm_stream_t stream) {
+    NM_REQ(act_ok(act), NM_ERR_SHAPE, "nm_spmm_glu_backward: unknown activation");
+    GradIn in{};
+    in.dY = (const uint16_t*)dH;
+    in.lddy = lddh;
+    in.G = (const uint16_t*)G;
+    in.U = (const uint16_t*)U;
+    in.ldg = ldg;
+    in.act = act;
+    in.X = (const uint16_t*)X;
+    in.ldx = ldx;
+    in.M = Mtok;
+    in.K = K;
+    in.R = R;
+    in.vals[0] = (const uint16_t*)vals_g;
+    in.vals[1] = (const uint16_t*)vals_u;
+    in.idx[0] = idx_g;
+    in.idx[1] = idx_u;
+    in.ldv = ldv;
+    in.ldi = ldi;
+    GradOut out{dX, dxdt, lddx, {dVg, dVu}, dvdt, lddv};
+    return backward_impl("nm_spmm_glu_backward", in, out, 2, ws, ws_bytes, stream);
+}
+
+nm_status nm_adamw(const nm_adamw_tensor* tensors, int count, nm_dtype sdt, double lr, double beta1, double beta2,
+                   double eps, int64_t step, const float* grad_scale, nm_stream_t stream) {
+    const char* fn = "nm_adamw";
+    NM_REQ(count >= 0, NM_ERR_SHAPE, "%s: negative count", fn);
+    NM_REQ(sdt == NM_F32 || sdt == NM_FP8, NM_ERR_DTYPE, "%s: states must be f32 or fp8 codes", fn);
+    NM_REQ(step >= 1, NM_ERR_SHAPE, "%s: step counts from 1", fn);
+    NM_REQ(beta1 >= 0.0 && beta1 < 1.0 && beta2 >= 0.0 && beta2 < 1.0 && eps >= 0.0 && lr >= 0.0, NM_ERR_SHAPE,
+           "%s: need 0 <= beta < 1, eps >= 0, lr >= 0", fn);
+    if (count == 0) return NM_OK;
+    NM_REQ(tensors, NM_ERR_NULL, "%s: tensors is NULL", fn);
+    NM_REQ(((uintptr_t)grad_scale & 3u) == 0, NM_ERR_ALIGN, "%s: grad_scale is not element-aligned", fn);
+    const bool s8 = sdt == NM_FP8;
+    for (int i = 0; i < count; ++i) {
+        const nm_adamw_tensor& t = tensors[i];
+        NM_REQ(t.n >= 0 && t.n < (1LL << 40), NM_ERR_SHAPE, "%s: tensor %d has a size out of range", fn, i);
+        NM_REQ((t.pdt == NM_F32 || t.pdt == NM_BF16) && (t.gdt == NM_F32 || t.gdt == NM_BF16), NM_ERR_DTYPE,
+               "%s: tensor %d: p and g must be f32 or bf16", fn, i);
+        if (t.n == 0) continue;
+        NM_REQ(t.p && t.g && t.m && t.v && (!s8 || (t.m_scale && t.v_scale)), NM_ERR_NULL, "%s: tensor %d: NULL pointer",
+               fn, i);
+        const int64_t ps = esize(t.pdt), gs = esize(t.gdt), ss = s8 ? 1 : 4, nb = (t.n + 255) / 256;
+        NM_REQ(((uintptr_t)t.p % ps) == 0 && ((uintptr_t)t.g % gs) == 0 && ((uintptr_t)t.m % ss) == 0 &&
+                   ((uintptr_t)t.v % ss) == 0 && ((uintptr_t)t.copy & 1u) == 0 &&
+                   (!s8 || (((uintptr_t)t.m_scale | (uintptr_t)t.v_scale) & 3u) == 0),
+               NM_ERR_ALIGN, "%s: tensor %d: a pointer is not element-aligned", fn, i);
+        const Range r[] = {span(t.p, 1, t.n, t.n, ps),
+                           span(t.m, 1, t.n, t.n, ss),
+                           span(t.v, 1, t.n, t.n, ss),
+                           span(t.copy, 1, t.n, t.n, 2),
+                           span(s8 ? t.m_scale : nullptr, 1, nb, nb, 4),
+                           span(s8 ? t.v_scale : nullptr, 1, nb, nb, 4),
+                           span(t.g, 1, t.n, t.n, gs),
+                           span(grad_scale, 1, 1, 1, 4)};
+        for (int a = 0; a < 6; ++a)
+            for (int b = a + 1; b < 8; ++b)
+                NM_REQ(!overlap(r[a], r[b]), NM_ERR_ALIAS, "%s: tensor %d: its arrays overlap", fn, i);
+    }
+    return launch_adamw(tensors, count, sdt, lr, beta1, beta2, eps, step, grad_scale, (hipStream_t)stream);
+}
+
 }  // extern "C"

@@ -164,6 +164,47 @@ __device__ __forceinline__ Moments moments_combine(Moments a, Moments b) {
     return Moments{n, a.mean + d * (b.n / n), a.m2 + b.m2 + d * d * (a.n * b.n / n)};
 }
 
+// ------------------------------------------------------------------ activations of gated blocks
+// f = act(g) and d = act'(g), in f32 with the hardware's 2^x and reciprocal (about 1e-7
+// relative).  sigmoid(x) = 1 / (1 + e^-x) is 0 or 1 exactly where e^-x over- or underflows, so
+// large |g| need no special case; the tanh form is g sigmoid(2 t) with the tanh's argument t,
+// which does not cancel for negative g as 1 + tanh(t) would.
+__device__ __forceinline__ float sigmoid_f32(float x) { return __builtin_amdgcn_rcpf(1.0f + __expf(-x)); }
+
+constexpr float kTanhC = 1.5957691216057308f;   // 2 sqrt(2 / pi)
+constexpr float kTanhA = 0.044715f;
+constexpr float kRsqrt2 = 0.70710678118654752f, kRsqrt2Pi = 0.39894228040143268f;
+
+template <int ACT>
+__device__ __forceinline__ float act_value(float g) {
+    if constexpr (ACT == NM_ACT_SILU) return g * sigmoid_f32(g);
+    else if constexpr (ACT == NM_ACT_GELU) return 0.5f * g * erfcf(-g * kRsqrt2);
+    else if constexpr (ACT == NM_ACT_GELU_TANH) return g * sigmoid_f32(kTanhC * g * __builtin_fmaf(kTanhA * g, g, 1.0f));
+    else return g > 0.0f ? g * g : g * 0.0f;   // NaN stays NaN
+}
+
+template <int ACT>
+__device__ __forceinline__ void act_and_grad(float g, float& f, float& d) {
+    if constexpr (ACT == NM_ACT_SILU) {
+        const float t = sigmoid_f32(g);
+        f = g * t;
+        d = __builtin_fmaf(f, 1.0f - t, t);
+    } else if constexpr (ACT == NM_ACT_GELU) {
+        const float c = 0.5f * erfcf(-g * kRsqrt2);
+        f = g * c;
+        d = __builtin_fmaf(g * kRsqrt2Pi, __expf(-0.5f * g * g), c);
+    } else if constexpr (ACT == NM_ACT_GELU_TANH) {
+        const float t = sigmoid_f32(kTanhC * g * __builtin_fmaf(kTanhA * g, g, 1.0f));
+        f = g * t;
+        // t (1 - t) is zero beyond |g| of about 10: g is held to 32 there so that g^2 stays finite
+        const float gc = __builtin_fabsf(g) > 32.0f ? 32.0f : g;
+        d = __builtin_fmaf(gc * t * (1.0f - t) * kTanhC, __builtin_fmaf(3.0f * kTanhA * gc, gc, 1.0f), t);
+    } else {
+        f = g > 0.0f ? g * g : g * 0.0f;
+        d = g > 0.0f ? 2.0f * g : g * 0.0f;
+    }
+}
+
 inline int index_bits(int M) {
     int b = 0;
     while ((1 << b) < M) ++b;
@@ -264,6 +305,61 @@ nm_status launch_dense_ring(const uint16_t* W, int64_t ldw, const uint16_t* X, i
 nm_status launch_bitmap_spmm(const void* X, int64_t Mtok, int64_t K, int64_t ldx, const void* vals, int64_t ldv,
                              const uint8_t* mask, int64_t ldm, const int32_t* offs, int64_t ldo, int64_t R, void* Y,
                              nm_dtype ydt, int64_t ldy, void* ws, size_t ws_bytes, hipStream_t s);
+// gated feed-forward block
+struct GluIn {
+    const void* X;
+    nm_dtype xdt;
+    int64_t Mtok, K, ldx;
+    const void* vals[2];       // gate, up
+    const uint32_t* idx[2];
+    int64_t R, ldv, ldi;
+    int Ns;
+    const float* x_scale;
+    float scale[2];
+    nm_act act;
+    void* H;
+    nm_dtype hdt;
+    int64_t ldh;
+    void *G, *U;
+    int64_t ldg;
+};
+size_t glu_ws(int64_t Mtok, int64_t K, int64_t R, int Ns, nm_dtype xdt);
+nm_status launch_glu(const GluIn& g, void* ws, hipStream_t s);
+// gradients of the sparse layer (G null) and of the gated block (bf16, plain 2:4)
+struct GradIn {
+    const uint16_t* dY;   // dY, or dH of the gated block: [M, R] (lddy)
+    int64_t lddy;
+    const uint16_t *G, *U;   // pre-activations of the gated block, or null
+    int64_t ldg;
+    nm_act act;
+    const uint16_t* X;
+    int64_t ldx, M, K, R;
+    const uint16_t* vals[2];
+    const uint32_t* idx[2];
+    int64_t ldv, ldi;
+};
+struct GradOut {
+    void* dX;   // null: not wanted
+    nm_dtype dxdt;
+    int64_t lddx;
+    void* dV[2];   // null: not wanted
+    nm_dtype dvdt;
+    int64_t lddv;
+};
+size_t grad_ws(int64_t M, int64_t K, int64_t R, int nmat);
+// nmat: 1, or 2 for the gated block
+nm_status launch_grad(const GradIn& in, const GradOut& out, int nmat, void* ws, hipStream_t s);
+// dX [M, K] = B [M, Rn] (ldb) WT^T, WT [K, Rn]: the dense split ring, Rn (a multiple of 64) split over
+// blocks where the tiles leave the CUs short (f32 partials in part, grad_x_part_bytes)
+size_t grad_x_part_bytes(int64_t M, int64_t K, int64_t Rn);
+nm_status launch_grad_x(const uint16_t* WT, int64_t Rn, const uint16_t* B, int64_t ldb, int64_t M, int64_t K, void* dX,
+                        nm_dtype dxdt, int64_t lddx, float* part, hipStream_t s);
+// dV of nmat weights: XT [K, Mp], DT [nmat * Rp, Mp], the kept positions of DT XT^T
+nm_status launch_grad_v(const uint16_t* XT, const uint16_t* DT, int64_t Mp, const GradIn& in, const GradOut& out,
+                        int nmat, int64_t Rp, hipStream_t s);
+// optimiser
+nm_status launch_adamw(const nm_adamw_tensor* ts, int count, nm_dtype sdt, double lr, double beta1, double beta2,
+                       double eps, int64_t step, const float* grad_scale, hipStream_t s);
 // Hutchinson
 size_t hutch_ws(int64_t n, int64_t K, int64_t R, int probes);
 size_t hutch_score_ws(int64_t n, int64_t K, int64_t R, int probes);
