@@ -103,12 +103,34 @@ struct SpmmArgs {
     int64_t ldsw;
     float eps;
     double* mpart;
-    // gradients at the packed positions (dense split ring): the stacked B rows hold one or two
-    // weights of rowsp rows each, prows of them real; positions and outputs of the second
+    // second weight of a pair.  Gradients at the packed positions (dense split ring): the stacked
+    // B rows hold one or two weights of rowsp rows each, prows of them real; positions and
+    // outputs of the second
     const uint32_t* idx2;
     void* Y2;
     int64_t rowsp;
+    // gated block (GLU): vals / idx / w_scale are the gate's and vals2 / idx2 / w_scale2 the up
+    // projection's, R features each; Y is H, Y2 and Y3 the rounded G and U (ldy2) or null
+    const uint8_t* vals2;
+    float w_scale2;
+    int act;
+    void* Y3;
+    int64_t ldy2;
 };
+
+// A gated block's tile interleaves the two weights so that a wave holds the gate and the up
+// accumulators of the same features and tokens: rows come in runs of 2 H, the first H rows of
+// the gate and the next H of the up projection (H = 64 in the many-token kernels, whose waves
+// hold 128 rows, and 32 in the K-split ring, whose waves hold 64).  Every DMA instruction
+// covers rows of one run, so the weight it reads is a wave-uniform choice.
+template <int H>
+__device__ __forceinline__ int glu_mat(int row) {
+    return (row / H) & 1;
+}
+template <int H>
+__device__ __forceinline__ int glu_feature(int row) {
+    return (row / (2 * H)) * H + row % H;
+}
 
 // Per-dtype step geometry of the register-staged kernel: a step stages 128 bytes of
 // activation columns per token.
@@ -623,8 +645,107 @@ __device__ __forceinline__ void store_tile(const SpmmArgs& a, const typename Mma
     }
 }
 
+// h = act(g) u for the four outputs of a lane
+template <int ACT>
+__device__ __forceinline__ void glu4(const float (&g)[4], const float (&u)[4], float (&h)[4]) {
+#pragma unroll
+    for (int e = 0; e < 4; ++e) h[e] = act_value<ACT>(g[e]) * u[e];
+}
+__device__ __forceinline__ void glu4(int act, const float (&g)[4], const float (&u)[4], float (&h)[4]) {
+    if (act == NM_ACT_SILU) glu4<NM_ACT_SILU>(g, u, h);
+    else if (act == NM_ACT_GELU) glu4<NM_ACT_GELU>(g, u, h);
+    else if (act == NM_ACT_GELU_TANH) glu4<NM_ACT_GELU_TANH>(g, u, h);
+    else glu4<NM_ACT_RELU2>(g, u, h);
+}
+// n (1..4) consecutive outputs; vec: all four at once (aligned)
+__device__ __forceinline__ void put4(void* p, bool f32, int64_t o, const float (&f)[4], int n, bool vec) {
+    if (f32) {
+        float* q = (float*)p + o;
+        if (vec) *(float4*)q = make_float4(f[0], f[1], f[2], f[3]);
+        else
+            for (int e = 0; e < n; ++e) q[e] = f[e];
+    } else {
+        uint16_t* q = (uint16_t*)p + o;
+        if (vec) *(uint2*)q = make_uint2(f32_to_bf16_bits(f[0]) | (f32_to_bf16_bits(f[1]) << 16),
+                                         f32_to_bf16_bits(f[2]) | (f32_to_bf16_bits(f[3]) << 16));
+        else
+            for (int e = 0; e < n; ++e) q[e] = (uint16_t)f32_to_bf16_bits(f[e]);
+    }
+}
+
+// Stores a gated block's wave tile: 64 features from fw (accumulator sub-tiles 0, 1 the gate,
+// 2, 3 the up projection) x ST * 32 tokens from tw.  Each 32-token column goes through the
+// wave's LDS buffer as raw accumulators (whole-vector writes); 16 lanes then take the 64
+// features of a token, 4 each, so that the activation is written once in a loop (not once
+// per accumulator) and a token's outputs leave as one 128-byte run.  With split-K partials
+// the raw sums go to part [split][Mtok][2 R], the gate's R first.
+template <typename T, int ST>
+__device__ __forceinline__ void store_glu_tile(const SpmmArgs& a, const typename Mma<T>::Acc (&acc)[4][ST], int64_t fw,
+                                               int64_t tw, int split, uint32_t* stage, int lane) {
+    using AccV = typename Mma<T>::Acc;
+    using AccS = typename Mma<T>::AccS;
+    const int l16 = lane & 15, t4 = lane >> 4;
+    const int ri = l16 >> 3, rq = (l16 & 7) >> 1, rh = l16 & 1;
+    const int64_t r = fw + 4 * l16;
+    const int n = a.R - r >= 4 ? 4 : (int)(a.R - r);
+    const int hs = a.ydt == NM_F32 ? 4 : 2;
+    const bool full = n == 4;
+    const bool vh = full && ((uintptr_t)a.Y % (4 * hs)) == 0 && a.ldy % 4 == 0;
+    const bool vg = full && (((uintptr_t)a.Y2 | (uintptr_t)a.Y3) % 8) == 0 && a.ldy2 % 4 == 0;
+#pragma unroll
+    for (int j = 0; j < ST; ++j) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) *(AccV*)&stage[(i * 64 + lane) * 20] = acc[i][j];
+        // lgkmcnt(0): this wave's LDS writes are done before any lane reads another's
+        __builtin_amdgcn_s_waitcnt(0xc07f);
+        __builtin_amdgcn_wave_barrier();
+        asm volatile("" ::: "memory");
+#pragma unroll 2
+        for (int p = 0; p < 8; ++p) {
+            const int tk = 4 * p + t4;
+            const int64_t tok = tw + j * 32 + tk;
+            const int at = (ri * 64 + tk + 32 * rh) * 20 + 4 * rq;
+            const uint4 rg = *(const uint4*)&stage[at], ru = *(const uint4*)&stage[at + 2 * 64 * 20];
+            if (tok >= a.Mtok || n <= 0) continue;
+            if (a.part) {
+                AccS* pg = (AccS*)a.part + ((int64_t)split * a.Mtok + tok) * 2 * a.R + r;
+                const uint32_t wg[4] = {rg.x, rg.y, rg.z, rg.w}, wu[4] = {ru.x, ru.y, ru.z, ru.w};
+                if (full && a.R % 4 == 0) {
+                    *(uint4*)pg = rg;
+                    *(uint4*)(pg + a.R) = ru;
+                } else {
+                    for (int e = 0; e < n; ++e) {
+                        pg[e] = __builtin_bit_cast(AccS, wg[e]);
+                        pg[e + a.R] = __builtin_bit_cast(AccS, wu[e]);
+                    }
+                }
+                continue;
+            }
+            const float xs = a.x_scale ? a.x_scale[tok] : 1.0f;
+            const float sg = __fmul_rn(a.w_scale, xs), su = __fmul_rn(a.w_scale2, xs);
+            float g[4] = {(float)__builtin_bit_cast(AccS, rg.x), (float)__builtin_bit_cast(AccS, rg.y),
+                          (float)__builtin_bit_cast(AccS, rg.z), (float)__builtin_bit_cast(AccS, rg.w)};
+            float u[4] = {(float)__builtin_bit_cast(AccS, ru.x), (float)__builtin_bit_cast(AccS, ru.y),
+                          (float)__builtin_bit_cast(AccS, ru.z), (float)__builtin_bit_cast(AccS, ru.w)};
+            float h[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) g[e] = __fmul_rn(sg, g[e]), u[e] = __fmul_rn(su, u[e]);
+            glu4(a.act, g, u, h);
+            put4(a.Y, a.ydt == NM_F32, tok * a.ldy + r, h, n, vh);
+            if (a.Y2) {
+                put4(a.Y2, false, tok * a.ldy2 + r, g, n, vg);
+                put4(a.Y3, false, tok * a.ldy2 + r, u, n, vg);
+            }
+        }
+        // the next column of sub-tiles overwrites the buffer only after every lane has read it
+        __builtin_amdgcn_s_waitcnt(0xc07f);
+        __builtin_amdgcn_wave_barrier();
+        asm volatile("" ::: "memory");
+    }
+}
+
 // NS-stage LDS ring of KB bytes of X per token per stage; see the comment block above.
-template <typename T, int SR, int ST, int KB, int NS, int WRN, int WTN, int OCC = 1, int IG = 1>
+template <typename T, int SR, int ST, int KB, int NS, int WRN, int WTN, int OCC = 1, int IG = 1, bool GLU = false>
 __global__ __launch_bounds__(64 * WRN * WTN, OCC) void spmm_ring_kernel(SpmmArgs a) {
     using RG = Ring<T, SR, ST, KB, NS, WRN, WTN, IG>;
     using FR = RingFrag<SR, ST>;
@@ -634,7 +755,8 @@ __global__ __launch_bounds__(64 * WRN * WTN, OCC) void spmm_ring_kernel(SpmmArgs
     const int wr = wave % WRN, wt = wave / WRN;
     int tr, tt;
     tile_of(blockIdx.x, gridDim.x, a.tiles_r, a.tiles_t, tr, tt);
-    const int64_t r0 = (int64_t)tr * RG::BR, t0 = (int64_t)tt * RG::BT;
+    const int64_t r0 = (int64_t)tr * (GLU ? RG::BR / 2 : RG::BR), t0 = (int64_t)tt * RG::BT;
+    static_assert(!GLU || SR == 4, "a wave's rows are one run of 64 gate and 64 up rows");
     // gridDim.y > 1: the stages split over blocks (split blockIdx.y takes stages s_begin ..
     // s_begin + nsteps - 1 and writes f32 / i32 partials); stage indices below are local
     const int spp = gridDim.y > 1 ? a.steps_per_split : a.nsteps;
@@ -646,10 +768,17 @@ __global__ __launch_bounds__(64 * WRN * WTN, OCC) void spmm_ring_kernel(SpmmArgs
     // per-lane byte offsets (from the block's base pointers, which live in SGPRs)
     // at stage 0; stage s adds s * (row bytes per stage)
     constexpr int ACH = RG::AROW / 16, BCH = KB / 16;  // 16-byte chunks per row
-    const void* baseA = uniform_ptr(a.vals + r0 * a.ldv * es);
-    const void* baseI = uniform_ptr(a.idx + r0 * a.ldi);
+    // GLU: the wave's value rows (and ungrouped index rows) are of one weight
+    static_assert(!GLU || 64 % (RG::NA * (64 / ACH)) == 0, "a wave's value rows in one run");
+    static_assert(!GLU || IG > 1 || 64 % (RG::NI * 64 / RG::AI) == 0, "a wave's index rows in one run");
+    const bool upA = GLU && glu_mat<64>(wave * RG::NA * (64 / ACH)) != 0;
+    const bool upI = GLU && IG == 1 && glu_mat<64>(wave * RG::NI * 64 / RG::AI) != 0;
+    const void* baseA = uniform_ptr((upA ? a.vals2 : a.vals) + r0 * a.ldv * es);
+    const void* baseI = uniform_ptr((upI ? a.idx2 : a.idx) + r0 * a.ldi);
+    const void* baseI2 = GLU && IG > 1 ? uniform_ptr(a.idx2 + r0 * a.ldi) : baseI;
     const void* baseB = uniform_ptr(a.X + t0 * a.ldx * es);
     const int64_t rmax = a.R - 1 - r0, tmax = a.Mtok - 1 - t0;
+    auto wrow = [](int row) { return GLU ? glu_feature<64>(row) : row; };
     uint32_t oA[RG::NA], oI[RG::NI], oB[RG::NB];
     // IG > 1: per batch p and instruction i, the row's byte offset and the piece (stage of the group)
     uint32_t gI[IG > 1 ? IG : 1][RG::NI];
@@ -661,7 +790,7 @@ __global__ __launch_bounds__(64 * WRN * WTN, OCC) void spmm_ring_kernel(SpmmArgs
             for (int i = 0; i < RG::NI; ++i) {
                 const int q = ((p * RG::NW + wave) * RG::NI + i) * 64 + lane;   // 16-byte slot of the group buffer
                 const int row = q / IG, c = (q % IG) ^ ((row >> 2) & (IG - 1));
-                const int64_t gr = row < rmax ? row : rmax;
+                const int64_t gr = wrow(row) < rmax ? wrow(row) : rmax;
                 gI[p][i] = (uint32_t)(gr * a.ldi * 4);
                 gC[p][i] = c;
             }
@@ -670,14 +799,14 @@ __global__ __launch_bounds__(64 * WRN * WTN, OCC) void spmm_ring_kernel(SpmmArgs
     for (int i = 0; i < RG::NA; ++i) {
         const int q = (wave * RG::NA + i) * 64 + lane;       // 16-byte chunk of the block's stage, row-major
         const int row = q / ACH, c = RG::alogical(row, q % ACH);
-        const int64_t gr = row < rmax ? row : rmax;
+        const int64_t gr = wrow(row) < rmax ? wrow(row) : rmax;
         oA[i] = (uint32_t)(gr * a.ldv * es + c * 16);
     }
 #pragma unroll
     for (int i = 0; i < RG::NI; ++i) {
         const int q = (wave * RG::NI + i) * 64 + lane;  // dword slot of the stage's [BR, AI] index block
         const int row = q / RG::AI, lw = (q % RG::AI) ^ iswz<RG::AI>(row);
-        const int64_t gr = row < rmax ? row : rmax;
+        const int64_t gr = wrow(row) < rmax ? wrow(row) : rmax;
         oI[i] = (uint32_t)(gr * a.ldi * 4 + lw * 4);
     }
 #pragma unroll
@@ -694,7 +823,9 @@ __global__ __launch_bounds__(64 * WRN * WTN, OCC) void spmm_ring_kernel(SpmmArgs
         for (int i = 0; i < RG::NI; ++i) {
             const int stg = g * IG + gC[p][i];
             const int sc = s_begin + (stg < nsteps ? stg : nsteps - 1);
-            dma16s(gb + (uint32_t)(((p * RG::NW + wave) * RG::NI + i) * 1024), baseI, gI[p][i] + (uint32_t)(sc * 16));
+            const int unit = (p * RG::NW + wave) * RG::NI + i;   // 64 / IG rows each
+            const void* base = GLU && glu_mat<64>(unit * (64 / IG)) ? baseI2 : baseI;
+            dma16s(gb + (uint32_t)(unit * 1024), base, gI[p][i] + (uint32_t)(sc * 16));
         }
     };
     auto issue = [&](int s) __attribute__((always_inline)) {
@@ -813,6 +944,11 @@ __global__ __launch_bounds__(64 * WRN * WTN, OCC) void spmm_ring_kernel(SpmmArgs
     // every wave has finished reading the ring: its LDS becomes the output staging buffers
     __syncthreads();
     static_assert(RG::LDS >= RG::NW * kStageWords<SR> * 4, "staging buffers fit in the ring");
+    if constexpr (GLU) {
+        store_glu_tile<T, ST>(a, acc, r0 + wr * 64, t0 + wt * ST * 32, split, (uint32_t*)smem + wave * kStageWords<SR>,
+                              lane);
+        return;
+    }
     if (a.part) {   // this split's partial tile, unscaled, into [split][Mtok][R]
         SpmmArgs b = a;
         using AccS = typename Mma<T>::AccS;
@@ -885,7 +1021,7 @@ struct Ring2 {
     __device__ static int swi(int r) { return (r >> 2) & 3; }
 };
 
-template <typename T, int SR, int ST, int WRN, int WTN, int IP = 16>
+template <typename T, int SR, int ST, int WRN, int WTN, int IP = 16, bool GLU = false>
 __global__ __launch_bounds__(64 * WRN * WTN, 1) void spmm_ring2_kernel(SpmmArgs a) {
     using RG = Ring2<T, SR, ST, WRN, WTN, IP>;
     using FR = RingFrag<SR, ST>;
@@ -895,7 +1031,8 @@ __global__ __launch_bounds__(64 * WRN * WTN, 1) void spmm_ring2_kernel(SpmmArgs 
     const int wr = wave % WRN, wt = wave / WRN;
     int tr, tt;
     tile_of(blockIdx.x, gridDim.x, a.tiles_r, a.tiles_t, tr, tt);
-    const int64_t r0 = (int64_t)tr * RG::BR, t0 = (int64_t)tt * RG::BT;
+    const int64_t r0 = (int64_t)tr * (GLU ? RG::BR / 2 : RG::BR), t0 = (int64_t)tt * RG::BT;
+    static_assert(!GLU || SR == 4, "a wave's rows are one run of 64 gate and 64 up rows");
     const int nsteps = a.nsteps;              // even, >= 2
     const int NG = nsteps >> 1;               // value groups = loop iterations
     const int NIGR = (nsteps + RG::IGS - 1) / RG::IGS;   // index groups
@@ -904,17 +1041,23 @@ __global__ __launch_bounds__(64 * WRN * WTN, 1) void spmm_ring2_kernel(SpmmArgs 
     // the last IP index bytes of a row (a partial last index group is clamped to them)
     const uint32_t ilast = (uint32_t)(nsteps * RG::AI * 4 - IP);
 
-    const void* baseA = uniform_ptr(a.vals + r0 * a.ldv * es);
+    // GLU: a wave's value rows (8 per load) and index rows (IP of a batch's) are of one weight
+    constexpr int IRW = RG::NIG * IP;   // index rows of a wave in a batch: 64 IP bytes a load, 64 bytes a row
+    static_assert(!GLU || (64 % (RG::NAG * 8) == 0 && 64 % IRW == 0), "a wave's rows in one run");
+    const bool upA = GLU && glu_mat<64>(wave * RG::NAG * 8) != 0;
+    const void* baseA = uniform_ptr((upA ? a.vals2 : a.vals) + r0 * a.ldv * es);
     const void* baseI = uniform_ptr(a.idx + r0 * a.ldi);
+    const void* baseI2 = GLU ? uniform_ptr(a.idx2 + r0 * a.ldi) : baseI;
     const void* baseB = uniform_ptr(a.X + t0 * a.ldx * es);
     const int64_t rmax = a.R - 1 - r0, tmax = a.Mtok - 1 - t0;
+    auto wrow = [](int row) { return GLU ? glu_feature<64>(row) : row; };
     uint32_t oA[RG::NAG], oI[RG::NIG], oB[RG::NBX];
     int pI[RG::NIG];
 #pragma unroll
     for (int i = 0; i < RG::NAG; ++i) {
         const int q = (wave * RG::NAG + i) * 64 + lane;   // 16-byte chunk of the group buffer, row-major
         const int row = q >> 3, c = (q & 7) ^ RG::swa(row);
-        const int64_t gr = row < rmax ? row : rmax;
+        const int64_t gr = wrow(row) < rmax ? wrow(row) : rmax;
         oA[i] = (uint32_t)(gr * a.ldv * es + c * 16);
     }
 #pragma unroll
@@ -957,11 +1100,12 @@ __global__ __launch_bounds__(64 * WRN * WTN, 1) void spmm_ring2_kernel(SpmmArgs 
 #pragma unroll
         for (int i = 0; i < RG::NIG; ++i) {
             const int row = b * (RG::BR / RG::IB) + (int)oI[i];
-            const int64_t gr = row < rmax ? row : rmax;
+            const int64_t gr = wrow(row) < rmax ? wrow(row) : rmax;
             uint32_t off = (uint32_t)(j * 64 + pI[i]);
             off = off < ilast ? off : ilast;
-            if constexpr (IP == 16) dma16s(st + (wave * RG::NIG + i) * 1024, baseI, (uint32_t)(gr * a.ldi * 4) + off);
-            else dma4s(st + (wave * RG::NIG + i) * 256, baseI, (uint32_t)(gr * a.ldi * 4) + off);
+            const void* base = GLU && glu_mat<64>(b * (RG::BR / RG::IB) + wave * IRW) ? baseI2 : baseI;
+            if constexpr (IP == 16) dma16s(st + (wave * RG::NIG + i) * 1024, base, (uint32_t)(gr * a.ldi * 4) + off);
+            else dma4s(st + (wave * RG::NIG + i) * 256, base, (uint32_t)(gr * a.ldi * 4) + off);
         }
     };
 
@@ -1071,6 +1215,10 @@ __global__ __launch_bounds__(64 * WRN * WTN, 1) void spmm_ring2_kernel(SpmmArgs 
     // every wave has finished reading the ring: its LDS becomes the output staging buffers
     __syncthreads();
     static_assert(RG::LDS >= RG::NW * kStageWords<SR> * 4, "staging buffers fit in the ring");
+    if constexpr (GLU) {
+        store_glu_tile<T, ST>(a, acc, r0 + wr * 64, t0 + wt * ST * 32, 0, (uint32_t*)smem + wave * kStageWords<SR>, lane);
+        return;
+    }
     store_tile<T, SR, ST>(a, acc, r0 + wr * SR * 32, t0 + wt * ST * 32, r0 + RG::BR <= a.R && t0 + RG::BT <= a.Mtok,
                           (uint32_t*)smem + wave * kStageWords<SR>, lane);
 }
@@ -1538,7 +1686,7 @@ constexpr int kRedStride = 20;
 // same stage order takes about 10 us.
 constexpr int kXresBytes = 64 * 1024 + 32 * 16;
 
-template <typename T, int SR, int ST, int KB, int NS, bool LIFT = false, int XRB_ = 0>
+template <typename T, int SR, int ST, int KB, int NS, bool LIFT = false, int XRB_ = 0, bool GLU = false>
 __global__ __launch_bounds__(256, 1) void spmm_ringk_kernel(SpmmArgs a) {
     constexpr bool XRES = XRB_ > 0;
     constexpr int es = sizeof(T);
@@ -1556,7 +1704,8 @@ __global__ __launch_bounds__(256, 1) void spmm_ringk_kernel(SpmmArgs a) {
                   "loads must split evenly over the 4 waves");
     static_assert(!XRES || ST == 1, "resident X for up to 32 tokens");
     constexpr int X_OFF = NS * STAGE, XRB = XRB_;
-    constexpr int RED = 4 * 64 * kRedStride * 4;        // one sub-tile of all four waves
+    constexpr int RED = (GLU ? 2 : 1) * 4 * 64 * kRedStride * 4;   // one sub-tile (GLU: a pair) of all four waves
+    static_assert(!GLU || SR == 2, "a tile is one run of 32 gate and 32 up rows");
     constexpr int LDS = X_OFF + XRB > RED ? X_OFF + XRB : RED;
     static_assert(LDS <= 160 * 1024, "LDS ring too large");
     __shared__ __attribute__((aligned(1024))) uint8_t smem[LDS];
@@ -1568,7 +1717,9 @@ __global__ __launch_bounds__(256, 1) void spmm_ringk_kernel(SpmmArgs a) {
     tile_of(blockIdx.x, gridDim.x, a.tiles_r, a.tiles_t, tr, tt);
     // a row tile holds TRW <= BR weight rows; its other rows re-read the last one (their
     // sums are not stored)
-    const int TRW = a.tile_rows > 0 && a.tile_rows < BR ? a.tile_rows : BR;
+    // (GLU: features, half the tile's rows)
+    constexpr int BF = GLU ? BR / 2 : BR;
+    const int TRW = a.tile_rows > 0 && a.tile_rows < BF ? a.tile_rows : BF;
     const int64_t r0 = (int64_t)tr * TRW, t0 = (int64_t)tt * BT;
     const int split = blockIdx.y;
     const int s_begin = split * a.steps_per_split;
@@ -1578,8 +1729,13 @@ __global__ __launch_bounds__(256, 1) void spmm_ringk_kernel(SpmmArgs a) {
     auto swa = [](int r) { return (r >> 1) & 7; };   // weight row r: logical chunk c at c ^ swa(r)
     auto swb = [](int t) { return t & 15; };         // X token t: logical chunk c at c ^ swb(t)
 
-    const void* baseA = uniform_ptr(a.vals + r0 * a.ldv * es);
-    const void* baseI = uniform_ptr(a.idx + r0 * a.ldi);
+    // GLU: a wave's value and index rows are of one weight
+    static_assert(!GLU || (32 % (NA * (64 / ACH)) == 0 && 32 % (NI * 64 / AI) == 0 && NA * (64 / ACH) == NI * 64 / AI),
+                  "a wave's rows in one run");
+    const bool up = GLU && glu_mat<32>(wave * NA * (64 / ACH)) != 0;
+    auto wrow = [](int row) { return GLU ? glu_feature<32>(row) : row; };
+    const void* baseA = uniform_ptr((up ? a.vals2 : a.vals) + r0 * a.ldv * es);
+    const void* baseI = uniform_ptr((up ? a.idx2 : a.idx) + r0 * a.ldi);
     const void* baseB = uniform_ptr(a.X + t0 * a.ldx * es);
     const int64_t rmax = (a.R - 1 - r0) < (TRW - 1) ? (a.R - 1 - r0) : (TRW - 1), tmax = a.Mtok - 1 - t0;
     uint32_t oA[NA], oI[NI], oB[NB > 0 ? NB : 1], oBc[NB > 0 ? NB : 1];
@@ -1587,14 +1743,14 @@ __global__ __launch_bounds__(256, 1) void spmm_ringk_kernel(SpmmArgs a) {
     for (int i = 0; i < NA; ++i) {
         const int q = (wave * NA + i) * 64 + lane;
         const int row = q / ACH, c = (q % ACH) ^ swa(row);
-        const int64_t gr = row < rmax ? row : rmax;
+        const int64_t gr = wrow(row) < rmax ? wrow(row) : rmax;
         oA[i] = (uint32_t)(gr * a.ldv * es + c * 16);
     }
 #pragma unroll
     for (int i = 0; i < NI; ++i) {
         const int q = (wave * NI + i) * 64 + lane;   // dword slot of the stage's [BR, AI] index block
         const int row = q / AI, lw = (q % AI) ^ iswz<AI>(row);
-        const int64_t gr = row < rmax ? row : rmax;
+        const int64_t gr = wrow(row) < rmax ? wrow(row) : rmax;
         oI[i] = (uint32_t)(gr * a.ldi * 4 + lw * 4);
     }
 #pragma unroll
@@ -1781,6 +1937,56 @@ __global__ __launch_bounds__(256, 1) void spmm_ringk_kernel(SpmmArgs a) {
     // time (whole-vector stores of the accumulators), by all 256 threads, which then write
     // the outputs along the rows (or the split's partials).
     float* red = (float*)smem;
+    if constexpr (GLU) {
+        // both sub-tiles of a 32-token column at once: the gate's and the up projection's sums of
+        // the same features, four consecutive ones per thread
+        using AccS = typename Mma<T>::AccS;
+#pragma unroll
+        for (int j = 0; j < ST; ++j) {
+            __syncthreads();
+#pragma unroll
+            for (int i = 0; i < 2; ++i) *(AccV*)&red[((i * 4 + wave) * 64 + lane) * kRedStride] = acc[i][j];
+            __syncthreads();
+            const int tk = tid >> 3, f4 = 4 * (tid & 7);
+            const int64_t gt = t0 + 32 * j + tk, gr = r0 + f4;
+            const int left = (int)(a.R - gr < TRW - f4 ? a.R - gr : TRW - f4), n = left < 4 ? left : 4;
+            if (gt >= a.Mtok || n <= 0) continue;
+            const int src = (tk + 32 * ((f4 >> 2) & 1)) * kRedStride + 4 * (f4 >> 3);
+            AccS v[2][4];
+#pragma unroll
+            for (int i = 0; i < 2; ++i)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    AccS t = 0;
+#pragma unroll
+                    for (int w = 0; w < 4; ++w) t += __builtin_bit_cast(AccS, red[(i * 4 + w) * 64 * kRedStride + src + e]);
+                    v[i][e] = t;
+                }
+            if (a.part) {
+                AccS* p = (AccS*)a.part + ((int64_t)split * a.Mtok + gt) * 2 * a.R + gr;
+                for (int e = 0; e < n; ++e) {
+                    p[e] = v[0][e];
+                    p[e + a.R] = v[1][e];
+                }
+                continue;
+            }
+            const float xs = a.x_scale ? a.x_scale[gt] : 1.0f;
+            const float sg = __fmul_rn(a.w_scale, xs), su = __fmul_rn(a.w_scale2, xs);
+            float g[4], u[4], hh[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) g[e] = __fmul_rn(sg, (float)v[0][e]), u[e] = __fmul_rn(su, (float)v[1][e]);
+            glu4(a.act, g, u, hh);
+            const int hs = a.ydt == NM_F32 ? 4 : 2;
+            put4(a.Y, a.ydt == NM_F32, gt * a.ldy + gr, hh, n,
+                 n == 4 && ((uintptr_t)a.Y % (4 * hs)) == 0 && a.ldy % 4 == 0 && gr % 4 == 0);
+            if (a.Y2) {
+                const bool vg = n == 4 && (((uintptr_t)a.Y2 | (uintptr_t)a.Y3) % 8) == 0 && a.ldy2 % 4 == 0 && gr % 4 == 0;
+                put4(a.Y2, false, gt * a.ldy2 + gr, g, n, vg);
+                put4(a.Y3, false, gt * a.ldy2 + gr, u, n, vg);
+            }
+        }
+        return;
+    }
 #pragma unroll
     for (int i = 0; i < SR; ++i)
 #pragma unroll
@@ -2515,6 +2721,27 @@ size_t spmm_lowrank_ws(int64_t Mtok, int64_t K, int64_t R, int Ns, int rank) {
     return a > b ? a : b;
 }
 
+// X lifted into XL [Mtok, K'] (one-byte codes and bf16 move alike)
+static void launch_lift(const void* X, nm_dtype xdt, int64_t ldx, int64_t Mtok, int64_t K, int Ns, void* XL, hipStream_t s) {
+    const int64_t Kl = lifted_cols(K, Ns);
+    const int es = xdt == NM_BF16 ? 2 : 1;
+    if (Ns == 4) {
+        const dim3 g(grid_cap(ceil_div(Mtok * (K / 8), 256), 8192));
+        if (es == 1)   // int8 or FP8 codes: the lift moves bytes
+            hipLaunchKernelGGL(lift68_kernel<int8_t>, g, dim3(256), 0, s, (const int8_t*)X, ldx, Mtok, K, (int8_t*)XL, Kl);
+        else
+            hipLaunchKernelGGL(lift68_kernel<uint16_t>, g, dim3(256), 0, s, (const uint16_t*)X, ldx, Mtok, K,
+                               (uint16_t*)XL, Kl);
+    } else {
+        const dim3 g(grid_cap(ceil_div(Mtok * (Kl / 4), 256), 8192));
+        if (es == 1)
+            hipLaunchKernelGGL(lift_kernel<int8_t>, g, dim3(256), 0, s, (const int8_t*)X, ldx, Mtok, K, Ns, (int8_t*)XL, Kl);
+        else
+            hipLaunchKernelGGL(lift_kernel<uint16_t>, g, dim3(256), 0, s, (const uint16_t*)X, ldx, Mtok, K, Ns,
+                               (uint16_t*)XL, Kl);
+    }
+}
+
 // Every workspace need of the call is known (and checked) before the first launch.
 static nm_status spmm_impl(const char* fn, const void* X, nm_dtype xdt, int64_t Mtok, int64_t K, int64_t ldx,
                            const void* vals, const uint32_t* idx, int64_t R, int64_t ldv, int64_t ldi, int Ns,
@@ -2588,21 +2815,7 @@ static nm_status spmm_impl(const char* fn, const void* X, nm_dtype xdt, int64_t 
     }
     if (Ns && !fused) {
         // (2N-2):2N: lift X into the workspace, then the plain product over the lifted width
-        if (Ns == 4) {
-            const dim3 g(grid_cap(ceil_div(Mtok * (K / 8), 256), 8192));
-            if (es == 1)   // int8 or FP8 codes: the lift moves bytes
-                hipLaunchKernelGGL(lift68_kernel<int8_t>, g, dim3(256), 0, s, (const int8_t*)X, ldx, Mtok, K, (int8_t*)XL, Kl);
-            else
-                hipLaunchKernelGGL(lift68_kernel<uint16_t>, g, dim3(256), 0, s, (const uint16_t*)X, ldx, Mtok, K,
-                                   (uint16_t*)XL, Kl);
-        } else {
-            const dim3 g(grid_cap(ceil_div(Mtok * (Kl / 4), 256), 8192));
-            if (es == 1)
-                hipLaunchKernelGGL(lift_kernel<int8_t>, g, dim3(256), 0, s, (const int8_t*)X, ldx, Mtok, K, Ns, (int8_t*)XL, Kl);
-            else
-                hipLaunchKernelGGL(lift_kernel<uint16_t>, g, dim3(256), 0, s, (const uint16_t*)X, ldx, Mtok, K, Ns,
-                                   (uint16_t*)XL, Kl);
-        }
+        launch_lift(X, xdt, ldx, Mtok, K, Ns, XL, s);
         a.X = XL;
     }
     if (xdt == NM_I8) return run_spmm<int8_t>(a, ring_ok, fused, PART, F32, s);
@@ -2744,13 +2957,24 @@ nm_status launch_hutch_u_ring(const uint16_t* X, int64_t ldx, int64_t n, int64_t
 }
 
 // ------------------------------------------------------------------ gated feed-forward block
-// H = act(G) . U (and the rounded G and U) from the two products in f32, P [2][Mtok][R].
-template <int ACT>
-__global__ __launch_bounds__(256) void glu_combine_kernel(const float* __restrict__ P, GluIn g) {
+// H = act(G) . U (and the rounded G and U) from sums of both projections: P holds S splits of
+// [Mtok][2 R] raw sums (the gate's R first), or with S == 0 the two finished products in f32,
+// [2][Mtok][R].
+template <typename Acc, int ACT>
+__global__ __launch_bounds__(256) void glu_combine_kernel(const Acc* __restrict__ P, int S, GluIn g) {
     const int64_t total = g.Mtok * g.R;
     for (int64_t t = (int64_t)blockIdx.x * blockDim.x + threadIdx.x; t < total; t += (int64_t)gridDim.x * blockDim.x) {
         const int64_t m = t / g.R, r = t - m * g.R;
-        const float x = P[t], u = P[total + t];
+        float x, u;
+        if (S) {
+            const float xs = g.x_scale ? g.x_scale[m] : 1.0f;
+            const Acc* p = P + m * 2 * g.R + r;
+            x = __fmul_rn(__fmul_rn(g.scale[0], xs), (float)split_sum(p, S, 2 * total));
+            u = __fmul_rn(__fmul_rn(g.scale[1], xs), (float)split_sum(p + g.R, S, 2 * total));
+        } else {
+            x = (float)P[t];
+            u = (float)P[total + t];
+        }
         const float h = act_value<ACT>(x) * u;
         if (g.hdt == NM_F32) ((float*)g.H)[m * g.ldh + r] = h;
         else ((uint16_t*)g.H)[m * g.ldh + r] = (uint16_t)f32_to_bf16_bits(h);
@@ -2761,34 +2985,277 @@ __global__ __launch_bounds__(256) void glu_combine_kernel(const float* __restric
     }
 }
 
-#define NM_BY_ACT(act, CALL)                                       \
-    do {                                                           \
-        if ((act) == NM_ACT_SILU) CALL(NM_ACT_SILU);               \
-        else if ((act) == NM_ACT_GELU) CALL(NM_ACT_GELU);          \
-        else if ((act) == NM_ACT_GELU_TANH) CALL(NM_ACT_GELU_TANH); \
-        else CALL(NM_ACT_RELU2);                                   \
-    } while (0)
+template <typename Acc>
+static void launch_glu_combine(const void* P, int S, const GluIn& g, hipStream_t s) {
+    const dim3 grid(grid_cap(ceil_div(g.Mtok * g.R, 256), 16384));
+#define NM_COMBINE(A) hipLaunchKernelGGL((glu_combine_kernel<Acc, A>), grid, dim3(256), 0, s, (const Acc*)P, S, g)
+    if (g.act == NM_ACT_SILU) NM_COMBINE(NM_ACT_SILU);
+    else if (g.act == NM_ACT_GELU) NM_COMBINE(NM_ACT_GELU);
+    else if (g.act == NM_ACT_GELU_TANH) NM_COMBINE(NM_ACT_GELU_TANH);
+    else NM_COMBINE(NM_ACT_RELU2);
+#undef NM_COMBINE
+}
+
+// The fused kernels by token count, as for the plain product with R features in place of
+// rows and half as many of them per tile:
+//   kind 1: K-split ring, 32 features x 32 / 64 / 128 tokens (up to 256 tokens)
+//   kind 2: ring tiles of 128 features x 128 tokens (narrow) or x 256 tokens (big), or big ones
+//           on the first features and narrow ones on the rest
+//   kind 0: none applies (K off the stage grid, unaligned index rows): two plain products
+struct GluPlan {
+    int kind, mid, xres, big, tiles_r, tiles_t, nsteps, KS, steps_per_split, tile_rows;
+    int64_t split_rows;
+};
+
+template <typename T>
+static GluPlan plan_glu(int64_t Mtok, int64_t K, int64_t R, bool ring_ok, bool lift) {
+    GluPlan p{};
+    using RB = Ring2<NM_RING_BIG>;
+    using RN = Ring<NM_RING_NARROW>;
+    constexpr int KOm = 256 / (int)sizeof(T);
+    static_assert(KOm == RN::KO, "the K-split and the narrow ring share their stage width");
+    if (!ring_ok || K % KOm) return p;
+    const int64_t cus = device_cus();
+    p.nsteps = (int)(K / KOm);
+    if (Mtok <= 256) {
+        const int64_t rt = ceil_div(R, 32);
+        p.kind = 1;
+        p.mid = Mtok <= 32 ? 1 : (Mtok <= 64 ? 2 : 4);
+        for (int m = 1; m < p.mid; m *= 2)
+            if (rt * ceil_div(Mtok, 32 * m) <= cus) {
+                p.mid = m;
+                break;
+            }
+        if (sizeof(T) == 2 && p.mid == 4 && !lift) {
+            // as for the plain product: 256-row tiles read a quarter of the X per weight byte
+            const int64_t tiles = ceil_div(R, RN::BR / 2) * ceil_div(Mtok, RN::BT);
+            int64_t ks = cus / tiles;
+            if (ks > p.nsteps / 2) ks = p.nsteps / 2;
+            if (ks < 1) ks = 1;
+            p.kind = 2;
+            p.mid = 0;
+            p.tiles_r = (int)ceil_div(R, RN::BR / 2);
+            p.tiles_t = (int)ceil_div(Mtok, RN::BT);
+            p.steps_per_split = (int)ceil_div(p.nsteps, ks);
+            p.KS = (int)ceil_div(p.nsteps, p.steps_per_split);
+            return p;
+        }
+        p.tiles_r = (int)rt;
+        p.tiles_t = (int)ceil_div(Mtok, 32 * p.mid);
+        int ks = 1;
+        while ((int64_t)p.tiles_r * p.tiles_t * ks < 160 && p.nsteps >= 8 * ks) ks *= 2;
+        p.steps_per_split = (int)ceil_div(p.nsteps, ks);
+        p.KS = (int)ceil_div(p.nsteps, p.steps_per_split);
+        if (!lift && p.mid == 1) {
+            const int64_t rows = Mtok < 32 ? Mtok : 32;
+            p.xres = rows * (ceil_div((int64_t)p.steps_per_split * 256, 1024) * 1024 + 16) <= kXresBytes;
+        }
+        return p;
+    }
+    p.kind = 2;
+    p.KS = 1;
+    p.steps_per_split = p.nsteps;
+    if (K % (2 * RB::KO) == 0) {
+        // whole rounds of tiles over the CUs, a round of big tiles counted as 1.5 narrow ones (as
+        // the plain product's plan)
+        const int64_t fb = RB::BR / 2, fn = RN::BR / 2;
+        const int64_t ttb = ceil_div(Mtok, RB::BT), tb = ceil_div(R, fb) * ttb;
+        const int64_t ttn = ceil_div(Mtok, RN::BT), tn = ceil_div(R, fn) * ttn;
+        int64_t best = 2 * ceil_div(tn, cus);
+        if (3 * ceil_div(tb, cus) < best) {
+            best = 3 * ceil_div(tb, cus);
+            p.big = 1;
+        }
+        const int64_t rtb = (tb / cus) * cus / ttb;
+        if (rtb >= 1 && rtb * fb < R) {
+            const int64_t rest = R - rtb * fb;
+            const int64_t c = 3 * ceil_div(rtb * ttb, cus) + 2 * ceil_div(ceil_div(rest, fn) * ttn, cus);
+            if (c < best) {
+                p.big = 0;
+                p.split_rows = rtb * fb;
+            }
+        }
+    }
+    return p;
+}
+
+template <typename T>
+static nm_status run_glu(SpmmArgs a, const GluPlan& p, bool lift, void* part, const GluIn& g, hipStream_t s) {
+    using RB = Ring2<NM_RING_BIG>;
+    using RN = Ring<NM_RING_NARROW>;
+    a.KS = p.KS;
+    a.steps_per_split = p.steps_per_split;
+    a.part = p.KS > 1 ? part : nullptr;
+    if (p.kind == 1) {
+        a.nsteps = p.nsteps;
+        a.tiles_r = p.tiles_r;
+        a.tiles_t = p.tiles_t;
+        a.tile_rows = p.tile_rows;
+        const dim3 grid((unsigned)(p.tiles_r * p.tiles_t), (unsigned)p.KS);
+#define NM_GLUK(ST, NS, LIFT, XRB) \
+    hipLaunchKernelGGL((spmm_ringk_kernel<T, 2, ST, 256, NS, LIFT, XRB, true>), grid, dim3(256), 0, s, a)
+        if (lift) {
+            if (p.mid == 1) NM_GLUK(1, 6, true, 0);
+            else if (p.mid == 2) NM_GLUK(2, 3, true, 0);
+            else if constexpr (sizeof(T) == 2) NM_GLUK(4, 3, true, 0);
+            else return set_error(NM_ERR_DEVICE, "nm_spmm_glu: no in-kernel lift for one-byte codes on 128-token tiles");
+        } else if (p.xres) NM_GLUK(1, 8, false, kXresBytes);
+        else if (p.mid == 1) NM_GLUK(1, 6, false, 0);
+        else if (p.mid == 2) NM_GLUK(2, 3, false, 0);
+        else NM_GLUK(4, 3, false, 0);
+#undef NM_GLUK
+    } else {
+        auto launch = [&](bool big, int64_t f_begin, int64_t f_end) {
+            SpmmArgs b = a;
+            const int64_t es = sizeof(T), hs = a.ydt == NM_BF16 ? 2 : 4;
+            b.vals = a.vals + f_begin * a.ldv * es;
+            b.vals2 = a.vals2 + f_begin * a.ldv * es;
+            b.idx = a.idx + f_begin * a.ldi;
+            b.idx2 = a.idx2 + f_begin * a.ldi;
+            b.Y = (uint8_t*)a.Y + f_begin * hs;
+            if (a.Y2) {
+                b.Y2 = (uint16_t*)a.Y2 + f_begin;
+                b.Y3 = (uint16_t*)a.Y3 + f_begin;
+            }
+            b.R = f_end - f_begin;
+            b.tiles_r = (int)ceil_div(b.R, (big ? RB::BR : RN::BR) / 2);
+            b.tiles_t = (int)ceil_div(a.Mtok, big ? RB::BT : RN::BT);
+            b.nsteps = (int)(a.K / (big ? RB::KO : RN::KO));
+            const dim3 grid((unsigned)(b.tiles_r * b.tiles_t), (unsigned)p.KS);
+            if (big) hipLaunchKernelGGL((spmm_ring2_kernel<NM_RING_BIG, true>), grid, dim3(512), 0, s, b);
+            else
+                hipLaunchKernelGGL((spmm_ring_kernel<NM_RING_NARROW, 1, sizeof(T) == 2 ? 4 : 1, true>), grid, dim3(256),
+                                   0, s, b);
+        };
+        if (p.split_rows > 0) {
+            launch(true, 0, p.split_rows);
+            launch(false, p.split_rows, a.R);
+        } else {
+            launch(p.big != 0, 0, a.R);
+        }
+    }
+    if (p.KS > 1) launch_glu_combine<typename Mma<T>::AccS>(part, p.KS, g, s);
+    return check_launch("nm_spmm_glu");
+}
+
+// Tokens per pass of the two-product form, so that its f32 buffers stay near 128 MB.
+static int64_t glu_chunk(int64_t Mtok, int64_t R) {
+    const int64_t c = ceil_div((int64_t)16 << 20, R);
+    return Mtok <= 256 || Mtok <= c ? Mtok : (c > 256 ? c : 256);
+}
+static size_t glu_plain_ws(int64_t Mtok, int64_t K, int64_t R, int Ns, nm_dtype xdt) {
+    const int64_t c = glu_chunk(Mtok, R), last = Mtok % c;
+    size_t w = spmm_ws(c, K, R, Ns, xdt);
+    if (last && spmm_ws(last, K, R, Ns, xdt) > w) w = spmm_ws(last, K, R, Ns, xdt);
+    return round256((size_t)(2 * c * R * 4)) + w;
+}
+
+// The fused form's lift: inside the K-split ring (6:8, up to 64 tokens of one-byte codes)
+static GluPlan glu_plan(int64_t Mtok, int64_t K, int64_t R, int Ns, nm_dtype xdt, bool ring_ok, bool* fused) {
+    const int64_t Kl = lifted_cols(K, Ns);
+    auto plan = [&](bool lift) {
+        return xdt == NM_BF16 ? plan_glu<uint16_t>(Mtok, Kl, R, ring_ok, lift) : plan_glu<int8_t>(Mtok, Kl, R, ring_ok, lift);
+    };
+    *fused = false;
+    if (Ns == 4) {
+        const GluPlan p = plan(true);
+        if (p.kind == 1 && (xdt == NM_BF16 || p.mid <= 2)) {
+            *fused = true;
+            return p;
+        }
+    }
+    return plan(false);
+}
+
+// Workspace of the fused form: the lifted activation, then the split-K partials.
+static void glu_fused_ws(const GluPlan& p, bool fused, int64_t Mtok, int64_t K, int64_t R, int Ns, nm_dtype xdt,
+                         size_t* xl, size_t* part) {
+    *xl = Ns && !fused ? lift_bytes(Mtok, K, Ns, xdt == NM_BF16 ? 2 : 1) : 0;
+    *part = p.KS > 1 ? round256((size_t)p.KS * (size_t)Mtok * (size_t)R * 8) : 0;
+}
 
 size_t glu_ws(int64_t Mtok, int64_t K, int64_t R, int Ns, nm_dtype xdt) {
-    return 2 * round256((size_t)Mtok * (size_t)R * 4) + spmm_ws(Mtok, K, R, Ns, xdt);
+    const size_t plain = glu_plain_ws(Mtok, K, R, Ns, xdt);
+    bool fused;
+    const GluPlan p = glu_plan(Mtok, K, R, Ns, xdt, true, &fused);
+    if (!p.kind) return plain;
+    size_t xl, part;
+    glu_fused_ws(p, fused, Mtok, K, R, Ns, xdt, &xl, &part);
+    return xl + part > plain ? xl + part : plain;
+}
+
+static nm_status glu_plain(const GluIn& in, void* ws, hipStream_t s) {
+    const int64_t c = glu_chunk(in.Mtok, in.R), es = in.xdt == NM_BF16 ? 2 : 1, hs = in.hdt == NM_BF16 ? 2 : 4;
+    for (int64_t m = 0; m < in.Mtok; m += c) {
+        GluIn g = in;
+        g.Mtok = in.Mtok - m < c ? in.Mtok - m : c;
+        g.X = (const uint8_t*)in.X + m * in.ldx * es;
+        if (in.x_scale) g.x_scale = in.x_scale + m;
+        g.H = (uint8_t*)in.H + m * in.ldh * hs;
+        if (in.G) {
+            g.G = (uint16_t*)in.G + m * in.ldg;
+            g.U = (uint16_t*)in.U + m * in.ldg;
+        }
+        float* P = (float*)ws;
+        uint8_t* rest = (uint8_t*)ws + round256((size_t)(2 * c * g.R * 4));
+        for (int i = 0; i < 2; ++i) {
+            const nm_status st =
+                spmm_impl("nm_spmm_glu", g.X, g.xdt, g.Mtok, g.K, g.ldx, g.vals[i], g.idx[i], g.R, g.ldv, g.ldi, g.Ns,
+                          g.x_scale, g.scale[i], nullptr, P + i * g.Mtok * g.R, NM_F32, g.R, rest,
+                          spmm_ws(g.Mtok, g.K, g.R, g.Ns, g.xdt), s);
+            if (st != NM_OK) return st;
+        }
+        launch_glu_combine<float>(P, 0, g, s);
+    }
+    return check_launch("nm_spmm_glu");
 }
 
 nm_status launch_glu(const GluIn& g, void* ws, hipStream_t s) {
-    float* P = (float*)ws;
-    const size_t one = (size_t)g.Mtok * (size_t)g.R;
-    uint8_t* rest = (uint8_t*)ws + 2 * round256(one * 4);
-    const size_t need = spmm_ws(g.Mtok, g.K, g.R, g.Ns, g.xdt);
-    for (int i = 0; i < 2; ++i) {
-        const nm_status st = spmm_impl("nm_spmm_glu", g.X, g.xdt, g.Mtok, g.K, g.ldx, g.vals[i], g.idx[i], g.R, g.ldv,
-                                       g.ldi, g.Ns, g.x_scale, g.scale[i], nullptr, P + i * one, NM_F32, g.R, rest,
-                                       need, s);
-        if (st != NM_OK) return st;
+    SpmmArgs a{};
+    const int64_t Kl = lifted_cols(g.K, g.Ns), es = g.xdt == NM_BF16 ? 2 : 1;
+    a.X = (const uint8_t*)g.X;
+    a.vals = (const uint8_t*)g.vals[0];
+    a.vals2 = (const uint8_t*)g.vals[1];
+    a.idx = g.idx[0];
+    a.idx2 = g.idx[1];
+    a.x_scale = g.x_scale;
+    a.w_scale = g.scale[0];
+    a.w_scale2 = g.scale[1];
+    a.act = g.act;
+    a.Y = g.H;
+    a.ydt = (int)g.hdt;
+    a.ldy = g.ldh;
+    a.Y2 = g.G;
+    a.Y3 = g.U;
+    a.ldy2 = g.ldg;
+    a.ldx = g.ldx;
+    a.ldv = g.ldv;
+    a.ldi = g.ldi;
+    a.Mtok = g.Mtok;
+    a.K = Kl;
+    a.R = g.R;
+    a.comp_bytes = Kl / 2 * es;
+    a.idx_words = (Kl + 31) / 32;
+    a.xrow_bytes = g.K * es;
+    auto ok = [&]() { return ring_ok_for(a, es) && ((uintptr_t)a.idx2 & 15u) == 0; };
+    bool fused;
+    GluPlan p = glu_plan(g.Mtok, g.K, g.R, g.Ns, g.xdt, ok(), &fused);
+    if (g.Ns && !fused) {   // the product then reads the lifted copy
+        a.ldx = Kl;
+        p = glu_plan(g.Mtok, g.K, g.R, g.Ns, g.xdt, ok(), &fused);
+        if (fused) p.kind = 0;   // not reached: the lifted copy's offsets only add limits
     }
-    const dim3 grid(grid_cap(ceil_div(g.Mtok * g.R, 256), 16384));
-#define NM_COMBINE(A) hipLaunchKernelGGL(glu_combine_kernel<A>, grid, dim3(256), 0, s, (const float*)P, g)
-    NM_BY_ACT(g.act, NM_COMBINE);
-#undef NM_COMBINE
-    return check_launch("nm_spmm_glu");
+    if (!p.kind) return glu_plain(g, ws, s);
+    size_t xl, part;
+    glu_fused_ws(p, fused, g.Mtok, g.K, g.R, g.Ns, g.xdt, &xl, &part);
+    if (g.Ns && !fused) {
+        launch_lift(g.X, g.xdt, g.ldx, g.Mtok, g.K, g.Ns, ws, s);
+        a.X = (const uint8_t*)ws;
+    }
+    void* PART = (uint8_t*)ws + xl;
+    if (g.xdt == NM_I8) return run_glu<int8_t>(a, p, fused, PART, g, s);
+    if (g.xdt == NM_FP8) return run_glu<fp8e4m3>(a, p, fused, PART, g, s);
+    return run_glu<uint16_t>(a, p, fused, PART, g, s);
 }
 
 // ------------------------------------------------------------------ gradients
