@@ -394,10 +394,15 @@ def nm_spmm_noalloc(X: torch.Tensor, vals: torch.Tensor, idx: torch.Tensor, R: i
 
 
 # ---------------------------------------------------------------- gated feed-forward block, training
-def _row_major(**tensors):
-    for name, t in tensors.items():
-        if t is not None and (t.dim() != 2 or (t.shape[1] > 1 and t.stride(1) != 1)):
-            raise ValueError(f"{name} must be a row-major 2-D tensor (unit stride along the last dimension)")
+# These run every layer of every step, so their checks are one expression each; what it found is
+# looked up only when it fails.
+def _raw_stream(t: torch.Tensor) -> int:
+    return torch._C._cuda_getCurrentRawStream(t.device.index)
+
+
+def _rows(t: torch.Tensor) -> bool:
+    """2-D with unit stride along the last dimension."""
+    return t.dim() == 2 and (t.stride(1) == 1 or t.shape[1] <= 1)
 
 
 def _ld2(t: torch.Tensor) -> int:
@@ -406,7 +411,10 @@ def _ld2(t: torch.Tensor) -> int:
 
 
 def _need(need: int, ws: torch.Tensor | None, device) -> torch.Tensor | None:
-    return ws if ws is not None and ws.numel() >= need else _ws(need, device)
+    """The caller's workspace where it has need bytes, else a new one."""
+    if need and (ws is None or ws.numel() * ws.element_size() < need):
+        ws = torch.empty(need, dtype=torch.uint8, device=device)
+    return ws
 
 
 def _same(what: str, *pairs):
@@ -415,37 +423,51 @@ def _same(what: str, *pairs):
             raise ValueError(f"{what}: got {a}, expected {b}")
 
 
+def _refuse(what: str, **tensors):
+    got = ", ".join(f"{k} {tuple(t.shape)} strides {t.stride()} {t.dtype} {t.device}" for k, t in tensors.items()
+                    if isinstance(t, torch.Tensor))
+    raise ValueError(f"{what}; got {got}")
+
+
 def nm_spmm_glu(X: torch.Tensor, vals_g: torch.Tensor, idx_g: torch.Tensor, vals_u: torch.Tensor, idx_u: torch.Tensor,
                 Ns: int = 0, act: int = NM_ACT_SILU, x_scale: torch.Tensor | None = None, g_scale: float = 1.0,
                 u_scale: float = 1.0, hdt: int | None = None, save: bool = False, out: torch.Tensor | None = None,
                 ws: torch.Tensor | None = None):
     """H = act(G) . U with G = X Wg^T and U = X Wu^T on packed weights, in one pass: H, or with
     save (H, G, U), the bf16 pre-activations that nm_spmm_glu_backward takes."""
-    _row_major(X=X, vals_g=vals_g, idx_g=idx_g, vals_u=vals_u, idx_u=idx_u, out=out)
+    if not (_rows(X) and _rows(vals_g) and _rows(idx_g) and vals_u.shape == vals_g.shape and idx_u.shape == idx_g.shape and
+            vals_u.stride() == vals_g.stride() and idx_u.stride() == idx_g.stride() and
+            vals_g.dtype == X.dtype == vals_u.dtype and idx_g.dtype == torch.int32 == idx_u.dtype and X.dtype in _DT and
+            X.device == vals_g.device == idx_g.device == vals_u.device == idx_u.device):
+        _refuse("X must be row-major and the gate and up weights packed alike, in X's type", X=X, vals_g=vals_g,
+                idx_g=idx_g, vals_u=vals_u, idx_u=idx_u)
     Mtok, K = X.shape
-    R = vals_g.shape[0]
-    Kl = lifted_width(K, Ns) if Ns else K
-    _same("packed weights", (vals_u.shape[0], R), (idx_g.shape[0], R), (idx_u.shape[0], R))
-    for t in (vals_g, vals_u):
-        if t.shape[1] < Kl // 2 or t.dtype != X.dtype:
-            raise ValueError(f"vals must hold {Kl // 2} values of {X.dtype} per row, got {tuple(t.shape)} {t.dtype}")
-    for t in (idx_g, idx_u):
-        if t.shape[1] < (Kl + 31) // 32 or t.dtype != torch.int32:
-            raise ValueError("idx must be int32 with one word per 32 (lifted) columns")
-    if R > 1 and (vals_u.stride(0) != vals_g.stride(0) or idx_u.stride(0) != idx_g.stride(0)):
-        raise ValueError("the gate and up weights must have the same row strides")
-    if x_scale is not None and (x_scale.dtype != torch.float32 or x_scale.numel() != Mtok or not x_scale.is_contiguous()):
-        raise ValueError("x_scale must be a contiguous f32 tensor with one value per token")
-    hdt = (NM_BF16 if out is None else dtype_code(out)) if hdt is None else hdt
-    H = out if out is not None else torch.empty((Mtok, R), dtype=_TORCH[hdt], device=X.device)
-    _same("out", (tuple(H.shape), (Mtok, R)), (H.dtype, _TORCH[hdt]))
+    R, slots = vals_g.shape
+    Kl = lifted_width(K, Ns) if Ns >= 2 else K
+    if slots < Kl // 2 or idx_g.shape[0] != R or idx_g.shape[1] < (Kl + 31) // 32:
+        _refuse(f"{Kl // 2} values and {(Kl + 31) // 32} index words per row are needed", vals=vals_g, idx=idx_g)
+    if x_scale is not None and not (x_scale.dtype == torch.float32 and x_scale.numel() == Mtok and x_scale.is_contiguous()
+                                    and x_scale.device == X.device):
+        _refuse(f"x_scale must be {Mtok} contiguous f32 values", x_scale=x_scale)
+    xdt = _DT[X.dtype]
+    if out is None:
+        hdt = NM_BF16 if hdt is None else hdt
+        H = torch.empty((Mtok, R), dtype=_TORCH[hdt], device=X.device)
+        ldh = R
+    else:
+        hdt = dtype_code(out) if hdt is None else hdt
+        if not (_rows(out) and out.shape == (Mtok, R) and out.dtype == _TORCH[hdt] and out.device == X.device):
+            _refuse(f"out must be a row-major {_TORCH[hdt]} tensor of ({Mtok}, {R})", out=out)
+        H, ldh = out, _ld2(out)
     G = torch.empty((Mtok, R), dtype=torch.bfloat16, device=X.device) if save else None
     U = torch.empty((Mtok, R), dtype=torch.bfloat16, device=X.device) if save else None
-    ws = _need(raw.nm_spmm_glu_workspace(Mtok, K, R, Ns, dtype_code(X)), ws, X.device)
-    _check(raw.nm_spmm_glu(_ptr(X), dtype_code(X), Mtok, K, _ld2(X), _ptr(vals_g), _ptr(idx_g), _ptr(vals_u),
-                           _ptr(idx_u), dtype_code(vals_g), R, _ld2(vals_g), _ld2(idx_g), Ns, _ptr(x_scale), g_scale,
-                           u_scale, act, _ptr(H), hdt, _ld2(H), _ptr(G), _ptr(U), R, _ptr(ws),
-                           0 if ws is None else ws.numel(), _stream(X)))
+    ws = _need(raw.nm_spmm_glu_workspace(Mtok, K, R, Ns, xdt), ws, X.device)
+    st = raw.nm_spmm_glu(X.data_ptr(), xdt, Mtok, K, _ld2(X), vals_g.data_ptr(), idx_g.data_ptr(), vals_u.data_ptr(),
+                         idx_u.data_ptr(), xdt, R, _ld2(vals_g), _ld2(idx_g), Ns, _ptr(x_scale), g_scale, u_scale, act,
+                         H.data_ptr(), hdt, ldh, _ptr(G), _ptr(U), R, _ptr(ws),
+                         0 if ws is None else ws.numel() * ws.element_size(), _raw_stream(X))
+    if st:
+        _check(st)
     return (H, G, U) if save else H
 
 
@@ -454,26 +476,21 @@ def _grad_out(t: torch.Tensor | None, want: bool, shape, dt: int, device):
         return None
     if t is None:
         return torch.empty(shape, dtype=_TORCH[dt], device=device)
-    _row_major(out=t)
-    _same("out", (tuple(t.shape), tuple(shape)), (t.dtype, _TORCH[dt]))
+    if not (_rows(t) and t.shape == shape and t.dtype == _TORCH[dt] and t.device == device):
+        _refuse(f"an output must be a row-major {_TORCH[dt]} tensor of {shape}", out=t)
     return t
 
 
-def _check_grad(X, dY, vals, idx):
+def _grad_inputs(X, dY, vals, idx):
+    """(tokens, columns, rows) of a backward call on a 2:4 weight."""
+    if not (_rows(X) and _rows(dY) and _rows(vals) and _rows(idx) and
+            X.dtype == dY.dtype == vals.dtype == torch.bfloat16 and idx.dtype == torch.int32 and
+            X.device == dY.device == vals.device == idx.device):
+        _refuse("the backward pass takes row-major bf16 tensors and an int32 idx", X=X, dY=dY, vals=vals, idx=idx)
     Mtok, K = X.shape
-    R = vals[0].shape[0]
-    _row_major(X=X, dY=dY)
-    _same("dY", (tuple(dY.shape), (Mtok, R)))
-    for t in (X, dY, *vals):
-        if t.dtype != torch.bfloat16:
-            raise ValueError(f"the backward pass takes bf16 tensors, got {t.dtype}")
-    for v, i in zip(vals, idx):
-        _row_major(vals=v, idx=i)
-        if v.shape[0] != R or v.shape[1] < K // 2 or i.shape[0] != R or i.shape[1] < (K + 31) // 32 or \
-                i.dtype != torch.int32:
-            raise ValueError("vals / idx do not hold a 2:4 weight of this shape")
-        if R > 1 and (v.stride(0) != vals[0].stride(0) or i.stride(0) != idx[0].stride(0)):
-            raise ValueError("the gate and up weights must have the same row strides")
+    R = vals.shape[0]
+    if not (dY.shape == (Mtok, R) and vals.shape[1] >= K // 2 and idx.shape[0] == R and idx.shape[1] >= (K + 31) // 32):
+        _refuse("the shapes do not belong to one 2:4 layer", X=X, dY=dY, vals=vals, idx=idx)
     return Mtok, K, R
 
 
@@ -481,14 +498,16 @@ def nm_spmm_backward(dY: torch.Tensor, X: torch.Tensor, vals: torch.Tensor, idx:
                      want_dv: bool = True, dxdt: int = NM_BF16, dvdt: int = NM_BF16, out_dx: torch.Tensor | None = None,
                      out_dv: torch.Tensor | None = None, ws: torch.Tensor | None = None):
     """(dX, dvals) of Y = X W^T on a 2:4 packed bf16 weight; what is not wanted is None."""
-    Mtok, K, R = _check_grad(X, dY, [vals], [idx])
+    Mtok, K, R = _grad_inputs(X, dY, vals, idx)
     dX = _grad_out(out_dx, want_dx, (Mtok, K), dxdt, X.device)
     dV = _grad_out(out_dv, want_dv, (R, K // 2), dvdt, X.device)
     ws = _need(raw.nm_spmm_backward_workspace(Mtok, K, R), ws, X.device)
-    _check(raw.nm_spmm_backward(_ptr(dY), _ld2(dY), _ptr(X), _ld2(X), Mtok, K, _ptr(vals), _ptr(idx), R, _ld2(vals),
-                                _ld2(idx), _ptr(dX), dxdt, K if dX is None else _ld2(dX), _ptr(dV), dvdt,
-                                K // 2 if dV is None else _ld2(dV), _ptr(ws), 0 if ws is None else ws.numel(),
-                                _stream(X)))
+    st = raw.nm_spmm_backward(dY.data_ptr(), _ld2(dY), X.data_ptr(), _ld2(X), Mtok, K, vals.data_ptr(), idx.data_ptr(), R,
+                              _ld2(vals), _ld2(idx), _ptr(dX), dxdt, K if dX is None else _ld2(dX), _ptr(dV), dvdt,
+                              K // 2 if dV is None else _ld2(dV), _ptr(ws),
+                              0 if ws is None else ws.numel() * ws.element_size(), _raw_stream(X))
+    if st:
+        _check(st)
     return dX, dV
 
 
@@ -499,21 +518,28 @@ def nm_spmm_glu_backward(dH: torch.Tensor, G: torch.Tensor, U: torch.Tensor, X: 
                          out_dv: tuple[torch.Tensor, torch.Tensor] | None = None, ws: torch.Tensor | None = None):
     """(dX, dvals_g, dvals_u) of nm_spmm_glu from its saved pre-activations; what is not wanted
     is None."""
-    Mtok, K, R = _check_grad(X, dH, [vals_g, vals_u], [idx_g, idx_u])
-    _row_major(G=G, U=U)
-    _same("G and U", (tuple(G.shape), (Mtok, R)), (tuple(U.shape), (Mtok, R)), (G.dtype, torch.bfloat16),
-          (U.dtype, torch.bfloat16), (_ld2(U), _ld2(G)))
+    Mtok, K, R = _grad_inputs(X, dH, vals_g, idx_g)
+    if not (vals_u.shape == vals_g.shape and idx_u.shape == idx_g.shape and vals_u.stride() == vals_g.stride() and
+            idx_u.stride() == idx_g.stride() and vals_u.dtype == torch.bfloat16 and idx_u.dtype == torch.int32 and
+            vals_u.device == idx_u.device == X.device):
+        _refuse("the gate and up weights must be packed alike", vals_g=vals_g, idx_g=idx_g, vals_u=vals_u, idx_u=idx_u)
+    if not (_rows(G) and _rows(U) and G.shape == U.shape == (Mtok, R) and G.dtype == U.dtype == torch.bfloat16 and
+            G.device == U.device == X.device and _ld2(G) == _ld2(U)):
+        _refuse("G and U must be row-major bf16 tensors of dH's shape with the same row stride", dH=dH, G=G, U=U)
     dX = _grad_out(out_dx, want_dx, (Mtok, K), dxdt, X.device)
     dVg = _grad_out(out_dv[0] if out_dv else None, want_dv, (R, K // 2), dvdt, X.device)
     dVu = _grad_out(out_dv[1] if out_dv else None, want_dv, (R, K // 2), dvdt, X.device)
-    if want_dv:
-        _same("out_dv row strides", (_ld2(dVu), _ld2(dVg)))
+    if want_dv and _ld2(dVu) != _ld2(dVg):
+        _refuse("the two weight gradients must have the same row stride", dVg=dVg, dVu=dVu)
     ws = _need(raw.nm_spmm_glu_backward_workspace(Mtok, K, R), ws, X.device)
-    _check(raw.nm_spmm_glu_backward(_ptr(dH), _ld2(dH), _ptr(G), _ptr(U), _ld2(G), act, _ptr(X), _ld2(X), Mtok, K,
-                                    _ptr(vals_g), _ptr(idx_g), _ptr(vals_u), _ptr(idx_u), R, _ld2(vals_g),
-                                    _ld2(idx_g), _ptr(dX), dxdt, K if dX is None else _ld2(dX), _ptr(dVg), _ptr(dVu),
-                                    dvdt, K // 2 if dVg is None else _ld2(dVg), _ptr(ws),
-                                    0 if ws is None else ws.numel(), _stream(X)))
+    st = raw.nm_spmm_glu_backward(dH.data_ptr(), _ld2(dH), G.data_ptr(), U.data_ptr(), _ld2(G), act, X.data_ptr(),
+                                  _ld2(X), Mtok, K, vals_g.data_ptr(), idx_g.data_ptr(), vals_u.data_ptr(),
+                                  idx_u.data_ptr(), R, _ld2(vals_g), _ld2(idx_g), _ptr(dX), dxdt,
+                                  K if dX is None else _ld2(dX), _ptr(dVg), _ptr(dVu), dvdt,
+                                  K // 2 if dVg is None else _ld2(dVg), _ptr(ws),
+                                  0 if ws is None else ws.numel() * ws.element_size(), _raw_stream(X))
+    if st:
+        _check(st)
     return dX, dVg, dVu
 
 
@@ -537,6 +563,8 @@ class AdamWTensors:
         per = lambda x: [float(x)] * n if isinstance(x, (int, float)) else [float(y) for y in x]  # noqa: E731
         lr_scale, weight_decay = per(lr_scale), per(weight_decay)
         _same("lr_scale and weight_decay", (len(lr_scale), n), (len(weight_decay), n))
+        if any(t.device.type != "cuda" for t in params):
+            raise ValueError("the tensors of an optimiser step are on a GPU")
         self.keep = [list(params)] + [None if t is None else list(t) for t in lists.values()]
         self.device = params[0].device if n else None
         kinds = {t.dtype for t in [*m, *v]}
@@ -546,6 +574,7 @@ class AdamWTensors:
         if self.sdt == NM_FP8 and (m_scale is None or v_scale is None):
             raise ValueError("8-bit states need m_scale and v_scale")
         self.count, self.array = n, (_AdamWTensor * max(n, 1))()
+        self.address = ctypes.addressof(self.array)
         for i in range(n):
             p, k = params[i], params[i].numel()
             for name, t in lists.items():
@@ -574,6 +603,7 @@ def nm_adamw(tensors: AdamWTensors, lr: float, step: int, beta1: float = 0.9, be
         raise ValueError("grad_scale must be one f32 value on the device")
     if tensors.count == 0:
         return
-    with torch.cuda.device(tensors.device):
-        _check(raw.nm_adamw(ctypes.addressof(tensors.array), tensors.count, tensors.sdt, lr, beta1, beta2, eps, step,
-                            _ptr(grad_scale), torch.cuda.current_stream(tensors.device).cuda_stream))
+    st = raw.nm_adamw(tensors.address, tensors.count, tensors.sdt, lr, beta1, beta2, eps, step, _ptr(grad_scale),
+                      torch._C._cuda_getCurrentRawStream(tensors.device.index))
+    if st:
+        _check(st)
