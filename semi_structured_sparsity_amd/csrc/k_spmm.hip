@@ -1686,24 +1686,26 @@ constexpr int kRedStride = 20;
 // same stage order takes about 10 us.
 constexpr int kXresBytes = 64 * 1024 + 32 * 16;
 
-template <typename T, int SR, int ST, int KB, int NS, bool LIFT = false, int XRB_ = 0, bool GLU = false>
-__global__ __launch_bounds__(256, 1) void spmm_ringk_kernel(SpmmArgs a) {
+template <typename T, int SR, int ST, int KB, int NS, bool LIFT = false, int XRB_ = 0, bool GLU = false, int IGS = 0, int OCC = 1>
+__global__ __launch_bounds__(256, OCC) void spmm_ringk_kernel(SpmmArgs a) {
     constexpr bool XRES = XRB_ > 0;
     constexpr int es = sizeof(T);
     constexpr int KO = KB / es, KDEP = es == 2 ? 32 : 64;
     static_assert(KO / KDEP == 4, "one depth per wave per stage");
-    static_assert(!(LIFT && XRES), "the resident X holds original columns of the unlifted product only");
     constexpr int BR = 32 * SR, BT = 32 * ST;
     constexpr int AROW = KO / 2 * es, ACH = AROW / 16, AI = KO / 32, BCH = KB / 16;
     static_assert(ACH == 8 && BCH == 16, "swizzles below are for 8-chunk weight rows and 16-chunk X rows");
-    constexpr int I_OFF = BR * AROW, B_OFF = I_OFF + BR * AI * 4, STAGE = B_OFF + (XRES ? 0 : BT * KB);
+    constexpr int I_OFF = BR * AROW, B_OFF = I_OFF + (IGS ? 0 : BR * AI * 4), STAGE = B_OFF + (XRES ? 0 : BT * KB);
+    // grouped index words: a row's 128 bytes of IGS stages at a time, in GB buffers after the ring
+    static_assert(IGS == 0 || (IGS * AI == 32 && (BR * 32) % (64 * 4 * IGS) == 0), "a group is a line per row");
+    constexpr int GB = IGS ? (NS - 2 + IGS - 1) / IGS + 2 : 0, GBYTES = BR * 128;
     constexpr int NA = BR * AROW / 1024 / 4, NI = BR * AI * 4 / 256 / 4, NB = XRES ? 0 : BT * KB / 1024 / 4;
     constexpr int PER = NA + NI + NB;   // loads per wave per stage
     static_assert(NA >= 1 && NI >= 1 && (XRES || NB >= 1) && (BR * AROW) % 4096 == 0 && (BR * AI * 4) % 1024 == 0 &&
                       (BT * KB) % 4096 == 0,
                   "loads must split evenly over the 4 waves");
     static_assert(!XRES || ST == 1, "resident X for up to 32 tokens");
-    constexpr int X_OFF = NS * STAGE, XRB = XRB_;
+    constexpr int G_OFF = NS * STAGE, X_OFF = G_OFF + GB * GBYTES, XRB = XRB_;
     constexpr int RED = (GLU ? 2 : 1) * 4 * 64 * kRedStride * 4;   // one sub-tile (GLU: a pair) of all four waves
     static_assert(!GLU || SR == 2, "a tile is one run of 32 gate and 32 up rows");
     constexpr int LDS = X_OFF + XRB > RED ? X_OFF + XRB : RED;
@@ -1753,6 +1755,21 @@ __global__ __launch_bounds__(256, 1) void spmm_ringk_kernel(SpmmArgs a) {
         const int64_t gr = wrow(row) < rmax ? wrow(row) : rmax;
         oI[i] = (uint32_t)(gr * a.ldi * 4 + lw * 4);
     }
+    // IGS: batch b (0 .. IGS - 1) of index group g, NI loads of two rows per wave: the wave's rows are
+    // those of its values, BR / 4 of the tile.  Words past the row's last are clamped to it (read,
+    // never used).
+    const uint32_t ilast = (uint32_t)(a.nsteps * AI * 4 - 4);
+    auto issue_group = [&](int g, int b) __attribute__((always_inline)) {
+#pragma unroll
+        for (int i = 0; i < NI; ++i) {
+            const int pair = wave * (BR / 8) + b * NI + i;
+            const int row = 2 * pair + h, lw = l32 ^ iswz<32>(row);
+            const int64_t gr = wrow(row) < rmax ? wrow(row) : rmax;
+            uint32_t off = (uint32_t)(s_begin * AI * 4 + g * 128 + lw * 4);
+            off = off < ilast ? off : ilast;
+            dma4s(sbase + (uint32_t)(G_OFF + (g % (GB ? GB : 1)) * GBYTES + pair * 256), baseI, (uint32_t)(gr * a.ldi * 4) + off);
+        }
+    };
 #pragma unroll
     for (int i = 0; i < NB; ++i) {
         const int row = (wave * NB + i) * (64 / BCH) + lane / BCH;
@@ -1773,7 +1790,12 @@ __global__ __launch_bounds__(256, 1) void spmm_ringk_kernel(SpmmArgs a) {
 #pragma unroll
         for (int i = 0; i < NA; ++i) dma16s(st + (wave * NA + i) * 1024, baseA, oA[i] + (uint32_t)(sg * AROW));
 #pragma unroll
-        for (int i = 0; i < NI; ++i) dma4s(st + I_OFF + (wave * NI + i) * 256, baseI, oI[i] + (uint32_t)(sg * AI * 4));
+        for (int i = 0; i < (IGS ? 0 : NI); ++i)
+            dma4s(st + I_OFF + (wave * NI + i) * 256, baseI, oI[i] + (uint32_t)(sg * AI * 4));
+        if constexpr (IGS > 0) {
+            // stage sl >= 1 carries batch (sl-1) % IGS of group (sl-1) / IGS + 1; group 0 is loaded up front
+            if (sl >= 1) issue_group((sl - 1) / IGS + 1, (sl - 1) % IGS);
+        }
         if constexpr (XRES) {
             // X is resident
         } else if constexpr (LIFT) {
@@ -1790,7 +1812,14 @@ __global__ __launch_bounds__(256, 1) void spmm_ringk_kernel(SpmmArgs a) {
     };
     // XRES: valid token rows of the tile, padded LDS row bytes of the resident X
     const int xmv = XRES ? (int)(a.Mtok - t0 < BT ? a.Mtok - t0 : BT) : 0;
-    const int xcpr = XRES ? (nloc * KB + 1023) / 1024 : 0;   // 1 KB loads per row
+    // (LIFT: original columns from the first stage's slot on)
+    const uint32_t xbeg = LIFT ? slot_start(s_begin) : (uint32_t)(s_begin * KB);
+    uint32_t xbytes = (uint32_t)(nloc * KB);
+    if constexpr (XRES && LIFT) {
+        const uint32_t end = nloc > 0 ? slot_start(s_end - 1) + KB : xbeg;
+        xbytes = (end < (uint32_t)a.xrow_bytes ? end : (uint32_t)a.xrow_bytes) - xbeg;
+    }
+    const int xcpr = XRES ? (int)((xbytes + 1023) / 1024) : 0;   // 1 KB loads per row
     const int xrowp = xcpr * 1024 + 16;
     struct Frag {
         i32x4_t a[SR];
@@ -1854,13 +1883,21 @@ __global__ __launch_bounds__(256, 1) void spmm_ringk_kernel(SpmmArgs a) {
         for (int i = 0; i < SR; ++i) {
             const int row = i * 32 + l32;
             f.a[i] = *(const i32x4_t*)(sA + row * AROW + ((2 * d + h) ^ swa(row)) * 16);
-            f.iw[i] = sI[row * AI + ((es == 2 ? d : 2 * d + h) ^ iswz<AI>(row))];
+            if constexpr (IGS > 0) {
+                const uint32_t* sG = (const uint32_t*)(smem + G_OFF + ((sl / IGS) % GB) * GBYTES);
+                f.iw[i] = sG[row * 32 + (((sl % IGS) * AI + (es == 2 ? d : 2 * d + h)) ^ iswz<32>(row))];
+            } else {
+                f.iw[i] = sI[row * AI + ((es == 2 ? d : 2 * d + h) ^ iswz<AI>(row))];
+            }
         }
 #pragma unroll
         for (int j = 0; j < ST; ++j) {
             const int tok = j * 32 + l32;
             const uint8_t* trow = sB + tok * KB;
-            if constexpr (XRES) {
+            if constexpr (XRES && LIFT) {
+                const uint8_t* xr = smem + X_OFF + (tok < xmv ? tok : xmv - 1) * xrowp;
+                f.b[j] = lifted_frag(xr + (slot_start(s_begin + sl) - xbeg), 0, s_begin + sl);
+            } else if constexpr (XRES) {
                 const uint8_t* xr = smem + X_OFF + (tok < xmv ? tok : xmv - 1) * xrowp + sl * KB;
                 const i32x4_t lo = *(const i32x4_t*)(xr + (4 * d + h) * 16);
                 const i32x4_t hi = *(const i32x4_t*)(xr + (4 * d + 2 + h) * 16);
@@ -1901,14 +1938,17 @@ __global__ __launch_bounds__(256, 1) void spmm_ringk_kernel(SpmmArgs a) {
         // row's padding.  The caller guarantees xmv * xrowp <= XRB; rows that would not fit
         // are not loaded.
         const int rows = xmv * xrowp <= XRB ? xmv : XRB / xrowp;
-        const uint32_t kbytes = (uint32_t)(nloc * KB);
         for (int q = wave; q < rows * xcpr; q += 4) {
             const int t = q / xcpr, c = q - t * xcpr;
             uint32_t off = (uint32_t)(c * 1024 + lane * 16);
-            off = off < kbytes - 16 ? off : kbytes - 16;
-            dma16s(sbase + (uint32_t)(X_OFF + t * xrowp + c * 1024), baseB,
-                   (uint32_t)(t * a.ldx * es) + (uint32_t)(s_begin * KB) + off);
+            off = off < xbytes - 16 ? off : xbytes - 16;
+            dma16s(sbase + (uint32_t)(X_OFF + t * xrowp + c * 1024), baseB, (uint32_t)(t * a.ldx * es) + xbeg + off);
         }
+    }
+    if constexpr (IGS > 0) {
+#pragma unroll
+        for (int b = 0; b < IGS; ++b)
+            if (nloc > 0) issue_group(0, b);
     }
 #pragma unroll
     for (int p = 0; p < NS; ++p)
@@ -2996,6 +3036,15 @@ static void launch_glu_combine(const void* P, int S, const GluIn& g, hipStream_t
 #undef NM_COMBINE
 }
 
+// Up to 64 tokens two blocks share a CU (80 KB of LDS each): while one waits at a stage's
+// barrier or reduces its tile the other keeps loads in flight.  That outweighs the ring
+// depth: 11008 x 4096 at 16 tokens 29.0 us with 8 stages and one block, 23.3 with 3 stages and
+// two; one token 25.1 -> 21.9 (8 stages against 5); 14336 x 4096 FP8 6:8 at 16 tokens
+// 38.9 -> 27.6; 64 tokens 39.5 -> 36.4 (5 stages against 2).  A resident X of up to 64 KB
+// beside one block's 8 stages was the slower form everywhere; up to kGluX bytes of it (one
+// token of 4096 bf16 columns) leave two blocks room for 5 stages.
+constexpr int kGluX = 16 * 1024;
+
 // The fused kernels by token count, as for the plain product with R features in place of
 // rows and half as many of them per tile:
 //   kind 1: K-split ring, 32 features x 32 / 64 / 128 tokens (up to 256 tokens)
@@ -3042,13 +3091,30 @@ static GluPlan plan_glu(int64_t Mtok, int64_t K, int64_t R, bool ring_ok, bool l
         }
         p.tiles_r = (int)rt;
         p.tiles_t = (int)ceil_div(Mtok, 32 * p.mid);
+        // more tiles than CUs: equal tiles that fill whole rounds (the rows a tile does not use re-read
+        // its last one, one line a load).  Measured: 11008 features at one token 23.1 -> 21.9 us (501
+        // tiles of 22 features in place of 344 of 32)
+        const int64_t tiles = rt * p.tiles_t, rounds = ceil_div(tiles, cus);
+        if (p.mid <= 2 && rounds > 1) {
+            const int64_t rows = ceil_div(R, rounds * cus / p.tiles_t);
+            if (rows < 32) {
+                p.tile_rows = (int)rows;
+                p.tiles_r = (int)ceil_div(R, rows);
+            }
+        }
+        // a K split (a second launch adds the partials) only where few tiles would run: 1000 features
+        // at one token (32 tiles) 11.7 -> 8.8 us in 4 splits, 3000 (94) 11.8 against 11.5 in two
         int ks = 1;
-        while ((int64_t)p.tiles_r * p.tiles_t * ks < 160 && p.nsteps >= 8 * ks) ks *= 2;
+        if (p.tiles_r * p.tiles_t < 64)
+            while ((int64_t)p.tiles_r * p.tiles_t * ks < 128 && p.nsteps >= 8 * ks) ks *= 2;
         p.steps_per_split = (int)ceil_div(p.nsteps, ks);
         p.KS = (int)ceil_div(p.nsteps, p.steps_per_split);
-        if (!lift && p.mid == 1) {
-            const int64_t rows = Mtok < 32 ? Mtok : 32;
-            p.xres = rows * (ceil_div((int64_t)p.steps_per_split * 256, 1024) * 1024 + 16) <= kXresBytes;
+        if (p.mid == 1) {
+            // bytes of a token's columns of one block's stages (lifted: at most 2/3 of the stages' 256
+            // bytes, and one slot), and the slots read past the last row
+            const int64_t cols = lift ? (int64_t)p.steps_per_split * 171 + 272 : (int64_t)p.steps_per_split * 256;
+            const int64_t need = (Mtok < 32 ? Mtok : 32) * (ceil_div(cols, 1024) * 1024 + 16) + (lift ? 512 : 0);
+            p.xres = need <= kGluX ? 1 : 0;
         }
         return p;
     }
@@ -3092,17 +3158,21 @@ static nm_status run_glu(SpmmArgs a, const GluPlan& p, bool lift, void* part, co
         a.tiles_t = p.tiles_t;
         a.tile_rows = p.tile_rows;
         const dim3 grid((unsigned)(p.tiles_r * p.tiles_t), (unsigned)p.KS);
-#define NM_GLUK(ST, NS, LIFT, XRB) \
-    hipLaunchKernelGGL((spmm_ringk_kernel<T, 2, ST, 256, NS, LIFT, XRB, true>), grid, dim3(256), 0, s, a)
+        // index words in groups of a line per row: IGS stages a group.  (Loaded stage by stage they touch as
+        // many lines as the values: one token 26.3 -> 23.0 us with the groups.)
+#define NM_GLUK(ST, NS, LIFT, XRB, OCC)                                                                              \
+    hipLaunchKernelGGL((spmm_ringk_kernel<T, 2, ST, 256, NS, LIFT, XRB, true, sizeof(T) == 2 ? 8 : 4, OCC>), grid, \
+                       dim3(256), 0, s, a)
         if (lift) {
-            if (p.mid == 1) NM_GLUK(1, 6, true, 0);
-            else if (p.mid == 2) NM_GLUK(2, 3, true, 0);
-            else if constexpr (sizeof(T) == 2) NM_GLUK(4, 3, true, 0);
+            if (p.xres) NM_GLUK(1, 5, true, kGluX, 2);
+            else if (p.mid == 1) NM_GLUK(1, 3, true, 0, 2);
+            else if (p.mid == 2) NM_GLUK(2, 2, true, 0, 2);
+            else if constexpr (sizeof(T) == 2) NM_GLUK(4, 3, true, 0, 1);
             else return set_error(NM_ERR_DEVICE, "nm_spmm_glu: no in-kernel lift for one-byte codes on 128-token tiles");
-        } else if (p.xres) NM_GLUK(1, 8, false, kXresBytes);
-        else if (p.mid == 1) NM_GLUK(1, 6, false, 0);
-        else if (p.mid == 2) NM_GLUK(2, 3, false, 0);
-        else NM_GLUK(4, 3, false, 0);
+        } else if (p.xres) NM_GLUK(1, 5, false, kGluX, 2);
+        else if (p.mid == 1) NM_GLUK(1, 3, false, 0, 2);
+        else if (p.mid == 2) NM_GLUK(2, 2, false, 0, 2);
+        else NM_GLUK(4, 3, false, 0, 1);
 #undef NM_GLUK
     } else {
         auto launch = [&](bool big, int64_t f_begin, int64_t f_end) {
