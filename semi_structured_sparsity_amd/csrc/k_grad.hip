@@ -1,0 +1,592 @@
+// Gradients of the sparse layer and of the gated feed-forward block (bf16, plain 2:4).
+//
+// For y = x W^T with W [R, K] packed 2:4, and for a gated block with pre-activations
+// G = x Wg^T, U = x Wu^T, H = act(G) . U:
+//   dG = dH . U . act'(G),  dU = dH . act(G)
+//   dX = dY W               (gated: dG Wg + dU Wu)
+//   dV[r, j] = sum_m dY[m, r] X[m, col(r, j)]   for the kept positions col(r, j) only.
+// Neither product can use the sparse instructions: they skip zeros of the operand along the
+// summed dimension, W is 2:4 along K, but dX sums over R and dV over the tokens.  Both run as
+// dense products on 256 x 256 tiles (grad_ring_kernel), bound by the matrix
+// cores and the operand stream; dV's epilogue keeps the packed positions of each tile, so the
+// dense gradient never exists.
+// The ring wants both operands with the summed dimension contiguous, so the operands
+// are laid out once, in the workspace, by the bandwidth-bound kernels below:
+//   D  [M, nmat * Rp]  dY, or dG | dU, the rows padded to Rp = a multiple of 64 with zeros,
+//   DT [nmat * Rp, Mp] its transpose, the tokens padded to Mp = a multiple of 64 with zeros,
+//   XT [K, Mp]         X transposed,
+//   WT [K, nmat * Rp]  the packed weights, dense and transposed.
+#include "nm_ring.h"
+
+namespace nm {
+
+// ------------------------------------------------------------------ layouts
+// The operands' layouts, in one launch whose blocks take 64 x 64 tiles of dY (or of dH, G and
+// U), 64 x 64 tiles of X and 64 x 128 tiles of the packed weights.  A thread holds two rows of its
+// tile (2 p and 2 p + 1); transposed tiles go through LDS as row-pair words t[column][pair]
+// with 33 words a column, the pairs of columns 64-127 swapped in eights, so that the 64
+// lanes of a write fall on distinct banks.
+struct PairTile {
+    uint32_t t[128][33];
+    __device__ static int at(int col, int pair) { return pair ^ (((col >> 6) & 1) * 8); }
+    __device__ __forceinline__ void put(int col, int pair, uint32_t lo, uint32_t hi) { t[col][at(col, pair)] = lo | (hi << 16); }
+    // rows 8 q .. 8 q + 7 of a column, 16 bytes
+    __device__ __forceinline__ uint4 get(int col, int q) const {
+        const uint32_t* w = &t[col][at(col, 4 * q)];
+        return make_uint4(w[0], w[1], w[2], w[3]);
+    }
+};
+
+// 8 bf16 of a row from column c; zero past cols (or if !ok)
+template <bool VEC>
+__device__ __forceinline__ void load_row8(const uint16_t* __restrict__ row, int64_t c, int64_t cols, bool ok,
+                                          uint32_t (&x)[8]) {
+    if (VEC && ok && c + 8 <= cols) {
+        const uint4 u = *(const uint4*)(row + c);
+        const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            x[2 * e] = w[e] & 0xffffu;
+            x[2 * e + 1] = w[e] >> 16;
+        }
+        return;
+    }
+#pragma unroll
+    for (int e = 0; e < 8; ++e) x[e] = ok && c + e < cols ? row[c + e] : 0u;
+}
+__device__ __forceinline__ uint4 pack8(const uint32_t (&x)[8]) {
+    return make_uint4(x[0] | (x[1] << 16), x[2] | (x[3] << 16), x[4] | (x[5] << 16), x[6] | (x[7] << 16));
+}
+
+struct LayoutArgs {
+    GradIn in;
+    int64_t Rp, Mp, Rn;
+    uint16_t *D, *DT, *XT, *WT;   // null: not needed
+    int nd, nw, nx;               // blocks of the dY tiles, of the weights, of X
+    int td, tw, tx;               // tiles along a row of each
+};
+
+// S [rows, cols] (lds), tile (ti, tj) -> T [cols, rowsp] and the copy C (ldc), both zero past the
+// edges
+template <bool VEC>
+__device__ __forceinline__ void transpose_tile(PairTile& tile, const uint16_t* __restrict__ S, int64_t lds, int64_t rows,
+                                               int64_t cols, uint16_t* __restrict__ T, int64_t rowsp,
+                                               uint16_t* __restrict__ C, int64_t ldc, int ti, int tj) {
+    const int tid = threadIdx.x, c8 = tid & 7, pair = tid >> 3;
+    const int64_t r0 = (int64_t)ti * 64, c0 = (int64_t)tj * 64;
+    const int64_t r = r0 + 2 * pair, c = c0 + 8 * c8;
+    uint32_t x[2][8];
+#pragma unroll
+    for (int k = 0; k < 2; ++k) load_row8<VEC>(S + (r + k) * lds, c, cols, r + k < rows, x[k]);
+    if (C) {
+#pragma unroll
+        for (int k = 0; k < 2; ++k)
+            if (r + k < rows) *(uint4*)(C + (r + k) * ldc + c) = pack8(x[k]);
+    }
+    if (!T) return;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) tile.put(c8 * 8 + e, pair, x[0][e], x[1][e]);
+    __syncthreads();
+#pragma unroll
+    for (int p = 0; p < 2; ++p) {
+        const int col = (tid >> 3) + 32 * p, q = tid & 7;
+        if (c0 + col < cols) *(uint4*)(T + (c0 + col) * rowsp + r0 + 8 * q) = tile.get(col, q);
+    }
+}
+
+// dG | dU from dH, G, U: rows of D [M, 2 Rp] and of DT [2 Rp, Mp], padded with zeros.  They are
+// rounded to bf16 here: operands of the bf16 matrix products, as the forward's activations are.
+template <int ACT, bool VEC>
+__device__ __forceinline__ void glu_grad_tile(PairTile& tile, const LayoutArgs& a, int ti, int tj) {
+    const GradIn& in = a.in;
+    const int tid = threadIdx.x, c8 = tid & 7, pair = tid >> 3;
+    const int64_t m0 = (int64_t)ti * 64, c0 = (int64_t)tj * 64;
+    const int64_t m = m0 + 2 * pair, c = c0 + 8 * c8;
+    uint32_t dg[2][8], du[2][8];
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+        const bool ok = m + k < in.M;
+        uint32_t h[8], g[8], u[8];
+        load_row8<VEC>(in.dY + (m + k) * in.lddy, c, in.R, ok, h);
+        load_row8<VEC>(in.G + (m + k) * in.ldg, c, in.R, ok, g);
+        load_row8<VEC>(in.U + (m + k) * in.ldg, c, in.R, ok, u);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            const float hf = bf16_bits_to_f32(h[e]), gf = bf16_bits_to_f32(g[e]), uf = bf16_bits_to_f32(u[e]);
+            float f, d;
+            act_and_grad<ACT>(gf, f, d);
+            dg[k][e] = f32_to_bf16_bits(hf * uf * d);
+            du[k][e] = f32_to_bf16_bits(hf * f);
+        }
+        if (a.D && ok) {
+            *(uint4*)(a.D + (m + k) * a.Rn + c) = pack8(dg[k]);
+            *(uint4*)(a.D + (m + k) * a.Rn + a.Rp + c) = pack8(du[k]);
+        }
+    }
+    if (!a.DT) return;
+    // columns 0-63 of the tile: dG, 64-127: dU
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+        tile.put(c8 * 8 + e, pair, dg[0][e], dg[1][e]);
+        tile.put(64 + c8 * 8 + e, pair, du[0][e], du[1][e]);
+    }
+    __syncthreads();
+#pragma unroll
+    for (int p = 0; p < 4; ++p) {
+        const int col = (tid >> 3) + 32 * p, q = tid & 7;
+        *(uint4*)(a.DT + ((int64_t)(p >> 1) * a.Rp + c0 + (col & 63)) * a.Mp + m0 + 8 * q) = tile.get(col, q);
+    }
+}
+
+// 64 rows x 128 columns of a packed 2:4 weight (a line of values per row) -> WT [K, Rn] at columns
+// off + r (rows past R: zero).  Thread (c, pair): rows 2 pair, 2 pair + 1, columns 16 c ..: 8
+// values and 16 bits of positions per row; K is a multiple of 16.
+__device__ __forceinline__ void decode_tile(PairTile& tile, const LayoutArgs& a, int mat, int ti, int tj) {
+    const GradIn& in = a.in;
+    const int tid = threadIdx.x, c = tid & 7, pair = tid >> 3;
+    const int64_t r0 = (int64_t)ti * 64, k0 = (int64_t)tj * 128, k = k0 + 16 * c;
+    uint32_t x[2][16];
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+        const int64_t r = r0 + 2 * pair + j;
+        const bool ok = r < in.R && k < in.K;
+        const uint4 v = ok ? *(const uint4*)(in.vals[mat] + r * in.ldv + k / 2) : make_uint4(0, 0, 0, 0);
+        const uint32_t b = ok ? in.idx[mat][r * in.ldi + k / 32] >> (16 * (c & 1)) : 0u;
+        const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+            const uint32_t v0 = w[q] & 0xffffu, v1 = w[q] >> 16;
+            const uint32_t p0 = (b >> (4 * q)) & 3u, p1 = (b >> (4 * q + 2)) & 3u;
+#pragma unroll
+            for (uint32_t e = 0; e < 4; ++e) x[j][4 * q + e] = (p0 == e ? v0 : 0u) | (p1 == e ? v1 : 0u);
+        }
+    }
+#pragma unroll
+    for (int e = 0; e < 16; ++e) tile.put(c * 16 + e, pair, x[0][e], x[1][e]);
+    __syncthreads();
+#pragma unroll
+    for (int p = 0; p < 4; ++p) {
+        const int col = (tid >> 3) + 32 * p, q = tid & 7;
+        if (k0 + col < in.K) *(uint4*)(a.WT + (k0 + col) * a.Rn + mat * a.Rp + r0 + 8 * q) = tile.get(col, q);
+    }
+}
+
+// ACT: the gated block's activation, or -1: dY itself
+template <int ACT, bool VEC>
+__global__ __launch_bounds__(256) void grad_layout_kernel(LayoutArgs a) {
+    __shared__ PairTile tile;
+    int b = blockIdx.x;
+    if (b < a.nw) {
+        const int mat = b / (a.nw / (ACT >= 0 ? 2 : 1));
+        b -= mat * (a.nw / 2);
+        decode_tile(tile, a, mat, b / a.tw, b % a.tw);
+    } else if (b < a.nw + a.nd) {
+        b -= a.nw;
+        if constexpr (ACT >= 0) glu_grad_tile<ACT, VEC>(tile, a, b / a.td, b % a.td);
+        else transpose_tile<VEC>(tile, a.in.dY, a.in.lddy, a.in.M, a.in.R, a.DT, a.Mp, a.D, a.Rn, b / a.td, b % a.td);
+    } else {
+        b -= a.nw + a.nd;
+        transpose_tile<true>(tile, a.in.X, a.in.ldx, a.in.M, a.in.K, a.XT, a.Mp, (uint16_t*)nullptr, 0, b / a.tx, b % a.tx);
+    }
+}
+
+// ------------------------------------------------------------------ products
+// One of the two products of a backward call: C^T tiles of 256 A rows x 256 B rows, summed over
+// nsteps stages of 64 columns.
+struct GradJob {
+    const uint16_t *A, *B;
+    int64_t lda, ldb, rowsA, rowsB;
+    int nsteps, spp;          // stages, stages per split
+    int tiles_a, tiles_b;     // tiles of a split
+};
+struct GradArgs {
+    GradJob x, v;             // dX: A = WT (columns k), B = D (tokens); dV: A = XT (k), B = DT (rows r)
+    int nx;                   // blocks of dX (tiles * splits), the first of the grid
+    // dX
+    void* dX;
+    float* part;              // split partials [split][M][K], or null
+    int64_t lddx;
+    int dxf32;
+    // dV
+    const uint32_t* idx[2];
+    void* dV[2];
+    int64_t ldi, lddv, R, Rp;
+    int dvf32;
+};
+
+// Gradient of packed 2:4 values: of the tile's columns k (rows rw .. of the accumulators) of
+// weight row r (the lane's token, from tw) only the kept positions are stored.  Elements
+// 4g .. 4g+3 of a lane's sub-tile are columns 32 i + 8 g + 4 h .. + 3, one group of 4, whose
+// two 2-bit positions are bits 4 (2 g + h) .. of the row's index word of those 32 columns.  A
+// lane's 8 kept values alternate in pairs with the other half-wave's; two swaps across the
+// halves leave each lane with the 8 consecutive values of 16 columns (K is a multiple of 16,
+// so all of them exist or none).
+template <int SR, int ST>
+__device__ __forceinline__ void store_grad_tile(const GradArgs& a, const f32x16_t (&acc)[SR][ST], int64_t rw,
+                                                int64_t tw, int lane) {
+    const int64_t K = a.v.rowsA;
+    const int h = lane >> 5, l32 = lane & 31;
+#pragma unroll
+    for (int j = 0; j < ST; ++j) {
+        const int64_t q = tw + j * 32 + l32;   // stacked row
+        const int mat = q >= a.Rp ? 1 : 0;
+        const int64_t r = q - mat * a.Rp;
+        const bool row_ok = q < a.v.rowsB && r < a.R;
+        const uint32_t* irow = (mat ? a.idx[1] : a.idx[0]) + (row_ok ? r : 0) * a.ldi;
+        uint8_t* orow = (uint8_t*)(mat ? a.dV[1] : a.dV[0]);
+#pragma unroll
+        for (int i = 0; i < SR; ++i) {
+            const int64_t k = rw + i * 32;
+            const uint32_t word = row_ok && k < K ? irow[k >> 5] : 0u;
+            float v0[4], v1[4];
+#pragma unroll
+            for (int g = 0; g < 4; ++g) {
+                const uint32_t b = (word >> (8 * g + 4 * h)) & 15u, p0 = b & 3u, p1 = b >> 2;
+                const float x0 = acc[i][j][4 * g], x1 = acc[i][j][4 * g + 1], x2 = acc[i][j][4 * g + 2],
+                            x3 = acc[i][j][4 * g + 3];
+                const float lo0 = p0 & 1u ? x1 : x0, hi0 = p0 & 1u ? x3 : x2;
+                const float lo1 = p1 & 1u ? x1 : x0, hi1 = p1 & 1u ? x3 : x2;
+                v0[g] = p0 & 2u ? hi0 : lo0;
+                v1[g] = p1 & 2u ? hi1 : lo1;
+            }
+            // lane half h: values of columns k + 16 h .. + 15
+            const int64_t kc = k + 16 * h;
+            const bool ok = row_ok && kc < K;
+            const int64_t o = r * a.lddv + kc / 2;
+            if (!a.dvf32) {
+                uint32_t w[4];
+#pragma unroll
+                for (int g = 0; g < 4; ++g) w[g] = f32_to_bf16_bits(v0[g]) | (f32_to_bf16_bits(v1[g]) << 16);
+                const auto s0 = __builtin_amdgcn_permlane32_swap(w[0], w[2], false, false);
+                const auto s1 = __builtin_amdgcn_permlane32_swap(w[1], w[3], false, false);
+                if (ok) *(uint4*)((uint16_t*)orow + o) = make_uint4(s0[0], s0[1], s1[0], s1[1]);
+            } else {
+                uint32_t a0[4], a1[4];
+#pragma unroll
+                for (int g = 0; g < 4; ++g) a0[g] = __float_as_uint(v0[g]), a1[g] = __float_as_uint(v1[g]);
+                const auto s0 = __builtin_amdgcn_permlane32_swap(a0[0], a0[2], false, false);
+                const auto s1 = __builtin_amdgcn_permlane32_swap(a1[0], a1[2], false, false);
+                const auto s2 = __builtin_amdgcn_permlane32_swap(a0[1], a0[3], false, false);
+                const auto s3 = __builtin_amdgcn_permlane32_swap(a1[1], a1[3], false, false);
+                if (ok) {
+                    *(uint4*)((float*)orow + o) = make_uint4(s0[0], s1[0], s0[1], s1[1]);
+                    *(uint4*)((float*)orow + o + 4) = make_uint4(s2[0], s3[0], s2[1], s3[1]);
+                }
+            }
+        }
+    }
+}
+
+// Both products in one grid, dX's blocks first: a dX tile sums over all rows of the weights and a
+// dV tile over all tokens, so the long blocks start first and the short ones fill the CUs
+// beside and after them; a launch of its own for each would end in a part-filled round, and
+// dX alone, with fewer tiles than CUs, would have to be split.
+// A tile is 256 x 256, eight waves of 128 x 64 (two per SIMD); stages of 64 columns (a
+// 128-byte line per row) in a two-slot LDS ring filled by DMA, dense v_mfma_f32_32x32x16_bf16.
+// Each depth's fragments are read while the previous depth's MFMAs issue; one barrier a
+// stage, before its last depth: the next stage has landed and every wave has read this one,
+// whose slot is then refilled.
+// Measured at 4096 tokens of an 8192 x 8192 layer: about 1.7 us a stage, 1.25 PFLOP/s.  What
+// bounds it is power and the operand stream together: a loop of the same MFMAs alone on
+// random operands runs a stage in 0.92 us, with the fragment reads 1.35, with the loads and
+// the barrier 1.60.  No faster, to 1%: the loads spread over the stage's depths, all of a
+// stage's fragments read ahead (4 sets), two depths ahead with 16 MFMAs between.
+__global__ __launch_bounds__(512, 1) void grad_ring_kernel(GradArgs g) {
+    constexpr int SR = 4, ST = 2, WRN = 2, WTN = 4, NW = 8, T = 256, ROWB = 128, D = 4;
+    constexpr int ASTAGE = T * ROWB, SLOT = 2 * ASTAGE, NL = ASTAGE / 1024 / NW;   // 4 loads of each operand per wave
+    __shared__ __attribute__((aligned(1024))) uint8_t smem[2 * SLOT > NW * kStageWords<SR> * 4 ? 2 * SLOT : NW * kStageWords<SR> * 4];
+    const int tid = threadIdx.x, lane = tid & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int wr = wave % WRN, wt = wave / WRN;
+    const bool isx = (int)blockIdx.x < g.nx;
+    const GradJob& job = isx ? g.x : g.v;
+    int bid = isx ? blockIdx.x : blockIdx.x - g.nx, split = 0;
+    const int tiles = job.tiles_a * job.tiles_b;
+    if (isx) {
+        split = bid / tiles;
+        bid -= split * tiles;
+    }
+    int ta, tb;
+    tile_of(bid, tiles, job.tiles_a, job.tiles_b, ta, tb);
+    const int64_t a0 = (int64_t)ta * T, b0 = (int64_t)tb * T;
+    const int s_begin = split * job.spp;
+    const int nsteps = job.nsteps - s_begin < job.spp ? job.nsteps - s_begin : job.spp;   // >= 1
+    const uint32_t sbase = lds_addr(smem);
+    auto sw = [](int r) { return (r >> 1) & 7; };   // row r: logical 16-byte chunk c at c ^ sw(r)
+    const void* baseA = uniform_ptr(job.A + a0 * job.lda + (int64_t)s_begin * 64);
+    const void* baseB = uniform_ptr(job.B + b0 * job.ldb + (int64_t)s_begin * 64);
+    const int64_t amax = job.rowsA - 1 - a0, bmax = job.rowsB - 1 - b0;
+    uint32_t oA[NL], oB[NL];
+#pragma unroll
+    for (int i = 0; i < NL; ++i) {
+        const int row = (wave * NL + i) * 8 + (lane >> 3);
+        const uint32_t c = (uint32_t)(((lane & 7) ^ sw(row)) * 16);
+        oA[i] = (uint32_t)((row < amax ? row : amax) * job.lda * 2) + c;
+        oB[i] = (uint32_t)((row < bmax ? row : bmax) * job.ldb * 2) + c;
+    }
+    auto issue = [&](int s) __attribute__((always_inline)) {
+        const uint32_t slot = sbase + (uint32_t)((s & 1) * SLOT);
+#pragma unroll
+        for (int i = 0; i < NL; ++i) dma16s(slot + (wave * NL + i) * 1024, baseA, oA[i] + (uint32_t)(s * ROWB));
+#pragma unroll
+        for (int i = 0; i < NL; ++i) dma16s(slot + ASTAGE + (wave * NL + i) * 1024, baseB, oB[i] + (uint32_t)(s * ROWB));
+    };
+    struct Frag {
+        i32x4_t a[SR], b[ST];
+    };
+    const int h = lane >> 5, l32 = lane & 31;
+    auto read_depth = [&](int s, int d, Frag& f) __attribute__((always_inline)) {
+        const uint8_t* sA = smem + (s & 1) * SLOT;
+        const uint8_t* sB = sA + ASTAGE;
+#pragma unroll
+        for (int i = 0; i < SR; ++i) {
+            const int row = (wr * SR + i) * 32 + l32;
+            f.a[i] = *(const i32x4_t*)(sA + row * ROWB + ((2 * d + h) ^ sw(row)) * 16);
+        }
+#pragma unroll
+        for (int j = 0; j < ST; ++j) {
+            const int row = (wt * ST + j) * 32 + l32;
+            f.b[j] = *(const i32x4_t*)(sB + row * ROWB + ((2 * d + h) ^ sw(row)) * 16);
+        }
+    };
+    f32x16_t acc[SR][ST];
+#pragma unroll
+    for (int i = 0; i < SR; ++i)
+#pragma unroll
+        for (int j = 0; j < ST; ++j) acc[i][j] = f32x16_t{};
+    auto mfmas = [&](const Frag& f) __attribute__((always_inline)) {
+#pragma unroll
+        for (int i = 0; i < SR; ++i)
+#pragma unroll
+            for (int j = 0; j < ST; ++j)
+                acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8_t, f.a[i]),
+                                                                     __builtin_bit_cast(bf16x8_t, f.b[j]), acc[i][j], 0, 0, 0);
+    };
+    // a depth's fragment reads, one after each of its first MFMAs
+    auto interleave = [&]() __attribute__((always_inline)) {
+#pragma unroll
+        for (int i = 0; i < SR + ST; ++i) {
+            __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);   // one MFMA
+            __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);   // one LDS read
+        }
+        __builtin_amdgcn_sched_group_barrier(0x008, SR * ST - SR - ST, 0);
+        __builtin_amdgcn_sched_barrier(0);
+    };
+    Frag fr[2];
+    issue(0);
+    if (nsteps > 1) issue(1);
+    if (nsteps > 1) wait_vm_barrier<2 * NL>();
+    else wait_vm_barrier<0>();
+    read_depth(0, 0, fr[0]);
+    for (int s = 0; s < nsteps; ++s) {
+#pragma unroll
+        for (int d = 0; d + 1 < D; ++d) {
+            read_depth(s, d + 1, fr[(d + 1) & 1]);
+            mfmas(fr[d & 1]);
+            interleave();
+        }
+        // the last depth's fragments complete before the branch (the barrier waits for them anyway)
+        __builtin_amdgcn_s_waitcnt(0xc07f);
+        if (s + 1 < nsteps) {
+            wait_vm_barrier<0>();
+            if (s + 2 < nsteps) issue(s + 2);
+            read_depth(s + 1, 0, fr[0]);
+        }
+        mfmas(fr[(D - 1) & 1]);
+    }
+    wait_vm_all();
+    if (!isx) {
+        store_grad_tile<SR, ST>(g, acc, a0 + wr * SR * 32, b0 + wt * ST * 32, lane);
+        return;
+    }
+    __syncthreads();   // every wave has read the ring: its LDS stages the output
+    SpmmArgs a{};
+    a.Mtok = job.rowsB;
+    a.R = job.rowsA;
+    a.Y = g.part ? (void*)(g.part + (int64_t)split * a.Mtok * a.R) : g.dX;
+    a.ydt = g.part || g.dxf32 ? NM_F32 : NM_BF16;
+    a.ldy = g.part ? a.R : g.lddx;
+    store_tile<uint16_t, SR, ST>(a, acc, a0 + wr * SR * 32, b0 + wt * ST * 32, a0 + T <= a.R && b0 + T <= a.Mtok,
+                                 (uint32_t*)smem + wave * kStageWords<SR>, lane);
+}
+
+// dX from its split partials, in split order
+__global__ __launch_bounds__(256) void grad_reduce_kernel(const float* __restrict__ part, int splits, int64_t M, int64_t K,
+                                                          void* __restrict__ dX, int64_t lddx, int f32) {
+    const int64_t total = M * K;
+    for (int64_t t = (int64_t)blockIdx.x * 256 + threadIdx.x; t < total; t += (int64_t)gridDim.x * 256) {
+        const int64_t m = t / K, k = t - m * K;
+        const float v = split_sum(part + t, splits, total);
+        if (f32) ((float*)dX)[m * lddx + k] = v;
+        else ((uint16_t*)dX)[m * lddx + k] = (uint16_t)f32_to_bf16_bits(v);
+    }
+}
+
+// ------------------------------------------------------------------ host side
+// Splits of dX's sum (Rn / 64 stages).  Beside dV no block should run longer than the whole
+// call's share of a CU (at least 16 stages); alone, the count whose rounds take least.  A
+// stage of a tile measured at about 1.8 us in full rounds, partials at about 4 TB/s with a
+// launch of their own.
+static int grad_x_splits(int64_t M, int64_t K, int64_t Rn, bool with_v) {
+    const int64_t cus = device_cus(), tiles = ceil_div(K, 256) * ceil_div(M, 256), ns = Rn / 64;
+    const int64_t vwork = with_v ? ceil_div(K, 256) * ceil_div(Rn, 256) * ceil_div(M, 64) : 0;
+    int best = 1;
+    double best_us = 1e30;
+    for (int64_t ks = 1; ks <= 16 && ks * 4 <= ns + 3; ++ks) {
+        const int64_t one = ceil_div(ns, ks) + 2;
+        const int64_t share = ceil_div(tiles * ks * one + vwork, cus), rounds = ceil_div(tiles * ks, cus) * one;
+        const int64_t stages = with_v ? (share > rounds ? share : rounds) : rounds;
+        const double us = 1.8 * (double)stages + (ks > 1 ? 4.0 + 8e-6 / 4.0 * (double)(ks * M * K) : 0.0);
+        if (us < best_us) {
+            best_us = us;
+            best = (int)ks;
+        }
+    }
+    return best;
+}
+
+static size_t grad_x_part_bytes(int64_t M, int64_t K, int64_t Rn) {
+    size_t n = 0;
+    for (int v = 0; v < 2; ++v) {
+        const int ks = grad_x_splits(M, K, Rn, v != 0);
+        if (ks > 1 && (size_t)ks * (size_t)(M * K) * 4 > n) n = (size_t)ks * (size_t)(M * K) * 4;
+    }
+    return n;
+}
+
+static int64_t up64(int64_t n) { return (n + 63) & ~(int64_t)63; }
+static size_t up256(size_t n) { return (n + 255) & ~(size_t)255; }
+
+// Workspace of one backward call, in the order it is carved.
+struct GradWs {
+    size_t d = 0, dt = 0, xt = 0, wt = 0, part = 0;
+    size_t total() const { return d + dt + xt + wt + part; }
+};
+static GradWs grad_ws_layout(int64_t M, int64_t K, int64_t R, int nmat) {
+    GradWs w;
+    if (M <= 0 || K <= 0 || R <= 0) return w;
+    const int64_t Rn = nmat * up64(R), Mp = up64(M);
+    w.d = up256((size_t)(M * Rn * 2));
+    w.dt = up256((size_t)(Rn * Mp * 2));
+    w.xt = up256((size_t)(K * Mp * 2));
+    w.wt = up256((size_t)(K * Rn * 2));
+    w.part = up256(grad_x_part_bytes(M, K, Rn));
+    return w;
+}
+size_t grad_ws(int64_t M, int64_t K, int64_t R, int nmat) { return grad_ws_layout(M, K, R, nmat).total(); }
+
+static bool rows16(const void* p, int64_t ld) { return ((uintptr_t)p & 15u) == 0 && ld % 8 == 0; }
+
+// a row-major matrix of width 2-byte units set to zero (ld in bytes)
+__global__ __launch_bounds__(256) void zero_rows_kernel(uint8_t* __restrict__ p, int64_t rows, int64_t width, int64_t ld) {
+    const int64_t n = rows * width;
+    for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < n; i += (int64_t)gridDim.x * 256)
+        *(uint16_t*)(p + (i / width) * ld + (i % width) * 2) = 0;
+}
+
+nm_status launch_grad(const GradIn& in, const GradOut& out, int nmat, void* ws, hipStream_t s) {
+    if (in.M == 0 || in.R == 0) {
+        // an empty sum: dV is zero without tokens, dX without rows
+        auto zero = [&](void* p, int64_t rows, int64_t width, int64_t ld) {   // in 2-byte units
+            if (p && rows > 0)
+                hipLaunchKernelGGL(zero_rows_kernel, dim3(grid_cap(ceil_div(rows * width, 256), 8192)), dim3(256), 0, s,
+                                   (uint8_t*)p, rows, width, ld * 2);
+        };
+        const int64_t vs = out.dvdt == NM_BF16 ? 1 : 2, xs = out.dxdt == NM_BF16 ? 1 : 2;
+        for (int i = 0; i < nmat; ++i) zero(out.dV[i], in.R, in.K / 2 * vs, out.lddv * vs);
+        zero(out.dX, in.M, in.K * xs, out.lddx * xs);
+        return check_launch("backward");
+    }
+    const int64_t Rp = up64(in.R), Rn = nmat * Rp, Mp = up64(in.M);
+    const GradWs w = grad_ws_layout(in.M, in.K, in.R, nmat);
+    uint8_t* p = (uint8_t*)ws;
+    uint16_t* D = (uint16_t*)p;
+    uint16_t* DT = (uint16_t*)(p + w.d);
+    uint16_t* XT = (uint16_t*)(p + w.d + w.dt);
+    uint16_t* WT = (uint16_t*)(p + w.d + w.dt + w.xt);
+    float* PART = (float*)(p + w.d + w.dt + w.xt + w.wt);
+    const bool dx = out.dX != nullptr, dv = out.dV[0] != nullptr;
+    const bool vec = rows16(in.dY, in.lddy) && (nmat == 1 || (rows16(in.G, in.ldg) && rows16(in.U, in.ldg)));
+    // dX reads dY itself where its rows are whole 64-column stages on 16-byte boundaries
+    const bool direct = nmat == 1 && vec && in.R == Rp && in.lddy < (1 << 23);
+    const uint16_t* B = direct ? in.dY : D;
+    const int64_t ldb = direct ? in.lddy : Rn;
+    LayoutArgs l{};
+    l.in = in;
+    l.Rp = Rp;
+    l.Mp = Mp;
+    l.Rn = Rn;
+    l.D = dx && !direct ? D : nullptr;
+    l.DT = dv ? DT : nullptr;
+    l.XT = XT;
+    l.WT = WT;
+    l.td = (int)(Rp / 64);
+    l.tw = (int)ceil_div(in.K, 128);
+    l.tx = (int)ceil_div(in.K, 64);
+    l.nd = l.D || l.DT ? l.td * (int)(Mp / 64) : 0;
+    l.nw = dx ? l.tw * (int)(Rp / 64) * nmat : 0;
+    l.nx = dv ? l.tx * (int)(Mp / 64) : 0;
+    const dim3 gl((unsigned)(l.nd + l.nw + l.nx));
+#define NM_LAYOUT(A)                                                                                  \
+    do {                                                                                              \
+        if (vec) hipLaunchKernelGGL((grad_layout_kernel<A, true>), gl, dim3(256), 0, s, l);           \
+        else hipLaunchKernelGGL((grad_layout_kernel<A, false>), gl, dim3(256), 0, s, l);              \
+    } while (0)
+    if (nmat == 1) NM_LAYOUT(-1);
+    else if (in.act == NM_ACT_SILU) NM_LAYOUT(NM_ACT_SILU);
+    else if (in.act == NM_ACT_GELU) NM_LAYOUT(NM_ACT_GELU);
+    else if (in.act == NM_ACT_GELU_TANH) NM_LAYOUT(NM_ACT_GELU_TANH);
+    else NM_LAYOUT(NM_ACT_RELU2);
+#undef NM_LAYOUT
+    GradArgs g{};
+    int nv = 0, splits = 1;
+    if (dx) {
+        splits = grad_x_splits(in.M, in.K, Rn, dv);
+        GradJob& j = g.x;
+        j.A = WT;
+        j.lda = Rn;
+        j.rowsA = in.K;
+        j.B = B;
+        j.ldb = ldb;
+        j.rowsB = in.M;
+        j.nsteps = (int)(Rn / 64);
+        j.spp = (int)ceil_div(j.nsteps, splits);
+        splits = (int)ceil_div(j.nsteps, j.spp);
+        j.tiles_a = (int)ceil_div(in.K, 256);
+        j.tiles_b = (int)ceil_div(in.M, 256);
+        g.nx = j.tiles_a * j.tiles_b * splits;
+        g.dX = out.dX;
+        g.part = splits > 1 ? PART : nullptr;
+        g.lddx = out.lddx;
+        g.dxf32 = out.dxdt == NM_F32;
+    }
+    if (dv) {
+        GradJob& j = g.v;
+        j.A = XT;
+        j.lda = Mp;
+        j.rowsA = in.K;
+        j.B = DT;
+        j.ldb = Mp;
+        j.rowsB = Rn;
+        j.nsteps = j.spp = (int)(Mp / 64);
+        j.tiles_a = (int)ceil_div(in.K, 256);
+        j.tiles_b = (int)ceil_div(Rn, 256);
+        nv = j.tiles_a * j.tiles_b;
+        for (int i = 0; i < 2; ++i) {
+            g.idx[i] = in.idx[i];
+            g.dV[i] = out.dV[i];
+        }
+        g.ldi = in.ldi;
+        g.lddv = out.lddv;
+        g.R = in.R;
+        g.Rp = Rp;
+        g.dvf32 = out.dvdt == NM_F32;
+    }
+    hipLaunchKernelGGL(grad_ring_kernel, dim3((unsigned)(g.nx + nv)), dim3(512), 0, s, g);
+    if (g.part)
+        hipLaunchKernelGGL(grad_reduce_kernel, dim3(grid_cap(ceil_div(in.M * in.K, 256), 8192)), dim3(256), 0, s, PART,
+                           splits, in.M, in.K, out.dX, out.lddx, g.dxf32);
+    return check_launch(nmat == 2 ? "nm_spmm_glu_backward" : "nm_spmm_backward");
+}
+
+}  // namespace nm

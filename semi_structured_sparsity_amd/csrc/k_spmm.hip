@@ -22,101 +22,9 @@
 // For both, the fragment of depth d (one instruction) is 16 bytes of
 // compressed values at byte 32d + 16(l/32) of a row's step, and two 16-byte B
 // reads at bytes 64d + 16(l/32) and 64d + 32 + 16(l/32) of a token's step.
-#include "nm_internal.h"
+#include "nm_ring.h"
 
 namespace nm {
-
-typedef __bf16 bf16x8_t __attribute__((ext_vector_type(8)));
-typedef __bf16 bf16x16_t __attribute__((ext_vector_type(16)));
-typedef float f32x16_t __attribute__((ext_vector_type(16)));
-typedef int i32x4_t __attribute__((ext_vector_type(4)));
-typedef int i32x8_t __attribute__((ext_vector_type(8)));
-typedef int i32x16_t __attribute__((ext_vector_type(16)));
-
-// OCP FP8 e4m3 code: one byte, multiplied by v_smfmac_f32_32x32x64_fp8_fp8 with the
-// int8 instruction's operand layout and f32 accumulation.
-struct fp8e4m3 {
-    uint8_t v;
-};
-
-// Accumulator types and the sparse instruction of each operand type.  A is the
-// lane's 16 bytes of compressed values, B its 32 bytes of the dense operand, idx
-// its index bits (bf16: the lane's 16-bit half already selected).
-template <typename T>
-struct Mma {   // bf16
-    using Acc = f32x16_t;
-    using AccS = float;
-    __device__ static Acc run(i32x4_t a, i32x8_t b, Acc c, int idx) {
-        return __builtin_amdgcn_smfmac_f32_32x32x32_bf16(__builtin_bit_cast(bf16x8_t, a),
-                                                         __builtin_bit_cast(bf16x16_t, b), c, idx, 0, 0);
-    }
-};
-template <>
-struct Mma<int8_t> {
-    using Acc = i32x16_t;
-    using AccS = int32_t;
-    __device__ static Acc run(i32x4_t a, i32x8_t b, Acc c, int idx) {
-        return __builtin_amdgcn_smfmac_i32_32x32x64_i8(a, b, c, idx, 0, 0);
-    }
-};
-template <>
-struct Mma<fp8e4m3> {
-    using Acc = f32x16_t;
-    using AccS = float;
-    __device__ static Acc run(i32x4_t a, i32x8_t b, Acc c, int idx) {
-        return __builtin_amdgcn_smfmac_f32_32x32x64_fp8_fp8(a, b, c, idx, 0, 0);
-    }
-};
-
-struct SpmmArgs {
-    const uint8_t* X;      // [Mtok, ldx] elements of T
-    const uint8_t* vals;   // [R, ldv] elements of T
-    const uint32_t* idx;   // [R, ldi] words
-    const float* x_scale;  // [Mtok] or null
-    void* Y;               // [Mtok, ldy] of ydt
-    void* part;            // split-K partials [KS][Mtok][R] (f32 or i32) or null
-    int64_t ldx, ldv, ldi, ldy;
-    int64_t Mtok, K, R;
-    int64_t comp_bytes;    // packed value bytes per row (K'/2 * sizeof(T))
-    int64_t idx_words;     // index words per row (ceil(K'/32): two 2-bit fields per 4 lifted columns)
-    int64_t xrow_bytes;    // bytes of one row of the original (unlifted) X, for the in-kernel lift
-    float w_scale;
-    int scaled;
-    int ydt;
-    int nsteps, KS, steps_per_split;
-    int tiles_r, tiles_t;
-    int tile_rows;         // K-split ring: weight rows per row tile (0: the tile's height)
-    // rank-r adapter term added to the accumulators (bf16 products only; rank 0: none):
-    // u [Mtok, rank] (ldu) and the stacked up-projection B [R, rank] (ldb), both bf16
-    const uint16_t* lr_u;
-    const uint16_t* lr_b;
-    int64_t ldu, ldb;
-    int rank;
-    // Hutchinson modes of the dense split ring: probes, their seed, stages per probe, rows
-    // per probe
-    uint64_t seed;
-    int probes, pstages;
-    int64_t prows;
-    // score epilogue of the Hutchinson second product: W [rows of D, K] bf16 (ldw), eps, and
-    // the per-block moments of the scores ([count | mean | m2][blocks])
-    const uint16_t* sw;
-    int64_t ldsw;
-    float eps;
-    double* mpart;
-    // second weight of a pair.  Gradients at the packed positions (dense split ring): the stacked
-    // B rows hold one or two weights of rowsp rows each, prows of them real; positions and
-    // outputs of the second
-    const uint32_t* idx2;
-    void* Y2;
-    int64_t rowsp;
-    // gated block (GLU): vals / idx / w_scale are the gate's and vals2 / idx2 / w_scale2 the up
-    // projection's, R features each; Y is H, Y2 and Y3 the rounded G and U (ldy2) or null
-    const uint8_t* vals2;
-    float w_scale2;
-    int act;
-    void* Y3;
-    int64_t ldy2;
-};
 
 // A gated block's tile interleaves the two weights so that a wave holds the gate and the up
 // accumulators of the same features and tokens: rows come in runs of 2 H, the first H rows of
@@ -165,24 +73,6 @@ struct Tile {
     static constexpr int PI = (NI + NT - 1) / NT;
     static constexpr int PB = (NB + NT - 1) / NT;
 };
-
-// Block index -> (R tile, token tile).  Workgroups are dispatched round-robin
-// over the 8 XCDs; the remap gives each XCD a contiguous range of tiles, and
-// the range is walked in groups of 8 R tiles so that the blocks resident on one
-// XCD at a time share their weight and activation tiles in that XCD's L2.
-__device__ __forceinline__ void tile_of(int bid, int nb, int tiles_r, int tiles_t, int& tr, int& tt) {
-    const int xcd = bid & 7, loc = bid >> 3;
-    const int base = nb >> 3, rem = nb & 7;
-    const int id = xcd * base + (xcd < rem ? xcd : rem) + loc;
-    const int GR = 8;
-    const int per_group = GR * tiles_t;
-    const int grp = id / per_group;
-    const int first = grp * GR;
-    const int gsz = (tiles_r - first) < GR ? (tiles_r - first) : GR;
-    const int in = id - grp * per_group;
-    tr = first + in % gsz;
-    tt = in / gsz;
-}
 
 template <typename T, int WR, int WT, int SR, int ST>
 __global__ __launch_bounds__(WR* WT * 64) void spmm_kernel(SpmmArgs a) {
@@ -381,60 +271,6 @@ __global__ __launch_bounds__(WR* WT * 64) void spmm_kernel(SpmmArgs a) {
 //   A values: row r (64 B = 4 chunks), logical chunk c stored at c ^ ((r>>2)&3)
 //   A index : row r, AI words, unswizzled
 //   X       : token t (128 B = 8 chunks), logical chunk c stored at c ^ ((t>>1)&7)
-typedef __attribute__((address_space(3))) uint8_t lds_u8;
-
-__device__ __forceinline__ uint32_t lds_addr(const void* p) {
-    return (uint32_t)(uintptr_t)(const lds_u8*)p;
-}
-__device__ __forceinline__ void dma16(uint32_t lds, const void* g) {
-    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, off" ::"s"(lds), "v"(g) : "memory", "m0");
-}
-// A block-uniform pointer, moved to scalar registers.
-__device__ __forceinline__ const void* uniform_ptr(const void* p) {
-    const uint64_t v = (uint64_t)(uintptr_t)p;
-    const uint32_t lo = __builtin_amdgcn_readfirstlane((uint32_t)v);
-    const uint32_t hi = __builtin_amdgcn_readfirstlane((uint32_t)(v >> 32));
-    return (const void*)(uintptr_t)(((uint64_t)hi << 32) | lo);
-}
-// saddr form: uniform 64-bit base in SGPRs + per-lane 32-bit byte offset
-__device__ __forceinline__ void dma16s(uint32_t lds, const void* base, uint32_t off) {
-    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2" ::"s"(lds), "v"(off), "s"(base)
-                 : "memory", "m0");
-}
-__device__ __forceinline__ void dma4s(uint32_t lds, const void* base, uint32_t off) {
-    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dword %1, %2" ::"s"(lds), "v"(off), "s"(base)
-                 : "memory", "m0");
-}
-__device__ __forceinline__ void dma4(uint32_t lds, const void* g) {
-    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dword %1, off" ::"s"(lds), "v"(g) : "memory", "m0");
-}
-// Wait until at most N vector-memory loads of this wave are in flight and all its LDS
-// reads are done, then meet the other waves.  The wait is a compiler builtin, so the
-// compiler's own wait-count bookkeeping knows that every earlier LDS read has completed;
-// the barrier is an opaque statement that no memory access moves across.
-template <int N>
-__device__ __forceinline__ void wait_vm_barrier() {
-    static_assert(N >= 0 && N < 64, "vmcnt is a 6-bit field");
-    __builtin_amdgcn_sched_barrier(0);  // SMFMACs written after the barrier stay after it
-    __builtin_amdgcn_s_waitcnt((N & 15) | ((N >> 4) << 14) | (7 << 4));  // vmcnt(N) expcnt(7) lgkmcnt(0)
-    asm volatile("s_barrier" ::: "memory");
-    __builtin_amdgcn_sched_barrier(0);
-}
-__device__ __forceinline__ void wait_vm_all() { asm volatile("s_waitcnt vmcnt(0)" ::: "memory"); }
-
-// Index words are read from LDS one dword per lane.  Such a read is served a half-wave
-// (32 lanes) at a time over 32 dword banks (measured with an LDS probe and the bank-conflict
-// counter), and the 32 lanes of a half-wave read one word from each of 32 consecutive rows.
-// A row of W index words (W a power of two, at most 32) therefore keeps logical word w at
-// w ^ iswz<W>(r), r counted from a multiple of 32: the 32 reads then hit 32 distinct banks.
-// Rows padded to a whole number of 16-byte pieces and swizzled by piece instead reach only
-// 8 banks (a 4-way conflict, 4x the read time).
-template <int W>
-__device__ __forceinline__ int iswz(int r) {
-    static_assert(W >= 1 && W <= 32 && (W & (W - 1)) == 0, "W a power of two up to 32");
-    return (r / (32 / W)) & (W - 1);
-}
-
 // A global_load_lds instruction costs about the same per 128-byte line it touches
 // whatever part of the line it uses (measured on the hardware), and a row's index
 // words for one stage fill only a few bytes of a line.  With IG > 1 the index
@@ -530,118 +366,6 @@ __device__ __forceinline__ void add_lowrank(const SpmmArgs& a, f32x16_t (&acc)[S
             for (int j = 0; j < ST; ++j)
                 acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8_t, bl[i]),
                                                                    __builtin_bit_cast(bf16x8_t, uu[j]), acc[i][j], 0, 0, 0);
-    }
-}
-
-// Words of the wave-private LDS buffer store_tile needs: SR sub-tiles x 64 lanes x 16
-// accumulators, each lane's 16 padded to 20 words (16-byte pieces of 16 consecutive lanes
-// then fall on distinct banks).
-template <int SR>
-constexpr int kStageWords = SR * 64 * 20;
-
-// Stores a wave's SR x ST accumulator tiles (rows from rw, tokens from tw).  A lane
-// holds token column l32 and rows 8*(e/4) + 4*h + e%4 of each 32x32 sub-tile.
-// bf16 tiles fully inside Y (inside) with 8-byte aligned rows are stored straight from
-// the accumulators, four consecutive rows per 8-byte store (measured as fast as staging
-// for them).  Everything else goes through a wave-private LDS buffer of kStageWords<SR>
-// words (stage, 16-byte aligned), since 4-byte outputs stored straight would scatter
-// every instruction over 32 token rows of Y: each 32-token column of sub-tiles is written
-// to LDS as whole accumulator vectors (stores of single extracted elements have been
-// miscompiled), read back as 4-row runs of one token (a lane's elements 4q..4q+3 are 4
-// consecutive rows), and stored as whole runs of Y's rows (32 lanes per token, 4
-// outputs per lane), scaled and converted on the way.  The caller has finished every
-// other use of the buffer.
-template <typename T, int SR, int ST>
-__device__ __forceinline__ void store_tile(const SpmmArgs& a, const typename Mma<T>::Acc (&acc)[SR][ST], int64_t rw,
-                                           int64_t tw, bool inside, uint32_t* stage, int lane) {
-    using AccV = typename Mma<T>::Acc;
-    using AccS = typename Mma<T>::AccS;
-    static_assert(SR == 4, "one token row of the wave's tile (4 sub-tiles) per half-wave");
-    const int h = lane >> 5, l32 = lane & 31;
-    if (inside && a.ydt == NM_BF16 && ((uintptr_t)a.Y % 8) == 0 && (a.ldy % 4) == 0) {
-#pragma unroll
-        for (int j = 0; j < ST; ++j) {
-            const int64_t tok = tw + j * 32 + l32;
-            const float sc = a.scaled ? __fmul_rn(a.w_scale, a.x_scale ? a.x_scale[tok] : 1.0f) : 1.0f;
-#pragma unroll
-            for (int i = 0; i < SR; ++i) {
-                uint16_t* yrow = (uint16_t*)a.Y + tok * a.ldy + rw + i * 32 + 4 * h;
-#pragma unroll
-                for (int g = 0; g < 4; ++g) {
-                    float f[4];
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        f[e] = (float)acc[i][j][4 * g + e];
-                        if (a.scaled) f[e] = __fmul_rn(sc, f[e]);
-                    }
-                    *(uint2*)(yrow + 8 * g) = make_uint2(f32_to_bf16_bits(f[0]) | (f32_to_bf16_bits(f[1]) << 16),
-                                                         f32_to_bf16_bits(f[2]) | (f32_to_bf16_bits(f[3]) << 16));
-                }
-            }
-        }
-        return;
-    }
-    const int es = a.ydt == NM_BF16 ? 2 : 4;
-    // 16-byte (4-byte outputs) or 8-byte (bf16) vector stores need aligned rows of Y
-    const bool vec = ((uintptr_t)a.Y % (4 * es)) == 0 && (a.ldy * es) % (4 * es) == 0;
-    // reader: lane l32 of a half-wave takes rows 4*l32 .. 4*l32+3 of the wave's 128, which
-    // are elements 4q .. 4q+3 of lane (token + 32 h') in sub-tile i
-    const int ri = l32 >> 3, rq = (l32 & 7) >> 1, rh = l32 & 1;
-#pragma unroll
-    for (int j = 0; j < ST; ++j) {
-#pragma unroll
-        for (int i = 0; i < SR; ++i) *(AccV*)&stage[(i * 64 + lane) * 20] = acc[i][j];
-        // lgkmcnt(0): this wave's LDS writes are done before any lane reads another's
-        __builtin_amdgcn_s_waitcnt(0xc07f);
-        __builtin_amdgcn_wave_barrier();
-        asm volatile("" ::: "memory");
-#pragma unroll 4
-        for (int p = 0; p < 16; ++p) {
-            const int tk = 2 * p + h;   // lanes 0-31 and 32-63 take two tokens per pass
-            const int64_t tok = tw + j * 32 + tk;
-            const uint4 raw = *(const uint4*)&stage[(ri * 64 + tk + 32 * rh) * 20 + 4 * rq];
-            const int64_t r = rw + 4 * l32;
-            if (tok >= a.Mtok || r >= a.R) continue;
-            const AccS v[4] = {__builtin_bit_cast(AccS, raw.x), __builtin_bit_cast(AccS, raw.y),
-                               __builtin_bit_cast(AccS, raw.z), __builtin_bit_cast(AccS, raw.w)};
-            const int64_t o = tok * a.ldy + r;
-            const bool full = vec && r + 3 < a.R;
-            if (a.ydt == NM_I32) {
-                if (full) {
-                    *(uint4*)((int32_t*)a.Y + o) = raw;
-                } else {
-                    for (int e = 0; e < 4 && r + e < a.R; ++e) ((int32_t*)a.Y)[o + e] = (int32_t)v[e];
-                }
-                continue;
-            }
-            float f[4];
-            if (a.scaled) {
-                const float sc = __fmul_rn(a.w_scale, a.x_scale ? a.x_scale[tok] : 1.0f);
-#pragma unroll
-                for (int e = 0; e < 4; ++e) f[e] = __fmul_rn(sc, (float)v[e]);
-            } else {
-#pragma unroll
-                for (int e = 0; e < 4; ++e) f[e] = (float)v[e];
-            }
-            if (a.ydt == NM_F32) {
-                if (full) {
-                    *(float4*)((float*)a.Y + o) = make_float4(f[0], f[1], f[2], f[3]);
-                } else {
-                    for (int e = 0; e < 4 && r + e < a.R; ++e) ((float*)a.Y)[o + e] = f[e];
-                }
-            } else {
-                if (full) {
-                    *(uint2*)((uint16_t*)a.Y + o) = make_uint2(f32_to_bf16_bits(f[0]) | (f32_to_bf16_bits(f[1]) << 16),
-                                                               f32_to_bf16_bits(f[2]) | (f32_to_bf16_bits(f[3]) << 16));
-                } else {
-                    for (int e = 0; e < 4 && r + e < a.R; ++e) ((uint16_t*)a.Y)[o + e] = (uint16_t)f32_to_bf16_bits(f[e]);
-                }
-            }
-        }
-        // the next column of sub-tiles overwrites the buffer only after every lane has read it
-        __builtin_amdgcn_s_waitcnt(0xc07f);
-        __builtin_amdgcn_wave_barrier();
-        asm volatile("" ::: "memory");
     }
 }
 
@@ -1276,68 +1000,6 @@ __device__ __forceinline__ Moments store_score_tile(const SpmmArgs& a, const f32
     return m;
 }
 
-// Gradient of packed 2:4 values: of the tile's columns k (rows rw .. of the accumulators) of
-// weight row r (the lane's token, from tw) only the kept positions are stored.  Elements
-// 4g .. 4g+3 of a lane's sub-tile are columns 32 i + 8 g + 4 h .. + 3, one group of 4, whose
-// two 2-bit positions are bits 4 (2 g + h) .. of the row's index word of those 32 columns.  A
-// lane's 8 kept values alternate in pairs with the other half-wave's; two swaps across the
-// halves leave each lane with the 8 consecutive values of 16 columns (K is a multiple of 16,
-// so all of them exist or none).
-template <int SR, int ST>
-__device__ __forceinline__ void store_grad_tile(const SpmmArgs& a, const f32x16_t (&acc)[SR][ST], int64_t rw,
-                                                int64_t tw, int lane) {
-    const int h = lane >> 5, l32 = lane & 31;
-#pragma unroll
-    for (int j = 0; j < ST; ++j) {
-        const int64_t q = tw + j * 32 + l32;   // stacked row
-        const int mat = q >= a.rowsp ? 1 : 0;
-        const int64_t r = q - mat * a.rowsp;
-        const bool row_ok = q < a.Mtok && r < a.prows;
-        const uint32_t* irow = (mat ? a.idx2 : a.idx) + (row_ok ? r : 0) * a.ldi;
-        uint8_t* orow = (uint8_t*)(mat ? a.Y2 : a.Y);
-#pragma unroll
-        for (int i = 0; i < SR; ++i) {
-            const int64_t k = rw + i * 32;
-            const uint32_t word = row_ok && k < a.R ? irow[k >> 5] : 0u;
-            float v0[4], v1[4];
-#pragma unroll
-            for (int g = 0; g < 4; ++g) {
-                const uint32_t b = (word >> (8 * g + 4 * h)) & 15u, p0 = b & 3u, p1 = b >> 2;
-                const float x0 = acc[i][j][4 * g], x1 = acc[i][j][4 * g + 1], x2 = acc[i][j][4 * g + 2],
-                            x3 = acc[i][j][4 * g + 3];
-                const float lo0 = p0 & 1u ? x1 : x0, hi0 = p0 & 1u ? x3 : x2;
-                const float lo1 = p1 & 1u ? x1 : x0, hi1 = p1 & 1u ? x3 : x2;
-                v0[g] = p0 & 2u ? hi0 : lo0;
-                v1[g] = p1 & 2u ? hi1 : lo1;
-            }
-            // lane half h: values of columns k + 16 h .. + 15
-            const int64_t kc = k + 16 * h;
-            const bool ok = row_ok && kc < a.R;
-            const int64_t o = r * a.ldy + kc / 2;
-            if (a.ydt == NM_BF16) {
-                uint32_t w[4];
-#pragma unroll
-                for (int g = 0; g < 4; ++g) w[g] = f32_to_bf16_bits(v0[g]) | (f32_to_bf16_bits(v1[g]) << 16);
-                const auto s0 = __builtin_amdgcn_permlane32_swap(w[0], w[2], false, false);
-                const auto s1 = __builtin_amdgcn_permlane32_swap(w[1], w[3], false, false);
-                if (ok) *(uint4*)((uint16_t*)orow + o) = make_uint4(s0[0], s0[1], s1[0], s1[1]);
-            } else {
-                uint32_t a0[4], a1[4];
-#pragma unroll
-                for (int g = 0; g < 4; ++g) a0[g] = __float_as_uint(v0[g]), a1[g] = __float_as_uint(v1[g]);
-                const auto s0 = __builtin_amdgcn_permlane32_swap(a0[0], a0[2], false, false);
-                const auto s1 = __builtin_amdgcn_permlane32_swap(a1[0], a1[2], false, false);
-                const auto s2 = __builtin_amdgcn_permlane32_swap(a0[1], a0[3], false, false);
-                const auto s3 = __builtin_amdgcn_permlane32_swap(a1[1], a1[3], false, false);
-                if (ok) {
-                    *(uint4*)((float*)orow + o) = make_uint4(s0[0], s1[0], s0[1], s1[1]);
-                    *(uint4*)((float*)orow + o + 4) = make_uint4(s2[0], s3[0], s2[1], s3[1]);
-                }
-            }
-        }
-    }
-}
-
 // ------------------------------------------------------------------ dense split ring (bf16)
 // Y = X W^T for a dense bf16 weight W [R, K] (ldv) with the split ring's tile, waves,
 // swizzles, DMA and epilogue, and dense MFMA (v_mfma_f32_32x32x16_bf16, whose operand and
@@ -1364,12 +1026,7 @@ __device__ __forceinline__ void store_grad_tile(const SpmmArgs& a, const f32x16_
 // for the A stages then measured the same as 2).
 // HUTCH_SCORE: HUTCH whose epilogue writes the score of D (store_score_tile) and the block's
 // moments of it instead of D.
-// GRADX: the plain product with its stages split over gridDim.y blocks (f32 partials,
-// summed by spmm_reduce_kernel).
-// GRADV: the gradient of packed 2:4 values: rows of the tile are columns k of the weight (A:
-// X transposed), tokens are rows r of the weight (B: dY transposed), and the epilogue writes
-// only the two kept positions of each group of 4 (store_grad_tile).
-// MODE: 0 plain, 1 HUTCH, 2 GEN, 3 HUTCH_SCORE, 4 GRADX, 5 GRADV.
+// MODE: 0 plain, 1 HUTCH, 2 GEN, 3 HUTCH_SCORE.
 template <int SR, int ST, int WRN, int WTN, int MODE = 0, int SK = 64, int NS = 2>
 __global__ __launch_bounds__(64 * WRN * WTN, 1) void dense_ring_kernel(SpmmArgs a) {
     constexpr bool HUTCH = MODE == 1 || MODE == 3, GEN = MODE == 2;
@@ -1391,16 +1048,14 @@ __global__ __launch_bounds__(64 * WRN * WTN, 1) void dense_ring_kernel(SpmmArgs 
     int tr, tt;
     tile_of(blockIdx.x, gridDim.x, a.tiles_r, a.tiles_t, tr, tt);
     const int64_t r0 = (int64_t)tr * BR, t0 = (int64_t)tt * BT;
-    // K / SK >= 1 (HUTCH: probes * stages per probe; GRADX: this split's, from s_begin)
-    const int s_begin = MODE == 4 ? (int)blockIdx.y * a.steps_per_split : 0;
-    const int nsteps = MODE == 4 && a.nsteps - s_begin > a.steps_per_split ? a.steps_per_split : a.nsteps - s_begin;
+    const int nsteps = a.nsteps;   // K / SK >= 1 (HUTCH: probes * stages per probe)
     const int PS = HUTCH ? a.pstages : nsteps;
     const uint32_t sbase = lds_addr(smem);
     // row / token r of CH chunks: logical chunk c at c ^ sw(r) (16 consecutive rows read by a
     // 16-byte LDS read then hit 64 distinct banks)
     auto sw = [](int r) { return CH == 8 ? ((r >> 1) & 7) : ((r >> 2) & 3); };
-    const void* baseW = uniform_ptr(a.vals + r0 * a.ldv * 2 + (int64_t)s_begin * ROWB);
-    const void* baseX = uniform_ptr(a.X + t0 * a.ldx * 2 + (int64_t)s_begin * ROWB);
+    const void* baseW = uniform_ptr(a.vals + r0 * a.ldv * 2);
+    const void* baseX = uniform_ptr(a.X + t0 * a.ldx * 2);
     const int64_t rmax = a.R - 1 - r0, tmax = a.Mtok - 1 - t0;
     uint32_t oW[NWL], oX[NXL];
     // GEN: half-wave h of a lane's B sub-tiles j = 0, 1 draws the Rademacher words of
@@ -1637,15 +1292,6 @@ __global__ __launch_bounds__(64 * WRN * WTN, 1) void dense_ring_kernel(SpmmArgs 
             __syncthreads();
         }
         if (tid < 3) a.mpart[(int64_t)tid * gridDim.x + blockIdx.x] = sh[tid * NT];
-    } else if constexpr (MODE == 5) {
-        store_grad_tile<SR, ST>(a, acc, r0 + wr * SR * 32, t0 + wt * ST * 32, lane);
-    } else if (MODE == 4 && a.part) {   // this split's partial tile into [split][Mtok][R]
-        SpmmArgs b = a;
-        b.Y = (float*)a.part + (int64_t)blockIdx.y * a.Mtok * a.R;
-        b.ydt = NM_F32;
-        b.ldy = a.R;
-        store_tile<uint16_t, SR, ST>(b, acc, r0 + wr * SR * 32, t0 + wt * ST * 32, false,
-                                     (uint32_t*)smem + wave * kStageWords<SR>, lane);
     } else {
         store_tile<uint16_t, SR, ST>(a, acc, r0 + wr * SR * 32, t0 + wt * ST * 32, r0 + BR <= a.R && t0 + BT <= a.Mtok,
                                      (uint32_t*)smem + wave * kStageWords<SR>, lane);
@@ -2340,18 +1986,6 @@ struct SpmmPlan {
 //           SIMD); bf16 index batches load 4 bytes per lane (16 do not split over 8 waves)
 #define NM_RING_NARROW T, 4, 2, 256, 2, 2, 2
 #define NM_RING_BIG T, 4, 2, 2, 4, 4
-
-// Compute units of the current device (cached per device).
-static int64_t device_cus() {
-    static int64_t cache[64] = {};
-    int dev = 0;
-    if (hipGetDevice(&dev) != hipSuccess || dev < 0 || dev >= 64) return 256;
-    if (cache[dev] == 0) {
-        int n = 0;
-        cache[dev] = (hipDeviceGetAttribute(&n, hipDeviceAttributeMultiprocessorCount, dev) == hipSuccess && n > 0) ? n : 256;
-    }
-    return cache[dev];
-}
 
 template <typename T>
 static SpmmPlan plan_for(int64_t Mtok, int64_t K, int64_t R, bool ring_ok, bool xres_ok = true) {
@@ -3326,87 +2960,6 @@ nm_status launch_glu(const GluIn& g, void* ws, hipStream_t s) {
     if (g.xdt == NM_I8) return run_glu<int8_t>(a, p, fused, PART, g, s);
     if (g.xdt == NM_FP8) return run_glu<fp8e4m3>(a, p, fused, PART, g, s);
     return run_glu<uint16_t>(a, p, fused, PART, g, s);
-}
-
-// ------------------------------------------------------------------ gradients
-// Splits of the summed dimension (Rn / 64 stages) of dX: the count whose rounds of blocks take
-// least, a stage of a 256 x 256 tile measured at about 0.9 us, and the partials written and
-// read back at about 4 TB/s with a launch of its own.
-static int grad_x_splits(int64_t M, int64_t K, int64_t Rn) {
-    const int64_t cus = device_cus(), tiles = ceil_div(K, 256) * ceil_div(M, 256), ns = Rn / kDenseSK;
-    int best = 1;
-    double best_us = 1e30;
-    for (int64_t ks = 1; ks <= 16 && ks * 4 <= ns + 3; ++ks) {
-        const double us = 0.9 * (double)(ceil_div(tiles * ks, cus) * (ceil_div(ns, ks) + 4)) +
-                          (ks > 1 ? 4.0 + 8e-6 / 4.0 * (double)(ks * M * K) : 0.0);
-        if (us < best_us) {
-            best_us = us;
-            best = (int)ks;
-        }
-    }
-    return best;
-}
-
-size_t grad_x_part_bytes(int64_t M, int64_t K, int64_t Rn) {
-    const int ks = grad_x_splits(M, K, Rn);
-    return ks > 1 ? (size_t)ks * (size_t)M * (size_t)K * 4 : 0;
-}
-
-nm_status launch_grad_x(const uint16_t* WT, int64_t Rn, const uint16_t* B, int64_t ldb, int64_t M, int64_t K, void* dX,
-                        nm_dtype dxdt, int64_t lddx, float* part, hipStream_t s) {
-    constexpr int SR = 4, ST = 2, WRN = 2, WTN = 4, BR = WRN * SR * 32, BT = WTN * ST * 32;
-    SpmmArgs a{};
-    a.vals = (const uint8_t*)WT;   // A: rows k of the transposed weight
-    a.ldv = Rn;
-    a.X = (const uint8_t*)B;       // B: token rows of dY
-    a.ldx = ldb;
-    a.Y = dX;
-    a.ydt = (int)dxdt;
-    a.ldy = lddx;
-    a.Mtok = M;
-    a.R = K;
-    a.K = Rn;
-    a.nsteps = (int)(Rn / kDenseSK);
-    a.steps_per_split = (int)ceil_div(a.nsteps, grad_x_splits(M, K, Rn));
-    a.KS = (int)ceil_div(a.nsteps, a.steps_per_split);
-    a.part = a.KS > 1 ? part : nullptr;
-    a.tiles_r = (int)ceil_div(K, BR);
-    a.tiles_t = (int)ceil_div(M, BT);
-    hipLaunchKernelGGL((dense_ring_kernel<SR, ST, WRN, WTN, 4, kDenseSK, kDenseNS>),
-                       dim3((unsigned)(a.tiles_r * a.tiles_t), (unsigned)a.KS), dim3(64 * WRN * WTN), 0, s, a);
-    if (a.KS > 1) {
-        const dim3 g(grid_cap(ceil_div(M * K, 256), 8192));
-        hipLaunchKernelGGL(spmm_reduce_kernel<float>, g, dim3(256), 0, s, a);
-    }
-    return check_launch("gradient of the activations");
-}
-
-nm_status launch_grad_v(const uint16_t* XT, const uint16_t* DT, int64_t Mp, const GradIn& in, const GradOut& out,
-                        int nmat, int64_t Rp, hipStream_t s) {
-    constexpr int SR = 4, ST = 2, WRN = 2, WTN = 4, BR = WRN * SR * 32, BT = WTN * ST * 32;
-    SpmmArgs a{};
-    a.vals = (const uint8_t*)XT;   // A: columns k of the weight
-    a.ldv = Mp;
-    a.X = (const uint8_t*)DT;      // B: stacked rows r of the weights
-    a.ldx = Mp;
-    a.Y = out.dV[0];
-    a.Y2 = out.dV[1];
-    a.ydt = (int)out.dvdt;
-    a.ldy = out.lddv;
-    a.idx = in.idx[0];
-    a.idx2 = in.idx[1];
-    a.ldi = in.ldi;
-    a.Mtok = nmat * Rp;
-    a.rowsp = Rp;
-    a.prows = in.R;
-    a.R = in.K;
-    a.K = Mp;
-    a.nsteps = (int)(Mp / kDenseSK);
-    a.tiles_r = (int)ceil_div(in.K, BR);
-    a.tiles_t = (int)ceil_div(a.Mtok, BT);
-    hipLaunchKernelGGL((dense_ring_kernel<SR, ST, WRN, WTN, 5, kDenseSK, kDenseNS>),
-                       dim3((unsigned)(a.tiles_r * a.tiles_t)), dim3(64 * WRN * WTN), 0, s, a);
-    return check_launch("gradient of the packed values");
 }
 
 }  // namespace nm

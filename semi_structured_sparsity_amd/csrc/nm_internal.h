@@ -349,14 +349,6 @@ struct GradOut {
 size_t grad_ws(int64_t M, int64_t K, int64_t R, int nmat);
 // nmat: 1, or 2 for the gated block
 nm_status launch_grad(const GradIn& in, const GradOut& out, int nmat, void* ws, hipStream_t s);
-// dX [M, K] = B [M, Rn] (ldb) WT^T, WT [K, Rn]: the dense split ring, Rn (a multiple of 64) split over
-// blocks where the tiles leave the CUs short (f32 partials in part, grad_x_part_bytes)
-size_t grad_x_part_bytes(int64_t M, int64_t K, int64_t Rn);
-nm_status launch_grad_x(const uint16_t* WT, int64_t Rn, const uint16_t* B, int64_t ldb, int64_t M, int64_t K, void* dX,
-                        nm_dtype dxdt, int64_t lddx, float* part, hipStream_t s);
-// dV of nmat weights: XT [K, Mp], DT [nmat * Rp, Mp], the kept positions of DT XT^T
-nm_status launch_grad_v(const uint16_t* XT, const uint16_t* DT, int64_t Mp, const GradIn& in, const GradOut& out,
-                        int nmat, int64_t Rp, hipStream_t s);
 // optimiser
 nm_status launch_adamw(const nm_adamw_tensor* ts, int count, nm_dtype sdt, double lr, double beta1, double beta2,
                        double eps, int64_t step, const float* grad_scale, hipStream_t s);
