@@ -58,6 +58,18 @@ __device__ __forceinline__ uint4 pack8(const uint32_t (&x)[8]) {
     return make_uint4(x[0] | (x[1] << 16), x[2] | (x[3] << 16), x[4] | (x[5] << 16), x[6] | (x[7] << 16));
 }
 
+// 16 columns of a packed 2:4 row from their 8 values and 16 bits of positions
+__device__ __forceinline__ void decode16(uint4 v, uint32_t b, uint32_t (&x)[16]) {
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+        const uint32_t v0 = w[q] & 0xffffu, v1 = w[q] >> 16;
+        const uint32_t p0 = (b >> (4 * q)) & 3u, p1 = (b >> (4 * q + 2)) & 3u;
+#pragma unroll
+        for (uint32_t e = 0; e < 4; ++e) x[4 * q + e] = (p0 == e ? v0 : 0u) | (p1 == e ? v1 : 0u);
+    }
+}
+
 struct LayoutArgs {
     GradIn in;
     int64_t Rp, Mp, Rn;
@@ -152,14 +164,7 @@ __device__ __forceinline__ void decode_tile(PairTile& tile, const LayoutArgs& a,
         const bool ok = r < in.R && k < in.K;
         const uint4 v = ok ? *(const uint4*)(in.vals[mat] + r * in.ldv + k / 2) : make_uint4(0, 0, 0, 0);
         const uint32_t b = ok ? in.idx[mat][r * in.ldi + k / 32] >> (16 * (c & 1)) : 0u;
-        const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-        for (int q = 0; q < 4; ++q) {
-            const uint32_t v0 = w[q] & 0xffffu, v1 = w[q] >> 16;
-            const uint32_t p0 = (b >> (4 * q)) & 3u, p1 = (b >> (4 * q + 2)) & 3u;
-#pragma unroll
-            for (uint32_t e = 0; e < 4; ++e) x[j][4 * q + e] = (p0 == e ? v0 : 0u) | (p1 == e ? v1 : 0u);
-        }
+        decode16(v, b, x[j]);
     }
 #pragma unroll
     for (int e = 0; e < 16; ++e) tile.put(c * 16 + e, pair, x[0][e], x[1][e]);
@@ -221,9 +226,26 @@ struct GradArgs {
 // lane's 8 kept values alternate in pairs with the other half-wave's; two swaps across the
 // halves leave each lane with the 8 consecutive values of 16 columns (K is a multiple of 16,
 // so all of them exist or none).
+// The positions are loaded before the products (grad_positions), so that no load is waited for here.
 template <int SR, int ST>
-__device__ __forceinline__ void store_grad_tile(const GradArgs& a, const f32x16_t (&acc)[SR][ST], int64_t rw,
-                                                int64_t tw, int lane) {
+__device__ __forceinline__ void grad_positions(const GradArgs& a, int64_t rw, int64_t tw, int lane, uint32_t (&word)[ST][SR]) {
+#pragma unroll
+    for (int j = 0; j < ST; ++j) {
+        const int64_t q = tw + j * 32 + (lane & 31);   // stacked row
+        const int mat = q >= a.Rp ? 1 : 0;
+        const int64_t r = q - mat * a.Rp;
+        const bool row_ok = q < a.v.rowsB && r < a.R;
+        const uint32_t* irow = (mat ? a.idx[1] : a.idx[0]) + (row_ok ? r : 0) * a.ldi;
+#pragma unroll
+        for (int i = 0; i < SR; ++i) {
+            const int64_t k = rw + i * 32;
+            word[j][i] = row_ok && k < a.v.rowsA ? irow[k >> 5] : 0u;
+        }
+    }
+}
+template <int SR, int ST>
+__device__ __forceinline__ void store_grad_tile(const GradArgs& a, const f32x16_t (&acc)[SR][ST],
+                                                const uint32_t (&words)[ST][SR], int64_t rw, int64_t tw, int lane) {
     const int64_t K = a.v.rowsA;
     const int h = lane >> 5, l32 = lane & 31;
 #pragma unroll
@@ -232,12 +254,11 @@ __device__ __forceinline__ void store_grad_tile(const GradArgs& a, const f32x16_
         const int mat = q >= a.Rp ? 1 : 0;
         const int64_t r = q - mat * a.Rp;
         const bool row_ok = q < a.v.rowsB && r < a.R;
-        const uint32_t* irow = (mat ? a.idx[1] : a.idx[0]) + (row_ok ? r : 0) * a.ldi;
         uint8_t* orow = (uint8_t*)(mat ? a.dV[1] : a.dV[0]);
 #pragma unroll
         for (int i = 0; i < SR; ++i) {
             const int64_t k = rw + i * 32;
-            const uint32_t word = row_ok && k < K ? irow[k >> 5] : 0u;
+            const uint32_t word = words[j][i];
             float v0[4], v1[4];
 #pragma unroll
             for (int g = 0; g < 4; ++g) {
@@ -372,6 +393,8 @@ __global__ __launch_bounds__(512, 1) void grad_ring_kernel(GradArgs g) {
         __builtin_amdgcn_sched_group_barrier(0x008, SR * ST - SR - ST, 0);
         __builtin_amdgcn_sched_barrier(0);
     };
+    uint32_t words[ST][SR] = {};
+    if (!isx) grad_positions<SR, ST>(g, a0 + wr * SR * 32, b0 + wt * ST * 32, lane, words);
     Frag fr[2];
     issue(0);
     if (nsteps > 1) issue(1);
@@ -396,7 +419,7 @@ __global__ __launch_bounds__(512, 1) void grad_ring_kernel(GradArgs g) {
     }
     wait_vm_all();
     if (!isx) {
-        store_grad_tile<SR, ST>(g, acc, a0 + wr * SR * 32, b0 + wt * ST * 32, lane);
+        store_grad_tile<SR, ST>(g, acc, words, a0 + wr * SR * 32, b0 + wt * ST * 32, lane);
         return;
     }
     __syncthreads();   // every wave has read the ring: its LDS stages the output
@@ -408,6 +431,177 @@ __global__ __launch_bounds__(512, 1) void grad_ring_kernel(GradArgs g) {
     a.ldy = g.part ? a.R : g.lddx;
     store_tile<uint16_t, SR, ST>(a, acc, a0 + wr * SR * 32, b0 + wt * ST * 32, a0 + T <= a.R && b0 + T <= a.Mtok,
                                  (uint32_t*)smem + wave * kStageWords<SR>, lane);
+}
+
+// ------------------------------------------------------------------ few tokens
+// Up to 64 tokens the dense ring pays for 256-token tiles and for a dense copy of the weights;
+// both products are then streams: dX reads the packed weights, dV writes its packed
+// values.  One grid holds both.
+// dX: a block sums dY W over a run of weight rows for 128 columns and all tokens (ST
+// sub-tiles of 32).  64 rows a step: values (a line per row), positions and the tokens' 64
+// columns of D are loaded PF steps ahead into registers (three blocks a CU then keep about
+// 100 KB in flight, which a CU's share of the HBM rate needs), the weight is decoded into LDS
+// as t[column][row pair] (36 words a column, and 8 more every 16 columns: writes and 16-byte
+// fragment reads free of bank conflicts), and multiplied with v_mfma_f32_32x32x16_bf16;
+// wave w takes columns 32 w .. + 31.  LDS is double buffered, one barrier a step.  Partials
+// [split][M][K] in f32 are added by grad_reduce_kernel.  Blocks of one split and all panels
+// run on one XCD, whose L2 then serves the positions' lines (8 panels each) once.
+// dV: 128 x 128 tiles, four waves of 64 x 64; the tile's 64 tokens (a line per row of XT and
+// of DT) are loaded whole into LDS, the epilogue is the ring's.
+struct FewArgs {
+    GradArgs g;
+    GradIn in;
+    int64_t M, K, Rn;
+    const uint16_t* D;
+    int64_t ldd;
+    int panels, splits, spp;   // 128-column panels of dX, splits of its Rn / 64 steps, steps per split
+    int tk, tr;                // 128-wide tiles of dV along K and along the stacked rows
+};
+constexpr int kFewCol = 36, kFewWords = 128 * kFewCol + 8 * 8;   // a decoded step
+constexpr int64_t kFewTokens = 64;                               // dV's tiles hold all tokens: Mp == 64
+
+template <int ST>
+__global__ __launch_bounds__(256, 3) void grad_few_kernel(FewArgs a) {
+    constexpr int PF = 4, DBYTES = 32 * ST * 128, LDS = 2 * (kFewWords * 4 + DBYTES);
+    static_assert(LDS >= 32 * 1024, "dV's tile fits");
+    __shared__ __attribute__((aligned(1024))) uint8_t smem[LDS];
+    const int tid = threadIdx.x, lane = tid & 63, h = lane >> 5, l32 = lane & 31;
+    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    auto sw = [](int r) { return (r >> 1) & 7; };   // 128-byte row r: logical 16-byte chunk c at c ^ sw(r)
+    if ((int)blockIdx.x >= a.g.nx) {   // dV
+        // an XCD walks whole row panels (nx is a multiple of 8)
+        const int b = blockIdx.x - a.g.nx, loc = b >> 3, tr = (loc / a.tk) * 8 + (b & 7);
+        if (tr >= a.tr) return;
+        const int64_t k0 = (int64_t)(loc % a.tk) * 128, q0 = (int64_t)tr * 128;
+        const void *baseA = uniform_ptr(a.g.v.A + k0 * 64), *baseB = uniform_ptr(a.g.v.B + q0 * 64);
+        const int64_t kmax = a.K - 1 - k0, qmax = a.Rn - 1 - q0;
+        const uint32_t sbase = lds_addr(smem);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int row = (wave * 4 + i) * 8 + (lane >> 3);
+            const uint32_t c = (uint32_t)(((lane & 7) ^ sw(row)) * 16);
+            dma16s(sbase + (wave * 4 + i) * 1024, baseA, (uint32_t)(row < kmax ? row : kmax) * 128u + c);
+            dma16s(sbase + 16384 + (wave * 4 + i) * 1024, baseB, (uint32_t)(row < qmax ? row : qmax) * 128u + c);
+        }
+        uint32_t words[2][2];
+        grad_positions<2, 2>(a.g, k0 + (wave & 1) * 64, q0 + (wave >> 1) * 64, lane, words);
+        f32x16_t acc[2][2];
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+#pragma unroll
+            for (int j = 0; j < 2; ++j) acc[i][j] = f32x16_t{};
+        wait_vm_barrier<0>();
+        const int ra = (wave & 1) * 64 + l32, rb = (wave >> 1) * 64 + l32;
+#pragma unroll
+        for (int d = 0; d < 4; ++d) {
+            i32x4_t fa[2], fb[2];
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                fa[i] = *(const i32x4_t*)(smem + (ra + 32 * i) * 128 + ((2 * d + h) ^ sw(ra + 32 * i)) * 16);
+                fb[i] = *(const i32x4_t*)(smem + 16384 + (rb + 32 * i) * 128 + ((2 * d + h) ^ sw(rb + 32 * i)) * 16);
+            }
+#pragma unroll
+            for (int i = 0; i < 2; ++i)
+#pragma unroll
+                for (int j = 0; j < 2; ++j)
+                    acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8_t, fa[i]),
+                                                                         __builtin_bit_cast(bf16x8_t, fb[j]), acc[i][j], 0, 0, 0);
+        }
+        store_grad_tile<2, 2>(a.g, acc, words, k0 + (wave & 1) * 64, q0 + (wave >> 1) * 64, lane);
+        return;
+    }
+    // dX: split 8 u + x of XCD x = b % 8, panels side by side
+    const int loc = blockIdx.x >> 3, panel = loc % a.panels, split = (loc / a.panels) * 8 + (blockIdx.x & 7);
+    if (split >= a.splits) return;
+    const int64_t k0 = (int64_t)panel * 128;
+    const int nstep = (int)(a.Rn / 64), s0 = split * a.spp, s1 = s0 + a.spp < nstep ? s0 + a.spp : nstep;
+    const int c = tid & 7, pair = tid >> 3;
+    const int64_t kc = k0 + 16 * c;
+    const int64_t Rp = a.g.Rp;
+    i32x4_t pv[PF][2], pd[PF][ST];   // values, positions and D of the steps ahead
+    uint32_t pi[PF][2];
+    // the tokens' rows of D: rows past M read the last one (their sums are not stored)
+    const uint16_t* dp[ST];
+#pragma unroll
+    for (int j = 0; j < ST; ++j) {
+        const int64_t m = 32 * j + (tid >> 3);
+        dp[j] = a.D + (m < a.M ? m : a.M - 1) * a.ldd + 8 * c;
+    }
+    // steps past the last reload it (never used); rows past R and columns past K read row 0 or
+    // column 0 and are zeroed at the decode
+    const bool kok = kc < a.K;
+    auto load = [&](int s, i32x4_t (&v)[2], uint32_t (&ix)[2], i32x4_t (&d)[ST]) __attribute__((always_inline)) {
+        const int64_t q0 = (int64_t)(s < s1 ? s : s1 - 1) * 64;
+        const int mat = q0 >= Rp ? 1 : 0;   // Rp is a multiple of 64: a step is of one weight
+        const uint16_t* vals = mat ? a.in.vals[1] : a.in.vals[0];
+        const uint32_t* idx = mat ? a.in.idx[1] : a.in.idx[0];
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+            const int64_t q = q0 - mat * Rp + 2 * pair + j, r = q < a.in.R ? q : 0, k = kok ? kc : 0;
+            v[j] = *(const i32x4_t*)(vals + r * a.in.ldv + k / 2);
+            ix[j] = idx[r * a.in.ldi + k / 32];
+        }
+#pragma unroll
+        for (int j = 0; j < ST; ++j) d[j] = *(const i32x4_t*)(dp[j] + q0);
+    };
+    f32x16_t acc[ST];
+#pragma unroll
+    for (int j = 0; j < ST; ++j) acc[j] = f32x16_t{};
+#pragma unroll
+    for (int u = 0; u < PF; ++u) load(s0 + u, pv[u], pi[u], pd[u]);
+    for (int sb = s0; sb < s1; sb += PF) {
+#pragma unroll
+        for (int u = 0; u < PF; ++u) {
+            const int s = sb + u;
+            if (s < s1) {   // the same for the whole block
+                uint8_t* const buf = smem + (u & 1) * (kFewWords * 4 + DBYTES);
+                uint8_t* const dbuf = buf + kFewWords * 4;
+                const int64_t q = (int64_t)s * 64 - (s * 64 >= Rp ? Rp : 0) + 2 * pair;
+                uint32_t x[2][16];
+#pragma unroll
+                for (int j = 0; j < 2; ++j) {
+                    const i32x4_t z = kok && q + j < a.in.R ? pv[u][j] : i32x4_t{0, 0, 0, 0};
+                    decode16(__builtin_bit_cast(uint4, z), pi[u][j] >> (16 * (c & 1)), x[j]);
+                }
+                uint32_t* w = (uint32_t*)buf + c * (16 * kFewCol + 8) + pair;
+#pragma unroll
+                for (int e = 0; e < 16; ++e) w[e * kFewCol] = x[0][e] | (x[1][e] << 16);
+#pragma unroll
+                for (int j = 0; j < ST; ++j) {
+                    const int m = 32 * j + (tid >> 3);
+                    *(i32x4_t*)(dbuf + m * 128 + (c ^ sw(m)) * 16) = pd[u][j];
+                }
+                load(s + PF, pv[u], pi[u], pd[u]);
+                __syncthreads();   // the buffer was last read two steps ago, before the last step's barrier
+                const int col = 32 * wave + l32;
+                const uint32_t* row = (const uint32_t*)buf + col * kFewCol + 8 * (col >> 4) + 4 * h;
+#pragma unroll
+                for (int d = 0; d < 4; ++d) {
+                    const i32x4_t fa = *(const i32x4_t*)(row + 8 * d);
+#pragma unroll
+                    for (int j = 0; j < ST; ++j) {
+                        const int m = 32 * j + l32;
+                        const i32x4_t fb = *(const i32x4_t*)(dbuf + m * 128 + ((2 * d + h) ^ sw(m)) * 16);
+                        acc[j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8_t, fa),
+                                                                          __builtin_bit_cast(bf16x8_t, fb), acc[j], 0, 0, 0);
+                    }
+                }
+            }
+        }
+    }
+    // a lane: token 32 j + l32, columns 8 g + 4 h .. + 3 of the wave's 32
+    float* part = a.g.part + (int64_t)split * a.M * a.K;
+#pragma unroll
+    for (int j = 0; j < ST; ++j) {
+        const int64_t m = 32 * j + l32;
+        if (m >= a.M) continue;
+#pragma unroll
+        for (int g = 0; g < 4; ++g) {
+            const int64_t k = k0 + 32 * wave + 8 * g + 4 * h;
+            if (k < a.K)
+                *(float4*)(part + m * a.K + k) = make_float4(acc[j][4 * g], acc[j][4 * g + 1], acc[j][4 * g + 2], acc[j][4 * g + 3]);
+        }
+    }
 }
 
 // dX from its split partials, in split order
@@ -457,6 +651,17 @@ static size_t grad_x_part_bytes(int64_t M, int64_t K, int64_t Rn) {
 static int64_t up64(int64_t n) { return (n + 63) & ~(int64_t)63; }
 static size_t up256(size_t n) { return (n + 255) & ~(size_t)255; }
 
+// Splits of the few-token dX: about three blocks a CU, in eights (one per XCD).
+static bool few_tokens(int64_t M) { return M <= kFewTokens; }
+static int few_splits(int64_t K, int64_t Rn, int* spp) {
+    const int64_t steps = Rn / 64, panels = ceil_div(K, 128);
+    int64_t n = ceil_div(3 * device_cus(), panels * 8) * 8;
+    // at least the steps loaded ahead per split: more splits of a small weight are all partials
+    if (n > steps / 4) n = steps / 4 > 1 ? steps / 4 : 1;
+    *spp = (int)ceil_div(steps, n);
+    return (int)ceil_div(steps, *spp);
+}
+
 // Workspace of one backward call, in the order it is carved.
 struct GradWs {
     size_t d = 0, dt = 0, xt = 0, wt = 0, part = 0;
@@ -469,6 +674,11 @@ static GradWs grad_ws_layout(int64_t M, int64_t K, int64_t R, int nmat) {
     w.d = up256((size_t)(M * Rn * 2));
     w.dt = up256((size_t)(Rn * Mp * 2));
     w.xt = up256((size_t)(K * Mp * 2));
+    if (few_tokens(M)) {
+        int spp;
+        w.part = up256((size_t)few_splits(K, Rn, &spp) * (size_t)(M * K) * 4);
+        return w;
+    }
     w.wt = up256((size_t)(K * Rn * 2));
     w.part = up256(grad_x_part_bytes(M, K, Rn));
     return w;
@@ -524,9 +734,10 @@ nm_status launch_grad(const GradIn& in, const GradOut& out, int nmat, void* ws, 
     l.tw = (int)ceil_div(in.K, 128);
     l.tx = (int)ceil_div(in.K, 64);
     l.nd = l.D || l.DT ? l.td * (int)(Mp / 64) : 0;
-    l.nw = dx ? l.tw * (int)(Rp / 64) * nmat : 0;
+    l.nw = dx && !few_tokens(in.M) ? l.tw * (int)(Rp / 64) * nmat : 0;
     l.nx = dv ? l.tx * (int)(Mp / 64) : 0;
     const dim3 gl((unsigned)(l.nd + l.nw + l.nx));
+    if (gl.x) {
 #define NM_LAYOUT(A)                                                                                  \
     do {                                                                                              \
         if (vec) hipLaunchKernelGGL((grad_layout_kernel<A, true>), gl, dim3(256), 0, s, l);           \
@@ -537,6 +748,7 @@ nm_status launch_grad(const GradIn& in, const GradOut& out, int nmat, void* ws, 
     else if (in.act == NM_ACT_GELU) NM_LAYOUT(NM_ACT_GELU);
     else if (in.act == NM_ACT_GELU_TANH) NM_LAYOUT(NM_ACT_GELU_TANH);
     else NM_LAYOUT(NM_ACT_RELU2);
+    }
 #undef NM_LAYOUT
     GradArgs g{};
     int nv = 0, splits = 1;
@@ -582,7 +794,30 @@ nm_status launch_grad(const GradIn& in, const GradOut& out, int nmat, void* ws, 
         g.Rp = Rp;
         g.dvf32 = out.dvdt == NM_F32;
     }
-    hipLaunchKernelGGL(grad_ring_kernel, dim3((unsigned)(g.nx + nv)), dim3(512), 0, s, g);
+    if (few_tokens(in.M)) {
+        FewArgs f{};
+        f.in = in;
+        f.M = in.M;
+        f.K = in.K;
+        f.Rn = Rn;
+        f.D = B;
+        f.ldd = ldb;
+        f.tk = (int)ceil_div(in.K, 128);
+        f.tr = (int)ceil_div(Rn, 128);
+        g.Rp = Rp;
+        if (dx) {
+            f.panels = (int)ceil_div(in.K, 128);
+            f.splits = splits = few_splits(in.K, Rn, &f.spp);
+            g.nx = (int)ceil_div(splits, 8) * 8 * f.panels;
+            g.part = PART;
+        }
+        f.g = g;
+        const dim3 gf((unsigned)(g.nx + (dv ? f.tk * (int)ceil_div(f.tr, 8) * 8 : 0)));
+        if (in.M <= 32) hipLaunchKernelGGL(grad_few_kernel<1>, gf, dim3(256), 0, s, f);
+        else hipLaunchKernelGGL(grad_few_kernel<2>, gf, dim3(256), 0, s, f);
+    } else {
+        hipLaunchKernelGGL(grad_ring_kernel, dim3((unsigned)(g.nx + nv)), dim3(512), 0, s, g);
+    }
     if (g.part)
         hipLaunchKernelGGL(grad_reduce_kernel, dim3(grid_cap(ceil_div(in.M * in.K, 256), 8192)), dim3(256), 0, s, PART,
                            splits, in.M, in.K, out.dX, out.lddx, g.dxf32);
