@@ -2681,7 +2681,7 @@ constexpr int kGluX = 16 * 1024;
 
 // The fused kernels by token count, as for the plain product with R features in place of
 // rows and half as many of them per tile:
-//   kind 1: K-split ring, 32 features x 32 / 64 / 128 tokens (up to 256 tokens)
+//   kind 1: K-split ring, 32 features x 32 or 64 tokens (up to 64 tokens, 128 of one-byte codes)
 //   kind 2: ring tiles of 128 features x 128 tokens (narrow) or x 256 tokens (big), or big ones
 //           on the first features and narrow ones on the rest
 //   kind 0: none applies (K off the stage grid, unaligned index rows): two plain products
@@ -2709,8 +2709,10 @@ static GluPlan plan_glu(int64_t Mtok, int64_t K, int64_t R, bool ring_ok, bool l
                 p.mid = m;
                 break;
             }
-        if (sizeof(T) == 2 && p.mid == 4 && !lift) {
-            // as for the plain product: 256-row tiles read a quarter of the X per weight byte
+        if (p.mid == 4 && !lift && (sizeof(T) == 2 || Mtok > 128)) {
+            // 256-row tiles read a quarter of the X per weight byte, their stages split over blocks:
+            // 11008 x 4096 bf16 at 128 tokens 57.0 -> 51.7 us, at 256 82.5 -> 68.5; int8 at 256
+            // 52.1 -> 43.6, but at 128 (half as many stages) 34.9 against 36.4
             const int64_t tiles = ceil_div(R, RN::BR / 2) * ceil_div(Mtok, RN::BT);
             int64_t ks = cus / tiles;
             if (ks > p.nsteps / 2) ks = p.nsteps / 2;
@@ -2723,6 +2725,7 @@ static GluPlan plan_glu(int64_t Mtok, int64_t K, int64_t R, bool ring_ok, bool l
             p.KS = (int)ceil_div(p.nsteps, p.steps_per_split);
             return p;
         }
+        if (p.mid == 4) p.mid = 2;   // 64-token tiles leave room for two blocks (int8, 128 tokens: 34.9 -> 32.2 us)
         p.tiles_r = (int)rt;
         p.tiles_t = (int)ceil_div(Mtok, 32 * p.mid);
         // more tiles than CUs: equal tiles that fill whole rounds (the rows a tile does not use re-read
@@ -2800,13 +2803,10 @@ static nm_status run_glu(SpmmArgs a, const GluPlan& p, bool lift, void* part, co
         if (lift) {
             if (p.xres) NM_GLUK(1, 5, true, kGluX, 2);
             else if (p.mid == 1) NM_GLUK(1, 3, true, 0, 2);
-            else if (p.mid == 2) NM_GLUK(2, 2, true, 0, 2);
-            else if constexpr (sizeof(T) == 2) NM_GLUK(4, 3, true, 0, 1);
-            else return set_error(NM_ERR_DEVICE, "nm_spmm_glu: no in-kernel lift for one-byte codes on 128-token tiles");
+            else NM_GLUK(2, 2, true, 0, 2);
         } else if (p.xres) NM_GLUK(1, 5, false, kGluX, 2);
         else if (p.mid == 1) NM_GLUK(1, 3, false, 0, 2);
-        else if (p.mid == 2) NM_GLUK(2, 2, false, 0, 2);
-        else NM_GLUK(4, 3, false, 0, 1);
+        else NM_GLUK(2, 2, false, 0, 2);
 #undef NM_GLUK
     } else {
         auto launch = [&](bool big, int64_t f_begin, int64_t f_end) {
@@ -2854,16 +2854,17 @@ static size_t glu_plain_ws(int64_t Mtok, int64_t K, int64_t R, int Ns, nm_dtype 
     return round256((size_t)(2 * c * R * 4)) + w;
 }
 
-// The fused form's lift: inside the K-split ring (6:8, up to 64 tokens of one-byte codes)
+// The lift runs inside the K-split ring for 6:8 up to 64 tokens.  Beyond, the fragments' gather
+// costs more than lifting first (11008 x 4096 bf16 at 128 tokens: 115 against 71 us).
 static GluPlan glu_plan(int64_t Mtok, int64_t K, int64_t R, int Ns, nm_dtype xdt, bool ring_ok, bool* fused) {
     const int64_t Kl = lifted_cols(K, Ns);
     auto plan = [&](bool lift) {
         return xdt == NM_BF16 ? plan_glu<uint16_t>(Mtok, Kl, R, ring_ok, lift) : plan_glu<int8_t>(Mtok, Kl, R, ring_ok, lift);
     };
     *fused = false;
-    if (Ns == 4) {
+    if (Ns == 4 && Mtok <= 64) {
         const GluPlan p = plan(true);
-        if (p.kind == 1 && (xdt == NM_BF16 || p.mid <= 2)) {
+        if (p.kind == 1) {
             *fused = true;
             return p;
         }
