@@ -277,7 +277,7 @@ __device__ __forceinline__ void store_grad_tile(const GradArgs& a, const f32x16_
             if (!a.dvf32) {
                 uint32_t w[4];
 #pragma unroll
-                for (int g = 0; g < 4; ++g) w[g] = f32_to_bf16_bits(v0[g]) | (f32_to_bf16_bits(v1[g]) << 16);
+                for (int g = 0; g < 4; ++g) w[g] = f32_to_bf16_pair(v0[g], v1[g]);
                 const auto s0 = __builtin_amdgcn_permlane32_swap(w[0], w[2], false, false);
                 const auto s1 = __builtin_amdgcn_permlane32_swap(w[1], w[3], false, false);
                 if (ok) *(uint4*)((uint16_t*)orow + o) = make_uint4(s0[0], s0[1], s1[0], s1[1]);

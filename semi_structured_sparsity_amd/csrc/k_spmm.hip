@@ -390,8 +390,7 @@ __device__ __forceinline__ void put4(void* p, bool f32, int64_t o, const float (
             for (int e = 0; e < n; ++e) q[e] = f[e];
     } else {
         uint16_t* q = (uint16_t*)p + o;
-        if (vec) *(uint2*)q = make_uint2(f32_to_bf16_bits(f[0]) | (f32_to_bf16_bits(f[1]) << 16),
-                                         f32_to_bf16_bits(f[2]) | (f32_to_bf16_bits(f[3]) << 16));
+        if (vec) *(uint2*)q = make_uint2(f32_to_bf16_pair(f[0], f[1]), f32_to_bf16_pair(f[2], f[3]));
         else
             for (int e = 0; e < n; ++e) q[e] = (uint16_t)f32_to_bf16_bits(f[e]);
     }

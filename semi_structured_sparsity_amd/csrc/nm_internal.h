@@ -25,6 +25,14 @@ __device__ __forceinline__ uint32_t f32_to_bf16_bits(float f) {
     return (u + 0x7fffu + ((u >> 16) & 1u)) >> 16;
 }
 
+// Two floats rounded to nearest even, packed (lo in the low half), by the conversion
+// instruction: the same bits as f32_to_bf16_bits for everything but NaN payloads.
+__device__ __forceinline__ uint32_t f32_to_bf16_pair(float lo, float hi) {
+    typedef __bf16 bf16x2_t __attribute__((ext_vector_type(2)));
+    typedef float f32x2_t __attribute__((ext_vector_type(2)));
+    return __builtin_bit_cast(uint32_t, __builtin_convertvector(f32x2_t{lo, hi}, bf16x2_t));
+}
+
 // Rank key of a score for top-N selection: NaN ranks below everything and
 // -0 compares equal to +0 (x + 0 maps -0 to +0).
 // sum over z < n of p[z * stride], added in z order starting from 0 (the order of a plain
