@@ -29,7 +29,7 @@ namespace nm {
 struct PairTile {
     uint32_t t[128][33];
     __device__ static int at(int col, int pair) { return pair ^ (((col >> 6) & 1) * 8); }
-    __device__ __forceinline__ void put(int col, int pair, uint32_t lo, uint32_t hi) { t[col][at(col, pair)] = lo | (hi << 16); }
+    __device__ __forceinline__ void put(int col, int pair, uint32_t w) { t[col][at(col, pair)] = w; }
     // rows 8 q .. 8 q + 7 of a column, 16 bytes
     __device__ __forceinline__ uint4 get(int col, int q) const {
         const uint32_t* w = &t[col][at(col, 4 * q)];
@@ -58,15 +58,37 @@ __device__ __forceinline__ uint4 pack8(const uint32_t (&x)[8]) {
     return make_uint4(x[0] | (x[1] << 16), x[2] | (x[3] << 16), x[4] | (x[5] << 16), x[6] | (x[7] << 16));
 }
 
-// 16 columns of a packed 2:4 row from their 8 values and 16 bits of positions
-__device__ __forceinline__ void decode16(uint4 v, uint32_t b, uint32_t (&x)[16]) {
-    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+// Decoding a group of 4 columns: its two values are one word, and its 4 bits of positions select
+// from a table the byte selectors that spread them over the columns' two words (v_perm_b32:
+// selectors 0-3 take a byte, 12 gives zero).  The table is 16 entries of 8 bytes in LDS, one bank
+// pair each.
+struct SpreadTable {
+    uint2 sel[16];
+    // by the first 16 threads of a block, before a barrier
+    __device__ void fill(int tid) {
+        if (tid >= 16) return;
+        const uint32_t p0 = tid & 3u, p1 = tid >> 2;
+        uint32_t w[2] = {0, 0};
+#pragma unroll
+        for (uint32_t e = 0; e < 4; ++e)
+            w[e >> 1] |= (p0 == e ? 0x0100u : p1 == e ? 0x0302u : 0x0c0cu) << (16 * (e & 1));
+        sel[tid] = make_uint2(w[0], w[1]);
+    }
+};
+// 16 columns of two packed rows (8 values and 16 bits of positions each) as the columns' row
+// pairs: x[e] = row 0's column e | row 1's column e << 16
+__device__ __forceinline__ void decode_pair16(const SpreadTable& t, uint4 v0, uint32_t b0, uint4 v1, uint32_t b1,
+                                              uint32_t (&x)[16]) {
+    const uint32_t a[4] = {v0.x, v0.y, v0.z, v0.w}, c[4] = {v1.x, v1.y, v1.z, v1.w};
 #pragma unroll
     for (int q = 0; q < 4; ++q) {
-        const uint32_t v0 = w[q] & 0xffffu, v1 = w[q] >> 16;
-        const uint32_t p0 = (b >> (4 * q)) & 3u, p1 = (b >> (4 * q + 2)) & 3u;
-#pragma unroll
-        for (uint32_t e = 0; e < 4; ++e) x[4 * q + e] = (p0 == e ? v0 : 0u) | (p1 == e ? v1 : 0u);
+        const uint2 sa = t.sel[(b0 >> (4 * q)) & 15u], sc = t.sel[(b1 >> (4 * q)) & 15u];
+        const uint32_t a0 = __builtin_amdgcn_perm(0, a[q], sa.x), a1 = __builtin_amdgcn_perm(0, a[q], sa.y);
+        const uint32_t c0 = __builtin_amdgcn_perm(0, c[q], sc.x), c1 = __builtin_amdgcn_perm(0, c[q], sc.y);
+        x[4 * q + 0] = __builtin_amdgcn_perm(c0, a0, 0x05040100u);
+        x[4 * q + 1] = __builtin_amdgcn_perm(c0, a0, 0x07060302u);
+        x[4 * q + 2] = __builtin_amdgcn_perm(c1, a1, 0x05040100u);
+        x[4 * q + 3] = __builtin_amdgcn_perm(c1, a1, 0x07060302u);
     }
 }
 
@@ -97,7 +119,7 @@ __device__ __forceinline__ void transpose_tile(PairTile& tile, const uint16_t* _
     }
     if (!T) return;
 #pragma unroll
-    for (int e = 0; e < 8; ++e) tile.put(c8 * 8 + e, pair, x[0][e], x[1][e]);
+    for (int e = 0; e < 8; ++e) tile.put(c8 * 8 + e, pair, x[0][e] | (x[1][e] << 16));
     __syncthreads();
 #pragma unroll
     for (int p = 0; p < 2; ++p) {
@@ -139,8 +161,8 @@ __device__ __forceinline__ void glu_grad_tile(PairTile& tile, const LayoutArgs& 
     // columns 0-63 of the tile: dG, 64-127: dU
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
-        tile.put(c8 * 8 + e, pair, dg[0][e], dg[1][e]);
-        tile.put(64 + c8 * 8 + e, pair, du[0][e], du[1][e]);
+        tile.put(c8 * 8 + e, pair, dg[0][e] | (dg[1][e] << 16));
+        tile.put(64 + c8 * 8 + e, pair, du[0][e] | (du[1][e] << 16));
     }
     __syncthreads();
 #pragma unroll
@@ -153,21 +175,24 @@ __device__ __forceinline__ void glu_grad_tile(PairTile& tile, const LayoutArgs& 
 // 64 rows x 128 columns of a packed 2:4 weight (a line of values per row) -> WT [K, Rn] at columns
 // off + r (rows past R: zero).  Thread (c, pair): rows 2 pair, 2 pair + 1, columns 16 c ..: 8
 // values and 16 bits of positions per row; K is a multiple of 16.
-__device__ __forceinline__ void decode_tile(PairTile& tile, const LayoutArgs& a, int mat, int ti, int tj) {
+__device__ __forceinline__ void decode_tile(PairTile& tile, SpreadTable& table, const LayoutArgs& a, int mat, int ti, int tj) {
     const GradIn& in = a.in;
     const int tid = threadIdx.x, c = tid & 7, pair = tid >> 3;
     const int64_t r0 = (int64_t)ti * 64, k0 = (int64_t)tj * 128, k = k0 + 16 * c;
-    uint32_t x[2][16];
+    table.fill(tid);
+    __syncthreads();
+    uint4 v[2];
+    uint32_t b[2], x[16];
 #pragma unroll
     for (int j = 0; j < 2; ++j) {
         const int64_t r = r0 + 2 * pair + j;
         const bool ok = r < in.R && k < in.K;
-        const uint4 v = ok ? *(const uint4*)(in.vals[mat] + r * in.ldv + k / 2) : make_uint4(0, 0, 0, 0);
-        const uint32_t b = ok ? in.idx[mat][r * in.ldi + k / 32] >> (16 * (c & 1)) : 0u;
-        decode16(v, b, x[j]);
+        v[j] = ok ? *(const uint4*)(in.vals[mat] + r * in.ldv + k / 2) : make_uint4(0, 0, 0, 0);
+        b[j] = ok ? in.idx[mat][r * in.ldi + k / 32] >> (16 * (c & 1)) : 0u;
     }
+    decode_pair16(table, v[0], b[0], v[1], b[1], x);
 #pragma unroll
-    for (int e = 0; e < 16; ++e) tile.put(c * 16 + e, pair, x[0][e], x[1][e]);
+    for (int e = 0; e < 16; ++e) tile.put(c * 16 + e, pair, x[e]);
     __syncthreads();
 #pragma unroll
     for (int p = 0; p < 4; ++p) {
@@ -180,11 +205,12 @@ __device__ __forceinline__ void decode_tile(PairTile& tile, const LayoutArgs& a,
 template <int ACT, bool VEC>
 __global__ __launch_bounds__(256) void grad_layout_kernel(LayoutArgs a) {
     __shared__ PairTile tile;
+    __shared__ SpreadTable table;
     int b = blockIdx.x;
     if (b < a.nw) {
         const int mat = b / (a.nw / (ACT >= 0 ? 2 : 1));
         b -= mat * (a.nw / 2);
-        decode_tile(tile, a, mat, b / a.tw, b % a.tw);
+        decode_tile(tile, table, a, mat, b / a.tw, b % a.tw);
     } else if (b < a.nw + a.nd) {
         b -= a.nw;
         if constexpr (ACT >= 0) glu_grad_tile<ACT, VEC>(tile, a, b / a.td, b % a.td);
@@ -434,7 +460,7 @@ __global__ __launch_bounds__(512, 1) void grad_ring_kernel(GradArgs g) {
 }
 
 // ------------------------------------------------------------------ few tokens
-// Up to 64 tokens the dense ring pays for 256-token tiles and for a dense copy of the weights;
+// Up to 128 tokens the dense ring pays for 256-token tiles and for a dense copy of the weights;
 // both products are then streams: dX reads the packed weights, dV writes its packed
 // values.  One grid holds both.
 // dX: a block sums dY W over a run of weight rows for 128 columns and all tokens (ST
@@ -446,8 +472,8 @@ __global__ __launch_bounds__(512, 1) void grad_ring_kernel(GradArgs g) {
 // wave w takes columns 32 w .. + 31.  LDS is double buffered, one barrier a step.  Partials
 // [split][M][K] in f32 are added by grad_reduce_kernel.  Blocks of one split and all panels
 // run on one XCD, whose L2 then serves the positions' lines (8 panels each) once.
-// dV: 128 x 128 tiles, four waves of 64 x 64; the tile's 64 tokens (a line per row of XT and
-// of DT) are loaded whole into LDS, the epilogue is the ring's.
+// dV: 128 x 128 tiles, four waves of 64 x 64; the tile's tokens (one or two lines per row of XT
+// and of DT) are loaded whole into LDS, the epilogue is the ring's.
 struct FewArgs {
     GradArgs g;
     GradIn in;
@@ -458,13 +484,15 @@ struct FewArgs {
     int tk, tr;                // 128-wide tiles of dV along K and along the stacked rows
 };
 constexpr int kFewCol = 36, kFewWords = 128 * kFewCol + 8 * 8;   // a decoded step
-constexpr int64_t kFewTokens = 64;                               // dV's tiles hold all tokens: Mp == 64
+constexpr int64_t kFewTokens = 128;                              // dV's tiles hold all tokens
 
 template <int ST>
-__global__ __launch_bounds__(256, 3) void grad_few_kernel(FewArgs a) {
+__global__ __launch_bounds__(256, ST == 4 ? 2 : 3) void grad_few_kernel(FewArgs a) {
     constexpr int PF = 4, DBYTES = 32 * ST * 128, LDS = 2 * (kFewWords * 4 + DBYTES);
-    static_assert(LDS >= 32 * 1024, "dV's tile fits");
+    constexpr int HV = ST == 4 ? 2 : 1;   // 64-token halves of dV: Mp == 64 HV
+    static_assert(LDS >= HV * 32 * 1024, "dV's tile fits");
     __shared__ __attribute__((aligned(1024))) uint8_t smem[LDS];
+    __shared__ SpreadTable table;
     const int tid = threadIdx.x, lane = tid & 63, h = lane >> 5, l32 = lane & 31;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     auto sw = [](int r) { return (r >> 1) & 7; };   // 128-byte row r: logical 16-byte chunk c at c ^ sw(r)
@@ -473,15 +501,19 @@ __global__ __launch_bounds__(256, 3) void grad_few_kernel(FewArgs a) {
         const int b = blockIdx.x - a.g.nx, loc = b >> 3, tr = (loc / a.tk) * 8 + (b & 7);
         if (tr >= a.tr) return;
         const int64_t k0 = (int64_t)(loc % a.tk) * 128, q0 = (int64_t)tr * 128;
-        const void *baseA = uniform_ptr(a.g.v.A + k0 * 64), *baseB = uniform_ptr(a.g.v.B + q0 * 64);
+        const void *baseA = uniform_ptr(a.g.v.A + k0 * 64 * HV), *baseB = uniform_ptr(a.g.v.B + q0 * 64 * HV);
         const int64_t kmax = a.K - 1 - k0, qmax = a.Rn - 1 - q0;
         const uint32_t sbase = lds_addr(smem);
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             const int row = (wave * 4 + i) * 8 + (lane >> 3);
             const uint32_t c = (uint32_t)(((lane & 7) ^ sw(row)) * 16);
-            dma16s(sbase + (wave * 4 + i) * 1024, baseA, (uint32_t)(row < kmax ? row : kmax) * 128u + c);
-            dma16s(sbase + 16384 + (wave * 4 + i) * 1024, baseB, (uint32_t)(row < qmax ? row : qmax) * 128u + c);
+#pragma unroll
+            for (int v = 0; v < HV; ++v) {
+                const uint32_t at = sbase + v * 32768 + (wave * 4 + i) * 1024;
+                dma16s(at, baseA, (uint32_t)(row < kmax ? row : kmax) * (128u * HV) + 128u * v + c);
+                dma16s(at + 16384, baseB, (uint32_t)(row < qmax ? row : qmax) * (128u * HV) + 128u * v + c);
+            }
         }
         uint32_t words[2][2];
         grad_positions<2, 2>(a.g, k0 + (wave & 1) * 64, q0 + (wave >> 1) * 64, lane, words);
@@ -493,12 +525,14 @@ __global__ __launch_bounds__(256, 3) void grad_few_kernel(FewArgs a) {
         wait_vm_barrier<0>();
         const int ra = (wave & 1) * 64 + l32, rb = (wave >> 1) * 64 + l32;
 #pragma unroll
-        for (int d = 0; d < 4; ++d) {
+        for (int dv = 0; dv < 4 * HV; ++dv) {
+            const int d = dv & 3;
+            const uint8_t* half = smem + (dv >> 2) * 32768;
             i32x4_t fa[2], fb[2];
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
-                fa[i] = *(const i32x4_t*)(smem + (ra + 32 * i) * 128 + ((2 * d + h) ^ sw(ra + 32 * i)) * 16);
-                fb[i] = *(const i32x4_t*)(smem + 16384 + (rb + 32 * i) * 128 + ((2 * d + h) ^ sw(rb + 32 * i)) * 16);
+                fa[i] = *(const i32x4_t*)(half + (ra + 32 * i) * 128 + ((2 * d + h) ^ sw(ra + 32 * i)) * 16);
+                fb[i] = *(const i32x4_t*)(half + 16384 + (rb + 32 * i) * 128 + ((2 * d + h) ^ sw(rb + 32 * i)) * 16);
             }
 #pragma unroll
             for (int i = 0; i < 2; ++i)
@@ -549,6 +583,8 @@ __global__ __launch_bounds__(256, 3) void grad_few_kernel(FewArgs a) {
     for (int j = 0; j < ST; ++j) acc[j] = f32x16_t{};
 #pragma unroll
     for (int u = 0; u < PF; ++u) load(s0 + u, pv[u], pi[u], pd[u]);
+    table.fill(tid);
+    __syncthreads();
     for (int sb = s0; sb < s1; sb += PF) {
 #pragma unroll
         for (int u = 0; u < PF; ++u) {
@@ -557,15 +593,14 @@ __global__ __launch_bounds__(256, 3) void grad_few_kernel(FewArgs a) {
                 uint8_t* const buf = smem + (u & 1) * (kFewWords * 4 + DBYTES);
                 uint8_t* const dbuf = buf + kFewWords * 4;
                 const int64_t q = (int64_t)s * 64 - (s * 64 >= Rp ? Rp : 0) + 2 * pair;
-                uint32_t x[2][16];
-#pragma unroll
-                for (int j = 0; j < 2; ++j) {
-                    const i32x4_t z = kok && q + j < a.in.R ? pv[u][j] : i32x4_t{0, 0, 0, 0};
-                    decode16(__builtin_bit_cast(uint4, z), pi[u][j] >> (16 * (c & 1)), x[j]);
-                }
+                uint32_t x[16];
+                const i32x4_t z0 = kok && q < a.in.R ? pv[u][0] : i32x4_t{0, 0, 0, 0};
+                const i32x4_t z1 = kok && q + 1 < a.in.R ? pv[u][1] : i32x4_t{0, 0, 0, 0};
+                decode_pair16(table, __builtin_bit_cast(uint4, z0), pi[u][0] >> (16 * (c & 1)),
+                              __builtin_bit_cast(uint4, z1), pi[u][1] >> (16 * (c & 1)), x);
                 uint32_t* w = (uint32_t*)buf + c * (16 * kFewCol + 8) + pair;
 #pragma unroll
-                for (int e = 0; e < 16; ++e) w[e * kFewCol] = x[0][e] | (x[1][e] << 16);
+                for (int e = 0; e < 16; ++e) w[e * kFewCol] = x[e];
 #pragma unroll
                 for (int j = 0; j < ST; ++j) {
                     const int m = 32 * j + (tid >> 3);
@@ -814,7 +849,8 @@ nm_status launch_grad(const GradIn& in, const GradOut& out, int nmat, void* ws, 
         f.g = g;
         const dim3 gf((unsigned)(g.nx + (dv ? f.tk * (int)ceil_div(f.tr, 8) * 8 : 0)));
         if (in.M <= 32) hipLaunchKernelGGL(grad_few_kernel<1>, gf, dim3(256), 0, s, f);
-        else hipLaunchKernelGGL(grad_few_kernel<2>, gf, dim3(256), 0, s, f);
+        else if (in.M <= 64) hipLaunchKernelGGL(grad_few_kernel<2>, gf, dim3(256), 0, s, f);
+        else hipLaunchKernelGGL(grad_few_kernel<4>, gf, dim3(256), 0, s, f);
     } else {
         hipLaunchKernelGGL(grad_ring_kernel, dim3((unsigned)(g.nx + nv)), dim3(512), 0, s, g);
     }
