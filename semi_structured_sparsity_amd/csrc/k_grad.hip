@@ -37,13 +37,20 @@ struct PairTile {
     }
 };
 
-// 8 bf16 of a row from column c; zero past cols (or if !ok)
-template <bool VEC>
+// 8 bf16 of a row from column c; zero past cols (or if !ok).  VEC: bytes of a load (16, or 4 where
+// rows are only even, else 2)
+template <int VEC>
 __device__ __forceinline__ void load_row8(const uint16_t* __restrict__ row, int64_t c, int64_t cols, bool ok,
                                           uint32_t (&x)[8]) {
-    if (VEC && ok && c + 8 <= cols) {
-        const uint4 u = *(const uint4*)(row + c);
-        const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+    if (VEC > 2 && ok && c + 8 <= cols) {
+        uint32_t w[4];
+        if constexpr (VEC == 16) {
+            const uint4 u = *(const uint4*)(row + c);
+            w[0] = u.x, w[1] = u.y, w[2] = u.z, w[3] = u.w;
+        } else {
+#pragma unroll
+            for (int e = 0; e < 4; ++e) w[e] = ((const uint32_t*)(row + c))[e];
+        }
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
             x[2 * e] = w[e] & 0xffffu;
@@ -102,7 +109,7 @@ struct LayoutArgs {
 
 // S [rows, cols] (lds), tile (ti, tj) -> T [cols, rowsp] and the copy C (ldc), both zero past the
 // edges
-template <bool VEC>
+template <int VEC>
 __device__ __forceinline__ void transpose_tile(PairTile& tile, const uint16_t* __restrict__ S, int64_t lds, int64_t rows,
                                                int64_t cols, uint16_t* __restrict__ T, int64_t rowsp,
                                                uint16_t* __restrict__ C, int64_t ldc, int ti, int tj) {
@@ -130,7 +137,7 @@ __device__ __forceinline__ void transpose_tile(PairTile& tile, const uint16_t* _
 
 // dG | dU from dH, G, U: rows of D [M, 2 Rp] and of DT [2 Rp, Mp], padded with zeros.  They are
 // rounded to bf16 here: operands of the bf16 matrix products, as the forward's activations are.
-template <int ACT, bool VEC>
+template <int ACT, int VEC>
 __device__ __forceinline__ void glu_grad_tile(PairTile& tile, const LayoutArgs& a, int ti, int tj) {
     const GradIn& in = a.in;
     const int tid = threadIdx.x, c8 = tid & 7, pair = tid >> 3;
@@ -149,8 +156,9 @@ __device__ __forceinline__ void glu_grad_tile(PairTile& tile, const LayoutArgs& 
             const float hf = bf16_bits_to_f32(h[e]), gf = bf16_bits_to_f32(g[e]), uf = bf16_bits_to_f32(u[e]);
             float f, d;
             act_and_grad<ACT>(gf, f, d);
-            dg[k][e] = f32_to_bf16_bits(hf * uf * d);
-            du[k][e] = f32_to_bf16_bits(hf * f);
+            const uint32_t both = f32_to_bf16_pair(hf * uf * d, hf * f);
+            dg[k][e] = both & 0xffffu;
+            du[k][e] = both >> 16;
         }
         if (a.D && ok) {
             *(uint4*)(a.D + (m + k) * a.Rn + c) = pack8(dg[k]);
@@ -202,7 +210,7 @@ __device__ __forceinline__ void decode_tile(PairTile& tile, SpreadTable& table, 
 }
 
 // ACT: the gated block's activation, or -1: dY itself
-template <int ACT, bool VEC>
+template <int ACT, int VEC>
 __global__ __launch_bounds__(256) void grad_layout_kernel(LayoutArgs a) {
     __shared__ PairTile tile;
     __shared__ SpreadTable table;
@@ -217,7 +225,7 @@ __global__ __launch_bounds__(256) void grad_layout_kernel(LayoutArgs a) {
         else transpose_tile<VEC>(tile, a.in.dY, a.in.lddy, a.in.M, a.in.R, a.DT, a.Mp, a.D, a.Rn, b / a.td, b % a.td);
     } else {
         b -= a.nw + a.nd;
-        transpose_tile<true>(tile, a.in.X, a.in.ldx, a.in.M, a.in.K, a.XT, a.Mp, (uint16_t*)nullptr, 0, b / a.tx, b % a.tx);
+        transpose_tile<16>(tile, a.in.X, a.in.ldx, a.in.M, a.in.K, a.XT, a.Mp, (uint16_t*)nullptr, 0, b / a.tx, b % a.tx);
     }
 }
 
@@ -720,7 +728,11 @@ static GradWs grad_ws_layout(int64_t M, int64_t K, int64_t R, int nmat) {
 }
 size_t grad_ws(int64_t M, int64_t K, int64_t R, int nmat) { return grad_ws_layout(M, K, R, nmat).total(); }
 
-static bool rows16(const void* p, int64_t ld) { return ((uintptr_t)p & 15u) == 0 && ld % 8 == 0; }
+// bytes that every row start is a multiple of: 16, 4 or 2
+static int row_align(const void* p, int64_t ld) {
+    const uintptr_t a = (uintptr_t)p | (uintptr_t)(ld * 2);
+    return (a & 15u) == 0 ? 16 : (a & 3u) == 0 ? 4 : 2;
+}
 
 // a row-major matrix of width 2-byte units set to zero (ld in bytes)
 __global__ __launch_bounds__(256) void zero_rows_kernel(uint8_t* __restrict__ p, int64_t rows, int64_t width, int64_t ld) {
@@ -751,9 +763,14 @@ nm_status launch_grad(const GradIn& in, const GradOut& out, int nmat, void* ws, 
     uint16_t* WT = (uint16_t*)(p + w.d + w.dt + w.xt);
     float* PART = (float*)(p + w.d + w.dt + w.xt + w.wt);
     const bool dx = out.dX != nullptr, dv = out.dV[0] != nullptr;
-    const bool vec = rows16(in.dY, in.lddy) && (nmat == 1 || (rows16(in.G, in.ldg) && rows16(in.U, in.ldg)));
+    int vec = row_align(in.dY, in.lddy);
+    if (nmat == 2) {
+        const int g = row_align(in.G, in.ldg), u = row_align(in.U, in.ldg);
+        vec = g < vec ? g : vec;
+        vec = u < vec ? u : vec;
+    }
     // dX reads dY itself where its rows are whole 64-column stages on 16-byte boundaries
-    const bool direct = nmat == 1 && vec && in.R == Rp && in.lddy < (1 << 23);
+    const bool direct = nmat == 1 && vec == 16 && in.R == Rp && in.lddy < (1 << 23);
     const uint16_t* B = direct ? in.dY : D;
     const int64_t ldb = direct ? in.lddy : Rn;
     LayoutArgs l{};
@@ -775,8 +792,9 @@ nm_status launch_grad(const GradIn& in, const GradOut& out, int nmat, void* ws, 
     if (gl.x) {
 #define NM_LAYOUT(A)                                                                                  \
     do {                                                                                              \
-        if (vec) hipLaunchKernelGGL((grad_layout_kernel<A, true>), gl, dim3(256), 0, s, l);           \
-        else hipLaunchKernelGGL((grad_layout_kernel<A, false>), gl, dim3(256), 0, s, l);              \
+        if (vec == 16) hipLaunchKernelGGL((grad_layout_kernel<A, 16>), gl, dim3(256), 0, s, l);       \
+        else if (vec == 4) hipLaunchKernelGGL((grad_layout_kernel<A, 4>), gl, dim3(256), 0, s, l);    \
+        else hipLaunchKernelGGL((grad_layout_kernel<A, 2>), gl, dim3(256), 0, s, l);                  \
     } while (0)
     if (nmat == 1) NM_LAYOUT(-1);
     else if (in.act == NM_ACT_SILU) NM_LAYOUT(NM_ACT_SILU);
