@@ -15,7 +15,8 @@
 //   D  [M, nmat * Rp]  dY, or dG | dU, the rows padded to Rp = a multiple of 64 with zeros,
 //   DT [nmat * Rp, Mp] its transpose, the tokens padded to Mp = a multiple of 64 with zeros,
 //   XT [K, Mp]         X transposed,
-//   WT [K, nmat * Rp]  the packed weights, dense and transposed.
+//   WT [K, nmat * Rp]  the packed weights, dense and transposed (many tokens; fewer decode them
+//                      in the product, ring_decodes).
 #include "nm_ring.h"
 
 namespace nm {
@@ -251,6 +252,9 @@ struct GradArgs {
     void* dV[2];
     int64_t ldi, lddv, R, Rp;
     int dvf32;
+    // dX from the packed weights (DEC)
+    const uint16_t* vals[2];
+    int64_t ldv;
 };
 
 // Gradient of packed 2:4 values: of the tile's columns k (rows rw .. of the accumulators) of
@@ -346,29 +350,29 @@ __device__ __forceinline__ void store_grad_tile(const GradArgs& a, const f32x16_
 // random operands runs a stage in 0.92 us, with the fragment reads 1.35, with the loads and
 // the barrier 1.60.  No faster, to 1%: the loads spread over the stage's depths, all of a
 // stage's fragments read ahead (4 sets), two depths ahead with 16 MFMAs between.
-__global__ __launch_bounds__(512, 1) void grad_ring_kernel(GradArgs g) {
+constexpr int kRingCol = 36, kRingA = (256 * kRingCol + 16 * 8) * 4;   // a decoded stage: words a column, bytes
+
+// A tile.  DEC: dX with the A operand decoded from the packed weights into the ring's slot, as
+// t[column][row pair] (36 words a column, 8 more every 16); each thread decodes two rows of 16
+// columns a stage, loaded a stage ahead.
+template <bool DEC>
+__device__ __forceinline__ void grad_tile(const GradArgs& g, const GradJob& job, bool isx, int bid, int split, uint8_t* smem) {
     constexpr int SR = 4, ST = 2, WRN = 2, WTN = 4, NW = 8, T = 256, ROWB = 128, D = 4;
-    constexpr int ASTAGE = T * ROWB, SLOT = 2 * ASTAGE, NL = ASTAGE / 1024 / NW;   // 4 loads of each operand per wave
-    __shared__ __attribute__((aligned(1024))) uint8_t smem[2 * SLOT > NW * kStageWords<SR> * 4 ? 2 * SLOT : NW * kStageWords<SR> * 4];
+    constexpr int STAGE = T * ROWB, NL = STAGE / 1024 / NW;   // 4 loads of an operand per wave
+    // slots: A, A, B, B (DEC: with A's padding) or A, B, A, B
+    constexpr int BOFF = DEC ? 2 * kRingA : STAGE, ASLOT = DEC ? kRingA : 2 * STAGE, BSLOT = DEC ? STAGE : 2 * STAGE;
+    static_assert(!DEC || BOFF + 2 * STAGE + sizeof(SpreadTable) <= NW * kStageWords<SR> * 4, "slots fit in the staging buffers");
     const int tid = threadIdx.x, lane = tid & 63;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int wr = wave % WRN, wt = wave / WRN;
-    const bool isx = (int)blockIdx.x < g.nx;
-    const GradJob& job = isx ? g.x : g.v;
-    int bid = isx ? blockIdx.x : blockIdx.x - g.nx, split = 0;
-    const int tiles = job.tiles_a * job.tiles_b;
-    if (isx) {
-        split = bid / tiles;
-        bid -= split * tiles;
-    }
     int ta, tb;
-    tile_of(bid, tiles, job.tiles_a, job.tiles_b, ta, tb);
+    tile_of(bid, job.tiles_a * job.tiles_b, job.tiles_a, job.tiles_b, ta, tb);
     const int64_t a0 = (int64_t)ta * T, b0 = (int64_t)tb * T;
     const int s_begin = split * job.spp;
     const int nsteps = job.nsteps - s_begin < job.spp ? job.nsteps - s_begin : job.spp;   // >= 1
     const uint32_t sbase = lds_addr(smem);
     auto sw = [](int r) { return (r >> 1) & 7; };   // row r: logical 16-byte chunk c at c ^ sw(r)
-    const void* baseA = uniform_ptr(job.A + a0 * job.lda + (int64_t)s_begin * 64);
+    const void* baseA = DEC ? nullptr : uniform_ptr(job.A + a0 * job.lda + (int64_t)s_begin * 64);
     const void* baseB = uniform_ptr(job.B + b0 * job.ldb + (int64_t)s_begin * 64);
     const int64_t amax = job.rowsA - 1 - a0, bmax = job.rowsB - 1 - b0;
     uint32_t oA[NL], oB[NL];
@@ -376,27 +380,61 @@ __global__ __launch_bounds__(512, 1) void grad_ring_kernel(GradArgs g) {
     for (int i = 0; i < NL; ++i) {
         const int row = (wave * NL + i) * 8 + (lane >> 3);
         const uint32_t c = (uint32_t)(((lane & 7) ^ sw(row)) * 16);
-        oA[i] = (uint32_t)((row < amax ? row : amax) * job.lda * 2) + c;
+        oA[i] = DEC ? 0 : (uint32_t)((row < amax ? row : amax) * job.lda * 2) + c;
         oB[i] = (uint32_t)((row < bmax ? row : bmax) * job.ldb * 2) + c;
     }
     auto issue = [&](int s) __attribute__((always_inline)) {
-        const uint32_t slot = sbase + (uint32_t)((s & 1) * SLOT);
+        if constexpr (!DEC) {
 #pragma unroll
-        for (int i = 0; i < NL; ++i) dma16s(slot + (wave * NL + i) * 1024, baseA, oA[i] + (uint32_t)(s * ROWB));
+            for (int i = 0; i < NL; ++i)
+                dma16s(sbase + (uint32_t)((s & 1) * ASLOT) + (wave * NL + i) * 1024, baseA, oA[i] + (uint32_t)(s * ROWB));
+        }
 #pragma unroll
-        for (int i = 0; i < NL; ++i) dma16s(slot + ASTAGE + (wave * NL + i) * 1024, baseB, oB[i] + (uint32_t)(s * ROWB));
+        for (int i = 0; i < NL; ++i)
+            dma16s(sbase + (uint32_t)(BOFF + (s & 1) * BSLOT) + (wave * NL + i) * 1024, baseB, oB[i] + (uint32_t)(s * ROWB));
+    };
+    // DEC: the thread's two rows (2 pair, 2 pair + 1 of the stage's 64) and 16 columns
+    SpreadTable& table = *(SpreadTable*)(smem + BOFF + 2 * STAGE);
+    const int dc = tid & 15, pair = tid >> 4;
+    const bool kok = a0 + 16 * dc < job.rowsA;
+    struct Packed {
+        i32x4_t v[2];
+        uint32_t ix[2];
+    };
+    auto load_packed = [&](int s, Packed& p) __attribute__((always_inline)) {
+        const int64_t q0 = (int64_t)(s_begin + (s < nsteps ? s : nsteps - 1)) * 64;
+        const int mat = q0 >= g.Rp ? 1 : 0;   // Rp is a multiple of 64: a stage is of one weight
+        const uint16_t* vals = mat ? g.vals[1] : g.vals[0];
+        const uint32_t* idx = mat ? g.idx[1] : g.idx[0];
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+            const int64_t q = q0 - mat * g.Rp + 2 * pair + j, r = q < g.R ? q : 0, k = kok ? a0 + 16 * dc : 0;
+            p.v[j] = *(const i32x4_t*)(vals + r * g.ldv + k / 2);
+            p.ix[j] = idx[r * g.ldi + k / 32];
+        }
+    };
+    auto decode = [&](int s, const Packed& p) __attribute__((always_inline)) {
+        const int64_t q0 = (int64_t)(s_begin + s) * 64, q = q0 - (q0 >= g.Rp ? g.Rp : 0) + 2 * pair;
+        const i32x4_t z0 = kok && q < g.R ? p.v[0] : i32x4_t{0, 0, 0, 0}, z1 = kok && q + 1 < g.R ? p.v[1] : i32x4_t{0, 0, 0, 0};
+        uint32_t x[16];
+        decode_pair16(table, __builtin_bit_cast(uint4, z0), p.ix[0] >> (16 * (dc & 1)), __builtin_bit_cast(uint4, z1),
+                      p.ix[1] >> (16 * (dc & 1)), x);
+        uint32_t* w = (uint32_t*)(smem + (s & 1) * ASLOT) + dc * (16 * kRingCol + 8) + pair;
+#pragma unroll
+        for (int e = 0; e < 16; ++e) w[e * kRingCol] = x[e];
     };
     struct Frag {
         i32x4_t a[SR], b[ST];
     };
     const int h = lane >> 5, l32 = lane & 31;
     auto read_depth = [&](int s, int d, Frag& f) __attribute__((always_inline)) {
-        const uint8_t* sA = smem + (s & 1) * SLOT;
-        const uint8_t* sB = sA + ASTAGE;
+        const uint8_t* sA = smem + (s & 1) * ASLOT;
+        const uint8_t* sB = smem + BOFF + (s & 1) * BSLOT;
 #pragma unroll
         for (int i = 0; i < SR; ++i) {
             const int row = (wr * SR + i) * 32 + l32;
-            f.a[i] = *(const i32x4_t*)(sA + row * ROWB + ((2 * d + h) ^ sw(row)) * 16);
+            f.a[i] = DEC ? *(const i32x4_t*)(sA + row * (kRingCol * 4) + (row >> 4) * 32 + (2 * d + h) * 16)
+                         : *(const i32x4_t*)(sA + row * ROWB + ((2 * d + h) ^ sw(row)) * 16);
         }
 #pragma unroll
         for (int j = 0; j < ST; ++j) {
@@ -428,19 +466,32 @@ __global__ __launch_bounds__(512, 1) void grad_ring_kernel(GradArgs g) {
         __builtin_amdgcn_sched_barrier(0);
     };
     uint32_t words[ST][SR] = {};
-    if (!isx) grad_positions<SR, ST>(g, a0 + wr * SR * 32, b0 + wt * ST * 32, lane, words);
+    if (!DEC && !isx) grad_positions<SR, ST>(g, a0 + wr * SR * 32, b0 + wt * ST * 32, lane, words);
     Frag fr[2];
+    Packed pk[2];
+    if constexpr (DEC) {
+        load_packed(0, pk[0]);
+        load_packed(1, pk[1]);
+        table.fill(tid);
+        __syncthreads();
+        decode(0, pk[0]);
+    }
     issue(0);
     if (nsteps > 1) issue(1);
-    if (nsteps > 1) wait_vm_barrier<2 * NL>();
+    if (nsteps > 1) wait_vm_barrier<(DEC ? 1 : 2) * NL>();
     else wait_vm_barrier<0>();
     read_depth(0, 0, fr[0]);
-    for (int s = 0; s < nsteps; ++s) {
+    // one stage; DEC: cur holds the next stage's packed rows, the stage after's are loaded into nxt
+    auto stage = [&](int s, Packed& cur, Packed& nxt) __attribute__((always_inline)) {
+        if constexpr (DEC) {
+            load_packed(s + 2, nxt);
+            if (s + 1 < nsteps) decode(s + 1, cur);
+        }
 #pragma unroll
         for (int d = 0; d + 1 < D; ++d) {
             read_depth(s, d + 1, fr[(d + 1) & 1]);
             mfmas(fr[d & 1]);
-            interleave();
+            if constexpr (!DEC) interleave();
         }
         // the last depth's fragments complete before the branch (the barrier waits for them anyway)
         __builtin_amdgcn_s_waitcnt(0xc07f);
@@ -450,9 +501,17 @@ __global__ __launch_bounds__(512, 1) void grad_ring_kernel(GradArgs g) {
             read_depth(s + 1, 0, fr[0]);
         }
         mfmas(fr[(D - 1) & 1]);
+    };
+    if constexpr (DEC) {
+        for (int s = 0; s < nsteps; s += 2) {
+            stage(s, pk[1], pk[0]);
+            if (s + 1 < nsteps) stage(s + 1, pk[0], pk[1]);
+        }
+    } else {
+        for (int s = 0; s < nsteps; ++s) stage(s, pk[0], pk[1]);
     }
     wait_vm_all();
-    if (!isx) {
+    if (!DEC && !isx) {
         store_grad_tile<SR, ST>(g, acc, words, a0 + wr * SR * 32, b0 + wt * ST * 32, lane);
         return;
     }
@@ -465,6 +524,17 @@ __global__ __launch_bounds__(512, 1) void grad_ring_kernel(GradArgs g) {
     a.ldy = g.part ? a.R : g.lddx;
     store_tile<uint16_t, SR, ST>(a, acc, a0 + wr * SR * 32, b0 + wt * ST * 32, a0 + T <= a.R && b0 + T <= a.Mtok,
                                  (uint32_t*)smem + wave * kStageWords<SR>, lane);
+}
+
+template <bool DEC>
+__global__ __launch_bounds__(512, 1) void grad_ring_kernel(GradArgs g) {
+    __shared__ __attribute__((aligned(1024))) uint8_t smem[8 * kStageWords<4> * 4];
+    if ((int)blockIdx.x < g.nx) {
+        const int tiles = g.x.tiles_a * g.x.tiles_b, split = blockIdx.x / tiles;
+        grad_tile<DEC>(g, g.x, true, blockIdx.x - split * tiles, split, smem);
+    } else {
+        grad_tile<false>(g, g.v, false, blockIdx.x - g.nx, 0, smem);
+    }
 }
 
 // ------------------------------------------------------------------ few tokens
@@ -705,6 +775,13 @@ static int few_splits(int64_t K, int64_t Rn, int* spp) {
     return (int)ceil_div(steps, *spp);
 }
 
+// Whether dX's tiles decode the packed weights themselves.  Every token tile decodes them again
+// (about half a microsecond a stage), the dense copy costs 3 bytes per weight once.
+// Measured on the gated block's backward at 11008 x 4096: 129 tokens 193 -> 137 us, 256
+// 211 -> 158, 512 297 -> 257, 768 391 -> 357, 1024 464 -> 462, 2048 767 -> 865; on small weights the longer
+// stages cost more than the copy (4096 x 1024 at 256 tokens 37.1 -> 40.2, 5504 x 2048 73 -> 59).
+static bool ring_decodes(int64_t M, int64_t K, int64_t Rn) { return M <= 3 * 256 && K * Rn >= ((int64_t)1 << 24); }
+
 // Workspace of one backward call, in the order it is carved.
 struct GradWs {
     size_t d = 0, dt = 0, xt = 0, wt = 0, part = 0;
@@ -722,7 +799,7 @@ static GradWs grad_ws_layout(int64_t M, int64_t K, int64_t R, int nmat) {
         w.part = up256((size_t)few_splits(K, Rn, &spp) * (size_t)(M * K) * 4);
         return w;
     }
-    w.wt = up256((size_t)(K * Rn * 2));
+    if (!ring_decodes(M, K, Rn)) w.wt = up256((size_t)(K * Rn * 2));
     w.part = up256(grad_x_part_bytes(M, K, Rn));
     return w;
 }
@@ -786,7 +863,8 @@ nm_status launch_grad(const GradIn& in, const GradOut& out, int nmat, void* ws, 
     l.tw = (int)ceil_div(in.K, 128);
     l.tx = (int)ceil_div(in.K, 64);
     l.nd = l.D || l.DT ? l.td * (int)(Mp / 64) : 0;
-    l.nw = dx && !few_tokens(in.M) ? l.tw * (int)(Rp / 64) * nmat : 0;
+    const bool dec = ring_decodes(in.M, in.K, Rn);
+    l.nw = dx && !few_tokens(in.M) && !dec ? l.tw * (int)(Rp / 64) * nmat : 0;
     l.nx = dv ? l.tx * (int)(Mp / 64) : 0;
     const dim3 gl((unsigned)(l.nd + l.nw + l.nx));
     if (gl.x) {
@@ -805,6 +883,15 @@ nm_status launch_grad(const GradIn& in, const GradOut& out, int nmat, void* ws, 
 #undef NM_LAYOUT
     GradArgs g{};
     int nv = 0, splits = 1;
+    for (int i = 0; i < 2; ++i) {
+        g.vals[i] = in.vals[i];
+        g.idx[i] = in.idx[i];
+        g.dV[i] = out.dV[i];
+    }
+    g.ldv = in.ldv;
+    g.ldi = in.ldi;
+    g.R = in.R;
+    g.Rp = Rp;
     if (dx) {
         splits = grad_x_splits(in.M, in.K, Rn, dv);
         GradJob& j = g.x;
@@ -837,14 +924,7 @@ nm_status launch_grad(const GradIn& in, const GradOut& out, int nmat, void* ws, 
         j.tiles_a = (int)ceil_div(in.K, 256);
         j.tiles_b = (int)ceil_div(Rn, 256);
         nv = j.tiles_a * j.tiles_b;
-        for (int i = 0; i < 2; ++i) {
-            g.idx[i] = in.idx[i];
-            g.dV[i] = out.dV[i];
-        }
-        g.ldi = in.ldi;
         g.lddv = out.lddv;
-        g.R = in.R;
-        g.Rp = Rp;
         g.dvf32 = out.dvdt == NM_F32;
     }
     if (few_tokens(in.M)) {
@@ -857,7 +937,6 @@ nm_status launch_grad(const GradIn& in, const GradOut& out, int nmat, void* ws, 
         f.ldd = ldb;
         f.tk = (int)ceil_div(in.K, 128);
         f.tr = (int)ceil_div(Rn, 128);
-        g.Rp = Rp;
         if (dx) {
             f.panels = (int)ceil_div(in.K, 128);
             f.splits = splits = few_splits(in.K, Rn, &f.spp);
@@ -870,7 +949,9 @@ nm_status launch_grad(const GradIn& in, const GradOut& out, int nmat, void* ws, 
         else if (in.M <= 64) hipLaunchKernelGGL(grad_few_kernel<2>, gf, dim3(256), 0, s, f);
         else hipLaunchKernelGGL(grad_few_kernel<4>, gf, dim3(256), 0, s, f);
     } else {
-        hipLaunchKernelGGL(grad_ring_kernel, dim3((unsigned)(g.nx + nv)), dim3(512), 0, s, g);
+        const dim3 gr((unsigned)(g.nx + nv));
+        if (dec) hipLaunchKernelGGL(grad_ring_kernel<true>, gr, dim3(512), 0, s, g);
+        else hipLaunchKernelGGL(grad_ring_kernel<false>, gr, dim3(512), 0, s, g);
     }
     if (g.part)
         hipLaunchKernelGGL(grad_reduce_kernel, dim3(grid_cap(ceil_div(in.M * in.K, 256), 8192)), dim3(256), 0, s, PART,

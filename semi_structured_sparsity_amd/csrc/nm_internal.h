@@ -188,7 +188,7 @@ __device__ __forceinline__ float act_value(float g) {
     if constexpr (ACT == NM_ACT_SILU) return g * sigmoid_f32(g);
     else if constexpr (ACT == NM_ACT_GELU) return 0.5f * g * erfcf(-g * kRsqrt2);
     else if constexpr (ACT == NM_ACT_GELU_TANH) return g * sigmoid_f32(kTanhC * g * __builtin_fmaf(kTanhA * g, g, 1.0f));
-    else return g > 0.0f ? g * g : g * 0.0f;   // NaN stays NaN
+    else return g <= 0.0f ? 0.0f : g * g;   // NaN stays NaN
 }
 
 template <int ACT>
@@ -208,8 +208,8 @@ __device__ __forceinline__ void act_and_grad(float g, float& f, float& d) {
         const float gc = __builtin_fabsf(g) > 32.0f ? 32.0f : g;
         d = __builtin_fmaf(gc * t * (1.0f - t) * kTanhC, __builtin_fmaf(3.0f * kTanhA * gc, gc, 1.0f), t);
     } else {
-        f = g > 0.0f ? g * g : g * 0.0f;
-        d = g > 0.0f ? 2.0f * g : g * 0.0f;
+        f = g <= 0.0f ? 0.0f : g * g;
+        d = g <= 0.0f ? 0.0f : 2.0f * g;
     }
 }
 

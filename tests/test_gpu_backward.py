@@ -28,8 +28,10 @@ def _np(t):
     return t.float().cpu().numpy().astype(np.float64)
 
 
+# (the last three: weights large enough that dX's tiles decode them, ragged everywhere)
 SIZES = [(1, 1, 16), (1, 64, 64), (3, 70, 48), (17, 33, 272), (64, 64, 64), (65, 130, 528), (129, 200, 1024),
-         (200, 1000, 272), (300, 257, 512), (513, 520, 784)]
+         (200, 1000, 272), (300, 257, 512), (513, 520, 784),
+         (130, 4100, 4112), (257, 8195, 2064), (600, 2111, 8208)]
 
 
 @pytest.mark.parametrize("Mt,R,K", SIZES)

@@ -182,3 +182,24 @@ def test_glu_binding_refuses(nm):
         nm.nm_spmm_glu(X, vg, ig, vg, ig, act=9)
     with pytest.raises(nm.NMError):
         nm.nm_spmm_glu(X, vg, ig, vg, ig, hdt=nm.NM_F32, out=X.view(torch.float32)[:, :8])
+
+
+def test_glu_infinite_gates(nm):
+    """An infinite pre-activation: max(g, 0)^2 has its limits, and the other activations' positive
+    side is infinite."""
+    K, R = 64, 8
+    v = torch.ones((R, K // 2), dtype=torch.bfloat16, device=dev())
+    i = torch.full((R, 2), 0x44444444, dtype=torch.int32, device=dev())      # columns 0 and 1 of every four
+    X = torch.zeros((3, K), dtype=torch.bfloat16, device=dev())
+    X[0, 0], X[1, 0], X[2, 0] = float("-inf"), float("inf"), 1.0
+    up = torch.ones_like(v) * 0.5
+    for a in B.ACTS:
+        H = nm.nm_spmm_glu(X, v, i, up, i, act=a, hdt=nm.NM_F32).cpu()
+        assert torch.isposinf(H[1]).all() and torch.isfinite(H[2]).all()
+        if a == B.RELU2:
+            assert torch.isnan(H[0]).all()      # 0 times an up product of -inf
+    inf = torch.full((1, R), float("-inf"), dtype=torch.bfloat16, device=dev())
+    one = torch.ones((1, R), dtype=torch.bfloat16, device=dev())
+    X1 = torch.ones((1, K), dtype=torch.bfloat16, device=dev())
+    dX, dvg, dvu = nm.nm_spmm_glu_backward(one, inf, one, X1, v, i, up, i, act=B.RELU2)
+    assert not dX.any() and not dvg.any() and not dvu.any()
