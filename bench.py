@@ -583,8 +583,8 @@ def traffic_for(key: str, files):
 
 
 # kernel sources of each launch (for the staleness check of committed counter figures)
-SOURCES = {"hutchinson+score+stats": ("k_hutch.hip", "k_spmm.hip", "k_gate.hip"), "gate+pack": ("k_gate.hip",),
-           f"spmm M={M_TOK}": ("k_spmm.hip",)}
+SOURCES = {"hutchinson+score+stats": ("k_hutch.hip", "k_spmm.hip", "nm_ring.h", "k_gate.hip"), "gate+pack": ("k_gate.hip",),
+           f"spmm M={M_TOK}": ("k_spmm.hip", "nm_ring.h")}
 
 
 def main():

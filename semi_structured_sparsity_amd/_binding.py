@@ -397,6 +397,8 @@ def nm_spmm_noalloc(X: torch.Tensor, vals: torch.Tensor, idx: torch.Tensor, R: i
 # These run every layer of every step, so their checks are one expression each; what it found is
 # looked up only when it fails.
 def _raw_stream(t: torch.Tensor) -> int:
+    if not t.is_cuda:
+        raise ValueError(f"tensors must be on a GPU, got {t.device}")
     return torch._C._cuda_getCurrentRawStream(t.device.index)
 
 
