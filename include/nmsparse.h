@@ -410,35 +410,38 @@ nm_status nm_spmm_glu(const void* X, nm_dtype xdt, int64_t Mtok, int64_t K, int6
                       size_t ws_bytes, nm_stream_t stream);
 
 /* ---------------------------------------------------------------- gradients
- * Backward pass of the plain 2:4 layer Y = X W^T in bf16, for training the kept values of a
- * fixed mask ("Sparse-BitNet", section 2 and "SparseForge", Methodology 3: training continues
+ * Backward pass of the sparse layer Y = X W^T in bf16, for training the kept values of a fixed
+ * mask ("Sparse-BitNet", section 2 and "SparseForge", Methodology 3: training continues
  * under the N:M mask):
  *   dX = dY W                                          [Mtok, K] (lddx), bf16 or f32, or NULL
- *   dV[r, j] = sum_m dY[m, r] X[m, column of value j]  [R, K/2] (lddv), bf16 or f32, or NULL
- * dV has the layout of vals; a padding slot's entry is the derivative at its position.  All
+ *   dV[r, j] = sum_m dY[m, r] X[m, column of value j]  [R, K'/2] (lddv), bf16 or f32, or NULL
+ * Ns: 0 for plain 2:4 (K' = K), or 3 <= Ns <= 8 for weights decomposed into windows over the
+ * lifted width K' = (2 - 2/Ns) K.  dV has the layout of vals; a padding slot's entry is the
+ * derivative at its position (W is the sum of what its slots place at a column).  All
  * sums in f32 in a fixed order, one rounding.  dY: bf16 [Mtok, R] (lddy), any alignment of 2
  * bytes (16-byte aligned rows are read faster).  X, vals: bf16 with 16-byte aligned rows; idx
- * 4-byte aligned; dV 16-byte aligned rows.  Requires K % 16 == 0 and Mtok, K, R <= 2^21.
+ * 4-byte aligned; dV 16-byte aligned rows.  Requires K % 2Ns == 0, K' % 16 == 0 and
+ * Mtok, K, R <= 2^21.
  * Zero tokens give dV = 0.  vals may be NULL when dX is, X when dV is; idx is always needed.
  * ws: nm_spmm_backward_workspace(...) bytes, 16-byte aligned. */
-size_t nm_spmm_backward_workspace(int64_t Mtok, int64_t K, int64_t R);
+size_t nm_spmm_backward_workspace(int64_t Mtok, int64_t K, int64_t R, int Ns);
 nm_status nm_spmm_backward(const void* dY, int64_t lddy, const void* X, int64_t ldx, int64_t Mtok, int64_t K,
-                           const void* vals, const uint32_t* idx, int64_t R, int64_t ldv, int64_t ldi, void* dX,
+                           const void* vals, const uint32_t* idx, int64_t R, int64_t ldv, int64_t ldi, int Ns, void* dX,
                            nm_dtype dxdt, int64_t lddx, void* dV, nm_dtype dvdt, int64_t lddv, void* ws,
                            size_t ws_bytes, nm_stream_t stream);
 
-/* Backward pass of nm_spmm_glu (bf16, plain 2:4, scales 1) from its saved pre-activations:
+/* Backward pass of nm_spmm_glu (bf16, scales 1) from its saved pre-activations:
  *   dG = dH . U . act'(G),  dU = dH . act(G)   (f32, rounded once to bf16 as operands)
  *   dX = dG Wg + dU Wu, dVg and dVu as dV of nm_spmm_backward from dG and dU.
  * dH (lddh), G and U (ldg): bf16 [Mtok, R].  dX NULL, or dVg and dVu both NULL: not computed.
  * Requirements of nm_spmm_backward for both weights.
  * ws: nm_spmm_glu_backward_workspace(...) bytes, 16-byte aligned. */
-size_t nm_spmm_glu_backward_workspace(int64_t Mtok, int64_t K, int64_t R);
+size_t nm_spmm_glu_backward_workspace(int64_t Mtok, int64_t K, int64_t R, int Ns);
 nm_status nm_spmm_glu_backward(const void* dH, int64_t lddh, const void* G, const void* U, int64_t ldg, nm_act act,
                                const void* X, int64_t ldx, int64_t Mtok, int64_t K, const void* vals_g,
                                const uint32_t* idx_g, const void* vals_u, const uint32_t* idx_u, int64_t R,
-                               int64_t ldv, int64_t ldi, void* dX, nm_dtype dxdt, int64_t lddx, void* dVg, void* dVu,
-                               nm_dtype dvdt, int64_t lddv, void* ws, size_t ws_bytes, nm_stream_t stream);
+                               int64_t ldv, int64_t ldi, int Ns, void* dX, nm_dtype dxdt, int64_t lddx, void* dVg,
+                               void* dVu, nm_dtype dvdt, int64_t lddv, void* ws, size_t ws_bytes, nm_stream_t stream);
 
 /* ---------------------------------------------------------------- optimiser
  * One AdamW step (decoupled weight decay) over count tensors, for the packed values, adapters

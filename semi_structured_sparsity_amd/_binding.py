@@ -87,11 +87,11 @@ SIGNATURES = {
     "nm_spmm_glu_workspace": (_SZ, [_I64, _I64, _I64, _I, _I]),
     "nm_spmm_glu": (_I, [_P, _I, _I64, _I64, _I64, _P, _P, _P, _P, _I, _I64, _I64, _I64, _I, _P, _F, _F, _I, _P, _I,
                          _I64, _P, _P, _I64, _P, _SZ, _P]),
-    "nm_spmm_backward_workspace": (_SZ, [_I64, _I64, _I64]),
-    "nm_spmm_backward": (_I, [_P, _I64, _P, _I64, _I64, _I64, _P, _P, _I64, _I64, _I64, _P, _I, _I64, _P, _I, _I64,
+    "nm_spmm_backward_workspace": (_SZ, [_I64, _I64, _I64, _I]),
+    "nm_spmm_backward": (_I, [_P, _I64, _P, _I64, _I64, _I64, _P, _P, _I64, _I64, _I64, _I, _P, _I, _I64, _P, _I, _I64,
                               _P, _SZ, _P]),
-    "nm_spmm_glu_backward_workspace": (_SZ, [_I64, _I64, _I64]),
-    "nm_spmm_glu_backward": (_I, [_P, _I64, _P, _P, _I64, _I, _P, _I64, _I64, _I64, _P, _P, _P, _P, _I64, _I64, _I64,
+    "nm_spmm_glu_backward_workspace": (_SZ, [_I64, _I64, _I64, _I]),
+    "nm_spmm_glu_backward": (_I, [_P, _I64, _P, _P, _I64, _I, _P, _I64, _I64, _I64, _P, _P, _P, _P, _I64, _I64, _I64, _I,
                                   _P, _I, _I64, _P, _P, _I, _I64, _P, _SZ, _P]),
     "nm_adamw": (_I, [_P, _I, _I, _D, _D, _D, _D, _I64, _P, _P]),
 }
@@ -483,30 +483,31 @@ def _grad_out(t: torch.Tensor | None, want: bool, shape, dt: int, device):
     return t
 
 
-def _grad_inputs(X, dY, vals, idx):
-    """(tokens, columns, rows) of a backward call on a 2:4 weight."""
+def _grad_inputs(X, dY, vals, idx, Ns):
+    """(tokens, columns, rows, lifted columns) of a backward call."""
     if not (_rows(X) and _rows(dY) and _rows(vals) and _rows(idx) and
             X.dtype == dY.dtype == vals.dtype == torch.bfloat16 and idx.dtype == torch.int32 and
             X.device == dY.device == vals.device == idx.device):
         _refuse("the backward pass takes row-major bf16 tensors and an int32 idx", X=X, dY=dY, vals=vals, idx=idx)
     Mtok, K = X.shape
     R = vals.shape[0]
-    if not (dY.shape == (Mtok, R) and vals.shape[1] >= K // 2 and idx.shape[0] == R and idx.shape[1] >= (K + 31) // 32):
-        _refuse("the shapes do not belong to one 2:4 layer", X=X, dY=dY, vals=vals, idx=idx)
-    return Mtok, K, R
+    Kl = lifted_width(K, Ns) if Ns >= 2 else K
+    if not (dY.shape == (Mtok, R) and vals.shape[1] >= Kl // 2 and idx.shape[0] == R and idx.shape[1] >= (Kl + 31) // 32):
+        _refuse("the shapes do not belong to one sparse layer", X=X, dY=dY, vals=vals, idx=idx)
+    return Mtok, K, R, Kl
 
 
-def nm_spmm_backward(dY: torch.Tensor, X: torch.Tensor, vals: torch.Tensor, idx: torch.Tensor, want_dx: bool = True,
-                     want_dv: bool = True, dxdt: int = NM_BF16, dvdt: int = NM_BF16, out_dx: torch.Tensor | None = None,
-                     out_dv: torch.Tensor | None = None, ws: torch.Tensor | None = None):
-    """(dX, dvals) of Y = X W^T on a 2:4 packed bf16 weight; what is not wanted is None."""
-    Mtok, K, R = _grad_inputs(X, dY, vals, idx)
+def nm_spmm_backward(dY: torch.Tensor, X: torch.Tensor, vals: torch.Tensor, idx: torch.Tensor, Ns: int = 0,
+                     want_dx: bool = True, want_dv: bool = True, dxdt: int = NM_BF16, dvdt: int = NM_BF16,
+                     out_dx: torch.Tensor | None = None, out_dv: torch.Tensor | None = None, ws: torch.Tensor | None = None):
+    """(dX, dvals) of Y = X W^T on a packed bf16 weight; what is not wanted is None."""
+    Mtok, K, R, Kl = _grad_inputs(X, dY, vals, idx, Ns)
     dX = _grad_out(out_dx, want_dx, (Mtok, K), dxdt, X.device)
-    dV = _grad_out(out_dv, want_dv, (R, K // 2), dvdt, X.device)
-    ws = _need(raw.nm_spmm_backward_workspace(Mtok, K, R), ws, X.device)
+    dV = _grad_out(out_dv, want_dv, (R, Kl // 2), dvdt, X.device)
+    ws = _need(raw.nm_spmm_backward_workspace(Mtok, K, R, Ns), ws, X.device)
     st = raw.nm_spmm_backward(dY.data_ptr(), _ld2(dY), X.data_ptr(), _ld2(X), Mtok, K, vals.data_ptr(), idx.data_ptr(), R,
-                              _ld2(vals), _ld2(idx), _ptr(dX), dxdt, K if dX is None else _ld2(dX), _ptr(dV), dvdt,
-                              K // 2 if dV is None else _ld2(dV), _ptr(ws),
+                              _ld2(vals), _ld2(idx), Ns, _ptr(dX), dxdt, K if dX is None else _ld2(dX), _ptr(dV), dvdt,
+                              Kl // 2 if dV is None else _ld2(dV), _ptr(ws),
                               0 if ws is None else ws.numel() * ws.element_size(), _raw_stream(X))
     if st:
         _check(st)
@@ -514,13 +515,13 @@ def nm_spmm_backward(dY: torch.Tensor, X: torch.Tensor, vals: torch.Tensor, idx:
 
 
 def nm_spmm_glu_backward(dH: torch.Tensor, G: torch.Tensor, U: torch.Tensor, X: torch.Tensor, vals_g: torch.Tensor,
-                         idx_g: torch.Tensor, vals_u: torch.Tensor, idx_u: torch.Tensor, act: int = NM_ACT_SILU,
-                         want_dx: bool = True, want_dv: bool = True, dxdt: int = NM_BF16, dvdt: int = NM_BF16,
-                         out_dx: torch.Tensor | None = None,
+                         idx_g: torch.Tensor, vals_u: torch.Tensor, idx_u: torch.Tensor, Ns: int = 0,
+                         act: int = NM_ACT_SILU, want_dx: bool = True, want_dv: bool = True, dxdt: int = NM_BF16,
+                         dvdt: int = NM_BF16, out_dx: torch.Tensor | None = None,
                          out_dv: tuple[torch.Tensor, torch.Tensor] | None = None, ws: torch.Tensor | None = None):
     """(dX, dvals_g, dvals_u) of nm_spmm_glu from its saved pre-activations; what is not wanted
     is None."""
-    Mtok, K, R = _grad_inputs(X, dH, vals_g, idx_g)
+    Mtok, K, R, Kl = _grad_inputs(X, dH, vals_g, idx_g, Ns)
     if not (vals_u.shape == vals_g.shape and idx_u.shape == idx_g.shape and vals_u.stride() == vals_g.stride() and
             idx_u.stride() == idx_g.stride() and vals_u.dtype == torch.bfloat16 and idx_u.dtype == torch.int32 and
             vals_u.device == idx_u.device == X.device):
@@ -529,16 +530,16 @@ def nm_spmm_glu_backward(dH: torch.Tensor, G: torch.Tensor, U: torch.Tensor, X: 
             G.device == U.device == X.device and _ld2(G) == _ld2(U)):
         _refuse("G and U must be row-major bf16 tensors of dH's shape with the same row stride", dH=dH, G=G, U=U)
     dX = _grad_out(out_dx, want_dx, (Mtok, K), dxdt, X.device)
-    dVg = _grad_out(out_dv[0] if out_dv else None, want_dv, (R, K // 2), dvdt, X.device)
-    dVu = _grad_out(out_dv[1] if out_dv else None, want_dv, (R, K // 2), dvdt, X.device)
+    dVg = _grad_out(out_dv[0] if out_dv else None, want_dv, (R, Kl // 2), dvdt, X.device)
+    dVu = _grad_out(out_dv[1] if out_dv else None, want_dv, (R, Kl // 2), dvdt, X.device)
     if want_dv and _ld2(dVu) != _ld2(dVg):
         _refuse("the two weight gradients must have the same row stride", dVg=dVg, dVu=dVu)
-    ws = _need(raw.nm_spmm_glu_backward_workspace(Mtok, K, R), ws, X.device)
+    ws = _need(raw.nm_spmm_glu_backward_workspace(Mtok, K, R, Ns), ws, X.device)
     st = raw.nm_spmm_glu_backward(dH.data_ptr(), _ld2(dH), G.data_ptr(), U.data_ptr(), _ld2(G), act, X.data_ptr(),
                                   _ld2(X), Mtok, K, vals_g.data_ptr(), idx_g.data_ptr(), vals_u.data_ptr(),
-                                  idx_u.data_ptr(), R, _ld2(vals_g), _ld2(idx_g), _ptr(dX), dxdt,
+                                  idx_u.data_ptr(), R, _ld2(vals_g), _ld2(idx_g), Ns, _ptr(dX), dxdt,
                                   K if dX is None else _ld2(dX), _ptr(dVg), _ptr(dVu), dvdt,
-                                  K // 2 if dVg is None else _ld2(dVg), _ptr(ws),
+                                  Kl // 2 if dVg is None else _ld2(dVg), _ptr(ws),
                                   0 if ws is None else ws.numel() * ws.element_size(), _raw_stream(X))
     if st:
         _check(st)

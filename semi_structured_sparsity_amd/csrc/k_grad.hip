@@ -5,6 +5,9 @@
 //   dG = dH . U . act'(G),  dU = dH . act(G)
 //   dX = dY W               (gated: dG Wg + dU Wu)
 //   dV[r, j] = sum_m dY[m, r] X[m, col(r, j)]   for the kept positions col(r, j) only.
+// A (2N-2):2N weight is a plain 2:4 one over the lifted width K' (lifted column 4 w + j of window
+// w reads column orig of X): dV reads X's rows by that map, dX' is formed over K' and folded, each
+// column's lifted ones (two at most) added in f32.
 // Neither product can use the sparse instructions: they skip zeros of the operand along the
 // summed dimension, W is 2:4 along K, but dX sums over R and dV over the tokens.  Both run as
 // dense products on 256 x 256 tiles (grad_ring_kernel), bound by the matrix
@@ -98,6 +101,14 @@ __device__ __forceinline__ void decode_pair16(const SpreadTable& t, uint4 v0, ui
         x[4 * q + 2] = __builtin_amdgcn_perm(c1, a1, 0x05040100u);
         x[4 * q + 3] = __builtin_amdgcn_perm(c1, a1, 0x07060302u);
     }
+}
+
+// Column of X under lifted column k of a (2 Ns - 2):2 Ns weight (Ns 0: itself).  From a window's
+// first column on, the columns below never come before it.
+__device__ __forceinline__ int64_t orig_col(int64_t k, int Ns) {
+    if (Ns == 0) return k;
+    const uint32_t w = (uint32_t)(k >> 2), n = (uint32_t)Ns - 1, g = w / n;   // below 2^20
+    return (int64_t)(2 * (n + 1) * g + 2 * (w - g * n)) + (k & 3);
 }
 
 struct LayoutArgs {
@@ -195,7 +206,7 @@ __device__ __forceinline__ void decode_tile(PairTile& tile, SpreadTable& table, 
 #pragma unroll
     for (int j = 0; j < 2; ++j) {
         const int64_t r = r0 + 2 * pair + j;
-        const bool ok = r < in.R && k < in.K;
+        const bool ok = r < in.R && k < in.Kl;
         v[j] = ok ? *(const uint4*)(in.vals[mat] + r * in.ldv + k / 2) : make_uint4(0, 0, 0, 0);
         b[j] = ok ? in.idx[mat][r * in.ldi + k / 32] >> (16 * (c & 1)) : 0u;
     }
@@ -206,7 +217,7 @@ __device__ __forceinline__ void decode_tile(PairTile& tile, SpreadTable& table, 
 #pragma unroll
     for (int p = 0; p < 4; ++p) {
         const int col = (tid >> 3) + 32 * p, q = tid & 7;
-        if (k0 + col < in.K) *(uint4*)(a.WT + (k0 + col) * a.Rn + mat * a.Rp + r0 + 8 * q) = tile.get(col, q);
+        if (k0 + col < in.Kl) *(uint4*)(a.WT + (k0 + col) * a.Rn + mat * a.Rp + r0 + 8 * q) = tile.get(col, q);
     }
 }
 
@@ -244,14 +255,14 @@ struct GradArgs {
     int nx;                   // blocks of dX (tiles * splits), the first of the grid
     // dX
     void* dX;
-    float* part;              // split partials [split][M][K], or null
+    float* part;              // partials [split][M][K'] (splits, or a lifted weight), or null
     int64_t lddx;
     int dxf32;
     // dV
     const uint32_t* idx[2];
     void* dV[2];
     int64_t ldi, lddv, R, Rp;
-    int dvf32;
+    int dvf32, Ns;
     // dX from the packed weights (DEC)
     const uint16_t* vals[2];
     int64_t ldv;
@@ -372,7 +383,10 @@ __device__ __forceinline__ void grad_tile(const GradArgs& g, const GradJob& job,
     const int nsteps = job.nsteps - s_begin < job.spp ? job.nsteps - s_begin : job.spp;   // >= 1
     const uint32_t sbase = lds_addr(smem);
     auto sw = [](int r) { return (r >> 1) & 7; };   // row r: logical 16-byte chunk c at c ^ sw(r)
-    const void* baseA = DEC ? nullptr : uniform_ptr(job.A + a0 * job.lda + (int64_t)s_begin * 64);
+    // dV of a lifted weight reads X's rows by their columns (job.lda is then XT's row length)
+    const int ns = isx ? 0 : g.Ns;
+    const int64_t first = orig_col(a0, ns);
+    const void* baseA = DEC ? nullptr : uniform_ptr(job.A + first * job.lda + (int64_t)s_begin * 64);
     const void* baseB = uniform_ptr(job.B + b0 * job.ldb + (int64_t)s_begin * 64);
     const int64_t amax = job.rowsA - 1 - a0, bmax = job.rowsB - 1 - b0;
     uint32_t oA[NL], oB[NL];
@@ -380,7 +394,7 @@ __device__ __forceinline__ void grad_tile(const GradArgs& g, const GradJob& job,
     for (int i = 0; i < NL; ++i) {
         const int row = (wave * NL + i) * 8 + (lane >> 3);
         const uint32_t c = (uint32_t)(((lane & 7) ^ sw(row)) * 16);
-        oA[i] = DEC ? 0 : (uint32_t)((row < amax ? row : amax) * job.lda * 2) + c;
+        oA[i] = DEC ? 0 : (uint32_t)((orig_col(a0 + (row < amax ? row : amax), ns) - first) * job.lda * 2) + c;
         oB[i] = (uint32_t)((row < bmax ? row : bmax) * job.ldb * 2) + c;
     }
     auto issue = [&](int s) __attribute__((always_inline)) {
@@ -579,17 +593,19 @@ __global__ __launch_bounds__(256, ST == 4 ? 2 : 3) void grad_few_kernel(FewArgs 
         const int b = blockIdx.x - a.g.nx, loc = b >> 3, tr = (loc / a.tk) * 8 + (b & 7);
         if (tr >= a.tr) return;
         const int64_t k0 = (int64_t)(loc % a.tk) * 128, q0 = (int64_t)tr * 128;
-        const void *baseA = uniform_ptr(a.g.v.A + k0 * 64 * HV), *baseB = uniform_ptr(a.g.v.B + q0 * 64 * HV);
+        const int64_t first = orig_col(k0, a.g.Ns);
+        const void *baseA = uniform_ptr(a.g.v.A + first * 64 * HV), *baseB = uniform_ptr(a.g.v.B + q0 * 64 * HV);
         const int64_t kmax = a.K - 1 - k0, qmax = a.Rn - 1 - q0;
         const uint32_t sbase = lds_addr(smem);
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             const int row = (wave * 4 + i) * 8 + (lane >> 3);
             const uint32_t c = (uint32_t)(((lane & 7) ^ sw(row)) * 16);
+            const uint32_t arow = (uint32_t)(orig_col(k0 + (row < kmax ? row : kmax), a.g.Ns) - first);
 #pragma unroll
             for (int v = 0; v < HV; ++v) {
                 const uint32_t at = sbase + v * 32768 + (wave * 4 + i) * 1024;
-                dma16s(at, baseA, (uint32_t)(row < kmax ? row : kmax) * (128u * HV) + 128u * v + c);
+                dma16s(at, baseA, arow * (128u * HV) + 128u * v + c);
                 dma16s(at + 16384, baseB, (uint32_t)(row < qmax ? row : qmax) * (128u * HV) + 128u * v + c);
             }
         }
@@ -717,13 +733,23 @@ __global__ __launch_bounds__(256, ST == 4 ? 2 : 3) void grad_few_kernel(FewArgs 
     }
 }
 
-// dX from its split partials, in split order
+// dX [M, K] from its partials [splits][M][Kl], in split order; Ns: column k from the lifted columns
+// above it, windows in order
 __global__ __launch_bounds__(256) void grad_reduce_kernel(const float* __restrict__ part, int splits, int64_t M, int64_t K,
-                                                          void* __restrict__ dX, int64_t lddx, int f32) {
+                                                          int64_t Kl, int Ns, void* __restrict__ dX, int64_t lddx, int f32) {
     const int64_t total = M * K;
     for (int64_t t = (int64_t)blockIdx.x * 256 + threadIdx.x; t < total; t += (int64_t)gridDim.x * 256) {
         const int64_t m = t / K, k = t - m * K;
-        const float v = split_sum(part + t, splits, total);
+        float v;
+        if (Ns == 0) {
+            v = split_sum(part + t, splits, total);
+        } else {
+            const int g = (int)((uint32_t)k / (uint32_t)(2 * Ns)), p = (int)k - g * 2 * Ns;
+            const int last = p / 2 < Ns - 2 ? p / 2 : Ns - 2;   // windows that cover p start at 2 w in p - 3 .. p
+            v = 0.0f;
+            for (int w = p > 3 ? (p - 2) / 2 : 0; w <= last; ++w)
+                v += split_sum(part + m * Kl + 4 * (g * (Ns - 1) + w) + p - 2 * w, splits, M * Kl);
+        }
         if (f32) ((float*)dX)[m * lddx + k] = v;
         else ((uint16_t*)dX)[m * lddx + k] = (uint16_t)f32_to_bf16_bits(v);
     }
@@ -752,8 +778,9 @@ static int grad_x_splits(int64_t M, int64_t K, int64_t Rn, bool with_v) {
     return best;
 }
 
-static size_t grad_x_part_bytes(int64_t M, int64_t K, int64_t Rn) {
-    size_t n = 0;
+// partials of dX: with splits, or a lifted dX' to fold
+static size_t grad_x_part_bytes(int64_t M, int64_t K, int64_t Rn, bool lifted) {
+    size_t n = lifted ? (size_t)(M * K) * 4 : 0;
     for (int v = 0; v < 2; ++v) {
         const int ks = grad_x_splits(M, K, Rn, v != 0);
         if (ks > 1 && (size_t)ks * (size_t)(M * K) * 4 > n) n = (size_t)ks * (size_t)(M * K) * 4;
@@ -787,23 +814,25 @@ struct GradWs {
     size_t d = 0, dt = 0, xt = 0, wt = 0, part = 0;
     size_t total() const { return d + dt + xt + wt + part; }
 };
-static GradWs grad_ws_layout(int64_t M, int64_t K, int64_t R, int nmat) {
+static int64_t lifted_width(int64_t K, int Ns) { return Ns ? K / (2 * Ns) * 4 * (Ns - 1) : K; }
+static GradWs grad_ws_layout(int64_t M, int64_t Korig, int64_t R, int Ns, int nmat) {
     GradWs w;
-    if (M <= 0 || K <= 0 || R <= 0) return w;
+    if (M <= 0 || Korig <= 0 || R <= 0) return w;
+    const int64_t K = lifted_width(Korig, Ns);
     const int64_t Rn = nmat * up64(R), Mp = up64(M);
     w.d = up256((size_t)(M * Rn * 2));
     w.dt = up256((size_t)(Rn * Mp * 2));
-    w.xt = up256((size_t)(K * Mp * 2));
+    w.xt = up256((size_t)(Korig * Mp * 2));
     if (few_tokens(M)) {
         int spp;
         w.part = up256((size_t)few_splits(K, Rn, &spp) * (size_t)(M * K) * 4);
         return w;
     }
     if (!ring_decodes(M, K, Rn)) w.wt = up256((size_t)(K * Rn * 2));
-    w.part = up256(grad_x_part_bytes(M, K, Rn));
+    w.part = up256(grad_x_part_bytes(M, K, Rn, Ns != 0));
     return w;
 }
-size_t grad_ws(int64_t M, int64_t K, int64_t R, int nmat) { return grad_ws_layout(M, K, R, nmat).total(); }
+size_t grad_ws(int64_t M, int64_t K, int64_t R, int Ns, int nmat) { return grad_ws_layout(M, K, R, Ns, nmat).total(); }
 
 // bytes that every row start is a multiple of: 16, 4 or 2
 static int row_align(const void* p, int64_t ld) {
@@ -818,7 +847,9 @@ __global__ __launch_bounds__(256) void zero_rows_kernel(uint8_t* __restrict__ p,
         *(uint16_t*)(p + (i / width) * ld + (i % width) * 2) = 0;
 }
 
-nm_status launch_grad(const GradIn& in, const GradOut& out, int nmat, void* ws, hipStream_t s) {
+nm_status launch_grad(const GradIn& given, const GradOut& out, int nmat, void* ws, hipStream_t s) {
+    GradIn in = given;
+    in.Kl = lifted_width(in.K, in.Ns);
     if (in.M == 0 || in.R == 0) {
         // an empty sum: dV is zero without tokens, dX without rows
         auto zero = [&](void* p, int64_t rows, int64_t width, int64_t ld) {   // in 2-byte units
@@ -827,12 +858,12 @@ nm_status launch_grad(const GradIn& in, const GradOut& out, int nmat, void* ws, 
                                    (uint8_t*)p, rows, width, ld * 2);
         };
         const int64_t vs = out.dvdt == NM_BF16 ? 1 : 2, xs = out.dxdt == NM_BF16 ? 1 : 2;
-        for (int i = 0; i < nmat; ++i) zero(out.dV[i], in.R, in.K / 2 * vs, out.lddv * vs);
+        for (int i = 0; i < nmat; ++i) zero(out.dV[i], in.R, in.Kl / 2 * vs, out.lddv * vs);
         zero(out.dX, in.M, in.K * xs, out.lddx * xs);
         return check_launch("backward");
     }
     const int64_t Rp = up64(in.R), Rn = nmat * Rp, Mp = up64(in.M);
-    const GradWs w = grad_ws_layout(in.M, in.K, in.R, nmat);
+    const GradWs w = grad_ws_layout(in.M, in.K, in.R, in.Ns, nmat);
     uint8_t* p = (uint8_t*)ws;
     uint16_t* D = (uint16_t*)p;
     uint16_t* DT = (uint16_t*)(p + w.d);
@@ -860,10 +891,10 @@ nm_status launch_grad(const GradIn& in, const GradOut& out, int nmat, void* ws, 
     l.XT = XT;
     l.WT = WT;
     l.td = (int)(Rp / 64);
-    l.tw = (int)ceil_div(in.K, 128);
+    l.tw = (int)ceil_div(in.Kl, 128);
     l.tx = (int)ceil_div(in.K, 64);
     l.nd = l.D || l.DT ? l.td * (int)(Mp / 64) : 0;
-    const bool dec = ring_decodes(in.M, in.K, Rn);
+    const bool dec = ring_decodes(in.M, in.Kl, Rn);
     l.nw = dx && !few_tokens(in.M) && !dec ? l.tw * (int)(Rp / 64) * nmat : 0;
     l.nx = dv ? l.tx * (int)(Mp / 64) : 0;
     const dim3 gl((unsigned)(l.nd + l.nw + l.nx));
@@ -888,27 +919,28 @@ nm_status launch_grad(const GradIn& in, const GradOut& out, int nmat, void* ws, 
         g.idx[i] = in.idx[i];
         g.dV[i] = out.dV[i];
     }
+    g.Ns = in.Ns;
     g.ldv = in.ldv;
     g.ldi = in.ldi;
     g.R = in.R;
     g.Rp = Rp;
     if (dx) {
-        splits = grad_x_splits(in.M, in.K, Rn, dv);
+        splits = grad_x_splits(in.M, in.Kl, Rn, dv);
         GradJob& j = g.x;
         j.A = WT;
         j.lda = Rn;
-        j.rowsA = in.K;
+        j.rowsA = in.Kl;
         j.B = B;
         j.ldb = ldb;
         j.rowsB = in.M;
         j.nsteps = (int)(Rn / 64);
         j.spp = (int)ceil_div(j.nsteps, splits);
         splits = (int)ceil_div(j.nsteps, j.spp);
-        j.tiles_a = (int)ceil_div(in.K, 256);
+        j.tiles_a = (int)ceil_div(in.Kl, 256);
         j.tiles_b = (int)ceil_div(in.M, 256);
         g.nx = j.tiles_a * j.tiles_b * splits;
         g.dX = out.dX;
-        g.part = splits > 1 ? PART : nullptr;
+        g.part = splits > 1 || in.Ns ? PART : nullptr;
         g.lddx = out.lddx;
         g.dxf32 = out.dxdt == NM_F32;
     }
@@ -916,12 +948,12 @@ nm_status launch_grad(const GradIn& in, const GradOut& out, int nmat, void* ws, 
         GradJob& j = g.v;
         j.A = XT;
         j.lda = Mp;
-        j.rowsA = in.K;
+        j.rowsA = in.Kl;
         j.B = DT;
         j.ldb = Mp;
         j.rowsB = Rn;
         j.nsteps = j.spp = (int)(Mp / 64);
-        j.tiles_a = (int)ceil_div(in.K, 256);
+        j.tiles_a = (int)ceil_div(in.Kl, 256);
         j.tiles_b = (int)ceil_div(Rn, 256);
         nv = j.tiles_a * j.tiles_b;
         g.lddv = out.lddv;
@@ -931,15 +963,15 @@ nm_status launch_grad(const GradIn& in, const GradOut& out, int nmat, void* ws, 
         FewArgs f{};
         f.in = in;
         f.M = in.M;
-        f.K = in.K;
+        f.K = in.Kl;
         f.Rn = Rn;
         f.D = B;
         f.ldd = ldb;
-        f.tk = (int)ceil_div(in.K, 128);
+        f.tk = (int)ceil_div(in.Kl, 128);
         f.tr = (int)ceil_div(Rn, 128);
         if (dx) {
-            f.panels = (int)ceil_div(in.K, 128);
-            f.splits = splits = few_splits(in.K, Rn, &f.spp);
+            f.panels = (int)ceil_div(in.Kl, 128);
+            f.splits = splits = few_splits(in.Kl, Rn, &f.spp);
             g.nx = (int)ceil_div(splits, 8) * 8 * f.panels;
             g.part = PART;
         }
@@ -955,7 +987,7 @@ nm_status launch_grad(const GradIn& in, const GradOut& out, int nmat, void* ws, 
     }
     if (g.part)
         hipLaunchKernelGGL(grad_reduce_kernel, dim3(grid_cap(ceil_div(in.M * in.K, 256), 8192)), dim3(256), 0, s, PART,
-                           splits, in.M, in.K, out.dX, out.lddx, g.dxf32);
+                           splits, in.M, in.K, in.Kl, in.Ns, out.dX, out.lddx, g.dxf32);
     return check_launch(nmat == 2 ? "nm_spmm_glu_backward" : "nm_spmm_backward");
 }
 

@@ -755,19 +755,24 @@ static nm_status backward_impl(const char* fn, GradIn in, GradOut out, int nmat,
     const int64_t M = in.M, K = in.K, R = in.R, most = 1 << 21;
     NM_REQ(M >= 0 && K >= 0 && R >= 0, NM_ERR_SHAPE, "%s: negative size", fn);
     NM_REQ(M <= most && K <= most && R <= most, NM_ERR_SHAPE, "%s: sizes up to 2^21", fn);
-    NM_REQ(K % 16 == 0, NM_ERR_SHAPE, "%s: K must be a multiple of 16", fn);
+    const int Ns = in.Ns;
+    NM_REQ(Ns == 0 || (Ns >= 3 && Ns <= 8), NM_ERR_PATTERN,
+           "%s: supported patterns are plain 2:4 (Ns=0) and (2N-2):2N via slide (3 <= Ns <= 8), got Ns=%d", fn, Ns);
+    NM_REQ(Ns == 0 || K % (2 * Ns) == 0, NM_ERR_SHAPE, "%s: K must be a multiple of 2N = %d", fn, 2 * Ns);
+    const int64_t Kl = Ns ? K / (2 * Ns) * 4 * (Ns - 1) : K;
+    NM_REQ(Kl % 16 == 0, NM_ERR_SHAPE, "%s: the (lifted) width %lld must be a multiple of 16", fn, (long long)Kl);
     const bool dv = out.dV[0] != nullptr;
     NM_REQ(nmat == 1 || !out.dV[0] == !out.dV[1], NM_ERR_NULL, "%s: dVg and dVu are both given or both NULL", fn);
     NM_REQ(!out.dX || out.dxdt == NM_BF16 || out.dxdt == NM_F32, NM_ERR_DTYPE, "%s: dX must be bf16 or f32", fn);
     NM_REQ(!dv || out.dvdt == NM_BF16 || out.dvdt == NM_F32, NM_ERR_DTYPE, "%s: dV must be bf16 or f32", fn);
     if (K == 0 || (!out.dX && !dv)) return NM_OK;
     // without tokens dV is zero, without rows dX is: nothing but the outputs is touched then
-    const int64_t iw = (K + 31) / 32;
+    const int64_t iw = (Kl + 31) / 32;
     if (M > 0 && R > 0) {
         NM_REQ(in.dY && (nmat == 1 || (in.G && in.U)) && (in.X || !dv), NM_ERR_NULL, "%s: NULL input", fn);
         for (int i = 0; i < nmat; ++i)
             NM_REQ(in.idx[i] && (in.vals[i] || !out.dX), NM_ERR_NULL, "%s: NULL weight", fn);
-        NM_REQ(in.lddy >= R && (nmat == 1 || in.ldg >= R) && (!dv || in.ldx >= K) && (!out.dX || in.ldv >= K / 2) &&
+        NM_REQ(in.lddy >= R && (nmat == 1 || in.ldg >= R) && (!dv || in.ldx >= K) && (!out.dX || in.ldv >= Kl / 2) &&
                    in.ldi >= iw,
                NM_ERR_SHAPE, "%s: leading dimension too small", fn);
         NM_REQ(((uintptr_t)in.dY & 1u) == 0 && ((uintptr_t)in.G & 1u) == 0 && ((uintptr_t)in.U & 1u) == 0, NM_ERR_ALIGN,
@@ -781,17 +786,17 @@ static nm_status backward_impl(const char* fn, GradIn in, GradOut out, int nmat,
     NM_REQ(!out.dX || (out.lddx >= K && ((uintptr_t)out.dX & (uintptr_t)(xs - 1)) == 0), NM_ERR_SHAPE,
            "%s: lddx < K, or dX not element-aligned", fn);
     for (int i = 0; dv && i < nmat; ++i)
-        NM_REQ(out.lddv >= K / 2 && aligned16(out.dV[i]) && (out.lddv * vs) % 16 == 0, NM_ERR_ALIGN,
-               "%s: dV needs lddv >= K/2 and 16-byte aligned rows", fn);
-    const size_t need = grad_ws(M, K, R, nmat);
+        NM_REQ(out.lddv >= Kl / 2 && aligned16(out.dV[i]) && (out.lddv * vs) % 16 == 0, NM_ERR_ALIGN,
+               "%s: dV needs lddv >= K'/2 and 16-byte aligned rows", fn);
+    const size_t need = grad_ws(M, K, R, Ns, nmat);
     NM_REQ(need == 0 || (ws && ws_bytes >= need), NM_ERR_WORKSPACE, "%s: workspace of %zu bytes needed", fn, need);
     NM_REQ(need == 0 || aligned16(ws), NM_ERR_ALIGN, "%s: ws must be 16-byte aligned", fn);
     const Range rin[] = {span(in.dY, M, R, in.lddy, 2),         span(in.G, M, R, in.ldg, 2),
                          span(in.U, M, R, in.ldg, 2),           span(in.X, M, K, in.ldx, 2),
-                         span(in.vals[0], R, K / 2, in.ldv, 2), span(in.vals[1], R, K / 2, in.ldv, 2),
+                         span(in.vals[0], R, Kl / 2, in.ldv, 2), span(in.vals[1], R, Kl / 2, in.ldv, 2),
                          span(in.idx[0], R, iw, in.ldi, 4),     span(in.idx[1], R, iw, in.ldi, 4)};
-    Range rout[4] = {span(out.dX, M, K, out.lddx, xs), span(out.dV[0], R, K / 2, out.lddv, vs),
-                     span(out.dV[1], R, K / 2, out.lddv, vs), {0, 0}};
+    Range rout[4] = {span(out.dX, M, K, out.lddx, xs), span(out.dV[0], R, Kl / 2, out.lddv, vs),
+                     span(out.dV[1], R, Kl / 2, out.lddv, vs), {0, 0}};
     if (need) rout[3] = Range{(uintptr_t)ws, (uintptr_t)ws + need};
     for (int i = 0; i < 4; ++i) {
         for (const Range& r : rin) NM_REQ(!overlap(rout[i], r), NM_ERR_ALIAS, "%s: an output or ws overlaps an input", fn);
@@ -800,10 +805,15 @@ static nm_status backward_impl(const char* fn, GradIn in, GradOut out, int nmat,
     return launch_grad(in, out, nmat, ws, (hipStream_t)stream);
 }
 
-size_t nm_spmm_backward_workspace(int64_t Mtok, int64_t K, int64_t R) { return grad_ws(Mtok, K, R, 1); }
+static size_t backward_ws(int64_t Mtok, int64_t K, int64_t R, int Ns, int nmat) {
+    const bool ok = Ns == 0 || (Ns >= 3 && Ns <= 8 && K % (2 * Ns) == 0);
+    return ok ? grad_ws(Mtok, K, R, Ns, nmat) : 0;   // the call refuses the others
+}
+
+size_t nm_spmm_backward_workspace(int64_t Mtok, int64_t K, int64_t R, int Ns) { return backward_ws(Mtok, K, R, Ns, 1); }
 
 nm_status nm_spmm_backward(const void* dY, int64_t lddy, const void* X, int64_t ldx, int64_t Mtok, int64_t K,
-                           const void* vals, const uint32_t* idx, int64_t R, int64_t ldv, int64_t ldi, void* dX,
+                           const void* vals, const uint32_t* idx, int64_t R, int64_t ldv, int64_t ldi, int Ns, void* dX,
                            nm_dtype dxdt, int64_t lddx, void* dV, nm_dtype dvdt, int64_t lddv, void* ws,
                            size_t ws_bytes, nm_stream_t stream) {
     GradIn in{};
@@ -818,17 +828,20 @@ nm_status nm_spmm_backward(const void* dY, int64_t lddy, const void* X, int64_t 
     in.idx[0] = idx;
     in.ldv = ldv;
     in.ldi = ldi;
+    in.Ns = Ns;
     GradOut out{dX, dxdt, lddx, {dV, nullptr}, dvdt, lddv};
     return backward_impl("nm_spmm_backward", in, out, 1, ws, ws_bytes, stream);
 }
 
-size_t nm_spmm_glu_backward_workspace(int64_t Mtok, int64_t K, int64_t R) { return grad_ws(Mtok, K, R, 2); }
+size_t nm_spmm_glu_backward_workspace(int64_t Mtok, int64_t K, int64_t R, int Ns) {
+    return backward_ws(Mtok, K, R, Ns, 2);
+}
 
 nm_status nm_spmm_glu_backward(const void* dH, int64_t lddh, const void* G, const void* U, int64_t ldg, nm_act act,
                                const void* X, int64_t ldx, int64_t Mtok, int64_t K, const void* vals_g,
                                const uint32_t* idx_g, const void* vals_u, const uint32_t* idx_u, int64_t R,
-                               int64_t ldv, int64_t ldi, void* dX, nm_dtype dxdt, int64_t lddx, void* dVg, void* dVu,
-                               nm_dtype dvdt, int64_t lddv, void* ws, size_t ws_bytes, nm_stream_t stream) {
+                               int64_t ldv, int64_t ldi, int Ns, void* dX, nm_dtype dxdt, int64_t lddx, void* dVg,
+                               void* dVu, nm_dtype dvdt, int64_t lddv, void* ws, size_t ws_bytes, nm_stream_t stream) {
     NM_REQ(act_ok(act), NM_ERR_SHAPE, "nm_spmm_glu_backward: unknown activation");
     GradIn in{};
     in.dY = (const uint16_t*)dH;
@@ -848,6 +861,7 @@ nm_status nm_spmm_glu_backward(const void* dH, int64_t lddh, const void* G, cons
     in.idx[1] = idx_u;
     in.ldv = ldv;
     in.ldi = ldi;
+    in.Ns = Ns;
     GradOut out{dX, dxdt, lddx, {dVg, dVu}, dvdt, lddv};
     return backward_impl("nm_spmm_glu_backward", in, out, 2, ws, ws_bytes, stream);
 }

@@ -333,7 +333,7 @@ struct GluIn {
 };
 size_t glu_ws(int64_t Mtok, int64_t K, int64_t R, int Ns, nm_dtype xdt);
 nm_status launch_glu(const GluIn& g, void* ws, hipStream_t s);
-// gradients of the sparse layer (G null) and of the gated block (bf16, plain 2:4)
+// gradients of the sparse layer (G null) and of the gated block (bf16, 2:4 or lifted)
 struct GradIn {
     const uint16_t* dY;   // dY, or dH of the gated block: [M, R] (lddy)
     int64_t lddy;
@@ -345,6 +345,8 @@ struct GradIn {
     const uint16_t* vals[2];
     const uint32_t* idx[2];
     int64_t ldv, ldi;
+    int Ns;
+    int64_t Kl;   // lifted width (set by launch_grad)
 };
 struct GradOut {
     void* dX;   // null: not wanted
@@ -354,7 +356,7 @@ struct GradOut {
     nm_dtype dvdt;
     int64_t lddv;
 };
-size_t grad_ws(int64_t M, int64_t K, int64_t R, int nmat);
+size_t grad_ws(int64_t M, int64_t K, int64_t R, int Ns, int nmat);
 // nmat: 1, or 2 for the gated block
 nm_status launch_grad(const GradIn& in, const GradOut& out, int nmat, void* ws, hipStream_t s);
 // optimiser

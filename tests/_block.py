@@ -73,15 +73,17 @@ def weight(g, R, K, Ns=0, scale=0.05, integer=False, dtype="bf16"):
     return dense, v.to(dev()), torch.from_numpy(np.ascontiguousarray(idx).view(np.int32)).to(dev())
 
 
-def columns(idx, K):
-    """Column of every packed value of a 2:4 weight: [R, K/2]."""
+def columns(idx, K, Ns=0):
+    """Column of every packed value: [R, K/2], or [R, K'/2] of a lifted weight."""
     w = idx.cpu().numpy().view(np.uint32)
-    j = np.arange(K // 2)
-    return 4 * (j // 2)[None] + ((w[:, j // 16] >> (2 * (j % 16)).astype(np.uint32)[None]) & 3).astype(np.int64)
+    j = np.arange((O.lifted_width(K, Ns) if Ns else K) // 2)
+    win = j // 2
+    start = 2 * Ns * (win // (Ns - 1)) + 2 * (win % (Ns - 1)) if Ns else 4 * win
+    return start[None] + ((w[:, j // 16] >> (2 * (j % 16)).astype(np.uint32)[None]) & 3).astype(np.int64)
 
 
-def take(full, idx, K):
-    return np.take_along_axis(full, columns(idx, K), axis=1)
+def take(full, idx, K, Ns=0):
+    return np.take_along_axis(full, columns(idx, K, Ns), axis=1)
 
 
 def strided(t, extra):

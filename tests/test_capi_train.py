@@ -75,7 +75,7 @@ def _bwd(nm, two=False, **kw):
     a.update(X=X, ldx=64, M=4, K=64, vg=VG, ig=IG)
     if two:
         a.update(vu=VU, iu=IU)
-    a.update(R=8, ldv=32, ldi=2, dX=P(11 << 32), dxdt=1, lddx=64, dV=P(12 << 32))
+    a.update(R=8, ldv=32, ldi=2, Ns=0, dX=P(11 << 32), dxdt=1, lddx=64, dV=P(12 << 32))
     if two:
         a.update(dVu=P(13 << 32))
     a.update(dvdt=1, lddv=32, ws=WS, n=BIG)
@@ -88,6 +88,9 @@ def _bwd(nm, two=False, **kw):
 def test_backward_refuses(nm, two):
     b = lambda **kw: _bwd(nm, two, **kw)  # noqa: E731
     assert b(K=40) == "NM_ERR_SHAPE" and b(M=-1) == "NM_ERR_SHAPE" and b(M=(1 << 21) + 1) == "NM_ERR_SHAPE"
+    assert b(Ns=2) == "NM_ERR_PATTERN" and b(Ns=9) == "NM_ERR_PATTERN" and b(Ns=-1) == "NM_ERR_PATTERN"
+    assert b(Ns=5) == "NM_ERR_SHAPE" and b(Ns=4, K=80, ldx=80) == "NM_ERR_SHAPE"      # 64 % 10, 120 % 16
+    assert b(Ns=4, ldv=47) in ("NM_ERR_SHAPE", "NM_ERR_ALIGN") and b(Ns=4, lddv=32, ldv=48, ldi=3) == "NM_ERR_ALIGN"
     assert b(dxdt=2) == "NM_ERR_DTYPE" and b(dvdt=4) == "NM_ERR_DTYPE"
     for k in ["dY", "X", "vg", "ig"] + (["G", "U", "vu", "iu"] if two else []):
         assert b(**{k: None}) == "NM_ERR_NULL", k
@@ -113,12 +116,14 @@ def test_backward_nothing_to_do(nm, two):
 
 def test_backward_workspace(nm):
     one, two = nm.raw.nm_spmm_backward_workspace, nm.raw.nm_spmm_glu_backward_workspace
-    assert one(0, 64, 8) == 0 and two(4, 64, 0) == 0
+    assert one(0, 64, 8, 0) == 0 and two(4, 64, 0, 0) == 0
     # the transposed operands and the dense transposed weights of many tokens
     M, K, R = 2048, 4096, 11008
-    assert two(M, K, R) >= 2 * (2 * M * R * 2) + K * M * 2 + K * 2 * R * 2
+    assert two(M, K, R, 0) >= 2 * (2 * M * R * 2) + K * M * 2 + K * 2 * R * 2
+    # a lifted dX is folded from f32
+    assert two(M, K, R, 4) >= M * K * 3 // 2 * 4 and two(M, K, R, 2) == 0
     # few tokens stream the packed weight: no dense copy of it
-    assert two(8, K, R) < K * 2 * R * 2
+    assert two(8, K, R, 0) < K * 2 * R * 2
 
 
 def _adamw(nm, n=300, sdt=0, lr=1e-3, b1=0.9, b2=0.999, eps=1e-8, step=1, gs=None, count=1, **kw):

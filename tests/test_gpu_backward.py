@@ -44,7 +44,7 @@ def test_backward_integers_exact(nm, Mt, R, K, extra):
     W, v, i = B.weight(g, R, K, integer=True)
     if extra:
         dY, X, v, i = B.strided(dY, extra), B.strided(X, 16), B.strided(v, 16), B.strided(i, extra)
-    ws = B.nan_ws(nm.raw.nm_spmm_backward_workspace(Mt, K, R))
+    ws = B.nan_ws(nm.raw.nm_spmm_backward_workspace(Mt, K, R, 0))
     dX, dV = nm.nm_spmm_backward(dY, X, v, i, dxdt=nm.NM_F32, dvdt=nm.NM_F32, ws=ws)
     assert np.array_equal(_np(dX), dYf @ W)
     assert np.array_equal(_np(dV), B.take(dYf.T @ Xf, i.contiguous(), K))
@@ -82,7 +82,7 @@ def test_glu_backward_integers_exact(nm, Mt, R, K, extra):
         vg, vu, ig, iu = B.strided(vg, 8), B.strided(vu, 8), B.strided(ig, extra), B.strided(iu, extra)
     f, d, _ = B.act(B.RELU2, Gf)
     dG, dU = dHf * Uf * d, dHf * f
-    ws = B.nan_ws(nm.raw.nm_spmm_glu_backward_workspace(Mt, K, R))
+    ws = B.nan_ws(nm.raw.nm_spmm_glu_backward_workspace(Mt, K, R, 0))
     dX, dVg, dVu = nm.nm_spmm_glu_backward(dH, G, U, X, vg, ig, vu, iu, act=B.RELU2, dxdt=nm.NM_F32, dvdt=nm.NM_F32, ws=ws)
     assert np.array_equal(_np(dX), dG @ Wg + dU @ Wu)
     assert np.array_equal(_np(dVg), B.take(dG.T @ Xf, ig.contiguous(), K))
@@ -92,6 +92,91 @@ def test_glu_backward_integers_exact(nm, Mt, R, K, extra):
     assert n1 is None and n2 is None and torch.equal(only, dX.to(torch.bfloat16))
     n1, a, b = nm.nm_spmm_glu_backward(dH, G, U, X, vg, ig, vu, iu, act=B.RELU2, want_dx=False, ws=ws)
     assert n1 is None and torch.equal(a, dVg.to(torch.bfloat16)) and torch.equal(b, dVu.to(torch.bfloat16))
+
+
+# (2N-2):2N weights: every N, tokens on both sides of each kernel's range, the last two decoded by
+# dX's tiles; row lengths that are no multiple of 8 among them (N = 3, 5, 7)
+LIFTED = [(3, 1, 40, 12), (3, 140, 130, 540), (4, 17, 33, 224), (4, 300, 257, 512), (5, 64, 70, 170), (5, 520, 260, 1310),
+          (6, 33, 100, 528), (6, 700, 200, 480), (7, 100, 130, 308), (7, 800, 120, 644), (8, 128, 65, 448), (8, 200, 90, 320),
+          (4, 130, 6161, 2080), (7, 300, 4100, 2548)]
+
+
+@pytest.mark.parametrize("Ns,Mt,R,K", LIFTED)
+@pytest.mark.parametrize("extra", [0, 8])
+def test_lifted_backward_integers_exact(nm, Ns, Mt, R, K, extra):
+    g = np.random.default_rng(Ns + Mt + R + K + extra)
+    dY, dYf = _rand(g, (Mt, R), integer=2)
+    X, Xf = _rand(g, (Mt, K), integer=2)
+    W, v, i = B.weight(g, R, K, Ns=Ns, integer=True)
+    X = B.strided(X, 8 - K % 8 if K % 8 else extra)      # rows of 16-byte alignment
+    if extra:
+        dY, v, i = B.strided(dY, extra), B.strided(v, 16), B.strided(i, extra)
+    ws = B.nan_ws(nm.raw.nm_spmm_backward_workspace(Mt, K, R, Ns))
+    dX, dV = nm.nm_spmm_backward(dY, X, v, i, Ns=Ns, dxdt=nm.NM_F32, dvdt=nm.NM_F32, ws=ws)
+    assert np.array_equal(_np(dX), dYf @ W)
+    assert np.array_equal(_np(dV), B.take(dYf.T @ Xf, i.contiguous(), K, Ns))
+    ws.fill_(0xFF)
+    dX2, dV2 = nm.nm_spmm_backward(dY, X, v, i, Ns=Ns, ws=ws)
+    assert torch.equal(dX2, dX.to(torch.bfloat16)) and torch.equal(dV2, dV.to(torch.bfloat16))
+    only, n1 = nm.nm_spmm_backward(dY, X, v, i, Ns=Ns, want_dv=False, ws=ws)
+    assert n1 is None and torch.equal(only, dX2)
+
+
+@pytest.mark.parametrize("Ns,Mt,R,K", LIFTED)
+def test_lifted_glu_backward_integers_exact(nm, Ns, Mt, R, K):
+    g = np.random.default_rng(Ns + Mt + R + K)
+    dH, dHf = _rand(g, (Mt, R), integer=1)
+    G, Gf = _rand(g, (Mt, R), integer=4)
+    U, Uf = _rand(g, (Mt, R), integer=4)
+    X, Xf = _rand(g, (Mt, K), integer=2)
+    X = B.strided(X, -K % 8)
+    Wg, vg, ig = B.weight(g, R, K, Ns=Ns, integer=True)
+    Wu, vu, iu = B.weight(g, R, K, Ns=Ns, integer=True)
+    f, d, _ = B.act(B.RELU2, Gf)
+    dG, dU = dHf * Uf * d, dHf * f
+    ws = B.nan_ws(nm.raw.nm_spmm_glu_backward_workspace(Mt, K, R, Ns))
+    dX, dVg, dVu = nm.nm_spmm_glu_backward(dH, G, U, X, vg, ig, vu, iu, Ns=Ns, act=B.RELU2, dxdt=nm.NM_F32,
+                                           dvdt=nm.NM_F32, ws=ws)
+    assert np.array_equal(_np(dX), dG @ Wg + dU @ Wu)
+    assert np.array_equal(_np(dVg), B.take(dG.T @ Xf, ig, K, Ns))
+    assert np.array_equal(_np(dVu), B.take(dU.T @ Xf, iu, K, Ns))
+
+
+def test_lifted_backward_adds_windows(nm):
+    """Two slots may place a value at one column: dX sees their sum, and each slot has the
+    column's derivative."""
+    Ns, Mt, R, K = 4, 3, 8, 32
+    g = np.random.default_rng(12)
+    dY, dYf = _rand(g, (Mt, R), integer=2)
+    X, Xf = _rand(g, (Mt, K), integer=2)
+    v, vf = _rand(g, (R, O.lifted_width(K, Ns) // 2), integer=3)
+    # pairs of ascending positions in every window
+    pairs = np.array([(a, b) for a in range(4) for b in range(a + 1, 4)])[g.integers(0, 6, (R, 12))].reshape(R, 24)
+    words = np.zeros((R, 2), np.uint32)
+    for j in range(24):
+        words[:, j // 16] |= (pairs[:, j].astype(np.uint32) << np.uint32(2 * (j % 16)))
+    i = torch.from_numpy(words.view(np.int32)).to(dev())
+    cols = B.columns(i, K, Ns)
+    W = np.zeros((R, K))
+    np.add.at(W, (np.arange(R)[:, None], cols), vf)
+    assert any(len(set(c)) < len(c) for c in cols)
+    dX, dV = nm.nm_spmm_backward(dY, X, v, i, Ns=Ns, dxdt=nm.NM_F32, dvdt=nm.NM_F32)
+    assert np.array_equal(_np(dX), dYf @ W)
+    assert np.array_equal(_np(dV), np.take_along_axis(dYf.T @ Xf, cols, axis=1))
+    assert np.array_equal(_np(nm.nm_spmm(X, v, i, Ns=Ns, ydt=nm.NM_F32)), Xf @ W.T)
+
+
+@pytest.mark.parametrize("Ns,Mt,R,K", [(4, 20, 300, 512), (5, 700, 200, 640)])
+def test_lifted_backward_random(nm, Ns, Mt, R, K):
+    g = np.random.default_rng(Mt)
+    dY, dYf = _rand(g, (Mt, R), 0.1)
+    X, Xf = _rand(g, (Mt, K))
+    W, v, i = B.weight(g, R, K, Ns=Ns)
+    dX, dV = nm.nm_spmm_backward(dY, X, v, i, Ns=Ns, dxdt=nm.NM_F32, dvdt=nm.NM_F32)
+    # a column's two windows are one sum more
+    assert (np.abs(_np(dX) - dYf @ W) <= (R + 17) * 2.0 ** -24 * (np.abs(dYf) @ np.abs(W)) + 1e-37).all()
+    tol = (Mt + 16) * 2.0 ** -24 * (np.abs(dYf).T @ np.abs(Xf)) + 1e-37
+    assert (np.abs(_np(dV) - B.take(dYf.T @ Xf, i, K, Ns)) <= B.take(tol, i, K, Ns)).all()
 
 
 def _operands(a, dHf, Gf, Uf):
@@ -241,7 +326,7 @@ def test_backward_runs_twice_alike_on_other_streams_and_in_a_graph(nm):
     torch.cuda.synchronize()
     assert all(torch.equal(x, y) for x, y in zip(ref, again))
     outs = [torch.empty_like(t) for t in ref]
-    ws = B.nan_ws(nm.raw.nm_spmm_glu_backward_workspace(Mt, K, R))
+    ws = B.nan_ws(nm.raw.nm_spmm_glu_backward_workspace(Mt, K, R, 0))
     graph = torch.cuda.CUDAGraph()
     with torch.cuda.graph(graph):
         nm.nm_spmm_glu_backward(dY, G, dY, X, v, i, v, i, out_dx=outs[0], out_dv=(outs[1], outs[2]), ws=ws)

@@ -10,7 +10,7 @@ import torch
 pytestmark = pytest.mark.gpu
 
 
-def _reference(width, hidden, tokens, steps, lr, seed):
+def _reference(width, hidden, tokens, steps, lr, seed, Ns):
     """Masked dense weights, f32 throughout, on the example's random numbers."""
     dev = torch.device("cuda")
     g = torch.Generator(device=dev)
@@ -20,8 +20,8 @@ def _reference(width, hidden, tokens, steps, lr, seed):
              "d": rand(width, hidden) * hidden ** -0.5}
     mask, param = {}, {}
     for k, w in dense.items():
-        a = w.view(w.shape[0], -1, 4).abs()
-        mask[k] = torch.zeros_like(a).scatter_(-1, a.topk(2, -1).indices, 1.0).view_as(w)
+        a = w.view(w.shape[0], -1, 2 * Ns if Ns else 4).abs()
+        mask[k] = torch.zeros_like(a).scatter_(-1, a.topk(2 * Ns - 2 if Ns else 2, -1).indices, 1.0).view_as(w)
         param[k] = (w * mask[k]).to(torch.bfloat16).float().requires_grad_()
     opt = torch.optim.AdamW(list(param.values()), lr=lr, betas=(0.9, 0.999), weight_decay=0.0)
     mix = rand(width // 8, width) * (width // 8) ** -0.5
@@ -48,12 +48,13 @@ def _reference(width, hidden, tokens, steps, lr, seed):
     return before, loss(*held).item()
 
 
-def test_training_follows_the_masked_dense_block():
+@pytest.mark.parametrize("Ns", [0, 4])
+def test_training_follows_the_masked_dense_block(Ns):
     path = Path(__file__).resolve().parents[1] / "examples" / "train_pruned_block.py"
     spec = importlib.util.spec_from_file_location("train_pruned_block", path)
     example = importlib.util.module_from_spec(spec)
     spec.loader.exec_module(example)
-    size = dict(width=256, hidden=704, tokens=256, steps=40, lr=5e-4, seed=3)
+    size = dict(width=256, hidden=704, tokens=256, steps=40, lr=5e-4, seed=3, Ns=Ns)
     before, after, one, many = example.train(**size)
     ref_before, ref_after = _reference(**size)
     assert abs(before - ref_before) < 0.02 * ref_before
