@@ -7,7 +7,8 @@
 //   dV[r, j] = sum_m dY[m, r] X[m, col(r, j)]   for the kept positions col(r, j) only.
 // A (2N-2):2N weight is a plain 2:4 one over the lifted width K' (lifted column 4 w + j of window
 // w reads column orig of X): dV reads X's rows by that map, dX' is formed over K' and folded, each
-// column's lifted ones (two at most) added in f32.
+// column's lifted ones (two at most) added in f32, except where dX has a dense copy of the weights
+// to read, which is made over K.
 // Neither product can use the sparse instructions: they skip zeros of the operand along the
 // summed dimension, W is 2:4 along K, but dX sums over R and dV over the tokens.  Both run as
 // dense products on 256 x 256 tiles (grad_ring_kernel), bound by the matrix
@@ -111,6 +112,13 @@ __device__ __forceinline__ int64_t orig_col(int64_t k, int Ns) {
     return (int64_t)(2 * (n + 1) * g + 2 * (w - g * n)) + (k & 3);
 }
 
+// Groups of a lifted weight in a tile of its dense copy: the most whose windows fit 128 lifted
+// columns and end at a multiple of 16.
+__host__ __device__ inline int lifted_tile_groups(int Ns) { return (32 / (Ns - 1)) & ~3; }
+// Lifted columns over column p of a group: window w's is 4 w + p - 2 w, for first <= w <= last.
+__device__ __forceinline__ int first_window(int p) { return p > 3 ? (p - 2) / 2 : 0; }
+__device__ __forceinline__ int last_window(int p, int Ns) { return p / 2 < Ns - 2 ? p / 2 : Ns - 2; }
+
 struct LayoutArgs {
     GradIn in;
     int64_t Rp, Mp, Rn;
@@ -195,10 +203,14 @@ __device__ __forceinline__ void glu_grad_tile(PairTile& tile, const LayoutArgs& 
 // 64 rows x 128 columns of a packed 2:4 weight (a line of values per row) -> WT [K, Rn] at columns
 // off + r (rows past R: zero).  Thread (c, pair): rows 2 pair, 2 pair + 1, columns 16 c ..: 8
 // values and 16 bits of positions per row; K is a multiple of 16.
+// A lifted weight's copy has the original columns (a third to an eighth fewer): a tile holds whole
+// groups, and a column under two windows is their sum, rounded to bf16 (exact where one of them is
+// zero, as in any decomposed weight).
 __device__ __forceinline__ void decode_tile(PairTile& tile, SpreadTable& table, const LayoutArgs& a, int mat, int ti, int tj) {
     const GradIn& in = a.in;
     const int tid = threadIdx.x, c = tid & 7, pair = tid >> 3;
-    const int64_t r0 = (int64_t)ti * 64, k0 = (int64_t)tj * 128, k = k0 + 16 * c;
+    const int Ns = in.Ns, groups = Ns ? lifted_tile_groups(Ns) : 0, width = Ns ? groups * 4 * (Ns - 1) : 128;
+    const int64_t r0 = (int64_t)ti * 64, k0 = (int64_t)tj * width, k = k0 + 16 * c;
     table.fill(tid);
     __syncthreads();
     uint4 v[2];
@@ -206,14 +218,33 @@ __device__ __forceinline__ void decode_tile(PairTile& tile, SpreadTable& table, 
 #pragma unroll
     for (int j = 0; j < 2; ++j) {
         const int64_t r = r0 + 2 * pair + j;
-        const bool ok = r < in.R && k < in.Kl;
+        const bool ok = r < in.R && k < in.Kl && 16 * c < width;
         v[j] = ok ? *(const uint4*)(in.vals[mat] + r * in.ldv + k / 2) : make_uint4(0, 0, 0, 0);
-        b[j] = ok ? in.idx[mat][r * in.ldi + k / 32] >> (16 * (c & 1)) : 0u;
+        b[j] = ok ? in.idx[mat][r * in.ldi + k / 32] >> (k & 16) : 0u;
     }
     decode_pair16(table, v[0], b[0], v[1], b[1], x);
 #pragma unroll
     for (int e = 0; e < 16; ++e) tile.put(c * 16 + e, pair, x[e]);
     __syncthreads();
+    if (Ns) {
+        const int span = groups * 2 * Ns, q = tid & 7;
+        const int64_t o0 = (int64_t)tj * span;
+        for (int col = tid >> 3; col < span && o0 + col < in.K; col += 32) {
+            const int g = col / (2 * Ns), p = col - g * 2 * Ns, w0 = first_window(p), w1 = last_window(p, Ns);
+            const int l0 = 4 * (g * (Ns - 1) + w0) + p - 2 * w0;
+            uint4 u = tile.get(l0, q);
+            if (w1 > w0) {   // the next window's column is two on
+                const uint4 v = tile.get(l0 + 2, q);
+                auto add = [](uint32_t a, uint32_t b) {
+                    return f32_to_bf16_pair(bf16_bits_to_f32(a & 0xffffu) + bf16_bits_to_f32(b & 0xffffu),
+                                            bf16_bits_to_f32(a >> 16) + bf16_bits_to_f32(b >> 16));
+                };
+                u = make_uint4(add(u.x, v.x), add(u.y, v.y), add(u.z, v.z), add(u.w, v.w));
+            }
+            *(uint4*)(a.WT + (o0 + col) * a.Rn + mat * a.Rp + r0 + 8 * q) = u;
+        }
+        return;
+    }
 #pragma unroll
     for (int p = 0; p < 4; ++p) {
         const int col = (tid >> 3) + 32 * p, q = tid & 7;
@@ -745,9 +776,8 @@ __global__ __launch_bounds__(256) void grad_reduce_kernel(const float* __restric
             v = split_sum(part + t, splits, total);
         } else {
             const int g = (int)((uint32_t)k / (uint32_t)(2 * Ns)), p = (int)k - g * 2 * Ns;
-            const int last = p / 2 < Ns - 2 ? p / 2 : Ns - 2;   // windows that cover p start at 2 w in p - 3 .. p
             v = 0.0f;
-            for (int w = p > 3 ? (p - 2) / 2 : 0; w <= last; ++w)
+            for (int w = first_window(p); w <= last_window(p, Ns); ++w)
                 v += split_sum(part + m * Kl + 4 * (g * (Ns - 1) + w) + p - 2 * w, splits, M * Kl);
         }
         if (f32) ((float*)dX)[m * lddx + k] = v;
@@ -778,7 +808,7 @@ static int grad_x_splits(int64_t M, int64_t K, int64_t Rn, bool with_v) {
     return best;
 }
 
-// partials of dX: with splits, or a lifted dX' to fold
+// partials of dX over K columns: with splits, or a lifted dX' to fold
 static size_t grad_x_part_bytes(int64_t M, int64_t K, int64_t Rn, bool lifted) {
     size_t n = lifted ? (size_t)(M * K) * 4 : 0;
     for (int v = 0; v < 2; ++v) {
@@ -828,8 +858,9 @@ static GradWs grad_ws_layout(int64_t M, int64_t Korig, int64_t R, int Ns, int nm
         w.part = up256((size_t)few_splits(K, Rn, &spp) * (size_t)(M * K) * 4);
         return w;
     }
-    if (!ring_decodes(M, K, Rn)) w.wt = up256((size_t)(K * Rn * 2));
-    w.part = up256(grad_x_part_bytes(M, K, Rn, Ns != 0));
+    const bool dec = ring_decodes(M, K, Rn);
+    if (!dec) w.wt = up256((size_t)(Korig * Rn * 2));
+    w.part = up256(grad_x_part_bytes(M, dec ? K : Korig, Rn, dec && Ns != 0));
     return w;
 }
 size_t grad_ws(int64_t M, int64_t K, int64_t R, int Ns, int nmat) { return grad_ws_layout(M, K, R, Ns, nmat).total(); }
@@ -891,10 +922,11 @@ nm_status launch_grad(const GradIn& given, const GradOut& out, int nmat, void* w
     l.XT = XT;
     l.WT = WT;
     l.td = (int)(Rp / 64);
-    l.tw = (int)ceil_div(in.Kl, 128);
+    l.tw = (int)ceil_div(in.Kl, in.Ns ? lifted_tile_groups(in.Ns) * 4 * (in.Ns - 1) : 128);
     l.tx = (int)ceil_div(in.K, 64);
     l.nd = l.D || l.DT ? l.td * (int)(Mp / 64) : 0;
-    const bool dec = ring_decodes(in.M, in.Kl, Rn);
+    const bool dec = !few_tokens(in.M) && ring_decodes(in.M, in.Kl, Rn);
+    const int64_t Kx = few_tokens(in.M) || dec ? in.Kl : in.K;   // columns of dX's product
     l.nw = dx && !few_tokens(in.M) && !dec ? l.tw * (int)(Rp / 64) * nmat : 0;
     l.nx = dv ? l.tx * (int)(Mp / 64) : 0;
     const dim3 gl((unsigned)(l.nd + l.nw + l.nx));
@@ -925,22 +957,22 @@ nm_status launch_grad(const GradIn& given, const GradOut& out, int nmat, void* w
     g.R = in.R;
     g.Rp = Rp;
     if (dx) {
-        splits = grad_x_splits(in.M, in.Kl, Rn, dv);
+        splits = grad_x_splits(in.M, Kx, Rn, dv);
         GradJob& j = g.x;
         j.A = WT;
         j.lda = Rn;
-        j.rowsA = in.Kl;
+        j.rowsA = Kx;
         j.B = B;
         j.ldb = ldb;
         j.rowsB = in.M;
         j.nsteps = (int)(Rn / 64);
         j.spp = (int)ceil_div(j.nsteps, splits);
         splits = (int)ceil_div(j.nsteps, j.spp);
-        j.tiles_a = (int)ceil_div(in.Kl, 256);
+        j.tiles_a = (int)ceil_div(Kx, 256);
         j.tiles_b = (int)ceil_div(in.M, 256);
         g.nx = j.tiles_a * j.tiles_b * splits;
         g.dX = out.dX;
-        g.part = splits > 1 || in.Ns ? PART : nullptr;
+        g.part = splits > 1 || Kx != in.K ? PART : nullptr;
         g.lddx = out.lddx;
         g.dxf32 = out.dxdt == NM_F32;
     }
@@ -987,7 +1019,7 @@ nm_status launch_grad(const GradIn& given, const GradOut& out, int nmat, void* w
     }
     if (g.part)
         hipLaunchKernelGGL(grad_reduce_kernel, dim3(grid_cap(ceil_div(in.M * in.K, 256), 8192)), dim3(256), 0, s, PART,
-                           splits, in.M, in.K, in.Kl, in.Ns, out.dX, out.lddx, g.dxf32);
+                           splits, in.M, in.K, Kx, Kx != in.K ? in.Ns : 0, out.dX, out.lddx, g.dxf32);
     return check_launch(nmat == 2 ? "nm_spmm_glu_backward" : "nm_spmm_backward");
 }
 
