@@ -837,7 +837,11 @@ static int few_splits(int64_t K, int64_t Rn, int* spp) {
 // Measured on the gated block's backward at 11008 x 4096: 129 tokens 193 -> 137 us, 256
 // 211 -> 158, 512 297 -> 257, 768 391 -> 357, 1024 464 -> 462, 2048 767 -> 865; on small weights the longer
 // stages cost more than the copy (4096 x 1024 at 256 tokens 37.1 -> 40.2, 5504 x 2048 73 -> 59).
-static bool ring_decodes(int64_t M, int64_t K, int64_t Rn) { return M <= 3 * 256 && K * Rn >= ((int64_t)1 << 24); }
+// A lifted weight's copy is over K, the decoded tiles over K': 6:8 at 256 tokens 267 -> 204 us, 512
+// 363 -> 343, 768 463 -> 476; 8:10 (K = 4160) 267 -> 223, 370 -> 359, 473 -> 502.
+static bool ring_decodes(int64_t M, int64_t K, int64_t Rn, int Ns) {
+    return M <= (Ns ? 2 : 3) * 256 && K * Rn >= ((int64_t)1 << 24);
+}
 
 // Workspace of one backward call, in the order it is carved.
 struct GradWs {
@@ -858,7 +862,7 @@ static GradWs grad_ws_layout(int64_t M, int64_t Korig, int64_t R, int Ns, int nm
         w.part = up256((size_t)few_splits(K, Rn, &spp) * (size_t)(M * K) * 4);
         return w;
     }
-    const bool dec = ring_decodes(M, K, Rn);
+    const bool dec = ring_decodes(M, K, Rn, Ns);
     if (!dec) w.wt = up256((size_t)(Korig * Rn * 2));
     w.part = up256(grad_x_part_bytes(M, dec ? K : Korig, Rn, dec && Ns != 0));
     return w;
@@ -925,7 +929,7 @@ nm_status launch_grad(const GradIn& given, const GradOut& out, int nmat, void* w
     l.tw = (int)ceil_div(in.Kl, in.Ns ? lifted_tile_groups(in.Ns) * 4 * (in.Ns - 1) : 128);
     l.tx = (int)ceil_div(in.K, 64);
     l.nd = l.D || l.DT ? l.td * (int)(Mp / 64) : 0;
-    const bool dec = !few_tokens(in.M) && ring_decodes(in.M, in.Kl, Rn);
+    const bool dec = !few_tokens(in.M) && ring_decodes(in.M, in.Kl, Rn, in.Ns);
     const int64_t Kx = few_tokens(in.M) || dec ? in.Kl : in.K;   // columns of dX's product
     l.nw = dx && !few_tokens(in.M) && !dec ? l.tw * (int)(Rp / 64) * nmat : 0;
     l.nx = dv ? l.tx * (int)(Mp / 64) : 0;
