@@ -402,20 +402,21 @@ def _raw_stream(t: torch.Tensor) -> int:
     return torch._C._cuda_getCurrentRawStream(t.device.index)
 
 
-def _rows(t: torch.Tensor) -> bool:
-    """2-D with unit stride along the last dimension."""
-    return t.dim() == 2 and (t.stride(1) == 1 or t.shape[1] <= 1)
+def _mat(t: torch.Tensor):
+    """(rows, columns, leading dimension) of a row-major 2-D view (a one-row view's may be
+    anything), or None.  Each property of a tensor costs about 0.1 us and these calls are short:
+    they are read once."""
+    shape, stride = t.shape, t.stride()
+    if len(shape) != 2 or (stride[1] != 1 and shape[1] > 1):
+        return None
+    r, c = shape
+    return r, c, stride[0] if r > 1 else max(stride[0], c)
 
 
-def _ld2(t: torch.Tensor) -> int:
-    """Leading dimension of a 2-D row-major view; a one-row view's may be anything."""
-    return t.stride(0) if t.shape[0] > 1 else max(t.stride(0), t.shape[1])
-
-
-def _need(need: int, ws: torch.Tensor | None, device) -> torch.Tensor | None:
+def _need(need: int, ws: torch.Tensor | None, like: torch.Tensor) -> torch.Tensor | None:
     """The caller's workspace where it has need bytes, else a new one."""
-    if need and (ws is None or ws.numel() * ws.element_size() < need):
-        ws = torch.empty(need, dtype=torch.uint8, device=device)
+    if need and (ws is None or ws.nbytes < need):
+        ws = like.new_empty(need, dtype=torch.uint8)
     return ws
 
 
@@ -437,78 +438,78 @@ def nm_spmm_glu(X: torch.Tensor, vals_g: torch.Tensor, idx_g: torch.Tensor, vals
                 ws: torch.Tensor | None = None):
     """H = act(G) . U with G = X Wg^T and U = X Wu^T on packed weights, in one pass: H, or with
     save (H, G, U), the bf16 pre-activations that nm_spmm_glu_backward takes."""
-    if not (_rows(X) and _rows(vals_g) and _rows(idx_g) and vals_u.shape == vals_g.shape and idx_u.shape == idx_g.shape and
-            vals_u.stride() == vals_g.stride() and idx_u.stride() == idx_g.stride() and
+    x, v, i, dev = _mat(X), _mat(vals_g), _mat(idx_g), X.device
+    if not (x and v and i and v == _mat(vals_u) and i == _mat(idx_u) and
             vals_g.dtype == X.dtype == vals_u.dtype and idx_g.dtype == torch.int32 == idx_u.dtype and X.dtype in _DT and
-            X.device == vals_g.device == idx_g.device == vals_u.device == idx_u.device):
+            dev == vals_g.device and dev == idx_g.device and dev == vals_u.device and dev == idx_u.device):
         _refuse("X must be row-major and the gate and up weights packed alike, in X's type", X=X, vals_g=vals_g,
                 idx_g=idx_g, vals_u=vals_u, idx_u=idx_u)
-    Mtok, K = X.shape
-    R, slots = vals_g.shape
+    (Mtok, K, ldx), (R, slots, ldv), (irows, words, ldi) = x, v, i
     Kl = lifted_width(K, Ns) if Ns >= 2 else K
-    if slots < Kl // 2 or idx_g.shape[0] != R or idx_g.shape[1] < (Kl + 31) // 32:
+    if slots < Kl // 2 or irows != R or words < (Kl + 31) // 32:
         _refuse(f"{Kl // 2} values and {(Kl + 31) // 32} index words per row are needed", vals=vals_g, idx=idx_g)
     if x_scale is not None and not (x_scale.dtype == torch.float32 and x_scale.numel() == Mtok and x_scale.is_contiguous()
-                                    and x_scale.device == X.device):
+                                    and x_scale.device == dev):
         _refuse(f"x_scale must be {Mtok} contiguous f32 values", x_scale=x_scale)
     xdt = _DT[X.dtype]
     if out is None:
         hdt = NM_BF16 if hdt is None else hdt
-        H = torch.empty((Mtok, R), dtype=_TORCH[hdt], device=X.device)
-        ldh = R
+        H, ldh = X.new_empty((Mtok, R), dtype=_TORCH[hdt]), R
     else:
         hdt = dtype_code(out) if hdt is None else hdt
-        if not (_rows(out) and out.shape == (Mtok, R) and out.dtype == _TORCH[hdt] and out.device == X.device):
+        h = _mat(out)
+        if not (h and h[:2] == (Mtok, R) and out.dtype == _TORCH[hdt] and out.device == dev):
             _refuse(f"out must be a row-major {_TORCH[hdt]} tensor of ({Mtok}, {R})", out=out)
-        H, ldh = out, _ld2(out)
-    G = torch.empty((Mtok, R), dtype=torch.bfloat16, device=X.device) if save else None
-    U = torch.empty((Mtok, R), dtype=torch.bfloat16, device=X.device) if save else None
-    ws = _need(raw.nm_spmm_glu_workspace(Mtok, K, R, Ns, xdt), ws, X.device)
-    st = raw.nm_spmm_glu(X.data_ptr(), xdt, Mtok, K, _ld2(X), vals_g.data_ptr(), idx_g.data_ptr(), vals_u.data_ptr(),
-                         idx_u.data_ptr(), xdt, R, _ld2(vals_g), _ld2(idx_g), Ns, _ptr(x_scale), g_scale, u_scale, act,
-                         H.data_ptr(), hdt, ldh, _ptr(G), _ptr(U), R, _ptr(ws),
-                         0 if ws is None else ws.numel() * ws.element_size(), _raw_stream(X))
+        H, ldh = out, h[2]
+    G = X.new_empty((Mtok, R), dtype=torch.bfloat16) if save else None
+    U = X.new_empty((Mtok, R), dtype=torch.bfloat16) if save else None
+    ws = _need(raw.nm_spmm_glu_workspace(Mtok, K, R, Ns, xdt), ws, X)
+    st = raw.nm_spmm_glu(X.data_ptr(), xdt, Mtok, K, ldx, vals_g.data_ptr(), idx_g.data_ptr(), vals_u.data_ptr(),
+                         idx_u.data_ptr(), xdt, R, ldv, ldi, Ns, _ptr(x_scale), g_scale, u_scale, act, H.data_ptr(), hdt,
+                         ldh, _ptr(G), _ptr(U), R, _ptr(ws), 0 if ws is None else ws.nbytes, _raw_stream(X))
     if st:
         _check(st)
     return (H, G, U) if save else H
 
 
-def _grad_out(t: torch.Tensor | None, want: bool, shape, dt: int, device):
+def _grad_out(t: torch.Tensor | None, want: bool, rows: int, cols: int, dt: int, X: torch.Tensor):
+    """(output or None, its leading dimension)."""
     if not want:
-        return None
+        return None, cols
+    dtype = _TORCH[dt]
     if t is None:
-        return torch.empty(shape, dtype=_TORCH[dt], device=device)
-    if not (_rows(t) and t.shape == shape and t.dtype == _TORCH[dt] and t.device == device):
-        _refuse(f"an output must be a row-major {_TORCH[dt]} tensor of {shape}", out=t)
-    return t
+        return X.new_empty((rows, cols), dtype=dtype), cols
+    m = _mat(t)
+    if not (m and m[:2] == (rows, cols) and t.dtype == dtype and t.device == X.device):
+        _refuse(f"an output must be a row-major {dtype} tensor of {(rows, cols)}", out=t)
+    return t, m[2]
 
 
 def _grad_inputs(X, dY, vals, idx, Ns):
-    """(tokens, columns, rows, lifted columns) of a backward call."""
-    if not (_rows(X) and _rows(dY) and _rows(vals) and _rows(idx) and
-            X.dtype == dY.dtype == vals.dtype == torch.bfloat16 and idx.dtype == torch.int32 and
-            X.device == dY.device == vals.device == idx.device):
+    """(tokens, columns, rows, lifted columns) of a backward call and the leading dimensions of X,
+    dY, vals and idx."""
+    x, y, v, i, dev, bf16 = _mat(X), _mat(dY), _mat(vals), _mat(idx), X.device, torch.bfloat16
+    if not (x and y and v and i and X.dtype == bf16 and dY.dtype == bf16 and vals.dtype == bf16 and
+            idx.dtype == torch.int32 and dev == dY.device and dev == vals.device and dev == idx.device):
         _refuse("the backward pass takes row-major bf16 tensors and an int32 idx", X=X, dY=dY, vals=vals, idx=idx)
-    Mtok, K = X.shape
-    R = vals.shape[0]
+    (Mtok, K, ldx), (R, slots, ldv), (irows, words, ldi) = x, v, i
     Kl = lifted_width(K, Ns) if Ns >= 2 else K
-    if not (dY.shape == (Mtok, R) and vals.shape[1] >= Kl // 2 and idx.shape[0] == R and idx.shape[1] >= (Kl + 31) // 32):
+    if not (y[0] == Mtok and y[1] == R and slots >= Kl // 2 and irows == R and words >= (Kl + 31) // 32):
         _refuse("the shapes do not belong to one sparse layer", X=X, dY=dY, vals=vals, idx=idx)
-    return Mtok, K, R, Kl
+    return Mtok, K, R, Kl, ldx, y[2], ldv, ldi
 
 
 def nm_spmm_backward(dY: torch.Tensor, X: torch.Tensor, vals: torch.Tensor, idx: torch.Tensor, Ns: int = 0,
                      want_dx: bool = True, want_dv: bool = True, dxdt: int = NM_BF16, dvdt: int = NM_BF16,
                      out_dx: torch.Tensor | None = None, out_dv: torch.Tensor | None = None, ws: torch.Tensor | None = None):
     """(dX, dvals) of Y = X W^T on a packed bf16 weight; what is not wanted is None."""
-    Mtok, K, R, Kl = _grad_inputs(X, dY, vals, idx, Ns)
-    dX = _grad_out(out_dx, want_dx, (Mtok, K), dxdt, X.device)
-    dV = _grad_out(out_dv, want_dv, (R, Kl // 2), dvdt, X.device)
-    ws = _need(raw.nm_spmm_backward_workspace(Mtok, K, R, Ns), ws, X.device)
-    st = raw.nm_spmm_backward(dY.data_ptr(), _ld2(dY), X.data_ptr(), _ld2(X), Mtok, K, vals.data_ptr(), idx.data_ptr(), R,
-                              _ld2(vals), _ld2(idx), Ns, _ptr(dX), dxdt, K if dX is None else _ld2(dX), _ptr(dV), dvdt,
-                              Kl // 2 if dV is None else _ld2(dV), _ptr(ws),
-                              0 if ws is None else ws.numel() * ws.element_size(), _raw_stream(X))
+    Mtok, K, R, Kl, ldx, ldy, ldv, ldi = _grad_inputs(X, dY, vals, idx, Ns)
+    dX, lddx = _grad_out(out_dx, want_dx, Mtok, K, dxdt, X)
+    dV, lddv = _grad_out(out_dv, want_dv, R, Kl // 2, dvdt, X)
+    ws = _need(raw.nm_spmm_backward_workspace(Mtok, K, R, Ns), ws, X)
+    st = raw.nm_spmm_backward(dY.data_ptr(), ldy, X.data_ptr(), ldx, Mtok, K, vals.data_ptr(), idx.data_ptr(), R, ldv, ldi,
+                              Ns, _ptr(dX), dxdt, lddx, _ptr(dV), dvdt, lddv, _ptr(ws), 0 if ws is None else ws.nbytes,
+                              _raw_stream(X))
     if st:
         _check(st)
     return dX, dV
@@ -521,26 +522,25 @@ def nm_spmm_glu_backward(dH: torch.Tensor, G: torch.Tensor, U: torch.Tensor, X: 
                          out_dv: tuple[torch.Tensor, torch.Tensor] | None = None, ws: torch.Tensor | None = None):
     """(dX, dvals_g, dvals_u) of nm_spmm_glu from its saved pre-activations; what is not wanted
     is None."""
-    Mtok, K, R, Kl = _grad_inputs(X, dH, vals_g, idx_g, Ns)
-    if not (vals_u.shape == vals_g.shape and idx_u.shape == idx_g.shape and vals_u.stride() == vals_g.stride() and
-            idx_u.stride() == idx_g.stride() and vals_u.dtype == torch.bfloat16 and idx_u.dtype == torch.int32 and
-            vals_u.device == idx_u.device == X.device):
+    Mtok, K, R, Kl, ldx, ldh, ldv, ldi = _grad_inputs(X, dH, vals_g, idx_g, Ns)
+    v, i, dev, bf16 = _mat(vals_u), _mat(idx_u), X.device, torch.bfloat16
+    if not (v and i and v == (R, vals_g.shape[1], ldv) and i == (R, idx_g.shape[1], ldi) and vals_u.dtype == bf16 and
+            idx_u.dtype == torch.int32 and dev == vals_u.device and dev == idx_u.device):
         _refuse("the gate and up weights must be packed alike", vals_g=vals_g, idx_g=idx_g, vals_u=vals_u, idx_u=idx_u)
-    if not (_rows(G) and _rows(U) and G.shape == U.shape == (Mtok, R) and G.dtype == U.dtype == torch.bfloat16 and
-            G.device == U.device == X.device and _ld2(G) == _ld2(U)):
+    m = _mat(G)
+    if not (m and m == _mat(U) and m[0] == Mtok and m[1] == R and G.dtype == bf16 and U.dtype == bf16 and
+            dev == G.device and dev == U.device):
         _refuse("G and U must be row-major bf16 tensors of dH's shape with the same row stride", dH=dH, G=G, U=U)
-    dX = _grad_out(out_dx, want_dx, (Mtok, K), dxdt, X.device)
-    dVg = _grad_out(out_dv[0] if out_dv else None, want_dv, (R, Kl // 2), dvdt, X.device)
-    dVu = _grad_out(out_dv[1] if out_dv else None, want_dv, (R, Kl // 2), dvdt, X.device)
-    if want_dv and _ld2(dVu) != _ld2(dVg):
+    dX, lddx = _grad_out(out_dx, want_dx, Mtok, K, dxdt, X)
+    dVg, lddv = _grad_out(out_dv[0] if out_dv else None, want_dv, R, Kl // 2, dvdt, X)
+    dVu, lddu = _grad_out(out_dv[1] if out_dv else None, want_dv, R, Kl // 2, dvdt, X)
+    if lddu != lddv:
         _refuse("the two weight gradients must have the same row stride", dVg=dVg, dVu=dVu)
-    ws = _need(raw.nm_spmm_glu_backward_workspace(Mtok, K, R, Ns), ws, X.device)
-    st = raw.nm_spmm_glu_backward(dH.data_ptr(), _ld2(dH), G.data_ptr(), U.data_ptr(), _ld2(G), act, X.data_ptr(),
-                                  _ld2(X), Mtok, K, vals_g.data_ptr(), idx_g.data_ptr(), vals_u.data_ptr(),
-                                  idx_u.data_ptr(), R, _ld2(vals_g), _ld2(idx_g), Ns, _ptr(dX), dxdt,
-                                  K if dX is None else _ld2(dX), _ptr(dVg), _ptr(dVu), dvdt,
-                                  Kl // 2 if dVg is None else _ld2(dVg), _ptr(ws),
-                                  0 if ws is None else ws.numel() * ws.element_size(), _raw_stream(X))
+    ws = _need(raw.nm_spmm_glu_backward_workspace(Mtok, K, R, Ns), ws, X)
+    st = raw.nm_spmm_glu_backward(dH.data_ptr(), ldh, G.data_ptr(), U.data_ptr(), m[2], act, X.data_ptr(), ldx, Mtok, K,
+                                  vals_g.data_ptr(), idx_g.data_ptr(), vals_u.data_ptr(), idx_u.data_ptr(), R, ldv, ldi, Ns,
+                                  _ptr(dX), dxdt, lddx, _ptr(dVg), _ptr(dVu), dvdt, lddv, _ptr(ws),
+                                  0 if ws is None else ws.nbytes, _raw_stream(X))
     if st:
         _check(st)
     return dX, dVg, dVu

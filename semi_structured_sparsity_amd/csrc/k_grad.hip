@@ -749,8 +749,23 @@ __global__ __launch_bounds__(256, ST == 4 ? 2 : 3) void grad_few_kernel(FewArgs 
             }
         }
     }
-    // a lane: token 32 j + l32, columns 8 g + 4 h .. + 3 of the wave's 32
+    // a lane: token 32 j + l32, columns 8 g + 4 h .. + 3 of the wave's 32; no partials: dX itself
     float* part = a.g.part + (int64_t)split * a.M * a.K;
+    if (!a.g.part) {
+#pragma unroll
+        for (int j = 0; j < ST; ++j) {
+            const int64_t m = 32 * j + l32;
+            if (m >= a.M) continue;
+#pragma unroll
+            for (int e = 0; e < 16; ++e) {
+                const int64_t k = k0 + 32 * wave + 8 * (e >> 2) + 4 * h + (e & 3), o = m * a.g.lddx + k;
+                if (k >= a.K) continue;
+                if (a.g.dxf32) ((float*)a.g.dX)[o] = acc[j][e];
+                else ((uint16_t*)a.g.dX)[o] = (uint16_t)f32_to_bf16_bits(acc[j][e]);
+            }
+        }
+        return;
+    }
 #pragma unroll
     for (int j = 0; j < ST; ++j) {
         const int64_t m = 32 * j + l32;
@@ -1009,7 +1024,7 @@ nm_status launch_grad(const GradIn& given, const GradOut& out, int nmat, void* w
             f.panels = (int)ceil_div(in.Kl, 128);
             f.splits = splits = few_splits(in.Kl, Rn, &f.spp);
             g.nx = (int)ceil_div(splits, 8) * 8 * f.panels;
-            g.part = PART;
+            g.part = splits > 1 || Kx != in.K ? PART : nullptr;
         }
         f.g = g;
         const dim3 gf((unsigned)(g.nx + (dv ? f.tk * (int)ceil_div(f.tr, 8) * 8 : 0)));
