@@ -593,7 +593,8 @@ __global__ __launch_bounds__(512, 1) void grad_ring_kernel(GradArgs g) {
 // as t[column][row pair] (36 words a column, and 8 more every 16 columns: writes and 16-byte
 // fragment reads free of bank conflicts), and multiplied with v_mfma_f32_32x32x16_bf16;
 // wave w takes columns 32 w .. + 31.  LDS is double buffered, one barrier a step.  Partials
-// [split][M][K] in f32 are added by grad_reduce_kernel.  Blocks of one split and all panels
+// [split][M][K] in f32 are added by grad_reduce_kernel (a single split of a plain weight is dX
+// itself).  Blocks of one split and all panels
 // run on one XCD, whose L2 then serves the positions' lines (8 panels each) once.
 // dV: 128 x 128 tiles, four waves of 64 x 64; the tile's tokens (one or two lines per row of XT
 // and of DT) are loaded whole into LDS, the epilogue is the ring's.
