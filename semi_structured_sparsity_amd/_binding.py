@@ -417,6 +417,8 @@ def _need(need: int, ws: torch.Tensor | None, like: torch.Tensor) -> torch.Tenso
     """The caller's workspace where it has need bytes, else a new one."""
     if need and (ws is None or ws.nbytes < need):
         ws = like.new_empty(need, dtype=torch.uint8)
+    elif ws is not None and not (ws.is_contiguous() and ws.device == like.device):
+        _refuse(f"ws must be contiguous and on {like.device}", ws=ws)
     return ws
 
 
@@ -592,11 +594,18 @@ class AdamWTensors:
                 raise ValueError("copies are bf16")
             if self.sdt == NM_FP8 and (m_scale[i].dtype != torch.float32 or v_scale[i].dtype != torch.float32):
                 raise ValueError("scales are float32")
+            if any(t.dtype not in (torch.float32, torch.bfloat16) for t in (p, grads[i])):
+                raise ValueError(f"params[{i}] and its gradient must be float32 or bfloat16")
             f8 = self.sdt == NM_FP8
             self.array[i] = _AdamWTensor(
                 _ptr(p), _ptr(grads[i]), _ptr(m[i]), _ptr(v[i]), _ptr(m_scale[i]) if f8 else None,
                 _ptr(v_scale[i]) if f8 else None, None if copies is None else _ptr(copies[i]), k, dtype_code(p),
                 dtype_code(grads[i]), lr_scale[i], weight_decay[i])
+        # what a step writes, by address: a tensor listed twice would be updated by two blocks at once
+        written = [params, m, v, copies] + ([m_scale, v_scale] if self.sdt == NM_FP8 else [])
+        spans = sorted((t.data_ptr(), t.data_ptr() + t.nbytes) for ts in written if ts is not None for t in ts if t.numel())
+        if any(a[1] > b[0] for a, b in zip(spans, spans[1:])):
+            raise ValueError("the tensors of a step must not overlap")
 
 
 def nm_adamw(tensors: AdamWTensors, lr: float, step: int, beta1: float = 0.9, beta2: float = 0.999, eps: float = 1e-8,
@@ -606,6 +615,8 @@ def nm_adamw(tensors: AdamWTensors, lr: float, step: int, beta1: float = 0.9, be
         raise ValueError("grad_scale must be one f32 value on the device")
     if tensors.count == 0:
         return
+    if grad_scale is not None and grad_scale.device != tensors.device:
+        raise ValueError(f"grad_scale must be on {tensors.device}, got {grad_scale.device}")
     st = raw.nm_adamw(tensors.address, tensors.count, tensors.sdt, lr, beta1, beta2, eps, step, _ptr(grad_scale),
                       torch._C._cuda_getCurrentRawStream(tensors.device.index))
     if st:

@@ -287,7 +287,15 @@ def test_adamw_binding_refuses(nm):
     for kw in (dict(lr=-1.0, step=1), dict(lr=1.0, step=0), dict(lr=1.0, step=1, beta1=1.0), dict(lr=1.0, step=1, eps=-1.0)):
         with pytest.raises(nm.NMError):
             nm.nm_adamw(t, **kw)
+    with pytest.raises(ValueError):
+        nm.AdamWTensors([x], [y], [x], [w])
+    with pytest.raises(ValueError):
+        nm.AdamWTensors([x, x], [y, y], [z, z.clone()], [w, w.clone()])
+    with pytest.raises(ValueError):
+        nm.AdamWTensors([x.half()], [y], [z], [w])
     with pytest.raises(nm.NMError):
-        nm.nm_adamw(nm.AdamWTensors([x], [y], [x], [w]), lr=1.0, step=1)
+        nm.nm_adamw(nm.AdamWTensors([x], [x], [z], [w]), lr=1.0, step=1)
     with pytest.raises(ValueError):
         nm.nm_adamw(t, lr=1.0, step=1, grad_scale=torch.ones(2, device=dev()))
+    with pytest.raises(ValueError):
+        nm.nm_adamw(t, lr=1.0, step=1, grad_scale=torch.ones(1))

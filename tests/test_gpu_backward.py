@@ -347,7 +347,10 @@ def test_backward_binding_refuses(nm):
                 lambda: nm.nm_spmm_backward(dY, X, v[:, :8], i), lambda: nm.nm_spmm_backward(dY.t(), X, v, i),
                 lambda: nm.nm_spmm_backward(dY, X, v, i, out_dv=torch.empty((8, 31), dtype=torch.bfloat16, device=dev())),
                 lambda: nm.nm_spmm_glu_backward(dY, dY, dY[:, :4], X, v, i, v, i),
-                lambda: nm.nm_spmm_glu_backward(dY, dY, dY, X, v, i, v[:4], i[:4])):
+                lambda: nm.nm_spmm_glu_backward(dY, dY, dY, X, v, i, v[:4], i[:4]),
+                lambda: nm.nm_spmm_backward(dY, X, v, i, Ns=5), lambda: nm.nm_spmm_backward(dY, X, v.cpu(), i),
+                lambda: nm.nm_spmm_backward(dY, X, v, i, ws=torch.empty(1 << 20, dtype=torch.uint8)),
+                lambda: nm.nm_spmm_backward(dY, X, v, i, ws=torch.empty((1, 64), device=dev()).expand(4096, 64))):
         with pytest.raises(ValueError):
             bad()
     with pytest.raises(nm.NMError):

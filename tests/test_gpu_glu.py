@@ -178,6 +178,8 @@ def test_glu_binding_refuses(nm):
         nm.nm_spmm_glu(X, vg, ig, vg, ig, out=torch.empty((4, 9), dtype=torch.bfloat16, device=dev()))
     with pytest.raises(ValueError):
         nm.nm_spmm_glu(X, vg, ig, vg, ig, x_scale=torch.ones(3, device=dev()))
+    with pytest.raises(ValueError):
+        nm.nm_spmm_glu(X, vg, ig, vg, ig, ws=torch.empty(1 << 20, dtype=torch.uint8))
     with pytest.raises(nm.NMError):
         nm.nm_spmm_glu(X, vg, ig, vg, ig, act=9)
     with pytest.raises(nm.NMError):
