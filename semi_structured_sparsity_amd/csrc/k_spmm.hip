@@ -468,8 +468,26 @@ __device__ __forceinline__ void store_glu_tile(const SpmmArgs& a, const typename
 }
 
 // NS-stage LDS ring of KB bytes of X per token per stage; see the comment block above.
-template <typename T, int SR, int ST, int KB, int NS, int WRN, int WTN, int OCC = 1, int IG = 1, bool GLU = false>
+// TAIL: the width ends inside the last stage.  Loads past a row's end re-read its last piece (values
+// and X 16 bytes, index words 4), and the fragments of columns past the end are zeroed in
+// registers, weights and activations both, before they are multiplied.  (Two plain products and a
+// combining launch, which such widths took before: 132 tokens of 760 x 1248 fp8 41.4 -> 5.8 us, one
+// of 127 x 1088 int8 6:8 20.6 -> 7.7, 381 of 1935 x 576 bf16 37.7 -> 23.6.)
+__device__ __forceinline__ void zero_unless(bool keep, i32x4_t& v) {
+#pragma unroll
+    for (int e = 0; e < 4; ++e) v[e] = keep ? v[e] : 0;
+}
+__device__ __forceinline__ void zero_unless(bool lo, bool hi, i32x8_t& v) {
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+        v[e] = lo ? v[e] : 0;
+        v[4 + e] = hi ? v[4 + e] : 0;
+    }
+}
+
+template <typename T, int SR, int ST, int KB, int NS, int WRN, int WTN, int OCC = 1, int IG = 1, bool GLU = false, bool TAIL = false>
 __global__ __launch_bounds__(64 * WRN * WTN, OCC) void spmm_ring_kernel(SpmmArgs a) {
+    static_assert(!TAIL || IG == 1, "index words are clamped one by one");
     using RG = Ring<T, SR, ST, KB, NS, WRN, WTN, IG>;
     using FR = RingFrag<SR, ST>;
     __shared__ __attribute__((aligned(1024))) uint8_t smem[RG::LDS];
@@ -523,21 +541,21 @@ __global__ __launch_bounds__(64 * WRN * WTN, OCC) void spmm_ring_kernel(SpmmArgs
         const int q = (wave * RG::NA + i) * 64 + lane;       // 16-byte chunk of the block's stage, row-major
         const int row = q / ACH, c = RG::alogical(row, q % ACH);
         const int64_t gr = wrow(row) < rmax ? wrow(row) : rmax;
-        oA[i] = (uint32_t)(gr * a.ldv * es + c * 16);
+        oA[i] = (uint32_t)(gr * a.ldv * es + (TAIL ? 0 : c * 16));
     }
 #pragma unroll
     for (int i = 0; i < RG::NI; ++i) {
         const int q = (wave * RG::NI + i) * 64 + lane;  // dword slot of the stage's [BR, AI] index block
         const int row = q / RG::AI, lw = (q % RG::AI) ^ iswz<RG::AI>(row);
         const int64_t gr = wrow(row) < rmax ? wrow(row) : rmax;
-        oI[i] = (uint32_t)(gr * a.ldi * 4 + lw * 4);
+        oI[i] = (uint32_t)(gr * a.ldi * 4 + (TAIL ? 0 : lw * 4));
     }
 #pragma unroll
     for (int i = 0; i < RG::NB; ++i) {
         const int row = (wave * RG::NB + i) * (64 / BCH) + lane / BCH;
         const int c = (lane % BCH) ^ RG::swb(row);
         const int64_t gt = row < tmax ? row : tmax;
-        oB[i] = (uint32_t)(gt * a.ldx * es + c * 16);
+        oB[i] = (uint32_t)(gt * a.ldx * es + (TAIL ? 0 : c * 16));
     }
     // IG > 1: batch p of index group g (stages past the last are clamped to it: read, never used)
     auto issue_group = [&](int g, int p) __attribute__((always_inline)) {
@@ -551,23 +569,40 @@ __global__ __launch_bounds__(64 * WRN * WTN, OCC) void spmm_ring_kernel(SpmmArgs
             dma16s(gb + (uint32_t)(unit * 1024), base, gI[p][i] + (uint32_t)(sc * 16));
         }
     };
+    // TAIL: the offsets along a row of the lane's pieces at stage sg, clamped to the row's last piece
+    const uint32_t aend = (uint32_t)a.comp_bytes - 16, iend = (uint32_t)a.idx_words * 4 - 4, bend = (uint32_t)(a.K * es) - 16;
+    auto tailA = [&](int i, int sg) __attribute__((always_inline)) -> uint32_t {
+        const int q = (wave * RG::NA + i) * 64 + lane;
+        const uint32_t o = (uint32_t)(RG::alogical(q / ACH, q % ACH) * 16 + sg * RG::AROW);
+        return o < aend ? o : aend;
+    };
+    auto tailI = [&](int i, int sg) __attribute__((always_inline)) -> uint32_t {
+        const int q = (wave * RG::NI + i) * 64 + lane, row = q / RG::AI;
+        const uint32_t o = (uint32_t)((((q % RG::AI) ^ iswz<RG::AI>(row)) + sg * RG::AI) * 4);
+        return o < iend ? o : iend;
+    };
+    auto tailB = [&](int i, int sg) __attribute__((always_inline)) -> uint32_t {
+        const int row = (wave * RG::NB + i) * (64 / BCH) + lane / BCH;
+        const uint32_t o = (uint32_t)(((lane % BCH) ^ RG::swb(row)) * 16 + sg * KB);
+        return o < bend ? o : bend;
+    };
     auto issue = [&](int s) __attribute__((always_inline)) {
         const uint32_t st = sbase + (uint32_t)((s % NS) * RG::STAGE);
         const int sg = s_begin + s;   // the stage's place in the whole K
 #pragma unroll
         for (int i = 0; i < RG::NA; ++i)
-            dma16s(st + RG::A_OFF + (wave * RG::NA + i) * 1024, baseA, oA[i] + (uint32_t)(sg * RG::AROW));
+            dma16s(st + RG::A_OFF + (wave * RG::NA + i) * 1024, baseA, oA[i] + (TAIL ? tailA(i, sg) : (uint32_t)(sg * RG::AROW)));
         if constexpr (IG > 1) {
             // stage s >= 1 carries batch (s-1) % IG of group (s-1) / IG + 1; group 0 is loaded up front
             if (s >= 1) issue_group((s - 1) / IG + 1, (s - 1) % IG);
         } else {
 #pragma unroll
             for (int i = 0; i < RG::NI; ++i)
-                dma4s(st + RG::I_OFF + (wave * RG::NI + i) * 256, baseI, oI[i] + (uint32_t)(sg * RG::AI * 4));
+                dma4s(st + RG::I_OFF + (wave * RG::NI + i) * 256, baseI, oI[i] + (TAIL ? tailI(i, sg) : (uint32_t)(sg * RG::AI * 4)));
         }
 #pragma unroll
         for (int i = 0; i < RG::NB; ++i)
-            dma16s(st + RG::B_OFF + (wave * RG::NB + i) * 1024, baseB, oB[i] + (uint32_t)(sg * KB));
+            dma16s(st + RG::B_OFF + (wave * RG::NB + i) * 1024, baseB, oB[i] + (TAIL ? tailB(i, sg) : (uint32_t)(sg * KB)));
     };
     const int h = lane >> 5, l32 = lane & 31;
     i32x4_t ipc[SR];   // IG > 1: the current stage's index piece of each row sub-tile (one word per depth)
@@ -598,6 +633,17 @@ __global__ __launch_bounds__(64 * WRN * WTN, OCC) void spmm_ring_kernel(SpmmArgs
             const i32x4_t lo = *(const i32x4_t*)(trow + ((4 * d + h) ^ sw) * 16);
             const i32x4_t hi = *(const i32x4_t*)(trow + ((4 * d + 2 + h) ^ sw) * 16);
             f.b[j] = __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
+        }
+        if constexpr (TAIL) {
+            if (s_begin + S == a.nsteps - 1) {
+                // columns of the stage: a lane's values from (2d + h) KO / 8 * (KDEP / 32 chunks), X pieces of 16 bytes
+                const int left = (int)(a.K - (int64_t)(a.nsteps - 1) * RG::KO), xc = 16 / (int)sizeof(T);
+                const bool ka = (2 * d + h) * 2 * xc < left;
+#pragma unroll
+                for (int i = 0; i < SR; ++i) zero_unless(ka, f.a[i]);
+#pragma unroll
+                for (int j = 0; j < ST; ++j) zero_unless((4 * d + h) * xc < left, (4 * d + 2 + h) * xc < left, f.b[j]);
+            }
         }
     };
 
@@ -1331,7 +1377,7 @@ constexpr int kRedStride = 20;
 // same stage order takes about 10 us.
 constexpr int kXresBytes = 64 * 1024 + 32 * 16;
 
-template <typename T, int SR, int ST, int KB, int NS, bool LIFT = false, int XRB_ = 0, bool GLU = false, int IGS = 0, int OCC = 1>
+template <typename T, int SR, int ST, int KB, int NS, bool LIFT = false, int XRB_ = 0, bool GLU = false, int IGS = 0, int OCC = 1, bool TAIL = false>
 __global__ __launch_bounds__(256, OCC) void spmm_ringk_kernel(SpmmArgs a) {
     constexpr bool XRES = XRB_ > 0;
     constexpr int es = sizeof(T);
@@ -1391,7 +1437,7 @@ __global__ __launch_bounds__(256, OCC) void spmm_ringk_kernel(SpmmArgs a) {
         const int q = (wave * NA + i) * 64 + lane;
         const int row = q / ACH, c = (q % ACH) ^ swa(row);
         const int64_t gr = wrow(row) < rmax ? wrow(row) : rmax;
-        oA[i] = (uint32_t)(gr * a.ldv * es + c * 16);
+        oA[i] = (uint32_t)(gr * a.ldv * es + (TAIL ? 0 : c * 16));
     }
 #pragma unroll
     for (int i = 0; i < NI; ++i) {
@@ -1403,7 +1449,8 @@ __global__ __launch_bounds__(256, OCC) void spmm_ringk_kernel(SpmmArgs a) {
     // IGS: batch b (0 .. IGS - 1) of index group g, NI loads of two rows per wave: the wave's rows are
     // those of its values, BR / 4 of the tile.  Words past the row's last are clamped to it (read,
     // never used).
-    const uint32_t ilast = (uint32_t)(a.nsteps * AI * 4 - 4);
+    static_assert(!TAIL || IGS > 0, "index words are clamped in their groups");
+    const uint32_t ilast = (uint32_t)(TAIL ? a.idx_words * 4 - 4 : a.nsteps * AI * 4 - 4);
     auto issue_group = [&](int g, int b) __attribute__((always_inline)) {
 #pragma unroll
         for (int i = 0; i < NI; ++i) {
@@ -1420,7 +1467,7 @@ __global__ __launch_bounds__(256, OCC) void spmm_ringk_kernel(SpmmArgs a) {
         const int row = (wave * NB + i) * (64 / BCH) + lane / BCH;
         const int c = (lane % BCH) ^ swb(row);
         const int64_t gt = row < tmax ? row : tmax;
-        oB[i] = (uint32_t)(gt * a.ldx * es + (LIFT ? 0 : c * 16));
+        oB[i] = (uint32_t)(gt * a.ldx * es + (LIFT || TAIL ? 0 : c * 16));
         oBc[i] = (uint32_t)(c * 16);
     }
     // LIFT: first original byte of stage sg's slot (a multiple of 16), and the last 16-byte
@@ -1429,11 +1476,18 @@ __global__ __launch_bounds__(256, OCC) void spmm_ringk_kernel(SpmmArgs a) {
         return es == 2 ? (uint32_t)(16 * ((32 * sg) / 3)) : (uint32_t)(8 * (((64 * sg) / 3) & ~1));
     };
     const uint32_t xlast = (uint32_t)(a.xrow_bytes - 16);
+    // TAIL: pieces past a row's end are its last one
+    const uint32_t aend = (uint32_t)a.comp_bytes - 16, bend = (uint32_t)(a.K * es) - 16;
+    auto tailA = [&](int i, int sg) __attribute__((always_inline)) -> uint32_t {
+        const int q = (wave * NA + i) * 64 + lane;
+        const uint32_t o = (uint32_t)(((q % ACH) ^ swa(q / ACH)) * 16 + sg * AROW);
+        return o < aend ? o : aend;
+    };
     auto issue = [&](int sl) __attribute__((always_inline)) {   // local stage sl of this block's range
         const int sg = s_begin + sl;
         const uint32_t st = sbase + (uint32_t)((sl % NS) * STAGE);
 #pragma unroll
-        for (int i = 0; i < NA; ++i) dma16s(st + (wave * NA + i) * 1024, baseA, oA[i] + (uint32_t)(sg * AROW));
+        for (int i = 0; i < NA; ++i) dma16s(st + (wave * NA + i) * 1024, baseA, oA[i] + (TAIL ? tailA(i, sg) : (uint32_t)(sg * AROW)));
 #pragma unroll
         for (int i = 0; i < (IGS ? 0 : NI); ++i)
             dma4s(st + I_OFF + (wave * NI + i) * 256, baseI, oI[i] + (uint32_t)(sg * AI * 4));
@@ -1452,7 +1506,10 @@ __global__ __launch_bounds__(256, OCC) void spmm_ringk_kernel(SpmmArgs a) {
             }
         } else {
 #pragma unroll
-            for (int i = 0; i < NB; ++i) dma16s(st + B_OFF + (wave * NB + i) * 1024, baseB, oB[i] + (uint32_t)(sg * KB));
+            for (int i = 0; i < NB; ++i) {
+                const uint32_t o = oBc[i] + (uint32_t)(sg * KB);
+                dma16s(st + B_OFF + (wave * NB + i) * 1024, baseB, oB[i] + (TAIL ? (o < bend ? o : bend) : (uint32_t)(sg * KB)));
+            }
         }
     };
     // XRES: valid token rows of the tile, padded LDS row bytes of the resident X
@@ -1463,6 +1520,9 @@ __global__ __launch_bounds__(256, OCC) void spmm_ringk_kernel(SpmmArgs a) {
     if constexpr (XRES && LIFT) {
         const uint32_t end = nloc > 0 ? slot_start(s_end - 1) + KB : xbeg;
         xbytes = (end < (uint32_t)a.xrow_bytes ? end : (uint32_t)a.xrow_bytes) - xbeg;
+    }
+    if constexpr (XRES && TAIL && !LIFT) {
+        if (xbeg + xbytes > bend + 16) xbytes = bend + 16 - xbeg;
     }
     const int xcpr = XRES ? (int)((xbytes + 1023) / 1024) : 0;   // 1 KB loads per row
     const int xrowp = xcpr * 1024 + 16;
@@ -1553,6 +1613,16 @@ __global__ __launch_bounds__(256, OCC) void spmm_ringk_kernel(SpmmArgs a) {
                 const i32x4_t lo = *(const i32x4_t*)(trow + ((4 * d + h) ^ swb(tok)) * 16);
                 const i32x4_t hi = *(const i32x4_t*)(trow + ((4 * d + 2 + h) ^ swb(tok)) * 16);
                 f.b[j] = __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
+            }
+        }
+        if constexpr (TAIL) {
+            if (s_begin + sl == a.nsteps - 1) {
+                const int left = (int)(a.K - (int64_t)(a.nsteps - 1) * KO), xc = 16 / es;
+                const bool ka = (2 * d + h) * 2 * xc < left;
+#pragma unroll
+                for (int i = 0; i < SR; ++i) zero_unless(ka, f.a[i]);
+#pragma unroll
+                for (int j = 0; j < ST; ++j) zero_unless((4 * d + h) * xc < left, (4 * d + 2 + h) * xc < left, f.b[j]);
             }
         }
     };
@@ -2236,9 +2306,12 @@ size_t spmm_ws(int64_t Mtok, int64_t K, int64_t R, int Ns, nm_dtype xdt) {
 
 // The DMA ring kernels take 16-byte pieces of the index rows and 32-bit per-lane offsets
 // from a block's base pointers.
+static bool ring_idx_ok(const SpmmArgs& a) { return ((uintptr_t)a.idx & 15u) == 0 && (a.ldi % 4) == 0; }
+static bool ring_limits_ok(const SpmmArgs& a, int64_t es) {
+    return a.R * a.ldv * es < (1LL << 32) && a.R * a.ldi * 4 < (1LL << 32) && a.Mtok * a.ldx * es < (1LL << 32);
+}
 static bool ring_ok_for(const SpmmArgs& a, int64_t es) {
-    return ((uintptr_t)a.idx & 15u) == 0 && (a.ldi % 4) == 0 && a.R * a.ldv * es < (1LL << 32) &&
-           a.R * a.ldi * 4 < (1LL << 32) && a.Mtok * a.ldx * es < (1LL << 32);
+    return ring_idx_ok(a) && ring_limits_ok(a, es);
 }
 
 static bool lift_fused(int64_t Mtok, int64_t K, int64_t R, int Ns, nm_dtype xdt, bool ring_ok) {
@@ -2685,7 +2758,7 @@ constexpr int kGluX = 16 * 1024;
 //           on the first features and narrow ones on the rest
 //   kind 0: none applies (K off the stage grid, unaligned index rows): two plain products
 struct GluPlan {
-    int kind, mid, xres, big, tiles_r, tiles_t, nsteps, KS, steps_per_split, tile_rows;
+    int kind, mid, xres, big, tail, tiles_r, tiles_t, nsteps, KS, steps_per_split, tile_rows;
     int64_t split_rows;
 };
 
@@ -2696,9 +2769,10 @@ static GluPlan plan_glu(int64_t Mtok, int64_t K, int64_t R, bool ring_ok, bool l
     using RN = Ring<NM_RING_NARROW>;
     constexpr int KOm = 256 / (int)sizeof(T);
     static_assert(KOm == RN::KO, "the K-split and the narrow ring share their stage width");
-    if (!ring_ok || K % KOm) return p;
+    if (!ring_ok || K % (32 / (int)sizeof(T))) return p;   // (a piece of 16 value bytes is inside a row or past it)
     const int64_t cus = device_cus();
-    p.nsteps = (int)(K / KOm);
+    p.nsteps = (int)ceil_div(K, KOm);
+    p.tail = K % KOm != 0;
     if (Mtok <= 256) {
         const int64_t rt = ceil_div(R, 32);
         p.kind = 1;
@@ -2797,15 +2871,19 @@ static nm_status run_glu(SpmmArgs a, const GluPlan& p, bool lift, void* part, co
         // index words in groups of a line per row: IGS stages a group.  (Loaded stage by stage they touch as
         // many lines as the values: one token 26.3 -> 23.0 us with the groups.)
 #define NM_GLUK(ST, NS, LIFT, XRB, OCC)                                                                              \
-    hipLaunchKernelGGL((spmm_ringk_kernel<T, 2, ST, 256, NS, LIFT, XRB, true, sizeof(T) == 2 ? 8 : 4, OCC>), grid, \
-                       dim3(256), 0, s, a)
+    if (p.tail)                                                                                                       \
+        hipLaunchKernelGGL((spmm_ringk_kernel<T, 2, ST, 256, NS, LIFT, XRB, true, sizeof(T) == 2 ? 8 : 4, OCC, true>), \
+                           grid, dim3(256), 0, s, a);                                                                 \
+    else                                                                                                              \
+        hipLaunchKernelGGL((spmm_ringk_kernel<T, 2, ST, 256, NS, LIFT, XRB, true, sizeof(T) == 2 ? 8 : 4, OCC>), grid, \
+                           dim3(256), 0, s, a)
         if (lift) {
-            if (p.xres) NM_GLUK(1, 5, true, kGluX, 2);
-            else if (p.mid == 1) NM_GLUK(1, 3, true, 0, 2);
-            else NM_GLUK(2, 2, true, 0, 2);
-        } else if (p.xres) NM_GLUK(1, 5, false, kGluX, 2);
-        else if (p.mid == 1) NM_GLUK(1, 3, false, 0, 2);
-        else NM_GLUK(2, 2, false, 0, 2);
+            if (p.xres) { NM_GLUK(1, 5, true, kGluX, 2); }
+            else if (p.mid == 1) { NM_GLUK(1, 3, true, 0, 2); }
+            else { NM_GLUK(2, 2, true, 0, 2); }
+        } else if (p.xres) { NM_GLUK(1, 5, false, kGluX, 2); }
+        else if (p.mid == 1) { NM_GLUK(1, 3, false, 0, 2); }
+        else { NM_GLUK(2, 2, false, 0, 2); }
 #undef NM_GLUK
     } else {
         auto launch = [&](bool big, int64_t f_begin, int64_t f_end) {
@@ -2823,9 +2901,11 @@ static nm_status run_glu(SpmmArgs a, const GluPlan& p, bool lift, void* part, co
             b.R = f_end - f_begin;
             b.tiles_r = (int)ceil_div(b.R, (big ? RB::BR : RN::BR) / 2);
             b.tiles_t = (int)ceil_div(a.Mtok, big ? RB::BT : RN::BT);
-            b.nsteps = (int)(a.K / (big ? RB::KO : RN::KO));
+            b.nsteps = (int)ceil_div(a.K, big ? RB::KO : RN::KO);
             const dim3 grid((unsigned)(b.tiles_r * b.tiles_t), (unsigned)p.KS);
             if (big) hipLaunchKernelGGL((spmm_ring2_kernel<NM_RING_BIG, true>), grid, dim3(512), 0, s, b);
+            else if (p.tail)
+                hipLaunchKernelGGL((spmm_ring_kernel<NM_RING_NARROW, 1, 1, true, true>), grid, dim3(256), 0, s, b);
             else
                 hipLaunchKernelGGL((spmm_ring_kernel<NM_RING_NARROW, 1, sizeof(T) == 2 ? 4 : 1, true>), grid, dim3(256),
                                    0, s, b);
@@ -2941,7 +3021,11 @@ nm_status launch_glu(const GluIn& g, void* ws, hipStream_t s) {
     a.comp_bytes = Kl / 2 * es;
     a.idx_words = (Kl + 31) / 32;
     a.xrow_bytes = g.K * es;
-    auto ok = [&]() { return ring_ok_for(a, es) && ((uintptr_t)a.idx2 & 15u) == 0; };
+    // whole stages load index words 16 bytes at a time, a width that ends inside one word by word
+    const bool words = Kl % (256 / es) != 0;
+    auto ok = [&]() {
+        return ring_limits_ok(a, es) && (words || (ring_idx_ok(a) && ((uintptr_t)a.idx2 & 15u) == 0));
+    };
     bool fused;
     GluPlan p = glu_plan(g.Mtok, g.K, g.R, g.Ns, g.xdt, ok(), &fused);
     if (g.Ns && !fused) {   // the product then reads the lifted copy

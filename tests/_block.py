@@ -52,7 +52,8 @@ def weight(g, R, K, Ns=0, scale=0.05, integer=False, dtype="bf16"):
         Wb = g.integers(-1, 2, (R, K)).astype(np.int8)
         dense = Wb.astype(np.float64)
     elif dtype == "fp8":
-        Wt = torch.from_numpy((g.standard_normal((R, K))).astype(np.float32)).to(torch.float8_e4m3fn)
+        Wt = torch.from_numpy((g.integers(-8, 9, (R, K)) if integer else g.standard_normal((R, K))).astype(np.float32))
+        Wt = Wt.to(torch.float8_e4m3fn)
         Wb, dense = Wt.view(torch.uint8).numpy(), Wt.float().numpy().astype(np.float64)
     else:
         Wb = O.f32_to_bf16((g.integers(-2, 3, (R, K)) if integer else g.standard_normal((R, K)) * scale).astype(np.float32))

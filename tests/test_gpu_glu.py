@@ -16,25 +16,26 @@ def nm():
     return m
 
 
-def _inputs(g, Mt, K, dtype):
+def _inputs(g, Mt, K, dtype, integer=False):
     """(X on the device, X in f64, x_scale or None)."""
     if dtype == "int8":
         X = g.integers(-127, 128, (Mt, K)).astype(np.int8)
         xs = (g.random(Mt) * 0.02 + 0.001).astype(np.float32)
         return torch.from_numpy(X).to(dev()), X.astype(np.float64), xs
     if dtype == "fp8":
-        X = torch.from_numpy(g.standard_normal((Mt, K)).astype(np.float32)).to(torch.float8_e4m3fn)
+        X = torch.from_numpy((g.integers(-8, 9, (Mt, K)) if integer else g.standard_normal((Mt, K))).astype(np.float32))
+        X = X.to(torch.float8_e4m3fn)
         xs = (g.random(Mt) * 0.5 + 0.1).astype(np.float32)
         return X.to(dev()), X.float().numpy().astype(np.float64), xs
     X = O.f32_to_bf16(g.standard_normal((Mt, K)).astype(np.float32))
     return np_bf16(X).to(dev()), O.bf16_to_f32(X).astype(np.float64), None
 
 
-def _check(nm, Mt, R, K, Ns, a, dtype, hdt, save, seed, extra=0):
+def _check(nm, Mt, R, K, Ns, a, dtype, hdt, save, seed, extra=0, integer=False):
     g = np.random.default_rng(seed)
-    X, Xf, xs = _inputs(g, Mt, K, dtype)
-    Wg, vg, ig = B.weight(g, R, K, Ns, dtype=dtype)
-    Wu, vu, iu = B.weight(g, R, K, Ns, dtype=dtype)
+    X, Xf, xs = _inputs(g, Mt, K, dtype, integer)
+    Wg, vg, ig = B.weight(g, R, K, Ns, dtype=dtype, integer=integer)
+    Wu, vu, iu = B.weight(g, R, K, Ns, dtype=dtype, integer=integer)
     gs, us = (1.0, 1.0) if dtype == "bf16" else (0.031, 0.017)
     if extra:
         X = B.strided(X, 16 * extra)
@@ -50,7 +51,7 @@ def _check(nm, Mt, R, K, Ns, a, dtype, hdt, save, seed, extra=0):
     sx = np.ones((Mt, 1)) if xs is None else xs[:, None].astype(np.float64)
     sg, su = np.float64(np.float32(gs)) * sx, np.float64(np.float32(us)) * sx
     G, U = Xf @ Wg.T * sg, Xf @ Wu.T * su
-    if dtype == "int8":     # exact sums, the scale and the product rounded once each
+    if dtype == "int8" or (dtype == "fp8" and integer):     # exact sums, the scale and the product rounded once each
         eG, eU = 4 * 2.0 ** -24 * np.abs(G), 4 * 2.0 ** -24 * np.abs(U)
     else:
         n = K * 2.0 ** -24 + 4 * 2.0 ** -24
@@ -87,6 +88,57 @@ def test_glu_types_and_windows(nm, dtype, Ns, Mt, R):
     K = {0: 512, 3: 768, 4: 1024, 5: 640}[Ns]
     _check(nm, Mt, R, K, Ns, B.RELU2 if dtype == "int8" else B.SILU, dtype, nm.NM_F32, True, Mt * 7 + R + Ns)
     _check(nm, Mt, R, K, Ns, B.GELU_TANH, dtype, nm.NM_BF16, False, Mt * 7 + R + Ns + 1)
+
+
+# widths that end inside a 256-byte stage, the first one or a later one, on every token range's kernel;
+# FP8 on small integers, whose sums are
+# exact: the matrix instruction adds products of unlike size with less than f32's precision, which
+# few terms do not average out
+@pytest.mark.parametrize("dtype,Ns,K", [("bf16", 0, 48), ("bf16", 0, 176), ("bf16", 0, 1104), ("bf16", 4, 64), ("bf16", 4, 896),
+                                        ("int8", 0, 96), ("int8", 0, 544), ("int8", 4, 192), ("int8", 4, 1216),
+                                        ("fp8", 0, 32), ("fp8", 0, 1184), ("fp8", 4, 320), ("fp8", 4, 960)])
+@pytest.mark.parametrize("Mt,R", [(1, 130), (20, 70), (50, 200), (100, 65), (200, 300), (300, 129)])
+def test_glu_widths_inside_a_stage(nm, dtype, Ns, K, Mt, R):
+    fp8 = dtype == "fp8"
+    _check(nm, Mt, R, K, Ns, B.SILU, dtype, nm.NM_F32, True, Mt + R + K + Ns, integer=fp8)
+    _check(nm, Mt, R, K, Ns, B.GELU, dtype, nm.NM_BF16, False, Mt + R + K + Ns + 1, extra=1, integer=fp8)
+
+
+@pytest.mark.parametrize("Mt", [1, 20, 50, 100, 200, 300])
+@pytest.mark.parametrize("K,Ns", [(400, 0), (896, 4)])
+def test_glu_widths_inside_a_stage_keep_rows_apart(nm, Mt, K, Ns):
+    """A weight row or a token row of NaN stays in its own outputs, with rows that follow each other
+    without a gap."""
+    g = np.random.default_rng(Mt + K)
+    R = 100
+    X, _, _ = _inputs(g, Mt, K, "bf16")
+    _, vg, ig = B.weight(g, R, K, Ns)
+    _, vu, iu = B.weight(g, R, K, Ns)
+    ref = nm.nm_spmm_glu(X, vg, ig, vu, iu, Ns=Ns, hdt=nm.NM_F32)
+    vg[6], vu[51] = float("nan"), float("nan")
+    X[Mt // 2] = float("nan")
+    H = nm.nm_spmm_glu(X, vg, ig, vu, iu, Ns=Ns, hdt=nm.NM_F32)
+    rows, cols = torch.arange(Mt, device=dev()) != Mt // 2, torch.ones(R, dtype=torch.bool, device=dev())
+    cols[[6, 51]] = False
+    assert torch.isnan(H[~rows]).all() and torch.isnan(H[:, ~cols]).all()
+    assert torch.equal(H[rows][:, cols], ref[rows][:, cols])
+
+
+@pytest.mark.parametrize("dtype,K,Ns", [("bf16", 400, 0), ("int8", 320, 4)])
+def test_glu_rows_far_apart(nm, dtype, K, Ns):
+    """Token rows whose offsets pass 32 bits: two products and a combination, the same answer."""
+    g = np.random.default_rng(K)
+    Mt, R, es = 9, 200, 2 if dtype == "bf16" else 1
+    X, _, xs = _inputs(g, Mt, K, dtype)
+    _, vg, ig = B.weight(g, R, K, Ns, dtype=dtype)
+    _, vu, iu = B.weight(g, R, K, Ns, dtype=dtype)
+    x_scale = None if xs is None else torch.from_numpy(xs).to(dev())
+    far = torch.empty(((Mt - 1) * 2 ** 29 // es + K,), dtype=X.dtype, device=dev()).as_strided((Mt, K), (2 ** 29 // es, 1))
+    far.copy_(X)
+    near = nm.nm_spmm_glu(X, vg, ig, vu, iu, Ns=Ns, x_scale=x_scale, hdt=nm.NM_F32)
+    H = nm.nm_spmm_glu(far, vg, ig, vu, iu, Ns=Ns, x_scale=x_scale, hdt=nm.NM_F32)
+    # the sums' orders differ (int8: exact); |terms| of a sum is at most K times its largest
+    assert torch.allclose(H, near, rtol=1e-4, atol=1e-4 * near.abs().max().item())
 
 
 # many-token tiles in whole and ragged rounds, a split of few-token stages
