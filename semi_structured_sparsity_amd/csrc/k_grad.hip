@@ -294,6 +294,7 @@ struct GradArgs {
     void* dV[2];
     int64_t ldi, lddv, R, Rp;
     int dvf32, Ns;
+    float* vpart;             // partials of the packed dV [split][weight][R][K'/2] where its tokens are split, or null
     // dX from the packed weights (DEC)
     const uint16_t* vals[2];
     int64_t ldv;
@@ -557,7 +558,17 @@ __device__ __forceinline__ void grad_tile(const GradArgs& g, const GradJob& job,
     }
     wait_vm_all();
     if (!DEC && !isx) {
-        store_grad_tile<SR, ST>(g, acc, words, a0 + wr * SR * 32, b0 + wt * ST * 32, lane);
+        if (g.vpart) {
+            GradArgs p = g;
+            const int64_t half = job.rowsA / 2, one = g.R * half;
+            p.dV[0] = g.vpart + (int64_t)split * (job.rowsB > g.Rp ? 2 : 1) * one;
+            p.dV[1] = (float*)p.dV[0] + one;
+            p.lddv = half;
+            p.dvf32 = 1;
+            store_grad_tile<SR, ST>(p, acc, words, a0 + wr * SR * 32, b0 + wt * ST * 32, lane);
+        } else {
+            store_grad_tile<SR, ST>(g, acc, words, a0 + wr * SR * 32, b0 + wt * ST * 32, lane);
+        }
         return;
     }
     __syncthreads();   // every wave has read the ring: its LDS stages the output
@@ -578,7 +589,8 @@ __global__ __launch_bounds__(512, 1) void grad_ring_kernel(GradArgs g) {
         const int tiles = g.x.tiles_a * g.x.tiles_b, split = blockIdx.x / tiles;
         grad_tile<DEC>(g, g.x, true, blockIdx.x - split * tiles, split, smem);
     } else {
-        grad_tile<false>(g, g.v, false, blockIdx.x - g.nx, 0, smem);
+        const int tiles = g.v.tiles_a * g.v.tiles_b, b = blockIdx.x - g.nx, split = b / tiles;
+        grad_tile<false>(g, g.v, false, b - split * tiles, split, smem);
     }
 }
 
@@ -801,6 +813,19 @@ __global__ __launch_bounds__(256) void grad_reduce_kernel(const float* __restric
     }
 }
 
+// Packed dV of one weight (blockIdx.y) from its partials, in split order
+__global__ __launch_bounds__(256) void grad_reduce_v_kernel(const float* __restrict__ part, int splits, int64_t R, int64_t half,
+                                                            GradOut out) {
+    const int64_t total = R * half, all = total * gridDim.y;
+    void* dV = out.dV[blockIdx.y];
+    for (int64_t t = (int64_t)blockIdx.x * 256 + threadIdx.x; t < total; t += (int64_t)gridDim.x * 256) {
+        const int64_t r = t / half, o = r * out.lddv + t - r * half;
+        const float v = split_sum(part + blockIdx.y * total + t, splits, all);
+        if (out.dvdt == NM_F32) ((float*)dV)[o] = v;
+        else ((uint16_t*)dV)[o] = (uint16_t)f32_to_bf16_bits(v);
+    }
+}
+
 // ------------------------------------------------------------------ host side
 // Splits of dX's sum (Rn / 64 stages).  Beside dV no block should run longer than the whole
 // call's share of a CU (at least 16 stages); alone, the count whose rounds take least.  A
@@ -822,6 +847,30 @@ static int grad_x_splits(int64_t M, int64_t K, int64_t Rn, bool with_v) {
         }
     }
     return best;
+}
+
+// Splits of dV's sum (the tokens, Mp / 64 stages) where its tiles, beside dX's blocks, leave CUs idle:
+// a stage is about 1.7 us, the partials' launch 6 and each megabyte of them 1.  Measured, plain and
+// gated: 2048 tokens of 1024 x 1024 62.8 -> 43.9 and 68.0 -> 55.7 us, 2000 of 512 x 512 51.8 -> 30.8 and
+// 60.0 -> 34.0; without the partials' price 1163 of 459 x 3600, gated, went from 46.7 to 59.2.
+// As many as nx = 0 gives is the most any call takes.
+static int grad_v_splits(int64_t M, int64_t K, int64_t R, int64_t Rn, int nmat, int64_t nx) {
+    const int64_t tiles = ceil_div(K, 256) * ceil_div(Rn, 256), ns = ceil_div(M, 64);
+    const double one_mb = (double)(nmat * R * (K / 2)) * 4e-6;
+    int best = 1;
+    double best_us = 1.7 * (double)ns;
+    for (int64_t n = 2; n * tiles <= device_cus() - nx && n <= ns / 4; ++n) {
+        const double us = 1.7 * (double)ceil_div(ns, n) + 6.0 + one_mb * (double)n;
+        if (us < best_us) {
+            best_us = us;
+            best = (int)n;
+        }
+    }
+    return best;
+}
+static size_t grad_v_part_bytes(int64_t M, int64_t K, int64_t R, int64_t Rn, int nmat) {
+    const int n = grad_v_splits(M, K, R, Rn, nmat, 0);
+    return n > 1 ? (size_t)n * (size_t)(nmat * R * (K / 2)) * 4 : 0;
 }
 
 // partials of dX over K columns: with splits, or a lifted dX' to fold
@@ -861,8 +910,8 @@ static bool ring_decodes(int64_t M, int64_t K, int64_t Rn, int Ns) {
 
 // Workspace of one backward call, in the order it is carved.
 struct GradWs {
-    size_t d = 0, dt = 0, xt = 0, wt = 0, part = 0;
-    size_t total() const { return d + dt + xt + wt + part; }
+    size_t d = 0, dt = 0, xt = 0, wt = 0, part = 0, vpart = 0;
+    size_t total() const { return d + dt + xt + wt + part + vpart; }
 };
 static int64_t lifted_width(int64_t K, int Ns) { return Ns ? K / (2 * Ns) * 4 * (Ns - 1) : K; }
 static GradWs grad_ws_layout(int64_t M, int64_t Korig, int64_t R, int Ns, int nmat) {
@@ -881,6 +930,7 @@ static GradWs grad_ws_layout(int64_t M, int64_t Korig, int64_t R, int Ns, int nm
     const bool dec = ring_decodes(M, K, Rn, Ns);
     if (!dec) w.wt = up256((size_t)(Korig * Rn * 2));
     w.part = up256(grad_x_part_bytes(M, dec ? K : Korig, Rn, dec && Ns != 0));
+    w.vpart = up256(grad_v_part_bytes(M, K, R, Rn, nmat));
     return w;
 }
 size_t grad_ws(int64_t M, int64_t K, int64_t R, int Ns, int nmat) { return grad_ws_layout(M, K, R, Ns, nmat).total(); }
@@ -965,7 +1015,7 @@ nm_status launch_grad(const GradIn& given, const GradOut& out, int nmat, void* w
     }
 #undef NM_LAYOUT
     GradArgs g{};
-    int nv = 0, splits = 1;
+    int nv = 0, splits = 1, vsplits = 1;
     for (int i = 0; i < 2; ++i) {
         g.vals[i] = in.vals[i];
         g.idx[i] = in.idx[i];
@@ -1008,6 +1058,13 @@ nm_status launch_grad(const GradIn& given, const GradOut& out, int nmat, void* w
         j.tiles_a = (int)ceil_div(in.Kl, 256);
         j.tiles_b = (int)ceil_div(Rn, 256);
         nv = j.tiles_a * j.tiles_b;
+        if (!few_tokens(in.M)) {
+            vsplits = grad_v_splits(in.M, in.Kl, in.R, Rn, nmat, g.nx);
+            j.spp = (int)ceil_div(j.nsteps, vsplits);
+            vsplits = (int)ceil_div(j.nsteps, j.spp);
+            nv *= vsplits;
+            g.vpart = vsplits > 1 ? (float*)((uint8_t*)PART + w.part) : nullptr;
+        }
         g.lddv = out.lddv;
         g.dvf32 = out.dvdt == NM_F32;
     }
@@ -1040,6 +1097,9 @@ nm_status launch_grad(const GradIn& given, const GradOut& out, int nmat, void* w
     if (g.part)
         hipLaunchKernelGGL(grad_reduce_kernel, dim3(grid_cap(ceil_div(in.M * in.K, 256), 8192)), dim3(256), 0, s, PART,
                            splits, in.M, in.K, Kx, Kx != in.K ? in.Ns : 0, out.dX, out.lddx, g.dxf32);
+    if (g.vpart)
+        hipLaunchKernelGGL(grad_reduce_v_kernel, dim3(grid_cap(ceil_div(in.R * in.Kl / 2, 256), 4096), (unsigned)nmat), dim3(256),
+                           0, s, g.vpart, vsplits, in.R, in.Kl / 2, out);
     return check_launch(nmat == 2 ? "nm_spmm_glu_backward" : "nm_spmm_backward");
 }
 

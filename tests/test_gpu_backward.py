@@ -28,10 +28,11 @@ def _np(t):
     return t.float().cpu().numpy().astype(np.float64)
 
 
-# (the last three: weights large enough that dX's tiles decode them, ragged everywhere)
+# (the last five: weights large enough that dX's tiles decode them, ragged everywhere, and many tokens of
+# small weights, which split dV's sum)
 SIZES = [(1, 1, 16), (1, 64, 64), (3, 70, 48), (17, 33, 272), (64, 64, 64), (65, 130, 528), (129, 200, 1024),
          (200, 1000, 272), (300, 257, 512), (513, 520, 784),
-         (130, 4100, 4112), (257, 8195, 2064), (600, 2111, 8208)]
+         (130, 4100, 4112), (257, 8195, 2064), (600, 2111, 8208), (1400, 130, 272), (900, 301, 528)]
 
 
 @pytest.mark.parametrize("Mt,R,K", SIZES)
@@ -98,7 +99,7 @@ def test_glu_backward_integers_exact(nm, Mt, R, K, extra):
 # dX's tiles; row lengths that are no multiple of 8 among them (N = 3, 5, 7)
 LIFTED = [(3, 1, 40, 12), (3, 140, 130, 540), (4, 17, 33, 224), (4, 300, 257, 512), (5, 64, 70, 170), (5, 520, 260, 1310),
           (6, 33, 100, 528), (6, 700, 200, 480), (7, 100, 130, 308), (7, 800, 120, 644), (8, 128, 65, 448), (8, 200, 90, 320),
-          (4, 130, 6161, 2080), (7, 300, 4100, 2548)]
+          (4, 130, 6161, 2080), (7, 300, 4100, 2548), (4, 1100, 70, 160)]
 
 
 @pytest.mark.parametrize("Ns,Mt,R,K", LIFTED)
