@@ -468,8 +468,14 @@ nm_status nm_quant_lift(const void* X, nm_dtype xdt, int64_t Mtok, int64_t K, in
     return check_launch(fn);
 }
 
+// Whether a product over K columns with pattern Ns exists; the queries answer 0 for the others, whose
+// lifted width may be 0 (the call refuses them).
+static bool product_shape_ok(int64_t K, int Ns) {
+    return K > 0 && (Ns == 0 || (Ns >= 3 && Ns <= 8 && K % (2 * Ns) == 0));
+}
+
 size_t nm_spmm_workspace(int64_t Mtok, int64_t K, int64_t R, int Ns, nm_dtype xdt) {
-    if (Mtok <= 0 || K <= 0 || R <= 0) return 0;
+    if (Mtok <= 0 || R <= 0 || !product_shape_ok(K, Ns)) return 0;
     return spmm_ws(Mtok, K, R, Ns, xdt);
 }
 
@@ -640,7 +646,7 @@ nm_status nm_spmm_bitmap(const void* X, int64_t Mtok, int64_t K, int64_t ldx, co
 }
 
 size_t nm_spmm_lowrank_workspace(int64_t Mtok, int64_t K, int64_t R, int Ns, int rank) {
-    if (Mtok <= 0 || K <= 0 || R <= 0 || rank <= 0) return 0;
+    if (Mtok <= 0 || R <= 0 || rank <= 0 || !product_shape_ok(K, Ns)) return 0;
     return spmm_lowrank_ws(Mtok, K, R, Ns, rank);
 }
 
@@ -682,7 +688,7 @@ nm_status nm_spmm_lowrank(const void* X, int64_t Mtok, int64_t K, int64_t ldx, c
 }
 
 size_t nm_spmm_glu_workspace(int64_t Mtok, int64_t K, int64_t R, int Ns, nm_dtype xdt) {
-    if (Mtok <= 0 || K <= 0 || R <= 0) return 0;
+    if (Mtok <= 0 || R <= 0 || !product_shape_ok(K, Ns)) return 0;
     return glu_ws(Mtok, K, R, Ns, xdt);
 }
 
@@ -749,10 +755,12 @@ nm_status nm_spmm_glu(const void* X, nm_dtype xdt, int64_t Mtok, int64_t K, int6
     return launch_glu(g, ws, (hipStream_t)stream);
 }
 
+constexpr int64_t kBackwardMost = 1 << 21;   // tokens, columns, rows
+
 // Checks and launch of both backward calls; nmat 2: the gated block (G and U given).
 static nm_status backward_impl(const char* fn, GradIn in, GradOut out, int nmat, void* ws, size_t ws_bytes,
                                nm_stream_t stream) {
-    const int64_t M = in.M, K = in.K, R = in.R, most = 1 << 21;
+    const int64_t M = in.M, K = in.K, R = in.R, most = kBackwardMost;
     NM_REQ(M >= 0 && K >= 0 && R >= 0, NM_ERR_SHAPE, "%s: negative size", fn);
     NM_REQ(M <= most && K <= most && R <= most, NM_ERR_SHAPE, "%s: sizes up to 2^21", fn);
     const int Ns = in.Ns;
@@ -806,8 +814,9 @@ static nm_status backward_impl(const char* fn, GradIn in, GradOut out, int nmat,
 }
 
 static size_t backward_ws(int64_t Mtok, int64_t K, int64_t R, int Ns, int nmat) {
-    const bool ok = Ns == 0 || (Ns >= 3 && Ns <= 8 && K % (2 * Ns) == 0);
-    return ok ? grad_ws(Mtok, K, R, Ns, nmat) : 0;   // the call refuses the others
+    // the call refuses the others
+    const bool ok = product_shape_ok(K, Ns) && Mtok <= kBackwardMost && K <= kBackwardMost && R <= kBackwardMost;
+    return ok ? grad_ws(Mtok, K, R, Ns, nmat) : 0;
 }
 
 size_t nm_spmm_backward_workspace(int64_t Mtok, int64_t K, int64_t R, int Ns) { return backward_ws(Mtok, K, R, Ns, 1); }
