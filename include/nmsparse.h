@@ -451,7 +451,9 @@ nm_status nm_spmm_glu_backward(const void* dH, int64_t lddh, const void* G, cons
  *   p  = p (1 - l weight_decay) - l / (1 - beta1^step) m / (sqrt(v / (1 - beta2^step)) + eps),
  *   l  = lr lr_scale,
  * in f32; m, v and sqrt(v) with one rounding per operation in the order written ((1 - beta2) g'
- * first, then times g'), every stored value rounded once.  grad_scale: device f32 [1] (a clipping factor or the
+ * first, then times g'), every stored value rounded once.  p's update takes the denominator as
+ * fma(sqrt(v), 1 / sqrt(1 - beta2^step), eps) and an approximate reciprocal of it (about 1e-7 relative).
+ * grad_scale: device f32 [1] (a clipping factor or the
  * inverse of a loss scale), or NULL for 1.  step counts from 1.
  *   p: pdt F32 or BF16; g: gdt F32 or BF16; copy: bf16 copy of the new p (the packed values a
  *   product reads beside f32 masters), or NULL.

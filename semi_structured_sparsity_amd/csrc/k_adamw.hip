@@ -3,8 +3,8 @@
 //   p  = p (1 - lr wd) - lr / (1 - b1^t) * m / (sqrt(v / (1 - b2^t)) + eps),
 // all in f32.  m, v and r = sqrt(v) take one rounding per operation in the order written, with
 // no contraction, as does the quotient that picks a code below: codes are decided by them, so
-// every correct evaluation of this order gives the same codes.  The parameter's update uses
-// fused multiply-adds and the hardware's reciprocal (about 1e-7 relative).
+// every correct evaluation of this order gives the same codes.  The parameter's update takes the
+// denominator as fma(r, 1 / sqrt(1 - b2^t), eps) and the hardware's reciprocal of it (about 1e-7 relative).
 //
 // States in 8 bits: m and r = sqrt(v) are e4m3 codes with one f32 scale per 256 consecutive
 // elements, scale = max |x| * (1 / 448), code = the e4m3 value nearest x * (448 * (1 / max)).  e4m3
@@ -230,8 +230,9 @@ __device__ __forceinline__ void adamw_update(const AdamWArgs& a, const AdamWDesc
         const float g = x.g[e] * gs;
         m[e] = __fadd_rn(__fmul_rn(a.b1, m[e]), __fmul_rn(a.c1, g));
         v[e] = __fadd_rn(__fmul_rn(a.b2, v[e]), __fmul_rn(__fmul_rn(a.c2, g), g));
-        // 8-bit states: correctly rounded, it decides codes; otherwise the hardware's (1 ulp)
-        r[e] = S8 ? sqrtf(v[e]) : __builtin_amdgcn_sqrtf(v[e]);
+        // correctly rounded: it decides codes, and the hardware's root takes v below 2^-126 for zero (an
+        // update of m over eps then)
+        r[e] = sqrtf(v[e]);
         const float d = __builtin_fmaf(r[e], a.rbc2, a.eps);
         p[e] = __builtin_fmaf(-t.alpha, m[e] * __builtin_amdgcn_rcpf(d), x.p[e] * t.decay);
     }
