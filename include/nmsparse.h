@@ -466,7 +466,7 @@ nm_status nm_spmm_glu_backward(const void* dH, int64_t lddh, const void* G, cons
  *   the m and v of before that rounding.  Zeroed codes and scales are the zero state.
  * tensors is a HOST array, read before the call returns; the tensors must not overlap each
  * other.  Element-aligned pointers are accepted; 16-byte aligned ones (8-byte for codes) are
- * read and written in whole vectors.  Allocates nothing, one launch per 44 tensors. */
+ * read and written in whole vectors.  Allocates nothing; a launch takes 44 tensors and 2^35 elements. */
 typedef struct {
     void* p;
     const void* g;

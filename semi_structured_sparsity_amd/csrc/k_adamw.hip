@@ -17,10 +17,11 @@
 // The step is bound by HBM: per parameter 8 B (f32 p read and written) or 4 B (bf16), the
 // gradient's 2 or 4 B, 16 B of f32 states or 4 + 4/128 B of codes and scales, 2 B of the
 // bf16 copy.  Descriptors travel as kernel arguments (no table upload, graph capture
-// safe), kMaxTensors a launch; a block finds its tensor by a binary search over the
+// safe), kMaxTensors a launch, a tensor that passes a launch's most blocks in pieces; a block finds its tensor by a binary search over the
 // tensors' first block numbers, in scalar registers.
 #include <math.h>
 
+#include "nm_adamw_pieces.h"
 #include "nm_internal.h"
 
 namespace nm {
@@ -315,48 +316,43 @@ nm_status launch_adamw(const nm_adamw_tensor* ts, int count, nm_dtype sdt, doubl
     a.rbc2 = (float)(1.0 / sqrt(bc2));
     a.eps = (float)eps;
     const bool s8 = sdt == NM_FP8;
-    const int64_t most = (int64_t)1 << 30;   // blocks of one launch
     int k = 0;
     int64_t blocks = 0;
-    auto flush = [&]() -> nm_status {
-        if (!k) return NM_OK;
-        a.count = k;
-        a.first[k] = (uint32_t)blocks;
-        if (s8) hipLaunchKernelGGL(adamw_kernel<true>, dim3((unsigned)blocks), dim3(256), 0, s, a);
-        else hipLaunchKernelGGL(adamw_kernel<false>, dim3((unsigned)blocks), dim3(256), 0, s, a);
-        k = 0;
-        blocks = 0;
-        return check_launch("nm_adamw");
-    };
-    for (int i = 0; i < count; ++i) {
-        const nm_adamw_tensor& t = ts[i];
-        if (t.n == 0) continue;
-        const int64_t nb = ceil_div(t.n, kChunk);
-        if (k == kMaxTensors || blocks + nb > most) {
-            const nm_status st = flush();
-            if (st != NM_OK) return st;
-        }
-        const double l = lr * (double)t.lr_scale;
-        AdamWDesc& d = a.t[k];
-        d.p = t.p;
-        d.g = t.g;
-        d.m = t.m;
-        d.v = t.v;
-        d.ms = t.m_scale;
-        d.vs = t.v_scale;
-        d.c = (uint16_t*)t.copy;
-        d.n = t.n;
-        d.alpha = (float)(l / bc1);
-        d.decay = (float)(1.0 - l * (double)t.weight_decay);
-        const uintptr_t al = (uintptr_t)t.p | (uintptr_t)t.g | (uintptr_t)t.copy |
-                             (s8 ? ((uintptr_t)t.m | (uintptr_t)t.v) << 1 : (uintptr_t)t.m | (uintptr_t)t.v);
-        d.flags = (t.pdt == NM_BF16 ? kPBf16 : 0u) | (t.gdt == NM_BF16 ? kGBf16 : 0u) | ((al & 15u) == 0 ? kVec : 0u);
-        d.pad = 0;
-        a.first[k] = (uint32_t)blocks;
-        blocks += nb;
-        ++k;
-    }
-    return flush();
+    nm_status st = NM_OK;
+    adamw_pieces(
+        count, kChunk, kMaxTensors, kAdamWMostBlocks, [&](int i) { return ts[i].n; },
+        [&](int i, int64_t at, int64_t n, int64_t block) {
+            const nm_adamw_tensor& t = ts[i];
+            const int64_t ps = t.pdt == NM_BF16 ? 2 : 4, gs = t.gdt == NM_BF16 ? 2 : 4, ss = s8 ? 1 : 4;
+            const double l = lr * (double)t.lr_scale;
+            AdamWDesc& d = a.t[k];
+            d.p = (uint8_t*)t.p + at * ps;
+            d.g = (const uint8_t*)t.g + at * gs;
+            d.m = (uint8_t*)t.m + at * ss;
+            d.v = (uint8_t*)t.v + at * ss;
+            d.ms = s8 ? t.m_scale + at / 256 : nullptr;
+            d.vs = s8 ? t.v_scale + at / 256 : nullptr;
+            d.c = t.copy ? (uint16_t*)t.copy + at : nullptr;
+            d.n = n;
+            d.alpha = (float)(l / bc1);
+            d.decay = (float)(1.0 - l * (double)t.weight_decay);
+            const uintptr_t al = (uintptr_t)t.p | (uintptr_t)t.g | (uintptr_t)t.copy |
+                                 (s8 ? ((uintptr_t)t.m | (uintptr_t)t.v) << 1 : (uintptr_t)t.m | (uintptr_t)t.v);
+            d.flags = (t.pdt == NM_BF16 ? kPBf16 : 0u) | (t.gdt == NM_BF16 ? kGBf16 : 0u) | ((al & 15u) == 0 ? kVec : 0u);
+            d.pad = 0;
+            a.first[k++] = (uint32_t)block;
+            blocks = block + ceil_div(n, kChunk);
+        },
+        [&]() {
+            a.count = k;
+            a.first[k] = (uint32_t)blocks;
+            if (s8) hipLaunchKernelGGL(adamw_kernel<true>, dim3((unsigned)blocks), dim3(256), 0, s, a);
+            else hipLaunchKernelGGL(adamw_kernel<false>, dim3((unsigned)blocks), dim3(256), 0, s, a);
+            k = 0;
+            st = check_launch("nm_adamw");
+            return st == NM_OK;
+        });
+    return st;
 }
 
 }  // namespace nm
