@@ -76,7 +76,7 @@ def train(width: int = 1024, hidden: int = 2816, tokens: int = 512, steps: int =
         dh, _ = nm.nm_spmm_backward(dy, h, vals["d"], idx["d"], Ns=Ns, out_dv=grad["d"], ws=ws)
         nm.nm_spmm_glu_backward(dh, pre_g, pre_u, x, vals["g"], idx["g"], vals["u"], idx["u"], Ns=Ns,
                                 want_dx=False, out_dv=(grad["g"], grad["u"]), ws=ws)
-        nm.nm_adamw(trained, lr=lr * min(1.0, step / 10), step=step)
+        nm.nm_adamw_unbiased(trained, lr=lr * min(1.0, step / 10), step=step, seed=seed)
     after = loss_of(held, held_want)
     return before, after, forward(held[:1], False)[0], forward(held, False)[0]
 

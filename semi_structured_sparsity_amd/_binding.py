@@ -13,6 +13,7 @@ Each C entry point is exposed twice:
 from __future__ import annotations
 
 import ctypes
+import warnings
 from pathlib import Path
 
 import torch
@@ -94,6 +95,7 @@ SIGNATURES = {
     "nm_spmm_glu_backward": (_I, [_P, _I64, _P, _P, _I64, _I, _P, _I64, _I64, _I64, _P, _P, _P, _P, _I64, _I64, _I64, _I,
                                   _P, _I, _I64, _P, _P, _I, _I64, _P, _SZ, _P]),
     "nm_adamw": (_I, [_P, _I, _I, _D, _D, _D, _D, _I64, _P, _P]),
+    "nm_adamw_unbiased": (_I, [_P, _I, _D, _D, _D, _D, _I64, _U64, _P, _P]),
 }
 for _name, (_res, _args) in SIGNATURES.items():
     _fn = getattr(raw, _name)
@@ -608,16 +610,44 @@ class AdamWTensors:
             raise ValueError("the tensors of a step must not overlap")
 
 
-def nm_adamw(tensors: AdamWTensors, lr: float, step: int, beta1: float = 0.9, beta2: float = 0.999, eps: float = 1e-8,
-             grad_scale: torch.Tensor | None = None) -> None:
-    """One AdamW step over every tensor of the list, in place; step counts from 1."""
+# the largest beta2 that nearest 8-bit codes follow falling gradients at
+NM_ADAMW_NEAREST_BETA2 = 0.95
+
+
+def _adamw_ready(tensors: AdamWTensors, grad_scale: torch.Tensor | None) -> bool:
     if grad_scale is not None and (grad_scale.dtype != torch.float32 or grad_scale.numel() != 1):
         raise ValueError("grad_scale must be one f32 value on the device")
     if tensors.count == 0:
-        return
+        return False
     if grad_scale is not None and grad_scale.device != tensors.device:
         raise ValueError(f"grad_scale must be on {tensors.device}, got {grad_scale.device}")
+    return True
+
+
+def nm_adamw(tensors: AdamWTensors, lr: float, step: int, beta1: float = 0.9, beta2: float = 0.999, eps: float = 1e-8,
+             grad_scale: torch.Tensor | None = None) -> None:
+    """One AdamW step over every tensor of the list, in place; step counts from 1.  8-bit states are held
+    to the nearest codes, which is for beta2 <= 0.95 only (a warning beyond): use nm_adamw_unbiased there."""
+    if not _adamw_ready(tensors, grad_scale):
+        return
+    if tensors.sdt == NM_FP8 and beta2 > NM_ADAMW_NEAREST_BETA2:
+        warnings.warn(f"nearest 8-bit states do not follow falling gradients with beta2 {beta2} (above "
+                      f"{NM_ADAMW_NEAREST_BETA2}): use nm_adamw_unbiased", stacklevel=2)
     st = raw.nm_adamw(tensors.address, tensors.count, tensors.sdt, lr, beta1, beta2, eps, step, _ptr(grad_scale),
                       torch._C._cuda_getCurrentRawStream(tensors.device.index))
+    if st:
+        _check(st)
+
+
+def nm_adamw_unbiased(tensors: AdamWTensors, lr: float, step: int, seed: int = 0, beta1: float = 0.9, beta2: float = 0.999,
+                      eps: float = 1e-8, grad_scale: torch.Tensor | None = None) -> None:
+    """nm_adamw on 8-bit states with unbiased codes, for any beta2.  The codes are a function of seed, step,
+    tensor and element."""
+    if tensors.sdt != NM_FP8 and tensors.count:
+        raise ValueError("unbiased codes are of 8-bit states")
+    if not _adamw_ready(tensors, grad_scale):
+        return
+    st = raw.nm_adamw_unbiased(tensors.address, tensors.count, lr, beta1, beta2, eps, step, seed & (2 ** 64 - 1),
+                               _ptr(grad_scale), torch._C._cuda_getCurrentRawStream(tensors.device.index))
     if st:
         _check(st)

@@ -875,9 +875,9 @@ nm_status nm_spmm_glu_backward(const void* dH, int64_t lddh, const void* G, cons
     return backward_impl("nm_spmm_glu_backward", in, out, 2, ws, ws_bytes, stream);
 }
 
-nm_status nm_adamw(const nm_adamw_tensor* tensors, int count, nm_dtype sdt, double lr, double beta1, double beta2,
-                   double eps, int64_t step, const float* grad_scale, nm_stream_t stream) {
-    const char* fn = "nm_adamw";
+static nm_status adamw_impl(const char* fn, const nm_adamw_tensor* tensors, int count, nm_dtype sdt, double lr, double beta1,
+                            double beta2, double eps, int64_t step, const uint64_t* seed, const float* grad_scale,
+                            nm_stream_t stream) {
     NM_REQ(count >= 0, NM_ERR_SHAPE, "%s: negative count", fn);
     NM_REQ(sdt == NM_F32 || sdt == NM_FP8, NM_ERR_DTYPE, "%s: states must be f32 or fp8 codes", fn);
     NM_REQ(step >= 1, NM_ERR_SHAPE, "%s: step counts from 1", fn);
@@ -912,7 +912,17 @@ nm_status nm_adamw(const nm_adamw_tensor* tensors, int count, nm_dtype sdt, doub
             for (int b = a + 1; b < 8; ++b)
                 NM_REQ(!overlap(r[a], r[b]), NM_ERR_ALIAS, "%s: tensor %d: its arrays overlap", fn, i);
     }
-    return launch_adamw(tensors, count, sdt, lr, beta1, beta2, eps, step, grad_scale, (hipStream_t)stream);
+    return launch_adamw(tensors, count, sdt, lr, beta1, beta2, eps, step, seed, grad_scale, (hipStream_t)stream);
+}
+
+nm_status nm_adamw(const nm_adamw_tensor* tensors, int count, nm_dtype sdt, double lr, double beta1, double beta2,
+                   double eps, int64_t step, const float* grad_scale, nm_stream_t stream) {
+    return adamw_impl("nm_adamw", tensors, count, sdt, lr, beta1, beta2, eps, step, nullptr, grad_scale, stream);
+}
+
+nm_status nm_adamw_unbiased(const nm_adamw_tensor* tensors, int count, double lr, double beta1, double beta2, double eps,
+                            int64_t step, uint64_t seed, const float* grad_scale, nm_stream_t stream) {
+    return adamw_impl("nm_adamw_unbiased", tensors, count, NM_FP8, lr, beta1, beta2, eps, step, &seed, grad_scale, stream);
 }
 
 }  // extern "C"

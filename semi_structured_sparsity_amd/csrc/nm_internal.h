@@ -134,7 +134,7 @@ __device__ __forceinline__ uint32_t top6of8_bits(const float (&k)[8]) {
 // SplitMix64 (Steele, Lea and Flood, OOPSLA 2014) as a counter-based
 // generator: output number i of a generator seeded with s is the variant-13
 // finaliser applied to s + (i+1) * 0x9E3779B97F4A7C15.
-__device__ __forceinline__ uint64_t splitmix64_at(uint64_t seed, uint64_t i) {
+__host__ __device__ __forceinline__ uint64_t splitmix64_at(uint64_t seed, uint64_t i) {
     uint64_t z = seed + (i + 1ull) * 0x9E3779B97F4A7C15ull;
     z = (z ^ (z >> 30)) * 0xBF58476D1CE4E5B9ull;
     z = (z ^ (z >> 27)) * 0x94D049BB133111EBull;
@@ -360,8 +360,9 @@ size_t grad_ws(int64_t M, int64_t K, int64_t R, int Ns, int nmat);
 // nmat: 1, or 2 for the gated block
 nm_status launch_grad(const GradIn& in, const GradOut& out, int nmat, void* ws, hipStream_t s);
 // optimiser
+// seed: unbiased codes of 8-bit states, or null for nearest ones
 nm_status launch_adamw(const nm_adamw_tensor* ts, int count, nm_dtype sdt, double lr, double beta1, double beta2,
-                       double eps, int64_t step, const float* grad_scale, hipStream_t s);
+                       double eps, int64_t step, const uint64_t* seed, const float* grad_scale, hipStream_t s);
 // Hutchinson
 size_t hutch_ws(int64_t n, int64_t K, int64_t R, int probes);
 size_t hutch_score_ws(int64_t n, int64_t K, int64_t R, int probes);
