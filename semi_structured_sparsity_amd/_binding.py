@@ -12,6 +12,7 @@ Each C entry point is exposed twice:
 """
 from __future__ import annotations
 
+import bisect
 import ctypes
 import warnings
 from pathlib import Path
@@ -603,11 +604,19 @@ class AdamWTensors:
                 _ptr(p), _ptr(grads[i]), _ptr(m[i]), _ptr(v[i]), _ptr(m_scale[i]) if f8 else None,
                 _ptr(v_scale[i]) if f8 else None, None if copies is None else _ptr(copies[i]), k, dtype_code(p),
                 dtype_code(grads[i]), lr_scale[i], weight_decay[i])
-        # what a step writes, by address: a tensor listed twice would be updated by two blocks at once
+        # what a step writes, by address: a tensor listed twice would be updated by two blocks at once, and a
+        # gradient inside another tensor's would be read while it is written (inside its own: the call refuses)
         written = [params, m, v, copies] + ([m_scale, v_scale] if self.sdt == NM_FP8 else [])
-        spans = sorted((t.data_ptr(), t.data_ptr() + t.nbytes) for ts in written if ts is not None for t in ts if t.numel())
+        spans = sorted((t.data_ptr(), t.data_ptr() + t.nbytes, i) for ts in written if ts is not None
+                       for i, t in enumerate(ts) if t.numel())
         if any(a[1] > b[0] for a, b in zip(spans, spans[1:])):
             raise ValueError("the tensors of a step must not overlap")
+        starts = [a for a, _, _ in spans]
+        for i, t in enumerate(grads):
+            a, b = t.data_ptr(), t.data_ptr() + t.nbytes
+            for k in range(max(bisect.bisect_right(starts, a) - 1, 0), bisect.bisect_left(starts, b)):
+                if t.numel() and spans[k][1] > a and spans[k][2] != i:
+                    raise ValueError(f"grads[{i}] overlaps what the step writes of tensor {spans[k][2]}")
 
 
 # the largest beta2 that nearest 8-bit codes follow falling gradients at
