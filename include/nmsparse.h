@@ -14,6 +14,8 @@
  *    on `stream` (a hipStream_t passed as void*, NULL = the null stream) and the
  *    call returns immediately.  NM_OK means "enqueued"; results are valid once
  *    the caller synchronises the stream.
+ *  - The pointers and the stream belong to the current device: the null stream is the current
+ *    device's.  (The Python wrappers make their tensors' device current.)
  *  - Every argument is validated before anything is enqueued; on an error
  *    nothing is written and the status says why.  nm_last_error() then returns
  *    a message (thread-local, valid until the next call on this thread).

@@ -14,6 +14,7 @@ from __future__ import annotations
 
 import bisect
 import ctypes
+import functools
 import warnings
 from pathlib import Path
 
@@ -618,6 +619,9 @@ class AdamWTensors:
                 if t.numel() and spans[k][1] > a and spans[k][2] != i:
                     raise ValueError(f"grads[{i}] overlaps what the step writes of tensor {spans[k][2]}")
 
+    def get_device(self) -> int:
+        return -1 if self.device is None else self.device.index
+
 
 # the largest beta2 that nearest 8-bit codes follow falling gradients at
 NM_ADAMW_NEAREST_BETA2 = 0.95
@@ -660,3 +664,26 @@ def nm_adamw_unbiased(tensors: AdamWTensors, lr: float, step: int, seed: int = 0
                                _ptr(grad_scale), torch._C._cuda_getCurrentRawStream(tensors.device.index))
     if st:
         _check(st)
+
+
+# ---------------------------------------------------------------- the current device
+def _on_device(fn):
+    """fn with its tensors' device current: the library launches on the current device, and a default
+    stream is the same 0 on every one."""
+    @functools.wraps(fn)
+    def call(*args, **kwargs):
+        first = args[0] if args else next((x for x in kwargs.values() if isinstance(x, (torch.Tensor, AdamWTensors))), None)
+        try:
+            index = first.get_device()
+        except AttributeError:      # no tensor: fn says so
+            index = -1
+        if index < 0 or index == torch._C._cuda_getDevice():
+            return fn(*args, **kwargs)
+        with torch.cuda.device(index):
+            return fn(*args, **kwargs)
+    return call
+
+
+for _name in SIGNATURES:
+    if not _name.endswith("_workspace") and _name not in ("nm_abi_version", "nm_last_error"):
+        globals()[_name] = _on_device(globals()[_name])
