@@ -420,7 +420,10 @@ nm_status nm_spmm_glu(const void* X, nm_dtype xdt, int64_t Mtok, int64_t K, int6
  * Ns: 0 for plain 2:4 (K' = K), or 3 <= Ns <= 8 for weights decomposed into windows over the
  * lifted width K' = (2 - 2/Ns) K.  dV has the layout of vals; a padding slot's entry is the
  * derivative at its position (W is the sum of what its slots place at a
- * column; dX may take a sum of two nonzero ones rounded to bf16).  All
+ * column; dX may take a sum of two nonzero ones rounded to bf16).  Such an entry is the gradient of a
+ * weight outside the mask: a step under the mask zeroes it, else an optimiser brings that weight back.
+ * nm_pack (nm_slide_decompose) of a weight of ones under the same mask gives 1 at the slots
+ * of kept weights and 0 at padding; masks of exactly N of M have no padding.  All
  * sums in f32 in a fixed order, one rounding.  dY: bf16 [Mtok, R] (lddy), any alignment of 2
  * bytes (16-byte aligned rows are read faster).  X, vals: bf16 with 16-byte aligned rows; idx
  * 4-byte aligned; dV 16-byte aligned rows.  Requires K % 2Ns == 0, K' % 16 == 0 and

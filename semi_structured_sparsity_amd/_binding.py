@@ -552,6 +552,16 @@ def nm_spmm_glu_backward(dH: torch.Tensor, G: torch.Tensor, U: torch.Tensor, X: 
     return dX, dVg, dVu
 
 
+def kept_slots(mask: torch.Tensor, K: int, Ns: int = 0) -> torch.Tensor:
+    """Which slots of a weight packed 2:4 (or decomposed, Ns >= 3) under mask hold kept weights: bool, the shape of
+    vals.  The others are padding, of groups with fewer mask bits than slots, and their gradients are those of
+    pruned weights: a training step zeroes them (dvals.masked_fill_(~kept, 0)), or the optimiser brings the weights
+    back.  A mask of exactly N of M has none."""
+    ones = torch.ones((mask.shape[0], K), dtype=torch.int8, device=mask.device)
+    vals, _ = nm_slide_decompose(ones, mask, Ns) if Ns else nm_pack(ones, mask, 2, 4)
+    return vals.view(torch.bool)
+
+
 class _AdamWTensor(ctypes.Structure):
     _fields_ = [("p", _P), ("g", _P), ("m", _P), ("v", _P), ("m_scale", _P), ("v_scale", _P), ("copy", _P), ("n", _I64),
                 ("pdt", _I), ("gdt", _I), ("lr_scale", _F), ("weight_decay", _F)]
