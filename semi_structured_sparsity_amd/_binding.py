@@ -571,7 +571,9 @@ class AdamWTensors:
     """The tensors of an optimiser, as nm_adamw takes them: lists of contiguous parameters,
     gradients and states (f32, or float8_e4m3fn codes with f32 scales per 256 elements), kept
     for as long as the object lives.  copies: bf16 copies of the parameters, or None; lr_scale
-    and weight_decay: one number, or one per tensor.  Build it once and use it every step."""
+    and weight_decay: one number, or one per tensor.  Build it once and use it every step: it holds
+    the tensors' addresses (about 4 us a tensor to build, a launch of many is 6), so gradients go into the same tensors
+    every step (out_dv of the backward calls); tensors allocated anew need a new list."""
 
     def __init__(self, params, grads, m, v, m_scale=None, v_scale=None, copies=None, lr_scale=1.0, weight_decay=0.0):
         n = len(params)
@@ -594,39 +596,42 @@ class AdamWTensors:
             raise ValueError("8-bit states need m_scale and v_scale")
         self.count, self.array = n, (_AdamWTensor * max(n, 1))()
         self.address = ctypes.addressof(self.array)
+        f8, spans, read = self.sdt == NM_FP8, [], []      # (first byte, past the last, tensor) of what a step writes, and of the gradients
         for i in range(n):
-            p, k = params[i], params[i].numel()
+            p, k, dev = params[i], params[i].numel(), params[i].device
             for name, t in lists.items():
-                if t is None or (self.sdt == NM_F32 and name.endswith("scale")):
+                scale = name.endswith("scale")
+                if t is None or (scale and not f8):
                     continue
-                want = (k + 255) // 256 if name.endswith("scale") else k
-                if t[i].numel() != want or not t[i].is_contiguous() or t[i].device != p.device:
-                    raise ValueError(f"{name}[{i}]: {want} contiguous elements on {p.device} expected")
-            if not p.is_contiguous() or p.device != self.device:
+                want = (k + 255) // 256 if scale else k
+                if t[i].numel() != want or not t[i].is_contiguous() or t[i].device != dev:
+                    raise ValueError(f"{name}[{i}]: {want} contiguous elements on {dev} expected")
+            if not p.is_contiguous() or dev != self.device:
                 raise ValueError(f"params[{i}] must be contiguous and on {self.device}")
             if copies is not None and copies[i].dtype != torch.bfloat16:
                 raise ValueError("copies are bf16")
-            if self.sdt == NM_FP8 and (m_scale[i].dtype != torch.float32 or v_scale[i].dtype != torch.float32):
+            if f8 and (m_scale[i].dtype != torch.float32 or v_scale[i].dtype != torch.float32):
                 raise ValueError("scales are float32")
-            if any(t.dtype not in (torch.float32, torch.bfloat16) for t in (p, grads[i])):
+            pdt, gdt = _DT.get(p.dtype), _DT.get(grads[i].dtype)
+            if pdt not in (NM_F32, NM_BF16) or gdt not in (NM_F32, NM_BF16):
                 raise ValueError(f"params[{i}] and its gradient must be float32 or bfloat16")
-            f8 = self.sdt == NM_FP8
-            self.array[i] = _AdamWTensor(
-                _ptr(p), _ptr(grads[i]), _ptr(m[i]), _ptr(v[i]), _ptr(m_scale[i]) if f8 else None,
-                _ptr(v_scale[i]) if f8 else None, None if copies is None else _ptr(copies[i]), k, dtype_code(p),
-                dtype_code(grads[i]), lr_scale[i], weight_decay[i])
+            at = (_ptr(p), _ptr(grads[i]), _ptr(m[i]), _ptr(v[i]), _ptr(m_scale[i]) if f8 else None,
+                  _ptr(v_scale[i]) if f8 else None, None if copies is None else _ptr(copies[i]))
+            self.array[i] = _AdamWTensor(*at, k, pdt, gdt, lr_scale[i], weight_decay[i])
+            if k:
+                es, ss, blocks = (4, 2)[pdt], 1 if f8 else 4, (k + 255) // 256
+                read.append((at[1], at[1] + k * (4, 2)[gdt], i))
+                spans += [(a, a + b, i) for a, b in ((at[0], k * es), (at[2], k * ss), (at[3], k * ss), (at[4], 4 * blocks),
+                                                     (at[5], 4 * blocks), (at[6], 2 * k)) if a is not None]
         # what a step writes, by address: a tensor listed twice would be updated by two blocks at once, and a
         # gradient inside another tensor's would be read while it is written (inside its own: the call refuses)
-        written = [params, m, v, copies] + ([m_scale, v_scale] if self.sdt == NM_FP8 else [])
-        spans = sorted((t.data_ptr(), t.data_ptr() + t.nbytes, i) for ts in written if ts is not None
-                       for i, t in enumerate(ts) if t.numel())
+        spans.sort()
         if any(a[1] > b[0] for a, b in zip(spans, spans[1:])):
             raise ValueError("the tensors of a step must not overlap")
         starts = [a for a, _, _ in spans]
-        for i, t in enumerate(grads):
-            a, b = t.data_ptr(), t.data_ptr() + t.nbytes
+        for a, b, i in read:
             for k in range(max(bisect.bisect_right(starts, a) - 1, 0), bisect.bisect_left(starts, b)):
-                if t.numel() and spans[k][1] > a and spans[k][2] != i:
+                if spans[k][1] > a and spans[k][2] != i:
                     raise ValueError(f"grads[{i}] overlaps what the step writes of tensor {spans[k][2]}")
 
     def get_device(self) -> int:
