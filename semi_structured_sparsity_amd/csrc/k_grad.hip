@@ -1,4 +1,4 @@
-// Gradients of the sparse layer and of the gated feed-forward block (bf16, plain 2:4).
+// Gradients of the sparse layer and of the gated feed-forward block (bf16, 2:4 and lifted (2N-2):2N).
 //
 // For y = x W^T with W [R, K] packed 2:4, and for a gated block with pre-activations
 // G = x Wg^T, U = x Wu^T, H = act(G) . U:
@@ -203,7 +203,7 @@ __device__ __forceinline__ void glu_grad_tile(PairTile& tile, const LayoutArgs& 
 // 64 rows x 128 columns of a packed 2:4 weight (a line of values per row) -> WT [K, Rn] at columns
 // off + r (rows past R: zero).  Thread (c, pair): rows 2 pair, 2 pair + 1, columns 16 c ..: 8
 // values and 16 bits of positions per row; K is a multiple of 16.
-// A lifted weight's copy has the original columns (a third to an eighth fewer): a tile holds whole
+// A lifted weight's copy has the original columns (a quarter fewer at N = 3, three sevenths at N = 8): a tile holds whole
 // groups, and a column under two windows is their sum, rounded to bf16 (exact where one of them is
 // zero, as in any decomposed weight).
 __device__ __forceinline__ void decode_tile(PairTile& tile, SpreadTable& table, const LayoutArgs& a, int mat, int ti, int tj) {

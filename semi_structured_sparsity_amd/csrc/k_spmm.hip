@@ -2777,7 +2777,7 @@ constexpr int kGluX = 16 * 1024;
 //   kind 1: K-split ring, 32 features x 32 or 64 tokens (up to 64 tokens, 128 of one-byte codes)
 //   kind 2: ring tiles of 128 features x 128 tokens (narrow) or x 256 tokens (big), or big ones
 //           on the first features and narrow ones on the rest
-//   kind 0: none applies (K off the stage grid, unaligned index rows): two plain products
+//   kind 0: none applies (offsets past 32 bits; whole-stage widths with index rows off 16 bytes): two plain products
 struct GluPlan {
     int kind, mid, xres, big, tail, tiles_r, tiles_t, nsteps, KS, steps_per_split, tile_rows;
     int64_t split_rows;
@@ -3052,7 +3052,9 @@ nm_status launch_glu(const GluIn& g, void* ws, hipStream_t s) {
     if (g.Ns && !fused) {   // the product then reads the lifted copy
         a.ldx = Kl;
         p = glu_plan(g.Mtok, g.K, g.R, g.Ns, g.xdt, ok(), &fused);
-        if (fused) p.kind = 0;   // not reached: the lifted copy's offsets only add limits
+        // 6:8 of up to 64 tokens whose rows lie so far apart that their offsets pass 32 bits: the plan for
+        // the near copy lifts in the ring, from X itself; two products do not
+        if (fused) p.kind = 0;
     }
     if (!p.kind) return glu_plain(g, ws, s);
     size_t xl, part;
