@@ -469,10 +469,11 @@ nm_status nm_spmm_glu_backward(const void* dH, int64_t lddh, const void* G, cons
  *   to x * (448 * (1 / max)), one rounding per operation; a nonzero r keeps at least the smallest code 2^-9, a block whose magnitudes are
  *   all below 2^-118 is stored as zeros, NaN and infinities as the NaN code.  p is updated with
  *   the m and v of before that rounding.  Zeroed codes and scales are the zero state.
- *   Nearest codes are for beta2 <= 0.95: a change below half a unit (3-6%) is lost in every step, so with
- *   a larger beta2 an element's r does not fall when its gradients do (over 5000 steps after
- *   a tenfold fall: r 1.05 times the f32 one at beta2 0.95, 13 times at 0.99, 7 times at 0.999).  Use
- *   nm_adamw_unbiased, or f32 states, beyond.
+ *   Nearest codes lose a change below half a unit (3-6%) in every step, and a step takes at most
+ *   1 - sqrt(beta2) off r.  So an element's r falls with its gradients only where the noise of its block's
+ *   maximum carries it: thousands of steps after a tenfold fall r was 1.0 to 1.1 times the f32 one at beta2 0.9
+ *   and 1 to 13 times at 0.95, 13 at 0.99, 7 at 0.999 (and 6 at 0.9 for gradients of constant size).  Training with
+ *   8-bit states is for nm_adamw_unbiased.
  * tensors is a HOST array, read before the call returns; the tensors must not overlap each
  * other.  Element-aligned pointers are accepted; 16-byte aligned ones (8-byte for codes) are
  * read and written in whole vectors.  Allocates nothing; a launch takes 44 tensors and 2^35 elements. */

@@ -594,7 +594,7 @@ class AdamWTensors:
         self.sdt = NM_FP8 if kinds == {torch.float8_e4m3fn} else NM_F32
         if self.sdt == NM_FP8 and (m_scale is None or v_scale is None):
             raise ValueError("8-bit states need m_scale and v_scale")
-        self.count, self.array = n, (_AdamWTensor * max(n, 1))()
+        self.count, self.array, self.warned = n, (_AdamWTensor * max(n, 1))(), False
         self.address = ctypes.addressof(self.array)
         f8, spans, read = self.sdt == NM_FP8, [], []      # (first byte, past the last, tensor) of what a step writes, and of the gradients
         for i in range(n):
@@ -638,10 +638,6 @@ class AdamWTensors:
         return -1 if self.device is None else self.device.index
 
 
-# the largest beta2 that nearest 8-bit codes follow falling gradients at
-NM_ADAMW_NEAREST_BETA2 = 0.95
-
-
 def _adamw_ready(tensors: AdamWTensors, grad_scale: torch.Tensor | None) -> bool:
     if grad_scale is not None and (grad_scale.dtype != torch.float32 or grad_scale.numel() != 1):
         raise ValueError("grad_scale must be one f32 value on the device")
@@ -655,12 +651,14 @@ def _adamw_ready(tensors: AdamWTensors, grad_scale: torch.Tensor | None) -> bool
 def nm_adamw(tensors: AdamWTensors, lr: float, step: int, beta1: float = 0.9, beta2: float = 0.999, eps: float = 1e-8,
              grad_scale: torch.Tensor | None = None) -> None:
     """One AdamW step over every tensor of the list, in place; step counts from 1.  8-bit states are held
-    to the nearest codes, which is for beta2 <= 0.95 only (a warning beyond): use nm_adamw_unbiased there."""
+    to the nearest codes, which do not follow gradients that fall (a warning, once a list): train with
+    nm_adamw_unbiased."""
     if not _adamw_ready(tensors, grad_scale):
         return
-    if tensors.sdt == NM_FP8 and beta2 > NM_ADAMW_NEAREST_BETA2:
-        warnings.warn(f"nearest 8-bit states do not follow falling gradients with beta2 {beta2} (above "
-                      f"{NM_ADAMW_NEAREST_BETA2}): use nm_adamw_unbiased", stacklevel=2)
+    if tensors.sdt == NM_FP8 and not tensors.warned:
+        tensors.warned = True
+        warnings.warn("8-bit states held to the nearest codes do not follow gradients that fall: train with nm_adamw_unbiased",
+                      stacklevel=3)
     st = raw.nm_adamw(tensors.address, tensors.count, tensors.sdt, lr, beta1, beta2, eps, step, _ptr(grad_scale),
                       torch._C._cuda_getCurrentRawStream(tensors.device.index))
     if st:

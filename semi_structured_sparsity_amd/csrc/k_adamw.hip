@@ -14,19 +14,20 @@
 // A block whose maximum is below 2^-118 (its reciprocal would overflow) stores zeros.  NaN and
 // infinite elements store the NaN code and do not enter the block's scale.
 //
-// Nearest codes lose a change below half a unit (3-6%) in every step.  A step takes at most
-// 1 - sqrt(b2) off r, so from b2 of about 0.97 on r never falls at an element that does not hold
-// its block's maximum (measured over 6000 steps, half of a block's gradients tenfold smaller from step 1000
-// on: r 1.05, 13 and 7 times the f32 one at b2 0.95, 0.99 and 0.999).  The unbiased form
-// (UNB) takes one of the two neighbouring codes with the probability that gives x on average: 1.01, 1.01
-// and 1.02 there.  Its random bits are a function of seed, step, tensor and element (88.8 M f32 masters 264 ->
-// 266 us, 14.3 M bf16 parameters 34 -> 40).
+// Nearest codes lose a change below half a unit (3-6%) in every step, and a step takes at most
+// 1 - sqrt(b2) off r: 2.5% at b2 0.95.  Only the scale's own fluctuation then moves r at an element that does
+// not hold its block's maximum.  Half of a block's gradients tenfold smaller from step 1000 on, r thousands
+// of steps later over the f32 one: normal gradients 1.01, 1.05, 13 and 7 at b2 0.9, 0.95, 0.99 and 0.999,
+// uniform ones 1.00, 13 at 0.9, 0.95, a mean with 10% noise 1.03-1.12, 8 there, constant size 6, 10.
+// The unbiased form (UNB) takes one of the two neighbouring codes with the probability that gives x on
+// average: 1.00-1.02 for all of these.  Its random bits are a function of seed, step, tensor and
+// element (88.8 M f32 masters 264 -> 266 us, 14.3 M bf16 parameters 34 -> 40).
 //
 // The step is bound by HBM: per parameter 8 B (f32 p read and written) or 4 B (bf16), the
 // gradient's 2 or 4 B, 16 B of f32 states or 4 + 4/128 B of codes and scales, 2 B of the
 // bf16 copy.  Descriptors travel as kernel arguments (no table upload, graph capture
-// safe), kMaxTensors a launch, a tensor that passes a launch's most blocks in pieces; a block finds its tensor by a binary search over the
-// tensors' first block numbers, in scalar registers.
+// safe), kMaxTensors a launch, a tensor that passes a launch's most blocks in pieces; a block
+// finds its tensor by a binary search over the tensors' first block numbers, in scalar registers.
 #include <math.h>
 
 #include "nm_adamw_pieces.h"

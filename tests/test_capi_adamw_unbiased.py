@@ -1,5 +1,4 @@
-"""Host-side checks of the optimiser step with unbiased 8-bit states (the pointers are never dereferenced), and
-that nearest codes beyond their beta2 say so."""
+"""Host-side checks of the optimiser step with unbiased 8-bit states (the pointers are never dereferenced)."""
 import ctypes
 import warnings
 

@@ -119,7 +119,18 @@ def test_nonfinite_values_and_zeros(nm):
     assert (v.float()[~bad & (gr != 0)] > 0).all()
 
 
-def _train(nm, step_of, b2, f8, steps, fall_at, n=8192):
+def _gradients(kind, gr, g):
+    if kind == "normal":
+        gr.normal_(generator=g)
+    elif kind == "uniform":
+        gr.uniform_(-1, 1, generator=g)
+    elif kind == "constant":      # signs
+        gr.uniform_(-1, 1, generator=g).sign_()
+    else:                         # a mean of its own for every element, with 10% noise
+        gr.normal_(generator=g).mul_(0.1).add_(1.0).mul_(torch.linspace(0.2, 1.7, 256, device=gr.device).repeat(gr.numel() // 256))
+
+
+def _train(nm, step_of, b2, f8, steps, fall_at, kind="normal", n=8192):
     """The second moments' roots after gradients whose second half of every block falls tenfold."""
     g = torch.Generator(device=dev())
     g.manual_seed(5)
@@ -130,7 +141,7 @@ def _train(nm, step_of, b2, f8, steps, fall_at, n=8192):
     t = nm.AdamWTensors([p], [gr], [m], [v], [ms] if f8 else None, [vs] if f8 else None)
     small = (torch.arange(n, device=dev()) % 256) >= 128
     for s in range(1, steps + 1):
-        gr.normal_(generator=g)
+        _gradients(kind, gr, g)
         if s > fall_at:
             gr.mul_(torch.where(small, 0.1, 1.0))
         step_of(t, s, b2)
@@ -138,16 +149,18 @@ def _train(nm, step_of, b2, f8, steps, fall_at, n=8192):
     return r, m.float() * ms.repeat_interleave(256) if f8 else m, small
 
 
-@pytest.mark.parametrize("b2", [0.95, 0.99, 0.999])
-def test_thousands_of_steps_follow_f32_states(nm, b2):
+@pytest.mark.parametrize("kind,b2", [("normal", 0.95), ("normal", 0.99), ("normal", 0.999), ("uniform", 0.95), ("uniform", 0.999),
+                                     ("constant", 0.95), ("constant", 0.999), ("mean", 0.95), ("mean", 0.999)])
+def test_thousands_of_steps_follow_f32_states(nm, kind, b2):
     """An unbiased code of r adds its variance to v: per step at most |change| unit, in the mean
-    (1 - b2) / 2 E|g^2 / v - 1| r unit <= (1 - b2) 0.49 r^2 / 8, so v settles at most 6.1% and r 3.1% above.  The stationary
-    spread of r by that variance is at most 0.17 of it, more while r still falls (its units were larger); the mean
-    over 4096 elements then has a standard error of 0.4%, five of which are allowed.  m's rounding adds at most 1.4% of
-    m^2 to its variance (u <= m / 8, 5.3 steps), 0.7% to its mean size."""
+    (1 - b2) / 2 E|g^2 / v - 1| r unit <= (1 - b2) r^2 / 16 (the mean is 0.97 for normal gradients, less for the
+    others and at most 1 while r falls), so v settles at most 6.3% and r 3.1% above.  The stationary spread of r by that
+    variance is at most 0.18 of it, more while r still falls (its units were larger); the mean over 4096
+    elements then has a standard error of 0.4%, five of which are allowed.  m's rounding adds at most 1.4% of m^2 to its
+    variance (u <= m / 8, 5.3 steps), 0.7% to its mean size."""
     steps, fall_at = 5000, 1000
-    r32, m32, small = _train(nm, lambda t, s, b: nm.nm_adamw(t, lr=1e-4, step=s, beta2=b), b2, False, steps, fall_at)
-    r8, m8, _ = _train(nm, lambda t, s, b: nm.nm_adamw_unbiased(t, lr=1e-4, step=s, seed=11, beta2=b), b2, True, steps, fall_at)
+    r32, m32, small = _train(nm, lambda t, s, b: nm.nm_adamw(t, lr=1e-4, step=s, beta2=b), b2, False, steps, fall_at, kind)
+    r8, m8, _ = _train(nm, lambda t, s, b: nm.nm_adamw_unbiased(t, lr=1e-4, step=s, seed=11, beta2=b), b2, True, steps, fall_at, kind)
     for half in (small, ~small):
         ratio = (r8 / r32)[half]
         assert abs(ratio.mean().item() - 1) < 0.031 + 5 * 0.004, ratio.mean()
@@ -155,19 +168,17 @@ def test_thousands_of_steps_follow_f32_states(nm, b2):
         assert abs(m8[half].abs().mean().item() / m32[half].abs().mean().item() - 1) < 0.05
 
 
-def test_nearest_codes_follow_at_their_beta2_and_say_so_beyond(nm):
-    steps, fall_at = 3000, 1000
+def test_nearest_codes_say_what_they_are_not_for(nm):
+    """Once a list, with 8-bit states only; the unbiased step says nothing."""
+    near = lambda t, s, b: nm.nm_adamw(t, lr=1e-4, step=s, beta2=b)  # noqa: E731
+    for b2 in (0.9, 0.999):
+        with pytest.warns(UserWarning, match="nm_adamw_unbiased") as said:
+            _train(nm, near, b2, True, 3, 1)
+        assert len(said) == 1 and said[0].filename == __file__
     with warnings.catch_warnings():
-        warnings.simplefilter("error")      # nothing is said at 0.95, nor of f32 states
-        near = lambda t, s, b: nm.nm_adamw(t, lr=1e-4, step=s, beta2=b)  # noqa: E731
-        r32, _, small = _train(nm, near, 0.95, False, steps, fall_at)
-        r8, _, _ = _train(nm, near, 0.95, True, steps, fall_at)
-        for half in (small, ~small):
-            # a code is within 1/16 of r
-            assert abs((r8 / r32)[half].mean().item() - 1) < 1 / 16 + 0.02
+        warnings.simplefilter("error")
         _train(nm, near, 0.999, False, 2, 1)
-    with pytest.warns(UserWarning, match="nm_adamw_unbiased"):
-        _train(nm, near, 0.999, True, 2, 1)
+        _train(nm, lambda t, s, b: nm.nm_adamw_unbiased(t, lr=1e-4, step=s, beta2=b), 0.999, True, 2, 1)
 
 
 def test_runs_twice_alike_on_a_stream_and_in_a_graph(nm):
