@@ -462,6 +462,8 @@ nm_status nm_spmm_glu_backward(const void* dH, int64_t lddh, const void* G, cons
  * inverse of a loss scale), or NULL for 1.  step counts from 1.
  *   p: pdt F32 or BF16; g: gdt F32 or BF16; copy: bf16 copy of the new p (the packed values a
  *   product reads beside f32 masters), or NULL.
+ *   (A bf16 p is rounded to nearest like every stored value: an update below half its unit, 2^-9 to 2^-8
+ *   of p, is lost; f32 masters with a copy keep it.)
  *   sdt F32: m, v f32 [n].  m_scale and v_scale are ignored.
  *   sdt FP8: m and v hold e4m3 codes [n] of m and of r = sqrt(v), with f32 scales per 256
  *   consecutive elements (m_scale, v_scale [ceil(n/256)]): value = code * scale, scale = max * (1/448)

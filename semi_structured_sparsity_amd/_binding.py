@@ -128,8 +128,8 @@ def _ld(t: torch.Tensor) -> int:
 
 
 def _stream(t: torch.Tensor | None = None):
-    dev = t.device if t is not None and t.is_cuda else None
-    return torch.cuda.current_stream(dev).cuda_stream
+    index = -1 if t is None else t.get_device()
+    return torch.cuda.current_stream().cuda_stream if index < 0 else torch._C._cuda_getCurrentRawStream(index)
 
 
 def _ws(nbytes: int, device) -> torch.Tensor | None:
@@ -400,10 +400,22 @@ def nm_spmm_noalloc(X: torch.Tensor, vals: torch.Tensor, idx: torch.Tensor, R: i
 # ---------------------------------------------------------------- gated feed-forward block, training
 # These run every layer of every step, so their checks are one expression each; what it found is
 # looked up only when it fails.
-def _raw_stream(t: torch.Tensor) -> int:
-    if not t.is_cuda:
+def _enter(t) -> tuple[int, int]:
+    """t's device made current, for the call of the library (it launches there, and a default stream is the same
+    0 on every device): (the current stream, the device to go back to or -1)."""
+    index = t.get_device()
+    if index < 0:
         raise ValueError(f"tensors must be on a GPU, got {t.device}")
-    return torch._C._cuda_getCurrentRawStream(t.device.index)
+    now = torch._C._cuda_getDevice()
+    if now == index:
+        return torch._C._cuda_getCurrentRawStream(index), -1
+    torch._C._cuda_setDevice(index)
+    return torch._C._cuda_getCurrentRawStream(index), now
+
+
+def _leave(back: int):
+    if back >= 0:
+        torch._C._cuda_setDevice(back)
 
 
 def _mat(t: torch.Tensor):
@@ -470,9 +482,13 @@ def nm_spmm_glu(X: torch.Tensor, vals_g: torch.Tensor, idx_g: torch.Tensor, vals
     G = X.new_empty((Mtok, R), dtype=torch.bfloat16) if save else None
     U = X.new_empty((Mtok, R), dtype=torch.bfloat16) if save else None
     ws = _need(raw.nm_spmm_glu_workspace(Mtok, K, R, Ns, xdt), ws, X)
-    st = raw.nm_spmm_glu(X.data_ptr(), xdt, Mtok, K, ldx, vals_g.data_ptr(), idx_g.data_ptr(), vals_u.data_ptr(),
-                         idx_u.data_ptr(), xdt, R, ldv, ldi, Ns, _ptr(x_scale), g_scale, u_scale, act, H.data_ptr(), hdt,
-                         ldh, _ptr(G), _ptr(U), R, _ptr(ws), 0 if ws is None else ws.nbytes, _raw_stream(X))
+    stream, back = _enter(X)
+    try:
+        st = raw.nm_spmm_glu(X.data_ptr(), xdt, Mtok, K, ldx, vals_g.data_ptr(), idx_g.data_ptr(), vals_u.data_ptr(),
+                             idx_u.data_ptr(), xdt, R, ldv, ldi, Ns, _ptr(x_scale), g_scale, u_scale, act, H.data_ptr(), hdt,
+                             ldh, _ptr(G), _ptr(U), R, _ptr(ws), 0 if ws is None else ws.nbytes, stream)
+    finally:
+        _leave(back)
     if st:
         _check(st)
     return (H, G, U) if save else H
@@ -513,9 +529,13 @@ def nm_spmm_backward(dY: torch.Tensor, X: torch.Tensor, vals: torch.Tensor, idx:
     dX, lddx = _grad_out(out_dx, want_dx, Mtok, K, dxdt, X)
     dV, lddv = _grad_out(out_dv, want_dv, R, Kl // 2, dvdt, X)
     ws = _need(raw.nm_spmm_backward_workspace(Mtok, K, R, Ns), ws, X)
-    st = raw.nm_spmm_backward(dY.data_ptr(), ldy, X.data_ptr(), ldx, Mtok, K, vals.data_ptr(), idx.data_ptr(), R, ldv, ldi,
-                              Ns, _ptr(dX), dxdt, lddx, _ptr(dV), dvdt, lddv, _ptr(ws), 0 if ws is None else ws.nbytes,
-                              _raw_stream(X))
+    stream, back = _enter(X)
+    try:
+        st = raw.nm_spmm_backward(dY.data_ptr(), ldy, X.data_ptr(), ldx, Mtok, K, vals.data_ptr(), idx.data_ptr(), R, ldv,
+                                  ldi, Ns, _ptr(dX), dxdt, lddx, _ptr(dV), dvdt, lddv, _ptr(ws),
+                                  0 if ws is None else ws.nbytes, stream)
+    finally:
+        _leave(back)
     if st:
         _check(st)
     return dX, dV
@@ -543,10 +563,14 @@ def nm_spmm_glu_backward(dH: torch.Tensor, G: torch.Tensor, U: torch.Tensor, X: 
     if lddu != lddv:
         _refuse("the two weight gradients must have the same row stride", dVg=dVg, dVu=dVu)
     ws = _need(raw.nm_spmm_glu_backward_workspace(Mtok, K, R, Ns), ws, X)
-    st = raw.nm_spmm_glu_backward(dH.data_ptr(), ldh, G.data_ptr(), U.data_ptr(), m[2], act, X.data_ptr(), ldx, Mtok, K,
-                                  vals_g.data_ptr(), idx_g.data_ptr(), vals_u.data_ptr(), idx_u.data_ptr(), R, ldv, ldi, Ns,
-                                  _ptr(dX), dxdt, lddx, _ptr(dVg), _ptr(dVu), dvdt, lddv, _ptr(ws),
-                                  0 if ws is None else ws.nbytes, _raw_stream(X))
+    stream, back = _enter(X)
+    try:
+        st = raw.nm_spmm_glu_backward(dH.data_ptr(), ldh, G.data_ptr(), U.data_ptr(), m[2], act, X.data_ptr(), ldx, Mtok, K,
+                                      vals_g.data_ptr(), idx_g.data_ptr(), vals_u.data_ptr(), idx_u.data_ptr(), R, ldv,
+                                      ldi, Ns, _ptr(dX), dxdt, lddx, _ptr(dVg), _ptr(dVu), dvdt, lddv, _ptr(ws),
+                                      0 if ws is None else ws.nbytes, stream)
+    finally:
+        _leave(back)
     if st:
         _check(st)
     return dX, dVg, dVu
@@ -659,8 +683,11 @@ def nm_adamw(tensors: AdamWTensors, lr: float, step: int, beta1: float = 0.9, be
         tensors.warned = True
         warnings.warn("8-bit states held to the nearest codes do not follow gradients that fall: train with nm_adamw_unbiased",
                       stacklevel=3)
-    st = raw.nm_adamw(tensors.address, tensors.count, tensors.sdt, lr, beta1, beta2, eps, step, _ptr(grad_scale),
-                      torch._C._cuda_getCurrentRawStream(tensors.device.index))
+    stream, back = _enter(tensors)
+    try:
+        st = raw.nm_adamw(tensors.address, tensors.count, tensors.sdt, lr, beta1, beta2, eps, step, _ptr(grad_scale), stream)
+    finally:
+        _leave(back)
     if st:
         _check(st)
 
@@ -673,19 +700,22 @@ def nm_adamw_unbiased(tensors: AdamWTensors, lr: float, step: int, seed: int = 0
         raise ValueError("unbiased codes are of 8-bit states")
     if not _adamw_ready(tensors, grad_scale):
         return
-    st = raw.nm_adamw_unbiased(tensors.address, tensors.count, lr, beta1, beta2, eps, step, seed & (2 ** 64 - 1),
-                               _ptr(grad_scale), torch._C._cuda_getCurrentRawStream(tensors.device.index))
+    stream, back = _enter(tensors)
+    try:
+        st = raw.nm_adamw_unbiased(tensors.address, tensors.count, lr, beta1, beta2, eps, step, seed & (2 ** 64 - 1),
+                                   _ptr(grad_scale), stream)
+    finally:
+        _leave(back)
     if st:
         _check(st)
 
 
 # ---------------------------------------------------------------- the current device
 def _on_device(fn):
-    """fn with its tensors' device current: the library launches on the current device, and a default
-    stream is the same 0 on every one."""
+    """fn with its tensors' device current, as _enter makes it (the wrappers that use that are not wrapped)."""
     @functools.wraps(fn)
     def call(*args, **kwargs):
-        first = args[0] if args else next((x for x in kwargs.values() if isinstance(x, (torch.Tensor, AdamWTensors))), None)
+        first = args[0] if args else next((x for x in kwargs.values() if isinstance(x, torch.Tensor)), None)
         try:
             index = first.get_device()
         except AttributeError:      # no tensor: fn says so
@@ -697,6 +727,7 @@ def _on_device(fn):
     return call
 
 
+_ENTER = ("nm_spmm_glu", "nm_spmm_backward", "nm_spmm_glu_backward", "nm_adamw", "nm_adamw_unbiased")
 for _name in SIGNATURES:
-    if not _name.endswith("_workspace") and _name not in ("nm_abi_version", "nm_last_error"):
+    if not _name.endswith("_workspace") and _name not in ("nm_abi_version", "nm_last_error", *_ENTER):
         globals()[_name] = _on_device(globals()[_name])
