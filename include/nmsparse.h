@@ -70,8 +70,10 @@ typedef enum {
  * 3 mantissa bits; no infinities, 0x7f/0xff NaN, largest finite 448).  FP8 is
  * one of the precisions the sliding-window product runs in ("SlideSparse",
  * section 3); here it is carried as raw codes by the packers and multiplied by
- * nm_spmm with f32 accumulation. */
-typedef enum { NM_F32 = 0, NM_BF16 = 1, NM_I8 = 2, NM_I32 = 3, NM_FP8 = 4 } nm_dtype;
+ * nm_spmm with f32 accumulation.
+ * NM_I4, NM_FP4: 4-bit codes of packed weights, two to a byte (nmsparse_layers.h; no call
+ * of this header takes them). */
+typedef enum { NM_F32 = 0, NM_BF16 = 1, NM_I8 = 2, NM_I32 = 3, NM_FP8 = 4, NM_I4 = 5, NM_FP4 = 6 } nm_dtype;
 
 typedef enum { NM_SCORE_HESSIAN = 0, NM_SCORE_MAGNITUDE = 1 } nm_score_mode;
 

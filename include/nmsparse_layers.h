@@ -1,0 +1,60 @@
+/*
+ * nmsparse_layers.h - what surrounds and contains a pruned feed-forward block (nmsparse.h,
+ * whose conventions hold here): its packed weights in 4 bits.
+ */
+#ifndef NMSPARSE_LAYERS_H
+#define NMSPARSE_LAYERS_H
+
+#include "nmsparse.h"
+
+#ifdef __cplusplus
+extern "C" {
+#endif
+
+/* ---------------------------------------------------------------- 4-bit packed weights
+ * A packed 2:4 (or decomposed (2N-2):2N) weight whose kept values are 4-bit codes with one bf16
+ * scale per group of `group` consecutive columns of the (lifted) width K', that is of group / 2
+ * kept values: value = code value * scale.  2:4 weights then take 1.5 bits a weight and the
+ * scales.
+ *   codes [R, ldc] bytes: kept value j of a row in byte j / 2, low half for even j.  A code is a
+ *     sign (bit 3) and a magnitude: NM_I4 0 .. 7; NM_FP4 (OCP e2m1) 0, 0.5, 1, 1.5, 2, 3, 4, 6.
+ *   scales [ceil(K' / group), lds] bf16: scale of group g of row r at scales[g * lds + r].
+ *   idx as in nm_spmm.
+ * group: 64, 128 or 256.  The last group of a row may be shorter. */
+
+/* 4-bit codes of packed values (nm_pack, nm_prune_pack, nm_prune_slide ...), per row and group:
+ *   top = max |v|,  s = top / 7 (NM_I4) or top / 6 (NM_FP4) in f32, rounded to bf16,
+ *   code = the nearest to v / s (f32 quotient, ties to the even code, held to 7 or 6);
+ *   s = 0 gives codes 0, a group with a NaN or an infinity a NaN scale and codes 0.
+ * vals: bf16 or f32 [R, slots] (ldv), slots = K' / 2 a multiple of 8.  values (nullable): code * s
+ * rounded to vdt, [R, slots] (ldo): what the products then multiply with, for measuring the error
+ * or training through it.
+ * vals and values: 16-byte aligned rows; codes 4-byte aligned, ldc a multiple of 4; scales 2-byte. */
+nm_status nm_quant_w4(const void* vals, nm_dtype vdt, int64_t R, int64_t slots, int64_t ldv, nm_dtype qdt, int group,
+                      void* codes, int64_t ldc, void* scales, int64_t lds, void* values, int64_t ldo,
+                      nm_stream_t stream);
+
+/* Y = X W^T on a 4-bit packed weight, made for few tokens (serving: the weight is read once for
+ * up to 64 tokens; more are taken 64 at a time).
+ *   X: bf16 [Mtok, K] (ldx), K the original width; Y: bf16 or f32 [Mtok, R] (ldy).
+ *   Ns: 0, or 3 <= Ns <= 8 over K' = (2 - 2/Ns) K (the lift is done in the activation's loads).
+ * Code values times X are summed in f32 within 64 columns, scaled in f32 and added up in f32 in a
+ * fixed order; one rounding at the end.
+ * Requires K % 2Ns == 0, K' % 16 == 0; X and codes 16-byte aligned with 16-byte row strides, idx
+ * 4-byte aligned, scales 8-byte aligned with lds % 4 == 0; ldc < 2^26, ldi < 2^24.  No workspace. */
+nm_status nm_spmm_w4(const void* X, int64_t Mtok, int64_t K, int64_t ldx, const void* codes, nm_dtype qdt,
+                     const uint32_t* idx, const void* scales, int64_t R, int64_t ldc, int64_t ldi, int64_t lds,
+                     int group, int Ns, void* Y, nm_dtype ydt, int64_t ldy, nm_stream_t stream);
+
+/* H = act(X Wg^T) . (X Wu^T) on two 4-bit weights packed alike (same ldc, ldi, lds, group): the
+ * gated block of nm_spmm_glu.  Sums as in nm_spmm_w4; activation and product in f32, H rounded once. */
+nm_status nm_spmm_glu_w4(const void* X, int64_t Mtok, int64_t K, int64_t ldx, const void* codes_g,
+                         const uint32_t* idx_g, const void* scales_g, const void* codes_u, const uint32_t* idx_u,
+                         const void* scales_u, nm_dtype qdt, int64_t R, int64_t ldc, int64_t ldi, int64_t lds, int group,
+                         int Ns, nm_act act, void* H, nm_dtype hdt, int64_t ldh, nm_stream_t stream);
+
+#ifdef __cplusplus
+}
+#endif
+
+#endif /* NMSPARSE_LAYERS_H */

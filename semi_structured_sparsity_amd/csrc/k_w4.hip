@@ -1,0 +1,228 @@
+// 4-bit packed weights: the quantiser, and Y = X W^T and the gated block H = act(X Wg^T) . (X Wu^T)
+// for few tokens (nm_few.h has the operands' layout and the inner product).
+#include "nm_few.h"
+
+namespace nm {
+
+// ------------------------------------------------------------------ quantiser
+// One thread takes 8 consecutive values; the group / 16 threads of a group share its maximum by
+// lane moves.  s = bf16(top / 7 or 6), code = nearest to v / s.
+template <bool F32, bool FP4>
+__global__ __launch_bounds__(256) void quant_w4_kernel(const void* __restrict__ vals, int64_t ldv, int64_t R, int chunks,
+                                                       int chunks_pad, int glanes, uint8_t* __restrict__ codes, int64_t ldc,
+                                                       uint16_t* __restrict__ scales, int64_t lds, void* __restrict__ values,
+                                                       int64_t ldo) {
+    const int64_t id = (int64_t)blockIdx.x * 256 + threadIdx.x;
+    const int64_t r = id / chunks_pad;
+    const int c = (int)(id - r * chunks_pad);
+    const bool in = r < R && c < chunks;
+    float v[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = 0.0f;
+    if (in) {
+        if constexpr (F32) {
+            const float4* p = (const float4*)((const float*)vals + r * ldv + 8 * c);
+            const float4 a = p[0], b = p[1];
+            v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w, v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
+        } else {
+            const uint4 a = *(const uint4*)((const uint16_t*)vals + r * ldv + 8 * c);
+            const uint32_t w[4] = {a.x, a.y, a.z, a.w};
+#pragma unroll
+            for (int i = 0; i < 8; ++i) v[i] = __uint_as_float(i & 1 ? w[i / 2] & 0xffff0000u : w[i / 2] << 16);
+        }
+    }
+    // the maximum as bits: of magnitudes their order is that of the numbers, and a NaN or an infinity is
+    // at the top
+    uint32_t top = 0;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) top = max(top, __float_as_uint(v[i]) & 0x7fffffffu);
+    for (int off = 1; off < glanes; off <<= 1) top = max(top, (uint32_t)__shfl_xor((int)top, off));
+    const bool bad = top >= 0x7f800000u;
+    const uint32_t sb = bad ? 0x7fc0u : f32_to_bf16_bits(__fdiv_rn(__uint_as_float(top), FP4 ? 6.0f : 7.0f));
+    const float s = bf16_bits_to_f32(sb);
+    if (!in) return;
+    uint32_t word = 0;
+    float o[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        const float a = bad || s == 0.0f ? 0.0f : __builtin_fabsf(__fdiv_rn(v[i], s));
+        uint32_t m;
+        float val;
+        if constexpr (FP4) {
+            m = (a > 0.25f) + (a >= 0.75f) + (a > 1.25f) + (a >= 1.75f) + (a > 2.5f) + (a >= 3.5f) + (a > 5.0f);
+            val = m < 4 ? 0.5f * (float)m : (m < 6 ? (float)m - 2.0f : 2.0f * (float)m - 8.0f);
+        } else {
+            val = fminf(rintf(a), 7.0f);
+            m = (uint32_t)val;
+        }
+        const uint32_t neg = m && (__float_as_uint(v[i]) >> 31);
+        word |= (m | neg << 3) << (4 * i);
+        o[i] = (neg ? -val : val) * s;
+    }
+    *(uint32_t*)(codes + r * ldc + 4 * c) = word;
+    if (c % glanes == 0) scales[(int64_t)(c / glanes) * lds + r] = (uint16_t)sb;
+    if (!values) return;
+    if constexpr (F32) {
+        float4* p = (float4*)((float*)values + r * ldo + 8 * c);
+        p[0] = make_float4(o[0], o[1], o[2], o[3]);
+        p[1] = make_float4(o[4], o[5], o[6], o[7]);
+    } else {
+        *(uint4*)((uint16_t*)values + r * ldo + 8 * c) =
+            make_uint4(f32_to_bf16_pair(o[0], o[1]), f32_to_bf16_pair(o[2], o[3]), f32_to_bf16_pair(o[4], o[5]),
+                       f32_to_bf16_pair(o[6], o[7]));
+    }
+}
+
+nm_status launch_quant_w4(const void* vals, nm_dtype vdt, int64_t R, int64_t slots, int64_t ldv, nm_dtype qdt, int group,
+                          void* codes, int64_t ldc, void* scales, int64_t lds, void* values, int64_t ldo, hipStream_t s) {
+    const int chunks = (int)(slots / 8), glanes = group / 16;
+    const int pad = (int)(ceil_div(chunks, glanes) * glanes);
+    const int64_t blocks = ceil_div(R * pad, 256);
+    if (blocks >= 1LL << 31) return set_error(NM_ERR_SHAPE, "nm_quant_w4: weight too large for one launch");
+#define NM_Q(F32, FP4)                                                                                                  \
+    hipLaunchKernelGGL((quant_w4_kernel<F32, FP4>), dim3((unsigned)blocks), dim3(256), 0, s, vals, ldv, R, chunks, pad, \
+                       glanes, (uint8_t*)codes, ldc, (uint16_t*)scales, lds, values, ldo)
+    if (vdt == NM_F32 && qdt == NM_FP4) NM_Q(true, true);
+    else if (vdt == NM_F32) NM_Q(true, false);
+    else if (qdt == NM_FP4) NM_Q(false, true);
+    else NM_Q(false, false);
+#undef NM_Q
+    return check_launch("nm_quant_w4");
+}
+
+// ------------------------------------------------------------------ products
+struct W4Args {
+    const uint16_t* X;
+    int64_t ldx;
+    int Mtok, Ns, width, gshift;
+    const uint8_t* codes[2];
+    const uint32_t* idx[2];
+    const uint16_t* scales[2];
+    int64_t ldc, ldi, lds, R;
+    void* Y;
+    int64_t ldy;
+    int y32, act;
+};
+
+// A block of NW waves owns RT tiles of 16 rows (GLU: RT / 2 tiles of 16 features, gate and up
+// beside each other) and 16 CT tokens.  Its waves take units of 256 columns in turn and their sums
+// meet in LDS, added in wave order.
+template <int VT, int SPG, bool GLU, int RT, int CT, int NW>
+__global__ __launch_bounds__(NW * 64) void w4_kernel(W4Args a) {
+    static_assert(!GLU || RT % 2 == 0, "gate and up tiles in pairs");
+    constexpr int TR = GLU ? RT / 2 : RT;
+    __shared__ __attribute__((aligned(16))) float red[NW][RT][256];
+    const int tid = threadIdx.x, lane = tid & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int64_t f0 = (int64_t)blockIdx.x * (16 * TR);
+    const int64_t t0 = (int64_t)blockIdx.y * (16 * CT);
+    FewRows w[RT];
+#pragma unroll
+    for (int i = 0; i < RT; ++i) {
+        const int m = GLU ? i & 1 : 0;
+        int64_t r0 = f0 + 16 * (GLU ? i / 2 : i);
+        // a tile past the last row re-reads the block's first one (its sums are not stored)
+        r0 = r0 < a.R ? r0 : f0;
+        w[i] = few_rows(a.codes[m], a.idx[m], a.scales[m], a.ldc, a.ldi, a.lds, r0, a.R, lane);
+    }
+    const uint16_t* xrow[CT];
+#pragma unroll
+    for (int j = 0; j < CT; ++j) {
+        const int64_t t = t0 + 16 * j + (lane & 15);
+        xrow[j] = a.X + (t < a.Mtok ? t : a.Mtok - 1) * a.ldx;
+    }
+    few_f32x4 acc[RT][CT];
+#pragma unroll
+    for (int i = 0; i < RT; ++i)
+#pragma unroll
+        for (int j = 0; j < CT; ++j) acc[i][j] = few_f32x4{0, 0, 0, 0};
+    few_product<VT, SPG, RT, CT>(w, xrow, wave, NW, (a.width + 255) / 256, a.width, a.gshift, a.Ns, lane, acc);
+
+#pragma unroll
+    for (int j = 0; j < CT; ++j) {
+        if (t0 + 16 * j >= a.Mtok) break;
+        if (j) __syncthreads();
+#pragma unroll
+        for (int i = 0; i < RT; ++i) *(few_f32x4*)&red[wave][i][lane * 4] = acc[i][j];
+        __syncthreads();
+        // output e of a tile: lane e / 4's accumulator e % 4
+        for (int e = tid; e < TR * 256; e += NW * 64) {
+            const int tile = e >> 8, k = e & 255;
+            const int64_t tok = t0 + 16 * j + ((k >> 2) & 15), r = f0 + 16 * tile + 4 * (k >> 6) + (k & 3);
+            if (tok >= a.Mtok || r >= a.R) continue;
+            float v = 0.0f, up = 0.0f;
+#pragma unroll
+            for (int n = 0; n < NW; ++n) {
+                v += red[n][GLU ? 2 * tile : tile][k];
+                if constexpr (GLU) up += red[n][2 * tile + 1][k];
+            }
+            if constexpr (GLU) {
+                float f;
+                switch (a.act) {
+                    case NM_ACT_SILU: f = act_value<NM_ACT_SILU>(v); break;
+                    case NM_ACT_GELU: f = act_value<NM_ACT_GELU>(v); break;
+                    case NM_ACT_GELU_TANH: f = act_value<NM_ACT_GELU_TANH>(v); break;
+                    default: f = act_value<NM_ACT_RELU2>(v); break;
+                }
+                v = f * up;
+            }
+            if (a.y32) ((float*)a.Y)[tok * a.ldy + r] = v;
+            else ((uint16_t*)a.Y)[tok * a.ldy + r] = (uint16_t)f32_to_bf16_bits(v);
+        }
+    }
+}
+
+template <int VT, int SPG, bool GLU, int RT, int CT, int NW>
+static void w4_go(const W4Args& a, hipStream_t s) {
+    constexpr int rows = 16 * (GLU ? RT / 2 : RT);
+    const dim3 grid((unsigned)ceil_div(a.R, rows), (unsigned)ceil_div(a.Mtok, 16 * CT));
+    hipLaunchKernelGGL((w4_kernel<VT, SPG, GLU, RT, CT, NW>), grid, dim3(NW * 64), 0, s, a);
+}
+
+template <int VT, int SPG, bool GLU>
+static void w4_tokens(const W4Args& a, hipStream_t s) {
+    if (a.Mtok <= 16) w4_go<VT, SPG, GLU, 2, 1, 16>(a, s);
+    else if (a.Mtok <= 32) w4_go<VT, SPG, GLU, 2, 2, 8>(a, s);
+    else w4_go<VT, SPG, GLU, 2, 4, 8>(a, s);
+}
+
+template <int VT, bool GLU>
+static void w4_group(const W4Args& a, hipStream_t s) {
+    if (a.gshift == 6) w4_tokens<VT, 1, GLU>(a, s);
+    else if (a.gshift == 7) w4_tokens<VT, 2, GLU>(a, s);
+    else w4_tokens<VT, 4, GLU>(a, s);
+}
+
+nm_status launch_w4(const W4In& in, hipStream_t s) {
+    W4Args a{};
+    a.X = in.X;
+    a.ldx = in.ldx;
+    a.Mtok = (int)in.Mtok;
+    a.Ns = in.Ns;
+    a.width = (int)(in.Ns ? in.K / (2 * in.Ns) * 4 * (in.Ns - 1) : in.K);
+    a.gshift = in.group == 64 ? 6 : in.group == 128 ? 7 : 8;
+    for (int m = 0; m < 2; ++m) {
+        a.codes[m] = (const uint8_t*)in.codes[m];
+        a.idx[m] = in.idx[m];
+        a.scales[m] = (const uint16_t*)in.scales[m];
+    }
+    a.ldc = in.ldc;
+    a.ldi = in.ldi;
+    a.lds = in.lds;
+    a.R = in.R;
+    a.Y = in.Y;
+    a.ldy = in.ldy;
+    a.y32 = in.ydt == NM_F32;
+    a.act = in.act;
+    const bool glu = in.codes[1] != nullptr;
+    if (in.qdt == NM_FP4) {
+        if (glu) w4_group<kFewFP4, true>(a, s);
+        else w4_group<kFewFP4, false>(a, s);
+    } else {
+        if (glu) w4_group<kFewI4, true>(a, s);
+        else w4_group<kFewI4, false>(a, s);
+    }
+    return check_launch(glu ? "nm_spmm_glu_w4" : "nm_spmm_w4");
+}
+
+}  // namespace nm

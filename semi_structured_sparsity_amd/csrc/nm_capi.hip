@@ -6,7 +6,7 @@
 
 #include <mutex>
 
-#include "nm_internal.h"
+#include "nm_check.h"
 
 namespace nm {
 
@@ -26,25 +26,7 @@ nm_status check_launch(const char* what) {
     return NM_OK;
 }
 
-static int64_t esize(nm_dtype d) { return d == NM_BF16 ? 2 : (d == NM_I8 || d == NM_FP8) ? 1 : 4; }
 static bool dtype_ok(nm_dtype d) { return d == NM_F32 || d == NM_BF16 || d == NM_I8 || d == NM_I32 || d == NM_FP8; }
-static bool aligned16(const void* p) { return ((uintptr_t)p & 15u) == 0; }
-
-struct Range {
-    uintptr_t lo, hi;
-};
-// Byte range touched by a row-major [rows, cols] view with leading dimension ld.
-static Range span(const void* p, int64_t rows, int64_t cols, int64_t ld, int64_t es) {
-    if (!p || rows <= 0 || cols <= 0) return {0, 0};
-    const uintptr_t b = (uintptr_t)p;
-    return {b, b + (uintptr_t)(((rows - 1) * ld + cols) * es)};
-}
-static bool overlap(Range a, Range b) { return a.lo < a.hi && b.lo < b.hi && a.lo < b.hi && b.lo < a.hi; }
-
-#define NM_REQ(cond, st, ...)                                                \
-    do {                                                                     \
-        if (!(cond)) return set_error(st, __VA_ARGS__);                      \
-    } while (0)
 
 static nm_status check_pattern(int N, int M, const char* fn) {
     NM_REQ(M == 4 || M == 8, NM_ERR_PATTERN, "%s: M must be 4 or 8 (got %d)", fn, M);

@@ -1,0 +1,110 @@
+// C ABI of include/nmsparse_layers.h: argument validation and dispatch, as in nm_capi.hip.
+// Nothing is enqueued unless every check passes.
+#include "nm_check.h"
+
+using namespace nm;
+
+namespace {
+
+bool known_act(nm_act a) { return a == NM_ACT_SILU || a == NM_ACT_GELU || a == NM_ACT_GELU_TANH || a == NM_ACT_RELU2; }
+bool code4(nm_dtype d) { return d == NM_I4 || d == NM_FP4; }
+bool group_ok(int g) { return g == 64 || g == 128 || g == 256; }
+int64_t lifted(int64_t K, int Ns) { return Ns ? K / (2 * Ns) * 4 * (Ns - 1) : K; }
+
+constexpr int64_t kMost = (int64_t)1 << 24;   // tokens, columns, rows of one call
+
+// the checks of a 4-bit product; nw: 1, or 2 weights (gated block)
+nm_status w4_check(const char* fn, const W4In& in, int nw, bool* run) {
+    *run = false;
+    NM_REQ(in.Mtok >= 0 && in.K >= 0 && in.R >= 0, NM_ERR_SHAPE, "%s: negative size", fn);
+    NM_REQ(in.Mtok <= kMost && in.K <= kMost && in.R <= kMost, NM_ERR_SHAPE, "%s: sizes up to 2^24", fn);
+    NM_REQ(in.Ns == 0 || (in.Ns >= 3 && in.Ns <= 8), NM_ERR_PATTERN,
+           "%s: supported patterns are plain 2:4 (Ns=0) and (2N-2):2N via slide (3 <= Ns <= 8), got Ns=%d", fn, in.Ns);
+    NM_REQ(code4(in.qdt), NM_ERR_DTYPE, "%s: codes are NM_I4 or NM_FP4", fn);
+    NM_REQ(in.ydt == NM_BF16 || in.ydt == NM_F32, NM_ERR_DTYPE, "%s: the output must be bf16 or f32", fn);
+    NM_REQ(group_ok(in.group), NM_ERR_SHAPE, "%s: group must be 64, 128 or 256 (got %d)", fn, in.group);
+    NM_REQ(in.Ns == 0 || in.K % (2 * in.Ns) == 0, NM_ERR_SHAPE, "%s: K must be a multiple of 2N = %d", fn, 2 * in.Ns);
+    const int64_t Kl = lifted(in.K, in.Ns);
+    NM_REQ(Kl % 16 == 0, NM_ERR_SHAPE, "%s: the (lifted) width %lld must be a multiple of 16", fn, (long long)Kl);
+    if (in.Mtok == 0 || in.R == 0) return NM_OK;
+    NM_REQ(in.K > 0, NM_ERR_SHAPE, "%s: K == 0", fn);
+    NM_REQ(in.X && in.Y, NM_ERR_NULL, "%s: NULL argument", fn);
+    const int64_t iw = (Kl + 31) / 32, groups = ceil_div(Kl, in.group);
+    NM_REQ(in.ldx >= in.K && in.ldc >= Kl / 4 && in.ldi >= iw && in.lds >= in.R && in.ldy >= in.R, NM_ERR_SHAPE,
+           "%s: leading dimension too small", fn);
+    NM_REQ(in.ldc < (1 << 26) && in.ldi < (1 << 24), NM_ERR_SHAPE, "%s: leading dimension of the weight too large", fn);
+    NM_REQ(aligned16(in.X) && in.ldx % 8 == 0 && in.ldc % 16 == 0, NM_ERR_ALIGN,
+           "%s: X and codes need 16-byte aligned bases and row strides", fn);
+    NM_REQ(aligned_to(in.Y, esize(in.ydt)), NM_ERR_ALIGN, "%s: the output is not element-aligned", fn);
+    NM_REQ(in.lds % 4 == 0, NM_ERR_ALIGN, "%s: lds must be a multiple of 4", fn);
+    const Range y = span(in.Y, in.Mtok, in.R, in.ldy, esize(in.ydt));
+    NM_REQ(!overlap(y, span(in.X, in.Mtok, in.K, in.ldx, 2)), NM_ERR_ALIAS, "%s: the output overlaps X", fn);
+    for (int m = 0; m < nw; ++m) {
+        NM_REQ(in.codes[m] && in.idx[m] && in.scales[m], NM_ERR_NULL, "%s: NULL weight", fn);
+        NM_REQ(aligned16(in.codes[m]), NM_ERR_ALIGN, "%s: X and codes need 16-byte aligned bases and row strides", fn);
+        NM_REQ(aligned_to(in.idx[m], 4), NM_ERR_ALIGN, "%s: idx must be 4-byte aligned", fn);
+        NM_REQ(aligned_to(in.scales[m], 8), NM_ERR_ALIGN, "%s: scales must be 8-byte aligned", fn);
+        NM_REQ(!overlap(y, span(in.codes[m], in.R, Kl / 4, in.ldc, 1)) && !overlap(y, span(in.idx[m], in.R, iw, in.ldi, 4)) &&
+                   !overlap(y, span(in.scales[m], groups, in.R, in.lds, 2)),
+               NM_ERR_ALIAS, "%s: the output overlaps a weight", fn);
+    }
+    *run = true;
+    return NM_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+nm_status nm_quant_w4(const void* vals, nm_dtype vdt, int64_t R, int64_t slots, int64_t ldv, nm_dtype qdt, int group,
+                      void* codes, int64_t ldc, void* scales, int64_t lds, void* values, int64_t ldo,
+                      nm_stream_t stream) {
+    const char* fn = "nm_quant_w4";
+    NM_REQ(R >= 0 && slots >= 0, NM_ERR_SHAPE, "%s: negative size", fn);
+    NM_REQ(R <= kMost && slots <= kMost, NM_ERR_SHAPE, "%s: sizes up to 2^24", fn);
+    NM_REQ(vdt == NM_BF16 || vdt == NM_F32, NM_ERR_DTYPE, "%s: values must be bf16 or f32", fn);
+    NM_REQ(code4(qdt), NM_ERR_DTYPE, "%s: codes are NM_I4 or NM_FP4", fn);
+    NM_REQ(group_ok(group), NM_ERR_SHAPE, "%s: group must be 64, 128 or 256 (got %d)", fn, group);
+    NM_REQ(slots % 8 == 0, NM_ERR_SHAPE, "%s: slots must be a multiple of 8", fn);
+    if (R == 0 || slots == 0) return NM_OK;
+    NM_REQ(vals && codes && scales, NM_ERR_NULL, "%s: NULL argument", fn);
+    const int64_t es = esize(vdt), groups = ceil_div(2 * slots, group);
+    NM_REQ(ldv >= slots && ldc >= slots / 2 && lds >= R && (!values || ldo >= slots), NM_ERR_SHAPE,
+           "%s: leading dimension too small", fn);
+    NM_REQ(aligned16(vals) && ldv * es % 16 == 0 && (!values || (aligned16(values) && ldo * es % 16 == 0)), NM_ERR_ALIGN,
+           "%s: values need 16-byte aligned bases and row strides", fn);
+    NM_REQ(aligned_to(codes, 4) && ldc % 4 == 0 && aligned_to(scales, 2), NM_ERR_ALIGN,
+           "%s: codes need 4-byte aligned rows, scales 2-byte alignment", fn);
+    const Range in = span(vals, R, slots, ldv, es), out[] = {span(codes, R, slots / 2, ldc, 1), span(scales, groups, R, lds, 2),
+                                                              span(values, R, slots, ldo, es)};
+    for (int i = 0; i < 3; ++i) {
+        NM_REQ(!overlap(out[i], in), NM_ERR_ALIAS, "%s: an output overlaps the input", fn);
+        for (int j = 0; j < i; ++j) NM_REQ(!overlap(out[i], out[j]), NM_ERR_ALIAS, "%s: outputs overlap", fn);
+    }
+    return launch_quant_w4(vals, vdt, R, slots, ldv, qdt, group, codes, ldc, scales, lds, values, ldo, (hipStream_t)stream);
+}
+
+nm_status nm_spmm_w4(const void* X, int64_t Mtok, int64_t K, int64_t ldx, const void* codes, nm_dtype qdt,
+                     const uint32_t* idx, const void* scales, int64_t R, int64_t ldc, int64_t ldi, int64_t lds,
+                     int group, int Ns, void* Y, nm_dtype ydt, int64_t ldy, nm_stream_t stream) {
+    const W4In in{(const uint16_t*)X, Mtok, K, ldx, {codes, nullptr}, {idx, nullptr}, {scales, nullptr}, qdt, R, ldc, ldi,
+                  lds, group, Ns, NM_ACT_SILU, Y, ydt, ldy};
+    bool run = false;
+    const nm_status st = w4_check("nm_spmm_w4", in, 1, &run);
+    return st != NM_OK || !run ? st : launch_w4(in, (hipStream_t)stream);
+}
+
+nm_status nm_spmm_glu_w4(const void* X, int64_t Mtok, int64_t K, int64_t ldx, const void* codes_g,
+                         const uint32_t* idx_g, const void* scales_g, const void* codes_u, const uint32_t* idx_u,
+                         const void* scales_u, nm_dtype qdt, int64_t R, int64_t ldc, int64_t ldi, int64_t lds, int group,
+                         int Ns, nm_act act, void* H, nm_dtype hdt, int64_t ldh, nm_stream_t stream) {
+    const char* fn = "nm_spmm_glu_w4";
+    NM_REQ(known_act(act), NM_ERR_SHAPE, "%s: unknown activation", fn);
+    const W4In in{(const uint16_t*)X, Mtok, K, ldx, {codes_g, codes_u}, {idx_g, idx_u}, {scales_g, scales_u}, qdt, R, ldc,
+                  ldi, lds, group, Ns, act, H, hdt, ldh};
+    bool run = false;
+    const nm_status st = w4_check(fn, in, 2, &run);
+    return st != NM_OK || !run ? st : launch_w4(in, (hipStream_t)stream);
+}
+
+}  // extern "C"

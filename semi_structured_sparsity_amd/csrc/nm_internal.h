@@ -6,7 +6,7 @@
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
-#include "../../include/nmsparse.h"
+#include "../../include/nmsparse_layers.h"
 
 namespace nm {
 
@@ -363,6 +363,24 @@ nm_status launch_grad(const GradIn& in, const GradOut& out, int nmat, void* ws, 
 // seed: unbiased codes of 8-bit states, or null for nearest ones
 nm_status launch_adamw(const nm_adamw_tensor* ts, int count, nm_dtype sdt, double lr, double beta1, double beta2,
                        double eps, int64_t step, const uint64_t* seed, const float* grad_scale, hipStream_t s);
+// 4-bit packed weights
+nm_status launch_quant_w4(const void* vals, nm_dtype vdt, int64_t R, int64_t slots, int64_t ldv, nm_dtype qdt, int group,
+                          void* codes, int64_t ldc, void* scales, int64_t lds, void* values, int64_t ldo, hipStream_t s);
+struct W4In {
+    const uint16_t* X;
+    int64_t Mtok, K, ldx;
+    const void* codes[2];   // the weight, or gate and up
+    const uint32_t* idx[2];
+    const void* scales[2];
+    nm_dtype qdt;
+    int64_t R, ldc, ldi, lds;
+    int group, Ns;
+    nm_act act;
+    void* Y;
+    nm_dtype ydt;
+    int64_t ldy;
+};
+nm_status launch_w4(const W4In& in, hipStream_t s);
 // Hutchinson
 size_t hutch_ws(int64_t n, int64_t K, int64_t R, int probes);
 size_t hutch_score_ws(int64_t n, int64_t K, int64_t R, int probes);

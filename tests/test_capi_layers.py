@@ -1,0 +1,150 @@
+"""Host-side checks of nmsparse_layers.h: the header's functions are exported and bound, bad arguments are
+refused before anything reaches a GPU (the pointers below are never dereferenced), and every wrapper
+makes its tensors' device current."""
+import ctypes
+import re
+from pathlib import Path
+
+import pytest
+import torch
+
+import semi_structured_sparsity_amd as nm
+
+P = ctypes.c_void_p
+X, C, I, S, C2, I2, S2, Y, V = (P((i + 1) << 32) for i in range(9))
+HEADER = Path(__file__).resolve().parents[1] / "include" / "nmsparse_layers.h"
+
+
+def _name(st):
+    return nm.STATUS_NAMES[st]
+
+
+def test_header_library_and_binding_agree():
+    text = re.sub(r"/\*.*?\*/", "", HEADER.read_text(), flags=re.S)
+    declared = set(re.findall(r"\b(nm_[a-z0-9_]+)\s*\(", text))
+    assert declared == set(nm.LAYER_SIGNATURES)
+    for s in declared:
+        assert hasattr(nm.raw, s) and (s.endswith("_workspace") or callable(getattr(nm, s)))
+    assert not declared & set(nm.SIGNATURES)
+
+
+# ------------------------------------------------------------------ 4-bit weights
+def _quant(**kw):
+    a = dict(vals=X, vdt=1, R=8, slots=64, ldv=64, qdt=5, group=64, codes=C, ldc=32, scales=S, lds=8, values=V, ldo=64)
+    a.update(kw)
+    return _name(nm.raw.nm_quant_w4(*a.values(), None))
+
+
+def test_quant_refuses():
+    assert _quant(vdt=2) == "NM_ERR_DTYPE" and _quant(qdt=4) == "NM_ERR_DTYPE" and _quant(qdt=7) == "NM_ERR_DTYPE"
+    for g in (0, 32, 96, 512, -64):
+        assert _quant(group=g) == "NM_ERR_SHAPE"
+    assert _quant(slots=60) == "NM_ERR_SHAPE" and _quant(R=-1) == "NM_ERR_SHAPE" and _quant(slots=-8) == "NM_ERR_SHAPE"
+    assert _quant(R=1 << 25) == "NM_ERR_SHAPE" and _quant(slots=1 << 25) == "NM_ERR_SHAPE"
+    for k, v in (("ldv", 56), ("ldc", 28), ("lds", 7), ("ldo", 56)):
+        assert _quant(**{k: v}) == "NM_ERR_SHAPE", k
+    for k in ("vals", "codes", "scales"):
+        assert _quant(**{k: None}) == "NM_ERR_NULL", k
+    for k, p, off in (("vals", X, 8), ("codes", C, 2), ("scales", S, 1), ("values", V, 8)):
+        assert _quant(**{k: P(p.value + off)}) == "NM_ERR_ALIGN", k
+    for k, v in (("ldv", 68), ("ldc", 34), ("ldo", 68)):
+        assert _quant(**{k: v}) == "NM_ERR_ALIGN", k
+    for k in ("codes", "scales", "values"):
+        assert _quant(**{k: X}) == "NM_ERR_ALIAS", k
+    assert _quant(codes=S) == "NM_ERR_ALIAS" and _quant(values=C) == "NM_ERR_ALIAS"
+    assert _quant(R=0, vals=None) == "NM_OK" and _quant(slots=0, vals=None) == "NM_OK"
+
+
+def _w4(two=False, **kw):
+    a = dict(X=X, M=4, K=64, ldx=64, c=C)
+    if two:
+        a.update(i=I, s=S, c2=C2, i2=I2, s2=S2, qdt=5)
+    else:
+        a.update(qdt=5, i=I, s=S)
+    a.update(R=8, ldc=16, ldi=2, lds=8, group=64, Ns=0)
+    if two:
+        a.update(act=0)
+    a.update(Y=Y, ydt=1, ldy=8)
+    a.update(kw)
+    return _name((nm.raw.nm_spmm_glu_w4 if two else nm.raw.nm_spmm_w4)(*a.values(), None))
+
+
+@pytest.mark.parametrize("two", [False, True])
+def test_products_refuse(two):
+    f = lambda **kw: _w4(two, **kw)  # noqa: E731
+    assert f(qdt=1) == "NM_ERR_DTYPE" and f(ydt=2) == "NM_ERR_DTYPE" and f(ydt=5) == "NM_ERR_DTYPE"
+    assert f(group=32) == "NM_ERR_SHAPE" and f(group=0) == "NM_ERR_SHAPE"
+    assert f(Ns=2) == "NM_ERR_PATTERN" and f(Ns=9) == "NM_ERR_PATTERN" and f(Ns=-1) == "NM_ERR_PATTERN"
+    assert f(K=40) == "NM_ERR_SHAPE" and f(K=60, Ns=4) == "NM_ERR_SHAPE" and f(K=24, Ns=4) == "NM_ERR_SHAPE"
+    assert f(M=-1) == "NM_ERR_SHAPE" and f(K=-16) == "NM_ERR_SHAPE" and f(R=-1) == "NM_ERR_SHAPE" and f(K=0) == "NM_ERR_SHAPE"
+    assert f(M=(1 << 24) + 1) == "NM_ERR_SHAPE" and f(R=(1 << 24) + 1) == "NM_ERR_SHAPE"
+    for k, v in (("ldx", 56), ("ldc", 0), ("ldi", 1), ("lds", 4), ("ldy", 7), ("ldc", 1 << 26), ("ldi", 1 << 24)):
+        assert f(**{k: v}) == "NM_ERR_SHAPE", k
+    for k, v in (("ldx", 68), ("ldc", 24), ("lds", 10)):
+        assert f(**{k: v}) == "NM_ERR_ALIGN", k
+    ptrs = [("X", X, 8), ("c", C, 8), ("i", I, 2), ("s", S, 4), ("Y", Y, 1)]
+    if two:
+        ptrs += [("c2", C2, 8), ("i2", I2, 2), ("s2", S2, 4)]
+        assert f(act=4) == "NM_ERR_SHAPE" and f(act=-1) == "NM_ERR_SHAPE"
+    for k, p, off in ptrs:
+        assert f(**{k: None}) == "NM_ERR_NULL", k
+        assert f(**{k: P(p.value + off)}) == "NM_ERR_ALIGN", k
+        if k != "Y":
+            assert f(Y=p) == "NM_ERR_ALIAS", k
+    assert f(M=0, X=None, Y=None) == "NM_OK" and f(R=0, Y=None) == "NM_OK"
+
+
+# ------------------------------------------------------------------ the current device
+@pytest.fixture
+def seen(monkeypatch):
+    """The current device, where the tensors are, and (device, stream) of the library's calls; devices are
+    stood in for."""
+    state = {"current": 0, "log": [], "status": 0}
+    monkeypatch.setattr(torch._C, "_cuda_getDevice", lambda: state["current"], raising=False)
+    monkeypatch.setattr(torch._C, "_cuda_setDevice", lambda i: state.update(current=i), raising=False)
+    monkeypatch.setattr(torch._C, "_cuda_getCurrentRawStream", lambda i: 100 + i, raising=False)
+    monkeypatch.setattr(torch.Tensor, "get_device", lambda self: 1)
+    for name in CALLS:
+        def call(*args, n=len(nm.LAYER_SIGNATURES[name][1])):
+            assert len(args) == n
+            state["log"].append((state["current"], args[-1]))
+            return state["status"]
+        monkeypatch.setattr(nm.raw, name, call)
+    return state
+
+
+def _bf16(*shape):
+    return torch.zeros(shape, dtype=torch.bfloat16)
+
+
+def _u8(*shape):
+    return torch.zeros(shape, dtype=torch.uint8)
+
+
+_CODES, _IDX, _SC = _u8(8, 16), torch.zeros((8, 2), dtype=torch.int32), _bf16(1, 8)
+DO = {
+    "nm_quant_w4": lambda: nm.nm_quant_w4(_bf16(8, 64)),
+    "nm_spmm_w4": lambda: nm.nm_spmm_w4(_bf16(2, 64), _CODES, _IDX, _SC),
+    "nm_spmm_glu_w4": lambda: nm.nm_spmm_glu_w4(_bf16(2, 64), _CODES, _IDX, _SC, _CODES, _IDX, _SC),
+}
+CALLS = sorted(DO)
+
+
+def test_every_call_is_tested():
+    assert set(CALLS) == {n for n in nm.LAYER_SIGNATURES if not n.endswith("_workspace")}
+
+
+@pytest.mark.parametrize("name", CALLS)
+@pytest.mark.parametrize("current", [0, 1, 3])
+def test_the_tensors_device_is_current_during_a_call(seen, name, current):
+    seen["current"] = current
+    DO[name]()
+    assert seen["log"] == [(1, 101)] and seen["current"] == current
+
+
+@pytest.mark.parametrize("name", CALLS)
+def test_an_error_goes_back_too(seen, name):
+    seen["status"] = nm.NM_ERR_SHAPE
+    with pytest.raises(nm.NMError):
+        DO[name]()
+    assert seen["log"] == [(1, 101)] and seen["current"] == 0
