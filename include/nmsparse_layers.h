@@ -1,6 +1,7 @@
 /*
  * nmsparse_layers.h - what surrounds and contains a pruned feed-forward block (nmsparse.h,
- * whose conventions hold here): its packed weights in 4 bits.
+ * whose conventions hold here): its packed weights in 4 bits, and a
+ * mixture of such blocks.
  */
 #ifndef NMSPARSE_LAYERS_H
 #define NMSPARSE_LAYERS_H
@@ -52,6 +53,42 @@ nm_status nm_spmm_glu_w4(const void* X, int64_t Mtok, int64_t K, int64_t ldx, co
                          const uint32_t* idx_g, const void* scales_g, const void* codes_u, const uint32_t* idx_u,
                          const void* scales_u, nm_dtype qdt, int64_t R, int64_t ldc, int64_t ldi, int64_t lds, int group,
                          int Ns, nm_act act, void* H, nm_dtype hdt, int64_t ldh, nm_stream_t stream);
+
+/* ---------------------------------------------------------------- mixture of sparse blocks
+ * A whole mixture-of-experts layer for a few tokens (1 <= Mtok <= 64), its experts pruned gated
+ * blocks:
+ *   l[t, e] = x[t] . router[e]                                  (f32 sums)
+ *   p = softmax over all experts, or sigmoid, of l[t]
+ *   the topk experts with the largest p + bias (bias NULL: the largest l; of equal ones the lower
+ *   index; NaN ranks lowest), in descending order
+ *   w[t, j] = route_scale p of the j-th, with renorm divided by the sum of the topk p
+ *   Y[t] = sum_j w[t, j] (act(x[t] Wg_e^T) . (x[t] Wu_e^T)) Wd_e^T,  e the j-th expert of t
+ * H of a token and expert is rounded once to bf16; all else in f32, summed in a fixed order (a
+ * token's experts in j order), Y rounded once.  Experts that no token picks are not read.
+ *   X: bf16 [Mtok, K] (ldx); router: bf16 [E, K] (ldr); bias: f32 [E] or NULL.
+ *   gate, up: [F, K] each, down: [K, F]; packed bf16 values (vdt NM_BF16) or 4-bit codes (NM_I4,
+ *   NM_FP4) with scales.  Expert e's weight starts es_* elements (bytes of codes) after e - 1's.
+ *   Ns: 0, or 3 <= Ns <= 8 over both K' and F'.
+ *   Y: bf16 or f32 [Mtok, K] (ldy); sel: int32 [Mtok, topk] and wts: f32 [Mtok, topk], or NULL: the
+ *   experts that were picked and their weights.
+ * Requires 1 <= topk <= min(E, 16), E <= 512; K and F multiples of 16 and of 2Ns with K', F'
+ * multiples of 16; bases and row strides of X, router and values 16-byte aligned (experts' strides
+ * too), idx 4-byte, scales 8-byte with ld and expert strides multiples of 4.
+ * ws: nm_moe_workspace(...) bytes, 16-byte aligned; no initial contents. */
+typedef enum { NM_ROUTE_SOFTMAX = 0, NM_ROUTE_SIGMOID = 1 } nm_route;
+typedef struct {
+    const void* vals;      /* [E][rows, ld_vals] */
+    const uint32_t* idx;   /* [E][rows, ld_idx] */
+    const void* scales;    /* [E][groups, ld_scales] bf16, or NULL (bf16 values) */
+    int64_t ld_vals, ld_idx, ld_scales;
+    int64_t es_vals, es_idx, es_scales;
+} nm_experts;
+size_t nm_moe_workspace(int64_t Mtok, int64_t K, int64_t F, int E, int topk);
+nm_status nm_moe(const void* X, int64_t Mtok, int64_t K, int64_t ldx, const void* router, int64_t ldr, const float* bias,
+                 int E, int topk, nm_route route, int renorm, float route_scale, const nm_experts* gate,
+                 const nm_experts* up, const nm_experts* down, nm_dtype vdt, int group, int64_t F, int Ns, nm_act act,
+                 void* Y, nm_dtype ydt, int64_t ldy, int32_t* sel, float* wts, void* ws, size_t ws_bytes,
+                 nm_stream_t stream);
 
 #ifdef __cplusplus
 }

@@ -4,11 +4,14 @@ These run in every layer of every token, so their checks are one expression each
 its tensors' device current for the call."""
 from __future__ import annotations
 
+import ctypes
+
 import torch
 
-from ._binding import (NM_ACT_SILU, NM_BF16, _DT, _F, _I, _I64, _P, _TORCH, _check, _enter, _leave, _mat,
-                       _ptr, _refuse, dtype_code, lifted_width, raw)
+from ._binding import (NM_ACT_SILU, NM_BF16, _DT, _F, _I, _I64, _P, _SZ, _TORCH, _check, _enter, _leave, _mat,
+                       _need, _ptr, _refuse, dtype_code, lifted_width, raw)
 
+NM_ROUTE_SOFTMAX, NM_ROUTE_SIGMOID = range(2)
 NM_I4, NM_FP4 = 5, 6      # 4-bit codes of packed values: sign and 3-bit magnitude, or OCP e2m1
 
 LAYER_SIGNATURES = {
@@ -16,6 +19,9 @@ LAYER_SIGNATURES = {
     "nm_spmm_w4": (_I, [_P, _I64, _I64, _I64, _P, _I, _P, _P, _I64, _I64, _I64, _I64, _I, _I, _P, _I, _I64, _P]),
     "nm_spmm_glu_w4": (_I, [_P, _I64, _I64, _I64, _P, _P, _P, _P, _P, _P, _I, _I64, _I64, _I64, _I64, _I, _I, _I, _P, _I,
                             _I64, _P]),
+    "nm_moe_workspace": (_SZ, [_I64, _I64, _I64, _I, _I]),
+    "nm_moe": (_I, [_P, _I64, _I64, _I64, _P, _I64, _P, _I, _I, _I, _I, _F, _P, _P, _P, _I, _I, _I64, _I, _I, _P, _I, _I64, _P,
+                    _P, _P, _SZ, _P]),
 }
 for _name, (_res, _args) in LAYER_SIGNATURES.items():
     _fn = getattr(raw, _name)
@@ -120,3 +126,82 @@ def nm_spmm_glu_w4(X: torch.Tensor, codes_g: torch.Tensor, idx_g: torch.Tensor, 
     if st:
         _check(st)
     return H
+
+
+# ---------------------------------------------------------------- mixture of sparse blocks
+class _Experts(ctypes.Structure):
+    _fields_ = [("vals", _P), ("idx", _P), ("scales", _P), ("ld_vals", _I64), ("ld_idx", _I64), ("ld_scales", _I64),
+                ("es_vals", _I64), ("es_idx", _I64), ("es_scales", _I64)]
+
+
+class MoELayer:
+    """The weights of a mixture-of-experts layer, as nm_moe takes them: router [E, K] bf16, the experts' gate and up
+    [E, hidden, .] and down [E, K, .] weights stacked (the packers' vals or nm_quant_w4's codes, their idx, and scales
+    [E, groups, rows] of 4-bit ones), an optional f32 selection bias [E].  Checked once and kept for as long as the
+    object lives; build it once and use it every step."""
+
+    def __init__(self, router, gate, gate_idx, up, up_idx, down, down_idx, hidden, vdt=NM_BF16, group=128, Ns=0,
+                 gate_scales=None, up_scales=None, down_scales=None, bias=None):
+        r = _mat(router)
+        if not (r and router.dtype == torch.bfloat16 and router.device.type == "cuda"):
+            _refuse("router must be a row-major bf16 matrix on a GPU", router=router)
+        if vdt not in (NM_BF16, NM_I4, NM_FP4):
+            raise ValueError("vdt is NM_BF16, NM_I4 or NM_FP4")
+        if Ns and not 3 <= Ns <= 8:
+            raise ValueError(f"Ns is 0 or 3 to 8, got {Ns}")
+        self.experts, self.K, self.ldr = r
+        self.hidden, self.vdt, self.group, self.Ns, self.device = int(hidden), vdt, group, Ns, router.device
+        E, dev, four = self.experts, router.device, vdt != NM_BF16
+        lift = lambda n: lifted_width(n, Ns) if Ns else n  # noqa: E731
+        self.keep = [router, gate, gate_idx, gate_scales, up, up_idx, up_scales, down, down_idx, down_scales, bias]
+        self.router, self.bias = router, bias
+        if bias is not None and not (bias.dtype == torch.float32 and bias.shape == (E,) and bias.is_contiguous() and
+                                     bias.device == dev):
+            _refuse(f"bias must be {E} contiguous f32 values on {dev}", bias=bias)
+        self.weights = []
+        for name, rows, width, v, i, s in (("gate", self.hidden, lift(self.K), gate, gate_idx, gate_scales),
+                                           ("up", self.hidden, lift(self.K), up, up_idx, up_scales),
+                                           ("down", self.K, lift(self.hidden), down, down_idx, down_scales)):
+            slots = width // 4 if four else width // 2
+            ok = (v.dim() == 3 and i.dim() == 3 and v.dtype == (torch.uint8 if four else torch.bfloat16) and
+                  i.dtype == torch.int32 and v.shape[:2] == (E, rows) == i.shape[:2] and v.shape[2] >= slots and
+                  i.shape[2] >= (width + 31) // 32 and v.stride(2) == 1 == i.stride(2) and v.device == dev == i.device)
+            if four and ok:
+                ok = (s is not None and s.dim() == 3 and s.dtype == torch.bfloat16 and s.shape[0] == E and
+                      s.shape[1] * group >= width and s.shape[2] >= rows and s.stride(2) == 1 and s.device == dev)
+            if not ok:
+                _refuse(f"{name}: {slots} values{' and scales' if four else ''} and {(width + 31) // 32} index words a row for "
+                        f"{E} experts of {rows} rows", vals=v, idx=i, scales=s)
+            lds = 0 if not four else s.stride(1) if s.shape[1] > 1 else (s.shape[2] + 3) // 4 * 4
+            one = lambda t: t.stride(0) if E > 1 else 0  # noqa: E731
+            self.weights.append(_Experts(v.data_ptr(), i.data_ptr(), s.data_ptr() if four else None, v.stride(1), i.stride(1), lds,
+                                         one(v), one(i), one(s) if four else 0))
+        self.address = [ctypes.addressof(w) for w in self.weights]
+
+    def get_device(self) -> int:
+        return self.router.get_device()
+
+
+def nm_moe(layer: MoELayer, X: torch.Tensor, topk: int, act: int = NM_ACT_SILU, route: int = NM_ROUTE_SOFTMAX,
+           renorm: bool = False, route_scale: float = 1.0, ydt: int = NM_BF16, want_routing: bool = False,
+           out: torch.Tensor | None = None, ws: torch.Tensor | None = None):
+    """Y = sum over a token's topk experts of weight * gated block, for up to 64 tokens: Y, or with want_routing
+    (Y, experts [tokens, topk] int32, weights [tokens, topk] f32)."""
+    x = _mat(X)
+    if not (x and x[1] == layer.K and X.dtype == torch.bfloat16 and X.device == layer.device):
+        _refuse(f"X must be row-major bf16 tokens of {layer.K} columns on {layer.device}", X=X)
+    Mtok, K, ldx = x
+    Y, ldy, ydt = _out(out, ydt, Mtok, K, X)
+    sel = X.new_empty((Mtok, topk), dtype=torch.int32) if want_routing else None
+    wts = X.new_empty((Mtok, topk), dtype=torch.float32) if want_routing else None
+    ws = _need(raw.nm_moe_workspace(Mtok, K, layer.hidden, layer.experts, topk), ws, X)
+    stream, back = _enter(X)
+    try:
+        st = raw.nm_moe(X.data_ptr(), Mtok, K, ldx, layer.router.data_ptr(), layer.ldr, _ptr(layer.bias), layer.experts, topk, route,
+                        renorm, route_scale, *layer.address, layer.vdt, layer.group, layer.hidden, layer.Ns, act, Y.data_ptr(),
+                        ydt, ldy, _ptr(sel), _ptr(wts), _ptr(ws), 0 if ws is None else ws.nbytes, stream)
+    finally:
+        _leave(back)
+    if st:
+        _check(st)
+    return (Y, sel, wts) if want_routing else Y

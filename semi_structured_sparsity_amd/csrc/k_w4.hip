@@ -156,16 +156,7 @@ __global__ __launch_bounds__(NW * 64) void w4_kernel(W4Args a) {
                 v += red[n][GLU ? 2 * tile : tile][k];
                 if constexpr (GLU) up += red[n][2 * tile + 1][k];
             }
-            if constexpr (GLU) {
-                float f;
-                switch (a.act) {
-                    case NM_ACT_SILU: f = act_value<NM_ACT_SILU>(v); break;
-                    case NM_ACT_GELU: f = act_value<NM_ACT_GELU>(v); break;
-                    case NM_ACT_GELU_TANH: f = act_value<NM_ACT_GELU_TANH>(v); break;
-                    default: f = act_value<NM_ACT_RELU2>(v); break;
-                }
-                v = f * up;
-            }
+            if constexpr (GLU) v = few_act(a.act, v) * up;
             if (a.y32) ((float*)a.Y)[tok * a.ldy + r] = v;
             else ((uint16_t*)a.Y)[tok * a.ldy + r] = (uint16_t)f32_to_bf16_bits(v);
         }

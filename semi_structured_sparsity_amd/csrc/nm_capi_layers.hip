@@ -12,6 +12,8 @@ bool group_ok(int g) { return g == 64 || g == 128 || g == 256; }
 int64_t lifted(int64_t K, int Ns) { return Ns ? K / (2 * Ns) * 4 * (Ns - 1) : K; }
 
 constexpr int64_t kMost = (int64_t)1 << 24;   // tokens, columns, rows of one call
+constexpr int64_t kMoeMostTokens = 64;
+constexpr int kMoeMostExperts = 512, kMoeMostTopk = 16;
 
 // the checks of a 4-bit product; nw: 1, or 2 weights (gated block)
 nm_status w4_check(const char* fn, const W4In& in, int nw, bool* run) {
@@ -105,6 +107,105 @@ nm_status nm_spmm_glu_w4(const void* X, int64_t Mtok, int64_t K, int64_t ldx, co
     bool run = false;
     const nm_status st = w4_check(fn, in, 2, &run);
     return st != NM_OK || !run ? st : launch_w4(in, (hipStream_t)stream);
+}
+
+size_t nm_moe_workspace(int64_t Mtok, int64_t K, int64_t F, int E, int topk) {
+    if (Mtok <= 0 || Mtok > kMoeMostTokens || K <= 0 || F <= 0 || K > kMost || F > kMost || E <= 0 || E > kMoeMostExperts || topk <= 0 ||
+        topk > E || topk > kMoeMostTopk)
+        return 0;
+    return moe_ws(Mtok, K, F, E, topk);
+}
+
+nm_status nm_moe(const void* X, int64_t Mtok, int64_t K, int64_t ldx, const void* router, int64_t ldr, const float* bias,
+                 int E, int topk, nm_route route, int renorm, float route_scale, const nm_experts* gate,
+                 const nm_experts* up, const nm_experts* down, nm_dtype vdt, int group, int64_t F, int Ns, nm_act act,
+                 void* Y, nm_dtype ydt, int64_t ldy, int32_t* sel, float* wts, void* ws, size_t ws_bytes,
+                 nm_stream_t stream) {
+    const char* fn = "nm_moe";
+    NM_REQ(Mtok >= 0 && K >= 0 && F >= 0, NM_ERR_SHAPE, "%s: negative size", fn);
+    NM_REQ(Mtok <= kMoeMostTokens, NM_ERR_SHAPE, "%s: made for up to %lld tokens (got %lld)", fn, (long long)kMoeMostTokens,
+           (long long)Mtok);
+    NM_REQ(K <= kMost && F <= kMost, NM_ERR_SHAPE, "%s: widths up to 2^24", fn);
+    NM_REQ(E >= 1 && E <= kMoeMostExperts && topk >= 1 && topk <= E && topk <= kMoeMostTopk, NM_ERR_SHAPE,
+           "%s: need 1 <= topk <= min(E, 16), E <= 512 (got %d of %d)", fn, topk, E);
+    NM_REQ(route == NM_ROUTE_SOFTMAX || route == NM_ROUTE_SIGMOID, NM_ERR_SHAPE, "%s: unknown route", fn);
+    NM_REQ(known_act(act), NM_ERR_SHAPE, "%s: unknown activation", fn);
+    NM_REQ(Ns == 0 || (Ns >= 3 && Ns <= 8), NM_ERR_PATTERN,
+           "%s: supported patterns are plain 2:4 (Ns=0) and (2N-2):2N via slide (3 <= Ns <= 8), got Ns=%d", fn, Ns);
+    NM_REQ(vdt == NM_BF16 || code4(vdt), NM_ERR_DTYPE, "%s: weights are bf16 values or NM_I4 / NM_FP4 codes", fn);
+    NM_REQ(ydt == NM_BF16 || ydt == NM_F32, NM_ERR_DTYPE, "%s: Y must be bf16 or f32", fn);
+    NM_REQ(vdt == NM_BF16 || group_ok(group), NM_ERR_SHAPE, "%s: group must be 64, 128 or 256 (got %d)", fn, group);
+    NM_REQ(K % 16 == 0 && F % 16 == 0 && (Ns == 0 || (K % (2 * Ns) == 0 && F % (2 * Ns) == 0)), NM_ERR_SHAPE,
+           "%s: K and F must be multiples of 16 and of 2N", fn);
+    const int64_t Kl = lifted(K, Ns), Fl = lifted(F, Ns);
+    NM_REQ(Kl % 16 == 0 && Fl % 16 == 0, NM_ERR_SHAPE, "%s: the lifted widths must be multiples of 16", fn);
+    if (Mtok == 0 || K == 0) return NM_OK;
+    NM_REQ(F > 0, NM_ERR_SHAPE, "%s: F == 0", fn);
+    NM_REQ(X && router && Y && gate && up && down, NM_ERR_NULL, "%s: NULL argument", fn);
+    NM_REQ(ldx >= K && ldr >= K && ldy >= K, NM_ERR_SHAPE, "%s: leading dimension too small", fn);
+    NM_REQ(aligned16(X) && aligned16(router) && ldx % 8 == 0 && ldr % 8 == 0, NM_ERR_ALIGN,
+           "%s: X and router need 16-byte aligned bases and row strides", fn);
+    NM_REQ(aligned_to(Y, esize(ydt)) && aligned_to(sel, 4) && aligned_to(wts, 4) && aligned_to(bias, 4), NM_ERR_ALIGN,
+           "%s: an argument is not element-aligned", fn);
+    const size_t need = moe_ws(Mtok, K, F, E, topk);
+    NM_REQ(ws && ws_bytes >= need, NM_ERR_WORKSPACE, "%s: workspace of %zu bytes needed", fn, need);
+    NM_REQ(aligned16(ws), NM_ERR_ALIGN, "%s: ws must be 16-byte aligned", fn);
+    const Range out[] = {span(Y, Mtok, K, ldy, esize(ydt)), span(sel, Mtok, topk, topk, 4), span(wts, Mtok, topk, topk, 4),
+                         Range{(uintptr_t)ws, (uintptr_t)ws + need}};
+    const Range in[] = {span(X, Mtok, K, ldx, 2), span(router, E, K, ldr, 2), span(bias, 1, E, E, 4)};
+    for (int i = 0; i < 4; ++i) {
+        for (const Range& r : in) NM_REQ(!overlap(out[i], r), NM_ERR_ALIAS, "%s: an output or ws overlaps an input", fn);
+        for (int j = 0; j < i; ++j) NM_REQ(!overlap(out[i], out[j]), NM_ERR_ALIAS, "%s: outputs or ws overlap", fn);
+    }
+    MoeIn m{};
+    const nm_experts* w[3] = {gate, up, down};
+    for (int i = 0; i < 3; ++i) {
+        const nm_experts& e = *w[i];
+        const int64_t rows = i == 2 ? K : F, width = i == 2 ? Fl : Kl, iw = (width + 31) / 32;
+        const bool bf = vdt == NM_BF16;
+        const int64_t vbytes = bf ? width : width / 4, es = bf ? 2 : 1, groups = bf ? 1 : ceil_div(width, group);
+        NM_REQ(e.vals && e.idx && (bf || e.scales), NM_ERR_NULL, "%s: NULL weight", fn);
+        NM_REQ(e.ld_vals * es >= vbytes && e.ld_idx >= iw && (bf || e.ld_scales >= rows), NM_ERR_SHAPE,
+               "%s: a weight's leading dimension is too small", fn);
+        NM_REQ(e.ld_vals * es < (1 << 26) && e.ld_idx < (1 << 24), NM_ERR_SHAPE, "%s: a weight's leading dimension is too large",
+               fn);
+        NM_REQ(e.es_vals >= 0 && e.es_idx >= 0 && (bf || e.es_scales >= 0), NM_ERR_SHAPE, "%s: negative expert stride", fn);
+        NM_REQ(aligned16(e.vals) && e.ld_vals * es % 16 == 0 && e.es_vals * es % 16 == 0 && aligned_to(e.idx, 4) &&
+                   (bf || (aligned_to(e.scales, 8) && e.ld_scales % 4 == 0 && e.es_scales % 4 == 0)),
+               NM_ERR_ALIGN, "%s: a weight is not aligned (values 16 bytes, idx 4, scales 8)", fn);
+        for (const Range& o : out) {
+            Range v = span(e.vals, rows, vbytes, e.ld_vals * es, 1), x = span(e.idx, rows, iw, e.ld_idx, 4);
+            Range sc = bf ? Range{0, 0} : span(e.scales, groups, rows, e.ld_scales, 2);
+            v.hi += (uintptr_t)((E - 1) * e.es_vals * es);
+            x.hi += (uintptr_t)((E - 1) * e.es_idx * 4);
+            if (!bf) sc.hi += (uintptr_t)((E - 1) * e.es_scales * 2);
+            NM_REQ(!overlap(o, v) && !overlap(o, x) && !overlap(o, sc), NM_ERR_ALIAS, "%s: an output or ws overlaps a weight", fn);
+        }
+        m.w[i] = e;
+    }
+    m.X = X;
+    m.Mtok = Mtok;
+    m.K = K;
+    m.ldx = ldx;
+    m.router = router;
+    m.ldr = ldr;
+    m.bias = bias;
+    m.E = E;
+    m.topk = topk;
+    m.route = route;
+    m.renorm = renorm != 0;
+    m.route_scale = route_scale;
+    m.vdt = vdt;
+    m.group = group;
+    m.F = F;
+    m.Ns = Ns;
+    m.act = act;
+    m.Y = Y;
+    m.ydt = ydt;
+    m.ldy = ldy;
+    m.sel = sel;
+    m.wts = wts;
+    return launch_moe(m, ws, (hipStream_t)stream);
 }
 
 }  // extern "C"

@@ -67,6 +67,15 @@ __device__ __forceinline__ void few_swap16(uint32_t& a, uint32_t& b) {
     b = r[1];
 }
 
+__device__ __forceinline__ float few_act(int act, float g) {
+    switch (act) {
+        case NM_ACT_SILU: return act_value<NM_ACT_SILU>(g);
+        case NM_ACT_GELU: return act_value<NM_ACT_GELU>(g);
+        case NM_ACT_GELU_TANH: return act_value<NM_ACT_GELU_TANH>(g);
+        default: return act_value<NM_ACT_RELU2>(g);
+    }
+}
+
 // 16 rows of one packed weight, as a wave sees them
 struct FewRows {
     const uint8_t* vals;      // uniform: first row of the tile

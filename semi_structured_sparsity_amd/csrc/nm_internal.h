@@ -381,6 +381,31 @@ struct W4In {
     int64_t ldy;
 };
 nm_status launch_w4(const W4In& in, hipStream_t s);
+// mixture of sparse blocks
+struct MoeIn {
+    const void* X;
+    int64_t Mtok, K, ldx;
+    const void* router;
+    int64_t ldr;
+    const float* bias;
+    int E, topk;
+    nm_route route;
+    int renorm;
+    float route_scale;
+    nm_experts w[3];   // gate, up, down
+    nm_dtype vdt;
+    int group;
+    int64_t F;
+    int Ns;
+    nm_act act;
+    void* Y;
+    nm_dtype ydt;
+    int64_t ldy;
+    int32_t* sel;
+    float* wts;
+};
+size_t moe_ws(int64_t Mtok, int64_t K, int64_t F, int E, int topk);
+nm_status launch_moe(const MoeIn& in, void* ws, hipStream_t s);
 // Hutchinson
 size_t hutch_ws(int64_t n, int64_t K, int64_t R, int probes);
 size_t hutch_score_ws(int64_t n, int64_t K, int64_t R, int probes);

@@ -94,6 +94,65 @@ def test_products_refuse(two):
     assert f(M=0, X=None, Y=None) == "NM_OK" and f(R=0, Y=None) == "NM_OK"
 
 
+# ------------------------------------------------------------------ mixture of sparse blocks
+def _experts(base, rows, slots, words, groups, **kw):
+    e = nm._layers._Experts(base, base + (1 << 20), base + (2 << 20), slots, words, rows, rows * slots, rows * words, rows * groups)
+    for k, v in kw.items():
+        setattr(e, k, v)
+    return e
+
+
+def _moe(w=None, **kw):
+    """w: (which weight, field, value)"""
+    es = [_experts((20 + i) << 32, 32 if i < 2 else 64, 16, 2, 1) for i in range(3)]
+    if w:
+        setattr(es[w[0]], w[1], w[2])
+    a = dict(X=X, M=4, K=64, ldx=64, router=C, ldr=64, bias=None, E=4, topk=2, route=0, renorm=1, scale=1.0, gate=0, up=1, down=2,
+             vdt=5, group=64, F=32, Ns=0, act=0, Y=Y, ydt=1, ldy=64, sel=I, wts=S, ws=V, n=1 << 40)
+    a.update(kw)
+    for k in ("gate", "up", "down"):
+        a[k] = ctypes.byref(es[a[k]]) if a[k] is not None else None
+    return _name(nm.raw.nm_moe(*a.values(), None))
+
+
+def test_moe_refuses():
+    assert _moe(M=65) == "NM_ERR_SHAPE" and _moe(M=-1) == "NM_ERR_SHAPE" and _moe(K=-16) == "NM_ERR_SHAPE"
+    assert _moe(topk=0) == "NM_ERR_SHAPE" and _moe(topk=5) == "NM_ERR_SHAPE" and _moe(E=32, topk=17) == "NM_ERR_SHAPE"
+    assert _moe(E=0) == "NM_ERR_SHAPE" and _moe(E=513) == "NM_ERR_SHAPE"
+    assert _moe(route=2) == "NM_ERR_SHAPE" and _moe(act=4) == "NM_ERR_SHAPE" and _moe(group=96) == "NM_ERR_SHAPE"
+    assert _moe(vdt=2) == "NM_ERR_DTYPE" and _moe(ydt=2) == "NM_ERR_DTYPE"
+    assert _moe(Ns=2) == "NM_ERR_PATTERN" and _moe(Ns=9) == "NM_ERR_PATTERN"
+    assert _moe(K=40) == "NM_ERR_SHAPE" and _moe(F=40) == "NM_ERR_SHAPE" and _moe(F=0) == "NM_ERR_SHAPE" and _moe(Ns=3) == "NM_ERR_SHAPE"
+    for k in ("ldx", "ldr", "ldy"):
+        assert _moe(**{k: 56}) == "NM_ERR_SHAPE", k
+    for k in ("X", "router", "gate", "up", "down", "Y"):
+        assert _moe(**{k: None}) == "NM_ERR_NULL", k
+    for k, p, off in (("X", X, 8), ("router", C, 8), ("Y", Y, 1), ("sel", I, 2), ("wts", S, 2), ("ws", V, 8), ("bias", C2, 2)):
+        assert _moe(**{k: P(p.value + off)}) == "NM_ERR_ALIGN", k
+    assert _moe(ldx=68) == "NM_ERR_ALIGN" and _moe(ldr=68) == "NM_ERR_ALIGN"
+    assert _moe(ws=None) == "NM_ERR_WORKSPACE" and _moe(n=16) == "NM_ERR_WORKSPACE"
+    for w in range(3):
+        for f, v in (("vals", None), ("idx", None), ("scales", None)):
+            assert _moe(w=(w, f, v)) == "NM_ERR_NULL", (w, f)
+        for f, v in (("ld_vals", 0), ("ld_idx", 0), ("ld_scales", 28), ("es_vals", -16), ("es_idx", -1), ("es_scales", -4),
+                     ("ld_vals", 1 << 26), ("ld_idx", 1 << 24)):
+            assert _moe(w=(w, f, v)) == "NM_ERR_SHAPE", (w, f)
+        for f, v in (("vals", (30 << 32) + 8), ("idx", (30 << 32) + 2), ("scales", (30 << 32) + 4), ("ld_vals", 24), ("es_vals", 8),
+                     ("ld_scales", 66), ("es_scales", 66)):
+            assert _moe(w=(w, f, v)) == "NM_ERR_ALIGN", (w, f)
+        assert _moe(Y=P(((20 + w) << 32) + 3 * 16)) == "NM_ERR_ALIAS" and _moe(ws=P((20 + w) << 32)) == "NM_ERR_ALIAS"
+    assert _moe(Y=X) == "NM_ERR_ALIAS" and _moe(sel=S) == "NM_ERR_ALIAS" and _moe(ws=C) == "NM_ERR_ALIAS" and _moe(wts=Y) == "NM_ERR_ALIAS"
+    assert _moe(M=0, X=None, Y=None, gate=None) == "NM_OK"
+
+
+def test_moe_workspace_of_refused_sizes():
+    ws = nm.raw.nm_moe_workspace
+    assert ws(4, 64, 32, 4, 2) > 0
+    for bad in ((0, 64, 32, 4, 2), (65, 64, 32, 4, 2), (4, 0, 32, 4, 2), (4, 64, -1, 4, 2), (4, 64, 32, 0, 1), (4, 64, 32, 513, 2),
+                (4, 64, 32, 4, 5), (4, 64, 32, 64, 17), (4, 64, 32, 4, 0), (4, 1 << 40, 32, 4, 2), (-3, 64, 32, 4, 2)):
+        assert ws(*bad) == 0, bad
+
+
 # ------------------------------------------------------------------ the current device
 @pytest.fixture
 def seen(monkeypatch):
@@ -121,11 +180,20 @@ def _u8(*shape):
     return torch.zeros(shape, dtype=torch.uint8)
 
 
+def _layer():
+    """A layer's handle, as one on a GPU is."""
+    t = nm.MoELayer.__new__(nm.MoELayer)
+    t.experts, t.K, t.ldr, t.hidden, t.vdt, t.group, t.Ns, t.device = 4, 64, 64, 32, 1, 64, 0, torch.device("cpu")
+    t.router, t.bias, t.address = _bf16(4, 64), None, [0, 0, 0]
+    return t
+
+
 _CODES, _IDX, _SC = _u8(8, 16), torch.zeros((8, 2), dtype=torch.int32), _bf16(1, 8)
 DO = {
     "nm_quant_w4": lambda: nm.nm_quant_w4(_bf16(8, 64)),
     "nm_spmm_w4": lambda: nm.nm_spmm_w4(_bf16(2, 64), _CODES, _IDX, _SC),
     "nm_spmm_glu_w4": lambda: nm.nm_spmm_glu_w4(_bf16(2, 64), _CODES, _IDX, _SC, _CODES, _IDX, _SC),
+    "nm_moe": lambda: nm.nm_moe(_layer(), _bf16(2, 64), 2),
 }
 CALLS = sorted(DO)
 
