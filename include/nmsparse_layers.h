@@ -1,7 +1,7 @@
 /*
  * nmsparse_layers.h - what surrounds and contains a pruned feed-forward block (nmsparse.h,
- * whose conventions hold here): its packed weights in 4 bits, and a
- * mixture of such blocks.
+ * whose conventions hold here): its packed weights in 4 bits, a
+ * mixture of such blocks, and the norms before and after it.
  */
 #ifndef NMSPARSE_LAYERS_H
 #define NMSPARSE_LAYERS_H
@@ -89,6 +89,50 @@ nm_status nm_moe(const void* X, int64_t Mtok, int64_t K, int64_t ldx, const void
                  const nm_experts* up, const nm_experts* down, nm_dtype vdt, int group, int64_t F, int Ns, nm_act act,
                  void* Y, nm_dtype ydt, int64_t ldy, int32_t* sel, float* wts, void* ws, size_t ws_bytes,
                  nm_stream_t stream);
+
+/* ---------------------------------------------------------------- norms around a block
+ * The end of one block and the start of the next in one pass over the tokens:
+ *   Z = res_scale X + gate . norm_post(Y),  N = norm_pre(Z)
+ * X: the residual stream [Mtok, C] (ldx), Y: the block's output, bf16 [Mtok, C] (ldyb), or NULL
+ * (Z = res_scale X).  gate: [., C] (ldg), token m takes row m / gate_rows (gate_rows 0: all take row 0),
+ * or NULL for 1.
+ *   NM_NORM_RMS   v w / sqrt(mean(v^2) + eps) [+ b]
+ *   NM_NORM_LAYER (v - mean(v)) w / sqrt(mean((v - mean(v))^2) + eps) [+ b]
+ *   NM_NORM_NONE  v itself (its w and b must be NULL)
+ * over the C columns of a token; w, b [C] may be NULL (ones, zeros).  w, b and gate are all of wdt
+ * (bf16 or f32).  N is that of the unrounded Z; statistics and all else in f32, outputs rounded once.
+ *   Z: X's type [Mtok, C] (ldz), or NULL: not stored.  Z may be X itself (in place).
+ *   Nout: NULL if and only if pre is NM_NORM_NONE; ndt BF16 or F32 [Mtok, C] (ldn), or one-byte codes
+ *   I8 / FP8 with a scale per token in n_scale (f32 [Mtok]): codes and scale as nm_quant_lift has
+ *   them, of the unrounded N; written lifted for Ns >= 3 ([Mtok, K'], as nm_quant_lift), plain for Ns == 0.
+ * 1 <= C <= 32768.  Rows of 16-byte alignment with C % 8 == 0 are read in whole vectors; any element-
+ * aligned ones are accepted (codes need C % 8 == 0, C % 2Ns == 0 and 4-byte aligned rows). */
+typedef enum { NM_NORM_NONE = 0, NM_NORM_RMS = 1, NM_NORM_LAYER = 2 } nm_norm;
+nm_status nm_block_norm(const void* X, nm_dtype xdt, int64_t Mtok, int64_t C, int64_t ldx, float res_scale,
+                        const void* Y, int64_t ldyb, const void* gate, int64_t ldg, int64_t gate_rows, nm_norm post,
+                        const void* w_post, const void* b_post, nm_norm pre, const void* w_pre, const void* b_pre,
+                        nm_dtype wdt, float eps, void* Z, int64_t ldz, void* Nout, nm_dtype ndt, int Ns, int64_t ldn,
+                        float* n_scale, nm_stream_t stream);
+
+/* Gradients of nm_block_norm from Z as the forward pass stored it, with statistics taken from it
+ * and from Y anew.  dZ: gradient of Z from above in X's type [Mtok, C] (lddz), or NULL; dN: of N,
+ * bf16 or f32 [Mtok, C] (lddn), or NULL (needed for dw_pre, db_pre; not with pre NM_NORM_NONE).
+ * xdt is the type of Z, dZ and dX.
+ *   g = dZ + (gradient of N through norm_pre),  dX = res_scale g,
+ *   dgate = sum over its tokens of g . norm_post(Y),  dY = gradient of norm_post for g . gate
+ * dX: X's type [Mtok, C] (lddx), dY: bf16 [Mtok, C] (lddy), either may be NULL; dX may be dZ itself.
+ * dw_pre, db_pre, dw_post, db_post: f32 [C], dgate: f32 [gate rows, C] (contiguous); each may be NULL.
+ * Parameter sums are in f32 in a fixed order.  Zero tokens give zero parameter gradients (dgate has
+ * one row then).
+ * ws: nm_block_norm_backward_workspace(...) bytes, 16-byte aligned, no initial contents; may be NULL
+ * where no parameter gradient is wanted. */
+size_t nm_block_norm_backward_workspace(int64_t Mtok, int64_t C, int64_t gate_rows);
+nm_status nm_block_norm_backward(const void* Z, nm_dtype xdt, int64_t Mtok, int64_t C, int64_t ldz, const void* dZ,
+                                 int64_t lddz, const void* dN, nm_dtype dndt, int64_t lddn, float res_scale,
+                                 const void* Y, int64_t ldyb, const void* gate, int64_t ldg, int64_t gate_rows, nm_norm post, const void* w_post,
+                                 const void* b_post, nm_norm pre, const void* w_pre, nm_dtype wdt, float eps, void* dX,
+                                 int64_t lddx, void* dY, int64_t lddy, float* dw_pre, float* db_pre, float* dw_post,
+                                 float* db_post, float* dgate, void* ws, size_t ws_bytes, nm_stream_t stream);
 
 #ifdef __cplusplus
 }

@@ -5,13 +5,15 @@ its tensors' device current for the call."""
 from __future__ import annotations
 
 import ctypes
+from typing import NamedTuple
 
 import torch
 
-from ._binding import (NM_ACT_SILU, NM_BF16, _DT, _F, _I, _I64, _P, _SZ, _TORCH, _check, _enter, _leave, _mat,
+from ._binding import (NM_ACT_SILU, NM_BF16, NM_F32, _DT, _F, _I, _I64, _P, _SZ, _TORCH, _check, _enter, _leave, _mat,
                        _need, _ptr, _refuse, dtype_code, lifted_width, raw)
 
 NM_ROUTE_SOFTMAX, NM_ROUTE_SIGMOID = range(2)
+NM_NORM_NONE, NM_NORM_RMS, NM_NORM_LAYER = range(3)
 NM_I4, NM_FP4 = 5, 6      # 4-bit codes of packed values: sign and 3-bit magnitude, or OCP e2m1
 
 LAYER_SIGNATURES = {
@@ -22,6 +24,11 @@ LAYER_SIGNATURES = {
     "nm_moe_workspace": (_SZ, [_I64, _I64, _I64, _I, _I]),
     "nm_moe": (_I, [_P, _I64, _I64, _I64, _P, _I64, _P, _I, _I, _I, _I, _F, _P, _P, _P, _I, _I, _I64, _I, _I, _P, _I, _I64, _P,
                     _P, _P, _SZ, _P]),
+    "nm_block_norm": (_I, [_P, _I, _I64, _I64, _I64, _F, _P, _I64, _P, _I64, _I64, _I, _P, _P, _I, _P, _P, _I, _F, _P, _I64, _P, _I,
+                           _I, _I64, _P, _P]),
+    "nm_block_norm_backward_workspace": (_SZ, [_I64, _I64, _I64]),
+    "nm_block_norm_backward": (_I, [_P, _I, _I64, _I64, _I64, _P, _I64, _P, _I, _I64, _F, _P, _I64, _P, _I64, _I64, _I, _P, _P, _I,
+                                    _P, _I, _F, _P, _I64, _P, _I64, _P, _P, _P, _P, _P, _P, _SZ, _P]),
 }
 for _name, (_res, _args) in LAYER_SIGNATURES.items():
     _fn = getattr(raw, _name)
@@ -205,3 +212,124 @@ def nm_moe(layer: MoELayer, X: torch.Tensor, topk: int, act: int = NM_ACT_SILU, 
     if st:
         _check(st)
     return (Y, sel, wts) if want_routing else Y
+
+
+# ---------------------------------------------------------------- norms around a block
+_FLOATS = (torch.bfloat16, torch.float32)
+
+
+def _norm_side(X, C, gate, gate_rows, Mtok, vectors):
+    """(type code of the weights, the gate's row stride) after their checks."""
+    given = [t for t in (*vectors, gate) if t is not None]
+    wt, dev = given[0].dtype if given else torch.bfloat16, X.device
+    for t in vectors:
+        if t is not None and not (t.shape == (C,) and t.dtype == wt and t.is_contiguous() and t.device == dev):
+            _refuse(f"norm weights are {C} contiguous values of one type on {dev}", weight=t)
+    ldg = C
+    if gate is not None:
+        g = _mat(gate)
+        rows = (Mtok + gate_rows - 1) // gate_rows if gate_rows > 0 else 1
+        if not (g and g[0] >= rows and g[1] == C and gate.dtype == wt and gate.device == dev):
+            _refuse(f"gate must be row-major, {rows} rows of {C} in the weights' type", gate=gate)
+        ldg = g[2]
+    if wt not in _FLOATS:
+        _refuse("norm weights and gate are bf16 or f32", weight=given[0])
+    return _DT[wt], ldg
+
+
+def nm_block_norm(X: torch.Tensor, Y: torch.Tensor | None = None, gate: torch.Tensor | None = None, gate_rows: int = 0,
+                  res_scale: float = 1.0, post: int = NM_NORM_NONE, w_post: torch.Tensor | None = None,
+                  b_post: torch.Tensor | None = None, pre: int = NM_NORM_RMS, w_pre: torch.Tensor | None = None,
+                  b_pre: torch.Tensor | None = None, eps: float = 1e-6, ndt: int = NM_BF16, Ns: int = 0, want_z: bool = True,
+                  out_z: torch.Tensor | None = None):
+    """(Z, N, n_scale) with Z = res_scale X + gate . norm_post(Y) and N = norm_pre(Z): N in bf16 or f32, or int8 / FP8
+    codes (lifted for Ns >= 3) with their scales; what is not made is None.  gate: rows of C columns, one for gate_rows
+    tokens each (0: one row for all).  out_z may be X itself."""
+    x, dev = _mat(X), X.device
+    if not (x and X.dtype in _FLOATS):
+        _refuse("X must be a row-major bf16 or f32 matrix", X=X)
+    Mtok, C, ldx = x
+    y = None if Y is None else _mat(Y)
+    if Y is not None and not (y and y[:2] == (Mtok, C) and Y.dtype == torch.bfloat16 and Y.device == dev):
+        _refuse("Y must be row-major bf16 of X's shape", X=X, Y=Y)
+    wdt, ldg = _norm_side(X, C, gate, gate_rows, Mtok, (w_post, b_post, w_pre, b_pre))
+    Z, ldz = None, C
+    if out_z is not None:
+        z = _mat(out_z)
+        if not (z and z[:2] == (Mtok, C) and out_z.dtype == X.dtype and out_z.device == dev):
+            _refuse("out_z must be row-major, of X's shape and type", X=X, out_z=out_z)
+        Z, ldz = out_z, z[2]
+    elif want_z:
+        Z = X.new_empty((Mtok, C))
+    N = scale = None
+    width = lifted_width(C, Ns) if Ns >= 2 else C
+    if pre != NM_NORM_NONE:
+        N = X.new_empty((Mtok, width), dtype=_TORCH[ndt])
+        if ndt not in (NM_BF16, NM_F32):
+            scale = X.new_empty(Mtok, dtype=torch.float32)
+    stream, back = _enter(X)
+    try:
+        st = raw.nm_block_norm(X.data_ptr(), _DT[X.dtype], Mtok, C, ldx, res_scale, _ptr(Y), y[2] if y else C, _ptr(gate), ldg,
+                               gate_rows, post, _ptr(w_post), _ptr(b_post), pre, _ptr(w_pre), _ptr(b_pre), wdt, eps, _ptr(Z),
+                               ldz, _ptr(N), ndt, Ns, width, _ptr(scale), stream)
+    finally:
+        _leave(back)
+    if st:
+        _check(st)
+    return Z, N, scale
+
+
+class BlockNormGrads(NamedTuple):
+    """Gradients of nm_block_norm; what is not wanted, or not there, is None."""
+    dX: torch.Tensor | None
+    dY: torch.Tensor | None
+    dw_pre: torch.Tensor | None
+    db_pre: torch.Tensor | None
+    dw_post: torch.Tensor | None
+    db_post: torch.Tensor | None
+    dgate: torch.Tensor | None
+
+
+def nm_block_norm_backward(Z: torch.Tensor, dZ: torch.Tensor | None = None, dN: torch.Tensor | None = None,
+                           Y: torch.Tensor | None = None, gate: torch.Tensor | None = None, gate_rows: int = 0,
+                           res_scale: float = 1.0, post: int = NM_NORM_NONE, w_post: torch.Tensor | None = None,
+                           b_post: torch.Tensor | None = None, pre: int = NM_NORM_RMS, w_pre: torch.Tensor | None = None,
+                           b_pre: torch.Tensor | None = None, eps: float = 1e-6, want_dx: bool = True, want_dy: bool = True,
+                           want_params: bool = True, out_dx: torch.Tensor | None = None,
+                           ws: torch.Tensor | None = None) -> BlockNormGrads:
+    """Gradients of nm_block_norm from its stored Z: of X and Y in their types, and with want_params of each weight that
+    is given (a LAYER norm with a weight has a bias gradient too), in f32.  out_dx may be dZ itself."""
+    x, dev = _mat(Z), Z.device
+    if not (x and Z.dtype in _FLOATS):
+        _refuse("Z must be a row-major bf16 or f32 matrix", Z=Z)
+    Mtok, C, ldz = x
+    ld = {}
+    for name, t, types in (("dZ", dZ, (Z.dtype,)), ("dN", dN, _FLOATS), ("Y", Y, (torch.bfloat16,)), ("out_dx", out_dx, (Z.dtype,))):
+        m = None if t is None else _mat(t)
+        if t is not None and not (m and m[:2] == (Mtok, C) and t.dtype in types and t.device == dev):
+            _refuse(f"{name} must be row-major, of Z's shape, in {types}", Z=Z, **{name: t})
+        ld[name] = m[2] if m else C
+    if dN is None and pre != NM_NORM_NONE and want_params and w_pre is not None:
+        _refuse("dN is needed for norm_pre's gradients", w_pre=w_pre)
+    wdt, ldg = _norm_side(Z, C, gate, gate_rows, Mtok, (w_post, b_post, w_pre, b_pre))
+    dX = (Z.new_empty((Mtok, C)) if out_dx is None else out_dx) if want_dx else None
+    dY = Y.new_empty((Mtok, C)) if want_dy and Y is not None else None
+    gates = (Mtok + gate_rows - 1) // gate_rows if gate_rows > 0 and Mtok > 0 else 1
+    wanted = [w_pre is not None, b_pre is not None or (pre == NM_NORM_LAYER and w_pre is not None), w_post is not None,
+              b_post is not None or (post == NM_NORM_LAYER and w_post is not None)]
+    sums = [Z.new_empty(C, dtype=torch.float32) if want_params and w else None for w in wanted]
+    sums.append(Z.new_empty((gates, C), dtype=torch.float32) if want_params and gate is not None else None)
+    if any(s is not None for s in sums):
+        ws = _need(raw.nm_block_norm_backward_workspace(Mtok, C, gate_rows), ws, Z)
+    stream, back = _enter(Z)
+    try:
+        st = raw.nm_block_norm_backward(Z.data_ptr(), _DT[Z.dtype], Mtok, C, ldz, _ptr(dZ), ld["dZ"], _ptr(dN),
+                                        NM_BF16 if dN is None else _DT[dN.dtype], ld["dN"], res_scale, _ptr(Y), ld["Y"], _ptr(gate),
+                                        ldg, gate_rows, post, _ptr(w_post), _ptr(b_post), pre, _ptr(w_pre), wdt, eps, _ptr(dX),
+                                        C if out_dx is None else ld["out_dx"], _ptr(dY), C, *[_ptr(s) for s in sums], _ptr(ws),
+                                        0 if ws is None else ws.nbytes, stream)
+    finally:
+        _leave(back)
+    if st:
+        _check(st)
+    return BlockNormGrads(dX, dY, *sums)

@@ -12,6 +12,7 @@ bool group_ok(int g) { return g == 64 || g == 128 || g == 256; }
 int64_t lifted(int64_t K, int Ns) { return Ns ? K / (2 * Ns) * 4 * (Ns - 1) : K; }
 
 constexpr int64_t kMost = (int64_t)1 << 24;   // tokens, columns, rows of one call
+constexpr int64_t kNormMost = 32768;           // columns of a norm
 constexpr int64_t kMoeMostTokens = 64;
 constexpr int kMoeMostExperts = 512, kMoeMostTopk = 16;
 
@@ -206,6 +207,140 @@ nm_status nm_moe(const void* X, int64_t Mtok, int64_t K, int64_t ldx, const void
     m.sel = sel;
     m.wts = wts;
     return launch_moe(m, ws, (hipStream_t)stream);
+}
+
+// what both directions of the norms check: kinds, types, the side inputs
+static nm_status norm_check(const char* fn, int64_t Mtok, int64_t C, nm_dtype xdt, nm_dtype wdt, const void* Y,
+                            const void* gate, int64_t ldg, int64_t gate_rows, nm_norm post, const void* w_post,
+                            const void* b_post, nm_norm pre, const void* w_pre, const void* b_pre, float eps) {
+    NM_REQ(Mtok >= 0 && C >= 0, NM_ERR_SHAPE, "%s: negative size", fn);
+    NM_REQ(Mtok <= kMost && C <= kNormMost, NM_ERR_SHAPE, "%s: up to 2^24 tokens of 32768 columns", fn);
+    NM_REQ(C >= 1 || Mtok == 0, NM_ERR_SHAPE, "%s: C == 0", fn);
+    NM_REQ(xdt == NM_BF16 || xdt == NM_F32, NM_ERR_DTYPE, "%s: the residual stream must be bf16 or f32", fn);
+    NM_REQ(wdt == NM_BF16 || wdt == NM_F32, NM_ERR_DTYPE, "%s: weights and gate must be bf16 or f32", fn);
+    for (nm_norm k : {post, pre})
+        NM_REQ(k == NM_NORM_NONE || k == NM_NORM_RMS || k == NM_NORM_LAYER, NM_ERR_SHAPE, "%s: unknown norm", fn);
+    NM_REQ(post != NM_NORM_NONE || (!w_post && !b_post), NM_ERR_SHAPE, "%s: w_post and b_post belong to a norm", fn);
+    NM_REQ(pre != NM_NORM_NONE || (!w_pre && !b_pre), NM_ERR_SHAPE, "%s: w_pre and b_pre belong to a norm", fn);
+    NM_REQ(Mtok == 0 || Y || (!gate && post == NM_NORM_NONE), NM_ERR_NULL, "%s: a gate and norm_post need Y", fn);
+    NM_REQ(gate_rows >= 0, NM_ERR_SHAPE, "%s: negative gate_rows", fn);
+    NM_REQ(!gate || ldg >= C, NM_ERR_SHAPE, "%s: ldg < C", fn);
+    NM_REQ(eps >= 0.0f, NM_ERR_SHAPE, "%s: eps must not be negative", fn);
+    const int64_t ws = esize(wdt);
+    for (const void* p : {gate, w_post, b_post, w_pre, b_pre})
+        NM_REQ(aligned_to(p, ws), NM_ERR_ALIGN, "%s: a weight is not element-aligned", fn);
+    return NM_OK;
+}
+
+static int64_t gate_count(int64_t Mtok, int64_t gate_rows) {
+    return gate_rows > 0 && Mtok > 0 ? ceil_div(Mtok, gate_rows) : 1;
+}
+
+nm_status nm_block_norm(const void* X, nm_dtype xdt, int64_t Mtok, int64_t C, int64_t ldx, float res_scale,
+                        const void* Y, int64_t ldyb, const void* gate, int64_t ldg, int64_t gate_rows, nm_norm post,
+                        const void* w_post, const void* b_post, nm_norm pre, const void* w_pre, const void* b_pre,
+                        nm_dtype wdt, float eps, void* Z, int64_t ldz, void* Nout, nm_dtype ndt, int Ns, int64_t ldn,
+                        float* n_scale, nm_stream_t stream) {
+    const char* fn = "nm_block_norm";
+    const nm_status st = norm_check(fn, Mtok, C, xdt, wdt, Y, gate, ldg, gate_rows, post, w_post, b_post, pre, w_pre, b_pre, eps);
+    if (st != NM_OK) return st;
+    const bool code = ndt == NM_I8 || ndt == NM_FP8;
+    NM_REQ(ndt == NM_BF16 || ndt == NM_F32 || code, NM_ERR_DTYPE, "%s: N must be bf16, f32, int8 or FP8", fn);
+    NM_REQ(Ns == 0 || (code && Ns >= 3 && Ns <= 8), NM_ERR_PATTERN, "%s: Ns is 0, or 3 to 8 for codes (got %d)", fn, Ns);
+    if (Mtok == 0) return NM_OK;
+    NM_REQ(X, NM_ERR_NULL, "%s: X is NULL", fn);
+    NM_REQ(!Nout == (pre == NM_NORM_NONE), NM_ERR_NULL, "%s: N is given exactly with a norm_pre", fn);
+    NM_REQ(!Nout || !code || n_scale, NM_ERR_NULL, "%s: codes need n_scale", fn);
+    const int64_t xs = esize(xdt), ns = esize(ndt), width = lifted(C, Ns);
+    NM_REQ(!code || (C % 8 == 0 && (Ns == 0 || C % (2 * Ns) == 0)), NM_ERR_SHAPE,
+           "%s: codes need C a multiple of 8 and of 2N", fn);
+    NM_REQ(ldx >= C && (!Y || ldyb >= C) && (!Z || ldz >= C) && (!Nout || ldn >= width), NM_ERR_SHAPE,
+           "%s: leading dimension too small", fn);
+    NM_REQ(aligned_to(X, xs) && aligned_to(Y, 2) && aligned_to(Z, xs) && aligned_to(Nout, code ? 4 : ns) &&
+               (!code || ldn % 4 == 0) && aligned_to(n_scale, 4),
+           NM_ERR_ALIGN, "%s: an argument is not aligned (elements; codes: rows of 4 bytes)", fn);
+    // codes are made of whole vectors of 8 columns
+    if (code && Nout)
+        NM_REQ(aligned16(X) && ldx * xs % 16 == 0 && (!Y || (aligned16(Y) && ldyb % 8 == 0)) && (!Z || (aligned16(Z) && ldz * xs % 16 == 0)) &&
+                   (!gate || (aligned16(gate) && ldg * esize(wdt) % 16 == 0)) && aligned16(w_post) && aligned16(b_post) &&
+                   aligned16(w_pre) && aligned16(b_pre),
+               NM_ERR_ALIGN, "%s: codes need 16-byte aligned rows of every other argument", fn);
+    const int64_t gates = gate_count(Mtok, gate_rows), wsz = esize(wdt);
+    const Range rx = span(X, Mtok, C, ldx, xs);
+    const Range in[] = {span(Y, Mtok, C, ldyb, 2),      span(gate, gates, C, ldg, wsz), span(w_post, 1, C, C, wsz),
+                        span(b_post, 1, C, C, wsz), span(w_pre, 1, C, C, wsz),      span(b_pre, 1, C, C, wsz)};
+    const Range out[] = {span(Z, Mtok, C, ldz, xs), span(Nout, Mtok, width, ldn, ns),
+                         code && Nout ? span(n_scale, 1, Mtok, Mtok, 4) : Range{0, 0}};
+    const bool in_place = Z == X && ldz == ldx;
+    for (int i = 0; i < 3; ++i) {
+        NM_REQ((i == 0 && in_place) || !overlap(out[i], rx), NM_ERR_ALIAS, "%s: an output overlaps X (Z may be X itself)", fn);
+        for (const Range& r : in) NM_REQ(!overlap(out[i], r), NM_ERR_ALIAS, "%s: an output overlaps an input", fn);
+        for (int j = 0; j < i; ++j) NM_REQ(!overlap(out[i], out[j]), NM_ERR_ALIAS, "%s: outputs overlap", fn);
+    }
+    if (!Z && !Nout) return NM_OK;
+    const NormIn n{X,    xdt,    Mtok,   C,   ldx,   res_scale, Y,   ldyb, gate, ldg, gate_rows, post,    w_post,
+                   b_post, pre, w_pre, b_pre, wdt, eps, Z, ldz, Nout, ndt, Ns, ldn, n_scale};
+    return launch_block_norm(n, (hipStream_t)stream);
+}
+
+size_t nm_block_norm_backward_workspace(int64_t Mtok, int64_t C, int64_t gate_rows) {
+    if (Mtok <= 0 || Mtok > kMost || C <= 0 || C > kNormMost || gate_rows < 0) return 0;
+    return block_norm_bwd_ws(Mtok, C, gate_rows);
+}
+
+nm_status nm_block_norm_backward(const void* Z, nm_dtype xdt, int64_t Mtok, int64_t C, int64_t ldz, const void* dZ,
+                                 int64_t lddz, const void* dN, nm_dtype dndt, int64_t lddn, float res_scale,
+                                 const void* Y, int64_t ldyb, const void* gate, int64_t ldg, int64_t gate_rows, nm_norm post,
+                                 const void* w_post, const void* b_post, nm_norm pre, const void* w_pre, nm_dtype wdt, float eps,
+                                 void* dX, int64_t lddx, void* dY, int64_t lddy, float* dw_pre, float* db_pre, float* dw_post,
+                                 float* db_post, float* dgate, void* ws, size_t ws_bytes, nm_stream_t stream) {
+    const char* fn = "nm_block_norm_backward";
+    const nm_status st = norm_check(fn, Mtok, C, xdt, wdt, Y, gate, ldg, gate_rows, post, w_post, b_post, pre, w_pre, nullptr, eps);
+    if (st != NM_OK) return st;
+    NM_REQ(dndt == NM_BF16 || dndt == NM_F32, NM_ERR_DTYPE, "%s: dN must be bf16 or f32", fn);
+    const bool some = Mtok > 0;
+    NM_REQ(pre != NM_NORM_NONE || (!dN && !dw_pre && !db_pre), NM_ERR_NULL, "%s: dN, dw_pre and db_pre belong to a norm_pre", fn);
+    NM_REQ(!some || dN || (!dw_pre && !db_pre), NM_ERR_NULL, "%s: dw_pre and db_pre need dN", fn);
+    NM_REQ(post != NM_NORM_NONE || (!dw_post && !db_post), NM_ERR_NULL, "%s: dw_post and db_post belong to a norm_post", fn);
+    NM_REQ(!some || Y || !dY, NM_ERR_NULL, "%s: dY needs Y", fn);
+    NM_REQ(!some || gate || !dgate, NM_ERR_NULL, "%s: dgate needs a gate", fn);
+    if (C == 0) return NM_OK;
+    float* sums[5] = {dw_pre, db_pre, dw_post, db_post, dgate};
+    const int64_t xs = esize(xdt), ns = esize(dndt), wsz = esize(wdt), gates = gate_count(Mtok, gate_rows);
+    bool any = false;
+    for (float* p : sums) {
+        any |= p != nullptr;
+        NM_REQ(aligned_to(p, 4), NM_ERR_ALIGN, "%s: a parameter gradient is not element-aligned", fn);
+    }
+    if (some) {
+        NM_REQ(Z || !dN, NM_ERR_NULL, "%s: dN needs Z", fn);
+        NM_REQ((!Z || ldz >= C) && (!dZ || lddz >= C) && (!dN || lddn >= C) && (!Y || ldyb >= C) && (!dX || lddx >= C) &&
+                   (!dY || lddy >= C),
+               NM_ERR_SHAPE, "%s: leading dimension too small", fn);
+        NM_REQ(aligned_to(Z, xs) && aligned_to(dZ, xs) && aligned_to(dN, ns) && aligned_to(Y, 2) && aligned_to(dX, xs) &&
+                   aligned_to(dY, 2),
+               NM_ERR_ALIGN, "%s: an argument is not element-aligned", fn);
+    }
+    const size_t need = any && some ? block_norm_bwd_ws(Mtok, C, gate_rows) : 0;
+    NM_REQ(need == 0 || (ws && ws_bytes >= need), NM_ERR_WORKSPACE, "%s: workspace of %zu bytes needed", fn, need);
+    NM_REQ(need == 0 || aligned16(ws), NM_ERR_ALIGN, "%s: ws must be 16-byte aligned", fn);
+    const Range rdz = span(dZ, Mtok, C, lddz, xs);
+    const Range in[] = {span(Z, Mtok, C, ldz, xs),   span(dN, Mtok, C, lddn, ns),  span(Y, Mtok, C, ldyb, 2),  span(gate, gates, C, ldg, wsz),
+                        span(w_post, 1, C, C, wsz), span(b_post, 1, C, C, wsz), span(w_pre, 1, C, C, wsz)};
+    Range out[8] = {span(dX, Mtok, C, lddx, xs), span(dY, Mtok, C, lddy, 2)};
+    for (int i = 0; i < 5; ++i) out[2 + i] = span(sums[i], i == 4 ? gates : 1, C, C, 4);
+    if (need) out[7] = Range{(uintptr_t)ws, (uintptr_t)ws + need};
+    const bool in_place = dX == dZ && lddx == lddz;
+    for (int i = 0; i < 8; ++i) {
+        NM_REQ((i == 0 && in_place) || !overlap(out[i], rdz), NM_ERR_ALIAS, "%s: an output or ws overlaps dZ (dX may be dZ itself)", fn);
+        for (const Range& r : in) NM_REQ(!overlap(out[i], r), NM_ERR_ALIAS, "%s: an output or ws overlaps an input", fn);
+        for (int j = 0; j < i; ++j) NM_REQ(!overlap(out[i], out[j]), NM_ERR_ALIAS, "%s: outputs or ws overlap", fn);
+    }
+    if (!any && (!some || (!dX && !dY))) return NM_OK;
+    NormBwdIn n{Z,   xdt, Mtok, C,   ldz, dZ,   lddz,   dN,     dndt, lddn,  res_scale, Y,   ldyb, gate, ldg, gate_rows,
+                post, w_post, b_post, pre, w_pre, wdt, eps, dX, lddx, dY, lddy, {}};
+    for (int i = 0; i < 5; ++i) n.sums[i] = sums[i];
+    return launch_block_norm_bwd(n, ws, (hipStream_t)stream);
 }
 
 }  // extern "C"

@@ -406,6 +406,59 @@ struct MoeIn {
 };
 size_t moe_ws(int64_t Mtok, int64_t K, int64_t F, int E, int topk);
 nm_status launch_moe(const MoeIn& in, void* ws, hipStream_t s);
+// norms around a block
+struct NormIn {
+    const void* X;
+    nm_dtype xdt;
+    int64_t Mtok, C, ldx;
+    float res_scale;
+    const void* Y;
+    int64_t ldyb;
+    const void* gate;
+    int64_t ldg, gate_rows;
+    nm_norm post;
+    const void *w_post, *b_post;
+    nm_norm pre;
+    const void *w_pre, *b_pre;
+    nm_dtype wdt;
+    float eps;
+    void* Z;
+    int64_t ldz;
+    void* N;
+    nm_dtype ndt;
+    int Ns;
+    int64_t ldn;
+    float* n_scale;
+};
+nm_status launch_block_norm(const NormIn& in, hipStream_t s);
+struct NormBwdIn {
+    const void* Z;
+    nm_dtype xdt;
+    int64_t Mtok, C, ldz;
+    const void* dZ;
+    int64_t lddz;
+    const void* dN;
+    nm_dtype dndt;
+    int64_t lddn;
+    float res_scale;
+    const void* Y;
+    int64_t ldyb;
+    const void* gate;
+    int64_t ldg, gate_rows;
+    nm_norm post;
+    const void *w_post, *b_post;
+    nm_norm pre;
+    const void* w_pre;
+    nm_dtype wdt;
+    float eps;
+    void* dX;
+    int64_t lddx;
+    void* dY;
+    int64_t lddy;
+    float* sums[5];   // dw_pre, db_pre, dw_post, db_post, dgate; null: not wanted
+};
+size_t block_norm_bwd_ws(int64_t Mtok, int64_t C, int64_t gate_rows);
+nm_status launch_block_norm_bwd(const NormBwdIn& in, void* ws, hipStream_t s);
 // Hutchinson
 size_t hutch_ws(int64_t n, int64_t K, int64_t R, int probes);
 size_t hutch_score_ws(int64_t n, int64_t K, int64_t R, int probes);

@@ -153,6 +153,79 @@ def test_moe_workspace_of_refused_sizes():
         assert ws(*bad) == 0, bad
 
 
+# ------------------------------------------------------------------ norms around a block
+Q = [P((40 + i) << 32) for i in range(14)]
+
+
+def _norm(**kw):
+    a = dict(X=X, xdt=1, M=4, C=64, ldx=64, res=1.0, Y=Y, ldy=64, gate=Q[0], ldg=64, rows=2, post=1, wp=Q[1], bp=Q[2], pre=2, wn=Q[3],
+             bn=Q[4], wdt=1, eps=1e-6, Z=Q[5], ldz=64, N=Q[6], ndt=1, Ns=0, ldn=96, s=Q[7])
+    a.update(kw)
+    return _name(nm.raw.nm_block_norm(*a.values(), None))
+
+
+def test_norm_refuses():
+    assert _norm(M=-1) == "NM_ERR_SHAPE" and _norm(C=-1) == "NM_ERR_SHAPE" and _norm(C=0) == "NM_ERR_SHAPE"
+    assert _norm(C=32769, ldx=1 << 17) == "NM_ERR_SHAPE" and _norm(M=1 << 25) == "NM_ERR_SHAPE"
+    assert _norm(xdt=2) == "NM_ERR_DTYPE" and _norm(wdt=3) == "NM_ERR_DTYPE" and _norm(ndt=3) == "NM_ERR_DTYPE" and _norm(ndt=5) == "NM_ERR_DTYPE"
+    assert _norm(post=3) == "NM_ERR_SHAPE" and _norm(pre=-1) == "NM_ERR_SHAPE" and _norm(post=0) == "NM_ERR_SHAPE"
+    assert _norm(post=0, wp=None) == "NM_ERR_SHAPE" and _norm(pre=0) == "NM_ERR_SHAPE"
+    assert _norm(pre=0, wn=None, bn=None) == "NM_ERR_NULL" and _norm(N=None) == "NM_ERR_NULL"
+    assert _norm(Y=None) == "NM_ERR_NULL" and _norm(X=None) == "NM_ERR_NULL" and _norm(ndt=2, s=None) == "NM_ERR_NULL"
+    assert _norm(rows=-1) == "NM_ERR_SHAPE" and _norm(eps=-1.0) == "NM_ERR_SHAPE" and _norm(eps=float("nan")) == "NM_ERR_SHAPE"
+    assert _norm(Ns=4) == "NM_ERR_PATTERN" and _norm(Ns=2, ndt=4) == "NM_ERR_PATTERN" and _norm(Ns=9, ndt=4) == "NM_ERR_PATTERN"
+    assert _norm(Ns=3, ndt=4) == "NM_ERR_SHAPE" and _norm(C=60, ndt=2) == "NM_ERR_SHAPE"
+    for k in ("ldx", "ldy", "ldg", "ldz", "ldn"):
+        assert _norm(**{k: 63}) == "NM_ERR_SHAPE", k
+    assert _norm(Ns=4, ndt=4, ldn=92) == "NM_ERR_SHAPE"
+    for k, p in (("X", X), ("Y", Y), ("gate", Q[0]), ("wp", Q[1]), ("bp", Q[2]), ("wn", Q[3]), ("bn", Q[4]), ("Z", Q[5]), ("N", Q[6])):
+        assert _norm(**{k: P(p.value + 1)}) == "NM_ERR_ALIGN", k
+        if k != "N":
+            assert _norm(ndt=4, **{k: P(p.value + 8)}) == "NM_ERR_ALIGN", k
+    assert _norm(ndt=4, N=P(Q[6].value + 2)) == "NM_ERR_ALIGN" and _norm(ndt=4, ldn=98) == "NM_ERR_ALIGN" and _norm(ndt=4, ldx=68) == "NM_ERR_ALIGN"
+    for k in ("Z", "N"):
+        for p in (Y, *Q[:5]):
+            assert _norm(**{k: p}) == "NM_ERR_ALIAS", k
+    assert _norm(N=X) == "NM_ERR_ALIAS" and _norm(Z=Q[6]) == "NM_ERR_ALIAS" and _norm(Z=X, ldz=72) == "NM_ERR_ALIAS"
+    assert _norm(Z=P(X.value + 128)) == "NM_ERR_ALIAS" and _norm(ndt=2, s=Q[6]) == "NM_ERR_ALIAS"
+    assert _norm(M=0, X=None) == "NM_OK"
+
+
+def _norm_bwd(**kw):
+    a = dict(Z=X, xdt=1, M=4, C=64, ldz=64, dZ=C, lddz=64, dN=I, dndt=1, lddn=64, res=1.0, Y=Y, ldy=64, gate=Q[0], ldg=64, rows=2, post=1,
+             wp=Q[1], bp=Q[2], pre=2, wn=Q[3], wdt=1, eps=1e-6, dX=Q[4], lddx=64, dY=Q[5], lddy=64, dwn=Q[6], dbn=Q[7], dwp=Q[8],
+             dbp=Q[9], dgate=Q[10], ws=Q[11], n=1 << 31)
+    a.update(kw)
+    return _name(nm.raw.nm_block_norm_backward(*a.values(), None))
+
+
+def test_norm_backward_refuses():
+    f = _norm_bwd
+    assert f(M=-1) == "NM_ERR_SHAPE" and f(C=0) == "NM_ERR_SHAPE" and f(C=32769) == "NM_ERR_SHAPE" and f(pre=4) == "NM_ERR_SHAPE"
+    assert f(xdt=2) == "NM_ERR_DTYPE" and f(wdt=2) == "NM_ERR_DTYPE" and f(dndt=4) == "NM_ERR_DTYPE"
+    assert f(pre=0, wn=None) == "NM_ERR_NULL" and f(dN=None) == "NM_ERR_NULL" and f(Z=None) == "NM_ERR_NULL"
+    assert f(post=0, wp=None, bp=None) == "NM_ERR_NULL" and f(Y=None) == "NM_ERR_NULL" and f(gate=None) == "NM_ERR_NULL"
+    assert f(Y=None, gate=None, post=0, wp=None, bp=None, dwp=None, dbp=None, dgate=None) == "NM_ERR_NULL"      # dY is left
+    for k in ("ldz", "lddz", "lddn", "ldy", "ldg", "lddx", "lddy"):
+        assert f(**{k: 63}) == "NM_ERR_SHAPE", k
+    for k in ("Z", "dZ", "dN", "Y", "gate", "wp", "dX", "dY", "dwn", "dgate"):
+        v = dict(Z=X, dZ=C, dN=I, Y=Y, gate=Q[0], wp=Q[1], dX=Q[4], dY=Q[5], dwn=Q[6], dgate=Q[10])[k]
+        assert f(**{k: P(v.value + 1)}) == "NM_ERR_ALIGN", k
+    assert f(ws=P(Q[11].value + 8)) == "NM_ERR_ALIGN" and f(ws=None) == "NM_ERR_WORKSPACE" and f(n=8) == "NM_ERR_WORKSPACE"
+    for k in ("dX", "dY", "dwn", "dbn", "dwp", "dbp", "dgate", "ws"):
+        for p in (X, I, Y, Q[0], Q[1], Q[3]):
+            assert f(**{k: p}) == "NM_ERR_ALIAS", k
+        if k != "dX":
+            assert f(**{k: C}) == "NM_ERR_ALIAS" and f(**{k: Q[4]}) == "NM_ERR_ALIAS", k
+    assert f(dX=C, lddx=72) == "NM_ERR_ALIAS"
+
+
+def test_norm_workspace_of_refused_sizes():
+    ws = nm.raw.nm_block_norm_backward_workspace
+    assert ws(4, 64, 0) > 0 and ws(4096, 4096, 1) > 0
+    assert all(ws(*a) == 0 for a in ((0, 64, 0), (-1, 64, 0), (4, 0, 0), (4, 32769, 0), (1 << 25, 64, 0), (4, 64, -1)))
+
+
 # ------------------------------------------------------------------ the current device
 @pytest.fixture
 def seen(monkeypatch):
@@ -194,6 +267,8 @@ DO = {
     "nm_spmm_w4": lambda: nm.nm_spmm_w4(_bf16(2, 64), _CODES, _IDX, _SC),
     "nm_spmm_glu_w4": lambda: nm.nm_spmm_glu_w4(_bf16(2, 64), _CODES, _IDX, _SC, _CODES, _IDX, _SC),
     "nm_moe": lambda: nm.nm_moe(_layer(), _bf16(2, 64), 2),
+    "nm_block_norm": lambda: nm.nm_block_norm(_bf16(2, 64)),
+    "nm_block_norm_backward": lambda: nm.nm_block_norm_backward(_bf16(2, 64), dN=_bf16(2, 64), w_pre=_bf16(64)),
 }
 CALLS = sorted(DO)
 
