@@ -1,8 +1,10 @@
 // The norms before and after a block with its gate and residual scale, and their gradients:
 //   Z = a X + gate . norm_post(Y),  N = norm_pre(Z)
 // One pass over the tokens each way, bound by memory.  A block of threads holds a token's row in
-// registers (V consecutive columns a thread and vector, NV vectors), so that the statistics, Z, the second
-// norm and its codes are made without reading anything again.
+// registers (8 consecutive columns a thread and vector, NV vectors), so that the statistics, Z, the
+// second norm and its codes are made without reading anything again.
+#include <type_traits>
+
 #include "nm_codes.h"
 
 namespace nm {
@@ -33,59 +35,83 @@ struct NormArgs {
     float* n_scale;
 };
 
-// V columns from column c of a row, as f32
-template <int V>
-__device__ __forceinline__ void norm_load(float (&v)[V], const void* row, bool f32, int c) {
-    if constexpr (V == 8) {
+// 8 columns from column c of a row of C, as f32; zeros past its end.  Rows need only the alignment of
+// their elements (the hardware loads 16 bytes from anywhere); the row's last, part-filled vector goes
+// element by element.
+struct __attribute__((packed, aligned(2))) norm_u4 {
+    uint32_t x, y, z, w;
+};
+struct __attribute__((packed, aligned(4))) norm_f4 {
+    float x, y, z, w;
+};
+__device__ __forceinline__ void norm_widen(float (&v)[8], const norm_u4& a) {
+    const uint32_t w[4] = {a.x, a.y, a.z, a.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        v[2 * i] = __uint_as_float(w[i] << 16);
+        v[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+    }
+}
+__device__ __forceinline__ void norm_load(float (&v)[8], const void* row, bool f32, int c, int C) {
+    if (c + 8 <= C) {
         if (f32) {
-            const float4* p = (const float4*)((const float*)row + c);
-            const float4 a = p[0], b = p[1];
+            const norm_f4* p = (const norm_f4*)((const float*)row + c);
+            const norm_f4 a = p[0], b = p[1];
             v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w, v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
         } else {
-            const uint4 a = *(const uint4*)((const uint16_t*)row + c);
-            const uint32_t w[4] = {a.x, a.y, a.z, a.w};
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                v[2 * i] = __uint_as_float(w[i] << 16);
-                v[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
-            }
+            norm_widen(v, *(const norm_u4*)((const uint16_t*)row + c));
         }
     } else {
 #pragma unroll
-        for (int i = 0; i < V; ++i) v[i] = f32 ? ((const float*)row)[c + i] : bf16_bits_to_f32(((const uint16_t*)row)[c + i]);
+        for (int i = 0; i < 8; ++i)
+            v[i] = c + i >= C ? 0.0f : f32 ? ((const float*)row)[c + i] : bf16_bits_to_f32(((const uint16_t*)row)[c + i]);
     }
 }
-
-template <int V>
-__device__ __forceinline__ void norm_store(const float (&v)[V], void* row, bool f32, int c) {
-    if constexpr (V == 8) {
+__device__ __forceinline__ void norm_store(const float (&v)[8], void* row, bool f32, int c, int C) {
+    if (c + 8 <= C) {
         if (f32) {
-            float4* p = (float4*)((float*)row + c);
-            p[0] = make_float4(v[0], v[1], v[2], v[3]);
-            p[1] = make_float4(v[4], v[5], v[6], v[7]);
+            norm_f4* p = (norm_f4*)((float*)row + c);
+            p[0] = norm_f4{v[0], v[1], v[2], v[3]};
+            p[1] = norm_f4{v[4], v[5], v[6], v[7]};
         } else {
-            *(uint4*)((uint16_t*)row + c) = make_uint4(f32_to_bf16_pair(v[0], v[1]), f32_to_bf16_pair(v[2], v[3]),
-                                                       f32_to_bf16_pair(v[4], v[5]), f32_to_bf16_pair(v[6], v[7]));
+            *(norm_u4*)((uint16_t*)row + c) = norm_u4{f32_to_bf16_pair(v[0], v[1]), f32_to_bf16_pair(v[2], v[3]),
+                                                      f32_to_bf16_pair(v[4], v[5]), f32_to_bf16_pair(v[6], v[7])};
         }
     } else {
 #pragma unroll
-        for (int i = 0; i < V; ++i) {
-            if (f32) ((float*)row)[c + i] = v[i];
-            else ((uint16_t*)row)[c + i] = (uint16_t)f32_to_bf16_bits(v[i]);
-        }
+        for (int i = 0; i < 8; ++i)
+            if (c + i < C) {
+                if (f32) ((float*)row)[c + i] = v[i];
+                else ((uint16_t*)row)[c + i] = (uint16_t)f32_to_bf16_bits(v[i]);
+            }
     }
 }
 
-// Sums over the block, the same in every thread: lanes by a butterfly, waves in order.  `turn` picks
-// one of two buffers, so that one barrier a call is enough.
+// A wave's sum in every lane: rotations within 16 lanes, then the halves swapped.  Every lane adds
+// the same pairs, so that all hold the same bits.
+__device__ __forceinline__ float norm_wave_sum(float v) {
+    auto turn = [&](auto ctrl) __attribute__((always_inline)) {
+        v += __builtin_bit_cast(float, __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, v), decltype(ctrl)::value, 0xf, 0xf, false));
+    };
+    turn(std::integral_constant<int, 0x128>{});   // row_ror:8, 4, 2, 1
+    turn(std::integral_constant<int, 0x124>{});
+    turn(std::integral_constant<int, 0x122>{});
+    turn(std::integral_constant<int, 0x121>{});
+    uint32_t u = __float_as_uint(v);
+    auto r = __builtin_amdgcn_permlane16_swap(u, u, false, false);
+    u = __float_as_uint(__uint_as_float(r[0]) + __uint_as_float(r[1]));
+    r = __builtin_amdgcn_permlane32_swap(u, u, false, false);
+    return __uint_as_float(r[0]) + __uint_as_float(r[1]);
+}
+
+// Sums over the block, the same in every thread: waves in order.  `turn` picks one of two buffers, so
+// that one barrier a call is enough.
 struct NormSum {
     float (*buf)[16][2];   // [2][waves][2]
     int turn, waves, lane, wave;
     __device__ __forceinline__ void two(float& a, float& b) {
-        for (int off = 32; off; off >>= 1) {
-            a += __shfl_xor(a, off);
-            b += __shfl_xor(b, off);
-        }
+        a = norm_wave_sum(a);
+        b = norm_wave_sum(b);
         if (waves == 1) return;
         turn ^= 1;
         if (lane == 0) {
@@ -100,8 +126,13 @@ struct NormSum {
         }
     }
     __device__ __forceinline__ float one(float a) {
-        float b = 0.0f;
-        two(a, b);
+        a = norm_wave_sum(a);
+        if (waves == 1) return a;
+        turn ^= 1;
+        if (lane == 0) buf[turn][wave][0] = a;
+        __syncthreads();
+        a = 0.0f;
+        for (int w = 0; w < waves; ++w) a += buf[turn][w][0];
         return a;
     }
     __device__ __forceinline__ float most(float a) {
@@ -116,8 +147,8 @@ struct NormSum {
 };
 
 // norm of the row v in place: (v - mean) r w + b
-template <int V, int NV>
-__device__ __forceinline__ void norm_row(float (&v)[NV][V], const NormSide& n, bool w32, float eps, int C, int t, int nt,
+template <int NV>
+__device__ __forceinline__ void norm_row(float (&v)[NV][8], const NormSide& n, bool w32, float eps, int C, int t, int nt,
                                          NormSum& sum) {
     if (n.kind == NM_NORM_NONE) return;
     const float inv = 1.0f / (float)C;
@@ -126,30 +157,28 @@ __device__ __forceinline__ void norm_row(float (&v)[NV][V], const NormSide& n, b
 #pragma unroll
         for (int k = 0; k < NV; ++k)
 #pragma unroll
-            for (int i = 0; i < V; ++i) s += v[k][i];      // columns past the end hold zeros
+            for (int i = 0; i < 8; ++i) s += v[k][i];      // columns past the end hold zeros
         const float mean = sum.one(s) * inv;
 #pragma unroll
         for (int k = 0; k < NV; ++k)
-            if ((k * nt + t) * V < C) {
 #pragma unroll
-                for (int i = 0; i < V; ++i) v[k][i] -= mean;
-            }
+            for (int i = 0; i < 8; ++i) v[k][i] = (k * nt + t) * 8 + i < C ? v[k][i] - mean : 0.0f;
     }
     float q = 0.0f;
 #pragma unroll
     for (int k = 0; k < NV; ++k)
 #pragma unroll
-        for (int i = 0; i < V; ++i) q = __builtin_fmaf(v[k][i], v[k][i], q);
+        for (int i = 0; i < 8; ++i) q = __builtin_fmaf(v[k][i], v[k][i], q);
     const float r = 1.0f / __builtin_sqrtf(__builtin_fmaf(sum.one(q), inv, eps));
 #pragma unroll
     for (int k = 0; k < NV; ++k) {
-        const int c = (k * nt + t) * V;
+        const int c = (k * nt + t) * 8;
         if (c < C) {
-            float w[V], b[V];
-            if (n.w) norm_load<V>(w, n.w, w32, c);
-            if (n.b) norm_load<V>(b, n.b, w32, c);
+            float w[8], b[8];
+            if (n.w) norm_load(w, n.w, w32, c, C);
+            if (n.b) norm_load(b, n.b, w32, c, C);
 #pragma unroll
-            for (int i = 0; i < V; ++i) {
+            for (int i = 0; i < 8; ++i) {
                 v[k][i] *= r;
                 if (n.w) v[k][i] *= w[i];
                 if (n.b) v[k][i] += b[i];
@@ -158,78 +187,78 @@ __device__ __forceinline__ void norm_row(float (&v)[NV][V], const NormSide& n, b
     }
 }
 
-template <int V, int NV, bool X32>
+template <int NV, bool X32>
 __global__ __launch_bounds__(1024) void norm_kernel(NormArgs a) {
     __shared__ float buf[2][16][2];
     extern __shared__ __attribute__((aligned(16))) uint8_t codes[];   // a row's codes, where they are lifted
     const int t = threadIdx.x, nt = blockDim.x, C = a.C;
     NormSum sum{buf, 0, nt / 64, t & 63, t >> 6};
     const int64_t m = blockIdx.x;
-    float z[NV][V];
+    float z[NV][8];
     if (a.Y) {
-        float x[NV][V];
+        float x[NV][8];
 #pragma unroll
         for (int k = 0; k < NV; ++k) {
-            const int c = (k * nt + t) * V;
+            const int c = (k * nt + t) * 8;
             if (c < C) {
-                norm_load<V>(z[k], a.Y + m * a.ldyb, false, c);
-                norm_load<V>(x[k], (const uint8_t*)a.X + m * a.ldx * (X32 ? 4 : 2), X32, c);
+                norm_load(z[k], a.Y + m * a.ldyb, false, c, C);
+                norm_load(x[k], (const uint8_t*)a.X + m * a.ldx * (X32 ? 4 : 2), X32, c, C);
             } else {
 #pragma unroll
-                for (int i = 0; i < V; ++i) z[k][i] = 0.0f;
+                for (int i = 0; i < 8; ++i) z[k][i] = 0.0f;
             }
         }
-        norm_row<V, NV>(z, a.post, a.w32, a.eps, C, t, nt, sum);
+        norm_row<NV>(z, a.post, a.w32, a.eps, C, t, nt, sum);
         const uint8_t* gate = a.gate ? (const uint8_t*)a.gate + m / a.gate_rows * a.ldg * (a.w32 ? 4 : 2) : nullptr;
 #pragma unroll
         for (int k = 0; k < NV; ++k) {
-            const int c = (k * nt + t) * V;
+            const int c = (k * nt + t) * 8;
             if (c < C) {
-                float g[V];
-                if (gate) norm_load<V>(g, gate, a.w32, c);
+                float g[8];
+                if (gate) norm_load(g, gate, a.w32, c, C);
 #pragma unroll
-                for (int i = 0; i < V; ++i) z[k][i] = __builtin_fmaf(a.res, x[k][i], gate ? g[i] * z[k][i] : z[k][i]);
+                for (int i = 0; i < 8; ++i) z[k][i] = __builtin_fmaf(a.res, x[k][i], gate ? g[i] * z[k][i] : z[k][i]);
             }
         }
     } else {
 #pragma unroll
         for (int k = 0; k < NV; ++k) {
-            const int c = (k * nt + t) * V;
+            const int c = (k * nt + t) * 8;
             if (c < C) {
-                norm_load<V>(z[k], (const uint8_t*)a.X + m * a.ldx * (X32 ? 4 : 2), X32, c);
+                norm_load(z[k], (const uint8_t*)a.X + m * a.ldx * (X32 ? 4 : 2), X32, c, C);
 #pragma unroll
-                for (int i = 0; i < V; ++i) z[k][i] *= a.res;
+                for (int i = 0; i < 8; ++i) z[k][i] *= a.res;
             } else {
 #pragma unroll
-                for (int i = 0; i < V; ++i) z[k][i] = 0.0f;
+                for (int i = 0; i < 8; ++i) z[k][i] = 0.0f;
             }
         }
     }
     if (a.Z) {
 #pragma unroll
         for (int k = 0; k < NV; ++k) {
-            const int c = (k * nt + t) * V;
-            if (c < C) norm_store<V>(z[k], (uint8_t*)a.Z + m * a.ldz * (X32 ? 4 : 2), X32, c);
+            const int c = (k * nt + t) * 8;
+            if (c < C) norm_store(z[k], (uint8_t*)a.Z + m * a.ldz * (X32 ? 4 : 2), X32, c, C);
         }
     }
     if (!a.N) return;
-    norm_row<V, NV>(z, a.pre, a.w32, a.eps, C, t, nt, sum);
+    norm_row<NV>(z, a.pre, a.w32, a.eps, C, t, nt, sum);
     if (a.ndt == NM_BF16 || a.ndt == NM_F32) {
         const bool n32 = a.ndt == NM_F32;
 #pragma unroll
         for (int k = 0; k < NV; ++k) {
-            const int c = (k * nt + t) * V;
-            if (c < C) norm_store<V>(z[k], (uint8_t*)a.N + m * a.ldn * (n32 ? 4 : 2), n32, c);
+            const int c = (k * nt + t) * 8;
+            if (c < C) norm_store(z[k], (uint8_t*)a.N + m * a.ldn * (n32 ? 4 : 2), n32, c, C);
         }
         return;
     }
-    if constexpr (V == 8) {
+    {
         float top = 0.0f;
 #pragma unroll
         for (int k = 0; k < NV; ++k)
-            if ((k * nt + t) * V < C) {
+            if ((k * nt + t) * 8 < C) {
 #pragma unroll
-                for (int i = 0; i < V; ++i) top = __builtin_fmaxf(top, __builtin_fabsf(z[k][i]));
+                for (int i = 0; i < 8; ++i) top = __builtin_fmaxf(top, __builtin_fabsf(z[k][i]));
             }
         top = sum.most(top);
         const bool fp8 = a.ndt == NM_FP8;
@@ -240,7 +269,7 @@ __global__ __launch_bounds__(1024) void norm_kernel(NormArgs a) {
         const RowDiv rd = row_div(fast ? s : 1.0f);
 #pragma unroll
         for (int k = 0; k < NV; ++k) {
-            const int c = (k * nt + t) * V;
+            const int c = (k * nt + t) * 8;
             if (c >= C) continue;
             uint32_t q[8];
 #pragma unroll
@@ -298,82 +327,152 @@ struct NormBwdArgs {
     uint16_t* dY;
     int64_t lddy;
     float* sums[5];     // dw_pre, db_pre, dw_post, db_post, dgate; null: not wanted
-    float* part;        // [5][blocks][C]
+    float* part;        // [4][blocks][C]
     int rows, blocks;   // rows of a block, blocks
     int per_gate;       // blocks of a gate row; 0: a block holds whole gate rows and writes dgate itself
 };
 
+// A row's vectors as they were loaded, so that the next row's can be on their way while one is worked on.
+template <bool X32>
+struct NormRaw {
+    norm_u4 z[X32 ? 2 : 1], dz[X32 ? 2 : 1], dn, y;
+};
+template <bool X32>
+__device__ __forceinline__ void norm_raw(float (&v)[8], const norm_u4 (&r)[X32 ? 2 : 1]) {
+    if constexpr (X32) {
+        const uint32_t w[8] = {r[0].x, r[0].y, r[0].z, r[0].w, r[1].x, r[1].y, r[1].z, r[1].w};
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[i] = __uint_as_float(w[i]);
+    } else {
+        norm_widen(v, r[0]);
+    }
+}
+
 // A block walks its rows; a thread keeps its columns, so that the parameter sums stay in its registers
-// and leave once, as one partial per block.
-template <int V, int NV, bool X32>
-__global__ __launch_bounds__(1024) void norm_bwd_kernel(NormBwdArgs a) {
+// and leave once, as one partial per block.  With g the gradient of Z and y' the normalised Y these are
+//   dw_pre = sum dN z',  db_pre = sum dN,  A = sum g y',  B = sum g
+// and, while the gate's row is the same: dgate = w_post A + b_post B, dw_post = gate A, db_post = gate B.
+// L: a mean or a bias somewhere (else db_pre and B are not kept).  MULTI: the block holds several
+// gate rows, writes their dgate and keeps dw_post and db_post in place of A and B.
+template <int NV, int NT, bool X32, bool L, bool MULTI>
+__global__ __launch_bounds__(NT, NV == 1 && !L ? 4 : 1) void norm_bwd_kernel(NormBwdArgs a) {
+    constexpr bool AHEAD = NV == 1;   // rows loaded ahead and weights kept, while registers last
     __shared__ float buf[2][16][2];
     const int t = threadIdx.x, nt = blockDim.x, C = a.C;
     NormSum sum{buf, 0, nt / 64, t & 63, t >> 6};
     int64_t m0, m1;
-    if (a.per_gate) {
+    if (MULTI) {
+        m0 = (int64_t)blockIdx.x * a.rows;
+        m1 = m0 + a.rows;
+    } else {
         const int64_t g = blockIdx.x / a.per_gate, k = blockIdx.x % a.per_gate;
         m0 = g * a.gate_rows + k * a.rows;
         m1 = m0 + a.rows < (g + 1) * a.gate_rows ? m0 + a.rows : (g + 1) * a.gate_rows;
-    } else {
-        m0 = (int64_t)blockIdx.x * a.rows;
-        m1 = m0 + a.rows;
     }
     m1 = m1 < a.M ? m1 : a.M;
     const float inv = 1.0f / (float)C;
-    const bool pre = a.pre.kind != NM_NORM_NONE && a.dN, post = a.post.kind != NM_NORM_NONE;
-    const bool layer = (pre && a.pre.kind == NM_NORM_LAYER) || (post && a.post.kind == NM_NORM_LAYER);
-    float acc[5][NV][V];
+    const bool pre = a.pre.kind != NM_NORM_NONE && a.dN, post = a.post.kind != NM_NORM_NONE, block = a.Y != nullptr;
+    const bool lz = L && a.pre.kind == NM_NORM_LAYER, ly = L && a.post.kind == NM_NORM_LAYER;
+    float p0[NV][8], p1[L ? NV : 1][8], sa[NV][8], sb[L ? NV : 1][8], ta[MULTI ? NV : 1][8], tb[MULTI && L ? NV : 1][8];
+    float wpre[8], wpost[8];   // (wpost times the gate, where that stays the same)
 #pragma unroll
-    for (int s = 0; s < 5; ++s)
+    for (int k = 0; k < NV; ++k)
 #pragma unroll
-        for (int k = 0; k < NV; ++k)
+        for (int i = 0; i < 8; ++i) {
+            p0[k][i] = sa[k][i] = 0.0f;
+            if constexpr (L) p1[k][i] = sb[k][i] = 0.0f;
+            if constexpr (MULTI) ta[k][i] = 0.0f;
+            if constexpr (MULTI && L) tb[k][i] = 0.0f;
+        }
+    auto ones = [](float (&w)[8]) __attribute__((always_inline)) {
 #pragma unroll
-            for (int i = 0; i < V; ++i) acc[s][k][i] = 0.0f;
+        for (int i = 0; i < 8; ++i) w[i] = 1.0f;
+    };
+    auto side = [&](float (&w)[8], const void* p, int64_t row, int c) __attribute__((always_inline)) {
+        if (p) norm_load(w, (const uint8_t*)p + row * a.ldg * (a.w32 ? 4 : 2), a.w32, c, C);
+        else ones(w);
+    };
+    if constexpr (AHEAD) {
+        side(wpre, a.pre.w, 0, t * 8);
+        side(wpost, a.post.w, 0, t * 8);
+        if constexpr (!MULTI) {
+            float ga[8];
+            side(ga, a.gate, m0 < a.M ? m0 / a.gate_rows : 0, t * 8);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) wpost[i] *= ga[i];
+        }
+    }
+    const int64_t xs = X32 ? 4 : 2;
+    // whole vectors only: the row's last, part-filled one is loaded where it is used
+    auto fetch = [&](NormRaw<X32>& r, int64_t m) __attribute__((always_inline)) {
+        const int c = t * 8;
+        if (c + 8 > C) return;
+        if (pre) {
+            const norm_u4* z = (const norm_u4*)((const uint8_t*)a.Z + (m * a.ldz + c) * xs);
+#pragma unroll
+            for (int i = 0; i < (X32 ? 2 : 1); ++i) r.z[i] = z[i];
+            if (!a.dn32) r.dn = *(const norm_u4*)((const uint16_t*)a.dN + m * a.lddn + c);
+        }
+        if (a.dZ) {
+            const norm_u4* g = (const norm_u4*)((const uint8_t*)a.dZ + (m * a.lddz + c) * xs);
+#pragma unroll
+            for (int i = 0; i < (X32 ? 2 : 1); ++i) r.dz[i] = g[i];
+        }
+        if (block) r.y = *(const norm_u4*)(a.Y + m * a.ldyb + c);
+    };
+    NormRaw<X32> raw;
+    if (AHEAD && m0 < m1) fetch(raw, m0);
     for (int64_t m = m0; m < m1; ++m) {
-        float z[NV][V], d[NV][V], g[NV][V], y[NV][V];   // z, dn, dz, y; columns past the end hold zeros
+        float z[NV][8], d[NV][8], g[NV][8], y[NV][8];   // z, dn, dz, y; columns past the end hold zeros
 #pragma unroll
         for (int k = 0; k < NV; ++k) {
-            const int c = (k * nt + t) * V;
+            const int c = (k * nt + t) * 8;
 #pragma unroll
-            for (int i = 0; i < V; ++i) z[k][i] = d[k][i] = g[k][i] = y[k][i] = 0.0f;
-            if (c < C) {
+            for (int i = 0; i < 8; ++i) z[k][i] = d[k][i] = g[k][i] = y[k][i] = 0.0f;
+            if (AHEAD && c + 8 <= C) {
                 if (pre) {
-                    norm_load<V>(z[k], (const uint8_t*)a.Z + m * a.ldz * (X32 ? 4 : 2), X32, c);
-                    norm_load<V>(d[k], (const uint8_t*)a.dN + m * a.lddn * (a.dn32 ? 4 : 2), a.dn32, c);
+                    norm_raw<X32>(z[k], raw.z);
+                    if (a.dn32) norm_load(d[k], (const float*)a.dN + m * a.lddn, true, c, C);
+                    else norm_widen(d[k], raw.dn);
                 }
-                if (a.dZ) norm_load<V>(g[k], (const uint8_t*)a.dZ + m * a.lddz * (X32 ? 4 : 2), X32, c);
-                if (a.Y) norm_load<V>(y[k], a.Y + m * a.ldyb, false, c);
+                if (a.dZ) norm_raw<X32>(g[k], raw.dz);
+                if (block) norm_widen(y[k], raw.y);
+            } else if (c < C) {
+                if (pre) {
+                    norm_load(z[k], (const uint8_t*)a.Z + m * a.ldz * xs, X32, c, C);
+                    norm_load(d[k], (const uint8_t*)a.dN + m * a.lddn * (a.dn32 ? 4 : 2), a.dn32, c, C);
+                }
+                if (a.dZ) norm_load(g[k], (const uint8_t*)a.dZ + m * a.lddz * xs, X32, c, C);
+                if (block) norm_load(y[k], a.Y + m * a.ldyb, false, c, C);
             }
         }
+        if (AHEAD && m + 1 < m1) fetch(raw, m + 1);
         // statistics of z and y together
         float s0 = 0.0f, s1 = 0.0f;
-        if (layer) {
+        if (lz || ly) {
 #pragma unroll
             for (int k = 0; k < NV; ++k)
 #pragma unroll
-                for (int i = 0; i < V; ++i) {
+                for (int i = 0; i < 8; ++i) {
                     s0 += z[k][i];
                     s1 += y[k][i];
                 }
             sum.two(s0, s1);
-            const float mz = pre && a.pre.kind == NM_NORM_LAYER ? s0 * inv : 0.0f;
-            const float my = post && a.post.kind == NM_NORM_LAYER ? s1 * inv : 0.0f;
+            const float mz = lz ? s0 * inv : 0.0f, my = ly ? s1 * inv : 0.0f;
 #pragma unroll
             for (int k = 0; k < NV; ++k)
-                if ((k * nt + t) * V < C) {
 #pragma unroll
-                    for (int i = 0; i < V; ++i) {
-                        z[k][i] -= mz;
-                        y[k][i] -= my;
-                    }
+                for (int i = 0; i < 8; ++i) {
+                    const bool in = (k * nt + t) * 8 + i < C;
+                    z[k][i] = in ? z[k][i] - mz : 0.0f;
+                    y[k][i] = in ? y[k][i] - my : 0.0f;
                 }
             s0 = s1 = 0.0f;
         }
 #pragma unroll
         for (int k = 0; k < NV; ++k)
 #pragma unroll
-            for (int i = 0; i < V; ++i) {
+            for (int i = 0; i < 8; ++i) {
                 s0 = __builtin_fmaf(z[k][i], z[k][i], s0);
                 s1 = __builtin_fmaf(y[k][i], y[k][i], s1);
             }
@@ -385,68 +484,95 @@ __global__ __launch_bounds__(1024) void norm_bwd_kernel(NormBwdArgs a) {
             s0 = s1 = 0.0f;
 #pragma unroll
             for (int k = 0; k < NV; ++k) {
-                const int c = (k * nt + t) * V;
-                if (c < C) {
-                    float w[V];
-                    if (a.pre.w) norm_load<V>(w, a.pre.w, a.w32, c);
+                const int c = (k * nt + t) * 8;
+                float w[8];
+                if constexpr (!AHEAD) {
+                    if (c < C) side(w, a.pre.w, 0, c);
+                    else ones(w);
+                }
 #pragma unroll
-                    for (int i = 0; i < V; ++i) {
-                        z[k][i] *= rz;
-                        acc[0][k][i] = __builtin_fmaf(d[k][i], z[k][i], acc[0][k][i]);
-                        acc[1][k][i] += d[k][i];
-                        if (a.pre.w) d[k][i] *= w[i];
-                        s0 = __builtin_fmaf(d[k][i], z[k][i], s0);
-                        s1 += d[k][i];
-                    }
+                for (int i = 0; i < 8; ++i) {
+                    z[k][i] *= rz;
+                    p0[k][i] = __builtin_fmaf(d[k][i], z[k][i], p0[k][i]);
+                    if constexpr (L) p1[k][i] += d[k][i];
+                    d[k][i] *= AHEAD ? wpre[i] : w[i];
+                    s0 = __builtin_fmaf(d[k][i], z[k][i], s0);
+                    s1 += d[k][i];
                 }
             }
             sum.two(s0, s1);
             s0 *= inv;
-            s1 = a.pre.kind == NM_NORM_LAYER ? s1 * inv : 0.0f;
+            s1 = lz ? s1 * inv : 0.0f;
 #pragma unroll
             for (int k = 0; k < NV; ++k)
 #pragma unroll
-                for (int i = 0; i < V; ++i)
-                    g[k][i] = __builtin_fmaf(rz, d[k][i] - s1 - z[k][i] * s0, g[k][i]);
+                for (int i = 0; i < 8; ++i) {
+                    const float v = __builtin_fmaf(rz, d[k][i] - s1 - z[k][i] * s0, g[k][i]);
+                    g[k][i] = !L || (k * nt + t) * 8 + i < C ? v : 0.0f;
+                }
         }
         if (a.dX) {
 #pragma unroll
             for (int k = 0; k < NV; ++k) {
-                const int c = (k * nt + t) * V;
+                const int c = (k * nt + t) * 8;
                 if (c < C) {
-                    float o[V];
+                    float o[8];
 #pragma unroll
-                    for (int i = 0; i < V; ++i) o[i] = a.res * g[k][i];
-                    norm_store<V>(o, (uint8_t*)a.dX + m * a.lddx * (X32 ? 4 : 2), X32, c);
+                    for (int i = 0; i < 8; ++i) o[i] = a.res * g[k][i];
+                    norm_store(o, (uint8_t*)a.dX + m * a.lddx * xs, X32, c, C);
                 }
             }
         }
-        if (!a.Y) continue;
+        if (!block) continue;
         // through the gate and norm_post: y becomes its normalised value, g the gradient of that
-        const int64_t gr = m / a.gate_rows;
+        const int64_t gr = MULTI ? m / a.gate_rows : 0;
+        const bool ends = MULTI && (m + 1 == m1 || (m + 1) / a.gate_rows != gr);
         s0 = s1 = 0.0f;
 #pragma unroll
         for (int k = 0; k < NV; ++k) {
-            const int c = (k * nt + t) * V;
-            if (c < C) {
-                float w[V], b[V], ga[V];
-                if (a.post.w) norm_load<V>(w, a.post.w, a.w32, c);
-                if (a.post.b && a.sums[4]) norm_load<V>(b, a.post.b, a.w32, c);
-                if (a.gate) norm_load<V>(ga, (const uint8_t*)a.gate + gr * a.ldg * (a.w32 ? 4 : 2), a.w32, c);
+            const int c = (k * nt + t) * 8;
+            float w[8], ga[8];
+            if constexpr (!AHEAD) {
+                if (c < C) {
+                    side(w, a.post.w, 0, c);
+                    side(ga, a.gate, m / a.gate_rows, c);
+                } else {
+                    ones(w);
+                    ones(ga);
+                }
+            } else if constexpr (MULTI) {
+                if (c < C) side(ga, a.gate, gr, c);
+                else ones(ga);
+            }
 #pragma unroll
-                for (int i = 0; i < V; ++i) {
-                    y[k][i] *= ry;
-                    if (a.sums[4]) {
-                        float u = a.post.w ? y[k][i] * w[i] : y[k][i];
-                        if (a.post.b) u += b[i];
-                        acc[4][k][i] = __builtin_fmaf(g[k][i], u, acc[4][k][i]);
+            for (int i = 0; i < 8; ++i) {
+                y[k][i] *= ry;
+                sa[k][i] = __builtin_fmaf(g[k][i], y[k][i], sa[k][i]);
+                if constexpr (L) sb[k][i] += g[k][i];
+                if constexpr (!AHEAD || MULTI) g[k][i] *= ga[i];
+                g[k][i] *= AHEAD ? wpost[i] : w[i];
+                s0 = __builtin_fmaf(g[k][i], y[k][i], s0);
+                s1 += g[k][i];
+            }
+            if (MULTI && ends) {
+                if (a.sums[4] && c < C) {
+                    float o[8], b[8];
+                    if (L && a.post.b) norm_load(b, a.post.b, a.w32, c, C);
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) {
+                        o[i] = sa[k][i] * (AHEAD ? wpost[i] : w[i]);
+                        if (L && a.post.b) o[i] = __builtin_fmaf(sb[L ? k : 0][i], b[i], o[i]);
                     }
-                    if (a.gate) g[k][i] *= ga[i];
-                    acc[2][k][i] = __builtin_fmaf(g[k][i], y[k][i], acc[2][k][i]);
-                    acc[3][k][i] += g[k][i];
-                    if (a.post.w) g[k][i] *= w[i];
-                    s0 = __builtin_fmaf(g[k][i], y[k][i], s0);
-                    s1 += g[k][i];
+                    norm_store(o, a.sums[4] + gr * C, true, c, C);
+                }
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    ta[MULTI ? k : 0][i] = __builtin_fmaf(ga[i], sa[k][i], ta[MULTI ? k : 0][i]);
+                    sa[k][i] = 0.0f;
+                    if constexpr (L) {
+                        tb[MULTI ? k : 0][i] = __builtin_fmaf(ga[i], sb[k][i], tb[MULTI ? k : 0][i]);
+                        sb[k][i] = 0.0f;
+                    }
                 }
             }
         }
@@ -454,86 +580,102 @@ __global__ __launch_bounds__(1024) void norm_bwd_kernel(NormBwdArgs a) {
             if (post) {
                 sum.two(s0, s1);
                 s0 *= inv;
-                s1 = a.post.kind == NM_NORM_LAYER ? s1 * inv : 0.0f;
+                s1 = ly ? s1 * inv : 0.0f;
             } else {
                 s0 = s1 = 0.0f;
             }
 #pragma unroll
             for (int k = 0; k < NV; ++k) {
-                const int c = (k * nt + t) * V;
+                const int c = (k * nt + t) * 8;
                 if (c < C) {
-                    float o[V];
+                    float o[8];
 #pragma unroll
-                    for (int i = 0; i < V; ++i) o[i] = ry * (g[k][i] - s1 - y[k][i] * s0);
-                    norm_store<V>(o, a.dY + m * a.lddy, false, c);
+                    for (int i = 0; i < 8; ++i) o[i] = ry * (g[k][i] - s1 - y[k][i] * s0);
+                    norm_store(o, a.dY + m * a.lddy, false, c, C);
                 }
             }
         }
-        if (a.sums[4] && !a.per_gate && (m + 1 == m1 || (m + 1) / a.gate_rows != gr)) {
-#pragma unroll
-            for (int k = 0; k < NV; ++k) {
-                const int c = (k * nt + t) * V;
-                if (c < C) norm_store<V>(acc[4][k], a.sums[4] + gr * C, true, c);
-#pragma unroll
-                for (int i = 0; i < V; ++i) acc[4][k][i] = 0.0f;
-            }
-        }
     }
+    auto leave = [&](const float (&v)[8], int s, int c) __attribute__((always_inline)) {
+        norm_store(v, a.part + ((int64_t)s * a.blocks + blockIdx.x) * C, true, c, C);
+    };
 #pragma unroll
-    for (int s = 0; s < 5; ++s) {
-        if (!a.sums[s] || (s == 4 && !a.per_gate)) continue;
-#pragma unroll
-        for (int k = 0; k < NV; ++k) {
-            const int c = (k * nt + t) * V;
-            if (c < C) norm_store<V>(acc[s][k], a.part + ((int64_t)s * a.blocks + blockIdx.x) * C, true, c);
+    for (int k = 0; k < NV; ++k) {
+        const int c = (k * nt + t) * 8;
+        if (c >= C) continue;
+        if (a.sums[0]) leave(p0[k], 0, c);
+        if constexpr (L) {
+            if (a.sums[1]) leave(p1[k], 1, c);
+        }
+        if (a.sums[2] || (!MULTI && a.sums[4])) leave(MULTI ? ta[MULTI ? k : 0] : sa[k], 2, c);
+        if constexpr (L) {
+            if (a.sums[3] || (!MULTI && a.sums[4])) leave(MULTI ? tb[MULTI && L ? k : 0] : sb[k], 3, c);
         }
     }
 }
 
-// Partial sums of the blocks added in order: 64 columns a block, 16 runs of partials side by side.
-// grid: x columns, y sums (4: dgate, one z per gate row).
+// Partial sums of the blocks added in order: 32 columns a block, 32 runs of partials side by side.
+// grid: columns, for each sum in turn (4 ..: dgate's rows; a single one comes with dw_post, from the
+// same partials).
 __global__ __launch_bounds__(1024) void norm_sum_kernel(NormBwdArgs a, int gates) {
-    __shared__ float red[16][64];
-    const int s = blockIdx.y < 4 ? (int)blockIdx.y : 4, gr = blockIdx.y < 4 ? 0 : (int)blockIdx.y - 4;
-    if (!a.sums[s]) return;
-    const int c = blockIdx.x * 64 + (threadIdx.x & 63), run = threadIdx.x >> 6;
+    __shared__ float red[2][32][32];
+    const unsigned tiles = (a.C + 31) / 32, which = blockIdx.x / tiles;
+    const bool both = which == 2 && gates == 1 && a.sums[4];
+    const int s = which < 4 ? (int)which : 4, gr = which < 4 ? 0 : (int)which - 4;
+    if (!a.sums[s] && !both) return;
+    const int l = threadIdx.x & 31, c = (blockIdx.x - which * tiles) * 32 + l, run = threadIdx.x >> 5;
     const int first = s == 4 ? gr * a.per_gate : 0, count = s == 4 ? a.per_gate : a.blocks;
-    const int per = (count + 15) / 16, b0 = run * per, b1 = b0 + per < count ? b0 + per : count;
-    float v = 0.0f;
-    if (c < a.C) {
-        const float* p = a.part + ((int64_t)s * a.blocks + first) * a.C + c;
+    const int per = (count + 31) / 32, b0 = run * per, b1 = b0 + per < count ? b0 + per : count;
+    const bool in = c < a.C;
+    auto part = [&](int k, int b) { return a.part[((int64_t)k * a.blocks + first + b) * a.C + c]; };
+    auto side = [&](const void* p, int64_t at) { return !p ? 1.0f : a.w32 ? ((const float*)p)[at] : bf16_bits_to_f32(((const uint16_t*)p)[at]); };
+    const bool bias = (s == 4 || both) && a.post.b;
+    const bool gated = (s == 2 || s == 3) && a.per_gate && a.gate;
+    float v = 0.0f, w = 0.0f;
+    if (in && gated && gates > 1) {
 #pragma unroll 8
-        for (int b = b0; b < b1; ++b) v += p[(int64_t)b * a.C];
+        for (int b = b0; b < b1; ++b) v = __builtin_fmaf(side(a.gate, (int64_t)(b / a.per_gate) * a.ldg + c), part(s, b), v);
+    } else if (in) {
+#pragma unroll 8
+        for (int b = b0; b < b1; ++b) v += part(s == 4 ? 2 : s, b);
+        if (bias)
+#pragma unroll 8
+            for (int b = b0; b < b1; ++b) w += part(3, b);
     }
-    red[run][threadIdx.x & 63] = v;
+    red[0][run][l] = v;
+    red[1][run][l] = w;
     __syncthreads();
-    if (run || c >= a.C) return;
-    for (int i = 1; i < 16; ++i) v += red[i][threadIdx.x];
-    a.sums[s][(int64_t)gr * a.C + c] = v;
+    if (run || !in) return;
+    for (int i = 1; i < 32; ++i) {
+        v += red[0][i][l];
+        w += red[1][i][l];
+    }
+    if (s == 4 || both) {
+        float g = v * side(a.post.w, c);
+        if (bias) g = __builtin_fmaf(w, side(a.post.b, c), g);
+        a.sums[4][(int64_t)gr * a.C + c] = g;
+    }
+    if (s == 4 || !a.sums[s]) return;
+    a.sums[s][c] = gated && gates == 1 ? v * side(a.gate, c) : v;
 }
 
 // ------------------------------------------------------------------ host
-static bool aligned_rows(const void* p, int64_t ld, int64_t es) {
-    return !p || (((uintptr_t)p & 15u) == 0 && ld * es % 16 == 0);
-}
-
-// threads of a block for V columns a vector and NV vectors a thread
-static int norm_threads(int C, int V, int NV) {
-    const int t = (int)ceil_div(C, V * NV);
+template <int NV>
+static int norm_threads(int C) {
+    const int t = (int)ceil_div(C, 8 * NV);
     return (t + 63) / 64 * 64;
 }
 
-template <int V, int NV>
+template <int NV>
 static void norm_go(const NormArgs& a, bool x32, hipStream_t s) {
-    const dim3 grid((unsigned)a.M), block((unsigned)norm_threads(a.C, V, NV));
+    const dim3 grid((unsigned)a.M), block((unsigned)norm_threads<NV>(a.C));
     const size_t lds = a.Ns && a.Ns != 4 ? (size_t)a.C : 0;
-    if (x32) hipLaunchKernelGGL((norm_kernel<V, NV, true>), grid, block, lds, s, a);
-    else hipLaunchKernelGGL((norm_kernel<V, NV, false>), grid, block, lds, s, a);
+    if (x32) hipLaunchKernelGGL((norm_kernel<NV, true>), grid, block, lds, s, a);
+    else hipLaunchKernelGGL((norm_kernel<NV, false>), grid, block, lds, s, a);
 }
 
 nm_status launch_block_norm(const NormIn& in, hipStream_t s) {
     NormArgs a{};
-    const int64_t xs = in.xdt == NM_F32 ? 4 : 2, wsz = in.wdt == NM_F32 ? 4 : 2;
     a.X = in.X;
     a.ldx = in.ldx;
     a.M = (int)in.Mtok;
@@ -555,22 +697,10 @@ nm_status launch_block_norm(const NormIn& in, hipStream_t s) {
     a.ndt = in.ndt;
     a.Ns = in.Ns;
     a.n_scale = in.n_scale;
-    const bool code = in.ndt == NM_I8 || in.ndt == NM_FP8;
-    const bool vec = in.C % 8 == 0 && aligned_rows(in.X, in.ldx, xs) && aligned_rows(in.Y, in.ldyb, 2) &&
-                     aligned_rows(in.gate, in.ldg, wsz) && aligned_rows(in.Z, in.ldz, xs) && aligned_rows(in.w_post, 8, 2) &&
-                     aligned_rows(in.b_post, 8, 2) && aligned_rows(in.w_pre, 8, 2) && aligned_rows(in.b_pre, 8, 2) &&
-                     (code || aligned_rows(in.N, in.ldn, in.ndt == NM_F32 ? 4 : 2));
     const bool x32 = in.xdt == NM_F32;
-    if (vec) {
-        if (in.C <= 8192) norm_go<8, 1>(a, x32, s);
-        else if (in.C <= 16384) norm_go<8, 2>(a, x32, s);
-        else norm_go<8, 4>(a, x32, s);
-    } else if (code) {
-        return set_error(NM_ERR_ALIGN, "nm_block_norm: codes need 16-byte aligned rows of the inputs and Z");
-    } else {
-        if (in.C <= 4096) norm_go<1, 4>(a, x32, s);
-        else norm_go<1, 32>(a, x32, s);
-    }
+    if (in.C <= 8192) norm_go<1>(a, x32, s);
+    else if (in.C <= 16384) norm_go<2>(a, x32, s);
+    else norm_go<4>(a, x32, s);
     return check_launch("nm_block_norm");
 }
 
@@ -578,12 +708,14 @@ nm_status launch_block_norm(const NormIn& in, hipStream_t s) {
 struct NormPlan {
     int rows, blocks, per_gate, gates;
 };
-static NormPlan norm_plan(int64_t M, int64_t gate_rows) {
+constexpr int64_t kNormMulti = 8192;   // columns up to which a block may hold several gate rows
+static NormPlan norm_plan(int64_t M, int64_t C, int64_t gate_rows) {
     NormPlan p{};
     const int64_t gr = gate_rows > 0 && gate_rows < M ? gate_rows : (M > 0 ? M : 1);
-    const int64_t want = M / 512 > 4 ? M / 512 : 4;   // rows a block
+    const int64_t want = M > 512 ? M / 512 : 1;   // rows a block
     p.gates = (int)(M > 0 ? ceil_div(M, gr) : 1);
-    if (gr <= want) {
+    if (M <= 0) return p;   // no blocks, no partials
+    if (gr < want && C <= kNormMulti) {
         p.rows = (int)(want / gr * gr);
         p.blocks = (int)ceil_div(M, p.rows);
     } else {
@@ -595,20 +727,24 @@ static NormPlan norm_plan(int64_t M, int64_t gate_rows) {
 }
 
 size_t block_norm_bwd_ws(int64_t M, int64_t C, int64_t gate_rows) {
-    return (size_t)norm_plan(M, gate_rows).blocks * (size_t)C * 5 * 4;
+    return (size_t)norm_plan(M, C, gate_rows).blocks * (size_t)C * 4 * 4;
 }
 
-template <int V, int NV>
-static void norm_bwd_go(const NormBwdArgs& a, bool x32, hipStream_t s) {
-    const dim3 grid((unsigned)a.blocks), block((unsigned)norm_threads(a.C, V, NV));
-    if (x32) hipLaunchKernelGGL((norm_bwd_kernel<V, NV, true>), grid, block, 0, s, a);
-    else hipLaunchKernelGGL((norm_bwd_kernel<V, NV, false>), grid, block, 0, s, a);
+template <int NV, int NT, bool X32>
+static void norm_bwd_go(const NormBwdArgs& a, bool layer, hipStream_t s) {
+    const dim3 grid((unsigned)a.blocks), block((unsigned)norm_threads<NV>(a.C));
+    if (a.per_gate) {
+        if (layer) hipLaunchKernelGGL((norm_bwd_kernel<NV, NT, X32, true, false>), grid, block, 0, s, a);
+        else hipLaunchKernelGGL((norm_bwd_kernel<NV, NT, X32, false, false>), grid, block, 0, s, a);
+    } else if constexpr (NV <= 2) {
+        if (layer) hipLaunchKernelGGL((norm_bwd_kernel<NV, NT, X32, true, true>), grid, block, 0, s, a);
+        else hipLaunchKernelGGL((norm_bwd_kernel<NV, NT, X32, false, true>), grid, block, 0, s, a);
+    }
 }
 
 nm_status launch_block_norm_bwd(const NormBwdIn& in, void* ws, hipStream_t s) {
     NormBwdArgs a{};
-    const int64_t xs = in.xdt == NM_F32 ? 4 : 2, wsz = in.wdt == NM_F32 ? 4 : 2;
-    const NormPlan p = norm_plan(in.Mtok, in.gate_rows);
+    const NormPlan p = norm_plan(in.Mtok, in.C, in.gate_rows);
     a.Z = in.Z;
     a.ldz = in.ldz;
     a.dZ = in.dZ;
@@ -641,27 +777,27 @@ nm_status launch_block_norm_bwd(const NormBwdIn& in, void* ws, hipStream_t s) {
     a.rows = p.rows;
     a.blocks = p.blocks;
     a.per_gate = p.per_gate;
+    if (ceil_div(in.C, 32) * (4 + (int64_t)p.gates) >= 1LL << 31)
+        return set_error(NM_ERR_SHAPE, "nm_block_norm_backward: too many gate rows");
     const bool x32 = in.xdt == NM_F32;
     if (in.Mtok > 0) {
-        const bool vec = in.C % 8 == 0 && aligned_rows(in.Z, in.ldz, xs) && aligned_rows(in.dZ, in.lddz, xs) &&
-                         aligned_rows(in.dN, in.lddn, in.dndt == NM_F32 ? 4 : 2) && aligned_rows(in.Y, in.ldyb, 2) &&
-                         aligned_rows(in.gate, in.ldg, wsz) && aligned_rows(in.dX, in.lddx, xs) && aligned_rows(in.dY, in.lddy, 2) &&
-                         aligned_rows(in.w_post, 8, 2) && aligned_rows(in.b_post, 8, 2) && aligned_rows(in.w_pre, 8, 2) &&
-                         aligned_rows(in.sums[4], in.C, 4);
-        if (vec) {
-            if (in.C <= 8192) norm_bwd_go<8, 1>(a, x32, s);
-            else if (in.C <= 16384) norm_bwd_go<8, 2>(a, x32, s);
-            else norm_bwd_go<8, 4>(a, x32, s);
-        } else {
-            if (in.C <= 4096) norm_bwd_go<1, 4>(a, x32, s);
-            else norm_bwd_go<1, 32>(a, x32, s);
-        }
+        const bool layer = a.pre.kind == NM_NORM_LAYER || a.post.kind == NM_NORM_LAYER || a.sums[1] || a.sums[3] || a.post.b;
+        const auto go = [&](auto x) {
+            constexpr bool X32 = decltype(x)::value;
+            if (in.C <= 4096) norm_bwd_go<1, 512, X32>(a, layer, s);
+            else if (in.C <= kNormMulti) norm_bwd_go<2, 512, X32>(a, layer, s);
+            else if (in.C <= 16384) norm_bwd_go<4, 512, X32>(a, layer, s);
+            else norm_bwd_go<4, 1024, X32>(a, layer, s);
+        };
+        if (x32) go(std::true_type{});
+        else go(std::false_type{});
     }
     // without tokens every sum is of no partials; whole gate rows of a block are written by it
     if (sums) {
-        const bool reduce_gate = in.sums[4] && (p.per_gate > 0 || in.Mtok == 0);
-        hipLaunchKernelGGL(norm_sum_kernel, dim3((unsigned)ceil_div(in.C, 64), (unsigned)(reduce_gate ? 4 + p.gates : 4)), dim3(1024),
-                           0, s, a, p.gates);
+        // several gate rows that blocks wrote partials of (a block that holds whole ones has written them)
+        const bool rows = in.sums[4] && p.per_gate > 0 && p.gates > 1;
+        hipLaunchKernelGGL(norm_sum_kernel, dim3((unsigned)(ceil_div(in.C, 32) * (rows ? 4 + p.gates : 4))), dim3(1024), 0, s, a,
+                           p.gates);
     }
     return check_launch("nm_block_norm_backward");
 }
