@@ -1,7 +1,8 @@
 // A mixture-of-experts layer of sparse gated blocks for a few tokens, in three launches:
 //   moe_logits_kernel  router logits (dense MFMA), K split over blocks, partials in f32
 //   moe_up_kernel      every block picks the experts of all tokens for itself from the logits (no
-//                      launch between), then H = act(x Wg^T) . (x Wu^T) of one expert's 16 features
+//                      launch between), then makes H = act(x Wg^T) . (x Wu^T) tile by tile: tasks are (picked
+//                      expert, 16 or 32 features)
 //   moe_down_kernel    Y: a block owns output columns and adds up, for them, every picked expert's
 //                      product in a fixed order
 // An expert's tokens are gathered by lane in the activation's loads (16 at a time are the B
@@ -18,7 +19,8 @@ struct MoeArgs {
     const uint16_t* router;
     int64_t ldr;
     const float* bias;
-    int T, K, F, E, topk, sigmoid, renorm, Ns, wK, wF, gshift, act, ksplit;
+    int T, K, F, E, topk, sigmoid, renorm, wK, wF, gshift, act, ksplit;
+    FewLift lift;
     float route_scale;
     nm_experts w[3];       // gate, up, down; ld_vals and es_vals in bytes
     float* logits;         // [ksplit][T][E]
@@ -50,12 +52,9 @@ __global__ __launch_bounds__(256) void moe_logits_kernel(MoeArgs a) {
     few_f32x4 acc = {0, 0, 0, 0};
 #pragma unroll 4
     for (int s = s0 + wave; s < s1; s += 4) {
-        const int col = 32 * s + 8 * q;
-        uint4 w = make_uint4(0, 0, 0, 0), x = w;
-        if (col < a.K) {
-            w = *(const uint4*)(wr + col);
-            x = *(const uint4*)(xr + col);
-        }
+        const int col = 32 * s + 8 * q, at = col < a.K ? col : a.K - 8;
+        uint4 w = *(const uint4*)(wr + at), x = *(const uint4*)(xr + at);
+        if (32 * s + 32 > a.K && col >= a.K) w = x = make_uint4(0, 0, 0, 0);
         acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(few_bf16x8, w), __builtin_bit_cast(few_bf16x8, x), acc, 0,
                                                       0, 0);
     }
@@ -110,9 +109,36 @@ __device__ __forceinline__ void moe_pick(const MoeArgs& a, int t, int lane, int3
             if (!(key[i] == key[i])) key[i] = none;
         }
     }
-    uint32_t taken = 0;   // of this lane's experts
     float total = 0.0f, mine = 0.0f;
     int my_sel = 0;
+    if constexpr (NE == 1) {
+        // a lane's place: how many keys are before its own
+        const uint64_t k = __builtin_bit_cast(uint64_t, key[0]);
+        int place = 0;
+        for (int e = 0; e < a.E; ++e) {
+            const uint64_t o = (uint64_t)(uint32_t)__builtin_amdgcn_readlane((int)(k >> 32), e) << 32 |
+                               (uint32_t)__builtin_amdgcn_readlane((int)k, e);
+            const double ok = __builtin_bit_cast(double, o);
+            place += ok > key[0] || (ok == key[0] && e < lane) ? 1 : 0;
+        }
+        const bool in = lane < a.E && place < a.topk;
+        total = in ? p[0] : 0.0f;
+        if (a.renorm) {
+            // in descending order, as below
+            float sum = 0.0f;
+            for (int j = 0; j < a.topk; ++j) {
+                const uint64_t m = __ballot(in && place == j);
+                sum += __uint_as_float((uint32_t)__builtin_amdgcn_readlane((int)__float_as_uint(p[0]), __ffsll((unsigned long long)m) - 1));
+            }
+            total = sum;
+        }
+        if (in) {
+            sel[place] = lane;
+            wts[place] = a.route_scale * (a.renorm ? p[0] / total : p[0]);
+        }
+        return;
+    }
+    uint32_t taken = 0;   // of this lane's experts
     for (int j = 0; j < a.topk; ++j) {
         double best = none;
         int at = 1 << 30;
@@ -151,8 +177,6 @@ __device__ __forceinline__ void moe_pick(const MoeArgs& a, int t, int lane, int3
 }
 
 // ------------------------------------------------------------------ gate and up
-// grid: x feature tiles of 16, y picked experts.  A block finds the experts of all tokens, takes the
-// y-th picked one (in order of the expert's number) and its (token, slot) pairs in order.
 template <int NE>
 __device__ __forceinline__ void moe_route(const MoeArgs& a, int32_t* sel, float* wts, int tid, int nw) {
     const int lane = tid & 63, wave = tid >> 6;
@@ -175,25 +199,48 @@ __device__ __forceinline__ int moe_nth(const uint64_t (&used)[kMoeExperts / 64],
     return -1;
 }
 
-template <int VT, int SPG, int NW>
-__global__ __launch_bounds__(NW * 64) void moe_up_kernel(MoeArgs a) {
-    __shared__ __attribute__((aligned(16))) float red[NW][2][256];
+// The pairs (token, slot) of expert e in order, 16 from the n0-th: lane k of 16 (and its copies) gets
+// the k-th, or -1; the count of all that are left from n0 comes back.
+__device__ __forceinline__ int moe_pairs(const int32_t* sel, int pairs, int e, int n0, int lane, int& mine) {
+    int n = 0;
+    mine = -1;
+    for (int p0 = 0; p0 < pairs; p0 += 64) {
+        uint64_t m = __ballot(p0 + lane < pairs && sel[p0 + lane < pairs ? p0 + lane : 0] == e);
+        while (m) {
+            const int b = __ffsll((unsigned long long)m) - 1;
+            m &= m - 1;
+            if (n - n0 == (lane & 15)) mine = p0 + b;
+            ++n;
+        }
+    }
+    return n - n0;
+}
+
+// RT: tiles of 16 rows of a task, gate and up beside each other.  XL: the tokens in LDS.
+template <int VT, int SPG, int RT, int NW, bool XL>
+__global__ __launch_bounds__(NW * 64) void moe_up_kernel(MoeArgs a, int tiles, int blocks) {
+    constexpr int TR = RT / 2;   // feature tiles of a task
+    __shared__ __attribute__((aligned(16))) float red[NW][RT][256];
     __shared__ int32_t sel[kMoeTokens * kMoeTopk];
     __shared__ float wts[kMoeTokens * kMoeTopk];
     __shared__ uint64_t used[kMoeExperts / 64];
-    __shared__ int16_t list[kMoeTokens * kMoeTopk];
-    __shared__ int count;
+    extern __shared__ __attribute__((aligned(16))) uint8_t xlds[];
     const int tid = threadIdx.x, lane = tid & 63;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int nu = (a.wK + 255) / 256, pairs = a.T * a.topk, stride = few_lds_row(a.wK);
     if (tid < kMoeExperts / 64) used[tid] = 0;
+    if constexpr (XL) {
+        for (int t = 0; t < a.T; ++t)
+            for (int c = tid; c < nu * 32; c += NW * 64)
+                *(few_u32x4*)(xlds + t * stride + 16 * c) = few_x8(a.X + t * a.ldx, 8 * c, a.wK, a.lift);
+    }
     if (a.E <= 64) moe_route<1>(a, sel, wts, tid, NW);
     else if (a.E <= 128) moe_route<2>(a, sel, wts, tid, NW);
     else if (a.E <= 256) moe_route<4>(a, sel, wts, tid, NW);
     else moe_route<8>(a, sel, wts, tid, NW);
-    const int pairs = a.T * a.topk;
     for (int p = tid; p < pairs; p += NW * 64) {
         atomicOr((unsigned long long*)&used[sel[p] >> 6], 1ull << (sel[p] & 63));
-        if (blockIdx.x == 0 && blockIdx.y == 0) {
+        if (blockIdx.x == 0) {
             a.sel[p] = sel[p];
             a.wts[p] = wts[p];
             if (a.sel_out) a.sel_out[p] = sel[p];
@@ -201,48 +248,69 @@ __global__ __launch_bounds__(NW * 64) void moe_up_kernel(MoeArgs a) {
         }
     }
     __syncthreads();
-    const int e = moe_nth(used, blockIdx.y);
-    if (e < 0) return;
-    if (wave == 0) {
-        int n = 0;
-        for (int p0 = 0; p0 < pairs; p0 += 64) {
-            const bool hit = p0 + lane < pairs && sel[p0 + lane] == e;
-            const uint64_t m = __ballot(hit);
-            if (hit) list[n + __popcll(m & ((1ull << lane) - 1))] = (int16_t)(p0 + lane);
-            n += __popcll(m);
+    FewRows w[RT];
+    FewUnit<VT, SPG> cur[RT];
+    int e = -1;
+    int64_t f0 = 0;
+    // task -> expert and features, the rows' pointers and the wave's first unit on its way
+    auto start = [&](int task) __attribute__((always_inline)) {
+        e = __builtin_amdgcn_readfirstlane(moe_nth(used, task / tiles));
+        if (e < 0) return;
+        f0 = (int64_t)(task % tiles) * (16 * TR);
+#pragma unroll
+        for (int i = 0; i < RT; ++i) {
+            const nm_experts& x = a.w[i & 1];
+            const int64_t r0 = f0 + 16 * (i / 2) < a.F ? f0 + 16 * (i / 2) : f0;
+            w[i] = few_rows((const uint8_t*)x.vals + e * x.es_vals, x.idx + e * x.es_idx, (const uint16_t*)x.scales + e * x.es_scales,
+                            x.ld_vals, x.ld_idx, x.ld_scales, r0, a.F, lane);
+            if (wave < nu) cur[i].load(w[i], wave, a.wK, a.gshift, lane);
         }
-        if (lane == 0) count = n;
-    }
-    __syncthreads();
-    const int n = count;
-    const int64_t f0 = (int64_t)blockIdx.x * 16;
-    FewRows w[2];
+    };
+    start(blockIdx.x);
+    for (int task = blockIdx.x; e >= 0; task += blocks) {
+        const int expert = e;
+        const int64_t f = f0;
+        for (int c = 0;; c += 16) {
+            int mine;
+            const int left = moe_pairs(sel, pairs, expert, c, lane, mine);
+            const bool last = left <= 16;
+            const int pair = mine >= 0 ? mine : __shfl(mine, 0);
+            few_f32x4 acc[RT][1];
 #pragma unroll
-    for (int m = 0; m < 2; ++m)
-        w[m] = few_rows((const uint8_t*)a.w[m].vals + e * a.w[m].es_vals, a.w[m].idx + e * a.w[m].es_idx,
-                        (const uint16_t*)a.w[m].scales + e * a.w[m].es_scales, a.w[m].ld_vals, a.w[m].ld_idx, a.w[m].ld_scales,
-                        f0, a.F, lane);
-    for (int c = 0; c < n; c += 16) {
-        const int i = c + (lane & 15) < n ? c + (lane & 15) : n - 1;
-        const uint16_t* xrow[1] = {a.X + (int64_t)(list[i] / a.topk) * a.ldx};
-        few_f32x4 acc[2][1] = {{few_f32x4{0, 0, 0, 0}}, {few_f32x4{0, 0, 0, 0}}};
-        few_product<VT, SPG, 2, 1>(w, xrow, wave, NW, (a.wK + 255) / 256, a.wK, a.gshift, a.Ns, lane, acc);
-        if (c) __syncthreads();
-        *(few_f32x4*)&red[wave][0][lane * 4] = acc[0][0];
-        *(few_f32x4*)&red[wave][1][lane * 4] = acc[1][0];
-        __syncthreads();
-        if (tid < 256) {
-            const int k = c + ((tid >> 2) & 15);
-            const int64_t f = f0 + 4 * (tid >> 6) + (tid & 3);
-            if (k < n && f < a.F) {
-                float g = 0.0f, u = 0.0f;
+            for (int i = 0; i < RT; ++i) acc[i][0] = few_f32x4{0, 0, 0, 0};
+            if (c) {   // the expert's next 16 tokens: its rows again
 #pragma unroll
-                for (int v = 0; v < NW; ++v) {
-                    g += red[v][0][tid];
-                    u += red[v][1][tid];
-                }
-                a.H[(int64_t)list[k] * a.ldh + f] = (uint16_t)f32_to_bf16_bits(few_act(a.act, g) * u);
+                for (int i = 0; i < RT; ++i)
+                    if (wave < nu) cur[i].load(w[i], wave, a.wK, a.gshift, lane);
             }
+            if constexpr (XL) {
+                const FewXLds x{xlds + pair / a.topk * stride};
+                few_product<VT, SPG, RT, 1>(cur, w, x, wave, NW, nu, a.wK, a.gshift, a.lift, lane, acc);
+            } else {
+                const FewXDirect<1> x{{a.X + (int64_t)(pair / a.topk) * a.ldx}};
+                few_product<VT, SPG, RT, 1>(cur, w, x, wave, NW, nu, a.wK, a.gshift, a.lift, lane, acc);
+            }
+            if (last) start(task + blocks);
+            __syncthreads();   // the sums of the last round have been read
+#pragma unroll
+            for (int i = 0; i < RT; ++i) *(few_f32x4*)&red[wave][i][lane * 4] = acc[i][0];
+            __syncthreads();
+            // every wave finds the pair of its threads' token
+            for (int o = tid; o < TR * 256; o += NW * 64) {
+                const int tile = o >> 8, k = o & 255;
+                const int to = __shfl(mine, (k >> 2) & 15);
+                const int64_t r = f + 16 * tile + 4 * (k >> 6) + (k & 3);
+                if (to >= 0 && r < a.F) {
+                    float g = 0.0f, u = 0.0f;
+#pragma unroll
+                    for (int v = 0; v < NW; ++v) {
+                        g += red[v][2 * tile][k];
+                        u += red[v][2 * tile + 1][k];
+                    }
+                    a.H[(int64_t)to * a.ldh + r] = (uint16_t)f32_to_bf16_bits(few_act(a.act, g) * u);
+                }
+            }
+            if (last) break;
         }
     }
 }
@@ -269,40 +337,28 @@ __global__ __launch_bounds__(NW * 64) void moe_down_kernel(MoeArgs a, int slices
     const int64_t r0 = (int64_t)blockIdx.x * 16;
     const int units = (a.wF + 255) / 256;
     for (int item = wave;; item += NW) {
-        const int e = moe_nth(used, item / slices), sl = item % slices;
+        const int e = __builtin_amdgcn_readfirstlane(moe_nth(used, item / slices)), sl = item % slices;
         if (e < 0) break;
-        const FewRows w[1] = {few_rows((const uint8_t*)a.w[2].vals + e * a.w[2].es_vals, a.w[2].idx + e * a.w[2].es_idx,
-                                       (const uint16_t*)a.w[2].scales + e * a.w[2].es_scales, a.w[2].ld_vals, a.w[2].ld_idx,
-                                       a.w[2].ld_scales, r0, a.K, lane)};
-        // the expert's pairs, 16 at a time: lane k of 16 has the k-th from the position reached
-        int p0 = 0;
-        while (p0 < pairs) {
-            int mine = -1, n = 0, at = p0;
-            for (; at < pairs && n < 16; at += 64) {
-                uint64_t m = __ballot(at + lane < pairs && sel[at + lane < pairs ? at + lane : 0] == e);
-                while (m && n < 16) {
-                    const int b = __ffsll((unsigned long long)m) - 1;
-                    m &= m - 1;
-                    if ((lane & 15) == n) mine = at + b;
-                    p0 = at + b + 1;
-                    ++n;
-                }
-                if (m) break;
-            }
-            if (n < 16) p0 = pairs;
-            if (n == 0) break;
-            const bool real = mine >= 0;
-            const int first = __shfl(mine, 0);
-            const uint16_t* xrow[1] = {a.H + (int64_t)(real ? mine : first) * a.ldh};
+        const nm_experts& d = a.w[2];
+        const FewRows w[1] = {few_rows((const uint8_t*)d.vals + e * d.es_vals, d.idx + e * d.es_idx,
+                                       (const uint16_t*)d.scales + e * d.es_scales, d.ld_vals, d.ld_idx, d.ld_scales, r0, a.K, lane)};
+        for (int c = 0;; c += 16) {
+            FewUnit<VT, SPG> cur[1];
+            cur[0].load(w[0], sl, a.wF, a.gshift, lane);
+            int mine;
+            const int left = moe_pairs(sel, pairs, e, c, lane, mine);
+            const int pair = mine >= 0 ? mine : __shfl(mine, 0);
+            const FewXDirect<1> x{{a.H + (int64_t)pair * a.ldh}};
             few_f32x4 acc[1][1] = {{few_f32x4{0, 0, 0, 0}}};
-            few_product<VT, SPG, 1, 1>(w, xrow, sl, slices, units, a.wF, a.gshift, a.Ns, lane, acc);
-            if (real) {
+            few_product<VT, SPG, 1, 1>(cur, w, x, sl, slices, units, a.wF, a.gshift, a.lift, lane, acc);
+            if (mine >= 0) {
                 const float wt = a.wts[mine];
                 few_f32x4 v = acc[0][0];
 #pragma unroll
                 for (int k = 0; k < 4; ++k) v[k] *= wt;
                 *(few_f32x4*)&part[((int64_t)sl * pairs + mine) * 16 + 4 * (lane >> 4)] = v;
             }
+            if (left <= 16) break;
         }
     }
     __syncthreads();
@@ -338,7 +394,16 @@ template <int VT, int SPG>
 static nm_status moe_go(const MoeArgs& a, hipStream_t s) {
     const int pairs = a.T * a.topk, picked = pairs < a.E ? pairs : a.E;
     hipLaunchKernelGGL(moe_logits_kernel, dim3((a.E + 15) / 16, (a.T + 15) / 16, a.ksplit), dim3(256), 0, s, a);
-    hipLaunchKernelGGL((moe_up_kernel<VT, SPG, kMoeWaves>), dim3((a.F + 15) / 16, picked), dim3(kMoeWaves * 64), 0, s, a);
+    // two feature tiles of a 4-bit weight a task (a unit of its rows is a third of a bf16 one's)
+    constexpr int RT = VT == kFewBF16 ? 2 : 4, NW = 8;
+    const int tiles = (a.F + 8 * RT - 1) / (8 * RT);
+    const int64_t tasks = (int64_t)tiles * picked;
+    const int blocks = (int)(tasks < 512 ? tasks : 512);
+    const int64_t xbytes = (int64_t)a.T * few_lds_row(a.wK);
+    if (xbytes <= 32 * 1024)
+        hipLaunchKernelGGL((moe_up_kernel<VT, SPG, RT, NW, true>), dim3(blocks), dim3(NW * 64), (size_t)xbytes, s, a, tiles, blocks);
+    else
+        hipLaunchKernelGGL((moe_up_kernel<VT, SPG, RT, NW, false>), dim3(blocks), dim3(NW * 64), 0, s, a, tiles, blocks);
     // slices of an expert's width: so many that every wave of a block has one where few experts are
     // picked, as long as the partial sums fit
     int slices = (kMoeWaves + picked - 1) / picked;
@@ -365,7 +430,7 @@ nm_status launch_moe(const MoeIn& in, void* ws, hipStream_t s) {
     a.sigmoid = in.route == NM_ROUTE_SIGMOID;
     a.renorm = in.renorm;
     a.route_scale = in.route_scale;
-    a.Ns = in.Ns;
+    a.lift = few_lift(in.Ns);
     a.wK = (int)(in.Ns ? in.K / (2 * in.Ns) * 4 * (in.Ns - 1) : in.K);
     a.wF = (int)(in.Ns ? in.F / (2 * in.Ns) * 4 * (in.Ns - 1) : in.F);
     a.gshift = in.group == 64 ? 6 : in.group == 128 ? 7 : 8;

@@ -94,7 +94,8 @@ nm_status launch_quant_w4(const void* vals, nm_dtype vdt, int64_t R, int64_t slo
 struct W4Args {
     const uint16_t* X;
     int64_t ldx;
-    int Mtok, Ns, width, gshift;
+    int Mtok, width, gshift;
+    FewLift lift;
     const uint8_t* codes[2];
     const uint32_t* idx[2];
     const uint16_t* scales[2];
@@ -106,17 +107,21 @@ struct W4Args {
 
 // A block of NW waves owns RT tiles of 16 rows (GLU: RT / 2 tiles of 16 features, gate and up
 // beside each other) and 16 CT tokens.  Its waves take units of 256 columns in turn and their sums
-// meet in LDS, added in wave order.
-template <int VT, int SPG, bool GLU, int RT, int CT, int NW>
+// meet in LDS, added in wave order.  XL: the tokens (16 at most) in LDS.
+template <int VT, int SPG, bool GLU, int RT, int CT, int NW, bool XL>
 __global__ __launch_bounds__(NW * 64) void w4_kernel(W4Args a) {
     static_assert(!GLU || RT % 2 == 0, "gate and up tiles in pairs");
+    static_assert(!XL || CT == 1, "one tile of tokens in LDS");
     constexpr int TR = GLU ? RT / 2 : RT;
     __shared__ __attribute__((aligned(16))) float red[NW][RT][256];
+    extern __shared__ __attribute__((aligned(16))) uint8_t xlds[];
     const int tid = threadIdx.x, lane = tid & 63;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int64_t f0 = (int64_t)blockIdx.x * (16 * TR);
     const int64_t t0 = (int64_t)blockIdx.y * (16 * CT);
+    const int nu = (a.width + 255) / 256;
     FewRows w[RT];
+    FewUnit<VT, SPG> cur[RT];
 #pragma unroll
     for (int i = 0; i < RT; ++i) {
         const int m = GLU ? i & 1 : 0;
@@ -124,19 +129,31 @@ __global__ __launch_bounds__(NW * 64) void w4_kernel(W4Args a) {
         // a tile past the last row re-reads the block's first one (its sums are not stored)
         r0 = r0 < a.R ? r0 : f0;
         w[i] = few_rows(a.codes[m], a.idx[m], a.scales[m], a.ldc, a.ldi, a.lds, r0, a.R, lane);
-    }
-    const uint16_t* xrow[CT];
-#pragma unroll
-    for (int j = 0; j < CT; ++j) {
-        const int64_t t = t0 + 16 * j + (lane & 15);
-        xrow[j] = a.X + (t < a.Mtok ? t : a.Mtok - 1) * a.ldx;
+        if (wave < nu) cur[i].load(w[i], wave, a.width, a.gshift, lane);
     }
     few_f32x4 acc[RT][CT];
 #pragma unroll
     for (int i = 0; i < RT; ++i)
 #pragma unroll
         for (int j = 0; j < CT; ++j) acc[i][j] = few_f32x4{0, 0, 0, 0};
-    few_product<VT, SPG, RT, CT>(w, xrow, wave, NW, (a.width + 255) / 256, a.width, a.gshift, a.Ns, lane, acc);
+    if constexpr (XL) {
+        const int stride = few_lds_row(a.width), chunks = nu * 32;
+        for (int t = 0; t < a.Mtok; ++t)
+            for (int c = tid; c < chunks; c += NW * 64)
+                *(few_u32x4*)(xlds + t * stride + 16 * c) = few_x8(a.X + t * a.ldx, 8 * c, a.width, a.lift);
+        __syncthreads();
+        const int t = (lane & 15) < a.Mtok ? lane & 15 : a.Mtok - 1;
+        const FewXLds x{xlds + t * stride};
+        few_product<VT, SPG, RT, CT>(cur, w, x, wave, NW, nu, a.width, a.gshift, a.lift, lane, acc);
+    } else {
+        FewXDirect<CT> x;
+#pragma unroll
+        for (int j = 0; j < CT; ++j) {
+            const int64_t t = t0 + 16 * j + (lane & 15);
+            x.row[j] = a.X + (t < a.Mtok ? t : a.Mtok - 1) * a.ldx;
+        }
+        few_product<VT, SPG, RT, CT>(cur, w, x, wave, NW, nu, a.width, a.gshift, a.lift, lane, acc);
+    }
 
 #pragma unroll
     for (int j = 0; j < CT; ++j) {
@@ -163,18 +180,21 @@ __global__ __launch_bounds__(NW * 64) void w4_kernel(W4Args a) {
     }
 }
 
-template <int VT, int SPG, bool GLU, int RT, int CT, int NW>
+template <int VT, int SPG, bool GLU, int RT, int CT, int NW, bool XL>
 static void w4_go(const W4Args& a, hipStream_t s) {
     constexpr int rows = 16 * (GLU ? RT / 2 : RT);
     const dim3 grid((unsigned)ceil_div(a.R, rows), (unsigned)ceil_div(a.Mtok, 16 * CT));
-    hipLaunchKernelGGL((w4_kernel<VT, SPG, GLU, RT, CT, NW>), grid, dim3(NW * 64), 0, s, a);
+    const size_t lds = XL ? (size_t)a.Mtok * few_lds_row(a.width) : 0;
+    hipLaunchKernelGGL((w4_kernel<VT, SPG, GLU, RT, CT, NW, XL>), grid, dim3(NW * 64), lds, s, a);
 }
 
 template <int VT, int SPG, bool GLU>
 static void w4_tokens(const W4Args& a, hipStream_t s) {
-    if (a.Mtok <= 16) w4_go<VT, SPG, GLU, 2, 1, 16>(a, s);
-    else if (a.Mtok <= 32) w4_go<VT, SPG, GLU, 2, 2, 8>(a, s);
-    else w4_go<VT, SPG, GLU, 2, 4, 8>(a, s);
+    constexpr int W = GLU ? 2 : 1;
+    if (a.Mtok <= 16 && (int64_t)a.Mtok * few_lds_row(a.width) <= 32 * 1024) w4_go<VT, SPG, GLU, 2 * W, 1, 16, true>(a, s);
+    else if (a.Mtok <= 16) w4_go<VT, SPG, GLU, 2 * W, 1, 16, false>(a, s);
+    else if (a.Mtok <= 32) w4_go<VT, SPG, GLU, W, 2, 16, false>(a, s);
+    else w4_go<VT, SPG, GLU, W, 4, 8, false>(a, s);
 }
 
 template <int VT, bool GLU>
@@ -189,7 +209,7 @@ nm_status launch_w4(const W4In& in, hipStream_t s) {
     a.X = in.X;
     a.ldx = in.ldx;
     a.Mtok = (int)in.Mtok;
-    a.Ns = in.Ns;
+    a.lift = few_lift(in.Ns);
     a.width = (int)(in.Ns ? in.K / (2 * in.Ns) * 4 * (in.Ns - 1) : in.K);
     a.gshift = in.group == 64 ? 6 : in.group == 128 ? 7 : 8;
     for (int m = 0; m < 2; ++m) {

@@ -82,10 +82,12 @@ struct FewRows {
     const uint32_t* idx;
     const uint16_t* scales;   // uniform: the tile's first row, group 0
     int64_t lds;
-    uint32_t voff, ioff;      // the lane's row and place within it, in bytes
-    int last;                 // rows of the tile - 1 (lanes past it re-read its last row)
+    uint32_t voff, ioff;      // the lane's row, in bytes
+    uint32_t soff;            // the lane's four output rows
 };
 
+// Lanes past the weight's last row re-read it; of the scales those of a run of four rows (the rows
+// of scales are long enough for whole runs).
 __device__ __forceinline__ FewRows few_rows(const void* vals, const uint32_t* idx, const void* scales, int64_t ldv_bytes,
                                             int64_t ldi, int64_t lds, int64_t r0, int64_t R, int lane) {
     FewRows w;
@@ -93,14 +95,18 @@ __device__ __forceinline__ FewRows few_rows(const void* vals, const uint32_t* id
     w.idx = idx + r0 * ldi;
     w.scales = (const uint16_t*)scales + r0;
     w.lds = lds;
-    w.last = (int)(R - r0 < 16 ? R - r0 - 1 : 15);
-    const int row = (lane & 15) < w.last ? (lane & 15) : w.last;
+    const int last = (int)(R - r0 < 16 ? R - r0 - 1 : 15), q = lane >> 4;
+    const int row = (lane & 15) < last ? (lane & 15) : last;
     w.voff = (uint32_t)(row * ldv_bytes);
     w.ioff = (uint32_t)(row * ldi * 4);
+    w.soff = 4u * (uint32_t)(q < last / 4 ? q : last / 4);
     return w;
 }
 
 // A unit (256 columns) of a tile's rows in registers.  SPG: steps that share a scale (1, 2, 4).
+// Columns past the weight's width meet zeros of X, so that what is loaded for them need only be
+// readable and finite: the row's last bytes again.  (Codes always are finite, and a row with a NaN
+// scale is NaN already; bf16 values are zeroed.)
 template <int VT, int SPG>
 struct FewUnit {
     static constexpr int NC = VT == kFewBF16 ? 16 : 4, NS = VT == kFewBF16 ? 1 : 4 / SPG;
@@ -110,71 +116,47 @@ struct FewUnit {
     // u: unit; width: the weight's (lifted) columns; gshift: log2 of the columns a scale serves
     __device__ __forceinline__ void load(const FewRows& w, int u, int width, int gshift, int lane) {
         const int q = lane >> 4;
+        const bool whole = u * 256 + 256 <= width;   // uniform
         if constexpr (VT != kFewBF16) {
+            const int at = u * 64 + q * 16, most = (width / 4 - 1) & ~15;
+            const uint4 v = *(const uint4*)(w.vals + (w.voff + (at < most ? at : most)));
+            c[0] = v.x;
+            c[1] = v.y;
+            c[2] = v.z;
+            c[3] = v.w;
+            const int last = (width - 1) >> gshift;
 #pragma unroll
             for (int k = 0; k < NS; ++k) {
                 const int g = (u * 256 + k * SPG * 64) >> gshift;
-                if (u * 256 + k * SPG * 64 < width) {
-                    const uint16_t* p = w.scales + g * w.lds;
-                    if (w.last == 15) {
-                        const uint2 v = *(const uint2*)(p + 4 * q);
-                        s[k][0] = v.x;
-                        s[k][1] = v.y;
-                    } else {
-                        uint32_t h[4];
-#pragma unroll
-                        for (int j = 0; j < 4; ++j) h[j] = p[4 * q + j < w.last ? 4 * q + j : w.last];
-                        s[k][0] = h[0] | h[1] << 16;
-                        s[k][1] = h[2] | h[3] << 16;
-                    }
-                } else {
-                    s[k][0] = s[k][1] = 0;
-                }
-            }
-        }
-        if (u * 256 + 256 <= width) {
-            const few_pair ip = *(const few_pair*)((const uint8_t*)w.idx + (w.ioff + u * 32 + q * 8));
-            i[0] = ip.a;
-            i[1] = ip.b;
-            if constexpr (VT == kFewBF16) {
-#pragma unroll
-                for (int t = 0; t < 4; ++t) {
-                    const uint4 v = *(const uint4*)(w.vals + (w.voff + u * 256 + t * 64 + q * 16));
-                    c[4 * t] = v.x;
-                    c[4 * t + 1] = v.y;
-                    c[4 * t + 2] = v.z;
-                    c[4 * t + 3] = v.w;
-                }
-            } else {
-                const uint4 v = *(const uint4*)(w.vals + (w.voff + u * 64 + q * 16));
-                c[0] = v.x;
-                c[1] = v.y;
-                c[2] = v.z;
-                c[3] = v.w;
+                const uint2 sv = *(const uint2*)(w.scales + (g < last ? g : last) * w.lds + w.soff);
+                s[k][0] = sv.x;
+                s[k][1] = sv.y;
             }
         } else {
-            // the row ends inside this unit, at a multiple of 16 columns: a lane's piece of a step is
-            // inside or past the end as a whole, and is loaded by itself
 #pragma unroll
             for (int t = 0; t < 4; ++t) {
                 const int col = u * 256 + t * 64 + q * 16;
-                const bool in = col < width;
-                i[t] = in ? *(const uint16_t*)((const uint8_t*)w.idx + (w.ioff + col / 8)) : 0u;
-                if constexpr (VT == kFewBF16) {
-                    const uint4 v = in ? *(const uint4*)(w.vals + (w.voff + col)) : make_uint4(0, 0, 0, 0);
-                    c[4 * t] = v.x;
-                    c[4 * t + 1] = v.y;
-                    c[4 * t + 2] = v.z;
-                    c[4 * t + 3] = v.w;
-                } else {
-                    c[t] = in ? *(const uint32_t*)(w.vals + (w.voff + col / 4)) : 0u;
-                }
+                uint4 v = *(const uint4*)(w.vals + (w.voff + (col < width ? col : width - 16)));
+                if (!whole && col >= width) v = make_uint4(0, 0, 0, 0);
+                c[4 * t] = v.x;
+                c[4 * t + 1] = v.y;
+                c[4 * t + 2] = v.z;
+                c[4 * t + 3] = v.w;
             }
+        }
+        const uint8_t* ip = (const uint8_t*)w.idx;
+        if (whole) {
+            const few_pair p = *(const few_pair*)(ip + (w.ioff + u * 32 + q * 8));
+            i[0] = p.a;
+            i[1] = p.b;
+        } else {
+            const int at = u * 8 + q * 2, most = (width - 1) / 32;
+            i[0] = *(const uint32_t*)(ip + (w.ioff + 4 * (at < most ? at : most)));
+            i[1] = *(const uint32_t*)(ip + (w.ioff + 4 * (at + 1 < most ? at + 1 : most)));
         }
     }
     // the loaded words in the operands' order (once, after load)
-    __device__ __forceinline__ void order(int u, int width, int lane) {
-        if (u * 256 + 256 > width) return;
+    __device__ __forceinline__ void order(int lane) {
         if constexpr (VT != kFewBF16) {
             few_swap32(c[0], c[2]);
             few_swap32(c[1], c[3]);
@@ -199,67 +181,93 @@ struct FewUnit {
     }
 };
 
-// 8 (lifted) columns of a token's row of X, from column col of the width: zeros past its end.
+// The division of a window's number by Ns - 1, as a product: exact below 2^29.
+struct FewLift {
+    int Ns;
+    uint32_t magic;   // ceil(2^32 / (Ns - 1))
+};
+inline FewLift few_lift(int Ns) { return FewLift{Ns, Ns ? (uint32_t)(((1ull << 32) + (uint32_t)Ns - 2) / (uint32_t)(Ns - 1)) : 0u}; }
+
+// 8 (lifted) columns of a token's row of X, from column col of the width: zeros past its end (the load
+// itself goes to the row's last columns then, so that no branch is around it).
 // A lifted column 4 w + l of window w is original column 2 Ns (w / (Ns - 1)) + 2 (w % (Ns - 1)) + l.
-__device__ __forceinline__ few_u32x4 few_x8(const uint16_t* xrow, int col, int width, int Ns) {
-    if (col >= width) return few_u32x4{0, 0, 0, 0};
-    if (Ns == 0) {
-        const uint4 v = *(const uint4*)(xrow + col);
-        return few_u32x4{v.x, v.y, v.z, v.w};
+__device__ __forceinline__ few_u32x4 few_x8(const uint16_t* xrow, int col, int width, const FewLift& f) {
+    const int at = col < width ? col : width - 8;
+    few_u32x4 r;
+    if (f.Ns == 0) {
+        const uint4 v = *(const uint4*)(xrow + at);
+        r = few_u32x4{v.x, v.y, v.z, v.w};
+    } else {
+        // window w starts at 2 Ns g + 2 (w - (Ns - 1) g) = 2 (w + g), g = w / (Ns - 1)
+        const uint32_t win = (uint32_t)at >> 2;
+        const uint32_t g0 = __umulhi(win, f.magic), g1 = __umulhi(win + 1, f.magic);
+        const few_pair a = *(const few_pair*)(xrow + 2 * (win + g0)), b = *(const few_pair*)(xrow + 2 * (win + 1 + g1));
+        r = few_u32x4{a.a, a.b, b.a, b.b};
     }
-    const uint32_t win = (uint32_t)col >> 2, d = (uint32_t)(Ns - 1);
-    const uint32_t g0 = win / d, r0 = win - g0 * d, g1 = (win + 1) / d, r1 = win + 1 - g1 * d;
-    const few_pair a = *(const few_pair*)(xrow + 2 * (Ns * g0 + r0)), b = *(const few_pair*)(xrow + 2 * (Ns * g1 + r1));
-    return few_u32x4{a.a, a.b, b.a, b.b};
+    return col < width ? r : few_u32x4{0, 0, 0, 0};
 }
 
-// acc[i][j] += rows i (16 each) times tokens j (16 each), over units u0, u0 + du, ... < nu.
-template <int VT, int SPG, int RT, int CT>
-__device__ __forceinline__ void few_product(const FewRows (&w)[RT], const uint16_t* const (&xrow)[CT], int u0, int du, int nu,
-                                            int width, int gshift, int Ns, int lane, few_f32x4 (&acc)[RT][CT]) {
-    const int q = lane >> 4;
-    FewUnit<VT, SPG> cur[RT];
-    if (u0 < nu) {
-#pragma unroll
-        for (int i = 0; i < RT; ++i) cur[i].load(w[i], u0, width, gshift, lane);
+// Where a wave's activation fragments come from.
+// FewXDirect: the tokens' rows in memory (16 CT tokens; each load is whole lines of 16 rows).
+template <int CT>
+struct FewXDirect {
+    const uint16_t* row[CT];   // the lane's tokens
+    __device__ __forceinline__ few_u32x8 frag(int j, int col, int width, const FewLift& f) const {
+        const few_u32x4 lo = few_x8(row[j], col, width, f), hi = few_x8(row[j], col + 32, width, f);
+        return __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
     }
+};
+// FewXLds: the (lifted) rows of up to 16 tokens in LDS, zeros up to a whole unit.  With one token the
+// 64 lanes of a load want 64 bytes of memory, and the address unit still spends the time of 1 KB: from
+// LDS they are a broadcast.
+struct FewXLds {
+    const uint8_t* row;        // the lane's token
+    __device__ __forceinline__ few_u32x8 frag(int, int col, int, const FewLift&) const {
+        const few_u32x4 lo = *(const few_u32x4*)(row + 2 * col), hi = *(const few_u32x4*)(row + 2 * col + 64);
+        return __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
+    }
+};
+// bytes of a token's row in LDS: whole units, and 16 more so that 16 tokens' reads hit distinct banks
+__host__ __device__ __forceinline__ int few_lds_row(int width) { return (width + 255) / 256 * 512 + 16; }
+
+// acc[i][j] += rows i (16 each) times tokens j (16 each), over units u0, u0 + du, ... < nu.
+// cur holds unit u0 (loaded by the caller, who may have more to do while it is on its way).
+template <int VT, int SPG, int RT, int CT, typename XF>
+__device__ __forceinline__ void few_product(FewUnit<VT, SPG> (&cur)[RT], const FewRows (&w)[RT], const XF& x, int u0, int du, int nu,
+                                            int width, int gshift, const FewLift& lift, int lane, few_f32x4 (&acc)[RT][CT]) {
+    const int q = lane >> 4;
     for (int u = u0; u < nu; u += du) {
-        few_u32x8 x[4][CT];
-#pragma unroll
-        for (int t = 0; t < 4; ++t)
-#pragma unroll
-            for (int j = 0; j < CT; ++j) {
-                const int col = u * 256 + t * 64 + q * 8;
-                const few_u32x4 lo = few_x8(xrow[j], col, width, Ns), hi = few_x8(xrow[j], col + 32, width, Ns);
-                x[t][j] = __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
-            }
         FewUnit<VT, SPG> next[RT];
         if (u + du < nu) {
 #pragma unroll
             for (int i = 0; i < RT; ++i) next[i].load(w[i], u + du, width, gshift, lane);
         }
 #pragma unroll
-        for (int i = 0; i < RT; ++i) {
-            cur[i].order(u, width, lane);
-            few_f32x4 d[CT];
+        for (int i = 0; i < RT; ++i) cur[i].order(lane);
+        few_f32x4 d[RT][CT];
 #pragma unroll
-            for (int t = 0; t < 4; ++t) {
+        for (int t = 0; t < 4; ++t) {
+            few_u32x8 b[CT];
+#pragma unroll
+            for (int j = 0; j < CT; ++j) b[j] = x.frag(j, u * 256 + t * 64 + q * 8, width, lift);
+#pragma unroll
+            for (int i = 0; i < RT; ++i) {
                 const few_bf16x8 a = cur[i].values(t);
 #pragma unroll
                 for (int j = 0; j < CT; ++j) {
                     if constexpr (VT == kFewBF16) {
-                        acc[i][j] = __builtin_amdgcn_smfmac_f32_16x16x64_bf16(a, __builtin_bit_cast(few_bf16x16, x[t][j]),
-                                                                              acc[i][j], (int)cur[i].i[t], 0, 0);
+                        acc[i][j] = __builtin_amdgcn_smfmac_f32_16x16x64_bf16(a, __builtin_bit_cast(few_bf16x16, b[j]), acc[i][j],
+                                                                              (int)cur[i].i[t], 0, 0);
                     } else {
-                        if (t % SPG == 0) d[j] = few_f32x4{0, 0, 0, 0};
-                        d[j] = __builtin_amdgcn_smfmac_f32_16x16x64_bf16(a, __builtin_bit_cast(few_bf16x16, x[t][j]), d[j],
-                                                                         (int)cur[i].i[t], 0, 0);
+                        if (t % SPG == 0) d[i][j] = few_f32x4{0, 0, 0, 0};
+                        d[i][j] = __builtin_amdgcn_smfmac_f32_16x16x64_bf16(a, __builtin_bit_cast(few_bf16x16, b[j]), d[i][j],
+                                                                            (int)cur[i].i[t], 0, 0);
                         if (t % SPG == SPG - 1) {
                             const uint32_t s0 = cur[i].s[t / SPG][0], s1 = cur[i].s[t / SPG][1];
                             const float s[4] = {__uint_as_float(s0 << 16), __uint_as_float(s0 & 0xffff0000u),
                                                 __uint_as_float(s1 << 16), __uint_as_float(s1 & 0xffff0000u)};
 #pragma unroll
-                            for (int k = 0; k < 4; ++k) acc[i][j][k] = __builtin_fmaf(s[k], d[j][k], acc[i][j][k]);
+                            for (int k = 0; k < 4; ++k) acc[i][j][k] = __builtin_fmaf(s[k], d[i][j][k], acc[i][j][k]);
                         }
                     }
                 }
