@@ -217,7 +217,7 @@ __device__ __forceinline__ int moe_pairs(const int32_t* sel, int pairs, int e, i
 }
 
 // RT: tiles of 16 rows of a task, gate and up beside each other.  XL: the tokens in LDS.
-template <int VT, int SPG, int RT, int NW, bool XL>
+template <int VT, int SPG, int RT, int NW, bool XL, bool LIFT>
 __global__ __launch_bounds__(NW * 64) void moe_up_kernel(MoeArgs a, int tiles, int blocks) {
     constexpr int TR = RT / 2;   // feature tiles of a task
     __shared__ __attribute__((aligned(16))) float red[NW][RT][256];
@@ -230,9 +230,9 @@ __global__ __launch_bounds__(NW * 64) void moe_up_kernel(MoeArgs a, int tiles, i
     const int nu = (a.wK + 255) / 256, pairs = a.T * a.topk, stride = few_lds_row(a.wK);
     if (tid < kMoeExperts / 64) used[tid] = 0;
     if constexpr (XL) {
-        for (int t = 0; t < a.T; ++t)
-            for (int c = tid; c < nu * 32; c += NW * 64)
-                *(few_u32x4*)(xlds + t * stride + 16 * c) = few_x8(a.X + t * a.ldx, 8 * c, a.wK, a.lift);
+        FewStage<NW * 64> stage;
+        stage.load(a.X, a.ldx, a.T, a.wK, a.lift, xlds, tid);
+        stage.store(a.T, a.wK, xlds, tid);
     }
     if (a.E <= 64) moe_route<1>(a, sel, wts, tid, NW);
     else if (a.E <= 128) moe_route<2>(a, sel, wts, tid, NW);
@@ -263,7 +263,7 @@ __global__ __launch_bounds__(NW * 64) void moe_up_kernel(MoeArgs a, int tiles, i
             const int64_t r0 = f0 + 16 * (i / 2) < a.F ? f0 + 16 * (i / 2) : f0;
             w[i] = few_rows((const uint8_t*)x.vals + e * x.es_vals, x.idx + e * x.es_idx, (const uint16_t*)x.scales + e * x.es_scales,
                             x.ld_vals, x.ld_idx, x.ld_scales, r0, a.F, lane);
-            if (wave < nu) cur[i].load(w[i], wave, a.wK, a.gshift, lane);
+            cur[i].load(w[i], wave < nu ? wave : 0, a.wK, a.gshift, lane);
         }
     };
     start(blockIdx.x);
@@ -280,14 +280,13 @@ __global__ __launch_bounds__(NW * 64) void moe_up_kernel(MoeArgs a, int tiles, i
             for (int i = 0; i < RT; ++i) acc[i][0] = few_f32x4{0, 0, 0, 0};
             if (c) {   // the expert's next 16 tokens: its rows again
 #pragma unroll
-                for (int i = 0; i < RT; ++i)
-                    if (wave < nu) cur[i].load(w[i], wave, a.wK, a.gshift, lane);
+                for (int i = 0; i < RT; ++i) cur[i].load(w[i], wave < nu ? wave : 0, a.wK, a.gshift, lane);
             }
             if constexpr (XL) {
                 const FewXLds x{xlds + pair / a.topk * stride};
                 few_product<VT, SPG, RT, 1>(cur, w, x, wave, NW, nu, a.wK, a.gshift, a.lift, lane, acc);
             } else {
-                const FewXDirect<1> x{{a.X + (int64_t)(pair / a.topk) * a.ldx}};
+                const FewXDirect<1, LIFT> x{{a.X + (int64_t)(pair / a.topk) * a.ldx}};
                 few_product<VT, SPG, RT, 1>(cur, w, x, wave, NW, nu, a.wK, a.gshift, a.lift, lane, acc);
             }
             if (last) start(task + blocks);
@@ -318,7 +317,7 @@ __global__ __launch_bounds__(NW * 64) void moe_up_kernel(MoeArgs a, int tiles, i
 // ------------------------------------------------------------------ down
 // grid: x tiles of 16 output columns.  Wave work items are (picked expert, slice of its width); a
 // pair's partial sums stay in LDS per slice, weighted, and are added up token by token.
-template <int VT, int SPG, int NW>
+template <int VT, int SPG, int NW, bool LIFT>
 __global__ __launch_bounds__(NW * 64) void moe_down_kernel(MoeArgs a, int slices) {
     extern __shared__ __attribute__((aligned(16))) float part[];   // [slices][pairs][16]
     __shared__ int32_t sel[kMoeTokens * kMoeTopk];
@@ -348,7 +347,7 @@ __global__ __launch_bounds__(NW * 64) void moe_down_kernel(MoeArgs a, int slices
             int mine;
             const int left = moe_pairs(sel, pairs, e, c, lane, mine);
             const int pair = mine >= 0 ? mine : __shfl(mine, 0);
-            const FewXDirect<1> x{{a.H + (int64_t)pair * a.ldh}};
+            const FewXDirect<1, LIFT> x{{a.H + (int64_t)pair * a.ldh}};
             few_f32x4 acc[1][1] = {{few_f32x4{0, 0, 0, 0}}};
             few_product<VT, SPG, 1, 1>(cur, w, x, sl, slices, units, a.wF, a.gshift, a.lift, lane, acc);
             if (mine >= 0) {
@@ -390,8 +389,8 @@ size_t moe_ws(int64_t T, int64_t K, int64_t F, int E, int topk) {
     return up((size_t)kMoeSplit * T * E * 4) + up((size_t)T * topk * ((F + 7) / 8 * 8) * 2) + 2 * up((size_t)T * topk * 4);
 }
 
-template <int VT, int SPG>
-static nm_status moe_go(const MoeArgs& a, hipStream_t s) {
+template <int VT, int SPG, bool LIFT>
+static nm_status moe_run(const MoeArgs& a, hipStream_t s) {
     const int pairs = a.T * a.topk, picked = pairs < a.E ? pairs : a.E;
     hipLaunchKernelGGL(moe_logits_kernel, dim3((a.E + 15) / 16, (a.T + 15) / 16, a.ksplit), dim3(256), 0, s, a);
     // two feature tiles of a 4-bit weight a task (a unit of its rows is a third of a bf16 one's)
@@ -401,18 +400,23 @@ static nm_status moe_go(const MoeArgs& a, hipStream_t s) {
     const int blocks = (int)(tasks < 512 ? tasks : 512);
     const int64_t xbytes = (int64_t)a.T * few_lds_row(a.wK);
     if (xbytes <= 32 * 1024)
-        hipLaunchKernelGGL((moe_up_kernel<VT, SPG, RT, NW, true>), dim3(blocks), dim3(NW * 64), (size_t)xbytes, s, a, tiles, blocks);
+        hipLaunchKernelGGL((moe_up_kernel<VT, SPG, RT, NW, true, false>), dim3(blocks), dim3(NW * 64), (size_t)xbytes, s, a, tiles, blocks);
     else
-        hipLaunchKernelGGL((moe_up_kernel<VT, SPG, RT, NW, false>), dim3(blocks), dim3(NW * 64), 0, s, a, tiles, blocks);
+        hipLaunchKernelGGL((moe_up_kernel<VT, SPG, RT, NW, false, LIFT>), dim3(blocks), dim3(NW * 64), 0, s, a, tiles, blocks);
     // slices of an expert's width: so many that every wave of a block has one where few experts are
     // picked, as long as the partial sums fit
     int slices = (kMoeWaves + picked - 1) / picked;
     const int units = (a.wF + 255) / 256;
     if (slices > units) slices = units;
     while (slices > 1 && slices * pairs > 1024) --slices;
-    hipLaunchKernelGGL((moe_down_kernel<VT, SPG, kMoeWaves>), dim3((a.K + 15) / 16), dim3(kMoeWaves * 64),
+    hipLaunchKernelGGL((moe_down_kernel<VT, SPG, kMoeWaves, LIFT>), dim3((a.K + 15) / 16), dim3(kMoeWaves * 64),
                        (size_t)slices * pairs * 64, s, a, slices);
     return check_launch("nm_moe");
+}
+
+template <int VT, int SPG>
+static nm_status moe_go(const MoeArgs& a, hipStream_t s) {
+    return a.lift.Ns ? moe_run<VT, SPG, true>(a, s) : moe_run<VT, SPG, false>(a, s);
 }
 
 nm_status launch_moe(const MoeIn& in, void* ws, hipStream_t s) {
@@ -460,8 +464,8 @@ nm_status launch_moe(const MoeIn& in, void* ws, hipStream_t s) {
     a.ldy = in.ldy;
     a.y32 = in.ydt == NM_F32;
     if (in.vdt == NM_BF16) return moe_go<kFewBF16, 1>(a, s);
-    if (in.vdt == NM_I4) return a.gshift == 6 ? moe_go<kFewI4, 1>(a, s) : a.gshift == 7 ? moe_go<kFewI4, 2>(a, s) : moe_go<kFewI4, 4>(a, s);
-    return a.gshift == 6 ? moe_go<kFewFP4, 1>(a, s) : a.gshift == 7 ? moe_go<kFewFP4, 2>(a, s) : moe_go<kFewFP4, 4>(a, s);
+    if (in.vdt == NM_I4) return a.gshift == 6 ? moe_go<kFewI4, 1>(a, s) : moe_go<kFewI4, 2>(a, s);
+    return a.gshift == 6 ? moe_go<kFewFP4, 1>(a, s) : moe_go<kFewFP4, 2>(a, s);
 }
 
 }  // namespace nm

@@ -108,7 +108,7 @@ struct W4Args {
 // A block of NW waves owns RT tiles of 16 rows (GLU: RT / 2 tiles of 16 features, gate and up
 // beside each other) and 16 CT tokens.  Its waves take units of 256 columns in turn and their sums
 // meet in LDS, added in wave order.  XL: the tokens (16 at most) in LDS.
-template <int VT, int SPG, bool GLU, int RT, int CT, int NW, bool XL>
+template <int VT, int SPG, bool GLU, int RT, int CT, int NW, bool XL, bool LIFT>
 __global__ __launch_bounds__(NW * 64) void w4_kernel(W4Args a) {
     static_assert(!GLU || RT % 2 == 0, "gate and up tiles in pairs");
     static_assert(!XL || CT == 1, "one tile of tokens in LDS");
@@ -122,6 +122,8 @@ __global__ __launch_bounds__(NW * 64) void w4_kernel(W4Args a) {
     const int nu = (a.width + 255) / 256;
     FewRows w[RT];
     FewUnit<VT, SPG> cur[RT];
+    FewStage<NW * 64> stage;
+    if constexpr (XL) stage.load(a.X, a.ldx, a.Mtok, a.width, a.lift, xlds, tid);
 #pragma unroll
     for (int i = 0; i < RT; ++i) {
         const int m = GLU ? i & 1 : 0;
@@ -129,7 +131,7 @@ __global__ __launch_bounds__(NW * 64) void w4_kernel(W4Args a) {
         // a tile past the last row re-reads the block's first one (its sums are not stored)
         r0 = r0 < a.R ? r0 : f0;
         w[i] = few_rows(a.codes[m], a.idx[m], a.scales[m], a.ldc, a.ldi, a.lds, r0, a.R, lane);
-        if (wave < nu) cur[i].load(w[i], wave, a.width, a.gshift, lane);
+        cur[i].load(w[i], wave < nu ? wave : 0, a.width, a.gshift, lane);
     }
     few_f32x4 acc[RT][CT];
 #pragma unroll
@@ -137,16 +139,14 @@ __global__ __launch_bounds__(NW * 64) void w4_kernel(W4Args a) {
 #pragma unroll
         for (int j = 0; j < CT; ++j) acc[i][j] = few_f32x4{0, 0, 0, 0};
     if constexpr (XL) {
-        const int stride = few_lds_row(a.width), chunks = nu * 32;
-        for (int t = 0; t < a.Mtok; ++t)
-            for (int c = tid; c < chunks; c += NW * 64)
-                *(few_u32x4*)(xlds + t * stride + 16 * c) = few_x8(a.X + t * a.ldx, 8 * c, a.width, a.lift);
+        const int stride = few_lds_row(a.width);
+        stage.store(a.Mtok, a.width, xlds, tid);
         __syncthreads();
         const int t = (lane & 15) < a.Mtok ? lane & 15 : a.Mtok - 1;
         const FewXLds x{xlds + t * stride};
         few_product<VT, SPG, RT, CT>(cur, w, x, wave, NW, nu, a.width, a.gshift, a.lift, lane, acc);
     } else {
-        FewXDirect<CT> x;
+        FewXDirect<CT, LIFT> x;
 #pragma unroll
         for (int j = 0; j < CT; ++j) {
             const int64_t t = t0 + 16 * j + (lane & 15);
@@ -180,28 +180,35 @@ __global__ __launch_bounds__(NW * 64) void w4_kernel(W4Args a) {
     }
 }
 
-template <int VT, int SPG, bool GLU, int RT, int CT, int NW, bool XL>
+template <int VT, int SPG, bool GLU, int RT, int CT, int NW, bool XL, bool LIFT>
 static void w4_go(const W4Args& a, hipStream_t s) {
     constexpr int rows = 16 * (GLU ? RT / 2 : RT);
     const dim3 grid((unsigned)ceil_div(a.R, rows), (unsigned)ceil_div(a.Mtok, 16 * CT));
     const size_t lds = XL ? (size_t)a.Mtok * few_lds_row(a.width) : 0;
-    hipLaunchKernelGGL((w4_kernel<VT, SPG, GLU, RT, CT, NW, XL>), grid, dim3(NW * 64), lds, s, a);
+    hipLaunchKernelGGL((w4_kernel<VT, SPG, GLU, RT, CT, NW, XL, LIFT>), grid, dim3(NW * 64), lds, s, a);
+}
+
+template <int VT, int SPG, bool GLU, bool LIFT>
+static void w4_tokens(const W4Args& a, hipStream_t s) {
+    constexpr int W = GLU ? 2 : 1;
+    if (a.Mtok <= 16) w4_go<VT, SPG, GLU, 2 * W, 1, 8, false, LIFT>(a, s);
+    else if (a.Mtok <= 32) w4_go<VT, SPG, GLU, 2, 2, 8, false, LIFT>(a, s);
+    else if (a.Mtok <= 48) w4_go<VT, SPG, GLU, 2, 3, 8, false, LIFT>(a, s);
+    else w4_go<VT, SPG, GLU, 2, 4, 8, false, LIFT>(a, s);
 }
 
 template <int VT, int SPG, bool GLU>
-static void w4_tokens(const W4Args& a, hipStream_t s) {
+static void w4_lift(const W4Args& a, hipStream_t s) {
     constexpr int W = GLU ? 2 : 1;
-    if (a.Mtok <= 16 && (int64_t)a.Mtok * few_lds_row(a.width) <= 32 * 1024) w4_go<VT, SPG, GLU, 2 * W, 1, 16, true>(a, s);
-    else if (a.Mtok <= 16) w4_go<VT, SPG, GLU, 2 * W, 1, 16, false>(a, s);
-    else if (a.Mtok <= 32) w4_go<VT, SPG, GLU, W, 2, 16, false>(a, s);
-    else w4_go<VT, SPG, GLU, W, 4, 8, false>(a, s);
+    if (a.Mtok <= 16 && (int64_t)a.Mtok * few_lds_row(a.width) <= 32 * 1024) w4_go<VT, SPG, GLU, W, 1, 4, true, false>(a, s);
+    else if (a.lift.Ns) w4_tokens<VT, SPG, GLU, true>(a, s);
+    else w4_tokens<VT, SPG, GLU, false>(a, s);
 }
 
 template <int VT, bool GLU>
 static void w4_group(const W4Args& a, hipStream_t s) {
-    if (a.gshift == 6) w4_tokens<VT, 1, GLU>(a, s);
-    else if (a.gshift == 7) w4_tokens<VT, 2, GLU>(a, s);
-    else w4_tokens<VT, 4, GLU>(a, s);
+    if (a.gshift == 6) w4_lift<VT, 1, GLU>(a, s);
+    else w4_lift<VT, 2, GLU>(a, s);
 }
 
 nm_status launch_w4(const W4In& in, hipStream_t s) {

@@ -15,6 +15,8 @@
 // would take four times the instructions for the same lines.
 #pragma once
 
+#include <type_traits>
+
 #include "nm_internal.h"
 
 namespace nm {
@@ -103,10 +105,12 @@ __device__ __forceinline__ FewRows few_rows(const void* vals, const uint32_t* id
     return w;
 }
 
-// A unit (256 columns) of a tile's rows in registers.  SPG: steps that share a scale (1, 2, 4).
+// A unit (256 columns) of a tile's rows in registers.  SPG: steps that share a scale (1, 2; groups of
+// 256 columns load theirs twice a unit).
 // Columns past the weight's width meet zeros of X, so that what is loaded for them need only be
 // readable and finite: the row's last bytes again.  (Codes always are finite, and a row with a NaN
-// scale is NaN already; bf16 values are zeroed.)
+// scale is NaN already; bf16 values are zeroed.)  No load is behind a branch, so that the compiler
+// counts those in flight and waits for none too many.
 template <int VT, int SPG>
 struct FewUnit {
     static constexpr int NC = VT == kFewBF16 ? 16 : 4, NS = VT == kFewBF16 ? 1 : 4 / SPG;
@@ -116,7 +120,6 @@ struct FewUnit {
     // u: unit; width: the weight's (lifted) columns; gshift: log2 of the columns a scale serves
     __device__ __forceinline__ void load(const FewRows& w, int u, int width, int gshift, int lane) {
         const int q = lane >> 4;
-        const bool whole = u * 256 + 256 <= width;   // uniform
         if constexpr (VT != kFewBF16) {
             const int at = u * 64 + q * 16, most = (width / 4 - 1) & ~15;
             const uint4 v = *(const uint4*)(w.vals + (w.voff + (at < most ? at : most)));
@@ -137,7 +140,7 @@ struct FewUnit {
             for (int t = 0; t < 4; ++t) {
                 const int col = u * 256 + t * 64 + q * 16;
                 uint4 v = *(const uint4*)(w.vals + (w.voff + (col < width ? col : width - 16)));
-                if (!whole && col >= width) v = make_uint4(0, 0, 0, 0);
+                if (col >= width) v = make_uint4(0, 0, 0, 0);
                 c[4 * t] = v.x;
                 c[4 * t + 1] = v.y;
                 c[4 * t + 2] = v.z;
@@ -145,15 +148,9 @@ struct FewUnit {
             }
         }
         const uint8_t* ip = (const uint8_t*)w.idx;
-        if (whole) {
-            const few_pair p = *(const few_pair*)(ip + (w.ioff + u * 32 + q * 8));
-            i[0] = p.a;
-            i[1] = p.b;
-        } else {
-            const int at = u * 8 + q * 2, most = (width - 1) / 32;
-            i[0] = *(const uint32_t*)(ip + (w.ioff + 4 * (at < most ? at : most)));
-            i[1] = *(const uint32_t*)(ip + (w.ioff + 4 * (at + 1 < most ? at + 1 : most)));
-        }
+        const int word = u * 8 + q * 2, most = (width - 1) / 32;
+        i[0] = *(const uint32_t*)(ip + (w.ioff + 4 * (word < most ? word : most)));
+        i[1] = *(const uint32_t*)(ip + (w.ioff + 4 * (word + 1 < most ? word + 1 : most)));
     }
     // the loaded words in the operands' order (once, after load)
     __device__ __forceinline__ void order(int lane) {
@@ -191,10 +188,11 @@ inline FewLift few_lift(int Ns) { return FewLift{Ns, Ns ? (uint32_t)(((1ull << 3
 // 8 (lifted) columns of a token's row of X, from column col of the width: zeros past its end (the load
 // itself goes to the row's last columns then, so that no branch is around it).
 // A lifted column 4 w + l of window w is original column 2 Ns (w / (Ns - 1)) + 2 (w % (Ns - 1)) + l.
+template <bool LIFT>
 __device__ __forceinline__ few_u32x4 few_x8(const uint16_t* xrow, int col, int width, const FewLift& f) {
     const int at = col < width ? col : width - 8;
     few_u32x4 r;
-    if (f.Ns == 0) {
+    if constexpr (!LIFT) {
         const uint4 v = *(const uint4*)(xrow + at);
         r = few_u32x4{v.x, v.y, v.z, v.w};
     } else {
@@ -207,13 +205,14 @@ __device__ __forceinline__ few_u32x4 few_x8(const uint16_t* xrow, int col, int w
     return col < width ? r : few_u32x4{0, 0, 0, 0};
 }
 
-// Where a wave's activation fragments come from.
+// Where a wave's activation fragments come from; AHEAD: loads in flight that the multiplications wait for.
 // FewXDirect: the tokens' rows in memory (16 CT tokens; each load is whole lines of 16 rows).
-template <int CT>
+template <int CT, bool LIFT>
 struct FewXDirect {
+    static constexpr bool AHEAD = true;
     const uint16_t* row[CT];   // the lane's tokens
     __device__ __forceinline__ few_u32x8 frag(int j, int col, int width, const FewLift& f) const {
-        const few_u32x4 lo = few_x8(row[j], col, width, f), hi = few_x8(row[j], col + 32, width, f);
+        const few_u32x4 lo = few_x8<LIFT>(row[j], col, width, f), hi = few_x8<LIFT>(row[j], col + 32, width, f);
         return __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
     }
 };
@@ -221,6 +220,7 @@ struct FewXDirect {
 // 64 lanes of a load want 64 bytes of memory, and the address unit still spends the time of 1 KB: from
 // LDS they are a broadcast.
 struct FewXLds {
+    static constexpr bool AHEAD = false;
     const uint8_t* row;        // the lane's token
     __device__ __forceinline__ few_u32x8 frag(int, int col, int, const FewLift&) const {
         const few_u32x4 lo = *(const few_u32x4*)(row + 2 * col), hi = *(const few_u32x4*)(row + 2 * col + 64);
@@ -230,54 +230,103 @@ struct FewXLds {
 // bytes of a token's row in LDS: whole units, and 16 more so that 16 tokens' reads hit distinct banks
 __host__ __device__ __forceinline__ int few_lds_row(int width) { return (width + 255) / 256 * 512 + 16; }
 
-// acc[i][j] += rows i (16 each) times tokens j (16 each), over units u0, u0 + du, ... < nu.
-// cur holds unit u0 (loaded by the caller, who may have more to do while it is on its way).
+// Units u0, u0 + du, ... < nu: acc[i][j] += rows i (16 each) times tokens j (16 each).  cur holds
+// unit u0 (loaded by the caller, who may have more to do while it is on its way).
+// Loads return in order, so what is waited for first is issued first: a unit's activations (in two
+// halves where 16 CT tokens' would take too many registers), then the next unit's weight, then the
+// multiplications, which leave the weight in flight.
 template <int VT, int SPG, int RT, int CT, typename XF>
 __device__ __forceinline__ void few_product(FewUnit<VT, SPG> (&cur)[RT], const FewRows (&w)[RT], const XF& x, int u0, int du, int nu,
                                             int width, int gshift, const FewLift& lift, int lane, few_f32x4 (&acc)[RT][CT]) {
+    constexpr int BATCH = CT <= 2 ? 4 : 2;   // steps
     const int q = lane >> 4;
-    for (int u = u0; u < nu; u += du) {
-        FewUnit<VT, SPG> next[RT];
-        if (u + du < nu) {
-#pragma unroll
-            for (int i = 0; i < RT; ++i) next[i].load(w[i], u + du, width, gshift, lane);
-        }
-#pragma unroll
-        for (int i = 0; i < RT; ++i) cur[i].order(lane);
+    if (u0 >= nu) return;
+    FewUnit<VT, SPG> next[RT];
+    auto unit = [&](int u, auto more) __attribute__((always_inline)) {
         few_f32x4 d[RT][CT];
 #pragma unroll
-        for (int t = 0; t < 4; ++t) {
-            few_u32x8 b[CT];
+        for (int t0 = 0; t0 < 4; t0 += BATCH) {
+            few_u32x8 b[BATCH][CT];
 #pragma unroll
-            for (int j = 0; j < CT; ++j) b[j] = x.frag(j, u * 256 + t * 64 + q * 8, width, lift);
+            for (int t = 0; t < BATCH; ++t)
 #pragma unroll
-            for (int i = 0; i < RT; ++i) {
-                const few_bf16x8 a = cur[i].values(t);
+                for (int j = 0; j < CT; ++j) b[t][j] = x.frag(j, u * 256 + (t0 + t) * 64 + q * 8, width, lift);
+            if constexpr (decltype(more)::value) {
+                if (t0 + BATCH == 4) {
 #pragma unroll
-                for (int j = 0; j < CT; ++j) {
-                    if constexpr (VT == kFewBF16) {
-                        acc[i][j] = __builtin_amdgcn_smfmac_f32_16x16x64_bf16(a, __builtin_bit_cast(few_bf16x16, b[j]), acc[i][j],
-                                                                              (int)cur[i].i[t], 0, 0);
-                    } else {
-                        if (t % SPG == 0) d[i][j] = few_f32x4{0, 0, 0, 0};
-                        d[i][j] = __builtin_amdgcn_smfmac_f32_16x16x64_bf16(a, __builtin_bit_cast(few_bf16x16, b[j]), d[i][j],
-                                                                            (int)cur[i].i[t], 0, 0);
-                        if (t % SPG == SPG - 1) {
-                            const uint32_t s0 = cur[i].s[t / SPG][0], s1 = cur[i].s[t / SPG][1];
-                            const float s[4] = {__uint_as_float(s0 << 16), __uint_as_float(s0 & 0xffff0000u),
-                                                __uint_as_float(s1 << 16), __uint_as_float(s1 & 0xffff0000u)};
+                    for (int i = 0; i < RT; ++i) next[i].load(w[i], u + du, width, gshift, lane);
+                }
+            }
+            if constexpr (XF::AHEAD) __builtin_amdgcn_sched_barrier(0);
+            if (t0 == 0) {
 #pragma unroll
-                            for (int k = 0; k < 4; ++k) acc[i][j][k] = __builtin_fmaf(s[k], d[i][j][k], acc[i][j][k]);
+                for (int i = 0; i < RT; ++i) cur[i].order(lane);
+            }
+#pragma unroll
+            for (int t = t0; t < t0 + BATCH; ++t)
+#pragma unroll
+                for (int i = 0; i < RT; ++i) {
+                    const few_bf16x8 a = cur[i].values(t);
+#pragma unroll
+                    for (int j = 0; j < CT; ++j) {
+                        const few_bf16x16 bj = __builtin_bit_cast(few_bf16x16, b[t - t0][j]);
+                        if constexpr (VT == kFewBF16) {
+                            acc[i][j] = __builtin_amdgcn_smfmac_f32_16x16x64_bf16(a, bj, acc[i][j], (int)cur[i].i[t], 0, 0);
+                        } else {
+                            if (t % SPG == 0) d[i][j] = few_f32x4{0, 0, 0, 0};
+                            d[i][j] = __builtin_amdgcn_smfmac_f32_16x16x64_bf16(a, bj, d[i][j], (int)cur[i].i[t], 0, 0);
+                            if (t % SPG == SPG - 1) {
+                                const uint32_t s0 = cur[i].s[t / SPG][0], s1 = cur[i].s[t / SPG][1];
+                                const float s[4] = {__uint_as_float(s0 << 16), __uint_as_float(s0 & 0xffff0000u),
+                                                    __uint_as_float(s1 << 16), __uint_as_float(s1 & 0xffff0000u)};
+#pragma unroll
+                                for (int k = 0; k < 4; ++k) acc[i][j][k] = __builtin_fmaf(s[k], d[i][j][k], acc[i][j][k]);
+                            }
                         }
                     }
                 }
-            }
         }
-        if (u + du < nu) {
+    };
+    int u = u0;
+    for (; u + du < nu; u += du) {
+        unit(u, std::true_type{});
 #pragma unroll
-            for (int i = 0; i < RT; ++i) cur[i] = next[i];
+        for (int i = 0; i < RT; ++i) cur[i] = next[i];
+    }
+    unit(u, std::false_type{});
+}
+
+// The tokens' (lifted) rows into LDS, by all NT threads of a block: what few_lds_row lays out.  The
+// first two chunks of 16 bytes a thread are loaded here and stored by store(), so that the caller
+// can start the weight's loads between the two (loads return in order: behind them these would wait).
+template <int NT>
+struct FewStage {
+    few_u32x4 v[2];
+    __device__ __forceinline__ static few_u32x4 chunk(const uint16_t* X, int64_t ldx, int i, int per, int width, const FewLift& lift) {
+        const int t = i / per;
+        return lift.Ns ? few_x8<true>(X + t * ldx, 8 * (i - t * per), width, lift) : few_x8<false>(X + t * ldx, 8 * (i - t * per), width, lift);
+    }
+    __device__ __forceinline__ static void put(uint8_t* lds, int i, int per, int stride, const few_u32x4& v) {
+        const int t = i / per;
+        *(few_u32x4*)(lds + t * stride + 16 * (i - t * per)) = v;
+    }
+    __device__ __forceinline__ void load(const uint16_t* X, int64_t ldx, int T, int width, const FewLift& lift, uint8_t* lds, int tid) {
+        const int per = (width + 255) / 256 * 32, all = T * per, stride = few_lds_row(width);
+        for (int i = tid + 2 * NT; i < all; i += NT) put(lds, i, per, stride, chunk(X, ldx, i, per, width, lift));
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+            const int i = tid + k * NT;
+            v[k] = chunk(X, ldx, i < all ? i : 0, per, width, lift);
         }
     }
-}
+    __device__ __forceinline__ void store(int T, int width, uint8_t* lds, int tid) const {
+        const int per = (width + 255) / 256 * 32, all = T * per, stride = few_lds_row(width);
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+            const int i = tid + k * NT;
+            if (i < all) put(lds, i, per, stride, v[k]);
+        }
+    }
+};
 
 }  // namespace nm
