@@ -1,10 +1,12 @@
 // A mixture-of-experts layer of sparse gated blocks for a few tokens, in three launches:
 //   moe_logits_kernel  router logits (dense MFMA), K split over blocks, partials in f32
-//   moe_up_kernel      every block picks the experts of all tokens for itself from the logits (no
-//                      launch between), then makes H = act(x Wg^T) . (x Wu^T) tile by tile: tasks are (picked
-//                      expert, 16 or 32 features)
+//   moe_up_kernel      H = act(x Wg^T) . (x Wu^T) tile by tile: tasks are (picked expert, features).  For up to
+//                      four tokens every block picks the experts for itself first, a token a wave; for more
+//                      moe_pick_kernel does it, a launch before
 //   moe_down_kernel    Y: a block owns output columns and adds up, for them, every picked expert's
 //                      product in a fixed order
+// (One block that makes the logits and picks took 14 us for 64 experts of 2048: a CU alone reads 256 KB at about
+// 25 GB/s.  Logits and picking take 4 and 6 us as two launches, 4 and about 2.5 with the picking in moe_up_kernel.)
 // An expert's tokens are gathered by lane in the activation's loads (16 at a time are the B
 // operand); its weight is streamed as in the 4-bit products (nm_few.h).
 #include "nm_few.h"
@@ -66,22 +68,24 @@ __global__ __launch_bounds__(256) void moe_logits_kernel(MoeArgs a) {
         a.logits[((int64_t)blockIdx.z * a.T + tt) * a.E + ee] = (red[0][k] + red[1][k]) + (red[2][k] + red[3][k]);
 }
 
-// The topk experts of token t and their weights, by one wave: sel[0 .. topk), wts[0 .. topk).
-// Lane l holds experts l, l + 64, ...
+// e^x in 64 bits to about 2e-13 relative: 2^n e^r with |r| <= ln 2 / 2 and the series of e^r to r^10 / 10!
+__device__ __forceinline__ double moe_exp(double x) {
+    const double n = __builtin_rint(x * 1.4426950408889634);
+    const double r = __builtin_fma(-n, 0.6931471805599453, x);
+    double s = 1.0 / 3628800;
+    const double c[10] = {1.0 / 362880, 1.0 / 40320, 1.0 / 5040, 1.0 / 720, 1.0 / 120, 1.0 / 24, 1.0 / 6, 0.5, 1.0, 1.0};
+#pragma unroll
+    for (int i = 0; i < 10; ++i) s = __builtin_fma(s, r, c[i]);
+    const int k = n > 2000.0 ? 2000 : n < -2000.0 ? -2000 : (int)n;
+    return __builtin_ldexp(s, k);
+}
+
+// The topk experts of a token and their weights, by one wave: sel[0 .. topk), wts[0 .. topk).
+// Lane l holds experts l, l + 64, ... with logits l[]; keys: 64 doubles of the wave's own in LDS.
 template <int NE>
-__device__ __forceinline__ void moe_pick(const MoeArgs& a, int t, int lane, int32_t* sel, float* wts) {
-    float l[NE];
+__device__ __forceinline__ void moe_pick(const MoeArgs& a, const float (&l)[NE], int lane, double* keys, int32_t* sel, float* wts) {
     double key[NE];
     const double none = -__builtin_inf();
-#pragma unroll
-    for (int i = 0; i < NE; ++i) {
-        const int e = lane + 64 * i;
-        l[i] = 0.0f;
-        key[i] = none;
-        if (e < a.E) {
-            l[i] = split_sum(a.logits + (int64_t)t * a.E + e, a.ksplit, (int64_t)a.T * a.E);
-        }
-    }
     float top = -__builtin_inff();
 #pragma unroll
     for (int i = 0; i < NE; ++i)
@@ -91,18 +95,19 @@ __device__ __forceinline__ void moe_pick(const MoeArgs& a, int t, int lane, int3
 #pragma unroll
     for (int i = 0; i < NE; ++i) {
         const bool in = lane + 64 * i < a.E;
-        p[i] = !in ? 0.0f : a.sigmoid ? 1.0f / (1.0f + expf(-l[i])) : expf(l[i] - top);
+        p[i] = !in ? 0.0f : a.sigmoid ? sigmoid_f32(l[i]) : __expf(l[i] - top);
         sum += p[i];
     }
     for (int off = 32; off; off >>= 1) sum += __shfl_xor(sum, off);
 #pragma unroll
     for (int i = 0; i < NE; ++i) {
         const int e = lane + 64 * i;
+        key[i] = none;
         if (!a.sigmoid) p[i] = p[i] / sum;
         if (e < a.E) {
             // with a bias two probabilities may lie closer than f32 tells apart
             if (a.bias)
-                key[i] = (a.sigmoid ? 1.0 / (1.0 + exp(-(double)l[i])) : exp((double)l[i] - (double)top) / (double)sum) +
+                key[i] = (a.sigmoid ? 1.0 / (1.0 + moe_exp(-(double)l[i])) : moe_exp((double)l[i] - (double)top) / (double)sum) +
                          (double)a.bias[e];
             else
                 key[i] = (double)l[i];
@@ -112,26 +117,21 @@ __device__ __forceinline__ void moe_pick(const MoeArgs& a, int t, int lane, int3
     float total = 0.0f, mine = 0.0f;
     int my_sel = 0;
     if constexpr (NE == 1) {
-        // a lane's place: how many keys are before its own
-        const uint64_t k = __builtin_bit_cast(uint64_t, key[0]);
+        // a lane's place: how many keys are before its own (experts past the last rank behind all others)
+        keys[lane] = key[0];
+        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
         int place = 0;
-        for (int e = 0; e < a.E; ++e) {
-            const uint64_t o = (uint64_t)(uint32_t)__builtin_amdgcn_readlane((int)(k >> 32), e) << 32 |
-                               (uint32_t)__builtin_amdgcn_readlane((int)k, e);
-            const double ok = __builtin_bit_cast(double, o);
-            place += ok > key[0] || (ok == key[0] && e < lane) ? 1 : 0;
+#pragma unroll 4
+        for (int e = 0; e < 64; ++e) {
+            const double k = keys[e];
+            place += k > key[0] || (k == key[0] && e < lane) ? 1 : 0;
         }
         const bool in = lane < a.E && place < a.topk;
-        total = in ? p[0] : 0.0f;
-        if (a.renorm) {
-            // in descending order, as below
-            float sum = 0.0f;
-            for (int j = 0; j < a.topk; ++j) {
-                const uint64_t m = __ballot(in && place == j);
-                sum += __uint_as_float((uint32_t)__builtin_amdgcn_readlane((int)__float_as_uint(p[0]), __ffsll((unsigned long long)m) - 1));
+        if (a.renorm)
+            for (int j = 0; j < a.topk; ++j) {   // in descending order, as below
+                const int at = __ffsll((unsigned long long)__ballot(in && place == j)) - 1;
+                total += __uint_as_float((uint32_t)__builtin_amdgcn_readlane((int)__float_as_uint(p[0]), at));
             }
-            total = sum;
-        }
         if (in) {
             sel[place] = lane;
             wts[place] = a.route_scale * (a.renorm ? p[0] / total : p[0]);
@@ -176,14 +176,36 @@ __device__ __forceinline__ void moe_pick(const MoeArgs& a, int t, int lane, int3
     }
 }
 
-// ------------------------------------------------------------------ gate and up
-template <int NE>
-__device__ __forceinline__ void moe_route(const MoeArgs& a, int32_t* sel, float* wts, int tid, int nw) {
-    const int lane = tid & 63, wave = tid >> 6;
-    for (int t = wave; t < a.T; t += nw) moe_pick<NE>(a, t, lane, sel + t * a.topk, wts + t * a.topk);
-    __syncthreads();
+// Token t's experts by one wave, from the logits' partials: into sel and wts (the workspace's, or a block's
+// in LDS) and, where `out` says so, into the caller's.
+__device__ __forceinline__ void moe_token(const MoeArgs& a, int t, int lane, double* keys, int32_t* sel, float* wts, bool out) {
+    const auto pick = [&](auto ne) __attribute__((always_inline)) {
+        constexpr int NE = decltype(ne)::value;
+        float l[NE];
+#pragma unroll
+        for (int i = 0; i < NE; ++i)
+            l[i] = lane + 64 * i < a.E ? split_sum(a.logits + (int64_t)t * a.E + lane + 64 * i, a.ksplit, (int64_t)a.T * a.E) : 0.0f;
+        moe_pick<NE>(a, l, lane, keys, sel, wts);
+    };
+    if (a.E <= 64) pick(std::integral_constant<int, 1>{});
+    else if (a.E <= 128) pick(std::integral_constant<int, 2>{});
+    else if (a.E <= 256) pick(std::integral_constant<int, 4>{});
+    else pick(std::integral_constant<int, 8>{});
+    if (!out) return;
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    if (lane < a.topk) {
+        if (a.sel_out) a.sel_out[t * a.topk + lane] = sel[lane];
+        if (a.wts_out) a.wts_out[t * a.topk + lane] = wts[lane];
+    }
 }
 
+__global__ __launch_bounds__(256) void moe_pick_kernel(MoeArgs a) {
+    __shared__ double keys[4][64];
+    const int wave = threadIdx.x >> 6, t = blockIdx.x * 4 + wave;
+    if (t < a.T) moe_token(a, t, threadIdx.x & 63, keys[wave], a.sel + t * a.topk, a.wts + t * a.topk, true);
+}
+
+// ------------------------------------------------------------------ gate and up
 // the n-th (from 0) expert of those in sel[0 .. pairs), by number, or -1; one wave's lanes all get it
 __device__ __forceinline__ int moe_nth(const uint64_t (&used)[kMoeExperts / 64], int n) {
     for (int i = 0; i < kMoeExperts / 64; ++i) {
@@ -216,37 +238,40 @@ __device__ __forceinline__ int moe_pairs(const int32_t* sel, int pairs, int e, i
     return n - n0;
 }
 
-// RT: tiles of 16 rows of a task, gate and up beside each other.  XL: the tokens in LDS.
-template <int VT, int SPG, int RT, int NW, bool XL, bool LIFT>
+// RT: tiles of 16 rows of a task, gate and up beside each other.  XL: the tokens in LDS.  PICK: up to
+// NW tokens, whose experts are picked here.
+template <int VT, int SPG, int RT, int NW, bool XL, bool LIFT, bool PICK>
 __global__ __launch_bounds__(NW * 64) void moe_up_kernel(MoeArgs a, int tiles, int blocks) {
     constexpr int TR = RT / 2;   // feature tiles of a task
     __shared__ __attribute__((aligned(16))) float red[NW][RT][256];
     __shared__ int32_t sel[kMoeTokens * kMoeTopk];
-    __shared__ float wts[kMoeTokens * kMoeTopk];
     __shared__ uint64_t used[kMoeExperts / 64];
     extern __shared__ __attribute__((aligned(16))) uint8_t xlds[];
     const int tid = threadIdx.x, lane = tid & 63;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int nu = (a.wK + 255) / 256, pairs = a.T * a.topk, stride = few_lds_row(a.wK);
     if (tid < kMoeExperts / 64) used[tid] = 0;
-    if constexpr (XL) {
-        FewStage<NW * 64> stage;
-        stage.load(a.X, a.ldx, a.T, a.wK, a.lift, xlds, tid);
-        stage.store(a.T, a.wK, xlds, tid);
-    }
-    if (a.E <= 64) moe_route<1>(a, sel, wts, tid, NW);
-    else if (a.E <= 128) moe_route<2>(a, sel, wts, tid, NW);
-    else if (a.E <= 256) moe_route<4>(a, sel, wts, tid, NW);
-    else moe_route<8>(a, sel, wts, tid, NW);
-    for (int p = tid; p < pairs; p += NW * 64) {
-        atomicOr((unsigned long long*)&used[sel[p] >> 6], 1ull << (sel[p] & 63));
-        if (blockIdx.x == 0) {
-            a.sel[p] = sel[p];
-            a.wts[p] = wts[p];
-            if (a.sel_out) a.sel_out[p] = sel[p];
-            if (a.wts_out) a.wts_out[p] = wts[p];
+    FewStage<NW * 64> stage;
+    if constexpr (XL) stage.load(a.X, a.ldx, a.T, a.wK, a.lift, xlds, tid);
+    if constexpr (PICK) {
+        __shared__ double keys[NW][64];
+        __shared__ float wts[NW * kMoeTopk];
+        if (wave < a.T) {
+            moe_token(a, wave, lane, keys[wave], sel + wave * a.topk, wts + wave * a.topk, blockIdx.x == 0);
+            __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+            if (blockIdx.x == 0 && lane < a.topk) {
+                a.sel[wave * a.topk + lane] = sel[wave * a.topk + lane];
+                a.wts[wave * a.topk + lane] = wts[wave * a.topk + lane];
+            }
         }
     }
+    __syncthreads();
+    for (int p = tid; p < pairs; p += NW * 64) {
+        const int s = PICK ? sel[p] : a.sel[p];
+        if constexpr (!PICK) sel[p] = s;
+        atomicOr((unsigned long long*)&used[s >> 6], 1ull << (s & 63));
+    }
+    if constexpr (XL) stage.store(a.T, a.wK, xlds, tid);
     __syncthreads();
     FewRows w[RT];
     FewUnit<VT, SPG> cur[RT];
@@ -321,6 +346,7 @@ template <int VT, int SPG, int NW, bool LIFT>
 __global__ __launch_bounds__(NW * 64) void moe_down_kernel(MoeArgs a, int slices) {
     extern __shared__ __attribute__((aligned(16))) float part[];   // [slices][pairs][16]
     __shared__ int32_t sel[kMoeTokens * kMoeTopk];
+    __shared__ float wts[kMoeTokens * kMoeTopk];
     __shared__ uint64_t used[kMoeExperts / 64];
     const int tid = threadIdx.x, lane = tid & 63;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -330,6 +356,7 @@ __global__ __launch_bounds__(NW * 64) void moe_down_kernel(MoeArgs a, int slices
     for (int p = tid; p < pairs; p += NW * 64) {
         const int s = a.sel[p];
         sel[p] = s;
+        wts[p] = a.wts[p];
         atomicOr((unsigned long long*)&used[s >> 6], 1ull << (s & 63));
     }
     __syncthreads();
@@ -351,7 +378,7 @@ __global__ __launch_bounds__(NW * 64) void moe_down_kernel(MoeArgs a, int slices
             few_f32x4 acc[1][1] = {{few_f32x4{0, 0, 0, 0}}};
             few_product<VT, SPG, 1, 1>(cur, w, x, sl, slices, units, a.wF, a.gshift, a.lift, lane, acc);
             if (mine >= 0) {
-                const float wt = a.wts[mine];
+                const float wt = wts[mine];
                 few_f32x4 v = acc[0][0];
 #pragma unroll
                 for (int k = 0; k < 4; ++k) v[k] *= wt;
@@ -393,16 +420,23 @@ template <int VT, int SPG, bool LIFT>
 static nm_status moe_run(const MoeArgs& a, hipStream_t s) {
     const int pairs = a.T * a.topk, picked = pairs < a.E ? pairs : a.E;
     hipLaunchKernelGGL(moe_logits_kernel, dim3((a.E + 15) / 16, (a.T + 15) / 16, a.ksplit), dim3(256), 0, s, a);
-    // two feature tiles of a 4-bit weight a task (a unit of its rows is a third of a bf16 one's)
-    constexpr int RT = VT == kFewBF16 ? 2 : 4, NW = 8;
+    constexpr int RT = 2, NW = 4;
+    const bool pick = a.T <= NW;
+    if (!pick) hipLaunchKernelGGL(moe_pick_kernel, dim3((a.T + 3) / 4), dim3(256), 0, s, a);
     const int tiles = (a.F + 8 * RT - 1) / (8 * RT);
     const int64_t tasks = (int64_t)tiles * picked;
-    const int blocks = (int)(tasks < 512 ? tasks : 512);
+    const int blocks = (int)(tasks < 1024 ? tasks : 1024);
     const int64_t xbytes = (int64_t)a.T * few_lds_row(a.wK);
-    if (xbytes <= 32 * 1024)
-        hipLaunchKernelGGL((moe_up_kernel<VT, SPG, RT, NW, true, false>), dim3(blocks), dim3(NW * 64), (size_t)xbytes, s, a, tiles, blocks);
-    else
-        hipLaunchKernelGGL((moe_up_kernel<VT, SPG, RT, NW, false, LIFT>), dim3(blocks), dim3(NW * 64), 0, s, a, tiles, blocks);
+    const bool xl = xbytes <= 32 * 1024;
+    const auto up = [&](auto x, auto p) {
+        constexpr bool XL = decltype(x)::value, PICK = decltype(p)::value;
+        hipLaunchKernelGGL((moe_up_kernel<VT, SPG, RT, NW, XL, !XL && LIFT, PICK>), dim3(blocks), dim3(NW * 64), XL ? (size_t)xbytes : 0,
+                           s, a, tiles, blocks);
+    };
+    if (xl && pick) up(std::true_type{}, std::true_type{});
+    else if (xl) up(std::true_type{}, std::false_type{});
+    else if (pick) up(std::false_type{}, std::true_type{});
+    else up(std::false_type{}, std::false_type{});
     // slices of an expert's width: so many that every wave of a block has one where few experts are
     // picked, as long as the partial sums fit
     int slices = (kMoeWaves + picked - 1) / picked;
