@@ -21,6 +21,9 @@ extern "C" {
  *     sign (bit 3) and a magnitude: NM_I4 0 .. 7; NM_FP4 (OCP e2m1) 0, 0.5, 1, 1.5, 2, 3, 4, 6.
  *   scales [ceil(K' / group), lds] bf16: scale of group g of row r at scales[g * lds + r].
  *   idx as in nm_spmm.
+ * The products read whole 16 bytes of a row of codes and whole runs of four rows of scales: the bytes
+ * between must belong to the weight's memory, the last row's and the last group's too (a row takes K' / 4
+ * bytes rounded up to 16, a group R scales rounded up to 4); what they hold does not matter.
  * group: 64, 128 or 256.  The last group of a row may be shorter. */
 
 /* 4-bit codes of packed values (nm_pack, nm_prune_pack, nm_prune_slide ...), per row and group:
@@ -30,13 +33,15 @@ extern "C" {
  * vals: bf16 or f32 [R, slots] (ldv), slots = K' / 2 a multiple of 8.  values (nullable): code * s
  * rounded to vdt, [R, slots] (ldo): what the products then multiply with, for measuring the error
  * or training through it.
- * vals and values: 16-byte aligned rows; codes 4-byte aligned, ldc a multiple of 4; scales 2-byte. */
+ * A row's bytes of codes up to the next multiple of 16, where ldc has them, are set to 0.
+ * vals and values: 16-byte aligned rows; codes 4-byte aligned, ldc a multiple of 4; scales 2-byte.
+ * R up to 2^21. */
 nm_status nm_quant_w4(const void* vals, nm_dtype vdt, int64_t R, int64_t slots, int64_t ldv, nm_dtype qdt, int group,
                       void* codes, int64_t ldc, void* scales, int64_t lds, void* values, int64_t ldo,
                       nm_stream_t stream);
 
 /* Y = X W^T on a 4-bit packed weight, made for few tokens (serving: the weight is read once for
- * up to 64 tokens; more are taken 64 at a time).
+ * up to 32 tokens; more are taken 32 at a time).
  *   X: bf16 [Mtok, K] (ldx), K the original width; Y: bf16 or f32 [Mtok, R] (ldy).
  *   Ns: 0, or 3 <= Ns <= 8 over K' = (2 - 2/Ns) K (the lift is done in the activation's loads).
  * Code values times X are summed in f32 within 64 columns, scaled in f32 and added up in f32 in a
@@ -73,7 +78,8 @@ nm_status nm_spmm_glu_w4(const void* X, int64_t Mtok, int64_t K, int64_t ldx, co
  *   experts that were picked and their weights.
  * Requires 1 <= topk <= min(E, 16), E <= 512; K and F multiples of 16 and of 2Ns with K', F'
  * multiples of 16; bases and row strides of X, router and values 16-byte aligned (experts' strides
- * too), idx 4-byte, scales 8-byte with ld and expert strides multiples of 4.
+ * too), idx 4-byte, scales 8-byte with ld and expert strides multiples of 4.  Codes and scales are
+ * read in whole 16 bytes and runs of four rows, as by the 4-bit products.
  * ws: nm_moe_workspace(...) bytes, 16-byte aligned; no initial contents. */
 typedef enum { NM_ROUTE_SOFTMAX = 0, NM_ROUTE_SIGMOID = 1 } nm_route;
 typedef struct {

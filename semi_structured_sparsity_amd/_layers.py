@@ -48,12 +48,8 @@ def nm_quant_w4(vals: torch.Tensor, qdt: int = NM_I4, group: int = 128, want_val
     if group not in (64, 128, 256) or slots % 8:
         _refuse(f"group must be 64, 128 or 256 (got {group}) and a row a multiple of 8 values", vals=vals)
     ldc, lds = (slots // 2 + 15) // 16 * 16, (R + 3) // 4 * 4
-    # the bytes past a row's codes are never read as codes; zeroed where there are any, so that no
-    # stale memory travels with the weight
     codes = vals.new_empty((R, ldc), dtype=torch.uint8)
-    if ldc > slots // 2:
-        codes[:, slots // 2:].zero_()
-    scales = vals.new_empty(((2 * slots + group - 1) // group, lds), dtype=torch.bfloat16)[:, :R]
+    scales = vals.new_empty(((2 * slots + group - 1) // group, lds), dtype=torch.bfloat16)
     values = vals.new_empty((R, slots)) if want_values else None
     stream, back = _enter(vals)
     try:
@@ -63,19 +59,30 @@ def nm_quant_w4(vals: torch.Tensor, qdt: int = NM_I4, group: int = 128, want_val
         _leave(back)
     if st:
         _check(st)
+    if lds != R:
+        scales = scales[:, :R]
     return (codes, scales, values) if want_values else (codes, scales)
 
 
+def _holds(t: torch.Tensor, last: int) -> bool:
+    """Whether t's memory holds `last` elements from its first one."""
+    return t.untyped_storage().nbytes() >= (t.storage_offset() + last) * t.element_size()
+
+
 def _w4(codes, idx, scales, Kl, group):
-    """(rows, row strides of codes, idx and scales) of a 4-bit weight of Kl columns, or None."""
+    """(rows, row strides of codes, idx and scales) of a 4-bit weight of Kl columns, or None.  The products read
+    whole 16 bytes of a row of codes and runs of four rows of scales, the last row's and group's too."""
     c, i, s = _mat(codes), _mat(idx), _mat(scales)
     if not (c and i and s and codes.dtype == torch.uint8 and idx.dtype == torch.int32 and scales.dtype == torch.bfloat16):
         return None
     R = c[0]
     if i[0] != R or s[1] < R or c[1] < Kl // 4 or i[1] < (Kl + 31) // 32 or s[0] * group < Kl:
         return None
-    # one group's scales may have any stride: their row is as long as it is
-    return R, c[2], i[2], s[2] if s[0] > 1 else (s[1] + 3) // 4 * 4
+    lds = s[2] if s[0] > 1 else (R + 3) // 4 * 4      # one group's row of scales may have any stride
+    if (Kl % 64 and not _holds(codes, (R - 1) * c[2] + (Kl // 4 + 15) // 16 * 16)) or \
+            (R % 4 and not _holds(scales, ((Kl + group - 1) // group - 1) * lds + (R + 3) // 4 * 4)):
+        return None
+    return R, c[2], i[2], lds
 
 
 def _out(t, dt, rows, cols, X):
@@ -179,7 +186,10 @@ class MoELayer:
             if not ok:
                 _refuse(f"{name}: {slots} values{' and scales' if four else ''} and {(width + 31) // 32} index words a row for "
                         f"{E} experts of {rows} rows", vals=v, idx=i, scales=s)
-            lds = 0 if not four else s.stride(1) if s.shape[1] > 1 else (s.shape[2] + 3) // 4 * 4
+            lds = 0 if not four else s.stride(1) if s.shape[1] > 1 else (rows + 3) // 4 * 4
+            if four and not (_holds(v, (E - 1) * v.stride(0) + (rows - 1) * v.stride(1) + (slots + 15) // 16 * 16) and
+                             _holds(s, (E - 1) * s.stride(0) + ((width + group - 1) // group - 1) * lds + (rows + 3) // 4 * 4)):
+                _refuse(f"{name}: the last row of codes and of scales must be there up to whole 16 bytes and four rows", vals=v, scales=s)
             one = lambda t: t.stride(0) if E > 1 else 0  # noqa: E731
             self.weights.append(_Experts(v.data_ptr(), i.data_ptr(), s.data_ptr() if four else None, v.stride(1), i.stride(1), lds,
                                          one(v), one(i), one(s) if four else 0))

@@ -1,5 +1,6 @@
 // 4-bit packed weights: the quantiser, and Y = X W^T and the gated block H = act(X Wg^T) . (X Wu^T)
 // for few tokens (nm_few.h has the operands' layout and the inner product).
+#include "nm_codes.h"
 #include "nm_few.h"
 
 namespace nm {
@@ -7,14 +8,17 @@ namespace nm {
 // ------------------------------------------------------------------ quantiser
 // One thread takes 8 consecutive values; the group / 16 threads of a group share its maximum by
 // lane moves.  s = bf16(top / 7 or 6), code = nearest to v / s.
+// Bound by memory.  A block takes 64 rows by 128 values, so that the scales, whose rows run along the weight's
+// rows, leave as whole lines (a block a row, scales one by one: 11008 x 4096 33 us; so QQQ).
 template <bool F32, bool FP4>
-__global__ __launch_bounds__(256) void quant_w4_kernel(const void* __restrict__ vals, int64_t ldv, int64_t R, int chunks,
-                                                       int chunks_pad, int glanes, uint8_t* __restrict__ codes, int64_t ldc,
-                                                       uint16_t* __restrict__ scales, int64_t lds, void* __restrict__ values,
-                                                       int64_t ldo) {
-    const int64_t id = (int64_t)blockIdx.x * 256 + threadIdx.x;
-    const int64_t r = id / chunks_pad;
-    const int c = (int)(id - r * chunks_pad);
+__global__ __launch_bounds__(1024) void quant_w4_kernel(const void* __restrict__ vals, int64_t ldv, int64_t R, int chunks,
+                                                        int glanes, uint8_t* __restrict__ codes, int64_t ldc,
+                                                        uint16_t* __restrict__ scales, int64_t lds, void* __restrict__ values,
+                                                        int64_t ldo) {
+    __shared__ uint16_t sc[4][64];
+    const int tid = threadIdx.x, row = tid >> 4;
+    const int64_t r = (int64_t)blockIdx.y * 64 + row;
+    const int c = blockIdx.x * 16 + (tid & 15);
     const bool in = r < R && c < chunks;
     float v[8];
 #pragma unroll
@@ -40,27 +44,49 @@ __global__ __launch_bounds__(256) void quant_w4_kernel(const void* __restrict__ 
     const bool bad = top >= 0x7f800000u;
     const uint32_t sb = bad ? 0x7fc0u : f32_to_bf16_bits(__fdiv_rn(__uint_as_float(top), FP4 ? 6.0f : 7.0f));
     const float s = bf16_bits_to_f32(sb);
-    if (!in) return;
+    if ((tid & 15) % glanes == 0) sc[(tid & 15) / glanes][row] = (uint16_t)sb;
+    __syncthreads();
+    const int groups = 16 / glanes, all = (chunks + glanes - 1) / glanes;
+    if (tid < groups * 64) {
+        const int g = blockIdx.x * groups + (tid >> 6);
+        const int64_t at = (int64_t)blockIdx.y * 64 + (tid & 63);
+        if (g < all && at < R) scales[(int64_t)g * lds + at] = sc[tid >> 6][tid & 63];
+    }
+    if (!in) {   // the row's bytes up to the next 16
+        if (r < R && c < (chunks + 3) / 4 * 4 && 4 * (int64_t)c < ldc) *(uint32_t*)(codes + r * ldc + 4 * c) = 0;
+        return;
+    }
     uint32_t word = 0;
     float o[8];
+    const bool none = bad || s == 0.0f;
+    const RowDiv rd = row_div(none ? 1.0f : s);
+    float q[8];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        const float a = bad || s == 0.0f ? 0.0f : __builtin_fabsf(__fdiv_rn(v[i], s));
-        uint32_t m;
-        float val;
-        if constexpr (FP4) {
-            m = (a > 0.25f) + (a >= 0.75f) + (a > 1.25f) + (a >= 1.75f) + (a > 2.5f) + (a >= 3.5f) + (a > 5.0f);
-            val = m < 4 ? 0.5f * (float)m : (m < 6 ? (float)m - 2.0f : 2.0f * (float)m - 8.0f);
-        } else {
-            val = fminf(rintf(a), 7.0f);
-            m = (uint32_t)val;
+    for (int i = 0; i < 8; ++i) q[i] = none ? 0.0f : row_quot(v[i], rd);
+    if constexpr (FP4) {
+        // the conversion instructions round to the nearest code, ties to even, and hold to 6; a zero's
+        // sign goes
+        word = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(word, q[0], q[1], 1.0f, 0);
+        word = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(word, q[2], q[3], 1.0f, 1);
+        word = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(word, q[4], q[5], 1.0f, 2);
+        word = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(word, q[6], q[7], 1.0f, 3);
+        const uint32_t some = (word | word >> 1 | word >> 2) & 0x11111111u;
+        word = (word & 0x77777777u) | (word & some << 3);
+        typedef float f32x2_t __attribute__((ext_vector_type(2)));
+        const f32x2_t p0 = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(word, 1.0f, 0), p1 = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(word, 1.0f, 1);
+        const f32x2_t p2 = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(word, 1.0f, 2), p3 = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(word, 1.0f, 3);
+        o[0] = p0[0], o[1] = p0[1], o[2] = p1[0], o[3] = p1[1], o[4] = p2[0], o[5] = p2[1], o[6] = p3[0], o[7] = p3[1];
+    } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            o[i] = __builtin_fminf(__builtin_fmaxf(rintf(q[i]), -7.0f), 7.0f) + 0.0f;   // (-0 + 0 is +0)
+            const uint32_t m = (uint32_t)__builtin_fabsf(o[i]), neg = __float_as_uint(o[i]) >> 31;
+            word |= (m | neg << 3) << (4 * i);
         }
-        const uint32_t neg = m && (__float_as_uint(v[i]) >> 31);
-        word |= (m | neg << 3) << (4 * i);
-        o[i] = (neg ? -val : val) * s;
     }
+#pragma unroll
+    for (int i = 0; i < 8; ++i) o[i] *= s;
     *(uint32_t*)(codes + r * ldc + 4 * c) = word;
-    if (c % glanes == 0) scales[(int64_t)(c / glanes) * lds + r] = (uint16_t)sb;
     if (!values) return;
     if constexpr (F32) {
         float4* p = (float4*)((float*)values + r * ldo + 8 * c);
@@ -76,12 +102,12 @@ __global__ __launch_bounds__(256) void quant_w4_kernel(const void* __restrict__ 
 nm_status launch_quant_w4(const void* vals, nm_dtype vdt, int64_t R, int64_t slots, int64_t ldv, nm_dtype qdt, int group,
                           void* codes, int64_t ldc, void* scales, int64_t lds, void* values, int64_t ldo, hipStream_t s) {
     const int chunks = (int)(slots / 8), glanes = group / 16;
-    const int pad = (int)(ceil_div(chunks, glanes) * glanes);
-    const int64_t blocks = ceil_div(R * pad, 256);
-    if (blocks >= 1LL << 31) return set_error(NM_ERR_SHAPE, "nm_quant_w4: weight too large for one launch");
-#define NM_Q(F32, FP4)                                                                                                  \
-    hipLaunchKernelGGL((quant_w4_kernel<F32, FP4>), dim3((unsigned)blocks), dim3(256), 0, s, vals, ldv, R, chunks, pad, \
-                       glanes, (uint8_t*)codes, ldc, (uint16_t*)scales, lds, values, ldo)
+    // columns (and the bytes up to the next 16 of a row of codes) by rows
+    const dim3 grid((unsigned)ceil_div((chunks + 3) / 4 * 4, 16), (unsigned)ceil_div(R, 64));
+    if (grid.y > 65535u) return set_error(NM_ERR_SHAPE, "nm_quant_w4: weight too large for one launch");
+#define NM_Q(F32, FP4)                                                                                                   \
+    hipLaunchKernelGGL((quant_w4_kernel<F32, FP4>), grid, dim3(1024), 0, s, vals, ldv, R, chunks, glanes, (uint8_t*)codes, ldc, \
+                       (uint16_t*)scales, lds, values, ldo)
     if (vdt == NM_F32 && qdt == NM_FP4) NM_Q(true, true);
     else if (vdt == NM_F32) NM_Q(true, false);
     else if (qdt == NM_FP4) NM_Q(false, true);
@@ -188,21 +214,37 @@ static void w4_go(const W4Args& a, hipStream_t s) {
     hipLaunchKernelGGL((w4_kernel<VT, SPG, GLU, RT, CT, NW, XL, LIFT>), grid, dim3(NW * 64), lds, s, a);
 }
 
+// Up to four tokens whose rows fit 32 KB of LDS: one tile (or gate and up pair) a block, waves by the number of
+// tiles (one token of 11008 x 4096: 4 waves 8.4 us, 8 waves 8.8; of 4096 x 4096: 5.9 and 5.3).
+// Up to 16 tokens: from memory; lifted ones with two tiles a block, which share the lifting's arithmetic
+// (16 tokens of 6912 x 2560 6:8 gated: 15.5 us against 21.6), plain ones with one (of 11008 x 4096 gated: 23.5
+// against 25.5).
+// More: 32 at a time, four tiles a block where that still gives the chip blocks (32 tokens of 11008 x 4096: 17.8 us
+// against 24.3 with two; 33 of 4096 x 11008: 40 against 30).  Three or four tiles of tokens a wave took
+// longer (64 of 11008 x 4096: 53 us against 32).
 template <int VT, int SPG, bool GLU, bool LIFT>
 static void w4_tokens(const W4Args& a, hipStream_t s) {
     constexpr int W = GLU ? 2 : 1;
-    if (a.Mtok <= 16) w4_go<VT, SPG, GLU, 2 * W, 1, 8, false, LIFT>(a, s);
-    else if (a.Mtok <= 32) w4_go<VT, SPG, GLU, 2, 2, 8, false, LIFT>(a, s);
-    else if (a.Mtok <= 48) w4_go<VT, SPG, GLU, 2, 3, 8, false, LIFT>(a, s);
-    else w4_go<VT, SPG, GLU, 2, 4, 8, false, LIFT>(a, s);
+    if (a.Mtok <= 16) {
+        w4_go<VT, SPG, GLU, LIFT ? 2 * W : W, 1, 8, false, LIFT>(a, s);
+    } else if (ceil_div(a.R, 64 / W) * ceil_div(a.Mtok, 32) >= 160) {
+        w4_go<VT, SPG, GLU, 4, 2, 4, false, LIFT>(a, s);
+    } else {
+        w4_go<VT, SPG, GLU, 2, 2, 8, false, LIFT>(a, s);
+    }
 }
 
 template <int VT, int SPG, bool GLU>
 static void w4_lift(const W4Args& a, hipStream_t s) {
     constexpr int W = GLU ? 2 : 1;
-    if (a.Mtok <= 16 && (int64_t)a.Mtok * few_lds_row(a.width) <= 32 * 1024) w4_go<VT, SPG, GLU, W, 1, 4, true, false>(a, s);
-    else if (a.lift.Ns) w4_tokens<VT, SPG, GLU, true>(a, s);
-    else w4_tokens<VT, SPG, GLU, false>(a, s);
+    if (a.Mtok <= 4 && (int64_t)a.Mtok * few_lds_row(a.width) <= 32 * 1024) {
+        if (a.R >= 512 * 16) w4_go<VT, SPG, GLU, W, 1, 4, true, false>(a, s);
+        else w4_go<VT, SPG, GLU, W, 1, 8, true, false>(a, s);
+    } else if (a.lift.Ns) {
+        w4_tokens<VT, SPG, GLU, true>(a, s);
+    } else {
+        w4_tokens<VT, SPG, GLU, false>(a, s);
+    }
 }
 
 template <int VT, bool GLU>

@@ -12,6 +12,7 @@ bool group_ok(int g) { return g == 64 || g == 128 || g == 256; }
 int64_t lifted(int64_t K, int Ns) { return Ns ? K / (2 * Ns) * 4 * (Ns - 1) : K; }
 
 constexpr int64_t kMost = (int64_t)1 << 24;   // tokens, columns, rows of one call
+constexpr int64_t kQuantMost = (int64_t)1 << 21;   // rows of the quantiser
 constexpr int64_t kNormMost = 32768;           // columns of a norm
 constexpr int64_t kMoeMostTokens = 64;
 constexpr int kMoeMostExperts = 512, kMoeMostTopk = 16;
@@ -64,21 +65,22 @@ nm_status nm_quant_w4(const void* vals, nm_dtype vdt, int64_t R, int64_t slots, 
                       nm_stream_t stream) {
     const char* fn = "nm_quant_w4";
     NM_REQ(R >= 0 && slots >= 0, NM_ERR_SHAPE, "%s: negative size", fn);
-    NM_REQ(R <= kMost && slots <= kMost, NM_ERR_SHAPE, "%s: sizes up to 2^24", fn);
+    NM_REQ(R <= kQuantMost && slots <= kMost, NM_ERR_SHAPE, "%s: up to 2^21 rows of 2^24 values", fn);
     NM_REQ(vdt == NM_BF16 || vdt == NM_F32, NM_ERR_DTYPE, "%s: values must be bf16 or f32", fn);
     NM_REQ(code4(qdt), NM_ERR_DTYPE, "%s: codes are NM_I4 or NM_FP4", fn);
     NM_REQ(group_ok(group), NM_ERR_SHAPE, "%s: group must be 64, 128 or 256 (got %d)", fn, group);
     NM_REQ(slots % 8 == 0, NM_ERR_SHAPE, "%s: slots must be a multiple of 8", fn);
     if (R == 0 || slots == 0) return NM_OK;
     NM_REQ(vals && codes && scales, NM_ERR_NULL, "%s: NULL argument", fn);
-    const int64_t es = esize(vdt), groups = ceil_div(2 * slots, group);
+    const int64_t es = esize(vdt), groups = ceil_div(2 * slots, group), row16 = (slots / 2 + 15) / 16 * 16;
+    const int64_t codes_row = row16 < ldc ? row16 : ldc;
     NM_REQ(ldv >= slots && ldc >= slots / 2 && lds >= R && (!values || ldo >= slots), NM_ERR_SHAPE,
            "%s: leading dimension too small", fn);
     NM_REQ(aligned16(vals) && ldv * es % 16 == 0 && (!values || (aligned16(values) && ldo * es % 16 == 0)), NM_ERR_ALIGN,
            "%s: values need 16-byte aligned bases and row strides", fn);
     NM_REQ(aligned_to(codes, 4) && ldc % 4 == 0 && aligned_to(scales, 2), NM_ERR_ALIGN,
            "%s: codes need 4-byte aligned rows, scales 2-byte alignment", fn);
-    const Range in = span(vals, R, slots, ldv, es), out[] = {span(codes, R, slots / 2, ldc, 1), span(scales, groups, R, lds, 2),
+    const Range in = span(vals, R, slots, ldv, es), out[] = {span(codes, R, codes_row, ldc, 1), span(scales, groups, R, lds, 2),
                                                               span(values, R, slots, ldo, es)};
     for (int i = 0; i < 3; ++i) {
         NM_REQ(!overlap(out[i], in), NM_ERR_ALIAS, "%s: an output overlaps the input", fn);
