@@ -50,7 +50,7 @@ def nm_quant_w4(vals: torch.Tensor, qdt: int = NM_I4, group: int = 128, want_val
     ldc, lds = (slots // 2 + 15) // 16 * 16, (R + 3) // 4 * 4
     codes = vals.new_empty((R, ldc), dtype=torch.uint8)
     scales = vals.new_empty(((2 * slots + group - 1) // group, lds), dtype=torch.bfloat16)
-    values = vals.new_empty((R, slots)) if want_values else None
+    values = torch.empty_like(vals, memory_format=torch.contiguous_format) if want_values else None
     stream, back = _enter(vals)
     try:
         st = raw.nm_quant_w4(vals.data_ptr(), _DT[vals.dtype], R, slots, ldv, qdt, group, codes.data_ptr(), ldc,
@@ -225,25 +225,32 @@ def nm_moe(layer: MoELayer, X: torch.Tensor, topk: int, act: int = NM_ACT_SILU, 
 
 
 # ---------------------------------------------------------------- norms around a block
-_FLOATS = (torch.bfloat16, torch.float32)
+_FLOATS, _BF16, _ROWS = (torch.bfloat16, torch.float32), (torch.bfloat16,), torch.contiguous_format   # empty_like: half new_empty's time
 
 
-def _norm_side(X, C, gate, gate_rows, Mtok, vectors):
-    """(type code of the weights, the gate's row stride) after their checks."""
-    given = [t for t in (*vectors, gate) if t is not None]
-    wt, dev = given[0].dtype if given else torch.bfloat16, X.device
-    for t in vectors:
-        if t is not None and not (t.shape == (C,) and t.dtype == wt and t.is_contiguous() and t.device == dev):
-            _refuse(f"norm weights are {C} contiguous values of one type on {dev}", weight=t)
+def _norm_side(X, C, gate, gate_rows, Mtok, wp, bp, wn, bn):
+    """(type code of the weights, the gate's row stride) after their checks.  Each property of a tensor costs
+    about 0.1 us and these calls are short: they are read once."""
+    dev, wt, shape = X.device, None, (C,)
+    for t in (wp, bp, wn, bn):
+        if t is not None:
+            if wt is None:
+                wt = t.dtype
+            if not (t.shape == shape and t.dtype is wt and t.is_contiguous() and t.device == dev):
+                _refuse(f"norm weights are {C} contiguous values of one type on {dev}", weight=t)
     ldg = C
     if gate is not None:
         g = _mat(gate)
+        if wt is None:
+            wt = gate.dtype
         rows = (Mtok + gate_rows - 1) // gate_rows if gate_rows > 0 else 1
-        if not (g and g[0] >= rows and g[1] == C and gate.dtype == wt and gate.device == dev):
+        if not (g and g[0] >= rows and g[1] == C and gate.dtype is wt and gate.device == dev):
             _refuse(f"gate must be row-major, {rows} rows of {C} in the weights' type", gate=gate)
         ldg = g[2]
+    if wt is None:
+        return NM_BF16, ldg
     if wt not in _FLOATS:
-        _refuse("norm weights and gate are bf16 or f32", weight=given[0])
+        raise ValueError(f"norm weights and gate are bf16 or f32, got {wt}")
     return _DT[wt], ldg
 
 
@@ -262,7 +269,7 @@ def nm_block_norm(X: torch.Tensor, Y: torch.Tensor | None = None, gate: torch.Te
     y = None if Y is None else _mat(Y)
     if Y is not None and not (y and y[:2] == (Mtok, C) and Y.dtype == torch.bfloat16 and Y.device == dev):
         _refuse("Y must be row-major bf16 of X's shape", X=X, Y=Y)
-    wdt, ldg = _norm_side(X, C, gate, gate_rows, Mtok, (w_post, b_post, w_pre, b_pre))
+    wdt, ldg = _norm_side(X, C, gate, gate_rows, Mtok, w_post, b_post, w_pre, b_pre)
     Z, ldz = None, C
     if out_z is not None:
         z = _mat(out_z)
@@ -270,11 +277,11 @@ def nm_block_norm(X: torch.Tensor, Y: torch.Tensor | None = None, gate: torch.Te
             _refuse("out_z must be row-major, of X's shape and type", X=X, out_z=out_z)
         Z, ldz = out_z, z[2]
     elif want_z:
-        Z = X.new_empty((Mtok, C))
+        Z = torch.empty_like(X, memory_format=_ROWS)
     N = scale = None
     width = lifted_width(C, Ns) if Ns >= 2 else C
     if pre != NM_NORM_NONE:
-        N = X.new_empty((Mtok, width), dtype=_TORCH[ndt])
+        N = torch.empty_like(X, dtype=_TORCH[ndt], memory_format=_ROWS) if width == C else X.new_empty((Mtok, width), dtype=_TORCH[ndt])
         if ndt not in (NM_BF16, NM_F32):
             scale = X.new_empty(Mtok, dtype=torch.float32)
     stream, back = _enter(X)
@@ -309,35 +316,45 @@ def nm_block_norm_backward(Z: torch.Tensor, dZ: torch.Tensor | None = None, dN: 
                            ws: torch.Tensor | None = None) -> BlockNormGrads:
     """Gradients of nm_block_norm from its stored Z: of X and Y in their types, and with want_params of each weight that
     is given (a LAYER norm with a weight has a bias gradient too), in f32.  out_dx may be dZ itself."""
-    x, dev = _mat(Z), Z.device
-    if not (x and Z.dtype in _FLOATS):
+    x, dev, zt = _mat(Z), Z.device, Z.dtype
+    if not (x and zt in _FLOATS):
         _refuse("Z must be a row-major bf16 or f32 matrix", Z=Z)
     Mtok, C, ldz = x
-    ld = {}
-    for name, t, types in (("dZ", dZ, (Z.dtype,)), ("dN", dN, _FLOATS), ("Y", Y, (torch.bfloat16,)), ("out_dx", out_dx, (Z.dtype,))):
-        m = None if t is None else _mat(t)
-        if t is not None and not (m and m[:2] == (Mtok, C) and t.dtype in types and t.device == dev):
+    size = (Mtok, C)
+
+    def rows(name, t, types):
+        m = _mat(t)
+        if not (m and m[:2] == size and t.dtype in types and t.device == dev):
             _refuse(f"{name} must be row-major, of Z's shape, in {types}", Z=Z, **{name: t})
-        ld[name] = m[2] if m else C
+        return m[2]
+    lddz = C if dZ is None else rows("dZ", dZ, (zt,))
+    lddn = C if dN is None else rows("dN", dN, _FLOATS)
+    ldy = C if Y is None else rows("Y", Y, _BF16)
+    lddx = C if out_dx is None else rows("out_dx", out_dx, (zt,))
     if dN is None and pre != NM_NORM_NONE and want_params and w_pre is not None:
         _refuse("dN is needed for norm_pre's gradients", w_pre=w_pre)
-    wdt, ldg = _norm_side(Z, C, gate, gate_rows, Mtok, (w_post, b_post, w_pre, b_pre))
-    dX = (Z.new_empty((Mtok, C)) if out_dx is None else out_dx) if want_dx else None
-    dY = Y.new_empty((Mtok, C)) if want_dy and Y is not None else None
-    gates = (Mtok + gate_rows - 1) // gate_rows if gate_rows > 0 and Mtok > 0 else 1
-    wanted = [w_pre is not None, b_pre is not None or (pre == NM_NORM_LAYER and w_pre is not None), w_post is not None,
-              b_post is not None or (post == NM_NORM_LAYER and w_post is not None)]
-    sums = [Z.new_empty(C, dtype=torch.float32) if want_params and w else None for w in wanted]
-    sums.append(Z.new_empty((gates, C), dtype=torch.float32) if want_params and gate is not None else None)
-    if any(s is not None for s in sums):
-        ws = _need(raw.nm_block_norm_backward_workspace(Mtok, C, gate_rows), ws, Z)
+    wdt, ldg = _norm_side(Z, C, gate, gate_rows, Mtok, w_post, b_post, w_pre, b_pre)
+    dX = (torch.empty_like(Z, memory_format=_ROWS) if out_dx is None else out_dx) if want_dx else None
+    dY = torch.empty_like(Y, memory_format=_ROWS) if want_dy and Y is not None else None
+    sums = [None] * 5
+    if want_params:
+        some = False
+        for k, like in ((0, w_pre), (1, b_pre if b_pre is not None else w_pre if pre == NM_NORM_LAYER else None), (2, w_post),
+                        (3, b_post if b_post is not None else w_post if post == NM_NORM_LAYER else None)):
+            if like is not None:
+                sums[k], some = torch.empty_like(like, dtype=torch.float32), True
+        if gate is not None:
+            gates = (Mtok + gate_rows - 1) // gate_rows if gate_rows > 0 and Mtok > 0 else 1
+            sums[4], some = Z.new_empty((gates, C), dtype=torch.float32), True
+        if some:
+            ws = _need(raw.nm_block_norm_backward_workspace(Mtok, C, gate_rows), ws, Z)
     stream, back = _enter(Z)
     try:
-        st = raw.nm_block_norm_backward(Z.data_ptr(), _DT[Z.dtype], Mtok, C, ldz, _ptr(dZ), ld["dZ"], _ptr(dN),
-                                        NM_BF16 if dN is None else _DT[dN.dtype], ld["dN"], res_scale, _ptr(Y), ld["Y"], _ptr(gate),
+        st = raw.nm_block_norm_backward(Z.data_ptr(), _DT[zt], Mtok, C, ldz, _ptr(dZ), lddz, _ptr(dN),
+                                        NM_BF16 if dN is None else _DT[dN.dtype], lddn, res_scale, _ptr(Y), ldy, _ptr(gate),
                                         ldg, gate_rows, post, _ptr(w_post), _ptr(b_post), pre, _ptr(w_pre), wdt, eps, _ptr(dX),
-                                        C if out_dx is None else ld["out_dx"], _ptr(dY), C, *[_ptr(s) for s in sums], _ptr(ws),
-                                        0 if ws is None else ws.nbytes, stream)
+                                        lddx, _ptr(dY), C, *[_ptr(s) for s in sums], _ptr(ws), 0 if ws is None else ws.nbytes,
+                                        stream)
     finally:
         _leave(back)
     if st:
