@@ -47,17 +47,24 @@ nm_status nm_quant_w4(const void* vals, nm_dtype vdt, int64_t R, int64_t slots, 
  * Code values times X are summed in f32 within 64 columns, scaled in f32 and added up in f32 in a
  * fixed order; one rounding at the end.
  * Requires K % 2Ns == 0, K' % 16 == 0; X and codes 16-byte aligned with 16-byte row strides, idx
- * 4-byte aligned, scales 8-byte aligned with lds % 4 == 0; ldc < 2^26, ldi < 2^24.  No workspace. */
+ * 4-byte aligned, scales 8-byte aligned with lds % 4 == 0; ldc < 2^26, ldi < 2^24; up to 2^20 tokens.
+ * ws: nm_spmm_w4_workspace(...) bytes, 16-byte aligned, no initial contents: 0 for up to 16 tokens; for more
+ * the sums of a width that is split over blocks. */
+size_t nm_spmm_w4_workspace(int64_t Mtok, int64_t K, int64_t R, int Ns);
 nm_status nm_spmm_w4(const void* X, int64_t Mtok, int64_t K, int64_t ldx, const void* codes, nm_dtype qdt,
                      const uint32_t* idx, const void* scales, int64_t R, int64_t ldc, int64_t ldi, int64_t lds,
-                     int group, int Ns, void* Y, nm_dtype ydt, int64_t ldy, nm_stream_t stream);
+                     int group, int Ns, void* Y, nm_dtype ydt, int64_t ldy, void* ws, size_t ws_bytes,
+                     nm_stream_t stream);
 
 /* H = act(X Wg^T) . (X Wu^T) on two 4-bit weights packed alike (same ldc, ldi, lds, group): the
- * gated block of nm_spmm_glu.  Sums as in nm_spmm_w4; activation and product in f32, H rounded once. */
+ * gated block of nm_spmm_glu.  Sums as in nm_spmm_w4; activation and product in f32, H rounded once.
+ * ws: nm_spmm_glu_w4_workspace(...) bytes, as for nm_spmm_w4. */
+size_t nm_spmm_glu_w4_workspace(int64_t Mtok, int64_t K, int64_t R, int Ns);
 nm_status nm_spmm_glu_w4(const void* X, int64_t Mtok, int64_t K, int64_t ldx, const void* codes_g,
                          const uint32_t* idx_g, const void* scales_g, const void* codes_u, const uint32_t* idx_u,
                          const void* scales_u, nm_dtype qdt, int64_t R, int64_t ldc, int64_t ldi, int64_t lds, int group,
-                         int Ns, nm_act act, void* H, nm_dtype hdt, int64_t ldh, nm_stream_t stream);
+                         int Ns, nm_act act, void* H, nm_dtype hdt, int64_t ldh, void* ws, size_t ws_bytes,
+                         nm_stream_t stream);
 
 /* ---------------------------------------------------------------- mixture of sparse blocks
  * A whole mixture-of-experts layer for a few tokens (1 <= Mtok <= 64), its experts pruned gated

@@ -18,9 +18,11 @@ NM_I4, NM_FP4 = 5, 6      # 4-bit codes of packed values: sign and 3-bit magnitu
 
 LAYER_SIGNATURES = {
     "nm_quant_w4": (_I, [_P, _I, _I64, _I64, _I64, _I, _I, _P, _I64, _P, _I64, _P, _I64, _P]),
-    "nm_spmm_w4": (_I, [_P, _I64, _I64, _I64, _P, _I, _P, _P, _I64, _I64, _I64, _I64, _I, _I, _P, _I, _I64, _P]),
+    "nm_spmm_w4_workspace": (_SZ, [_I64, _I64, _I64, _I]),
+    "nm_spmm_w4": (_I, [_P, _I64, _I64, _I64, _P, _I, _P, _P, _I64, _I64, _I64, _I64, _I, _I, _P, _I, _I64, _P, _SZ, _P]),
+    "nm_spmm_glu_w4_workspace": (_SZ, [_I64, _I64, _I64, _I]),
     "nm_spmm_glu_w4": (_I, [_P, _I64, _I64, _I64, _P, _P, _P, _P, _P, _P, _I, _I64, _I64, _I64, _I64, _I, _I, _I, _P, _I,
-                            _I64, _P]),
+                            _I64, _P, _SZ, _P]),
     "nm_moe_workspace": (_SZ, [_I64, _I64, _I64, _I, _I]),
     "nm_moe": (_I, [_P, _I64, _I64, _I64, _P, _I64, _P, _I, _I, _I, _I, _F, _P, _P, _P, _I, _I, _I64, _I, _I, _P, _I, _I64, _P,
                     _P, _P, _SZ, _P]),
@@ -96,7 +98,8 @@ def _out(t, dt, rows, cols, X):
 
 
 def nm_spmm_w4(X: torch.Tensor, codes: torch.Tensor, idx: torch.Tensor, scales: torch.Tensor, qdt: int = NM_I4,
-               group: int = 128, Ns: int = 0, ydt: int = NM_BF16, out: torch.Tensor | None = None) -> torch.Tensor:
+               group: int = 128, Ns: int = 0, ydt: int = NM_BF16, out: torch.Tensor | None = None,
+               ws: torch.Tensor | None = None) -> torch.Tensor:
     """Y = X W^T on a 4-bit packed weight (nm_quant_w4's codes and scales, the packers' idx), made for few tokens."""
     x = _mat(X)
     Kl = lifted_width(x[1], Ns) if x and Ns >= 2 else x[1] if x else 0
@@ -106,10 +109,12 @@ def nm_spmm_w4(X: torch.Tensor, codes: torch.Tensor, idx: torch.Tensor, scales: 
                 scales=scales)
     (Mtok, K, ldx), (R, ldc, ldi, lds) = x, w
     Y, ldy, ydt = _out(out, ydt, Mtok, R, X)
+    if Mtok > 16 or ws is not None:
+        ws = _need(raw.nm_spmm_w4_workspace(Mtok, K, R, Ns), ws, X)
     stream, back = _enter(X)
     try:
         st = raw.nm_spmm_w4(X.data_ptr(), Mtok, K, ldx, codes.data_ptr(), qdt, idx.data_ptr(), scales.data_ptr(), R, ldc, ldi,
-                            lds, group, Ns, Y.data_ptr(), ydt, ldy, stream)
+                            lds, group, Ns, Y.data_ptr(), ydt, ldy, _ptr(ws), 0 if ws is None else ws.nbytes, stream)
     finally:
         _leave(back)
     if st:
@@ -119,7 +124,8 @@ def nm_spmm_w4(X: torch.Tensor, codes: torch.Tensor, idx: torch.Tensor, scales: 
 
 def nm_spmm_glu_w4(X: torch.Tensor, codes_g: torch.Tensor, idx_g: torch.Tensor, scales_g: torch.Tensor,
                    codes_u: torch.Tensor, idx_u: torch.Tensor, scales_u: torch.Tensor, qdt: int = NM_I4, group: int = 128,
-                   Ns: int = 0, act: int = NM_ACT_SILU, hdt: int = NM_BF16, out: torch.Tensor | None = None) -> torch.Tensor:
+                   Ns: int = 0, act: int = NM_ACT_SILU, hdt: int = NM_BF16, out: torch.Tensor | None = None,
+                   ws: torch.Tensor | None = None) -> torch.Tensor:
     """H = act(X Wg^T) . (X Wu^T) on two 4-bit weights packed alike, in one pass."""
     x = _mat(X)
     Kl = lifted_width(x[1], Ns) if x and Ns >= 2 else x[1] if x else 0
@@ -130,11 +136,13 @@ def nm_spmm_glu_w4(X: torch.Tensor, codes_g: torch.Tensor, idx_g: torch.Tensor, 
                 X=X, codes_g=codes_g, idx_g=idx_g, scales_g=scales_g, codes_u=codes_u, idx_u=idx_u, scales_u=scales_u)
     (Mtok, K, ldx), (R, ldc, ldi, lds) = x, w
     H, ldh, hdt = _out(out, hdt, Mtok, R, X)
+    if Mtok > 16 or ws is not None:
+        ws = _need(raw.nm_spmm_glu_w4_workspace(Mtok, K, R, Ns), ws, X)
     stream, back = _enter(X)
     try:
         st = raw.nm_spmm_glu_w4(X.data_ptr(), Mtok, K, ldx, codes_g.data_ptr(), idx_g.data_ptr(), scales_g.data_ptr(),
                                 codes_u.data_ptr(), idx_u.data_ptr(), scales_u.data_ptr(), qdt, R, ldc, ldi, lds, group, Ns,
-                                act, H.data_ptr(), hdt, ldh, stream)
+                                act, H.data_ptr(), hdt, ldh, _ptr(ws), 0 if ws is None else ws.nbytes, stream)
     finally:
         _leave(back)
     if st:

@@ -129,11 +129,18 @@ struct W4Args {
     void* Y;
     int64_t ldy;
     int y32, act;
+    float* part;      // [splits][1 or 2][Mtok][R] where the units are split over blocks (grid.z), else null
 };
+
+__device__ __forceinline__ void w4_store(const W4Args& a, int64_t tok, int64_t r, float v) {
+    if (a.y32) ((float*)a.Y)[tok * a.ldy + r] = v;
+    else ((uint16_t*)a.Y)[tok * a.ldy + r] = (uint16_t)f32_to_bf16_bits(v);
+}
 
 // A block of NW waves owns RT tiles of 16 rows (GLU: RT / 2 tiles of 16 features, gate and up
 // beside each other) and 16 CT tokens.  Its waves take units of 256 columns in turn and their sums
-// meet in LDS, added in wave order.  XL: the tokens (16 at most) in LDS.
+// meet in LDS, added in wave order; splits of the units over blocks leave partial sums for
+// w4_join_kernel.  XL: the tokens (16 at most) in LDS.
 template <int VT, int SPG, bool GLU, int RT, int CT, int NW, bool XL, bool LIFT>
 __global__ __launch_bounds__(NW * 64) void w4_kernel(W4Args a) {
     static_assert(!GLU || RT % 2 == 0, "gate and up tiles in pairs");
@@ -145,7 +152,7 @@ __global__ __launch_bounds__(NW * 64) void w4_kernel(W4Args a) {
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int64_t f0 = (int64_t)blockIdx.x * (16 * TR);
     const int64_t t0 = (int64_t)blockIdx.y * (16 * CT);
-    const int nu = (a.width + 255) / 256;
+    const int nu = (a.width + 255) / 256, first = XL ? wave : (int)blockIdx.z * NW + wave, step = XL ? NW : NW * (int)gridDim.z;
     FewRows w[RT];
     FewUnit<VT, SPG> cur[RT];
     FewStage<NW * 64> stage;
@@ -157,7 +164,7 @@ __global__ __launch_bounds__(NW * 64) void w4_kernel(W4Args a) {
         // a tile past the last row re-reads the block's first one (its sums are not stored)
         r0 = r0 < a.R ? r0 : f0;
         w[i] = few_rows(a.codes[m], a.idx[m], a.scales[m], a.ldc, a.ldi, a.lds, r0, a.R, lane);
-        cur[i].load(w[i], wave < nu ? wave : 0, a.width, a.gshift, lane);
+        cur[i].load(w[i], first < nu ? first : 0, a.width, a.gshift, lane);
     }
     few_f32x4 acc[RT][CT];
 #pragma unroll
@@ -170,7 +177,7 @@ __global__ __launch_bounds__(NW * 64) void w4_kernel(W4Args a) {
         __syncthreads();
         const int t = (lane & 15) < a.Mtok ? lane & 15 : a.Mtok - 1;
         const FewXLds x{xlds + t * stride};
-        few_product<VT, SPG, RT, CT>(cur, w, x, wave, NW, nu, a.width, a.gshift, a.lift, lane, acc);
+        few_product<VT, SPG, RT, CT>(cur, w, x, first, step, nu, a.width, a.gshift, a.lift, lane, acc);
     } else {
         FewXDirect<CT, LIFT> x;
 #pragma unroll
@@ -178,7 +185,7 @@ __global__ __launch_bounds__(NW * 64) void w4_kernel(W4Args a) {
             const int64_t t = t0 + 16 * j + (lane & 15);
             x.row[j] = a.X + (t < a.Mtok ? t : a.Mtok - 1) * a.ldx;
         }
-        few_product<VT, SPG, RT, CT>(cur, w, x, wave, NW, nu, a.width, a.gshift, a.lift, lane, acc);
+        few_product<VT, SPG, RT, CT>(cur, w, x, first, step, nu, a.width, a.gshift, a.lift, lane, acc);
     }
 
 #pragma unroll
@@ -199,19 +206,59 @@ __global__ __launch_bounds__(NW * 64) void w4_kernel(W4Args a) {
                 v += red[n][GLU ? 2 * tile : tile][k];
                 if constexpr (GLU) up += red[n][2 * tile + 1][k];
             }
+            if (!XL && a.part) {
+                float* p = a.part + ((int64_t)blockIdx.z * (GLU ? 2 : 1) * a.Mtok + tok) * a.R + r;
+                p[0] = v;
+                if constexpr (GLU) p[(int64_t)a.Mtok * a.R] = up;
+                continue;
+            }
             if constexpr (GLU) v = few_act(a.act, v) * up;
-            if (a.y32) ((float*)a.Y)[tok * a.ldy + r] = v;
-            else ((uint16_t*)a.Y)[tok * a.ldy + r] = (uint16_t)f32_to_bf16_bits(v);
+            w4_store(a, tok, r, v);
         }
     }
 }
 
+// The splits' partial sums added in order, and what follows a sum.
+template <bool GLU>
+__global__ __launch_bounds__(256) void w4_join_kernel(W4Args a, int splits) {
+    const int64_t r = (int64_t)blockIdx.x * 256 + threadIdx.x, tok = blockIdx.y;
+    if (r >= a.R) return;
+    const int64_t all = (int64_t)a.Mtok * a.R;
+    const float* p = a.part + tok * a.R + r;
+    float v = split_sum(p, splits, (GLU ? 2 : 1) * all);
+    if constexpr (GLU) v = few_act(a.act, v) * split_sum(p + all, splits, 2 * all);
+    w4_store(a, tok, r, v);
+}
+
 template <int VT, int SPG, bool GLU, int RT, int CT, int NW, bool XL, bool LIFT>
-static void w4_go(const W4Args& a, hipStream_t s) {
+static void w4_go(const W4Args& a, hipStream_t s, int splits = 1) {
     constexpr int rows = 16 * (GLU ? RT / 2 : RT);
-    const dim3 grid((unsigned)ceil_div(a.R, rows), (unsigned)ceil_div(a.Mtok, 16 * CT));
+    const dim3 grid((unsigned)ceil_div(a.R, rows), (unsigned)ceil_div(a.Mtok, 16 * CT), (unsigned)splits);
     const size_t lds = XL ? (size_t)a.Mtok * few_lds_row(a.width) : 0;
     hipLaunchKernelGGL((w4_kernel<VT, SPG, GLU, RT, CT, NW, XL, LIFT>), grid, dim3(NW * 64), lds, s, a);
+    if (splits > 1)
+        hipLaunchKernelGGL((w4_join_kernel<GLU>), dim3((unsigned)ceil_div(a.R, 256), (unsigned)a.Mtok), dim3(256), 0, s, a, splits);
+}
+
+// How a product of more than 16 tokens is cut up: tiles of 16 tokens a wave, and blocks that share a block's units
+// (their sums go through the workspace).  Splits pay where the rows alone leave the chip short of waves and a
+// wave is left at least a unit: 33 tokens of 4096 x 11008 29.7 us without, 21.8 with 8; 32 of 4096 x 4096 13.1
+// and 11.3 with 4; 20 of 1024 x 2048 7.0 and 9.0 with 2.
+struct W4Plan {
+    int ct, splits;
+};
+static W4Plan w4_plan(int64_t Mtok, int64_t width, int64_t R, bool glu) {
+    W4Plan p{2, 1};
+    if (Mtok <= 16) return p;
+    const int ct = Mtok > 32 && Mtok <= 48 ? 3 : 2;
+    const int64_t nu = ceil_div(width, 256), base = ceil_div(R, glu ? 32 : 64) * ceil_div(Mtok, 16 * ct);
+    int64_t splits = nu / 4 < 512 / base ? nu / 4 : 512 / base;
+    if (nu >= 16 && splits >= 2) p = W4Plan{ct, (int)splits};
+    return p;
+}
+size_t w4_ws(int64_t Mtok, int64_t width, int64_t R, bool glu) {
+    const W4Plan p = w4_plan(Mtok, width, R, glu);
+    return p.splits > 1 ? (size_t)p.splits * (glu ? 2 : 1) * (size_t)Mtok * (size_t)R * 4 : 0;
 }
 
 // Up to four tokens whose rows fit 32 KB of LDS: one tile (or gate and up pair) a block, waves by the number of
@@ -219,41 +266,42 @@ static void w4_go(const W4Args& a, hipStream_t s) {
 // Up to 16 tokens: from memory; lifted ones with two tiles a block, which share the lifting's arithmetic
 // (16 tokens of 6912 x 2560 6:8 gated: 15.5 us against 21.6), plain ones with one (of 11008 x 4096 gated: 23.5
 // against 25.5).
-// More: 32 at a time, four tiles a block where that still gives the chip blocks (32 tokens of 11008 x 4096: 17.8 us
-// against 24.3 with two; 33 of 4096 x 11008: 40 against 30).  Three or four tiles of tokens a wave took
-// longer (64 of 11008 x 4096: 53 us against 32).
+// More: split as planned; else 32 at a time, four tiles a block where that still gives the chip blocks (32 tokens
+// of 11008 x 4096: 17.8 us against 24.3 with two), two where not.
 template <int VT, int SPG, bool GLU, bool LIFT>
-static void w4_tokens(const W4Args& a, hipStream_t s) {
+static void w4_tokens(const W4Args& a, const W4Plan& p, hipStream_t s) {
     constexpr int W = GLU ? 2 : 1;
     if (a.Mtok <= 16) {
         w4_go<VT, SPG, GLU, LIFT ? 2 * W : W, 1, 8, false, LIFT>(a, s);
-    } else if (ceil_div(a.R, 64 / W) * ceil_div(a.Mtok, 32) >= 160) {
-        w4_go<VT, SPG, GLU, 4, 2, 4, false, LIFT>(a, s);
+    } else if (p.splits > 1 && p.ct == 3) {
+        w4_go<VT, SPG, GLU, 4, 3, 4, false, LIFT>(a, s, p.splits);
+    } else if (p.splits > 1 || ceil_div(a.R, 64 / W) * ceil_div(a.Mtok, 32) >= 160) {
+        w4_go<VT, SPG, GLU, 4, 2, 4, false, LIFT>(a, s, p.splits);
     } else {
         w4_go<VT, SPG, GLU, 2, 2, 8, false, LIFT>(a, s);
     }
 }
 
 template <int VT, int SPG, bool GLU>
-static void w4_lift(const W4Args& a, hipStream_t s) {
+static void w4_lift(const W4Args& a, const W4Plan& p, hipStream_t s) {
     constexpr int W = GLU ? 2 : 1;
     if (a.Mtok <= 4 && (int64_t)a.Mtok * few_lds_row(a.width) <= 32 * 1024) {
         if (a.R >= 512 * 16) w4_go<VT, SPG, GLU, W, 1, 4, true, false>(a, s);
         else w4_go<VT, SPG, GLU, W, 1, 8, true, false>(a, s);
     } else if (a.lift.Ns) {
-        w4_tokens<VT, SPG, GLU, true>(a, s);
+        w4_tokens<VT, SPG, GLU, true>(a, p, s);
     } else {
-        w4_tokens<VT, SPG, GLU, false>(a, s);
+        w4_tokens<VT, SPG, GLU, false>(a, p, s);
     }
 }
 
 template <int VT, bool GLU>
-static void w4_group(const W4Args& a, hipStream_t s) {
-    if (a.gshift == 6) w4_lift<VT, 1, GLU>(a, s);
-    else w4_lift<VT, 2, GLU>(a, s);
+static void w4_group(const W4Args& a, const W4Plan& p, hipStream_t s) {
+    if (a.gshift == 6) w4_lift<VT, 1, GLU>(a, p, s);
+    else w4_lift<VT, 2, GLU>(a, p, s);
 }
 
-nm_status launch_w4(const W4In& in, hipStream_t s) {
+nm_status launch_w4(const W4In& in, void* ws, hipStream_t s) {
     W4Args a{};
     a.X = in.X;
     a.ldx = in.ldx;
@@ -275,12 +323,14 @@ nm_status launch_w4(const W4In& in, hipStream_t s) {
     a.y32 = in.ydt == NM_F32;
     a.act = in.act;
     const bool glu = in.codes[1] != nullptr;
+    const W4Plan p = w4_plan(in.Mtok, a.width, in.R, glu);
+    a.part = p.splits > 1 ? (float*)ws : nullptr;
     if (in.qdt == NM_FP4) {
-        if (glu) w4_group<kFewFP4, true>(a, s);
-        else w4_group<kFewFP4, false>(a, s);
+        if (glu) w4_group<kFewFP4, true>(a, p, s);
+        else w4_group<kFewFP4, false>(a, p, s);
     } else {
-        if (glu) w4_group<kFewI4, true>(a, s);
-        else w4_group<kFewI4, false>(a, s);
+        if (glu) w4_group<kFewI4, true>(a, p, s);
+        else w4_group<kFewI4, false>(a, p, s);
     }
     return check_launch(glu ? "nm_spmm_glu_w4" : "nm_spmm_w4");
 }

@@ -12,16 +12,18 @@ bool group_ok(int g) { return g == 64 || g == 128 || g == 256; }
 int64_t lifted(int64_t K, int Ns) { return Ns ? K / (2 * Ns) * 4 * (Ns - 1) : K; }
 
 constexpr int64_t kMost = (int64_t)1 << 24;   // tokens, columns, rows of one call
+constexpr int64_t kW4MostTokens = (int64_t)1 << 20;
 constexpr int64_t kQuantMost = (int64_t)1 << 21;   // rows of the quantiser
 constexpr int64_t kNormMost = 32768;           // columns of a norm
 constexpr int64_t kMoeMostTokens = 64;
 constexpr int kMoeMostExperts = 512, kMoeMostTopk = 16;
 
 // the checks of a 4-bit product; nw: 1, or 2 weights (gated block)
-nm_status w4_check(const char* fn, const W4In& in, int nw, bool* run) {
+nm_status w4_check(const char* fn, const W4In& in, int nw, const void* ws, size_t ws_bytes, bool* run) {
     *run = false;
     NM_REQ(in.Mtok >= 0 && in.K >= 0 && in.R >= 0, NM_ERR_SHAPE, "%s: negative size", fn);
-    NM_REQ(in.Mtok <= kMost && in.K <= kMost && in.R <= kMost, NM_ERR_SHAPE, "%s: sizes up to 2^24", fn);
+    NM_REQ(in.Mtok <= kW4MostTokens && in.K <= kMost && in.R <= kMost, NM_ERR_SHAPE, "%s: up to 2^20 tokens, widths and rows up to 2^24",
+           fn);
     NM_REQ(in.Ns == 0 || (in.Ns >= 3 && in.Ns <= 8), NM_ERR_PATTERN,
            "%s: supported patterns are plain 2:4 (Ns=0) and (2N-2):2N via slide (3 <= Ns <= 8), got Ns=%d", fn, in.Ns);
     NM_REQ(code4(in.qdt), NM_ERR_DTYPE, "%s: codes are NM_I4 or NM_FP4", fn);
@@ -41,16 +43,20 @@ nm_status w4_check(const char* fn, const W4In& in, int nw, bool* run) {
            "%s: X and codes need 16-byte aligned bases and row strides", fn);
     NM_REQ(aligned_to(in.Y, esize(in.ydt)), NM_ERR_ALIGN, "%s: the output is not element-aligned", fn);
     NM_REQ(in.lds % 4 == 0, NM_ERR_ALIGN, "%s: lds must be a multiple of 4", fn);
+    const size_t need = w4_ws(in.Mtok, Kl, in.R, nw == 2);
+    NM_REQ(need == 0 || (ws && ws_bytes >= need), NM_ERR_WORKSPACE, "%s: workspace of %zu bytes needed", fn, need);
+    NM_REQ(need == 0 || aligned16(ws), NM_ERR_ALIGN, "%s: ws must be 16-byte aligned", fn);
     const Range y = span(in.Y, in.Mtok, in.R, in.ldy, esize(in.ydt));
-    NM_REQ(!overlap(y, span(in.X, in.Mtok, in.K, in.ldx, 2)), NM_ERR_ALIAS, "%s: the output overlaps X", fn);
+    const Range w = need ? Range{(uintptr_t)ws, (uintptr_t)ws + need} : Range{0, 0}, x = span(in.X, in.Mtok, in.K, in.ldx, 2);
+    NM_REQ(!overlap(y, x) && !overlap(w, x) && !overlap(y, w), NM_ERR_ALIAS, "%s: the output, X and ws overlap", fn);
     for (int m = 0; m < nw; ++m) {
         NM_REQ(in.codes[m] && in.idx[m] && in.scales[m], NM_ERR_NULL, "%s: NULL weight", fn);
         NM_REQ(aligned16(in.codes[m]), NM_ERR_ALIGN, "%s: X and codes need 16-byte aligned bases and row strides", fn);
         NM_REQ(aligned_to(in.idx[m], 4), NM_ERR_ALIGN, "%s: idx must be 4-byte aligned", fn);
         NM_REQ(aligned_to(in.scales[m], 8), NM_ERR_ALIGN, "%s: scales must be 8-byte aligned", fn);
-        NM_REQ(!overlap(y, span(in.codes[m], in.R, Kl / 4, in.ldc, 1)) && !overlap(y, span(in.idx[m], in.R, iw, in.ldi, 4)) &&
-                   !overlap(y, span(in.scales[m], groups, in.R, in.lds, 2)),
-               NM_ERR_ALIAS, "%s: the output overlaps a weight", fn);
+        for (const Range& r : {span(in.codes[m], in.R, Kl / 4, in.ldc, 1), span(in.idx[m], in.R, iw, in.ldi, 4),
+                               span(in.scales[m], groups, in.R, in.lds, 2)})
+            NM_REQ(!overlap(y, r) && !overlap(w, r), NM_ERR_ALIAS, "%s: the output or ws overlaps a weight", fn);
     }
     *run = true;
     return NM_OK;
@@ -89,27 +95,38 @@ nm_status nm_quant_w4(const void* vals, nm_dtype vdt, int64_t R, int64_t slots, 
     return launch_quant_w4(vals, vdt, R, slots, ldv, qdt, group, codes, ldc, scales, lds, values, ldo, (hipStream_t)stream);
 }
 
+static size_t w4_query(int64_t Mtok, int64_t K, int64_t R, int Ns, bool glu) {
+    if (Mtok <= 0 || Mtok > kW4MostTokens || K <= 0 || K > kMost || R <= 0 || R > kMost || !(Ns == 0 || (Ns >= 3 && Ns <= 8)) ||
+        (Ns && K % (2 * Ns)) || lifted(K, Ns) % 16)
+        return 0;
+    return w4_ws(Mtok, lifted(K, Ns), R, glu);
+}
+
+size_t nm_spmm_w4_workspace(int64_t Mtok, int64_t K, int64_t R, int Ns) { return w4_query(Mtok, K, R, Ns, false); }
+
+size_t nm_spmm_glu_w4_workspace(int64_t Mtok, int64_t K, int64_t R, int Ns) { return w4_query(Mtok, K, R, Ns, true); }
+
 nm_status nm_spmm_w4(const void* X, int64_t Mtok, int64_t K, int64_t ldx, const void* codes, nm_dtype qdt,
                      const uint32_t* idx, const void* scales, int64_t R, int64_t ldc, int64_t ldi, int64_t lds,
-                     int group, int Ns, void* Y, nm_dtype ydt, int64_t ldy, nm_stream_t stream) {
+                     int group, int Ns, void* Y, nm_dtype ydt, int64_t ldy, void* ws, size_t ws_bytes, nm_stream_t stream) {
     const W4In in{(const uint16_t*)X, Mtok, K, ldx, {codes, nullptr}, {idx, nullptr}, {scales, nullptr}, qdt, R, ldc, ldi,
                   lds, group, Ns, NM_ACT_SILU, Y, ydt, ldy};
     bool run = false;
-    const nm_status st = w4_check("nm_spmm_w4", in, 1, &run);
-    return st != NM_OK || !run ? st : launch_w4(in, (hipStream_t)stream);
+    const nm_status st = w4_check("nm_spmm_w4", in, 1, ws, ws_bytes, &run);
+    return st != NM_OK || !run ? st : launch_w4(in, ws, (hipStream_t)stream);
 }
 
 nm_status nm_spmm_glu_w4(const void* X, int64_t Mtok, int64_t K, int64_t ldx, const void* codes_g,
                          const uint32_t* idx_g, const void* scales_g, const void* codes_u, const uint32_t* idx_u,
                          const void* scales_u, nm_dtype qdt, int64_t R, int64_t ldc, int64_t ldi, int64_t lds, int group,
-                         int Ns, nm_act act, void* H, nm_dtype hdt, int64_t ldh, nm_stream_t stream) {
+                         int Ns, nm_act act, void* H, nm_dtype hdt, int64_t ldh, void* ws, size_t ws_bytes, nm_stream_t stream) {
     const char* fn = "nm_spmm_glu_w4";
     NM_REQ(known_act(act), NM_ERR_SHAPE, "%s: unknown activation", fn);
     const W4In in{(const uint16_t*)X, Mtok, K, ldx, {codes_g, codes_u}, {idx_g, idx_u}, {scales_g, scales_u}, qdt, R, ldc,
                   ldi, lds, group, Ns, act, H, hdt, ldh};
     bool run = false;
-    const nm_status st = w4_check(fn, in, 2, &run);
-    return st != NM_OK || !run ? st : launch_w4(in, (hipStream_t)stream);
+    const nm_status st = w4_check(fn, in, 2, ws, ws_bytes, &run);
+    return st != NM_OK || !run ? st : launch_w4(in, ws, (hipStream_t)stream);
 }
 
 size_t nm_moe_workspace(int64_t Mtok, int64_t K, int64_t F, int E, int topk) {

@@ -380,7 +380,8 @@ struct W4In {
     nm_dtype ydt;
     int64_t ldy;
 };
-nm_status launch_w4(const W4In& in, hipStream_t s);
+size_t w4_ws(int64_t Mtok, int64_t width, int64_t R, bool glu);   // width: the lifted one
+nm_status launch_w4(const W4In& in, void* ws, hipStream_t s);
 // mixture of sparse blocks
 struct MoeIn {
     const void* X;

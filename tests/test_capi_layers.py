@@ -64,7 +64,7 @@ def _w4(two=False, **kw):
     a.update(R=8, ldc=16, ldi=2, lds=8, group=64, Ns=0)
     if two:
         a.update(act=0)
-    a.update(Y=Y, ydt=1, ldy=8)
+    a.update(Y=Y, ydt=1, ldy=8, ws=V, n=1 << 40)
     a.update(kw)
     return _name((nm.raw.nm_spmm_glu_w4 if two else nm.raw.nm_spmm_w4)(*a.values(), None))
 
@@ -77,7 +77,7 @@ def test_products_refuse(two):
     assert f(Ns=2) == "NM_ERR_PATTERN" and f(Ns=9) == "NM_ERR_PATTERN" and f(Ns=-1) == "NM_ERR_PATTERN"
     assert f(K=40) == "NM_ERR_SHAPE" and f(K=60, Ns=4) == "NM_ERR_SHAPE" and f(K=24, Ns=4) == "NM_ERR_SHAPE"
     assert f(M=-1) == "NM_ERR_SHAPE" and f(K=-16) == "NM_ERR_SHAPE" and f(R=-1) == "NM_ERR_SHAPE" and f(K=0) == "NM_ERR_SHAPE"
-    assert f(M=(1 << 24) + 1) == "NM_ERR_SHAPE" and f(R=(1 << 24) + 1) == "NM_ERR_SHAPE"
+    assert f(M=(1 << 20) + 1) == "NM_ERR_SHAPE" and f(R=(1 << 24) + 1) == "NM_ERR_SHAPE"
     for k, v in (("ldx", 56), ("ldc", 0), ("ldi", 1), ("lds", 4), ("ldy", 7), ("ldc", 1 << 26), ("ldi", 1 << 24)):
         assert f(**{k: v}) == "NM_ERR_SHAPE", k
     for k, v in (("ldx", 68), ("ldc", 24), ("lds", 10)):
@@ -92,6 +92,22 @@ def test_products_refuse(two):
         if k != "Y":
             assert f(Y=p) == "NM_ERR_ALIAS", k
     assert f(M=0, X=None, Y=None) == "NM_OK" and f(R=0, Y=None) == "NM_OK"
+
+
+@pytest.mark.parametrize("two", [False, True])
+def test_products_that_need_a_workspace(two):
+    big = dict(M=33, K=8192, ldx=8192, R=64, ldc=2048, ldi=256, lds=64, ldy=64)
+    f = lambda **kw: _w4(two, **{**big, **kw})  # noqa: E731
+    query = nm.raw.nm_spmm_glu_w4_workspace if two else nm.raw.nm_spmm_w4_workspace
+    need = query(33, 8192, 64, 0)
+    assert need >= 2 * (1 + two) * 33 * 64 * 4
+    assert f(ws=None) == "NM_ERR_WORKSPACE" and f(n=need - 1) == "NM_ERR_WORKSPACE" and f(ws=P(V.value + 8)) == "NM_ERR_ALIGN"
+    for p in (X, C, I, S, Y) + ((C2, I2, S2) if two else ()):
+        assert f(ws=p) == "NM_ERR_ALIAS"
+    assert query(16, 8192, 64, 0) == 0 and query(33, 256, 64, 0) == 0
+    for bad in ((0, 8192, 64, 0), (33, 8200, 64, 0), (33, 8192, 0, 0), (33, 8192, 64, 2), (33, 8192, 64, 9), (33, 8192, 64, 3), (33, 1 << 40, 64, 0),
+                ((1 << 20) + 1, 8192, 64, 0), (33, 8192, -4, 0)):
+        assert query(*bad) == 0, bad
 
 
 # ------------------------------------------------------------------ mixture of sparse blocks

@@ -132,6 +132,30 @@ def test_glu(nm, T, R, K, Ns, a, qdt):
         _close(H, ref, err, hdt == nm.NM_BF16)
 
 
+@pytest.mark.parametrize("T,R,K,Ns", [(17, 64, 4096, 0), (33, 40, 8192, 0), (48, 130, 4112, 0), (64, 33, 6144, 0), (90, 70, 4096, 0),
+                                      (40, 70, 4096, 4), (20, 97, 5120, 5)])
+@pytest.mark.parametrize("qdt", [L.I4, L.FP4])
+def test_widths_split_over_blocks(nm, T, R, K, Ns, qdt):
+    """Few rows of a wide weight: partial sums through the workspace (full of NaN before), plain and gated."""
+    g = np.random.default_rng(T + R + K)
+    X, Xf = _x(g, T, K)
+    group = (64, 128, 256)[T % 3]
+    assert nm.raw.nm_spmm_w4_workspace(T, K, R, Ns) > 0
+    Wg, cg, ig, sg = L.w4_weight(nm, g, R, K, Ns, qdt, group)
+    Wu, cu, iu, su = L.w4_weight(nm, g, R, K, Ns, qdt, group)
+    G, U, eG, eU = Xf @ Wg.T, Xf @ Wu.T, L.product_bound(Xf, Wg, K), L.product_bound(Xf, Wu, K)
+    for ydt in (nm.NM_F32, nm.NM_BF16):
+        Y = nm.nm_spmm_w4(X, cg, ig, sg, qdt=qdt, group=group, Ns=Ns, ydt=ydt, ws=B.nan_ws(nm.raw.nm_spmm_w4_workspace(T, K, R, Ns)))
+        _close(Y, G, eG, ydt == nm.NM_BF16)
+        assert torch.equal(Y, nm.nm_spmm_w4(X, cg, ig, sg, qdt=qdt, group=group, Ns=Ns, ydt=ydt))
+    f, d, rel = B.act(B.SILU, G)
+    ref = f * U
+    err = (np.abs(d) * eG + B.CURVE[B.SILU] * eG * eG) * (np.abs(U) + eU) + np.abs(f) * eU + rel * np.abs(ref) + 2.0 ** -24 * np.abs(ref)
+    H = nm.nm_spmm_glu_w4(X, cg, ig, sg, cu, iu, su, qdt=qdt, group=group, Ns=Ns, hdt=nm.NM_F32,
+                          ws=B.nan_ws(nm.raw.nm_spmm_glu_w4_workspace(T, K, R, Ns)))
+    _close(H, ref, err, False)
+
+
 def test_rows_stay_apart(nm):
     """A token of NaN and a weight row with a NaN scale stay in their own outputs."""
     g = np.random.default_rng(3)
