@@ -118,13 +118,26 @@ __device__ __forceinline__ void moe_pick(const MoeArgs& a, const float (&l)[NE],
     int my_sel = 0;
     if constexpr (NE == 1) {
         // a lane's place: how many keys are before its own (experts past the last rank behind all others)
-        keys[lane] = key[0];
-        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
         int place = 0;
+        if (a.bias) {
+            keys[lane] = key[0];
+            __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
 #pragma unroll 4
-        for (int e = 0; e < 64; ++e) {
-            const double k = keys[e];
-            place += k > key[0] || (k == key[0] && e < lane) ? 1 : 0;
+            for (int e = 0; e < 64; ++e) {
+                const double k = keys[e];
+                place += k > key[0] || (k == key[0] && e < lane) ? 1 : 0;
+            }
+        } else {
+            const float mine = (float)key[0];
+            float* k32 = (float*)keys;
+            k32[lane] = mine;
+            __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+#pragma unroll 4
+            for (int e = 0; e < 64; e += 4) {
+                const few_f32x4 k = *(const few_f32x4*)(k32 + e);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) place += k[i] > mine || (k[i] == mine && e + i < lane) ? 1 : 0;
+            }
         }
         const bool in = lane < a.E && place < a.topk;
         if (a.renorm)
@@ -200,7 +213,7 @@ __device__ __forceinline__ void moe_token(const MoeArgs& a, int t, int lane, dou
 }
 
 __global__ __launch_bounds__(256) void moe_pick_kernel(MoeArgs a) {
-    __shared__ double keys[4][64];
+    __shared__ __attribute__((aligned(16))) double keys[4][64];
     const int wave = threadIdx.x >> 6, t = blockIdx.x * 4 + wave;
     if (t < a.T) moe_token(a, t, threadIdx.x & 63, keys[wave], a.sel + t * a.topk, a.wts + t * a.topk, true);
 }
@@ -221,6 +234,7 @@ __device__ __forceinline__ int moe_nth(const uint64_t (&used)[kMoeExperts / 64],
     return -1;
 }
 
+// (With one token the picked experts are its slots' and a pair is its slot: neither is looked for.)
 // The pairs (token, slot) of expert e in order, 16 from the n0-th: lane k of 16 (and its copies) gets
 // the k-th, or -1; the count of all that are left from n0 comes back.
 __device__ __forceinline__ int moe_pairs(const int32_t* sel, int pairs, int e, int n0, int lane, int& mine) {
@@ -254,7 +268,7 @@ __global__ __launch_bounds__(NW * 64) void moe_up_kernel(MoeArgs a, int tiles, i
     FewStage<NW * 64> stage;
     if constexpr (XL) stage.load(a.X, a.ldx, a.T, a.wK, a.lift, xlds, tid);
     if constexpr (PICK) {
-        __shared__ double keys[NW][64];
+        __shared__ __attribute__((aligned(16))) double keys[NW][64];
         __shared__ float wts[NW * kMoeTopk];
         if (wave < a.T) {
             moe_token(a, wave, lane, keys[wave], sel + wave * a.topk, wts + wave * a.topk, blockIdx.x == 0);
@@ -265,8 +279,9 @@ __global__ __launch_bounds__(NW * 64) void moe_up_kernel(MoeArgs a, int tiles, i
             }
         }
     }
-    __syncthreads();
-    for (int p = tid; p < pairs; p += NW * 64) {
+    const bool one = PICK && a.T == 1;
+    if (!one) __syncthreads();
+    for (int p = tid; p < pairs && !one; p += NW * 64) {
         const int s = PICK ? sel[p] : a.sel[p];
         if constexpr (!PICK) sel[p] = s;
         atomicOr((unsigned long long*)&used[s >> 6], 1ull << (s & 63));
@@ -279,7 +294,8 @@ __global__ __launch_bounds__(NW * 64) void moe_up_kernel(MoeArgs a, int tiles, i
     int64_t f0 = 0;
     // task -> expert and features, the rows' pointers and the wave's first unit on its way
     auto start = [&](int task) __attribute__((always_inline)) {
-        e = __builtin_amdgcn_readfirstlane(moe_nth(used, task / tiles));
+        const int n = task / tiles;
+        e = __builtin_amdgcn_readfirstlane(!one ? moe_nth(used, n) : n < pairs ? sel[n] : -1);
         if (e < 0) return;
         f0 = (int64_t)(task % tiles) * (16 * TR);
 #pragma unroll
@@ -296,8 +312,8 @@ __global__ __launch_bounds__(NW * 64) void moe_up_kernel(MoeArgs a, int tiles, i
         const int expert = e;
         const int64_t f = f0;
         for (int c = 0;; c += 16) {
-            int mine;
-            const int left = moe_pairs(sel, pairs, expert, c, lane, mine);
+            int mine = (lane & 15) == 0 ? task / tiles : -1;
+            const int left = one ? 1 : moe_pairs(sel, pairs, expert, c, lane, mine);
             const bool last = left <= 16;
             const int pair = mine >= 0 ? mine : __shfl(mine, 0);
             few_f32x4 acc[RT][1];
@@ -340,10 +356,11 @@ __global__ __launch_bounds__(NW * 64) void moe_up_kernel(MoeArgs a, int tiles, i
 }
 
 // ------------------------------------------------------------------ down
-// grid: x tiles of 16 output columns.  Wave work items are (picked expert, slice of its width); a
+// grid: x tiles of 16 output columns, or of 8 (the other rows of the sparse operand repeat the last) where
+// 16 would leave half the chip idle.  Wave work items are (picked expert, slice of its width); a
 // pair's partial sums stay in LDS per slice, weighted, and are added up token by token.
 template <int VT, int SPG, int NW, bool LIFT>
-__global__ __launch_bounds__(NW * 64) void moe_down_kernel(MoeArgs a, int slices) {
+__global__ __launch_bounds__(NW * 64) void moe_down_kernel(MoeArgs a, int slices, int rows) {
     extern __shared__ __attribute__((aligned(16))) float part[];   // [slices][pairs][16]
     __shared__ int32_t sel[kMoeTokens * kMoeTopk];
     __shared__ float wts[kMoeTokens * kMoeTopk];
@@ -351,34 +368,39 @@ __global__ __launch_bounds__(NW * 64) void moe_down_kernel(MoeArgs a, int slices
     const int tid = threadIdx.x, lane = tid & 63;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int pairs = a.T * a.topk;
-    if (tid < kMoeExperts / 64) used[tid] = 0;
-    __syncthreads();
-    for (int p = tid; p < pairs; p += NW * 64) {
-        const int s = a.sel[p];
-        sel[p] = s;
-        wts[p] = a.wts[p];
-        atomicOr((unsigned long long*)&used[s >> 6], 1ull << (s & 63));
+    const bool one = a.T == 1;
+    if (!one) {
+        if (tid < kMoeExperts / 64) used[tid] = 0;
+        __syncthreads();
+        for (int p = tid; p < pairs; p += NW * 64) {
+            const int s = a.sel[p];
+            sel[p] = s;
+            wts[p] = a.wts[p];
+            atomicOr((unsigned long long*)&used[s >> 6], 1ull << (s & 63));
+        }
+        __syncthreads();
     }
-    __syncthreads();
-    const int64_t r0 = (int64_t)blockIdx.x * 16;
+    const int64_t r0 = (int64_t)blockIdx.x * rows, r1 = r0 + rows < a.K ? r0 + rows : a.K;
     const int units = (a.wF + 255) / 256;
     for (int item = wave;; item += NW) {
-        const int e = __builtin_amdgcn_readfirstlane(moe_nth(used, item / slices)), sl = item % slices;
+        const int n = item / slices, sl = item - n * slices;
+        const int e = __builtin_amdgcn_readfirstlane(!one ? moe_nth(used, n) : n < pairs ? a.sel[n] : -1);
         if (e < 0) break;
         const nm_experts& d = a.w[2];
         const FewRows w[1] = {few_rows((const uint8_t*)d.vals + e * d.es_vals, d.idx + e * d.es_idx,
-                                       (const uint16_t*)d.scales + e * d.es_scales, d.ld_vals, d.ld_idx, d.ld_scales, r0, a.K, lane)};
+                                       (const uint16_t*)d.scales + e * d.es_scales, d.ld_vals, d.ld_idx, d.ld_scales, r0, r1, lane)};
         for (int c = 0;; c += 16) {
             FewUnit<VT, SPG> cur[1];
             cur[0].load(w[0], sl, a.wF, a.gshift, lane);
-            int mine;
-            const int left = moe_pairs(sel, pairs, e, c, lane, mine);
+            int mine = (lane & 15) == 0 ? n : -1;
+            const float wt1 = one ? a.wts[n] : 0.0f;
+            const int left = one ? 1 : moe_pairs(sel, pairs, e, c, lane, mine);
             const int pair = mine >= 0 ? mine : __shfl(mine, 0);
             const FewXDirect<1, LIFT> x{{a.H + (int64_t)pair * a.ldh}};
             few_f32x4 acc[1][1] = {{few_f32x4{0, 0, 0, 0}}};
             few_product<VT, SPG, 1, 1>(cur, w, x, sl, slices, units, a.wF, a.gshift, a.lift, lane, acc);
             if (mine >= 0) {
-                const float wt = wts[mine];
+                const float wt = one ? wt1 : wts[mine];
                 few_f32x4 v = acc[0][0];
 #pragma unroll
                 for (int k = 0; k < 4; ++k) v[k] *= wt;
@@ -390,10 +412,12 @@ __global__ __launch_bounds__(NW * 64) void moe_down_kernel(MoeArgs a, int slices
     __syncthreads();
     for (int o = tid; o < a.T * 16; o += NW * 64) {
         const int t = o >> 4, r = o & 15;
-        if (r0 + r >= a.K) continue;
+        if (r0 + r >= r1) continue;
         float v = 0.0f;
-        for (int j = 0; j < a.topk; ++j)
-            for (int s = 0; s < slices; ++s) v += part[((int64_t)s * pairs + t * a.topk + j) * 16 + r];
+        for (int s = 0; s < slices; ++s) {
+#pragma unroll 4
+            for (int j = 0; j < a.topk; ++j) v += part[(s * pairs + t * a.topk + j) * 16 + r];
+        }
         if (a.y32) ((float*)a.Y)[t * a.ldy + r0 + r] = v;
         else ((uint16_t*)a.Y)[t * a.ldy + r0 + r] = (uint16_t)f32_to_bf16_bits(v);
     }
@@ -443,8 +467,9 @@ static nm_status moe_run(const MoeArgs& a, hipStream_t s) {
     const int units = (a.wF + 255) / 256;
     if (slices > units) slices = units;
     while (slices > 1 && slices * pairs > 1024) --slices;
-    hipLaunchKernelGGL((moe_down_kernel<VT, SPG, kMoeWaves, LIFT>), dim3((a.K + 15) / 16), dim3(kMoeWaves * 64),
-                       (size_t)slices * pairs * 64, s, a, slices);
+    const int rows = a.K >= 256 * 16 ? 16 : 8;
+    hipLaunchKernelGGL((moe_down_kernel<VT, SPG, kMoeWaves, LIFT>), dim3((a.K + rows - 1) / rows), dim3(kMoeWaves * 64),
+                       (size_t)slices * pairs * 64, s, a, slices, rows);
     return check_launch("nm_moe");
 }
 
