@@ -8,11 +8,13 @@
 //
 // The products are bound by the stream of the weight: 1.5 bits a weight in 4 bits, 9 in bf16.  A
 // wave takes 16 weight rows and a unit of 256 columns (four steps) at a time.  In 4 bits a row's unit
-// is 64 bytes of codes and 32 of positions: its four lanes load 16 and 8 bytes each (one
-// instruction for a wave's codes, one for its positions), lane q of the four holding step q, and
+// is 64 bytes of codes and 32 of positions: its four lanes load 16 bytes and two words each (one
+// instruction for a wave's codes, two for its positions), lane q of the four holding step q, and
 // permlane swaps turn that into what each step's instruction wants (lane q holds quarter q of
 // every step): four for the codes, five for the positions, where loads in the operands' own order
 // would take four times the instructions for the same lines.
+// In 4 bits the products of a step or two are summed by the instruction in f32, scaled in f32 (one
+// fused multiply-add for each of a lane's four rows) and added up: no value is rounded to fewer bits.
 #pragma once
 
 #include <type_traits>
