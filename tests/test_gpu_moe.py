@@ -147,6 +147,32 @@ def test_lifted_experts_apart(nm, Ns, K, F, vdt):
     _check(nm, layer, dense, X, Xf, 6, B.RELU2, nm.NM_ROUTE_SOFTMAX, False, 1.0, nm.NM_BF16)
 
 
+@pytest.mark.parametrize("vdt", [BF16, L.I4])
+@pytest.mark.parametrize("T", [1, 9])
+def test_experts_gigabytes_apart(nm, T, vdt):
+    """Experts whose values, positions and scales start more than 2^32 bytes after the one before."""
+    g = np.random.default_rng(T + vdt)
+    K, F, E = 128, 64, 3
+    weights, dense = [], []
+    for rows, width in ((F, K), (F, K), (K, F)):
+        d, v, i, s = _stack(nm, g, E, rows, width, 0, vdt, 64, False)
+        dense.append(d)
+        weights.append((v, i, s))
+
+    def spread(t):
+        _, r, c = t.shape
+        rs, far = t.stride(1), ((1 << 32) + 256) // t.element_size()
+        out = torch.empty((E - 1) * far + r * rs, dtype=t.dtype, device=dev()).as_strided((E, r, c), (far, rs, 1))
+        out.copy_(t)
+        return out
+    far_w = [[None if t is None else spread(t) for t in w] for w in weights]
+    router = _x(g, E, K, K ** -0.5)
+    (gv, gi, gs), (uv, ui, us), (dv, di, ds) = far_w
+    layer = nm.MoELayer(router[0], gv, gi, uv, ui, dv, di, F, vdt=vdt, group=64, gate_scales=gs, up_scales=us, down_scales=ds)
+    X, Xf = _x(g, T, K)
+    _check(nm, layer, (router[1], *dense, None), X, Xf, 3, B.SILU, nm.NM_ROUTE_SOFTMAX, True, 1.0, nm.NM_F32)
+
+
 @pytest.mark.parametrize("E", [4, 65, 200])
 def test_equal_scores_go_to_the_lower_index(nm, E):
     """Router rows of small integers: exact logits, most of them equal."""
