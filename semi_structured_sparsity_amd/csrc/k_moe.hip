@@ -70,16 +70,17 @@ __global__ __launch_bounds__(256) void moe_logits_kernel(MoeArgs a) {
         a.logits[((int64_t)blockIdx.z * a.T + tt) * a.E + ee] = (red[0][k] + red[1][k]) + (red[2][k] + red[3][k]);
 }
 
-// e^x in 64 bits to about 2e-13 relative: 2^n e^r with |r| <= ln 2 / 2 and the series of e^r to r^10 / 10!
+// e^x in 64 bits to about 2e-13 relative: 2^n e^r with |r| <= ln 2 / 2 and the series of e^r to r^10 / 10!.
+// Past +-1000 it is infinity or 0 already, at +-infinity too (whose r would be NaN); a NaN stays one.
 __device__ __forceinline__ double moe_exp(double x) {
+    x = x > 1000.0 ? 1000.0 : x < -1000.0 ? -1000.0 : x;
     const double n = __builtin_rint(x * 1.4426950408889634);
     const double r = __builtin_fma(-n, 0.6931471805599453, x);
     double s = 1.0 / 3628800;
     const double c[10] = {1.0 / 362880, 1.0 / 40320, 1.0 / 5040, 1.0 / 720, 1.0 / 120, 1.0 / 24, 1.0 / 6, 0.5, 1.0, 1.0};
 #pragma unroll
     for (int i = 0; i < 10; ++i) s = __builtin_fma(s, r, c[i]);
-    const int k = n > 2000.0 ? 2000 : n < -2000.0 ? -2000 : (int)n;
-    return __builtin_ldexp(s, k);
+    return __builtin_ldexp(s, (int)n);
 }
 
 // The topk experts of a token and their weights, by one wave: sel[0 .. topk), wts[0 .. topk).

@@ -205,6 +205,37 @@ def test_a_token_of_nan_stays_alone(nm):
     assert torch.equal(Y[keep], ref[keep])
 
 
+def _routed(nm, E, T, logits, topk, route, renorm, bias):
+    """(experts, weights) of tokens that all have the given logits, rounded to bf16: column 0 of the router times 1."""
+    g = np.random.default_rng(E + T)
+    r = torch.zeros((E, 16))
+    r[:, 0] = torch.from_numpy(np.asarray(logits, np.float32))
+    layer, _ = _layer(nm, g, E, 16, 16, 0, BF16, 64, bias=True, router=(r.bfloat16().to(dev()), None))
+    layer.bias.copy_(torch.from_numpy(np.asarray(bias, np.float32)))
+    X = torch.zeros((T, 16), dtype=torch.bfloat16, device=dev())
+    X[:, 0] = 1
+    _, sel, wts = nm.nm_moe(layer, X, topk, route=route, renorm=renorm, want_routing=True)
+    return sel.cpu().numpy(), wts.cpu().numpy().astype(np.float64)
+
+
+@pytest.mark.parametrize("E", [8, 100, 500])
+@pytest.mark.parametrize("T", [1, 6])
+@pytest.mark.parametrize("sigmoid", [False, True])
+def test_infinite_logits_with_a_bias(nm, E, T, sigmoid):
+    """A logit of -inf is a probability of 0 (and +inf a sigmoid of 1): its expert is placed by its bias."""
+    lg = np.tile([-1.0, -np.inf, 0.5, -np.inf], E)[:E]
+    if sigmoid:
+        lg[4] = np.inf
+    p = B.sigmoid(lg) if sigmoid else np.exp(lg - lg.max()) / np.exp(lg - lg.max()).sum()
+    rising = np.linspace(0.0, 3.0, E)
+    for bias in (rising, rising + 10.0 * np.isinf(lg)):
+        want = np.argsort(-(p + bias.astype(np.float32)), kind="stable")[:5]
+        sel, wts = _routed(nm, E, T, lg, 5, nm.NM_ROUTE_SIGMOID if sigmoid else nm.NM_ROUTE_SOFTMAX, False, bias)
+        assert (sel == want).all()
+        # a probability of f32: the exponential and the sum of E of them
+        assert (np.abs(wts - p[want]) <= (E + 20) * 2.0 ** -23 * p[want]).all()
+
+
 def test_every_token_on_one_expert(nm):
     """A bias sends all 64 tokens to one expert; the others' weights of NaN are not read."""
     g = np.random.default_rng(3)
