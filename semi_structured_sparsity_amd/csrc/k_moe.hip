@@ -83,6 +83,15 @@ __device__ __forceinline__ double moe_exp(double x) {
     return __builtin_ldexp(s, (int)n);
 }
 
+// A picked expert's share before it is divided by the picked ones' sum: its probability over e^m (softmax) or
+// e^min(m, 0) (sigmoid), m the largest picked logit.  The largest share is 1/2 or more where every probability may
+// be too small for f32.
+__device__ __forceinline__ float moe_share(bool sigmoid, float l, float m) {
+    if (!sigmoid) return __expf(l - m);
+    m = m < 0.0f ? m : 0.0f;
+    return __builtin_amdgcn_rcpf(__expf(m) + __expf(m - l));
+}
+
 // The topk experts of a token and their weights, by one wave: sel[0 .. topk), wts[0 .. topk).
 // Lane l holds experts l, l + 64, ... with logits l[]; keys: 64 doubles of the wave's own in LDS.
 template <int NE>
@@ -101,12 +110,14 @@ __device__ __forceinline__ void moe_pick(const MoeArgs& a, const float (&l)[NE],
         p[i] = !in ? 0.0f : a.sigmoid ? sigmoid_f32(l[i]) : __expf(l[i] - top);
         sum += p[i];
     }
-    for (int off = 32; off; off >>= 1) sum += __shfl_xor(sum, off);
+    const bool whole = !a.sigmoid && (a.bias || !a.renorm);   // else the sum of all is not asked for
+    if (whole)
+        for (int off = 32; off; off >>= 1) sum += __shfl_xor(sum, off);
 #pragma unroll
     for (int i = 0; i < NE; ++i) {
         const int e = lane + 64 * i;
         key[i] = none;
-        if (!a.sigmoid) p[i] = p[i] / sum;
+        if (whole) p[i] = p[i] / sum;
         if (e < a.E) {
             // with a bias two probabilities may lie closer than f32 tells apart
             if (a.bias)
@@ -143,11 +154,19 @@ __device__ __forceinline__ void moe_pick(const MoeArgs& a, const float (&l)[NE],
             }
         }
         const bool in = lane < a.E && place < a.topk;
-        if (a.renorm)
+        if (a.renorm) {
+            // without a bias the largest logit is among the picked ones
+            float m = top;
+            if (a.bias) {
+                m = in ? l[0] : -__builtin_inff();
+                for (int off = 32; off; off >>= 1) m = __builtin_fmaxf(m, __shfl_xor(m, off));
+            }
+            p[0] = moe_share(a.sigmoid, l[0], m);
             for (int j = 0; j < a.topk; ++j) {   // in descending order, as below
                 const int at = __ffsll((unsigned long long)__ballot(in && place == j)) - 1;
                 total += __uint_as_float((uint32_t)__builtin_amdgcn_readlane((int)__float_as_uint(p[0]), at));
             }
+        }
         if (in) {
             sel[place] = lane;
             wts[place] = a.route_scale * (a.renorm ? p[0] / total : p[0]);
@@ -155,6 +174,7 @@ __device__ __forceinline__ void moe_pick(const MoeArgs& a, const float (&l)[NE],
         return;
     }
     uint32_t taken = 0;   // of this lane's experts
+    // lane j: the j-th's probability, or its logit where shares are made of them
     for (int j = 0; j < a.topk; ++j) {
         double best = none;
         int at = 1 << 30;
@@ -165,7 +185,7 @@ __device__ __forceinline__ void moe_pick(const MoeArgs& a, const float (&l)[NE],
             if (e < a.E && !(taken >> i & 1) && (at == 1 << 30 || key[i] > best)) {
                 best = key[i];
                 at = e;
-                bp = p[i];
+                bp = a.renorm ? l[i] : p[i];
             }
         }
         for (int off = 32; off; off >>= 1) {
@@ -180,11 +200,17 @@ __device__ __forceinline__ void moe_pick(const MoeArgs& a, const float (&l)[NE],
             }
         }
         if ((at & 63) == lane) taken |= 1u << (at >> 6);
-        total += bp;
         if (lane == j) {
             my_sel = at;
             mine = bp;
         }
+    }
+    if (a.renorm) {
+        float m = lane < a.topk ? mine : -__builtin_inff();
+        for (int off = 32; off; off >>= 1) m = __builtin_fmaxf(m, __shfl_xor(m, off));
+        mine = moe_share(a.sigmoid, mine, m);
+        for (int j = 0; j < a.topk; ++j)
+            total += __uint_as_float((uint32_t)__builtin_amdgcn_readlane((int)__float_as_uint(mine), j));
     }
     if (lane < a.topk) {
         sel[lane] = my_sel;

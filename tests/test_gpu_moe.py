@@ -236,6 +236,25 @@ def test_infinite_logits_with_a_bias(nm, E, T, sigmoid):
         assert (np.abs(wts - p[want]) <= (E + 20) * 2.0 ** -23 * p[want]).all()
 
 
+@pytest.mark.parametrize("E", [8, 100, 500])
+@pytest.mark.parametrize("T", [1, 6])
+@pytest.mark.parametrize("sigmoid", [False, True])
+def test_weights_of_probabilities_below_the_types_range(nm, E, T, sigmoid):
+    """Divided by their sum they are ordinary numbers: all of the sigmoid's, and those behind a softmax's top."""
+    lg = -100.0 - 0.5 * np.arange(E)
+    lg[0] = -100.0 if sigmoid else 60.0
+    lg = torch.from_numpy(lg).bfloat16().double().numpy()
+    bias = np.zeros(E)
+    bias[2:6] = [4, 3, 2.5, 2]        # experts 2 to 5, whatever their probabilities
+    sel, wts = _routed(nm, E, T, lg, 4, nm.NM_ROUTE_SIGMOID if sigmoid else nm.NM_ROUTE_SOFTMAX, True, bias)
+    assert (sel == [2, 3, 4, 5]).all()
+    d = lg[2:6] - lg[2]
+    want = np.exp(d) / np.exp(d).sum()          # a sigmoid this far below 0 is its exponential to 1e-43
+    # an f32 exponential of d and (the sigmoid's) its reciprocal, twice for the sum, three more roundings
+    tol = (2 * (2 * np.abs(d).max() + 4) + 7) * 2.0 ** -23
+    assert (np.abs(wts - want) <= tol * want).all(), np.abs(wts / want - 1).max() / tol
+
+
 def test_every_token_on_one_expert(nm):
     """A bias sends all 64 tokens to one expert; the others' weights of NaN are not read."""
     g = np.random.default_rng(3)
