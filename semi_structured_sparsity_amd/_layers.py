@@ -175,11 +175,8 @@ class MoELayer:
         self.hidden, self.vdt, self.group, self.Ns, self.device = int(hidden), vdt, group, Ns, router.device
         E, dev, four = self.experts, router.device, vdt != NM_BF16
         lift = lambda n: lifted_width(n, Ns) if Ns else n  # noqa: E731
-        self.keep = [router, gate, gate_idx, gate_scales, up, up_idx, up_scales, down, down_idx, down_scales, bias]
+        self.keep = [router, gate, gate_idx, gate_scales, up, up_idx, up_scales, down, down_idx, down_scales]
         self.router, self.bias = router, bias
-        if bias is not None and not (bias.dtype == torch.float32 and bias.shape == (E,) and bias.is_contiguous() and
-                                     bias.device == dev):
-            _refuse(f"bias must be {E} contiguous f32 values on {dev}", bias=bias)
         self.weights = []
         for name, rows, width, v, i, s in (("gate", self.hidden, lift(self.K), gate, gate_idx, gate_scales),
                                            ("up", self.hidden, lift(self.K), up, up_idx, up_scales),
@@ -202,6 +199,18 @@ class MoELayer:
             self.weights.append(_Experts(v.data_ptr(), i.data_ptr(), s.data_ptr() if four else None, v.stride(1), i.stride(1), lds,
                                          one(v), one(i), one(s) if four else 0))
         self.address = [ctypes.addressof(w) for w in self.weights]
+
+    @property
+    def bias(self):
+        """The selection bias; a new one may be set between calls."""
+        return self._bias
+
+    @bias.setter
+    def bias(self, bias):
+        if bias is not None and not (bias.dtype == torch.float32 and bias.shape == (self.experts,) and bias.is_contiguous() and
+                                     bias.device == self.device):
+            _refuse(f"bias must be {self.experts} contiguous f32 values on {self.device}", bias=bias)
+        self._bias = bias
 
     def get_device(self) -> int:
         return self.router.get_device()

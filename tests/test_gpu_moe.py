@@ -255,6 +255,17 @@ def test_weights_of_probabilities_below_the_types_range(nm, E, T, sigmoid):
     assert (np.abs(wts - want) <= tol * want).all(), np.abs(wts / want - 1).max() / tol
 
 
+def test_a_new_bias_is_checked(nm):
+    g = np.random.default_rng(4)
+    layer, _ = _layer(nm, g, 8, 64, 32, 0, BF16, 64)
+    for bad in (torch.zeros(7, device=dev()), torch.zeros(8, dtype=torch.bfloat16, device=dev()), torch.zeros(16, device=dev())[::2],
+                torch.zeros(8), torch.zeros((1, 8), device=dev())):
+        with pytest.raises(ValueError):
+            layer.bias = bad
+    layer.bias = torch.zeros(8, device=dev())
+    layer.bias = None
+
+
 def test_every_token_on_one_expert(nm):
     """A bias sends all 64 tokens to one expert; the others' weights of NaN are not read."""
     g = np.random.default_rng(3)
