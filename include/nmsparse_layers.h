@@ -83,7 +83,7 @@ nm_status nm_spmm_glu_w4(const void* X, int64_t Mtok, int64_t K, int64_t ldx, co
  *   Ns: 0, or 3 <= Ns <= 8 over both K' and F'.
  *   Y: bf16 or f32 [Mtok, K] (ldy); sel: int32 [Mtok, topk] and wts: f32 [Mtok, topk], or NULL: the
  *   experts that were picked and their weights.
- * Requires 1 <= topk <= min(E, 16), E <= 512; K and F multiples of 16 and of 2Ns with K', F'
+ * Requires 1 <= topk <= min(E, 16), E <= 512; K and F positive multiples of 16 and of 2Ns with K', F'
  * multiples of 16; bases and row strides of X, router and values 16-byte aligned (experts' strides
  * too), idx 4-byte, scales 8-byte with ld and expert strides multiples of 4.  Codes and scales are
  * read in whole 16 bytes and runs of four rows, as by the 4-bit products.

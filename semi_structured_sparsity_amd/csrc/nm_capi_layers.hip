@@ -159,8 +159,8 @@ nm_status nm_moe(const void* X, int64_t Mtok, int64_t K, int64_t ldx, const void
            "%s: K and F must be multiples of 16 and of 2N", fn);
     const int64_t Kl = lifted(K, Ns), Fl = lifted(F, Ns);
     NM_REQ(Kl % 16 == 0 && Fl % 16 == 0, NM_ERR_SHAPE, "%s: the lifted widths must be multiples of 16", fn);
-    if (Mtok == 0 || K == 0) return NM_OK;
-    NM_REQ(F > 0, NM_ERR_SHAPE, "%s: F == 0", fn);
+    if (Mtok == 0) return NM_OK;
+    NM_REQ(K > 0 && F > 0, NM_ERR_SHAPE, "%s: K == 0 or F == 0", fn);
     NM_REQ(X && router && Y && gate && up && down, NM_ERR_NULL, "%s: NULL argument", fn);
     NM_REQ(ldx >= K && ldr >= K && ldy >= K, NM_ERR_SHAPE, "%s: leading dimension too small", fn);
     NM_REQ(aligned16(X) && aligned16(router) && ldx % 8 == 0 && ldr % 8 == 0, NM_ERR_ALIGN,

@@ -139,6 +139,7 @@ def test_moe_refuses():
     assert _moe(vdt=2) == "NM_ERR_DTYPE" and _moe(ydt=2) == "NM_ERR_DTYPE"
     assert _moe(Ns=2) == "NM_ERR_PATTERN" and _moe(Ns=9) == "NM_ERR_PATTERN"
     assert _moe(K=40) == "NM_ERR_SHAPE" and _moe(F=40) == "NM_ERR_SHAPE" and _moe(F=0) == "NM_ERR_SHAPE" and _moe(Ns=3) == "NM_ERR_SHAPE"
+    assert _moe(K=0) == "NM_ERR_SHAPE" and _moe(M=0, K=0, X=None) == "NM_OK"      # no columns to pick experts by
     for k in ("ldx", "ldr", "ldy"):
         assert _moe(**{k: 56}) == "NM_ERR_SHAPE", k
     for k in ("X", "router", "gate", "up", "down", "Y"):
