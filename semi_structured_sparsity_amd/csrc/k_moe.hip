@@ -8,7 +8,7 @@
 // (One block that makes the logits and picks took 14 us for 64 experts of 2048: a CU alone reads 256 KB at about
 // 25 GB/s.  Logits and picking take 4 and 6 us as two launches; in moe_up_kernel the picking adds 4.)
 // Bound by the stream of the picked experts: 40 tokens on 16 experts of 4096 x 2816 in bf16 (621 MB) 160 us, 3.9
-// TB/s; by latency for few tokens: one on 8 of 64 experts of 2048 x 1024 in 4 bits (20 MB) 24.8 us, 83 at first.
+// TB/s; by latency for few tokens: one on 8 of 64 experts of 2048 x 1024 in 4 bits (20 MB) 25.0 us, 83 at first.
 // An expert's tokens are gathered by lane in the activation's loads (16 at a time are the B
 // operand); its weight is streamed as in the 4-bit products (nm_few.h).
 #include "nm_few.h"
